@@ -297,6 +297,123 @@ moe_status_t moe_debug_wait_timeout(void* workspace, moe_stream_t stream);
 moe_status_t moe_route_noalloc(const float* router_logits, int T, int E, int top_k, int32_t* topk_idx,
                                float* topk_w, int32_t* offsets, int32_t* perm, int32_t* inv, moe_stream_t stream);
 
+/* ---- operators around the experts ------------------------------------------------------- */
+
+/* What a transformer block runs next to its layer of experts: the norms on the way in and out
+ * (moe_block_enter, moe_block_leave), routing with the scoring rules of current routers
+ * (moe_route_scored, moe_layer_forward_scored) and the low-rank adapters of the requests in a
+ * batch (moe_adapters_add).  The pages have no counterpart to these entry points: they describe
+ * the experts alone.  All of them follow the conventions above (device pointers, caller-owned
+ * memory, one stream, nothing allocated, nothing synchronised, argument errors before anything is
+ * enqueued) and need no workspace unless they say so.  Matrices are row-major with a row pitch
+ * `ld*` in elements (>= the row's length). */
+typedef enum { MOE_DT_BF16 = 1, MOE_DT_F16 = 2, MOE_DT_F32 = 3 } moe_dtype_t;
+
+typedef enum { MOE_NORM_RMS = 1, MOE_NORM_LAYER = 2 } moe_norm_kind_t;
+
+/* norm(v) over a row v of H values, in fp32:
+ *   RMS:   v / sqrt(mean(v^2) + eps) * (weight + weight_offset) + bias
+ *   LAYER: (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * (weight + weight_offset) + bias
+ * The variance of LAYER is the mean of the squared differences, never a difference of means. */
+typedef struct {
+  int32_t kind;        /* moe_norm_kind_t */
+  int32_t dtype;       /* moe_dtype_t of weight and bias */
+  float eps;           /* > 0 */
+  float weight_offset; /* 0, or 1 where a checkpoint stores weight - 1 */
+  const void* weight;  /* (dev) [H], or NULL for all ones (weight_offset is then unused) */
+  const void* bias;    /* (dev) [H], or NULL for none */
+} moe_norm_t;
+
+typedef enum { MOE_GATE_LINEAR = 0, MOE_GATE_SIGMOID = 1, MOE_GATE_TANH = 2 } moe_gate_act_t;
+
+/* The norm in front of a block: y[t] = norm(x[t]), t < T.
+ *   x (dev) x_dtype [T, H] (pitch ldx); y (dev) y_dtype [T, H] (pitch ldy), may be x itself
+ *   (same pitch and type) but overlap it in no other way.
+ * Types: y_dtype equal to x_dtype, or x_dtype fp32 with any y_dtype.  Any H >= 1, any pitch and
+ * any alignment of the element's size (rows that are multiples of 16 bytes and start on 16-byte
+ * boundaries take wide loads).  Rows are independent: NaN and infinities stay in their row.
+ * Errors: MOE_ERR_INVALID_ARG for T < 0, H < 1, a pitch below H, a null or misaligned pointer, an
+ * unknown kind or type, eps <= 0; MOE_ERR_UNSUPPORTED for other type pairs or off sm_103;
+ * MOE_ERR_CUDA if the launch fails.  T = 0 enqueues nothing. */
+moe_status_t moe_block_enter(const void* x, int64_t ldx, int x_dtype, const moe_norm_t* norm, void* y, int64_t ldy,
+                             int y_dtype, int T, int H, moe_stream_t stream);
+
+/* The way out of a block, back into the residual stream, and into the next block:
+ *   out[t] = alpha * x[t] + beta * g(gate[t]) * post(block[t])
+ *   y[t]   = next(out[t])      (next != NULL; of out's value before it is rounded to x_dtype)
+ * post, next: norms, or NULL for the identity / no second output (y is then ignored).
+ * gate (dev) gate_dtype or NULL for 1: the factor of token t, channel c is
+ * g(gate[t * gate_ld + c * gate_step]): gate_ld = 0 shares it between tokens, gate_step = 0
+ * between channels; g = gate_act (moe_gate_act_t).
+ *   x (dev) x_dtype [T, H]; block (dev) act_dtype [T, H]; out (dev) x_dtype [T, H]; y (dev)
+ *   act_dtype [T, H].  out may be x and y may be block (same pitch); no other overlap.
+ * Types: act_dtype equal to x_dtype, or x_dtype fp32 with any act_dtype.  gate_step is 0 or 1.
+ * Errors as moe_block_enter. */
+moe_status_t moe_block_leave(const void* x, int64_t ldx, int x_dtype, const void* block, int64_t ldb, int act_dtype,
+                             const moe_norm_t* post, const void* gate, int64_t gate_ld, int gate_step, int gate_dtype,
+                             int gate_act, float alpha, float beta, const moe_norm_t* next, void* out, int64_t ldo,
+                             void* y, int64_t ldy, int T, int H, moe_stream_t stream);
+
+typedef enum { MOE_SCORE_SOFTMAX = 1, MOE_SCORE_SIGMOID = 2 } moe_score_t;
+
+/* How a router turns a token's logits l[0..E) into top_k experts and their weights:
+ *   score s_e = softmax(l)_e or sigmoid(l_e)
+ *   key       = s_e + bias_e where there is a bias (it chooses, it does not weigh); else l_e, whose
+ *               order is the scores' without the ties that rounding makes
+ *   groups    the experts stand in `groups` equal runs; a group's value is the sum of its
+ *               group_top (1 or 2) largest keys -- without a bias and with group_top = 2, of its
+ *               two largest scores -- and only the top_groups best groups' experts are candidates
+ *   choice    the top_k candidates of largest key, in descending order; ties between experts and
+ *               between groups go to the lower index; NaN keys count as -infinity
+ *   weight    scale * s_e, divided by the sum over the chosen if renormalize; 0 for all where that
+ *               sum is 0 (every chosen logit -infinity) */
+typedef struct {
+  int32_t score;       /* moe_score_t */
+  int32_t groups;      /* divides E, 1 .. 32 */
+  int32_t top_groups;  /* 1 .. groups, top_groups * E / groups >= top_k */
+  int32_t group_top;   /* 1 or 2 */
+  int32_t renormalize; /* 0 or 1 */
+  float scale;
+} moe_router_t;
+
+/* Routing alone: topk_idx (dev) i32 [T, top_k] and topk_w (dev) f32 [T, top_k] of
+ *   logits (dev) dtype [T, E] (pitch ld, NaN counts as -infinity) and bias (dev) f32 [E] or NULL.
+ * With {SOFTMAX, 1, 1, 1, 1, 1.0f}, no bias and fp32 logits the choice is moe_debug_route's.
+ * Errors: MOE_ERR_INVALID_ARG for bad sizes (E 1 .. 256, top_k 1 .. min(E, 8), T >= 0), a pitch
+ * below E, a router outside the ranges above, a null or misaligned pointer; MOE_ERR_UNSUPPORTED
+ * off sm_103; MOE_ERR_CUDA if the launch fails. */
+moe_status_t moe_route_scored(const moe_router_t* router, const void* logits, int64_t ld, int dtype, const float* bias,
+                              int T, int E, int top_k, int32_t* topk_idx, float* topk_w, moe_stream_t stream);
+
+/* moe_layer_forward with such a router in place of the renormalised softmax over the top_k logits:
+ * the same pass, workspace and errors, plus those of moe_route_scored. */
+moe_status_t moe_layer_forward_scored(const void* x, const moe_router_t* router, const void* logits, int64_t ld,
+                                      int dtype, const float* bias, int T, const moe_packed_desc_t* desc,
+                                      const void* packed, int top_k, void* out, void* workspace, size_t ws_bytes,
+                                      moe_stream_t stream);
+
+/* The low-rank adapters of many requests, added to the output of a projection that they share:
+ *   out[t] = base[t] + scale[a] * B[a] (A[a] x[t]),   a = slot[q] of the request q that t is in,
+ * and out[t] = base[t] where a is outside 0 .. n-1 (-1: a request without an adapter).
+ *   x (dev) bf16 [T, H] (pitch ldx); base, out (dev) bf16 [T, N] (pitches ldb, ldo); out may be
+ *   base (same pitch: added in place), no other overlap.
+ *   A (dev) bf16 [n, r, H], B (dev) bf16 [n, N, r]: n adapters' matrices, each as torch.nn.Linear
+ *   holds them.  rank (dev) i32 [n] or NULL: adapter a uses its first rank[a] (0 .. r) rows of A
+ *   and columns of B; what stands in the others is not used, whatever it is.  scale (dev) f32 [n]
+ *   or NULL for 1.
+ *   starts (dev) i32 [R + 1]: request q has tokens starts[q] .. starts[q+1]-1 (none is allowed);
+ *   starts[0] = 0, ascending, starts[R] = T.  slot (dev) i32 [R].  Values outside those ranges
+ *   are cut to them: they leave rows unwritten, but touch no memory outside the tensors.
+ * A[a] x is summed in fp32 and rounded to two bf16 terms (16 bits of significand) for the second
+ * product, which is summed in fp32 with base and rounded once.
+ * H and N multiples of 8; r a multiple of 8, 8 .. 128; pointers to matrices 16-byte aligned and
+ * pitches multiples of 8.
+ * Errors: MOE_ERR_INVALID_ARG for sizes outside these, T < 0, R < 0, n < 0, a null or misaligned
+ * pointer; MOE_ERR_UNSUPPORTED off sm_103; MOE_ERR_CUDA if the launch fails. */
+moe_status_t moe_adapters_add(const void* x, int64_t ldx, const void* base, int64_t ldb, const void* A, const void* B,
+                              const float* scale, const int32_t* rank, const int32_t* starts, const int32_t* slot,
+                              void* out, int64_t ldo, int T, int R, int n, int r, int H, int N, moe_stream_t stream);
+
 /* ---- measurement hooks ------------------------------------------------------------------ */
 
 /* Total number of CUDA kernels this library has enqueued in the calling process (all threads,

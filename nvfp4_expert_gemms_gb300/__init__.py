@@ -7,7 +7,8 @@ library cannot be loaded, every call raises.
 Names mirror the C ABI: moe_packed_size, moe_pack_experts, moe_workspace_size,
 moe_layer_forward, moe_workspace_size_host_io, moe_layer_forward_host,
 moe_get_device_error, moe_status_string, moe_debug_route, moe_debug_dequant,
-moe_debug_quant_act.
+moe_debug_quant_act.  The operators around the experts (norms in and out of the block, scored
+routing, request adapters) and MoEBlock, which runs them together, are in block.py.
 """
 from __future__ import annotations
 
@@ -31,7 +32,23 @@ EXPORTS = ("moe_packed_size", "moe_pack_experts", "moe_workspace_size", "moe_lay
            "moe_workspace_size_host_io", "moe_layer_forward_host", "moe_get_device_error", "moe_status_string",
            "moe_debug_route", "moe_debug_dequant", "moe_debug_quant_act", "moe_kernel_launch_count",
            "moe_time_next_step", "moe_layer_forward_static_act", "moe_calibrate_act_scales",
-           "moe_debug_quant_act_static", "moe_debug_quant_act_fp8", "moe_debug_wait_timeout")
+           "moe_debug_quant_act_static", "moe_debug_quant_act_fp8", "moe_debug_wait_timeout", "moe_block_enter",
+           "moe_block_leave", "moe_route_scored", "moe_layer_forward_scored", "moe_adapters_add")
+
+# The operators around the experts live in block.py (which needs torch at import) and are names of
+# this package too.
+_BLOCK = ("Norm", "Router", "MoEBlock", "moe_block_enter", "moe_block_leave", "moe_route_scored",
+          "moe_layer_forward_scored", "moe_adapters_add")
+
+
+def __getattr__(name):
+    if name in _BLOCK:
+        from . import block
+
+        for n in _BLOCK:
+            globals()[n] = getattr(block, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 class PackedDesc(C.Structure):

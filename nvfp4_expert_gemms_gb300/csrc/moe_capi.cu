@@ -4,6 +4,7 @@
 
 #include <atomic>
 
+#include "moe_block.cuh"
 #include "moe_internal.cuh"
 #include "moe_w8a8.cuh"
 
@@ -108,11 +109,12 @@ static moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_O
 
 
 // act_gs: null, or the static activation scales (dev, [2], W4A4 only).  calibrate: act_gs is
-// the output of the calibration instead (out unused, fp4 shapes only).
+// the output of the calibration instead (out unused, fp4 shapes only).  router: null, or the scored
+// router (checked) that picks the experts from its own logits.
 static moe_status_t forward_checked(const void* x, const float* logits, int T, const moe_packed_desc_t* d,
                                     const void* packed, int k, void* out, void* ws, size_t ws_bytes,
                                     cudaStream_t s, bool host_io_layout, const float* act_gs = nullptr,
-                                    bool calibrate = false) {
+                                    bool calibrate = false, const ScoreArgs* router = nullptr) {
   if (!desc_ok(d) || T < 0 || k < 1 || k > kMaxTopK || k > d->E) return MOE_ERR_INVALID_ARG;
   if (act_gs && (d->fmt != MOE_FMT_NVFP4_W4A4 || !aligned(act_gs, 4))) return MOE_ERR_INVALID_ARG;
   if (calibrate) {
@@ -144,7 +146,9 @@ static moe_status_t forward_checked(const void* x, const float* logits, int T, c
     pre.zero2_u32 = (unsigned*)(w + L.cnt);
     pre.n2_u32 = 1;
   }
-  if (launch_route(logits, T, d->E, k, rb, L, w, pre, s) != cudaSuccess) return MOE_ERR_CUDA;
+  if ((router ? launch_route_by(*router, T, d->E, k, rb, L, w, pre, s)
+              : launch_route(logits, T, d->E, k, rb, L, w, pre, s)) != cudaSuccess)
+    return MOE_ERR_CUDA;
   const StepEvents ev = g_pending_events;
   g_pending_events = StepEvents();
   if (calibrate)
@@ -252,6 +256,17 @@ moe_status_t moe_layer_forward_static_act(const void* x, const float* router_log
   if (!act_gs) return MOE_ERR_INVALID_ARG;
   return forward_checked(x, router_logits, T, d, packed, top_k, out, workspace, ws_bytes, (cudaStream_t)stream,
                          false, act_gs);
+}
+
+moe_status_t moe_layer_forward_scored(const void* x, const moe_router_t* router, const void* logits, int64_t ld,
+                                      int dtype, const float* bias, int T, const moe_packed_desc_t* d,
+                                      const void* packed, int top_k, void* out, void* workspace, size_t ws_bytes,
+                                      moe_stream_t stream) {
+  if (!desc_ok(d) || !router_ok(router, d->E, top_k) || !dtype_ok(dtype) || (T > 0 && ld < d->E)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(logits, dtype_size(dtype)) || !aligned(bias, 4)) return MOE_ERR_INVALID_ARG;
+  const ScoreArgs r = {*router, logits, ld, dtype, bias};
+  return forward_checked(x, (const float*)logits, T, d, packed, top_k, out, workspace, ws_bytes, (cudaStream_t)stream,
+                         false, nullptr, false, &r);
 }
 
 moe_status_t moe_calibrate_act_scales(const void* x, const float* router_logits, int T, const moe_packed_desc_t* d,

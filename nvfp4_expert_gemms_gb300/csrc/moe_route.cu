@@ -10,7 +10,10 @@
 //   3. route_scatter_kernel rank of each row inside its block from per-warp ballot masks
 // Up to kRouteTB tokens (decode) all three steps run in one block of one launch
 // (route_small_kernel), which produces the same outputs.
-#include "moe_internal.cuh"
+//
+// The kernels are templates over the scorer that picks a token's experts: the renormalised softmax
+// over the k largest logits (TopkScorer), or a scored router (RouterScorer, moe_score.cuh).
+#include "moe_score.cuh"
 
 namespace moe {
 
@@ -151,7 +154,24 @@ __device__ __forceinline__ void expert_scan(const int* cnt, int E, int row_block
   }
 }
 
-__global__ void __launch_bounds__(1024) route_topk_kernel(const float* __restrict__ logits, int T, int E, int k,
+struct TopkScorer {
+  const float* __restrict__ logits;
+  __device__ __forceinline__ int operator()(int t, int E, int k, int lane, int32_t* idx, float* w) const {
+    return route_token(logits, t, E, k, lane, idx, w);
+  }
+};
+
+template <int VT>
+struct RouterScorer {
+  ScoreArgs a;
+  ScoreGeom g;
+  __device__ __forceinline__ int operator()(int t, int E, int k, int lane, int32_t* idx, float* w) const {
+    return score_token<VT>(a, g, t, k, lane, idx, w);
+  }
+};
+
+template <class Scorer>
+__global__ void __launch_bounds__(1024) route_topk_kernel(const Scorer score, int T, int E, int k,
                                                          int32_t* __restrict__ topk_idx,
                                                          float* __restrict__ topk_w,
                                                          int32_t* __restrict__ blkcnt, int* err, RoutePrelude pre) {
@@ -166,7 +186,7 @@ __global__ void __launch_bounds__(1024) route_topk_kernel(const float* __restric
   const int t_end = min(T, (int)(blockIdx.x + 1) * kRouteTB);
   for (int t = blockIdx.x * kRouteTB + warp; t < t_end; t += 32) {  // 4 tokens per warp
     if (pre.x) row_absmax(pre, t, lane);
-    const int mi = route_token(logits, t, E, k, lane, topk_idx, topk_w);
+    const int mi = score(t, E, k, lane, topk_idx, topk_w);
     if (lane < k) atomicAdd(&cnt[mi], 1);
   }
   __syncthreads();
@@ -269,7 +289,8 @@ __global__ void __launch_bounds__(kRouteTB) route_scatter_kernel(const int32_t* 
 // histogram and per-32-token membership masks in shared memory, then the scan and tile table,
 // then each row's rank among the rows of its expert (tokens in order), as the three kernels
 // above compute them.
-__global__ void __launch_bounds__(1024) route_small_kernel(const float* __restrict__ logits, int T, int E, int k,
+template <class Scorer>
+__global__ void __launch_bounds__(1024) route_small_kernel(const Scorer score, int T, int E, int k,
                                                            int row_block, int max_tiles,
                                                            int32_t* __restrict__ topk_idx,
                                                            float* __restrict__ topk_w, int32_t* __restrict__ offsets,
@@ -289,7 +310,7 @@ __global__ void __launch_bounds__(1024) route_small_kernel(const float* __restri
   __syncthreads();
   for (int t = warp; t < T; t += 32) {
     if (pre.x) row_absmax(pre, t, lane);
-    const int mi = route_token(logits, t, E, k, lane, topk_idx, topk_w);
+    const int mi = score(t, E, k, lane, topk_idx, topk_w);
     if (lane < k) {
       atomicAdd(&cnt[mi], 1);
       atomicOr(&mask[t >> 5][mi], 1u << (t & 31));
@@ -332,9 +353,8 @@ __global__ void __launch_bounds__(1024) route_small_kernel(const float* __restri
   }
 }
 
-}  // namespace
-
-cudaError_t launch_route(const float* logits, int T, int E, int k, int row_block, const WsLayout& L, char* ws,
+template <class Scorer>
+cudaError_t launch_route_with(const Scorer& score, int T, int E, int k, int row_block, const WsLayout& L, char* ws,
                          const RoutePrelude& pre, cudaStream_t s) {
   int* err = (int*)(ws + L.err);
   int32_t* idx = (int32_t*)(ws + L.topk_idx);
@@ -349,11 +369,11 @@ cudaError_t launch_route(const float* logits, int T, int E, int k, int row_block
   const int nb = L.nb;
   if (T > 0 && T <= kRouteTB) {
     note_launches(1);
-    return launch_pdl(route_small_kernel, dim3(1), dim3(1024), 0, s, logits, T, E, k, row_block, L.max_tiles, idx,
+    return launch_pdl(route_small_kernel<Scorer>, dim3(1), dim3(1024), 0, s, score, T, E, k, row_block, L.max_tiles, idx,
                       w, off, toff, perm, inv, tiles, err, pre);
   }
   cudaError_t e = cudaSuccess;
-  if (T > 0) e = launch_pdl(route_topk_kernel, dim3(nb), dim3(1024), 0, s, logits, T, E, k, idx, w, blkcnt, err, pre);
+  if (T > 0) e = launch_pdl(route_topk_kernel<Scorer>, dim3(nb), dim3(1024), 0, s, score, T, E, k, idx, w, blkcnt, err, pre);
   else e = cudaMemsetAsync(err, 0, sizeof(int), s);
   if (e == cudaSuccess)
     e = launch_pdl(route_scan_kernel, dim3(1), dim3(1024), 0, s, (const int32_t*)blkcnt, T > 0 ? nb : 0, E, row_block,
@@ -363,6 +383,21 @@ cudaError_t launch_route(const float* logits, int T, int E, int k, int row_block
                    (const int32_t*)blkbase, perm, inv);
   note_launches(T > 0 ? 3 : 1);
   return e;
+}
+
+}  // namespace
+
+cudaError_t launch_route(const float* logits, int T, int E, int k, int row_block, const WsLayout& L, char* ws,
+                         const RoutePrelude& pre, cudaStream_t s) {
+  return launch_route_with(TopkScorer{logits}, T, E, k, row_block, L, ws, pre, s);
+}
+
+cudaError_t launch_route_by(const ScoreArgs& a, int T, int E, int k, int row_block, const WsLayout& L, char* ws,
+                            const RoutePrelude& pre, cudaStream_t s) {
+  const ScoreGeom g = score_geom(a, E);
+  if (g.per <= 4) return launch_route_with(RouterScorer<4>{a, g}, T, E, k, row_block, L, ws, pre, s);
+  if (g.per <= 8) return launch_route_with(RouterScorer<8>{a, g}, T, E, k, row_block, L, ws, pre, s);
+  return launch_route_with(RouterScorer<16>{a, g}, T, E, k, row_block, L, ws, pre, s);
 }
 
 }  // namespace moe
