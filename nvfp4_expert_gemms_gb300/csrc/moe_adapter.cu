@@ -15,7 +15,11 @@
 // significand, so that an adapter as large as base costs the sum no precision that shows in out's own
 // bf16 rounding.  The extra MMAs are hidden: HBM bytes of x, base and out bound large batches, the
 // reads of A and B (L2) small ones.
+#include <cooperative_groups.h>
+
 #include "moe_block.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace moe {
 namespace {
@@ -39,23 +43,36 @@ __device__ __forceinline__ float lo_f32(uint32_t p) { return __uint_as_float(p <
 __device__ __forceinline__ float hi_f32(uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); }
 
 struct Tile {
-  int slot, t0, rows;
+  int slot, t0, rows, rk;  // adapter (-1: none), first token, tokens (0: past the last tile), rank in use
+  float scale;
 };
 
-// The tile of this block: requests are cut into tiles of bm tokens in order; tile `want` of all.
-// slot = -1: no adapter; rows = 0: past the last tile.  Every thread of the block calls it.
+// Tile `want` of all: requests are cut into tiles of bm tokens in order.  Every thread of the block
+// calls it.  A thread also reads its request's rank and scale, whether or not the tile turns out to be
+// its own: that way they cost no further trip to memory.
+template <int WARPS>
 __device__ __forceinline__ Tile find_tile(const AdapterArgs& a, int want, int bm) {
-  __shared__ int wsum[kWarps];
+  __shared__ int wsum[WARPS];
   __shared__ Tile found;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) found = Tile{-1, 0, 0};
+  if (tid == 0) found = Tile{-1, 0, 0, 0, 1.f};
   int before = 0;  // tiles of the requests in front of this chunk
-  for (int q0 = 0; q0 < a.R; q0 += kWarps * 32) {
+  for (int q0 = 0; q0 < a.R; q0 += WARPS * 32) {
     const int q = q0 + tid;
-    int s = 0, e = 0;
+    int s = 0, e = 0, sl = -1, rk = 0;
+    float sc = 1.f;
     if (q < a.R) {
-      s = min(max(a.starts[q], 0), a.T);
-      e = min(max(a.starts[q + 1], s), a.T);
+      s = a.starts[q];
+      e = a.starts[q + 1];
+      sl = a.slot[q];
+      s = min(max(s, 0), a.T);
+      e = min(max(e, s), a.T);
+      if (sl >= 0 && sl < a.n) {
+        rk = a.rank ? min(max(a.rank[sl], 0), a.r) : a.r;
+        if (a.scale) sc = a.scale[sl];
+      } else {
+        sl = -1;
+      }
     }
     const int n = (e - s + bm - 1) / bm;
     int run = n;
@@ -68,16 +85,14 @@ __device__ __forceinline__ Tile find_tile(const AdapterArgs& a, int want, int bm
     __syncthreads();
     int base = before, all = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
       base += w < warp ? wsum[w] : 0;
       all += wsum[w];
     }
     const int first = base + run - n;
     if (want >= first && want < first + n) {
-      int sl = a.slot[q];
-      sl = sl >= 0 && sl < a.n ? sl : -1;
       const int t0 = s + (want - first) * bm;
-      found = Tile{sl, t0, min(bm, e - t0)};
+      found = Tile{sl, t0, min(bm, e - t0), rk, sc};
     }
     before += all;
     __syncthreads();
@@ -87,140 +102,433 @@ __device__ __forceinline__ Tile find_tile(const AdapterArgs& a, int want, int bm
   return found;
 }
 
-// One tile per blockIdx.x, output columns in gridDim.y parts.  WM warps along the tokens (16 each),
-// kWarps / WM along K (first product) and along N (second).  RT: rank steps of 16 (r <= 16 RT).
-template <int RT, int WM>
-__global__ void __launch_bounds__(32 * kWarps) adapter_kernel(const AdapterArgs a) {
-  constexpr int WK = kWarps / WM, BM = 16 * WM;
-  extern __shared__ float vpart[];  // [WK][WM][RT * 2][32][4], only with WK > 1
+// v (the sums of one rank step's two MMA tiles) times the adapter's scale, as the second product's A
+// operand in two bf16 terms.
+__device__ __forceinline__ void split_v(const float (&v0)[4], const float (&v1)[4], float sc, uint32_t (&hi)[4],
+                                        uint32_t (&lo)[4]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int row = 0; row < 2; ++row) {
+      const float c0 = (h ? v1 : v0)[2 * row] * sc, c1 = (h ? v1 : v0)[2 * row + 1] * sc;
+      const uint32_t p = pack_bf16(c0, c1);
+      hi[2 * h + row] = p;
+      lo[2 * h + row] = pack_bf16(c0 - lo_f32(p), c1 - hi_f32(p));
+    }
+}
+
+// Clears what stands past the adapter's rank in a lane's ranks k .. k+3 of a row of B.
+__device__ __forceinline__ uint2 cut_rank(uint2 b, int k, int rk) {
+  if (k + 4 > rk) {
+    b.x = k + 1 < rk ? b.x : k < rk ? b.x & 0xFFFFu : 0u;
+    b.y = k + 3 < rk ? b.y : k + 2 < rk ? b.y & 0xFFFFu : 0u;
+  }
+  return b;
+}
+
+// ---- few tokens per request ------------------------------------------------------------------
+// One tile of up to 16 tokens per cluster of blocks.  The blocks' warps share K (each lane's loads of x
+// and A are independent and all issued at once), v's parts are summed warp by warp in shared memory and
+// block by block through distributed shared memory, in a fixed order, and the blocks share N.  B and
+// base of a warp's first 32 columns are loaded before the sums meet.
+template <int RT>
+__global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kernel(const AdapterArgs a) {
+  extern __shared__ __align__(128) unsigned char few_smem[];
+  float4(*part)[2 * RT][32] = (float4(*)[2 * RT][32])few_smem;  // [kWarps]
+  float4(*mine)[32] = part[kWarps];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = cluster.num_blocks(), crank = cluster.block_rank();
   pdl_wait();
   pdl_trigger();
-  const Tile tile = find_tile(a, blockIdx.x, BM);
+  const Tile tile = find_tile<kWarps>(a, blockIdx.x / C, 16);
   if (tile.rows == 0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wm = warp / WK, wk = warp % WK;
+  const int rk = tile.rk;
+  if (rk == 0 && a.out == a.base) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int r0 = 16 * wm + g, r1 = r0 + 8;  // the lane's two rows of the tile
-  const bool ok0 = r0 < tile.rows, ok1 = r1 < tile.rows;
-  const int64_t t0 = tile.t0 + (ok0 ? r0 : 0), t1 = tile.t0 + (ok1 ? r1 : 0);
+  const bool ok0 = g < tile.rows, ok1 = g + 8 < tile.rows;
+  const int64_t t0 = tile.t0 + (ok0 ? g : 0), t1 = tile.t0 + (ok1 ? g + 8 : 0);
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  int rk = 0;
-  float sc = 1.f;
-  if (tile.slot >= 0) {
-    rk = a.rank ? min(max(a.rank[tile.slot], 0), a.r) : a.r;
-    if (a.scale) sc = a.scale[tile.slot];
-  }
+  const int part_w = crank * kWarps + warp, parts = C * kWarps;
   float v[2 * RT][4];
 #pragma unroll
   for (int j = 0; j < 2 * RT; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[j][i] = 0.f;
-  if (rk > 0 && 16 * wm < tile.rows) {
-    const __nv_bfloat16* A = a.A + (int64_t)tile.slot * a.r * a.H;
-    const __nv_bfloat16 *x0 = a.x + t0 * a.ldx, *x1 = a.x + t1 * a.ldx;
-#pragma unroll 2
-    for (int k = 32 * wk + 8 * t; k - 8 * t < a.H; k += 32 * WK) {
-      const bool in = k < a.H;
-      const uint4 p0 = in && ok0 ? *(const uint4*)(x0 + k) : zero, p1 = in && ok1 ? *(const uint4*)(x1 + k) : zero;
+  const __nv_bfloat16* A = a.A + (int64_t)max(tile.slot, 0) * a.r * a.H;
+  const __nv_bfloat16 *x0 = a.x + t0 * a.ldx, *x1 = a.x + t1 * a.ldx;
+  const __nv_bfloat16* B = a.B + (int64_t)max(tile.slot, 0) * a.N * a.r;
+  const __nv_bfloat16 *b0 = a.base + t0 * a.ldb, *b1 = a.base + t1 * a.ldb;
+  __nv_bfloat16 *o0 = a.out + t0 * a.ldo, *o1 = a.out + t1 * a.ldo;
+  uint2 bq[4][RT];
+  uint4 y0, y1;
+  auto load_cols = [&](int c) {  // B and base of columns c .. c+31
+    const int col = c + 8 * t;
+    y0 = ok0 && col < a.N ? *(const uint4*)(b0 + col) : zero;
+    y1 = ok1 && col < a.N ? *(const uint4*)(b1 + col) : zero;
 #pragma unroll
-      for (int j = 0; j < 2 * RT; ++j) {
-        if (16 * (j >> 1) >= rk) break;
-        const int row = 16 * (j >> 1) + 4 * (g >> 1) + 2 * (j & 1) + (g & 1);
-        const uint4 q = in && row < rk ? *(const uint4*)(A + (int64_t)row * a.H + k) : zero;
-        mma_bf16(v[j], p0.x, p1.x, p0.y, p1.y, q.x, q.y);
-        mma_bf16(v[j], p0.z, p1.z, p0.w, p1.w, q.z, q.w);
+    for (int j = 0; j < 4; ++j) {
+      const int n = c + 8 * (g >> 1) + 2 * j + (g & 1);
+#pragma unroll
+      for (int s = 0; s < RT; ++s) {
+        const int k = 16 * s + 4 * t;
+        bq[j][s] = n < a.N && k < rk ? *(const uint2*)(B + (int64_t)n * a.r + k) : make_uint2(0, 0);
       }
     }
+  };
+  if (rk > 0) {
+    constexpr int U = RT == 1 ? 4 : RT == 2 ? 2 : 1;  // steps whose loads are in flight together
+    for (int kb = 32 * part_w; kb < a.H; kb += 32 * parts * U) {
+      uint4 p0[U], p1[U], q[U][2 * RT];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = kb + 32 * parts * u + 8 * t;
+        const bool in = k < a.H;
+        p0[u] = in && ok0 ? *(const uint4*)(x0 + k) : zero;
+        p1[u] = in && ok1 ? *(const uint4*)(x1 + k) : zero;
+#pragma unroll
+        for (int j = 0; j < 2 * RT; ++j) {
+          const int row = 16 * (j >> 1) + 4 * (g >> 1) + 2 * (j & 1) + (g & 1);
+          q[u][j] = in && row < rk ? *(const uint4*)(A + (int64_t)row * a.H + k) : zero;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < 2 * RT; ++j)
+          if (16 * (j >> 1) < rk) {
+            mma_bf16(v[j], p0[u].x, p1[u].x, p0[u].y, p1[u].y, q[u][j].x, q[u][j].y);
+            mma_bf16(v[j], p0[u].z, p1[u].z, p0[u].w, p1[u].w, q[u][j].z, q[u][j].w);
+          }
+    }
   }
-  if constexpr (WK > 1) {  // v's partial sums over the warps' parts of K meet in every warp
-    float4* part = (float4*)vpart;
+  load_cols(32 * part_w);
+  if (rk > 0) {
 #pragma unroll
-    for (int j = 0; j < 2 * RT; ++j) part[((wk * WM + wm) * 2 * RT + j) * 32 + lane] = *(float4*)v[j];
+    for (int j = 0; j < 2 * RT; ++j)
+      if (ok0) part[warp][j][lane] = make_float4(v[j][0], v[j][1], v[j][2], v[j][3]);
     __syncthreads();
+    for (int e = threadIdx.x; e < 2 * RT * 32; e += 32 * kWarps) {
+      const int j = e >> 5, l = e & 31;
+      if ((l >> 2) >= tile.rows) continue;
+      float4 s = part[0][j][l];
 #pragma unroll
-    for (int j = 0; j < 2 * RT; ++j) {
-      float4 s = part[(wm * 2 * RT + j) * 32 + lane];
-#pragma unroll
-      for (int w = 1; w < WK; ++w) {
-        const float4 o = part[((w * WM + wm) * 2 * RT + j) * 32 + lane];
+      for (int w = 1; w < kWarps; ++w) {
+        const float4 o = part[w][j][l];
         s.x += o.x;
         s.y += o.y;
         s.z += o.z;
         s.w += o.w;
       }
-      *(float4*)v[j] = s;
+      mine[j][l] = s;
+    }
+    const float4(*all)[32] = mine;
+    if (C > 1) {
+      cluster.sync();
+      float4(*sum)[32] = part[0];
+      for (int e = threadIdx.x; e < 2 * RT * 32; e += 32 * kWarps) {
+        const int j = e >> 5, l = e & 31;
+        if ((l >> 2) >= tile.rows) continue;
+        float4 o[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (c < C) o[c] = *cluster.map_shared_rank(&mine[j][l], c);
+        float4 s = o[0];
+#pragma unroll
+        for (int c = 1; c < 8; ++c)
+          if (c < C) {
+            s.x += o[c].x;
+            s.y += o[c].y;
+            s.z += o[c].z;
+            s.w += o[c].w;
+          }
+        sum[j][l] = s;
+      }
+      all = part[0];
+      cluster.barrier_arrive();  // this block reads no other block's memory from here on
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 2 * RT; ++j) {
+      const float4 s = ok0 ? all[j][lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[j][0] = s.x;
+      v[j][1] = s.y;
+      v[j][2] = s.z;
+      v[j][3] = s.w;
     }
   }
-  if (16 * wm >= tile.rows) return;
-  // the second product's A operand: rank step s, rows r0 / r1, first and second k pair
   uint32_t hi[RT][4], lo[RT][4];
 #pragma unroll
-  for (int s = 0; s < RT; ++s)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int row = 0; row < 2; ++row) {
-        const float c0 = v[2 * s + h][2 * row] * sc, c1 = v[2 * s + h][2 * row + 1] * sc;
-        const uint32_t p = pack_bf16(c0, c1);
-        hi[s][2 * h + row] = p;
-        lo[s][2 * h + row] = pack_bf16(c0 - lo_f32(p), c1 - hi_f32(p));
-      }
-  const __nv_bfloat16* B = a.B + (int64_t)max(tile.slot, 0) * a.N * a.r;
-  const __nv_bfloat16 *b0 = a.base + t0 * a.ldb, *b1 = a.base + t1 * a.ldb;
-  __nv_bfloat16 *o0 = a.out + t0 * a.ldo, *o1 = a.out + t1 * a.ldo;
-  if (rk == 0 && a.out == a.base) return;
-  for (int c = 32 * (blockIdx.y * WK + wk); c < a.N; c += 32 * WK * gridDim.y) {
+  for (int s = 0; s < RT; ++s) split_v(v[2 * s], v[2 * s + 1], tile.scale, hi[s], lo[s]);
+  for (int c = 32 * part_w; c < a.N; c += 32 * parts) {
+    if (c != 32 * part_w) load_cols(c);
     const int col = c + 8 * t;
-    const uint4 y0 = ok0 && col < a.N ? *(const uint4*)(b0 + col) : zero;
-    const uint4 y1 = ok1 && col < a.N ? *(const uint4*)(b1 + col) : zero;
     const uint32_t w0[4] = {y0.x, y0.y, y0.z, y0.w}, w1[4] = {y1.x, y1.y, y1.z, y1.w};
     uint32_t q0[4], q1[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float d[4] = {lo_f32(w0[j]), hi_f32(w0[j]), lo_f32(w1[j]), hi_f32(w1[j])};
-      const int n = c + 8 * (g >> 1) + 2 * j + (g & 1);
 #pragma unroll
-      for (int s = 0; s < RT; ++s) {
-        if (16 * s >= rk) break;
-        const int k = 16 * s + 4 * t;
-        uint2 b = make_uint2(0, 0);
-        if (n < a.N && k < rk) {
-          b = *(const uint2*)(B + (int64_t)n * a.r + k);
-          if (k + 4 > rk) {  // what stands past the adapter's rank is not used
-            b.x = k + 1 < rk ? b.x : b.x & 0xFFFFu;
-            b.y = k + 2 < rk ? (k + 3 < rk ? b.y : b.y & 0xFFFFu) : 0u;
-          }
+      for (int s = 0; s < RT; ++s)
+        if (16 * s < rk) {
+          const uint2 b = cut_rank(bq[j][s], 16 * s + 4 * t, rk);
+          mma_bf16(d, lo[s][0], lo[s][1], lo[s][2], lo[s][3], b.x, b.y);
+          mma_bf16(d, hi[s][0], hi[s][1], hi[s][2], hi[s][3], b.x, b.y);
         }
-        mma_bf16(d, lo[s][0], lo[s][1], lo[s][2], lo[s][3], b.x, b.y);
-        mma_bf16(d, hi[s][0], hi[s][1], hi[s][2], hi[s][3], b.x, b.y);
-      }
       q0[j] = pack_bf16(d[0], d[1]);
       q1[j] = pack_bf16(d[2], d[3]);
     }
     if (ok0 && col < a.N) *(uint4*)(o0 + col) = make_uint4(q0[0], q0[1], q0[2], q0[3]);
     if (ok1 && col < a.N) *(uint4*)(o1 + col) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
   }
+  if (rk > 0 && C > 1) cluster.barrier_wait();  // no block leaves while another may still read its sums
 }
 
-template <int RT, int WM>
-cudaError_t launch_tiles(const AdapterArgs& a, int parts, cudaStream_t s) {
-  constexpr int BM = 16 * WM, WK = kWarps / WM;
-  const int64_t tiles = (int64_t)a.T / BM + (a.R < a.T ? a.R : a.T);  // at most one partial tile per request
-  const size_t smem = WK > 1 ? (size_t)WK * WM * RT * 2 * 32 * 16 : 0;
+// ---- many tokens per request -----------------------------------------------------------------
+// One tile of 16 WM tokens per block, WM x WK warps: WM along the tokens, WK along K (first product)
+// and N (second).  x and A, then base and B, stream through a ring of NS shared-memory stages filled
+// by cp.async NS - 1 stages ahead, so the bytes in flight do not depend on registers or warps.
+//   K stage  kKC columns of x ([BM][kKC]) and of A ([16 RT][kKC]); row i's 16-byte piece p sits at
+//            piece p ^ 4 (i & 1), so the 8 lanes that one 16-byte shared load serves at a time (two
+//            rows, four pieces) hit all banks once
+//   N stage  kNC columns of base ([BM][kNC], same placement) and kNC rows of B, row order (n-tile, lane
+//            group), pitch an odd multiple of 32 bytes (16 lanes of an 8-byte load: four rows)
+constexpr int kKC = 128, kNC = 128;
+
+template <int RT, int WM, int WK>
+struct Many {
+  static constexpr int BM = 16 * WM, threads = 32 * WM * WK;
+  static constexpr int pitch = 32 * (RT | 1);  // bytes of a row of B
+  static constexpr int xbytes = BM * kKC * 2, abytes = 16 * RT * kKC * 2;
+  static constexpr int ybytes = BM * kNC * 2, bbytes = kNC * pitch;
+  static constexpr int stage = xbytes + abytes > ybytes + bbytes ? xbytes + abytes : ybytes + bbytes;
+  static constexpr int vbytes = WK > 1 ? WM * 2 * RT * 32 * 16 : 0;  // one warp column's sums
+  static constexpr int budget = (BM > 64 ? 220 : 108) * 1024;         // one or two blocks per SM
+  static constexpr int NS = budget / stage > 4 ? 4 : budget / stage;
+  static constexpr int smem = NS * stage > vbytes ? NS * stage : vbytes;
+  static_assert(NS >= 2 && stage % 16 == 0 && vbytes <= stage, "");
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+
+template <int RT, int WM, int WK>
+__global__ void __launch_bounds__(32 * WM * WK) adapter_many_kernel(const AdapterArgs a) {
+  using G = Many<RT, WM, WK>;
+  constexpr int BM = G::BM, NT = G::threads, NS = G::NS;
+  extern __shared__ __align__(128) unsigned char ring[];
+  pdl_wait();
+  pdl_trigger();
+  const Tile tile = find_tile<WM * WK>(a, blockIdx.x, BM);
+  if (tile.rows == 0) return;
+  const int rk = tile.rk;
+  if (rk == 0 && a.out == a.base) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wm = warp % WM, wk = warp / WM;
+  const int g = lane >> 2, t = lane & 3, r0 = 16 * wm + g, r1 = r0 + 8;
+  const uint32_t ring_u = (uint32_t)__cvta_generic_to_shared(ring);
+  const __nv_bfloat16* A = a.A + (int64_t)max(tile.slot, 0) * a.r * a.H;
+  const __nv_bfloat16* B = a.B + (int64_t)max(tile.slot, 0) * a.N * a.r;
+  const __nv_bfloat16* x = a.x + (int64_t)tile.t0 * a.ldx;
+  const __nv_bfloat16* base = a.base + (int64_t)tile.t0 * a.ldb;
+  const int steps = (rk + 15) / 16;  // rank steps in use
+  const int kst = rk > 0 ? (a.H + kKC - 1) / kKC : 0, nst = (a.N + kNC - 1) / kNC;
+
+  auto fill_k = [&](int st, int at) {
+    const uint32_t xs = ring_u + at * G::stage, as = xs + G::xbytes;
+    constexpr int P = kKC / 8;  // pieces per row
+    const int k0 = st * kKC;
+#pragma unroll
+    for (int i = 0; i < BM * P / NT; ++i) {
+      const int e = tid + i * NT, row = e / P, p = e % P;
+      const bool in = row < tile.rows && k0 + 8 * p < a.H;
+      cp16(xs + row * (kKC * 2) + ((p ^ ((row & 1) << 2)) << 4), in ? x + (int64_t)row * a.ldx + k0 + 8 * p : x, in);
+    }
+    for (int e = tid; e < 16 * steps * P; e += NT) {
+      const int row = e / P, p = e % P;
+      const bool in = row < rk && k0 + 8 * p < a.H;
+      cp16(as + row * (kKC * 2) + ((p ^ ((row & 1) << 2)) << 4), in ? A + (int64_t)row * a.H + k0 + 8 * p : A, in);
+    }
+  };
+  auto fill_n = [&](int st, int at) {
+    const uint32_t ys = ring_u + at * G::stage, bs = ys + G::ybytes;
+    constexpr int P = kNC / 8;
+    const int c0 = st * kNC;
+#pragma unroll
+    for (int i = 0; i < BM * P / NT; ++i) {
+      const int e = tid + i * NT, row = e / P, p = e % P;
+      const bool in = row < tile.rows && c0 + 8 * p < a.N;
+      cp16(ys + row * (kNC * 2) + ((p ^ ((row & 1) << 2)) << 4), in ? base + (int64_t)row * a.ldb + c0 + 8 * p : base, in);
+    }
+    for (int e = tid; e < kNC * 2 * steps; e += NT) {
+      const int n = e / (2 * steps), p = e % (2 * steps), q = n & 31;
+      const int row = (n & ~31) + ((q & 6) << 2) + 2 * (q >> 3) + (q & 1);  // 8 (n-tile) + lane group
+      const bool in = c0 + n < a.N && 8 * p < a.r;
+      cp16(bs + row * G::pitch + 16 * p, in ? B + (int64_t)(c0 + n) * a.r + 8 * p : B, in);
+    }
+  };
+  auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+  auto wait = [] { asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory"); };
+
+  float v[2 * RT][4];
+#pragma unroll
+  for (int j = 0; j < 2 * RT; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[j][i] = 0.f;
+  if (kst > 0) {
+    for (int s = 0; s < NS - 1; ++s) {
+      if (s < kst) fill_k(s, s);
+      commit();
+    }
+    for (int st = 0; st < kst; ++st) {
+      wait();
+      __syncthreads();  // the stage has landed for every thread, and the one refilled below is read
+      if (st + NS - 1 < kst) fill_k(st + NS - 1, (st + NS - 1) % NS);
+      commit();
+      const unsigned char* xs = ring + (st % NS) * G::stage;
+      const unsigned char* as = xs + G::xbytes;
+      if (16 * wm < tile.rows)
+#pragma unroll
+        for (int i = 0; i < kKC / 32 / WK; ++i) {
+          const int p = (4 * (i * WK + wk) + t) ^ ((g & 1) << 2);
+          const uint4 p0 = *(const uint4*)(xs + r0 * (kKC * 2) + 16 * p), p1 = *(const uint4*)(xs + r1 * (kKC * 2) + 16 * p);
+#pragma unroll
+          for (int j = 0; j < 2 * RT; ++j)
+            if ((j >> 1) < steps) {
+              const int row = 16 * (j >> 1) + 4 * (g >> 1) + 2 * (j & 1) + (g & 1);
+              const uint4 q = *(const uint4*)(as + row * (kKC * 2) + 16 * p);
+              mma_bf16(v[j], p0.x, p1.x, p0.y, p1.y, q.x, q.y);
+              mma_bf16(v[j], p0.z, p1.z, p0.w, p1.w, q.z, q.w);
+            }
+        }
+    }
+    __syncthreads();
+  }
+  // the first N stages are on their way (from stage 1 of the ring on) while the sums meet in stage 0
+  for (int s = 0; s < NS - 1; ++s) {
+    if (s < nst) fill_n(s, (s + 1) % NS);
+    commit();
+  }
+  if (WK == 2 && rk > 0) {
+    float4* sum = (float4*)ring + wm * 2 * RT * 32 + lane;
+    if (wk == 1)
+#pragma unroll
+      for (int j = 0; j < 2 * RT; ++j) sum[32 * j] = make_float4(v[j][0], v[j][1], v[j][2], v[j][3]);
+    __syncthreads();
+    if (wk == 0)
+#pragma unroll
+      for (int j = 0; j < 2 * RT; ++j) {
+        const float4 o = sum[32 * j];
+        v[j][0] += o.x;
+        v[j][1] += o.y;
+        v[j][2] += o.z;
+        v[j][3] += o.w;
+        sum[32 * j] = make_float4(v[j][0], v[j][1], v[j][2], v[j][3]);
+      }
+    __syncthreads();
+    if (wk == 1)
+#pragma unroll
+      for (int j = 0; j < 2 * RT; ++j) {
+        const float4 o = sum[32 * j];
+        v[j][0] = o.x;
+        v[j][1] = o.y;
+        v[j][2] = o.z;
+        v[j][3] = o.w;
+      }
+  }
+  uint32_t hi[RT][4], lo[RT][4];
+#pragma unroll
+  for (int s = 0; s < RT; ++s) split_v(v[2 * s], v[2 * s + 1], tile.scale, hi[s], lo[s]);
+  const bool ok0 = r0 < tile.rows, ok1 = r1 < tile.rows;
+  __nv_bfloat16 *o0 = a.out + (int64_t)(tile.t0 + r0) * a.ldo, *o1 = o0 + 8 * a.ldo;
+  for (int st = 0; st < nst; ++st) {
+    wait();
+    __syncthreads();
+    if (st + NS - 1 < nst) fill_n(st + NS - 1, (st + NS) % NS);
+    commit();
+    const unsigned char* ys = ring + ((st + 1) % NS) * G::stage;
+    const unsigned char* bs = ys + G::ybytes;
+    if (16 * wm >= tile.rows) continue;
+#pragma unroll
+    for (int i = 0; i < kNC / 32 / WK; ++i) {
+      const int c = 32 * (i * WK + wk), col = st * kNC + c + 8 * t;
+      if (st * kNC + c >= a.N) break;
+      const int p = (c / 8 + t) ^ ((g & 1) << 2);
+      const uint4 y0 = *(const uint4*)(ys + r0 * (kNC * 2) + 16 * p), y1 = *(const uint4*)(ys + r1 * (kNC * 2) + 16 * p);
+      const uint32_t w0[4] = {y0.x, y0.y, y0.z, y0.w}, w1[4] = {y1.x, y1.y, y1.z, y1.w};
+      uint32_t q0[4], q1[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float d[4] = {lo_f32(w0[j]), hi_f32(w0[j]), lo_f32(w1[j]), hi_f32(w1[j])};
+#pragma unroll
+        for (int s = 0; s < RT; ++s)
+          if (s < steps) {
+            uint2 b = *(const uint2*)(bs + (c + 8 * j + g) * G::pitch + 32 * s + 8 * t);
+            if (16 * s + 16 > rk) b = cut_rank(b, 16 * s + 4 * t, rk);
+            mma_bf16(d, lo[s][0], lo[s][1], lo[s][2], lo[s][3], b.x, b.y);
+            mma_bf16(d, hi[s][0], hi[s][1], hi[s][2], hi[s][3], b.x, b.y);
+          }
+        q0[j] = pack_bf16(d[0], d[1]);
+        q1[j] = pack_bf16(d[2], d[3]);
+      }
+      if (ok0 && col < a.N) *(uint4*)(o0 + col) = make_uint4(q0[0], q0[1], q0[2], q0[3]);
+      if (ok1 && col < a.N) *(uint4*)(o1 + col) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
+    }
+  }
+}
+
+// At most one partial tile per request.
+int64_t tile_bound(const AdapterArgs& a, int bm) { return (int64_t)a.T / bm + (a.R < a.T ? a.R : a.T); }
+
+template <int RT, int WM, int WK>
+cudaError_t launch_many(const AdapterArgs& a, cudaStream_t s) {
+  using G = Many<RT, WM, WK>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(adapter_many_kernel<RT, WM, WK>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::smem);
+  if (e != cudaSuccess) return e;
+  note_launches(1);
+  return launch_pdl(adapter_many_kernel<RT, WM, WK>, dim3((unsigned)tile_bound(a, G::BM)), dim3(G::threads), G::smem, s, a);
+}
+
+template <int RT>
+cudaError_t launch_few(const AdapterArgs& a, int cluster, cudaStream_t s) {
+  constexpr int smem = (kWarps + 1) * 2 * RT * 32 * 16;
   if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(adapter_kernel<RT, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(adapter_few_kernel<RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tile_bound(a, 16) * cluster));
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   note_launches(1);
-  return launch_pdl(adapter_kernel<RT, WM>, dim3((unsigned)tiles, parts), dim3(32 * kWarps), smem, s, a);
+  return cudaLaunchKernelEx(&cfg, adapter_few_kernel<RT>, a);
 }
 
 template <int RT>
 cudaError_t launch_rank(const AdapterArgs& a, cudaStream_t s) {
-  if (a.T / (a.R > 0 ? a.R : 1) >= 512) return launch_tiles<RT, 8>(a, 1, s);
-  const int64_t tiles = (int64_t)a.T / 16 + (a.R < a.T ? a.R : a.T);
-  const int parts = tiles >= 152 ? 1 : tiles >= 32 ? 4 : 8;
-  return launch_tiles<RT, 1>(a, parts, s);
+#ifndef ADAPTER_PROBE
+  const int64_t tiles = tile_bound(a, 16);
+  if (a.T / (a.R > 0 ? a.R : 1) >= 256 && a.T >= 4096) return launch_many<RT, 4, 2>(a, s);
+  return launch_few<RT>(a, tiles >= 256 ? 2 : tiles >= 128 ? 4 : 8, s);
+#else
+  
+  if (g_many == 1) return launch_many<RT, 4, 2>(a, s);
+  if (g_many == 2) return launch_many<RT, 8, 2>(a, s);
+  if (g_many == 3) return launch_many<RT, 8, 1>(a, s);
+  if (g_many == 4) return launch_many<RT, 2, 2>(a, s);
+  return launch_few<RT>(a, g_cluster, s);
+#endif
 }
 
 }  // namespace

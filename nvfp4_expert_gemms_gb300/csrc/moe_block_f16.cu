@@ -1,0 +1,6 @@
+// Norm and residual kernels for a residual stream in fp16 around a block in fp16.
+#include "moe_block_rows.cuh"
+
+namespace moe {
+MOE_BLOCK_TYPES(launch_block_f16, __half, __half, MOE_DT_F16)
+}  // namespace moe
