@@ -17,20 +17,27 @@ namespace moe {
 
 struct ScoreGeom {
   int S, lanes_log2, per;  // experts per group, log2 of lanes per group, experts per lane
-  bool wide;               // a lane's logits are whole 16-byte pieces
+  bool wide;               // a lane's logits are whole aligned 8- or 16-byte pieces; so is its share of the bias
 };
 
-// Order-preserving key: larger key = larger value, 0 = no candidate; -0 counts as +0, NaN as -inf.
-__device__ __forceinline__ uint32_t order_key(float v) {
-  v = isnan(v) ? -INFINITY : v == 0.f ? 0.f : v;
-  const uint32_t u = __float_as_uint(v);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
+// A candidate's place while a warp sorts out the best ones.
+struct ScoreCand {
+  float key;
+  int expert;
+};
+constexpr float kNoKey = __builtin_nanf("");  // not a candidate: compares false with everything, loses every max
 
 __device__ __forceinline__ float load_logit(const ScoreArgs& a, int64_t at) {
   float v;
   load_any<1>(a.logits, a.dtype, at, &v);
-  return isnan(v) ? -INFINITY : v;
+  return fmaxf(v, -INFINITY);  // NaN counts as -infinity
+}
+
+// Largest value over the warp; NaNs do not count (NaN if there is nothing else).
+__device__ __forceinline__ float redux_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 // 1 / (1 + e^-l), each step rounded once.
@@ -38,50 +45,167 @@ __device__ __forceinline__ float sigmoid_rn(float l) { return __frcp_rn(__fadd_r
 // e^(l - m); 0 for an empty row (m = -inf)
 __device__ __forceinline__ float exp_rn(float l, float m) { return m == -INFINITY ? 0.f : expf(__fsub_rn(l, m)); }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-  return v;
-}
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
   return v;
 }
 
-// Writes the token's top_k experts and weights; returns the lane's expert (lane < k).  VT >= g.per.
+// The experts e0 .. e0 + cnt - 1 of a lane, their logits as fp32 (NaN as -infinity; -infinity past cnt).
+template <int VT>
+__device__ __forceinline__ void load_logits(const ScoreArgs& a, const ScoreGeom& g, int64_t at, int cnt, float (&l)[VT]) {
+  if (a.dtype == MOE_DT_F32) {
+    const float* p = (const float*)a.logits + at;
+    if (VT >= 4 && g.wide) {
+#pragma unroll
+      for (int i = 0; i < VT / 4; ++i) {
+        const float4 q = cnt ? ((const float4*)p)[i] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        l[4 * i] = q.x;
+        l[(4 * i + 1) % VT] = q.y;
+        l[(4 * i + 2) % VT] = q.z;
+        l[(4 * i + 3) % VT] = q.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VT; ++i) l[i] = i < cnt ? p[i] : -INFINITY;
+    }
+  } else {
+    const uint16_t* p = (const uint16_t*)a.logits + at;
+    uint32_t w[VT];
+    if (VT >= 4 && g.wide) {
+#pragma unroll
+      for (int i = 0; i < VT / 4; ++i) {
+        const uint2 q = cnt ? ((const uint2*)p)[i] : make_uint2(0, 0);
+        w[4 * i] = q.x & 0xFFFFu;
+        w[(4 * i + 1) % VT] = q.x >> 16;
+        w[(4 * i + 2) % VT] = q.y & 0xFFFFu;
+        w[(4 * i + 3) % VT] = q.y >> 16;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VT; ++i) w[i] = i < cnt ? p[i] : 0u;
+    }
+    if (a.dtype == MOE_DT_BF16) {
+#pragma unroll
+      for (int i = 0; i < VT; ++i) l[i] = i < cnt ? __uint_as_float(w[i] << 16) : -INFINITY;
+    } else {
+#pragma unroll
+      for (int i = 0; i < VT; ++i) l[i] = i < cnt ? __half2float(__ushort_as_half((unsigned short)w[i])) : -INFINITY;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VT; ++i) l[i] = fmaxf(l[i], -INFINITY);
+}
+
+// The experts of the k largest keys, in descending order, ties to the lower expert: returned in lanes
+// 0 .. k-1.  Lane order is expert order.
+//
+// Of the lanes' own maxima, the k-th largest bounds the k-th largest key from below, so only keys at
+// least that large can be chosen: about k of them.  They move to one lane each and a lane counts how many
+// stand in front of its own -- a few instructions per candidate in place of k rounds over every key.
+template <int VT>
+__device__ __forceinline__ int pick_top(float (&key)[VT], int e0, int k, int lane, ScoreCand* cand) {
+  if constexpr (VT >= 4) {
+    float lm = key[0];
+#pragma unroll
+    for (int i = 1; i < VT; ++i) lm = fmaxf(lm, key[i]);
+    float bound = -INFINITY, rem = lm;  // fewer than k lanes with candidates: every candidate
+    for (int seen = 0; seen < k;) {
+      const float m = redux_max(rem);
+      const uint32_t eq = __ballot_sync(0xffffffffu, rem == m);
+      if (!eq) {
+        bound = -INFINITY;
+        break;
+      }
+      seen += __popc(eq);
+      bound = m;
+      rem = rem == m ? kNoKey : rem;
+    }
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < VT; ++i) c += key[i] >= bound;
+    int incl = c;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += o;
+    }
+    const int total = __shfl_sync(0xffffffffu, incl, 31);
+    if (total <= 32) {
+      ScoreCand* to = cand + incl - c;
+#pragma unroll
+      for (int i = 0; i < VT; ++i)
+        if (key[i] >= bound) *to++ = ScoreCand{key[i], e0 + i};
+      __syncwarp();
+      const ScoreCand mine = lane < total ? cand[lane] : ScoreCand{kNoKey, 0};
+      int front = 0;
+      for (int j = 0; j < total; ++j) {
+        const float o = __shfl_sync(0xffffffffu, mine.key, j);
+        front += o > mine.key || (o == mine.key && j < lane);
+      }
+      __syncwarp();
+      if (lane < total && front < k) cand[front].expert = mine.expert;
+      __syncwarp();
+      const int e = cand[lane < k ? lane : 0].expert;
+      __syncwarp();
+      return e;
+    }
+  }
+  int mine = 0;  // few keys per lane, or more than 32 equal ones at the bound: one expert per round
+  for (int j = 0; j < k; ++j) {
+    float bk = key[0];
+    int be = 0;
+#pragma unroll
+    for (int i = 1; i < VT; ++i) {
+      const bool up = key[i] > bk || (isnan(bk) && !isnan(key[i]));
+      bk = up ? key[i] : bk;
+      be = up ? i : be;
+    }
+    const float m = redux_max(bk);
+    const int wl = __ffs(__ballot_sync(0xffffffffu, bk == m)) - 1;
+    const int we = __shfl_sync(0xffffffffu, e0 + be, wl);
+#pragma unroll
+    for (int i = 0; i < VT; ++i)
+      if (lane == wl && i == be) key[i] = kNoKey;  // taken
+    if (lane == j) mine = we;
+  }
+  return mine;
+}
+
+// Writes the token's top_k experts and weights; returns the lane's expert (lane < k).  VT >= g.per; cand:
+// 32 entries of shared memory for this warp.
 template <int VT>
 __device__ __forceinline__ int score_token(const ScoreArgs& a, const ScoreGeom& g, int t, int k, int lane,
-                                           int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
+                                           int32_t* __restrict__ topk_idx, float* __restrict__ topk_w, ScoreCand* cand) {
   const int lanes = 1 << g.lanes_log2, grp = lane >> g.lanes_log2, sub = lane & (lanes - 1);
   const int e0 = grp * g.S + sub * g.per;
   const int cnt = grp < a.r.groups ? min(max(g.S - sub * g.per, 0), g.per) : 0;
   const int64_t row = (int64_t)t * a.ld;
-  float l[VT];
-  if (g.wide && VT % 4 == 0) {  // per == VT, every lane whole
-#pragma unroll
-    for (int i = 0; i < VT; i += 4) {
-      const float4 q = cnt ? *(const float4*)((const float*)a.logits + row + e0 + i)
-                           : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      l[i] = q.x;
-      l[i + 1 < VT ? i + 1 : 0] = q.y;
-      l[i + 2 < VT ? i + 2 : 0] = q.z;
-      l[i + 3 < VT ? i + 3 : 0] = q.w;
-    }
-#pragma unroll
-    for (int i = 0; i < VT; ++i) l[i] = isnan(l[i]) ? -INFINITY : l[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < VT; ++i) l[i] = i < cnt ? load_logit(a, row + e0 + i) : -INFINITY;
-  }
   const bool softmax = a.r.score == MOE_SCORE_SOFTMAX, biased = a.bias != nullptr;
   const bool two = a.r.groups > 1 && a.r.group_top == 2;
+  float l[VT], key[VT];
+  load_logits<VT>(a, g, row + e0, cnt, l);
+  if (biased) {  // held in key until the scores are there
+    if (VT >= 4 && g.wide) {
+#pragma unroll
+      for (int i = 0; i < VT / 4; ++i) {
+        const float4 q = cnt ? ((const float4*)(a.bias + e0))[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+        key[4 * i] = q.x;
+        key[(4 * i + 1) % VT] = q.y;
+        key[(4 * i + 2) % VT] = q.z;
+        key[(4 * i + 3) % VT] = q.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VT; ++i) key[i] = i < cnt ? a.bias[e0 + i] : 0.f;
+    }
+  }
   float m = 0.f, den = 1.f;  // the row's maximum and sum of e^(l - m), where a score needs them
   if (softmax && (biased || two || !a.r.renormalize)) {
     m = l[0];
 #pragma unroll
     for (int i = 1; i < VT; ++i) m = fmaxf(m, l[i]);
-    m = warp_max(m);
+    m = redux_max(m);
     if (biased || !a.r.renormalize) {
       den = 0.f;
 #pragma unroll
@@ -89,60 +213,53 @@ __device__ __forceinline__ int score_token(const ScoreArgs& a, const ScoreGeom& 
       den = warp_sum(den);
     }
   }
-  uint32_t key[VT];
   float b1 = -INFINITY, b2 = -INFINITY;  // the lane's two largest group values
+  if (biased) {
 #pragma unroll
-  for (int i = 0; i < VT; ++i) {
-    float kv = l[i], gv = l[i];
-    if (biased) {
+    for (int i = 0; i < VT; ++i) {
       const float s = softmax ? (den > 0.f ? __fdiv_rn(exp_rn(l[i], m), den) : 0.f) : sigmoid_rn(l[i]);
-      kv = gv = __fadd_rn(s, i < cnt ? a.bias[e0 + i] : 0.f);
-    } else if (two) {
-      gv = softmax ? exp_rn(l[i], m) : sigmoid_rn(l[i]);
+      key[i] = i < cnt ? fmaxf(__fadd_rn(s, key[i]), -INFINITY) : kNoKey;
     }
-    key[i] = i < cnt ? order_key(kv) : 0u;
-    gv = i < cnt && !isnan(gv) ? gv : -INFINITY;
-    b2 = fmaxf(b2, fminf(b1, gv));
-    b1 = fmaxf(b1, gv);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VT; ++i) key[i] = i < cnt ? l[i] : kNoKey;
   }
   if (a.r.groups > 1) {
+    if (!biased && two) {
+#pragma unroll
+      for (int i = 0; i < VT; ++i) {
+        const float s = i < cnt ? (softmax ? exp_rn(l[i], m) : sigmoid_rn(l[i])) : -INFINITY;
+        b2 = fmaxf(b2, fminf(b1, s));
+        b1 = fmaxf(b1, s);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VT; ++i) {
+        const float s = fmaxf(key[i], -INFINITY);
+        b2 = fmaxf(b2, fminf(b1, s));
+        b1 = fmaxf(b1, s);
+      }
+    }
     for (int off = lanes >> 1; off > 0; off >>= 1) {
       const float o1 = __shfl_xor_sync(0xffffffffu, b1, off), o2 = __shfl_xor_sync(0xffffffffu, b2, off);
       b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
       b1 = fmaxf(b1, o1);
     }
-    const uint32_t gk = order_key(two && g.S > 1 ? __fadd_rn(b1, b2) : b1);
-    int better = 0;  // groups in front of this one
+    const float gv = fmaxf(two && g.S > 1 ? __fadd_rn(b1, b2) : b1, -INFINITY);
+    int front = 0;  // groups in front of this one
     for (int h = 0; h < a.r.groups; ++h) {
-      const uint32_t o = __shfl_sync(0xffffffffu, gk, h << g.lanes_log2);
-      better += o > gk || (o == gk && h < grp);
+      const float o = __shfl_sync(0xffffffffu, gv, h << g.lanes_log2);
+      front += o > gv || (o == gv && h < grp);
     }
-    if (better >= a.r.top_groups)
+    if (front >= a.r.top_groups)
 #pragma unroll
-      for (int i = 0; i < VT; ++i) key[i] = 0u;
+      for (int i = 0; i < VT; ++i) key[i] = kNoKey;
   }
-  int mine = 0;
-  for (int j = 0; j < k; ++j) {
-    uint32_t bk = key[0];
-    int be = 0;
-#pragma unroll
-    for (int i = 1; i < VT; ++i)
-      if (key[i] > bk) {
-        bk = key[i];
-        be = i;
-      }
-    const uint32_t wk = __reduce_max_sync(0xffffffffu, bk);
-    const int wl = __ffs(__ballot_sync(0xffffffffu, bk == wk)) - 1;
-    const int we = __shfl_sync(0xffffffffu, e0 + be, wl);
-#pragma unroll
-    for (int i = 0; i < VT; ++i)
-      if (lane == wl && i == be) key[i] = 0u;  // taken
-    if (lane == j) mine = we;
-  }
+  const int mine = pick_top<VT>(key, e0, k, lane, cand);
   float s = 0.f;
   if (softmax && a.r.renormalize) {
     const float ls = lane < k ? load_logit(a, row + mine) : -INFINITY;
-    const float ms = warp_max(ls);
+    const float ms = redux_max(ls);
     s = lane < k ? exp_rn(ls, ms) : 0.f;
   } else if (lane < k) {
     const float ls = load_logit(a, row + mine);
@@ -171,8 +288,8 @@ inline ScoreGeom score_geom(const ScoreArgs& a, int E) {
   g.S = E / a.r.groups;
   g.lanes_log2 = lg;
   g.per = (g.S + (1 << lg) - 1) >> lg;
-  g.wide = a.dtype == MOE_DT_F32 && g.per % 4 == 0 && (g.per & (g.per - 1)) == 0 && g.S == g.per << lg &&
-           a.ld % 4 == 0 && (uintptr_t)a.logits % 16 == 0;
+  g.wide = g.per % 4 == 0 && (g.per & (g.per - 1)) == 0 && g.S == g.per << lg && a.ld % 4 == 0 &&
+           (uintptr_t)a.logits % (4 * dtype_size(a.dtype)) == 0 && (uintptr_t)a.bias % 16 == 0;
   return g;
 }
 
