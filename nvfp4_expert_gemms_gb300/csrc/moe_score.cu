@@ -10,7 +10,7 @@ template <int VT>
 __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const ScoreArgs a, const ScoreGeom g, int T, int k,
                                                                  int32_t* __restrict__ topk_idx,
                                                                  float* __restrict__ topk_w) {
-  __shared__ ScoreCand cand[kScoreWarps][32];
+  __shared__ ScoreCand cand[kScoreWarps][64];
   const int warp = threadIdx.x >> 5, t = blockIdx.x * kScoreWarps + warp;
   pdl_wait();
   pdl_trigger();

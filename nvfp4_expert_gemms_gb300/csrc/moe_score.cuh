@@ -103,23 +103,28 @@ __device__ __forceinline__ void load_logits(const ScoreArgs& a, const ScoreGeom&
 // Of the lanes' own maxima, the k-th largest bounds the k-th largest key from below, so only keys at
 // least that large can be chosen: about k of them.  They move to one lane each and a lane counts how many
 // stand in front of its own -- a few instructions per candidate in place of k rounds over every key.
-template <int VT>
-__device__ __forceinline__ int pick_top(float (&key)[VT], int e0, int k, int lane, ScoreCand* cand) {
+//
+// SURE: key holds the keys, and there is always an answer (more than 32 keys at the bound, which takes
+// many equal ones, go through k rounds after all).  Else key holds estimates, each at most slack(estimate)
+// off: the candidates are those that could be chosen, final_key(l, expert) gives a candidate's key from
+// val, the logits, and false is returned where that does not decide.
+__device__ __forceinline__ float key_slack(float key) { return 9.6e-7f + 2.4e-7f * fabsf(key); }
+
+template <bool SURE, int VT, class FinalKey>
+__device__ __forceinline__ bool pick_top(float (&key)[VT], const float (&val)[VT], int e0, int k, int lane,
+                                         ScoreCand* cand, FinalKey final_key, int& chosen) {
   if constexpr (VT >= 4) {
-    float lm = key[0];
+    float rem = key[0], bound = 0.f;
 #pragma unroll
-    for (int i = 1; i < VT; ++i) lm = fmaxf(lm, key[i]);
-    float bound = -INFINITY, rem = lm;  // fewer than k lanes with candidates: every candidate
-    for (int seen = 0; seen < k;) {
-      const float m = redux_max(rem);
-      const uint32_t eq = __ballot_sync(0xffffffffu, rem == m);
-      if (!eq) {
-        bound = -INFINITY;
-        break;
-      }
-      seen += __popc(eq);
-      bound = m;
-      rem = rem == m ? kNoKey : rem;
+    for (int i = 1; i < VT; ++i) rem = fmaxf(rem, key[i]);
+    for (int j = 0; j < k; ++j) {  // equal maxima leave together: the bound is then a little lower
+      bound = redux_max(rem);
+      rem = rem == bound ? kNoKey : rem;
+    }
+    bound = fmaxf(bound, -INFINITY);  // NaN, fewer than k lanes with candidates: every candidate
+    if (!SURE) {
+      if (isinf(bound)) return false;
+      bound -= 2.f * key_slack(bound);
     }
     int c = 0;
 #pragma unroll
@@ -135,23 +140,24 @@ __device__ __forceinline__ int pick_top(float (&key)[VT], int e0, int k, int lan
       ScoreCand* to = cand + incl - c;
 #pragma unroll
       for (int i = 0; i < VT; ++i)
-        if (key[i] >= bound) *to++ = ScoreCand{key[i], e0 + i};
+        if (key[i] >= bound) *to++ = ScoreCand{SURE ? key[i] : val[i], e0 + i};
       __syncwarp();
-      const ScoreCand mine = lane < total ? cand[lane] : ScoreCand{kNoKey, 0};
+      ScoreCand mine = lane < total ? cand[lane] : ScoreCand{kNoKey, 0};
+      if (!SURE && lane < total) mine.key = final_key(mine.key, mine.expert);
       int front = 0;
+#pragma unroll 4
       for (int j = 0; j < total; ++j) {
         const float o = __shfl_sync(0xffffffffu, mine.key, j);
-        front += o > mine.key || (o == mine.key && j < lane);
+        front += j < lane ? o >= mine.key : o > mine.key;
       }
+      if (lane < total && front < k) cand[32 + front].expert = mine.expert;
       __syncwarp();
-      if (lane < total && front < k) cand[front].expert = mine.expert;
+      chosen = cand[32 + (lane < k ? lane : 0)].expert;
       __syncwarp();
-      const int e = cand[lane < k ? lane : 0].expert;
-      __syncwarp();
-      return e;
+      return true;
     }
+    if (!SURE) return false;
   }
-  int mine = 0;  // few keys per lane, or more than 32 equal ones at the bound: one expert per round
   for (int j = 0; j < k; ++j) {
     float bk = key[0];
     int be = 0;
@@ -167,13 +173,23 @@ __device__ __forceinline__ int pick_top(float (&key)[VT], int e0, int k, int lan
 #pragma unroll
     for (int i = 0; i < VT; ++i)
       if (lane == wl && i == be) key[i] = kNoKey;  // taken
-    if (lane == j) mine = we;
+    if (lane == j) chosen = we;
   }
-  return mine;
+  return true;
+}
+
+// A group's value from its lanes' two largest (in every lane of the group): their sum, or the largest.
+__device__ __forceinline__ float group_value(float b1, float b2, int lanes, bool both) {
+  for (int off = lanes >> 1; off > 0; off >>= 1) {
+    const float o1 = __shfl_xor_sync(0xffffffffu, b1, off), o2 = __shfl_xor_sync(0xffffffffu, b2, off);
+    b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+    b1 = fmaxf(b1, o1);
+  }
+  return fmaxf(both ? __fadd_rn(b1, b2) : b1, -INFINITY);
 }
 
 // Writes the token's top_k experts and weights; returns the lane's expert (lane < k).  VT >= g.per; cand:
-// 32 entries of shared memory for this warp.
+// 64 entries of shared memory for this warp.
 template <int VT>
 __device__ __forceinline__ int score_token(const ScoreArgs& a, const ScoreGeom& g, int t, int k, int lane,
                                            int32_t* __restrict__ topk_idx, float* __restrict__ topk_w, ScoreCand* cand) {
@@ -183,21 +199,21 @@ __device__ __forceinline__ int score_token(const ScoreArgs& a, const ScoreGeom& 
   const int64_t row = (int64_t)t * a.ld;
   const bool softmax = a.r.score == MOE_SCORE_SOFTMAX, biased = a.bias != nullptr;
   const bool two = a.r.groups > 1 && a.r.group_top == 2;
-  float l[VT], key[VT];
+  float l[VT], bv[VT];
   load_logits<VT>(a, g, row + e0, cnt, l);
-  if (biased) {  // held in key until the scores are there
+  if (biased) {
     if (VT >= 4 && g.wide) {
 #pragma unroll
       for (int i = 0; i < VT / 4; ++i) {
         const float4 q = cnt ? ((const float4*)(a.bias + e0))[i] : make_float4(0.f, 0.f, 0.f, 0.f);
-        key[4 * i] = q.x;
-        key[(4 * i + 1) % VT] = q.y;
-        key[(4 * i + 2) % VT] = q.z;
-        key[(4 * i + 3) % VT] = q.w;
+        bv[4 * i] = q.x;
+        bv[(4 * i + 1) % VT] = q.y;
+        bv[(4 * i + 2) % VT] = q.z;
+        bv[(4 * i + 3) % VT] = q.w;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < VT; ++i) key[i] = i < cnt ? a.bias[e0 + i] : 0.f;
+      for (int i = 0; i < VT; ++i) bv[i] = i < cnt ? a.bias[e0 + i] : 0.f;
     }
   }
   float m = 0.f, den = 1.f;  // the row's maximum and sum of e^(l - m), where a score needs them
@@ -213,49 +229,90 @@ __device__ __forceinline__ int score_token(const ScoreArgs& a, const ScoreGeom& 
       den = warp_sum(den);
     }
   }
-  float b1 = -INFINITY, b2 = -INFINITY;  // the lane's two largest group values
-  if (biased) {
-#pragma unroll
-    for (int i = 0; i < VT; ++i) {
-      const float s = softmax ? (den > 0.f ? __fdiv_rn(exp_rn(l[i], m), den) : 0.f) : sigmoid_rn(l[i]);
-      key[i] = i < cnt ? fmaxf(__fadd_rn(s, key[i]), -INFINITY) : kNoKey;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < VT; ++i) key[i] = i < cnt ? l[i] : kNoKey;
-  }
-  if (a.r.groups > 1) {
-    if (!biased && two) {
+  int mine = 0;
+  bool done = false;
+  if constexpr (VT >= 4) {
+    // Sigmoid keys with a bias: the fast exponential and division place every key to within key_slack
+    // (__expf: 2 + 1.173 |l| units, less than 1e-7 of the score after its slope; the division 2 units;
+    // the sum's rounding), which leaves few experts that could be chosen, and only those get their exact
+    // key.  Where groups or keys stand closer than that, everything is done exactly below.
+    if (biased && !softmax) {
+      float est[VT], b1 = -INFINITY, b2 = -INFINITY;
 #pragma unroll
       for (int i = 0; i < VT; ++i) {
-        const float s = i < cnt ? (softmax ? exp_rn(l[i], m) : sigmoid_rn(l[i])) : -INFINITY;
-        b2 = fmaxf(b2, fminf(b1, s));
-        b1 = fmaxf(b1, s);
+        const float v = __fdividef(1.f, 1.f + __expf(-l[i])) + bv[i];
+        est[i] = i < cnt ? fmaxf(v, -INFINITY) : kNoKey;
+      }
+      bool clear = true;
+      if (a.r.groups > 1) {
+#pragma unroll
+        for (int i = 0; i < VT; ++i) {
+          const float s = fmaxf(est[i], -INFINITY);
+          b2 = fmaxf(b2, fminf(b1, s));
+          b1 = fmaxf(b1, s);
+        }
+        const bool both = two && g.S > 1;
+        const float gv = group_value(b1, b2, lanes, both);
+        const float gap = 4.f * key_slack(gv), hi = gv + gap, lo = gv - gap;
+        int front = 0, near = 0;  // groups surely in front, and those that may be
+        for (int h = 0; h < a.r.groups; ++h) {
+          const float o = __shfl_sync(0xffffffffu, gv, h << g.lanes_log2);
+          front += o > hi;
+          near += o >= lo;
+        }
+        // itself counts among the near ones
+        clear = grp >= a.r.groups || (!isinf(gv) && (front < a.r.top_groups) == (near - 1 < a.r.top_groups));
+        if (front >= a.r.top_groups)
+#pragma unroll
+          for (int i = 0; i < VT; ++i) est[i] = kNoKey;
+      }
+      if (__all_sync(0xffffffffu, clear))
+        done = pick_top<false, VT>(est, l, e0, k, lane, cand,
+                                   [&](float lv, int e) { return fmaxf(__fadd_rn(sigmoid_rn(lv), a.bias[e]), -INFINITY); },
+                                   mine);
+    }
+  }
+  if (!done) {
+    float key[VT];
+    if (biased) {
+#pragma unroll
+      for (int i = 0; i < VT; ++i) {
+        const float s = softmax ? (den > 0.f ? __fdiv_rn(exp_rn(l[i], m), den) : 0.f) : sigmoid_rn(l[i]);
+        key[i] = i < cnt ? fmaxf(__fadd_rn(s, bv[i]), -INFINITY) : kNoKey;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < VT; ++i) {
-        const float s = fmaxf(key[i], -INFINITY);
-        b2 = fmaxf(b2, fminf(b1, s));
-        b1 = fmaxf(b1, s);
-      }
+      for (int i = 0; i < VT; ++i) key[i] = i < cnt ? l[i] : kNoKey;
     }
-    for (int off = lanes >> 1; off > 0; off >>= 1) {
-      const float o1 = __shfl_xor_sync(0xffffffffu, b1, off), o2 = __shfl_xor_sync(0xffffffffu, b2, off);
-      b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
-      b1 = fmaxf(b1, o1);
-    }
-    const float gv = fmaxf(two && g.S > 1 ? __fadd_rn(b1, b2) : b1, -INFINITY);
-    int front = 0;  // groups in front of this one
-    for (int h = 0; h < a.r.groups; ++h) {
-      const float o = __shfl_sync(0xffffffffu, gv, h << g.lanes_log2);
-      front += o > gv || (o == gv && h < grp);
-    }
-    if (front >= a.r.top_groups)
+    if (a.r.groups > 1) {
+      float b1 = -INFINITY, b2 = -INFINITY;  // the lane's two largest group values
+      if (!biased && two) {
 #pragma unroll
-      for (int i = 0; i < VT; ++i) key[i] = kNoKey;
+        for (int i = 0; i < VT; ++i) {
+          const float s = i < cnt ? (softmax ? exp_rn(l[i], m) : sigmoid_rn(l[i])) : -INFINITY;
+          b2 = fmaxf(b2, fminf(b1, s));
+          b1 = fmaxf(b1, s);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < VT; ++i) {
+          const float s = fmaxf(key[i], -INFINITY);
+          b2 = fmaxf(b2, fminf(b1, s));
+          b1 = fmaxf(b1, s);
+        }
+      }
+      const float gv = group_value(b1, b2, lanes, two && g.S > 1);
+      int front = 0;  // groups in front of this one
+      for (int h = 0; h < a.r.groups; ++h) {
+        const float o = __shfl_sync(0xffffffffu, gv, h << g.lanes_log2);
+        front += o > gv || (o == gv && h < grp);
+      }
+      if (front >= a.r.top_groups)
+#pragma unroll
+        for (int i = 0; i < VT; ++i) key[i] = kNoKey;
+    }
+    pick_top<true, VT>(key, l, e0, k, lane, cand, [](float v, int) { return v; }, mine);
   }
-  const int mine = pick_top<VT>(key, e0, k, lane, cand);
   float s = 0.f;
   if (softmax && a.r.renormalize) {
     const float ls = lane < k ? load_logit(a, row + mine) : -INFINITY;
