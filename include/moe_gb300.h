@@ -414,6 +414,12 @@ moe_status_t moe_adapters_add(const void* x, int64_t ldx, const void* base, int6
                               const float* scale, const int32_t* rank, const int32_t* starts, const int32_t* slot,
                               void* out, int64_t ldo, int T, int R, int n, int r, int H, int N, moe_stream_t stream);
 
+/* Synchronise `stream`, then read and clear the current device's error word of moe_adapters_add (it has no
+ * workspace to keep one in): MOE_OK, or MOE_ERR_DEVICE_TIMEOUT if a bounded device wait gave up and left
+ * rows unwritten.  Errors: MOE_ERR_INVALID_ARG for a null code; MOE_ERR_CUDA if a copy or the
+ * synchronisation fails. */
+moe_status_t moe_get_adapter_error(moe_stream_t stream, int32_t* code);
+
 /* ---- measurement hooks ------------------------------------------------------------------ */
 
 /* Total number of CUDA kernels this library has enqueued in the calling process (all threads,

@@ -33,12 +33,12 @@ EXPORTS = ("moe_packed_size", "moe_pack_experts", "moe_workspace_size", "moe_lay
            "moe_debug_route", "moe_debug_dequant", "moe_debug_quant_act", "moe_kernel_launch_count",
            "moe_time_next_step", "moe_layer_forward_static_act", "moe_calibrate_act_scales",
            "moe_debug_quant_act_static", "moe_debug_quant_act_fp8", "moe_debug_wait_timeout", "moe_block_enter",
-           "moe_block_leave", "moe_route_scored", "moe_layer_forward_scored", "moe_adapters_add")
+           "moe_block_leave", "moe_route_scored", "moe_layer_forward_scored", "moe_adapters_add", "moe_get_adapter_error")
 
 # The operators around the experts live in block.py (which needs torch at import) and are names of
 # this package too.
 _BLOCK = ("Norm", "Router", "MoEBlock", "moe_block_enter", "moe_block_leave", "moe_route_scored",
-          "moe_layer_forward_scored", "moe_adapters_add")
+          "moe_layer_forward_scored", "moe_adapters_add", "moe_get_adapter_error")
 
 
 def __getattr__(name):

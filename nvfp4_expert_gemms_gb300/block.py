@@ -60,6 +60,7 @@ def _f():
         L.moe_block_leave.argtypes = [P, Q, I, P, Q, I, P, P, Q, I, I, I, F, F, P, P, Q, P, Q, I, I, P]
         L.moe_route_scored.argtypes = [P, P, Q, I, P, I, I, I, P, P, P]
         L.moe_layer_forward_scored.argtypes = [P, P, P, Q, I, P, I, C.POINTER(PackedDesc), P, I, P, P, C.c_size_t, P]
+        L.moe_get_adapter_error.argtypes = [P, C.POINTER(C.c_int32)]
         L.moe_adapters_add.argtypes = [P, Q, P, Q, P, P, P, P, P, P, P, Q] + [I] * 6 + [P]
         _fns = L
     return _fns
@@ -179,6 +180,14 @@ def moe_layer_forward_scored(x, logits, router: Router, desc, packed, top_k: int
                                          C.byref(desc), packed.data_ptr(), top_k, out.data_ptr(), workspace.data_ptr(),
                                          workspace.numel() * workspace.element_size(),
                                          torch.cuda.current_stream(x.device).cuda_stream if stream is None else _handle(stream)), where)
+
+
+def moe_get_adapter_error(stream=None) -> int:
+    """Synchronise the stream, then read and clear the current device's error word of moe_adapters_add (0: none)."""
+    code = C.c_int32()
+    _check(_f().moe_get_adapter_error(torch.cuda.current_stream().cuda_stream if stream is None else _handle(stream),
+                                      C.byref(code)), "moe_get_adapter_error")
+    return code.value
 
 
 class MoEBlock:

@@ -17,7 +17,7 @@
 // reads of A and B (L2) small ones.
 #include <cooperative_groups.h>
 
-#include "moe_block.cuh"
+#include "moe_adapter.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -33,73 +33,6 @@ __device__ __forceinline__ void mma_bf16(float* d, uint32_t a0, uint32_t a1, uin
       "%2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *(const uint32_t*)&v;
-}
-__device__ __forceinline__ float lo_f32(uint32_t p) { return __uint_as_float(p << 16); }
-__device__ __forceinline__ float hi_f32(uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); }
-
-struct Tile {
-  int slot, t0, rows, rk;  // adapter (-1: none), first token, tokens (0: past the last tile), rank in use
-  float scale;
-};
-
-// Tile `want` of all: requests are cut into tiles of bm tokens in order.  Every thread of the block
-// calls it.  A thread also reads its request's rank and scale, whether or not the tile turns out to be
-// its own: that way they cost no further trip to memory.
-template <int WARPS>
-__device__ __forceinline__ Tile find_tile(const AdapterArgs& a, int want, int bm) {
-  __shared__ int wsum[WARPS];
-  __shared__ Tile found;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) found = Tile{-1, 0, 0, 0, 1.f};
-  int before = 0;  // tiles of the requests in front of this chunk
-  for (int q0 = 0; q0 < a.R; q0 += WARPS * 32) {
-    const int q = q0 + tid;
-    int s = 0, e = 0, sl = -1, rk = 0;
-    float sc = 1.f;
-    if (q < a.R) {
-      s = a.starts[q];
-      e = a.starts[q + 1];
-      sl = a.slot[q];
-      s = min(max(s, 0), a.T);
-      e = min(max(e, s), a.T);
-      if (sl >= 0 && sl < a.n) {
-        rk = a.rank ? min(max(a.rank[sl], 0), a.r) : a.r;
-        if (a.scale) sc = a.scale[sl];
-      } else {
-        sl = -1;
-      }
-    }
-    const int n = (e - s + bm - 1) / bm;
-    int run = n;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, run, off);
-      if (lane >= off) run += o;
-    }
-    if (lane == 31) wsum[warp] = run;
-    __syncthreads();
-    int base = before, all = 0;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      base += w < warp ? wsum[w] : 0;
-      all += wsum[w];
-    }
-    const int first = base + run - n;
-    if (want >= first && want < first + n) {
-      const int t0 = s + (want - first) * bm;
-      found = Tile{sl, t0, min(bm, e - t0), rk, sc};
-    }
-    before += all;
-    __syncthreads();
-    if (want < before) break;
-  }
-  __syncthreads();
-  return found;
 }
 
 // v (the sums of one rank step's two MMA tiles) times the adapter's scale, as the second product's A
@@ -477,9 +410,6 @@ __global__ void __launch_bounds__(32 * WM * WK) adapter_many_kernel(const Adapte
   }
 }
 
-// At most one partial tile per request.
-int64_t tile_bound(const AdapterArgs& a, int bm) { return (int64_t)a.T / bm + (a.R < a.T ? a.R : a.T); }
-
 template <int RT, int WM, int WK>
 cudaError_t launch_many(const AdapterArgs& a, cudaStream_t s) {
   using G = Many<RT, WM, WK>;
@@ -519,14 +449,16 @@ template <int RT>
 cudaError_t launch_rank(const AdapterArgs& a, cudaStream_t s) {
 #ifndef ADAPTER_PROBE
   const int64_t tiles = tile_bound(a, 16);
+  if (a.T / (a.R > 0 ? a.R : 1) >= 128 && adapter_tiles_fit(a)) return launch_adapter_tiles(a, s);
   if (a.T / (a.R > 0 ? a.R : 1) >= 256 && a.T >= 4096) return launch_many<RT, 4, 2>(a, s);
-  return launch_few<RT>(a, tiles >= 256 ? 2 : tiles >= 128 ? 4 : 8, s);
+  return launch_few<RT>(a, tiles > 76 ? 1 : tiles > 38 ? 2 : tiles > 19 ? 4 : 8, s);
 #else
   
   if (g_many == 1) return launch_many<RT, 4, 2>(a, s);
   if (g_many == 2) return launch_many<RT, 8, 2>(a, s);
   if (g_many == 3) return launch_many<RT, 8, 1>(a, s);
   if (g_many == 4) return launch_many<RT, 2, 2>(a, s);
+  if (g_many == 5) return launch_adapter_tiles(a, s);
   return launch_few<RT>(a, g_cluster, s);
 #endif
 }

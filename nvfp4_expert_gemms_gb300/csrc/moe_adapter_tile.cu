@@ -1,0 +1,434 @@
+// Request adapters for long requests: one block per tile of 128 tokens of one request, both products on
+// the 5th-generation tensor cores.
+//
+//   v = X A^T        M = 128 tokens, N = the adapter's rank (in steps of 16), K = H
+//   out = base + (scale v) B^T   M = 128, N = 128 columns at a time, K = rank, twice: v enters as two
+//                                bf16 terms, hi = bf16(v) and lo = bf16(v - hi) (16 bits of significand)
+//
+// X and A, then B, arrive by TMA in the 128-byte swizzle that the MMA reads, through one ring of shared
+// memory that is cut into stages of 64 columns for the first product and of 128 rows of B for the second.
+// v goes from tensor memory through registers (scaled, split, zero past the adapter's rank) back into
+// shared memory as the second product's A operand.  The accumulator of the second product has two
+// 128-column buffers (the first one lies where v's sums were), so the epilogue of one column block runs
+// under the MMAs of the next; it fetches base ahead of the accumulator, 32 bytes per lane and row, and
+// writes whole 32-byte sectors.
+//
+// Bound: HBM bytes of x, base and out.  An MMA's cost hardly depends on N here, so rank 128 costs little
+// more than rank 16; the register MMAs of moe_adapter.cu, whose cost grows with the rank, fall behind.
+//
+// Every wait gives up after about a second (moe_tc.cuh); the block then waits, with the same limit, for
+// its own copies and MMAs, frees its tensor memory, leaves its rows unfinished and records a timeout that
+// moe_get_adapter_error reads.
+#include <cudaTypedefs.h>
+#include <string.h>
+
+#include <atomic>
+
+#include "moe_adapter.cuh"
+#include "moe_tc.cuh"
+
+namespace moe {
+namespace {
+
+using namespace tc;
+
+__device__ int g_adapter_error;  // kDevOk or the first failure
+
+constexpr int kBM = 128, kEpiWarps = 8, kTileWarps = kEpiWarps + 3, kMaxSlots = 8;
+constexpr int kAtom = 128 * 128;  // bytes: 128 rows of 64 bf16 columns in the 128-byte swizzle
+constexpr int kNB = 256;          // rows of B per stage: two column blocks of the accumulator
+constexpr int kTmemCols = 256;
+constexpr int kSmem = 226 * 1024;  // of a block, one per SM: v, then the ring
+
+struct TileArgs {
+  CUtensorMap x, a, b;
+  AdapterArgs g;
+  int r16, katoms;    // rank in steps of 16 (all adapters), 64-column atoms of B
+  int ka, kslot;      // 64-column atoms and bytes of a K stage
+  int nk, nn;         // stages of the ring for the two products
+};
+
+struct Bars {
+  uint64_t full_k[kMaxSlots], empty_k[kMaxSlots], full_n[kMaxSlots], cut_n[kMaxSlots], empty_n[kMaxSlots];
+  uint64_t v_sums, v_ready, acc_full[2], acc_empty[2], done;
+  uint32_t tmem;
+  int abort;
+};
+
+// Byte of column chunk j (8 bf16) of row `row` in an operand of 64-column atoms.
+__device__ __forceinline__ uint32_t swz(int row, int j) {
+  return (j >> 3) * kAtom + row * 128 + (((j & 7) ^ (row & 7)) << 4);
+}
+
+// 16 tensor-memory lanes x 64 columns as fragments: v[4 j + 2 u + i] is row (lane / 4) + 8 u, column
+// 8 j + 2 (lane % 4) + i.
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+// B's rows, 256 from row 64 g on, dealt as the epilogue wants them (rows_map).
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int g) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %4, %4, "
+      "%5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(m), "r"(smem_u32(bar)), "r"(c0), "r"(0), "r"(g)
+      : "memory");
+}
+
+// A wait of the clean-up: with the limit, whatever the block's state.
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
+  int never = 0;
+  mbar_wait(bar, parity, &never);
+}
+
+__global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __grid_constant__ TileArgs p) {
+  extern __shared__ unsigned char dyn[];
+  __shared__ Bars bars;
+  const AdapterArgs& a = p.g;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();
+  const Tile tile = find_tile<kTileWarps>(a, blockIdx.x, kBM);
+  if (tile.rows == 0) return;
+  const int rk = tile.rk, steps = (rk + 15) / 16;
+  if (rk == 0) {  // no adapter: base as it is
+    if (a.out == a.base) return;
+    const int chunks = a.N / 8;
+    for (int64_t e = tid; e < (int64_t)tile.rows * chunks; e += 32 * kTileWarps) {
+      const int64_t t = tile.t0 + e / chunks;
+      const int c = (int)(e % chunks) * 8;
+      *(uint4*)(a.out + t * a.ldo + c) = *(const uint4*)(a.base + t * a.ldb + c);
+    }
+    return;
+  }
+  unsigned char* v_mem = (unsigned char*)(((uintptr_t)dyn + 1023) & ~(uintptr_t)1023);
+  unsigned char* ring = v_mem + 2 * p.katoms * kAtom;  // v's hi and lo, then the stages
+  const int natom = kNB * 128, nslot = p.katoms * natom;
+  const int atoms = (a.H + 63) / 64, kst = (atoms + p.ka - 1) / p.ka;
+  const int nblk = (a.N + 127) / 128, nst = (a.N + kNB - 1) / kNB;  // accumulator column blocks, stages of B
+  const bool partial = rk % 16 != 0;  // the last rank step of B holds columns that are not the adapter's
+  if (tid == 0) {
+    for (int i = 0; i < kMaxSlots; ++i) {
+      mbar_init(&bars.full_k[i], 1);
+      mbar_init(&bars.empty_k[i], 1);
+      mbar_init(&bars.full_n[i], 1);
+      mbar_init(&bars.cut_n[i], 1);
+      mbar_init(&bars.empty_n[i], 1);
+    }
+    mbar_init(&bars.v_sums, 1);
+    mbar_init(&bars.v_ready, 32 * kEpiWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.acc_full[i], 1);
+      mbar_init(&bars.acc_empty[i], kEpiWarps);
+    }
+    mbar_init(&bars.done, 1);
+    bars.abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) tmem_alloc(&bars.tmem, kTmemCols);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = bars.tmem;
+  volatile int* abort = &bars.abort;
+
+  if (warp == kEpiWarps) {  // ---- copies
+    if (lane == 0) {
+      prefetch_tmap(&p.x);
+      prefetch_tmap(&p.a);
+      prefetch_tmap(&p.b);
+      const uint32_t kbytes = p.kslot;
+      int k = 0, n = 0;
+      for (; k < kst; ++k) {
+        const int s = k % p.nk, u = k / p.nk;
+        if (u > 0 && !mbar_wait(&bars.empty_k[s], (u - 1) & 1, abort)) break;
+        unsigned char* at = ring + s * p.kslot;
+        mbar_arrive_expect_tx(&bars.full_k[s], kbytes);
+        if (p.ka == 1) {
+          tma_load_2d(at, &p.x, &bars.full_k[s], 64 * k, tile.t0);
+          tma_load_2d(at + kAtom, &p.a, &bars.full_k[s], 64 * k, tile.slot * a.r);
+        } else {  // atoms past H arrive as zeros
+          tma_load_3d(at, &p.x, &bars.full_k[s], 0, tile.t0, p.ka * k);
+          tma_load_3d(at + p.ka * kAtom, &p.a, &bars.full_k[s], 0, tile.slot * a.r, p.ka * k);
+        }
+      }
+      if (k == kst && mbar_wait(&bars.v_sums, 0, abort)) {  // every K stage has been read
+        for (; n < nst; ++n) {
+          const int s = n % p.nn, u = n / p.nn;
+          if (u > 0 && !mbar_wait(&bars.empty_n[s], (u - 1) & 1, abort)) break;
+          unsigned char* at = ring + s * nslot;
+          mbar_arrive_expect_tx(&bars.full_n[s], nslot);
+          for (int i = 0; i < p.katoms; ++i)
+            tma_load_5d(at + i * natom, &p.b, &bars.full_n[s], 64 * i, (tile.slot * a.N + kNB * n) / 64);
+        }
+      }
+      if (*abort) {  // copies in flight land before the block leaves
+        for (int i = k > p.nk ? k - p.nk : 0; i < k; ++i) drain(&bars.full_k[i % p.nk], (i / p.nk) & 1);
+        for (int i = n > p.nn ? n - p.nn : 0; i < n; ++i) drain(&bars.full_n[i % p.nn], (i / p.nn) & 1);
+      }
+    }
+  } else if (warp == kEpiWarps + 1) {  // ---- MMAs
+    if (lane == 0) {
+      const uint32_t id1 = idesc_bf16_f32(128, 16 * steps), id2 = idesc_bf16_f32(128, 128);
+      bool ok = true;
+      for (int k = 0; ok && k < kst; ++k) {
+        const int s = k % p.nk;
+        ok = mbar_wait(&bars.full_k[s], (k / p.nk) & 1, abort);
+        if (!ok) break;
+        fence_after_sync();
+        const uint32_t xs = smem_u32(ring + s * p.kslot), as = xs + p.ka * kAtom;
+        const int here = atoms - p.ka * k < p.ka ? atoms - p.ka * k : p.ka;
+        for (int i = 0; i < 4 * here; ++i)
+          mma_f16_ss(tmem, sdesc_k_sw128(xs + (i >> 2) * kAtom + (i & 3) * 32),
+                     sdesc_k_sw128(as + (i >> 2) * p.r16 * 128 + (i & 3) * 32), id1, (k | i) != 0);
+        mma_commit(&bars.empty_k[s]);
+      }
+      if (ok) {
+        mma_commit(&bars.v_sums);
+        ok = mbar_wait(&bars.v_ready, 0, abort);
+        fence_after_sync();
+      }
+      const uint32_t hi = smem_u32(v_mem), lo = hi + p.katoms * kAtom;
+      for (int n = 0; ok && n < nblk; ++n) {
+        const int st = n >> 1, s = st % p.nn, buf = n & 1;
+        if (n > 1) ok = mbar_wait(&bars.acc_empty[buf], ((n >> 1) - 1) & 1, abort);
+        if (ok && buf == 0) ok = mbar_wait(partial ? &bars.cut_n[s] : &bars.full_n[s], (st / p.nn) & 1, abort);
+        if (!ok) break;
+        fence_after_sync();
+        const uint32_t bs = smem_u32(ring + s * nslot) + buf * kAtom, acc = tmem + 128 * buf;
+        for (int i = 0; i < steps; ++i) {
+          const uint32_t off = (i >> 2) * kAtom + (i & 3) * 32;
+          const uint64_t b = sdesc_k_sw128(bs + (i >> 2) * natom + (i & 3) * 32);
+          mma_f16_ss(acc, sdesc_k_sw128(lo + off), b, id2, i != 0);
+          mma_f16_ss(acc, sdesc_k_sw128(hi + off), b, id2, 1);
+        }
+        if (buf == 1 || n == nblk - 1) mma_commit(&bars.empty_n[s]);
+        mma_commit(&bars.acc_full[buf]);
+      }
+      mma_commit(&bars.done);  // no arrival is on its way into this block's barriers when it leaves
+      drain(&bars.done, 0);
+    }
+  } else if (warp == kEpiWarps + 2) {  // ---- columns of B past the adapter's rank, where a step has some
+    if (partial) {
+      const int c0 = rk / 8, c1 = 2 * steps;  // 8-column chunks from the partial one on
+      for (int n = 0; n < nst; ++n) {
+        const int s = n % p.nn;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars.full_n[s], (n / p.nn) & 1, abort))) break;
+        unsigned char* bs = ring + s * nslot;
+        for (int row = lane; row < kNB; row += 32)
+          for (int c = c0; c < c1; ++c) {
+            uint4* q = (uint4*)(bs + (c >> 3) * natom + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+            const int keep = rk - 8 * c;  // columns of the chunk that stay
+            uint4 w = keep > 0 ? *q : make_uint4(0, 0, 0, 0);
+            uint32_t* e = (uint32_t*)&w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] = keep >= 2 * i + 2 ? e[i] : keep == 2 * i + 1 ? e[i] & 0xFFFFu : 0u;
+            *q = w;
+          }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.cut_n[s]);
+      }
+    }
+  } else {  // ---- v into shared memory, then out
+    const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
+    bool ok = __all_sync(0xffffffffu, mbar_wait(&bars.v_sums, 0, abort));
+    if (ok) {
+      fence_after_sync();
+      for (int s = half; s < steps; s += 2) {
+        uint32_t w[16];
+        tmem_ld_32x16(taddr(tmem, 32 * quarter, 16 * s), w);
+        tmem_ld_wait();
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float c0 = 16 * s + 2 * i < rk ? __uint_as_float(w[2 * i]) * tile.scale : 0.f;
+          const float c1 = 16 * s + 2 * i + 1 < rk ? __uint_as_float(w[2 * i + 1]) * tile.scale : 0.f;
+          hi[i] = pack_bf16(c0, c1);
+          lo[i] = pack_bf16(c0 - lo_f32(hi[i]), c1 - hi_f32(hi[i]));
+        }
+        unsigned char* to = v_mem;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          *(uint4*)(to + swz(row, 2 * s + h)) = make_uint4(hi[4 * h], hi[4 * h + 1], hi[4 * h + 2], hi[4 * h + 3]);
+          *(uint4*)(to + p.katoms * kAtom + swz(row, 2 * s + h)) =
+              make_uint4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]);
+        }
+      }
+      fence_before_sync();
+      fence_proxy_async_smem();
+      mbar_arrive(&bars.v_ready);
+    }
+    // The accumulator's fragments give a lane 16 consecutive columns (the map of B deals its rows so) of four
+    // rows of the tile: four lanes hold a row's 128 bytes.
+    const int g = lane >> 2, t = lane & 3;
+    const __nv_bfloat16* base[4];
+    __nv_bfloat16* out[4];
+    bool live[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 32 * quarter + g + 8 * i;
+      live[i] = r < tile.rows;
+      const int64_t at = tile.t0 + (live[i] ? r : 0);
+      base[i] = a.base + at * a.ldb + 64 * half + 16 * t;
+      out[i] = a.out + at * a.ldo + 64 * half + 16 * t;
+    }
+    uint4 y[4][2], next[4][2];
+    auto fetch = [&](uint4(&q)[4][2], int n) {  // the lane's columns of base in block n
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (live[i] && 128 * n + 64 * half < a.N)
+          asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                       : "=r"(q[i][0].x), "=r"(q[i][0].y), "=r"(q[i][0].z), "=r"(q[i][0].w), "=r"(q[i][1].x),
+                         "=r"(q[i][1].y), "=r"(q[i][1].z), "=r"(q[i][1].w)
+                       : "l"(base[i] + 128 * n)
+                       : "memory");
+    };
+    if (ok) fetch(next, 0);
+    for (int n = 0; ok && n < nblk; ++n) {
+      const int buf = n & 1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[i][0] = next[i][0];
+        y[i][1] = next[i][1];
+      }
+      if (n + 1 < nblk) fetch(next, n + 1);
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars.acc_full[buf], (n >> 1) & 1, abort));
+      if (!ok) break;
+      fence_after_sync();
+      uint32_t w[2][32];
+      tmem_ld_16x64(taddr(tmem, 32 * quarter, 128 * buf + 64 * half), w[0]);
+      tmem_ld_16x64(taddr(tmem, 32 * quarter + 16, 128 * buf + 64 * half), w[1]);
+      tmem_ld_wait();
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (live[i] && 128 * n + 64 * half < a.N) {
+          const uint32_t* b = (const uint32_t*)y[i];
+          uint32_t o[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            o[j] = pack_bf16(lo_f32(b[j]) + __uint_as_float(w[i >> 1][4 * j + 2 * (i & 1)]),
+                             hi_f32(b[j]) + __uint_as_float(w[i >> 1][4 * j + 2 * (i & 1) + 1]));
+          st_global_v8(out[i] + 128 * n, o);
+        }
+    }
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  if (warp == 0) {
+    tmem_relinquish();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  if (tid == 0 && bars.abort) set_dev_error(&g_adapter_error, kDevTimeout);
+}
+
+}  // namespace
+
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 fn = known.load(std::memory_order_relaxed);
+  if (!fn) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess)
+      fn = (PFN_cuTensorMapEncodeTiled_v12000)f;
+    known.store(fn, std::memory_order_relaxed);
+  }
+  return fn;
+}
+
+static bool bf16_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                     const cuuint32_t* box) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows of a [rows, cols] bf16 matrix as [cols / 64 atoms][rows][64]: one copy brings `height` rows x ka atoms.
+static bool atoms_map(CUtensorMap* m, const void* base, uint64_t rows, int cols, int64_t ld, int height, int ka) {
+  const cuuint64_t dims[3] = {64, rows, (cuuint64_t)cols / 64}, strides[2] = {(cuuint64_t)ld * 2, 128};
+  const cuuint32_t box[3] = {64, (cuuint32_t)height, (cuuint32_t)ka};
+  return bf16_map(m, base, 3, dims, strides, box);
+}
+
+// Rows of B [rows, r], 64 at a time in the order (j, a, b) of row 16 a + 2 j + b (a < 4, j < 8, b < 2): the
+// accumulator's column 8 j + 2 a + b is then output column 16 a + 2 j + b, and a lane's fragment (a = lane % 4)
+// 16 consecutive ones.  rows is a multiple of 64.
+static bool rows_map(CUtensorMap* m, const void* base, uint64_t rows, int r) {
+  const cuuint64_t one = (cuuint64_t)r * 2;
+  const cuuint64_t dims[5] = {(cuuint64_t)r, 2, 4, 8, rows / 64}, strides[4] = {one, 16 * one, 2 * one, 64 * one};
+  const cuuint32_t box[5] = {64, 2, 4, 8, kNB / 64};
+  return bf16_map(m, base, 5, dims, strides, box);
+}
+
+// 32-byte accesses to base and out, whole 64-column groups of B's rows.
+bool adapter_tiles_fit(const AdapterArgs& a) {
+  return a.N % 64 == 0 && a.ldb % 16 == 0 && a.ldo % 16 == 0 && (uintptr_t)a.base % 32 == 0 && (uintptr_t)a.out % 32 == 0 &&
+         (int64_t)a.n * a.N < INT32_MAX && (int64_t)a.n * a.r < INT32_MAX;
+}
+
+cudaError_t launch_adapter_tiles(const AdapterArgs& g, cudaStream_t s) {
+  TileArgs p;
+  memset(&p, 0, sizeof(p));
+  p.g = g;
+  p.r16 = (g.r + 15) / 16 * 16;
+  p.katoms = (g.r + 63) / 64;
+  // A stage costs the copy unit much the same whatever its size, so stages are as wide as two of them fit (H
+  // in whole atoms: the 3-D maps count columns by atoms).
+  const int64_t tiles = tile_bound(g, kBM);
+  const int ring = kSmem - 2 * p.katoms * kAtom - 1024, katom = kAtom + p.r16 * 128;
+  p.ka = g.H % 64 != 0 ? 1 : ring / (4 * katom) >= 2 ? 4 : ring / (2 * katom) >= 2 ? 2 : 1;
+#ifdef ADAPTER_PROBE
+  if (g_ka) p.ka = g_ka;
+#endif
+  p.kslot = p.ka * katom;
+  p.nk = ring / p.kslot < kMaxSlots ? ring / p.kslot : kMaxSlots;
+  p.nn = ring / (p.katoms * kNB * 128) < kMaxSlots ? ring / (p.katoms * kNB * 128) : kMaxSlots;
+  if (p.nk < 1 || p.nn < 1) return cudaErrorInvalidValue;
+  const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  const bool maps =
+      p.ka == 1 ? tc_make_map(&p.x, bf16, g.x, g.H, g.T, (uint64_t)g.ldx * 2, 64, kBM, sw) &&
+                      tc_make_map(&p.a, bf16, g.A, g.H, (uint64_t)g.n * g.r, (uint64_t)g.H * 2, 64, p.r16, sw)
+                : atoms_map(&p.x, g.x, g.T, g.H, g.ldx, kBM, p.ka) &&
+                      atoms_map(&p.a, g.A, (uint64_t)g.n * g.r, g.H, g.H, p.r16, p.ka);
+  if (!maps || !rows_map(&p.b, g.B, (uint64_t)g.n * g.N, g.r)) return cudaErrorInvalidValue;
+  static std::atomic<bool> set{false};
+  if (!set.load(std::memory_order_relaxed)) {
+    const cudaError_t e = cudaFuncSetAttribute(adapter_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    set.store(true, std::memory_order_relaxed);
+  }
+  note_launches(1);
+  return launch_pdl(adapter_tile_kernel, dim3((unsigned)tiles), dim3(32 * kTileWarps), kSmem, s, p);
+}
+
+}  // namespace moe
+
+extern "C" moe_status_t moe_get_adapter_error(moe_stream_t stream, int32_t* code) {
+  using namespace moe;
+  if (!code) return MOE_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  int32_t v = 0;
+  const int zero = 0;
+  if (cudaMemcpyFromSymbolAsync(&v, g_adapter_error, sizeof(v), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess ||
+      cudaMemcpyToSymbolAsync(g_adapter_error, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  *code = v;
+  return MOE_OK;
+}
