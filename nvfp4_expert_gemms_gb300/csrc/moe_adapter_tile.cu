@@ -10,8 +10,7 @@
 // v goes from tensor memory through registers (scaled, split, zero past the adapter's rank) back into
 // shared memory as the second product's A operand.  The accumulator of the second product has two
 // 128-column buffers (the first one lies where v's sums were), so the epilogue of one column block runs
-// under the MMAs of the next; it fetches base ahead of the accumulator, 32 bytes per lane and row, and
-// writes whole 32-byte sectors.
+// under the MMAs of the next; base comes with B's stages, and out is written in whole 32-byte sectors.
 //
 // Bound: HBM bytes of x, base and out.  An MMA's cost hardly depends on N here, so rank 128 costs little
 // more than rank 16; the register MMAs of moe_adapter.cu, whose cost grows with the rank, fall behind.
@@ -36,15 +35,15 @@ __device__ int g_adapter_error;  // kDevOk or the first failure
 
 constexpr int kBM = 128, kEpiWarps = 8, kTileWarps = kEpiWarps + 3, kMaxSlots = 8;
 constexpr int kAtom = 128 * 128;  // bytes: 128 rows of 64 bf16 columns in the 128-byte swizzle
-constexpr int kNB = 256;          // rows of B per stage: two column blocks of the accumulator
 constexpr int kTmemCols = 256;
 constexpr int kSmem = 226 * 1024;  // of a block, one per SM: v, then the ring
 
 struct TileArgs {
-  CUtensorMap x, a, b;
+  CUtensorMap x, a, b, y;
   AdapterArgs g;
   int r16, katoms;    // rank in steps of 16 (all adapters), 64-column atoms of B
   int ka, kslot;      // 64-column atoms and bytes of a K stage
+  int bps, nslot;     // 128-column blocks and bytes of an N stage
   int nk, nn;         // stages of the ring for the two products
 };
 
@@ -110,9 +109,9 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
   }
   unsigned char* v_mem = (unsigned char*)(((uintptr_t)dyn + 1023) & ~(uintptr_t)1023);
   unsigned char* ring = v_mem + 2 * p.katoms * kAtom;  // v's hi and lo, then the stages
-  const int natom = kNB * 128, nslot = p.katoms * natom;
+  const int natom = p.bps * kAtom, ybytes = p.katoms * natom;  // an atom of a stage's B; where its base begins
   const int atoms = (a.H + 63) / 64, kst = (atoms + p.ka - 1) / p.ka;
-  const int nblk = (a.N + 127) / 128, nst = (a.N + kNB - 1) / kNB;  // accumulator column blocks, stages of B
+  const int nblk = (a.N + 127) / 128, nst = (nblk + p.bps - 1) / p.bps;  // column blocks, N stages
   const bool partial = rk % 16 != 0;  // the last rank step of B holds columns that are not the adapter's
   if (tid == 0) {
     for (int i = 0; i < kMaxSlots; ++i) {
@@ -120,7 +119,7 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
       mbar_init(&bars.empty_k[i], 1);
       mbar_init(&bars.full_n[i], 1);
       mbar_init(&bars.cut_n[i], 1);
-      mbar_init(&bars.empty_n[i], 1);
+      mbar_init(&bars.empty_n[i], 1 + kEpiWarps);
     }
     mbar_init(&bars.v_sums, 1);
     mbar_init(&bars.v_ready, 32 * kEpiWarps);
@@ -163,10 +162,11 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
         for (; n < nst; ++n) {
           const int s = n % p.nn, u = n / p.nn;
           if (u > 0 && !mbar_wait(&bars.empty_n[s], (u - 1) & 1, abort)) break;
-          unsigned char* at = ring + s * nslot;
-          mbar_arrive_expect_tx(&bars.full_n[s], nslot);
+          unsigned char* at = ring + s * p.nslot;
+          mbar_arrive_expect_tx(&bars.full_n[s], p.nslot);
           for (int i = 0; i < p.katoms; ++i)
-            tma_load_5d(at + i * natom, &p.b, &bars.full_n[s], 64 * i, (tile.slot * a.N + kNB * n) / 64);
+            tma_load_5d(at + i * natom, &p.b, &bars.full_n[s], 64 * i, (tile.slot * a.N + 128 * p.bps * n) / 64);
+          tma_load_3d(at + ybytes, &p.y, &bars.full_n[s], 0, tile.t0, 2 * p.bps * n);
         }
       }
       if (*abort) {  // copies in flight land before the block leaves
@@ -197,19 +197,19 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
       }
       const uint32_t hi = smem_u32(v_mem), lo = hi + p.katoms * kAtom;
       for (int n = 0; ok && n < nblk; ++n) {
-        const int st = n >> 1, s = st % p.nn, buf = n & 1;
+        const int st = n / p.bps, sub = n % p.bps, s = st % p.nn, buf = n & 1;
         if (n > 1) ok = mbar_wait(&bars.acc_empty[buf], ((n >> 1) - 1) & 1, abort);
-        if (ok && buf == 0) ok = mbar_wait(partial ? &bars.cut_n[s] : &bars.full_n[s], (st / p.nn) & 1, abort);
+        if (ok && sub == 0) ok = mbar_wait(partial ? &bars.cut_n[s] : &bars.full_n[s], (st / p.nn) & 1, abort);
         if (!ok) break;
         fence_after_sync();
-        const uint32_t bs = smem_u32(ring + s * nslot) + buf * kAtom, acc = tmem + 128 * buf;
+        const uint32_t bs = smem_u32(ring + s * p.nslot) + sub * kAtom, acc = tmem + 128 * buf;
         for (int i = 0; i < steps; ++i) {
           const uint32_t off = (i >> 2) * kAtom + (i & 3) * 32;
           const uint64_t b = sdesc_k_sw128(bs + (i >> 2) * natom + (i & 3) * 32);
           mma_f16_ss(acc, sdesc_k_sw128(lo + off), b, id2, i != 0);
           mma_f16_ss(acc, sdesc_k_sw128(hi + off), b, id2, 1);
         }
-        if (buf == 1 || n == nblk - 1) mma_commit(&bars.empty_n[s]);
+        if (sub == p.bps - 1 || n == nblk - 1) mma_commit(&bars.empty_n[s]);
         mma_commit(&bars.acc_full[buf]);
       }
       mma_commit(&bars.done);  // no arrival is on its way into this block's barriers when it leaves
@@ -221,8 +221,8 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
       for (int n = 0; n < nst; ++n) {
         const int s = n % p.nn;
         if (!__all_sync(0xffffffffu, mbar_wait(&bars.full_n[s], (n / p.nn) & 1, abort))) break;
-        unsigned char* bs = ring + s * nslot;
-        for (int row = lane; row < kNB; row += 32)
+        unsigned char* bs = ring + s * p.nslot;
+        for (int row = lane; row < 128 * p.bps; row += 32)
           for (int c = c0; c < c1; ++c) {
             uint4* q = (uint4*)(bs + (c >> 3) * natom + row * 128 + (((c & 7) ^ (row & 7)) << 4));
             const int keep = rk - 8 * c;  // columns of the chunk that stay
@@ -269,47 +269,37 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
     // The accumulator's fragments give a lane 16 consecutive columns (the map of B deals its rows so) of four
     // rows of the tile: four lanes hold a row's 128 bytes.
     const int g = lane >> 2, t = lane & 3;
-    const __nv_bfloat16* base[4];
     __nv_bfloat16* out[4];
     bool live[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 32 * quarter + g + 8 * i;
       live[i] = r < tile.rows;
-      const int64_t at = tile.t0 + (live[i] ? r : 0);
-      base[i] = a.base + at * a.ldb + 64 * half + 16 * t;
-      out[i] = a.out + at * a.ldo + 64 * half + 16 * t;
+      out[i] = a.out + (int64_t)(tile.t0 + (live[i] ? r : 0)) * a.ldo + 64 * half + 16 * t;
     }
-    uint4 y[4][2], next[4][2];
-    auto fetch = [&](uint4(&q)[4][2], int n) {  // the lane's columns of base in block n
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (live[i] && 128 * n + 64 * half < a.N)
-          asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                       : "=r"(q[i][0].x), "=r"(q[i][0].y), "=r"(q[i][0].z), "=r"(q[i][0].w), "=r"(q[i][1].x),
-                         "=r"(q[i][1].y), "=r"(q[i][1].z), "=r"(q[i][1].w)
-                       : "l"(base[i] + 128 * n)
-                       : "memory");
-    };
-    if (ok) fetch(next, 0);
     for (int n = 0; ok && n < nblk; ++n) {
-      const int buf = n & 1;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        y[i][0] = next[i][0];
-        y[i][1] = next[i][1];
-      }
-      if (n + 1 < nblk) fetch(next, n + 1);
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars.acc_full[buf], (n >> 1) & 1, abort));
+      const int st = n / p.bps, sub = n % p.bps, s = st % p.nn, buf = n & 1;
+      if (sub == 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars.full_n[s], (st / p.nn) & 1, abort));
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars.acc_full[buf], (n >> 1) & 1, abort));
       if (!ok) break;
       fence_after_sync();
       uint32_t w[2][32];
       tmem_ld_16x64(taddr(tmem, 32 * quarter, 128 * buf + 64 * half), w[0]);
       tmem_ld_16x64(taddr(tmem, 32 * quarter + 16, 128 * buf + 64 * half), w[1]);
+      // base: the stage's atom of this half, a row's pieces 2 t and 2 t + 1 (eight lanes: all banks once)
+      const unsigned char* ys = ring + s * p.nslot + ybytes + (2 * sub + half) * kAtom;
+      uint4 y[4][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) y[i][h] = *(const uint4*)(ys + swz(32 * quarter + g + 8 * i, 2 * t + h));
       tmem_ld_wait();
       fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
+      if (lane == 0) {
+        mbar_arrive(&bars.acc_empty[buf]);
+        if (sub == p.bps - 1 || n == nblk - 1) mbar_arrive(&bars.empty_n[s]);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (live[i] && 128 * n + 64 * half < a.N) {
@@ -364,13 +354,13 @@ static bool atoms_map(CUtensorMap* m, const void* base, uint64_t rows, int cols,
   return bf16_map(m, base, 3, dims, strides, box);
 }
 
-// Rows of B [rows, r], 64 at a time in the order (j, a, b) of row 16 a + 2 j + b (a < 4, j < 8, b < 2): the
+// Rows of B [rows, r], `groups` times 64, each in the order (j, a, b) of row 16 a + 2 j + b (a < 4, j < 8, b < 2): the
 // accumulator's column 8 j + 2 a + b is then output column 16 a + 2 j + b, and a lane's fragment (a = lane % 4)
 // 16 consecutive ones.  rows is a multiple of 64.
-static bool rows_map(CUtensorMap* m, const void* base, uint64_t rows, int r) {
+static bool rows_map(CUtensorMap* m, const void* base, uint64_t rows, int r, int groups) {
   const cuuint64_t one = (cuuint64_t)r * 2;
   const cuuint64_t dims[5] = {(cuuint64_t)r, 2, 4, 8, rows / 64}, strides[4] = {one, 16 * one, 2 * one, 64 * one};
-  const cuuint32_t box[5] = {64, 2, 4, 8, kNB / 64};
+  const cuuint32_t box[5] = {64, 2, 4, 8, (cuuint32_t)groups};
   return bf16_map(m, base, 5, dims, strides, box);
 }
 
@@ -396,7 +386,9 @@ cudaError_t launch_adapter_tiles(const AdapterArgs& g, cudaStream_t s) {
 #endif
   p.kslot = p.ka * katom;
   p.nk = ring / p.kslot < kMaxSlots ? ring / p.kslot : kMaxSlots;
-  p.nn = ring / (p.katoms * kNB * 128) < kMaxSlots ? ring / (p.katoms * kNB * 128) : kMaxSlots;
+  p.bps = p.katoms == 1 ? 2 : 1;
+  p.nslot = p.bps * (p.katoms + 2) * kAtom;  // B's rows and base's columns of the stage's blocks
+  p.nn = ring / p.nslot < kMaxSlots ? ring / p.nslot : kMaxSlots;
   if (p.nk < 1 || p.nn < 1) return cudaErrorInvalidValue;
   const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
@@ -405,7 +397,9 @@ cudaError_t launch_adapter_tiles(const AdapterArgs& g, cudaStream_t s) {
                       tc_make_map(&p.a, bf16, g.A, g.H, (uint64_t)g.n * g.r, (uint64_t)g.H * 2, 64, p.r16, sw)
                 : atoms_map(&p.x, g.x, g.T, g.H, g.ldx, kBM, p.ka) &&
                       atoms_map(&p.a, g.A, (uint64_t)g.n * g.r, g.H, g.H, p.r16, p.ka);
-  if (!maps || !rows_map(&p.b, g.B, (uint64_t)g.n * g.N, g.r)) return cudaErrorInvalidValue;
+  if (!maps || !rows_map(&p.b, g.B, (uint64_t)g.n * g.N, g.r, 2 * p.bps) ||
+      !atoms_map(&p.y, g.base, g.T, g.N, g.ldb, kBM, 2 * p.bps))
+    return cudaErrorInvalidValue;
   static std::atomic<bool> set{false};
   if (!set.load(std::memory_order_relaxed)) {
     const cudaError_t e = cudaFuncSetAttribute(adapter_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
