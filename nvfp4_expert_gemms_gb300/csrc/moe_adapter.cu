@@ -93,19 +93,21 @@ __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kern
   const __nv_bfloat16* B = a.B + (int64_t)max(tile.slot, 0) * a.N * a.r;
   const __nv_bfloat16 *b0 = a.base + t0 * a.ldb, *b1 = a.base + t1 * a.ldb;
   __nv_bfloat16 *o0 = a.out + t0 * a.ldo, *o1 = a.out + t1 * a.ldo;
-  uint2 bq[4][RT];
-  uint4 y0, y1;
-  auto load_cols = [&](int c) {  // B and base of columns c .. c+31
+  struct Cols {
+    uint2 bq[4][RT];
+    uint4 y0, y1;
+  };
+  auto load_cols = [&](Cols& f, int c) {  // B and base of columns c .. c+31
     const int col = c + 8 * t;
-    y0 = ok0 && col < a.N ? *(const uint4*)(b0 + col) : zero;
-    y1 = ok1 && col < a.N ? *(const uint4*)(b1 + col) : zero;
+    f.y0 = ok0 && col < a.N ? *(const uint4*)(b0 + col) : zero;
+    f.y1 = ok1 && col < a.N ? *(const uint4*)(b1 + col) : zero;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int n = c + 8 * (g >> 1) + 2 * j + (g & 1);
 #pragma unroll
       for (int s = 0; s < RT; ++s) {
         const int k = 16 * s + 4 * t;
-        bq[j][s] = n < a.N && k < rk ? *(const uint2*)(B + (int64_t)n * a.r + k) : make_uint2(0, 0);
+        f.bq[j][s] = n < a.N && k < rk ? *(const uint2*)(B + (int64_t)n * a.r + k) : make_uint2(0, 0);
       }
     }
   };
@@ -135,7 +137,8 @@ __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kern
           }
     }
   }
-  load_cols(32 * part_w);
+  Cols now;
+  load_cols(now, 32 * part_w);
   if (rk > 0) {
 #pragma unroll
     for (int j = 0; j < 2 * RT; ++j)
@@ -194,9 +197,12 @@ __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kern
 #pragma unroll
   for (int s = 0; s < RT; ++s) split_v(v[2 * s], v[2 * s + 1], tile.scale, hi[s], lo[s]);
   for (int c = 32 * part_w; c < a.N; c += 32 * parts) {
-    if (c != 32 * part_w) load_cols(c);
+    constexpr bool AHEAD = RT <= 2;  // the next columns are loaded under these ones (registers allowing)
+    Cols next;
+    if (AHEAD && c + 32 * parts < a.N) load_cols(next, c + 32 * parts);
+    if (!AHEAD && c != 32 * part_w) load_cols(now, c);
     const int col = c + 8 * t;
-    const uint32_t w0[4] = {y0.x, y0.y, y0.z, y0.w}, w1[4] = {y1.x, y1.y, y1.z, y1.w};
+    const uint32_t w0[4] = {now.y0.x, now.y0.y, now.y0.z, now.y0.w}, w1[4] = {now.y1.x, now.y1.y, now.y1.z, now.y1.w};
     uint32_t q0[4], q1[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -204,7 +210,7 @@ __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kern
 #pragma unroll
       for (int s = 0; s < RT; ++s)
         if (16 * s < rk) {
-          const uint2 b = cut_rank(bq[j][s], 16 * s + 4 * t, rk);
+          const uint2 b = cut_rank(now.bq[j][s], 16 * s + 4 * t, rk);
           mma_bf16(d, lo[s][0], lo[s][1], lo[s][2], lo[s][3], b.x, b.y);
           mma_bf16(d, hi[s][0], hi[s][1], hi[s][2], hi[s][3], b.x, b.y);
         }
@@ -213,6 +219,7 @@ __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kern
     }
     if (ok0 && col < a.N) *(uint4*)(o0 + col) = make_uint4(q0[0], q0[1], q0[2], q0[3]);
     if (ok1 && col < a.N) *(uint4*)(o1 + col) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
+    if (AHEAD) now = next;
   }
   if (rk > 0 && C > 1) cluster.barrier_wait();  // no block leaves while another may still read its sums
 }
@@ -447,20 +454,19 @@ cudaError_t launch_few(const AdapterArgs& a, int cluster, cudaStream_t s) {
 
 template <int RT>
 cudaError_t launch_rank(const AdapterArgs& a, cudaStream_t s) {
-#ifndef ADAPTER_PROBE
-  const int64_t tiles = tile_bound(a, 16);
-  if (a.T / (a.R > 0 ? a.R : 1) >= 128 && adapter_tiles_fit(a)) return launch_adapter_tiles(a, s);
-  if (a.T / (a.R > 0 ? a.R : 1) >= 256 && a.T >= 4096) return launch_many<RT, 4, 2>(a, s);
-  return launch_few<RT>(a, tiles > 76 ? 1 : tiles > 38 ? 2 : tiles > 19 ? 4 : 8, s);
-#else
-  
+#ifdef ADAPTER_PROBE
   if (g_many == 1) return launch_many<RT, 4, 2>(a, s);
-  if (g_many == 2) return launch_many<RT, 8, 2>(a, s);
-  if (g_many == 3) return launch_many<RT, 8, 1>(a, s);
   if (g_many == 4) return launch_many<RT, 2, 2>(a, s);
   if (g_many == 5) return launch_adapter_tiles(a, s);
   return launch_few<RT>(a, g_cluster, s);
 #endif
+  const int64_t mean = a.T / (a.R > 0 ? a.R : 1), tiles = tile_bound(a, 16);
+  if constexpr (RT == 1)
+    if (a.T >= 8192 && mean >= 32) return launch_many<1, 2, 2>(a, s);
+  if (mean >= 128 && (int64_t)a.T * a.r >= 200000 && adapter_tiles_fit(a)) return launch_adapter_tiles(a, s);
+  // blocks of a cluster share a tile as long as the grid fits the device at once
+  const int64_t room = (int64_t)tc_num_sms() * (RT <= 4 ? 2 : 1);
+  return launch_few<RT>(a, 8 * tiles <= room ? 8 : 4 * tiles <= room ? 4 : 2 * tiles <= room ? 2 : 1, s);
 }
 
 }  // namespace

@@ -36,7 +36,7 @@ __device__ int g_adapter_error;  // kDevOk or the first failure
 constexpr int kBM = 128, kEpiWarps = 8, kTileWarps = kEpiWarps + 3, kMaxSlots = 8;
 constexpr int kAtom = 128 * 128;  // bytes: 128 rows of 64 bf16 columns in the 128-byte swizzle
 constexpr int kTmemCols = 256;
-constexpr int kSmem = 226 * 1024;  // of a block, one per SM: v, then the ring
+constexpr int kSmem = 225 * 1024;  // most that a block takes (one per SM): 1 KB alignment, v, two N stages
 
 struct TileArgs {
   CUtensorMap x, a, b, y;
@@ -44,11 +44,11 @@ struct TileArgs {
   int r16, katoms;    // rank in steps of 16 (all adapters), 64-column atoms of B
   int ka, kslot;      // 64-column atoms and bytes of a K stage
   int bps, nslot;     // 128-column blocks and bytes of an N stage
-  int nk, nn;         // stages of the ring for the two products
+  int nk;             // K stages
 };
 
 struct Bars {
-  uint64_t full_k[kMaxSlots], empty_k[kMaxSlots], full_n[kMaxSlots], cut_n[kMaxSlots], empty_n[kMaxSlots];
+  uint64_t full_k[kMaxSlots], empty_k[kMaxSlots], full_n[2], cut_n[2], empty_n[2];
   uint64_t v_sums, v_ready, acc_full[2], acc_empty[2], done;
   uint32_t tmem;
   int abort;
@@ -108,7 +108,9 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
     return;
   }
   unsigned char* v_mem = (unsigned char*)(((uintptr_t)dyn + 1023) & ~(uintptr_t)1023);
-  unsigned char* ring = v_mem + 2 * p.katoms * kAtom;  // v's hi and lo, then the stages
+  // v's hi and lo; then the K stages, whose memory is N stage 1 later; then N stage 0, which can be loaded
+  // while the first product runs
+  unsigned char* ring = v_mem + 2 * p.katoms * kAtom;
   const int natom = p.bps * kAtom, ybytes = p.katoms * natom;  // an atom of a stage's B; where its base begins
   const int atoms = (a.H + 63) / 64, kst = (atoms + p.ka - 1) / p.ka;
   const int nblk = (a.N + 127) / 128, nst = (nblk + p.bps - 1) / p.bps;  // column blocks, N stages
@@ -117,13 +119,13 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
     for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init(&bars.full_k[i], 1);
       mbar_init(&bars.empty_k[i], 1);
-      mbar_init(&bars.full_n[i], 1);
-      mbar_init(&bars.cut_n[i], 1);
-      mbar_init(&bars.empty_n[i], 1 + kEpiWarps);
     }
     mbar_init(&bars.v_sums, 1);
     mbar_init(&bars.v_ready, 32 * kEpiWarps);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.full_n[i], 1);
+      mbar_init(&bars.cut_n[i], 1);
+      mbar_init(&bars.empty_n[i], 1 + kEpiWarps);
       mbar_init(&bars.acc_full[i], 1);
       mbar_init(&bars.acc_empty[i], kEpiWarps);
     }
@@ -143,13 +145,21 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
       prefetch_tmap(&p.x);
       prefetch_tmap(&p.a);
       prefetch_tmap(&p.b);
-      const uint32_t kbytes = p.kslot;
       int k = 0, n = 0;
+      auto load_n = [&] {  // N stage n
+        unsigned char* at = ring + (1 - (n & 1)) * p.nslot;
+        uint64_t* full = &bars.full_n[n & 1];
+        mbar_arrive_expect_tx(full, p.nslot);
+        for (int i = 0; i < p.katoms; ++i)
+          tma_load_5d(at + i * natom, &p.b, full, 64 * i, (tile.slot * a.N + 128 * p.bps * n) / 64);
+        tma_load_3d(at + ybytes, &p.y, full, 0, tile.t0, 2 * p.bps * n);
+        ++n;
+      };
       for (; k < kst; ++k) {
         const int s = k % p.nk, u = k / p.nk;
         if (u > 0 && !mbar_wait(&bars.empty_k[s], (u - 1) & 1, abort)) break;
         unsigned char* at = ring + s * p.kslot;
-        mbar_arrive_expect_tx(&bars.full_k[s], kbytes);
+        mbar_arrive_expect_tx(&bars.full_k[s], p.kslot);
         if (p.ka == 1) {
           tma_load_2d(at, &p.x, &bars.full_k[s], 64 * k, tile.t0);
           tma_load_2d(at + kAtom, &p.a, &bars.full_k[s], 64 * k, tile.slot * a.r);
@@ -157,21 +167,16 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
           tma_load_3d(at, &p.x, &bars.full_k[s], 0, tile.t0, p.ka * k);
           tma_load_3d(at + p.ka * kAtom, &p.a, &bars.full_k[s], 0, tile.slot * a.r, p.ka * k);
         }
+        if (k == (kst < p.nk ? kst : p.nk) - 1) load_n();
       }
-      if (k == kst && mbar_wait(&bars.v_sums, 0, abort)) {  // every K stage has been read
-        for (; n < nst; ++n) {
-          const int s = n % p.nn, u = n / p.nn;
-          if (u > 0 && !mbar_wait(&bars.empty_n[s], (u - 1) & 1, abort)) break;
-          unsigned char* at = ring + s * p.nslot;
-          mbar_arrive_expect_tx(&bars.full_n[s], p.nslot);
-          for (int i = 0; i < p.katoms; ++i)
-            tma_load_5d(at + i * natom, &p.b, &bars.full_n[s], 64 * i, (tile.slot * a.N + 128 * p.bps * n) / 64);
-          tma_load_3d(at + ybytes, &p.y, &bars.full_n[s], 0, tile.t0, 2 * p.bps * n);
+      if (k == kst && mbar_wait(&bars.v_sums, 0, abort))  // every K stage has been read
+        while (n < nst) {
+          if (n > 1 && !mbar_wait(&bars.empty_n[n & 1], ((n >> 1) - 1) & 1, abort)) break;
+          load_n();
         }
-      }
       if (*abort) {  // copies in flight land before the block leaves
         for (int i = k > p.nk ? k - p.nk : 0; i < k; ++i) drain(&bars.full_k[i % p.nk], (i / p.nk) & 1);
-        for (int i = n > p.nn ? n - p.nn : 0; i < n; ++i) drain(&bars.full_n[i % p.nn], (i / p.nn) & 1);
+        for (int i = n > 2 ? n - 2 : 0; i < n; ++i) drain(&bars.full_n[i & 1], (i >> 1) & 1);
       }
     }
   } else if (warp == kEpiWarps + 1) {  // ---- MMAs
@@ -197,12 +202,12 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
       }
       const uint32_t hi = smem_u32(v_mem), lo = hi + p.katoms * kAtom;
       for (int n = 0; ok && n < nblk; ++n) {
-        const int st = n / p.bps, sub = n % p.bps, s = st % p.nn, buf = n & 1;
+        const int st = n / p.bps, sub = n % p.bps, s = st & 1, buf = n & 1;
         if (n > 1) ok = mbar_wait(&bars.acc_empty[buf], ((n >> 1) - 1) & 1, abort);
-        if (ok && sub == 0) ok = mbar_wait(partial ? &bars.cut_n[s] : &bars.full_n[s], (st / p.nn) & 1, abort);
+        if (ok && sub == 0) ok = mbar_wait(partial ? &bars.cut_n[s] : &bars.full_n[s], (st >> 1) & 1, abort);
         if (!ok) break;
         fence_after_sync();
-        const uint32_t bs = smem_u32(ring + s * p.nslot) + sub * kAtom, acc = tmem + 128 * buf;
+        const uint32_t bs = smem_u32(ring + (1 - s) * p.nslot) + sub * kAtom, acc = tmem + 128 * buf;
         for (int i = 0; i < steps; ++i) {
           const uint32_t off = (i >> 2) * kAtom + (i & 3) * 32;
           const uint64_t b = sdesc_k_sw128(bs + (i >> 2) * natom + (i & 3) * 32);
@@ -219,9 +224,9 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
     if (partial) {
       const int c0 = rk / 8, c1 = 2 * steps;  // 8-column chunks from the partial one on
       for (int n = 0; n < nst; ++n) {
-        const int s = n % p.nn;
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars.full_n[s], (n / p.nn) & 1, abort))) break;
-        unsigned char* bs = ring + s * p.nslot;
+        const int s = n & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars.full_n[s], (n >> 1) & 1, abort))) break;
+        unsigned char* bs = ring + (1 - s) * p.nslot;
         for (int row = lane; row < 128 * p.bps; row += 32)
           for (int c = c0; c < c1; ++c) {
             uint4* q = (uint4*)(bs + (c >> 3) * natom + row * 128 + (((c & 7) ^ (row & 7)) << 4));
@@ -278,8 +283,8 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
       out[i] = a.out + (int64_t)(tile.t0 + (live[i] ? r : 0)) * a.ldo + 64 * half + 16 * t;
     }
     for (int n = 0; ok && n < nblk; ++n) {
-      const int st = n / p.bps, sub = n % p.bps, s = st % p.nn, buf = n & 1;
-      if (sub == 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars.full_n[s], (st / p.nn) & 1, abort));
+      const int st = n / p.bps, sub = n % p.bps, s = st & 1, buf = n & 1;
+      if (sub == 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars.full_n[s], (st >> 1) & 1, abort));
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars.acc_full[buf], (n >> 1) & 1, abort));
       if (!ok) break;
       fence_after_sync();
@@ -287,7 +292,7 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
       tmem_ld_16x64(taddr(tmem, 32 * quarter, 128 * buf + 64 * half), w[0]);
       tmem_ld_16x64(taddr(tmem, 32 * quarter + 16, 128 * buf + 64 * half), w[1]);
       // base: the stage's atom of this half, a row's pieces 2 t and 2 t + 1 (eight lanes: all banks once)
-      const unsigned char* ys = ring + s * p.nslot + ybytes + (2 * sub + half) * kAtom;
+      const unsigned char* ys = ring + (1 - s) * p.nslot + ybytes + (2 * sub + half) * kAtom;
       uint4 y[4][2];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -376,20 +381,15 @@ cudaError_t launch_adapter_tiles(const AdapterArgs& g, cudaStream_t s) {
   p.g = g;
   p.r16 = (g.r + 15) / 16 * 16;
   p.katoms = (g.r + 63) / 64;
-  // A stage costs the copy unit much the same whatever its size, so stages are as wide as two of them fit (H
-  // in whole atoms: the 3-D maps count columns by atoms).
-  const int64_t tiles = tile_bound(g, kBM);
-  const int ring = kSmem - 2 * p.katoms * kAtom - 1024, katom = kAtom + p.r16 * 128;
-  p.ka = g.H % 64 != 0 ? 1 : ring / (4 * katom) >= 2 ? 4 : ring / (2 * katom) >= 2 ? 2 : 1;
-#ifdef ADAPTER_PROBE
-  if (g_ka) p.ka = g_ka;
-#endif
-  p.kslot = p.ka * katom;
-  p.nk = ring / p.kslot < kMaxSlots ? ring / p.kslot : kMaxSlots;
   p.bps = p.katoms == 1 ? 2 : 1;
   p.nslot = p.bps * (p.katoms + 2) * kAtom;  // B's rows and base's columns of the stage's blocks
-  p.nn = ring / p.nslot < kMaxSlots ? ring / p.nslot : kMaxSlots;
-  if (p.nk < 1 || p.nn < 1) return cudaErrorInvalidValue;
+  // A stage costs the copy unit much the same whatever its size, so K stages are as wide as two of them fit
+  // (H in whole atoms: the 3-D maps count columns by atoms).
+  const int64_t tiles = tile_bound(g, kBM);
+  const int katom = kAtom + p.r16 * 128;
+  p.ka = g.H % 64 != 0 ? 1 : p.nslot / (2 * katom) >= 2 ? 2 : 1;
+  p.kslot = p.ka * katom;
+  p.nk = p.nslot / p.kslot < kMaxSlots ? p.nslot / p.kslot : kMaxSlots;
   const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
   const bool maps =

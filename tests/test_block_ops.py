@@ -378,6 +378,19 @@ def test_adapters(r, H, N):
     run_adapters([700, 530, 515], [1, -1, 0], H, N, 2, r, 4, rank=[max(1, r // 2), r], in_place=True, pad=16)
 
 
+@pytest.mark.parametrize("r", [8, 16, 24, 40, 64, 72, 128])
+@pytest.mark.parametrize("H,N,pad", [(256, 128, 0), (2048, 1536, 16), (1000, 320, 0), (72, 64, 16), (512, 264, 8)])
+def test_adapters_long_requests(r, H, N, pad):
+    """Sizes whose requests fill whole tiles: every kernel for long requests, ranks and rows that end inside a
+    tile, requests without an adapter among them."""
+    n = 3
+    rank = [r, max(1, r - 5), max(1, r // 2)]
+    small = 200000 // r
+    run_adapters([small - 300, 1, 128, 0, 127, 4096, 600], [0, 1, 2, 0, 1, -1, 2], H, N, n, r, 11, rank=rank, pad=pad)
+    run_adapters([9000, 129], [1, 2], H, N, n, r, 12, rank=rank, pad=pad, in_place=True, scale=False)
+    run_adapters([200, 3000, 5200], [2, 7, 0], H, N, n, r, 13, pad=pad)
+
+
 def test_adapters_many_requests_and_edges():
     # more requests than one pass of the tile search holds, empty ones among them; slots out of range
     lens = [(i * 7) % 4 for i in range(700)]
@@ -397,7 +410,7 @@ def test_adapters_nan_stays_in_its_row_and_runs_repeat():
     x, base = rows(600, 256, torch.bfloat16, g), rows(600, 256, torch.bfloat16, g)
     a = torch.randn((1, 16, 256), generator=g, device="cuda").bfloat16()
     b = torch.randn((1, 256, 16), generator=g, device="cuda").bfloat16()
-    for lens in ([600], [3, 500, 1, 96]):
+    for lens in ([600], [3, 500, 1, 96], [300, 300]):
         starts = torch.tensor([sum(lens[:i]) for i in range(len(lens) + 1)], dtype=torch.int32, device="cuda")
         slot = torch.zeros(len(lens), dtype=torch.int32, device="cuda")
         want = M.moe_adapters_add(x, base, a, b, starts, slot)
@@ -410,6 +423,17 @@ def test_adapters_nan_stays_in_its_row_and_runs_repeat():
         keep[77] = keep[300] = False
         assert torch.equal(got[keep], want[keep])
         assert torch.isnan(got[77]).all() and not torch.isfinite(got[300]).any()
+    # the same in tiles of 128 tokens, where neighbours share one product
+    x, base = rows(4096, 256, torch.bfloat16, g), rows(4096, 256, torch.bfloat16, g)
+    a = torch.randn((2, 64, 256), generator=g, device="cuda").bfloat16()
+    b = torch.randn((2, 256, 64), generator=g, device="cuda").bfloat16()
+    starts, slot = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, 1000, 4096], [1, 0]))
+    want = M.moe_adapters_add(x, base, a, b, starts, slot)
+    assert torch.equal(want, M.moe_adapters_add(x, base, a, b, starts, slot))
+    x[999, 5] = float("nan")
+    got = M.moe_adapters_add(x, base, a, b, starts, slot)
+    assert torch.isnan(got[999]).all() and torch.equal(got[:999], want[:999]) and torch.equal(got[1000:], want[1000:])
+    assert M.moe_get_adapter_error() == 0
 
 
 # ------------------------------------------------------------------------------------------ together
