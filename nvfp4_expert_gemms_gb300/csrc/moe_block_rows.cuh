@@ -21,9 +21,12 @@
 namespace moe {
 namespace {
 
-constexpr int kStreamRows = 1216;       // rows from which blocks walk over rows
-constexpr int kStreamThreads = 512;     // threads of such a block
-constexpr int kStreamSmem = 113 * 1024; // and its shared memory: two blocks per SM
+constexpr int64_t kStreamSize = 1216 * 2048;  // elements from which blocks walk over rows (below: a block per row)
+// Shared memory and threads of such a block: two per SM (rows of up to 4096 columns), or one.
+template <int W, int N>
+constexpr int kStreamSmem = (W * N > 16 ? 226 : 113) * 1024;
+template <int N>
+constexpr int kStreamThreads = N <= 2 ? 512 : 256;
 
 // Sum over the threads of one row: a warp, or the whole block through shared memory.  `red` has two
 // buffers used in turn, so that one barrier per sum is enough: a buffer is written again only after
@@ -346,17 +349,17 @@ struct GroupSum {
   }
 };
 
-// The same, many rows: a group of W warps per row (two pieces of 8 columns per lane, 512 W >= H), groups
+// The same, many rows: a group of W warps per row (N pieces of 8 columns per lane, 256 W N >= H), groups
 // walking the rows with the grid's stride.  A warp copies its own columns of the next row's x, block and
 // per-element gate into shared memory (cp.async, two slots) while it works on the current one, so the
 // bytes in flight cost no registers; x waits there until it is added.  The column factors are in shared
 // memory, fp32, one copy per block.
-template <typename X, typename A, typename P, int W, bool LEAVE>
-__global__ void __launch_bounds__(kStreamThreads, 2) block_stream_kernel(const BlockArgs a) {
-  constexpr int N = 2, G = 32 * W;  // 256 W columns per step of N
+template <typename X, typename A, typename P, int W, int N, bool LEAVE>
+__global__ void __launch_bounds__(kStreamThreads<N>, N == 8 ? 1 : 2) block_stream_kernel(const BlockArgs a) {
+  constexpr int G = 32 * W;  // threads of a row; 256 W columns per step of N
   constexpr int kX = kPieces<X>, kA = LEAVE ? kPieces<A> : 0, kG = LEAVE ? kPieces<P> : 0;
   extern __shared__ __align__(16) uint4 smem[];  // column factors [LEAVE ? 4 : 2][N G], then [groups][2][row]
-  __shared__ __align__(16) float red[kStreamThreads / G][2][W < 4 ? 4 : W];
+  __shared__ __align__(16) float red[kStreamThreads<N> / G][2][W < 4 ? 4 : W];
   const int lane = threadIdx.x & 31, group = threadIdx.x / G, w = threadIdx.x / 32 % W, H = a.H;
   const P *pb = (const P*)a.post.bias, *nb = (const P*)a.next.bias, *gate = (const P*)a.gate;
   const bool full_gate = LEAVE && gate && a.gate_step && a.gate_ld, token_gate = LEAVE && gate && !a.gate_step;
@@ -691,19 +694,20 @@ cudaError_t launch_row(const BlockArgs& a, cudaStream_t s) {
   return launch_pdl(block_row_kernel<X, A, P, N, LEAVE>, dim3(a.T), dim3(threads), 0, s, a);
 }
 
-template <typename X, typename A, typename P, int W, bool LEAVE>
+template <typename X, typename A, typename P, int W, int N, bool LEAVE>
 cudaError_t launch_stream(const BlockArgs& a, cudaStream_t s) {
   const bool full_gate = LEAVE && a.gate && a.gate_step && a.gate_ld;
-  const int slot = 2 * (kPieces<X> + (LEAVE ? kPieces<A> : 0) + (full_gate ? kPieces<P> : 0)) * 512 * W;
-  const int factors = (LEAVE ? 4 : 2) * 1024 * W;
-  constexpr int most_groups = kStreamThreads / (32 * W);
-  const int fits = (kStreamSmem - factors) / (2 * slot), groups = fits < most_groups ? fits : most_groups;
+  const int slot = N * (kPieces<X> + (LEAVE ? kPieces<A> : 0) + (full_gate ? kPieces<P> : 0)) * 512 * W;
+  const int factors = (LEAVE ? 4 : 2) * 512 * W * N;
+  constexpr int most_groups = kStreamThreads<N> / (32 * W), most_smem = kStreamSmem<W, N>;
+  const int fits = (most_smem - factors) / (2 * slot), groups = fits < most_groups ? fits : most_groups;
+  if (groups < 1) return launch_pdl(block_long_kernel<X, A, LEAVE>, dim3(a.T), dim3(1024), 0, s, a);
   const int smem = factors + groups * 2 * slot;
-  const auto kernel = block_stream_kernel<X, A, P, W, LEAVE>;
+  const auto kernel = block_stream_kernel<X, A, P, W, N, LEAVE>;
   static std::atomic<int> fit[2];  // resident blocks per SM of this kernel
   int per_sm = fit[full_gate].load(std::memory_order_relaxed);
   if (per_sm == 0) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem);
     if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, 32 * W * groups, smem);
     if (e != cudaSuccess) return e;
     fit[full_gate].store(per_sm, std::memory_order_relaxed);
@@ -720,19 +724,24 @@ cudaError_t launch_narrow(const BlockArgs& a, cudaStream_t s) {
 
 template <typename X, typename A, typename P, bool LEAVE>
 cudaError_t launch_typed(const BlockArgs& a, bool wide, cudaStream_t s) {
+  if (a.H <= 128) return launch_narrow<X, A, P, 32, 4, LEAVE>(a, s);
   if (wide) {
-    if (a.H <= 4096 && a.T >= kStreamRows) {
-      if (a.H <= 512) return launch_stream<X, A, P, 1, LEAVE>(a, s);
-      if (a.H <= 1024) return launch_stream<X, A, P, 2, LEAVE>(a, s);
-      if (a.H <= 2048) return launch_stream<X, A, P, 4, LEAVE>(a, s);
-      return launch_stream<X, A, P, 8, LEAVE>(a, s);
+    if ((int64_t)a.T * a.H >= kStreamSize || a.H > 4096) {
+      // four pieces per lane: fewer instructions per row's sums than two, more warps than eight (16384 x 2048
+      // fp32 / bf16: 67.4, 66.9, 68.6 us with 2, 4, 8; bf16 50.7, 46.5, 47.5; 4096 x 2048: 21.5, 18.3, 20.0)
+      if (a.H <= 512) return launch_stream<X, A, P, 1, 2, LEAVE>(a, s);
+      if (a.H <= 1024) return launch_stream<X, A, P, 1, 4, LEAVE>(a, s);
+      if (a.H <= 2048) return launch_stream<X, A, P, 2, 4, LEAVE>(a, s);
+      if (a.H <= 4096) return launch_stream<X, A, P, 4, 4, LEAVE>(a, s);
+      if (a.H <= 8192) return launch_stream<X, A, P, 8, 4, LEAVE>(a, s);
+    } else {
+      return launch_row<X, A, P, 1, LEAVE>(a, s);
     }
-    if (a.H <= 4096) return launch_row<X, A, P, 1, LEAVE>(a, s);
-    if (a.H <= 8192) return launch_row<X, A, P, 2, LEAVE>(a, s);
   } else {
-    if (a.H <= 128) return launch_narrow<X, A, P, 32, 4, LEAVE>(a, s);
+    if (a.H <= 512) return launch_narrow<X, A, P, 32, 16, LEAVE>(a, s);
     if (a.H <= 1024) return launch_narrow<X, A, P, 128, 8, LEAVE>(a, s);
     if (a.H <= 2048) return launch_narrow<X, A, P, 256, 8, LEAVE>(a, s);
+    if (a.H <= 4096) return launch_narrow<X, A, P, 512, 8, LEAVE>(a, s);
     if (a.H <= 8192) return launch_narrow<X, A, P, 1024, 8, LEAVE>(a, s);
   }
   return launch_pdl(block_long_kernel<X, A, LEAVE>, dim3(a.T), dim3(1024), 0, s, a);

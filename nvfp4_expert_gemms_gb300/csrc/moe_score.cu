@@ -11,10 +11,11 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const ScoreArgs
                                                                  int32_t* __restrict__ topk_idx,
                                                                  float* __restrict__ topk_w) {
   __shared__ ScoreCand cand[kScoreWarps][64];
-  const int warp = threadIdx.x >> 5, t = blockIdx.x * kScoreWarps + warp;
+  const int warp = threadIdx.x >> 5;
+  const uint32_t t = blockIdx.x * kScoreWarps + warp;
   pdl_wait();
   pdl_trigger();
-  if (t < T) score_token<VT>(a, g, t, k, threadIdx.x & 31, topk_idx, topk_w, cand[warp]);
+  if (t < (uint32_t)T) score_token<VT>(a, g, (int)t, k, threadIdx.x & 31, topk_idx, topk_w, cand[warp]);
 }
 
 }  // namespace
@@ -31,7 +32,7 @@ cudaError_t launch_route_scored(const ScoreArgs& a, int T, int E, int k, int32_t
                                 cudaStream_t s) {
   if (T == 0) return cudaSuccess;
   const ScoreGeom g = score_geom(a, E);
-  const dim3 grid((T + kScoreWarps - 1) / kScoreWarps), block(32 * kScoreWarps);
+  const dim3 grid((unsigned)(((int64_t)T + kScoreWarps - 1) / kScoreWarps)), block(32 * kScoreWarps);
   note_launches(1);
   if (g.per <= 1) return launch_pdl(score_kernel<1>, grid, block, 0, s, a, g, T, k, topk_idx, topk_w);
   if (g.per <= 2) return launch_pdl(score_kernel<2>, grid, block, 0, s, a, g, T, k, topk_idx, topk_w);

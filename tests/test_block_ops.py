@@ -524,6 +524,50 @@ def test_moe_block(T, stream_type):
     assert torch.equal(again, out)
 
 
+def test_example_runs():
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_block.py")
+    spec = importlib.util.spec_from_file_location("moe_block_example", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    x = example.main(["--format", "fp8", "--hidden", "256", "--inner", "128", "--experts", "16", "--top-k", "4", "--steps", "1"])
+    assert x.shape == (5, 256) and torch.isfinite(x).all()
+
+
+def test_operators_in_a_graph():
+    """Captured once, replayed on new inputs: the same results as direct calls."""
+    g = gen(21)
+    T, H, E, r = 4000, 256, 64, 64
+    x, b = rows(T, H, torch.float32, g), rows(T, H, torch.bfloat16, g)
+    (pre, _), (post, _) = make_norm("rms", H, torch.bfloat16, g), make_norm("layer", H, torch.bfloat16, g)
+    lg = rows(T, E, torch.float32, g)
+    router = M.Router("sigmoid", groups=8, top_groups=4, group_top=2)
+    bias = 0.1 * torch.randn(E, generator=g, device="cuda")
+    A = torch.randn((2, r, H), generator=g, device="cuda").bfloat16()
+    B = torch.randn((2, H, r), generator=g, device="cuda").bfloat16()
+    starts, slot = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, 1000, 4000], [1, 0]))
+
+    def work():
+        h = M.moe_block_enter(x, pre, dtype=torch.bfloat16)
+        idx, w = M.moe_route_scored(lg, router, 4, bias=bias)
+        m = M.moe_adapters_add(h, b, A, B, starts, slot)
+        few = M.moe_adapters_add(h[:64], b[:64], A, B, starts.clamp(max=64), slot)
+        return (idx, w, m, few) + M.moe_block_leave(x, m, post=post, next=pre)
+
+    work()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = work()
+    for t in (x, b, lg):
+        t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+    graph.replay()
+    for p, q in zip(got, work()):
+        assert torch.equal(p, q)
+
+
 # ------------------------------------------------------------------------------------------ refusals
 def refused(status, f, *args, **kw):
     with pytest.raises(M.MoEError) as e:
