@@ -166,8 +166,8 @@ struct RouterScorer {
   ScoreArgs a;
   ScoreGeom g;
   __device__ __forceinline__ int operator()(int t, int E, int k, int lane, int32_t* idx, float* w) const {
-    __shared__ ScoreCand cand[32][64];  // a warp of the 1024-thread block each
-    return score_token<VT>(a, g, t, k, lane, idx, w, cand[threadIdx.x >> 5]);
+    __shared__ ScoreScratch scratch[32];  // a warp of the 1024-thread block each
+    return score_token<VT>(a, g, t, k, lane, idx, w, scratch[threadIdx.x >> 5]);
   }
 };
 

@@ -10,12 +10,12 @@ template <int VT>
 __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const ScoreArgs a, const ScoreGeom g, int T, int k,
                                                                  int32_t* __restrict__ topk_idx,
                                                                  float* __restrict__ topk_w) {
-  __shared__ ScoreCand cand[kScoreWarps][64];
+  __shared__ ScoreScratch scratch[kScoreWarps];
   const int warp = threadIdx.x >> 5;
   const uint32_t t = blockIdx.x * kScoreWarps + warp;
   pdl_wait();
   pdl_trigger();
-  if (t < (uint32_t)T) score_token<VT>(a, g, (int)t, k, threadIdx.x & 31, topk_idx, topk_w, cand[warp]);
+  if (t < (uint32_t)T) score_token<VT>(a, g, (int)t, k, threadIdx.x & 31, topk_idx, topk_w, scratch[warp]);
 }
 
 }  // namespace

@@ -18,12 +18,15 @@ namespace moe {
 struct ScoreGeom {
   int S, lanes_log2, per;  // experts per group, log2 of lanes per group, experts per lane
   bool wide;               // a lane's logits are whole aligned 8- or 16-byte pieces; so is its share of the bias
+  bool full;               // and every lane has its VT experts
 };
 
-// A candidate's place while a warp sorts out the best ones.
-struct ScoreCand {
-  float key;
-  int expert;
+// What a warp keeps in shared memory while it sorts out the best ones.
+struct ScoreScratch {
+  int cand[32];    // experts that could be chosen, and (few experts per lane) their logits
+  float logit[32];
+  int expert[8];   // the chosen, in order, and their scores
+  float score[8];
 };
 constexpr float kNoKey = __builtin_nanf("");  // not a candidate: compares false with everything, loses every max
 
@@ -59,7 +62,7 @@ __device__ __forceinline__ void load_logits(const ScoreArgs& a, const ScoreGeom&
     if (VT >= 4 && g.wide) {
 #pragma unroll
       for (int i = 0; i < VT / 4; ++i) {
-        const float4 q = cnt ? ((const float4*)p)[i] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        const float4 q = g.full || cnt ? ((const float4*)p)[i] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
         l[4 * i] = q.x;
         l[(4 * i + 1) % VT] = q.y;
         l[(4 * i + 2) % VT] = q.z;
@@ -97,67 +100,119 @@ __device__ __forceinline__ void load_logits(const ScoreArgs& a, const ScoreGeom&
   for (int i = 0; i < VT; ++i) l[i] = fmaxf(l[i], -INFINITY);
 }
 
-// The experts of the k largest keys, in descending order, ties to the lower expert: returned in lanes
-// 0 .. k-1.  Lane order is expert order.
-//
-// Of the lanes' own maxima, the k-th largest bounds the k-th largest key from below, so only keys at
-// least that large can be chosen: about k of them.  They move to one lane each and a lane counts how many
-// stand in front of its own -- a few instructions per candidate in place of k rounds over every key.
-//
-// SURE: key holds the keys, and there is always an answer (more than 32 keys at the bound, which takes
-// many equal ones, go through k rounds after all).  Else key holds estimates, each at most slack(estimate)
-// off: the candidates are those that could be chosen, final_key(l, expert) gives a candidate's key from
-// val, the logits, and false is returned where that does not decide.
+// How far an estimated key may be off (see score_token).
 __device__ __forceinline__ float key_slack(float key) { return 9.6e-7f + 2.4e-7f * fabsf(key); }
 
-template <bool SURE, int VT, class FinalKey>
-__device__ __forceinline__ bool pick_top(float (&key)[VT], const float (&val)[VT], int e0, int k, int lane,
-                                         ScoreCand* cand, FinalKey final_key, int& chosen) {
-  if constexpr (VT >= 4) {
-    float rem = key[0], bound = 0.f;
+// A lane's largest key (kNoKey: it has none) and, where asked, its second (-infinity: it has none).  FULL: every
+// key is one.
+template <bool FULL, int VT>
+__device__ __forceinline__ float lane_top(const float (&key)[VT], int cnt, bool second, float& b2) {
+  const auto value = [](float v) { return FULL ? v : fmaxf(v, -INFINITY); };
+  float hi = key[0];
+  if (!second) {
 #pragma unroll
-    for (int i = 1; i < VT; ++i) rem = fmaxf(rem, key[i]);
-    for (int j = 0; j < k; ++j) {  // equal maxima leave together: the bound is then a little lower
-      bound = redux_max(rem);
-      rem = rem == bound ? kNoKey : rem;
-    }
-    bound = fmaxf(bound, -INFINITY);  // NaN, fewer than k lanes with candidates: every candidate
-    if (!SURE) {
-      if (isinf(bound)) return false;
-      bound -= 2.f * key_slack(bound);
-    }
-    int c = 0;
-#pragma unroll
-    for (int i = 0; i < VT; ++i) c += key[i] >= bound;
-    int incl = c;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += o;
-    }
-    const int total = __shfl_sync(0xffffffffu, incl, 31);
-    if (total <= 32) {
-      ScoreCand* to = cand + incl - c;
-#pragma unroll
-      for (int i = 0; i < VT; ++i)
-        if (key[i] >= bound) *to++ = ScoreCand{SURE ? key[i] : val[i], e0 + i};
-      __syncwarp();
-      ScoreCand mine = lane < total ? cand[lane] : ScoreCand{kNoKey, 0};
-      if (!SURE && lane < total) mine.key = final_key(mine.key, mine.expert);
-      int front = 0;
-#pragma unroll 4
-      for (int j = 0; j < total; ++j) {
-        const float o = __shfl_sync(0xffffffffu, mine.key, j);
-        front += j < lane ? o >= mine.key : o > mine.key;
-      }
-      if (lane < total && front < k) cand[32 + front].expert = mine.expert;
-      __syncwarp();
-      chosen = cand[32 + (lane < k ? lane : 0)].expert;
-      __syncwarp();
-      return true;
-    }
-    if (!SURE) return false;
+    for (int i = 1; i < VT; ++i) hi = fmaxf(hi, key[i]);
+    return hi;
   }
+  b2 = -INFINITY;
+  hi = value(hi);
+#pragma unroll
+  for (int i = 1; i < VT; i += 2) {  // a pair, and with it the two best so far
+    const float u = value(key[i]), w = i + 1 < VT ? value(key[i + 1 < VT ? i + 1 : i]) : -INFINITY;
+    const float p = fmaxf(u, w);
+    b2 = fmaxf(fmaxf(b2, fminf(u, w)), fminf(hi, p));
+    hi = fmaxf(hi, p);
+  }
+  return FULL || cnt > 0 ? hi : kNoKey;
+}
+
+// The value of a lane's group, in every lane of the group, from its lanes' largest and second keys: their
+// sum, or the largest.
+__device__ __forceinline__ float group_value(float b1, float b2, int lanes, bool both) {
+  b1 = fmaxf(b1, -INFINITY);
+  for (int off = lanes >> 1; off > 0; off >>= 1) {
+    const float o1 = __shfl_xor_sync(0xffffffffu, b1, off);
+    if (both) {
+      const float o2 = __shfl_xor_sync(0xffffffffu, b2, off);
+      b2 = fmaxf(fmaxf(fminf(b1, o1), b2), o2);
+    }
+    b1 = fmaxf(b1, o1);
+  }
+  return fmaxf(both ? __fadd_rn(b1, b2) : b1, -INFINITY);
+}
+
+// The experts of the k largest keys, in descending order, ties to the lower expert, and their scores:
+// returned in lanes 0 .. k-1.  Lane order is expert order.
+//
+// Of the lanes' own maxima (`top`; kNoKey: the lane has no candidate), the k-th largest bounds the k-th
+// largest key from below, so only keys at least that large can be chosen: about k of them.  They move to
+// one lane each, which computes its candidate's key and counts how many stand in front of it -- a few
+// instructions per candidate in place of k rounds over every key.  key holds the keys, or (slack) values
+// that are at most key_slack off.  False where that leaves more than 32, or a bound without slack.
+template <int VT, class KeyOf>
+__device__ __forceinline__ bool pick_top(const float (&key)[VT], const float (&l)[VT], float top, bool slack, int e0, int k, int lane,
+                                         ScoreScratch& sc, KeyOf key_of, int& chosen, float& score) {
+  float bound = 0.f, rem = top;
+#pragma unroll 4
+  for (int j = 0; j < k; ++j) {  // equal maxima leave together: the bound is then a little lower
+    bound = redux_max(rem);
+    rem = rem == bound ? kNoKey : rem;
+  }
+  bound = fmaxf(bound, -INFINITY);  // NaN, fewer than k lanes with candidates: every candidate
+  if (slack) {
+    if (isinf(bound)) return false;
+    bound -= 2.f * key_slack(bound);
+  }
+  uint32_t mask = 0;
+  if (!isnan(top)) {
+#pragma unroll
+    for (int i = 0; i < VT; ++i) mask |= key[i] >= bound ? 1u << i : 0u;
+  }
+  const int c = __popc(mask);
+  int incl = c;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += o;
+  }
+  const int total = __shfl_sync(0xffffffffu, incl, 31);
+  if (total > 32) return false;
+  int at = incl - c;
+  if constexpr (VT <= 4) {
+#pragma unroll
+    for (int i = 0; i < VT; ++i)
+      if (mask >> i & 1) {
+        sc.cand[at] = e0 + i;
+        sc.logit[at++] = l[i];
+      }
+  } else {  // the logit is read again: cheaper than picking it out of VT registers
+    for (; mask; mask &= mask - 1) sc.cand[at++] = e0 + __ffs(mask) - 1;
+  }
+  __syncwarp();
+  const int e = sc.cand[lane < total ? lane : 0];
+  float sv;
+  const float mine = key_of(e, VT <= 4 ? sc.logit[lane < total ? lane : 0] : kNoKey, sv);
+  int front = 0;
+#pragma unroll 4
+  for (int j = 0; j < total; ++j) {
+    const float o = __shfl_sync(0xffffffffu, mine, j);
+    front += j < lane ? o >= mine : o > mine;
+  }
+  if (lane < total && front < k) {
+    sc.expert[front] = e;
+    sc.score[front] = sv;
+  }
+  __syncwarp();
+  chosen = sc.expert[lane & 7];
+  score = sc.score[lane & 7];
+  __syncwarp();
+  return true;
+}
+
+// The same by k rounds over every key: few keys per lane, or very many equal ones.
+template <int VT>
+__device__ __forceinline__ int pick_by_rounds(float (&key)[VT], int e0, int k, int lane) {
+  int chosen = 0;
   for (int j = 0; j < k; ++j) {
     float bk = key[0];
     int be = 0;
@@ -175,53 +230,26 @@ __device__ __forceinline__ bool pick_top(float (&key)[VT], const float (&val)[VT
       if (lane == wl && i == be) key[i] = kNoKey;  // taken
     if (lane == j) chosen = we;
   }
-  return true;
+  return chosen;
 }
 
-// A group's value from its lanes' two largest (in every lane of the group): their sum, or the largest.
-__device__ __forceinline__ float group_value(float b1, float b2, int lanes, bool both) {
-  for (int off = lanes >> 1; off > 0; off >>= 1) {
-    const float o1 = __shfl_xor_sync(0xffffffffu, b1, off), o2 = __shfl_xor_sync(0xffffffffu, b2, off);
-    b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
-    b1 = fmaxf(b1, o1);
-  }
-  return fmaxf(both ? __fadd_rn(b1, b2) : b1, -INFINITY);
-}
-
-// Writes the token's top_k experts and weights; returns the lane's expert (lane < k).  VT >= g.per; cand:
-// 64 entries of shared memory for this warp.
+// Writes the token's top_k experts and weights; returns the lane's expert (lane < k).  VT >= g.per; sc:
+// this warp's.
 template <int VT>
 __device__ __forceinline__ int score_token(const ScoreArgs& a, const ScoreGeom& g, int t, int k, int lane,
-                                           int32_t* __restrict__ topk_idx, float* __restrict__ topk_w, ScoreCand* cand) {
+                                           int32_t* __restrict__ topk_idx, float* __restrict__ topk_w, ScoreScratch& sc) {
   const int lanes = 1 << g.lanes_log2, grp = lane >> g.lanes_log2, sub = lane & (lanes - 1);
   const int e0 = grp * g.S + sub * g.per;
-  const int cnt = grp < a.r.groups ? min(max(g.S - sub * g.per, 0), g.per) : 0;
+  const int cnt = g.full ? VT : grp < a.r.groups ? min(max(g.S - sub * g.per, 0), g.per) : 0;
   const int64_t row = (int64_t)t * a.ld;
   const bool softmax = a.r.score == MOE_SCORE_SOFTMAX, biased = a.bias != nullptr;
-  const bool two = a.r.groups > 1 && a.r.group_top == 2;
-  float l[VT], bv[VT];
+  const bool grouped = a.r.groups > 1, two = grouped && a.r.group_top == 2 && g.S > 1;
+  float l[VT];
   load_logits<VT>(a, g, row + e0, cnt, l);
-  if (biased) {
-    if (VT >= 4 && g.wide) {
-#pragma unroll
-      for (int i = 0; i < VT / 4; ++i) {
-        const float4 q = cnt ? ((const float4*)(a.bias + e0))[i] : make_float4(0.f, 0.f, 0.f, 0.f);
-        bv[4 * i] = q.x;
-        bv[(4 * i + 1) % VT] = q.y;
-        bv[(4 * i + 2) % VT] = q.z;
-        bv[(4 * i + 3) % VT] = q.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < VT; ++i) bv[i] = i < cnt ? a.bias[e0 + i] : 0.f;
-    }
-  }
   float m = 0.f, den = 1.f;  // the row's maximum and sum of e^(l - m), where a score needs them
   if (softmax && (biased || two || !a.r.renormalize)) {
-    m = l[0];
-#pragma unroll
-    for (int i = 1; i < VT; ++i) m = fmaxf(m, l[i]);
-    m = redux_max(m);
+    float none;
+    m = redux_max(lane_top<false, VT>(l, cnt, false, none));
     if (biased || !a.r.renormalize) {
       den = 0.f;
 #pragma unroll
@@ -229,7 +257,16 @@ __device__ __forceinline__ int score_token(const ScoreArgs& a, const ScoreGeom& 
       den = warp_sum(den);
     }
   }
+  // expert e's key (known: its logit, with few experts per lane); sv: its sigmoid score, or its logit where the score is a softmax's
+  auto key_of = [&](int e, float known, float& sv) {
+    const float lv = VT <= 4 ? known : load_logit(a, row + e);
+    sv = softmax ? lv : sigmoid_rn(lv);
+    if (!biased) return lv;
+    const float s = softmax ? (den > 0.f ? __fdiv_rn(exp_rn(lv, m), den) : 0.f) : sv;
+    return fmaxf(__fadd_rn(s, a.bias[e]), -INFINITY);
+  };
   int mine = 0;
+  float sv = 0.f, b2 = -INFINITY;
   bool done = false;
   if constexpr (VT >= 4) {
     // Sigmoid keys with a bias: the fast exponential and division place every key to within key_slack
@@ -237,39 +274,43 @@ __device__ __forceinline__ int score_token(const ScoreArgs& a, const ScoreGeom& 
     // the sum's rounding), which leaves few experts that could be chosen, and only those get their exact
     // key.  Where groups or keys stand closer than that, everything is done exactly below.
     if (biased && !softmax) {
-      float est[VT], b1 = -INFINITY, b2 = -INFINITY;
+      float est[VT];
+      if (g.full) {
 #pragma unroll
-      for (int i = 0; i < VT; ++i) {
-        const float v = __fdividef(1.f, 1.f + __expf(-l[i])) + bv[i];
-        est[i] = i < cnt ? fmaxf(v, -INFINITY) : kNoKey;
+        for (int i = 0; i < VT / 4; ++i) {
+          const float4 q = ((const float4*)(a.bias + e0))[i];
+          est[4 * i] = q.x;
+          est[4 * i + 1] = q.y;
+          est[4 * i + 2] = q.z;
+          est[4 * i + 3] = q.w;
+        }
+#pragma unroll
+        for (int i = 0; i < VT; ++i) est[i] = fmaxf(__fdividef(1.f, 1.f + __expf(-l[i])) + est[i], -INFINITY);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VT; ++i) est[i] = i < cnt ? a.bias[e0 + i] : 0.f;
+#pragma unroll
+        for (int i = 0; i < VT; ++i)
+          est[i] = i < cnt ? fmaxf(__fdividef(1.f, 1.f + __expf(-l[i])) + est[i], -INFINITY) : kNoKey;
       }
+      float top = g.full ? lane_top<true, VT>(est, cnt, two, b2) : lane_top<false, VT>(est, cnt, two, b2);
       bool clear = true;
-      if (a.r.groups > 1) {
-#pragma unroll
-        for (int i = 0; i < VT; ++i) {
-          const float s = fmaxf(est[i], -INFINITY);
-          b2 = fmaxf(b2, fminf(b1, s));
-          b1 = fmaxf(b1, s);
+      if (grouped) {
+        const float gv = group_value(top, b2, lanes, two);
+        float bound = 0.f, rem = grp < a.r.groups ? gv : kNoKey;
+#pragma unroll 4
+        for (int j = 0; j < a.r.top_groups; ++j) {
+          bound = redux_max(rem);
+          rem = rem == bound ? kNoKey : rem;
         }
-        const bool both = two && g.S > 1;
-        const float gv = group_value(b1, b2, lanes, both);
-        const float gap = 4.f * key_slack(gv), hi = gv + gap, lo = gv - gap;
-        int front = 0, near = 0;  // groups surely in front, and those that may be
-        for (int h = 0; h < a.r.groups; ++h) {
-          const float o = __shfl_sync(0xffffffffu, gv, h << g.lanes_log2);
-          front += o > hi;
-          near += o >= lo;
-        }
-        // itself counts among the near ones
-        clear = grp >= a.r.groups || (!isinf(gv) && (front < a.r.top_groups) == (near - 1 < a.r.top_groups));
-        if (front >= a.r.top_groups)
-#pragma unroll
-          for (int i = 0; i < VT; ++i) est[i] = kNoKey;
+        // the last group kept, and no other within reach of it
+        const float gap = 4.f * key_slack(bound);
+        const uint32_t near = __ballot_sync(0xffffffffu, grp < a.r.groups && fabsf(gv - bound) <= gap);
+        const uint32_t kept = __ballot_sync(0xffffffffu, grp < a.r.groups && gv >= bound);
+        clear = __popc(near) == lanes && __popc(kept) == lanes * a.r.top_groups && !isinf(bound);
+        if (!(gv >= bound)) top = kNoKey;
       }
-      if (__all_sync(0xffffffffu, clear))
-        done = pick_top<false, VT>(est, l, e0, k, lane, cand,
-                                   [&](float lv, int e) { return fmaxf(__fadd_rn(sigmoid_rn(lv), a.bias[e]), -INFINITY); },
-                                   mine);
+      if (clear) done = pick_top<VT>(est, l, top, true, e0, k, lane, sc, key_of, mine, sv);
     }
   }
   if (!done) {
@@ -278,49 +319,47 @@ __device__ __forceinline__ int score_token(const ScoreArgs& a, const ScoreGeom& 
 #pragma unroll
       for (int i = 0; i < VT; ++i) {
         const float s = softmax ? (den > 0.f ? __fdiv_rn(exp_rn(l[i], m), den) : 0.f) : sigmoid_rn(l[i]);
-        key[i] = i < cnt ? fmaxf(__fadd_rn(s, bv[i]), -INFINITY) : kNoKey;
+        key[i] = i < cnt ? fmaxf(__fadd_rn(s, a.bias[e0 + i]), -INFINITY) : kNoKey;
       }
     } else {
 #pragma unroll
       for (int i = 0; i < VT; ++i) key[i] = i < cnt ? l[i] : kNoKey;
     }
-    if (a.r.groups > 1) {
-      float b1 = -INFINITY, b2 = -INFINITY;  // the lane's two largest group values
-      if (!biased && two) {
-#pragma unroll
-        for (int i = 0; i < VT; ++i) {
-          const float s = i < cnt ? (softmax ? exp_rn(l[i], m) : sigmoid_rn(l[i])) : -INFINITY;
-          b2 = fmaxf(b2, fminf(b1, s));
-          b1 = fmaxf(b1, s);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < VT; ++i) {
-          const float s = fmaxf(key[i], -INFINITY);
-          b2 = fmaxf(b2, fminf(b1, s));
-          b1 = fmaxf(b1, s);
-        }
+    b2 = -INFINITY;
+    float top = lane_top<false, VT>(key, cnt, two, b2);
+    if (grouped) {
+      float g1 = top;
+      if (two && !biased) {  // scores in place of logits, whose order they have
+        g1 = isnan(top) ? -INFINITY : softmax ? exp_rn(top, m) : sigmoid_rn(top);
+        b2 = cnt < 2 ? -INFINITY : softmax ? exp_rn(b2, m) : sigmoid_rn(b2);
       }
-      const float gv = group_value(b1, b2, lanes, two && g.S > 1);
+      const float gv = group_value(g1, b2, lanes, two);
       int front = 0;  // groups in front of this one
       for (int h = 0; h < a.r.groups; ++h) {
         const float o = __shfl_sync(0xffffffffu, gv, h << g.lanes_log2);
         front += o > gv || (o == gv && h < grp);
       }
-      if (front >= a.r.top_groups)
+      if (front >= a.r.top_groups) {
+        top = kNoKey;
 #pragma unroll
         for (int i = 0; i < VT; ++i) key[i] = kNoKey;
+      }
     }
-    pick_top<true, VT>(key, l, e0, k, lane, cand, [](float v, int) { return v; }, mine);
+    if constexpr (VT >= 4)
+      done = pick_top<VT>(key, l, top, false, e0, k, lane, sc, key_of, mine, sv);
+    if (!done) {
+      mine = pick_by_rounds<VT>(key, e0, k, lane);
+      if (lane < k) {
+        sv = load_logit(a, row + mine);
+        if (!softmax) sv = sigmoid_rn(sv);
+      }
+    }
   }
-  float s = 0.f;
-  if (softmax && a.r.renormalize) {
-    const float ls = lane < k ? load_logit(a, row + mine) : -INFINITY;
-    const float ms = redux_max(ls);
-    s = lane < k ? exp_rn(ls, ms) : 0.f;
-  } else if (lane < k) {
-    const float ls = load_logit(a, row + mine);
-    s = softmax ? (den > 0.f ? exp_rn(ls, m) / den : 0.f) : sigmoid_rn(ls);
+  float s = lane < k ? sv : 0.f;
+  if (softmax) {
+    const float ms = a.r.renormalize ? redux_max(lane < k ? sv : -INFINITY) : m;
+    s = lane < k ? exp_rn(sv, ms) : 0.f;
+    if (!a.r.renormalize) s = den > 0.f ? s / den : 0.f;
   }
   if (a.r.renormalize) {
     float tot = s;
@@ -347,6 +386,7 @@ inline ScoreGeom score_geom(const ScoreArgs& a, int E) {
   g.per = (g.S + (1 << lg) - 1) >> lg;
   g.wide = g.per % 4 == 0 && (g.per & (g.per - 1)) == 0 && g.S == g.per << lg && a.ld % 4 == 0 &&
            (uintptr_t)a.logits % (4 * dtype_size(a.dtype)) == 0 && (uintptr_t)a.bias % 16 == 0;
+  g.full = g.wide && G == a.r.groups;
   return g;
 }
 
