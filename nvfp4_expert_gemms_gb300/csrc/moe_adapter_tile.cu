@@ -108,8 +108,7 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
     return;
   }
   unsigned char* v_mem = (unsigned char*)(((uintptr_t)dyn + 1023) & ~(uintptr_t)1023);
-  // v's hi and lo; then the K stages, whose memory is N stage 1 later; then N stage 0, which can be loaded
-  // while the first product runs
+  // v's hi and lo, then the K stages, whose memory is the two N stages' later
   unsigned char* ring = v_mem + 2 * p.katoms * kAtom;
   const int natom = p.bps * kAtom, ybytes = p.katoms * natom;  // an atom of a stage's B; where its base begins
   const int atoms = (a.H + 63) / 64, kst = (atoms + p.ka - 1) / p.ka;
@@ -167,7 +166,6 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
           tma_load_3d(at, &p.x, &bars.full_k[s], 0, tile.t0, p.ka * k);
           tma_load_3d(at + p.ka * kAtom, &p.a, &bars.full_k[s], 0, tile.slot * a.r, p.ka * k);
         }
-        if (k == (kst < p.nk ? kst : p.nk) - 1) load_n();
       }
       if (k == kst && mbar_wait(&bars.v_sums, 0, abort))  // every K stage has been read
         while (n < nst) {
@@ -383,13 +381,13 @@ cudaError_t launch_adapter_tiles(const AdapterArgs& g, cudaStream_t s) {
   p.katoms = (g.r + 63) / 64;
   p.bps = p.katoms == 1 ? 2 : 1;
   p.nslot = p.bps * (p.katoms + 2) * kAtom;  // B's rows and base's columns of the stage's blocks
-  // A stage costs the copy unit much the same whatever its size, so K stages are as wide as two of them fit
-  // (H in whole atoms: the 3-D maps count columns by atoms).
+  // K stages: four at least in the memory of the N stages, two atoms wide where that leaves as many (H in
+  // whole atoms then: the 3-D maps count columns by atoms)
   const int64_t tiles = tile_bound(g, kBM);
   const int katom = kAtom + p.r16 * 128;
-  p.ka = g.H % 64 != 0 ? 1 : p.nslot / (2 * katom) >= 2 ? 2 : 1;
+  p.ka = g.H % 64 == 0 && 2 * p.nslot / (2 * katom) >= 4 ? 2 : 1;
   p.kslot = p.ka * katom;
-  p.nk = p.nslot / p.kslot < kMaxSlots ? p.nslot / p.kslot : kMaxSlots;
+  p.nk = 2 * p.nslot / p.kslot < kMaxSlots ? 2 * p.nslot / p.kslot : kMaxSlots;
   const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
   const bool maps =
