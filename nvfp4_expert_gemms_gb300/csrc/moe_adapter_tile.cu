@@ -45,6 +45,7 @@ struct TileArgs {
   int ka, kslot;      // 64-column atoms and bytes of a K stage
   int bps, nslot;     // 128-column blocks and bytes of an N stage
   int nk;             // K stages
+  bool dealt;         // B's rows dealt for a direct epilogue (whole 64-column groups, 32-byte rows of out)
 };
 
 struct Bars {
@@ -149,9 +150,13 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
         unsigned char* at = ring + (1 - (n & 1)) * p.nslot;
         uint64_t* full = &bars.full_n[n & 1];
         mbar_arrive_expect_tx(full, p.nslot);
+        const int c0 = 128 * p.bps * n;
         for (int i = 0; i < p.katoms; ++i)
-          tma_load_5d(at + i * natom, &p.b, full, 64 * i, (tile.slot * a.N + 128 * p.bps * n) / 64);
-        tma_load_3d(at + ybytes, &p.y, full, 0, tile.t0, 2 * p.bps * n);
+          if (p.dealt) tma_load_5d(at + i * natom, &p.b, full, 64 * i, (tile.slot * a.N + c0) / 64);
+          else tma_load_2d(at + i * natom, &p.b, full, 64 * i, tile.slot * a.N + c0);
+        if (p.dealt) tma_load_3d(at + ybytes, &p.y, full, 0, tile.t0, c0 / 64);
+        else
+          for (int i = 0; i < 2 * p.bps; ++i) tma_load_2d(at + ybytes + i * kAtom, &p.y, full, c0 + 64 * i, tile.t0);
         ++n;
       };
       for (; k < kst; ++k) {
@@ -269,51 +274,71 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
       fence_proxy_async_smem();
       mbar_arrive(&bars.v_ready);
     }
-    // The accumulator's fragments give a lane 16 consecutive columns (the map of B deals its rows so) of four
-    // rows of the tile: four lanes hold a row's 128 bytes.
-    const int g = lane >> 2, t = lane & 3;
-    __nv_bfloat16* out[4];
-    bool live[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 32 * quarter + g + 8 * i;
-      live[i] = r < tile.rows;
-      out[i] = a.out + (int64_t)(tile.t0 + (live[i] ? r : 0)) * a.ldo + 64 * half + 16 * t;
-    }
+    // The accumulator's fragments: with B's rows dealt, a lane holds 16 consecutive columns of four rows of
+    // the tile and four lanes a row's 128 bytes, which go out as they are.  Else it holds pairs of columns,
+    // which are added in place to base in shared memory, from where the warp writes whole rows.
+    const int g = lane >> 2, t = lane & 3, r0 = 32 * quarter;
     for (int n = 0; ok && n < nblk; ++n) {
-      const int st = n / p.bps, sub = n % p.bps, s = st & 1, buf = n & 1;
+      const int st = n / p.bps, sub = n % p.bps, s = st & 1, buf = n & 1, col = 128 * n + 64 * half;
+      const bool last = sub == p.bps - 1 || n == nblk - 1;
       if (sub == 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars.full_n[s], (st >> 1) & 1, abort));
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars.acc_full[buf], (n >> 1) & 1, abort));
       if (!ok) break;
       fence_after_sync();
       uint32_t w[2][32];
-      tmem_ld_16x64(taddr(tmem, 32 * quarter, 128 * buf + 64 * half), w[0]);
-      tmem_ld_16x64(taddr(tmem, 32 * quarter + 16, 128 * buf + 64 * half), w[1]);
-      // base: the stage's atom of this half, a row's pieces 2 t and 2 t + 1 (eight lanes: all banks once)
-      const unsigned char* ys = ring + (1 - s) * p.nslot + ybytes + (2 * sub + half) * kAtom;
-      uint4 y[4][2];
+      tmem_ld_16x64(taddr(tmem, r0, 128 * buf + 64 * half), w[0]);
+      tmem_ld_16x64(taddr(tmem, r0 + 16, 128 * buf + 64 * half), w[1]);
+      unsigned char* ys = ring + (1 - s) * p.nslot + ybytes + (2 * sub + half) * kAtom;  // base of this half
+      if (p.dealt) {
+        uint4 y[4][2];  // a row's pieces 2 t and 2 t + 1 (eight lanes: all banks once)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) y[i][h] = *(const uint4*)(ys + swz(32 * quarter + g + 8 * i, 2 * t + h));
-      tmem_ld_wait();
-      fence_before_sync();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&bars.acc_empty[buf]);
-        if (sub == p.bps - 1 || n == nblk - 1) mbar_arrive(&bars.empty_n[s]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (live[i] && 128 * n + 64 * half < a.N) {
-          const uint32_t* b = (const uint32_t*)y[i];
-          uint32_t o[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            o[j] = pack_bf16(lo_f32(b[j]) + __uint_as_float(w[i >> 1][4 * j + 2 * (i & 1)]),
-                             hi_f32(b[j]) + __uint_as_float(w[i >> 1][4 * j + 2 * (i & 1) + 1]));
-          st_global_v8(out[i] + 128 * n, o);
+          for (int h = 0; h < 2; ++h) y[i][h] = *(const uint4*)(ys + swz(r0 + g + 8 * i, 2 * t + h));
+        tmem_ld_wait();
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars.acc_empty[buf]);
+          if (last) mbar_arrive(&bars.empty_n[s]);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = r0 + g + 8 * i;
+          if (r < tile.rows && col < a.N) {
+            const uint32_t* b = (const uint32_t*)y[i];
+            uint32_t o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              o[j] = pack_bf16(lo_f32(b[j]) + __uint_as_float(w[i >> 1][4 * j + 2 * (i & 1)]),
+                               hi_f32(b[j]) + __uint_as_float(w[i >> 1][4 * j + 2 * (i & 1) + 1]));
+            st_global_v8(a.out + (int64_t)(tile.t0 + r) * a.ldo + col + 16 * t, o);
+          }
+        }
+      } else {
+        tmem_ld_wait();
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {  // columns 8 j + 2 t and the next: 32 lanes on 32 banks
+            uint32_t* q = (uint32_t*)(ys + swz(r0 + g + 8 * i, j)) + t;
+            *q = pack_bf16(lo_f32(*q) + __uint_as_float(w[i >> 1][4 * j + 2 * (i & 1)]),
+                           hi_f32(*q) + __uint_as_float(w[i >> 1][4 * j + 2 * (i & 1) + 1]));
+          }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = r0 + 4 * i + (lane >> 3), c = col + 8 * (lane & 7);
+          const uint4 q = *(const uint4*)(ys + swz(r, lane & 7));
+          if (r < tile.rows && c < a.N) *(uint4*)(a.out + (int64_t)(tile.t0 + r) * a.ldo + c) = q;
+        }
+        fence_proxy_async_smem();  // the next copy into this memory comes after these accesses
+        __syncwarp();
+        if (lane == 0 && last) mbar_arrive(&bars.empty_n[s]);
+      }
     }
   }
   fence_before_sync();
@@ -367,10 +392,8 @@ static bool rows_map(CUtensorMap* m, const void* base, uint64_t rows, int r, int
   return bf16_map(m, base, 5, dims, strides, box);
 }
 
-// 32-byte accesses to base and out, whole 64-column groups of B's rows.
-bool adapter_tiles_fit(const AdapterArgs& a) {
-  return a.N % 64 == 0 && a.ldb % 16 == 0 && a.ldo % 16 == 0 && (uintptr_t)a.base % 32 == 0 && (uintptr_t)a.out % 32 == 0 &&
-         (int64_t)a.n * a.N < INT32_MAX && (int64_t)a.n * a.r < INT32_MAX;
+bool adapter_tiles_fit(const AdapterArgs& a) {  // rows of A and B by 32-bit coordinates
+  return (int64_t)a.n * a.N < INT32_MAX && (int64_t)a.n * a.r < INT32_MAX;
 }
 
 cudaError_t launch_adapter_tiles(const AdapterArgs& g, cudaStream_t s) {
@@ -395,9 +418,12 @@ cudaError_t launch_adapter_tiles(const AdapterArgs& g, cudaStream_t s) {
                       tc_make_map(&p.a, bf16, g.A, g.H, (uint64_t)g.n * g.r, (uint64_t)g.H * 2, 64, p.r16, sw)
                 : atoms_map(&p.x, g.x, g.T, g.H, g.ldx, kBM, p.ka) &&
                       atoms_map(&p.a, g.A, (uint64_t)g.n * g.r, g.H, g.H, p.r16, p.ka);
-  if (!maps || !rows_map(&p.b, g.B, (uint64_t)g.n * g.N, g.r, 2 * p.bps) ||
-      !atoms_map(&p.y, g.base, g.T, g.N, g.ldb, kBM, 2 * p.bps))
-    return cudaErrorInvalidValue;
+  p.dealt = g.N % 64 == 0 && g.ldo % 16 == 0 && (uintptr_t)g.out % 32 == 0;
+  const uint64_t brows = (uint64_t)g.n * g.N;
+  const bool nmaps = p.dealt ? rows_map(&p.b, g.B, brows, g.r, 2 * p.bps) && atoms_map(&p.y, g.base, g.T, g.N, g.ldb, kBM, 2 * p.bps)
+                             : tc_make_map(&p.b, bf16, g.B, g.r, brows, (uint64_t)g.r * 2, 64, 128 * p.bps, sw) &&
+                                   tc_make_map(&p.y, bf16, g.base, g.N, g.T, (uint64_t)g.ldb * 2, 64, kBM, sw);
+  if (!maps || !nmaps) return cudaErrorInvalidValue;
   static std::atomic<bool> set{false};
   if (!set.load(std::memory_order_relaxed)) {
     const cudaError_t e = cudaFuncSetAttribute(adapter_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
