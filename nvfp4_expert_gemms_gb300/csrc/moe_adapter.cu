@@ -461,9 +461,14 @@ cudaError_t launch_rank(const AdapterArgs& a, cudaStream_t s) {
   return launch_few<RT>(a, g_cluster, s);
 #endif
   const int64_t mean = a.T / (a.R > 0 ? a.R : 1), tiles = tile_bound(a, 16);
+  // Long requests.  Ranks up to 16: register MMAs keep up with HBM (16384 tokens, 2048 -> 2048: 40.2 us, the
+  // tcgen05 tiles 40.2 even and 59.4 ragged; 4096 tokens: tiles of 32 tokens 22.7 us, the kernel for few 15.4).
+  // Higher ranks: the tcgen05 tiles from where the kernel for few, whose time goes by T r (H + N), takes longer
+  // than their some 20 us (4096 tokens at rank 64: 22.0 against 28.9 us; at rank 32: 19.4 against 17.2).
   if constexpr (RT == 1)
     if (a.T >= 8192 && mean >= 32) return launch_many<1, 2, 2>(a, s);
-  if (mean >= 128 && (int64_t)a.T * a.r >= 200000 && adapter_tiles_fit(a)) return launch_adapter_tiles(a, s);
+  if (RT > 1 && mean >= 128 && (double)a.T * (16 * RT) * (a.H + a.N) >= 8e8 && adapter_tiles_fit(a))
+    return launch_adapter_tiles(a, s);
   // blocks of a cluster share a tile as long as the grid fits the device at once
   const int64_t room = (int64_t)tc_num_sms() * (RT <= 4 ? 2 : 1);
   return launch_few<RT>(a, 8 * tiles <= room ? 8 : 4 * tiles <= room ? 4 : 2 * tiles <= room ? 2 : 1, s);

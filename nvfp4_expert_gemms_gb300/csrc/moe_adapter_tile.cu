@@ -18,6 +18,7 @@
 // Every wait gives up after about a second (moe_tc.cuh); the block then waits, with the same limit, for
 // its own copies and MMAs, frees its tensor memory, leaves its rows unfinished and records a timeout that
 // moe_get_adapter_error reads.
+#include <cooperative_groups.h>
 #include <cudaTypedefs.h>
 #include <string.h>
 
@@ -25,6 +26,8 @@
 
 #include "moe_adapter.cuh"
 #include "moe_tc.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace moe {
 namespace {
@@ -95,13 +98,15 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
-  const Tile tile = find_tile<kTileWarps>(a, blockIdx.x, kBM);
-  if (tile.rows == 0) return;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = cluster.num_blocks(), crank = cluster.block_rank();
+  const Tile tile = find_tile<kTileWarps>(a, blockIdx.x / C, kBM);
+  if (tile.rows == 0) return;  // the whole cluster
   const int rk = tile.rk, steps = (rk + 15) / 16;
   if (rk == 0) {  // no adapter: base as it is
     if (a.out == a.base) return;
     const int chunks = a.N / 8;
-    for (int64_t e = tid; e < (int64_t)tile.rows * chunks; e += 32 * kTileWarps) {
+    for (int64_t e = crank * 32 * kTileWarps + tid; e < (int64_t)tile.rows * chunks; e += C * 32 * kTileWarps) {
       const int64_t t = tile.t0 + e / chunks;
       const int c = (int)(e % chunks) * 8;
       *(uint4*)(a.out + t * a.ldo + c) = *(const uint4*)(a.base + t * a.ldb + c);
@@ -112,8 +117,12 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
   // v's hi and lo, then the K stages, whose memory is the two N stages' later
   unsigned char* ring = v_mem + 2 * p.katoms * kAtom;
   const int natom = p.bps * kAtom, ybytes = p.katoms * natom;  // an atom of a stage's B; where its base begins
-  const int atoms = (a.H + 63) / 64, kst = (atoms + p.ka - 1) / p.ka;
-  const int nblk = (a.N + 127) / 128, nst = (nblk + p.bps - 1) / p.bps;  // column blocks, N stages
+  // this block's part of the K stages and of the N stages (column blocks)
+  const int atoms = (a.H + 63) / 64, kall = (atoms + p.ka - 1) / p.ka, kper = (kall + C - 1) / C;
+  const int k0 = min(crank * kper, kall), kst = min(kper, kall - k0);
+  const int ball = (a.N + 127) / 128, nall = (ball + p.bps - 1) / p.bps, nper = (nall + C - 1) / C;
+  const int n0 = min(crank * nper, nall), nst = min(nper, nall - n0);
+  const int b0 = n0 * p.bps, nblk = max(0, min(nst * p.bps, ball - b0));
   const bool partial = rk % 16 != 0;  // the last rank step of B holds columns that are not the adapter's
   if (tid == 0) {
     for (int i = 0; i < kMaxSlots; ++i) {
@@ -140,27 +149,32 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
   const uint32_t tmem = bars.tmem;
   volatile int* abort = &bars.abort;
 
-  if (warp == kEpiWarps) {  // ---- copies
+  const int quarter = warp & 3, half = warp >> 2;  // of the epilogue's warps: tensor-memory lanes, columns
+  int kdone = 0, n = 0;                            // copies issued: K stages, N stages
+  bool ok = true;
+  auto load_n = [&] {  // N stage n
+    unsigned char* at = ring + (1 - (n & 1)) * p.nslot;
+    uint64_t* full = &bars.full_n[n & 1];
+    const int c0 = 128 * p.bps * (n0 + n);
+    mbar_arrive_expect_tx(full, p.nslot);
+    for (int i = 0; i < p.katoms; ++i)
+      if (p.dealt) tma_load_5d(at + i * natom, &p.b, full, 64 * i, (tile.slot * a.N + c0) / 64);
+      else tma_load_2d(at + i * natom, &p.b, full, 64 * i, tile.slot * a.N + c0);
+    if (p.dealt) tma_load_3d(at + ybytes, &p.y, full, 0, tile.t0, c0 / 64);
+    else
+      for (int i = 0; i < 2 * p.bps; ++i) tma_load_2d(at + ybytes + i * kAtom, &p.y, full, c0 + 64 * i, tile.t0);
+    ++n;
+  };
+
+  // ---- the first product
+  if (warp == kEpiWarps) {  // copies
     if (lane == 0) {
       prefetch_tmap(&p.x);
       prefetch_tmap(&p.a);
       prefetch_tmap(&p.b);
-      int k = 0, n = 0;
-      auto load_n = [&] {  // N stage n
-        unsigned char* at = ring + (1 - (n & 1)) * p.nslot;
-        uint64_t* full = &bars.full_n[n & 1];
-        mbar_arrive_expect_tx(full, p.nslot);
-        const int c0 = 128 * p.bps * n;
-        for (int i = 0; i < p.katoms; ++i)
-          if (p.dealt) tma_load_5d(at + i * natom, &p.b, full, 64 * i, (tile.slot * a.N + c0) / 64);
-          else tma_load_2d(at + i * natom, &p.b, full, 64 * i, tile.slot * a.N + c0);
-        if (p.dealt) tma_load_3d(at + ybytes, &p.y, full, 0, tile.t0, c0 / 64);
-        else
-          for (int i = 0; i < 2 * p.bps; ++i) tma_load_2d(at + ybytes + i * kAtom, &p.y, full, c0 + 64 * i, tile.t0);
-        ++n;
-      };
-      for (; k < kst; ++k) {
-        const int s = k % p.nk, u = k / p.nk;
+      prefetch_tmap(&p.y);
+      for (; kdone < kst; ++kdone) {
+        const int s = kdone % p.nk, u = kdone / p.nk, k = k0 + kdone;
         if (u > 0 && !mbar_wait(&bars.empty_k[s], (u - 1) & 1, abort)) break;
         unsigned char* at = ring + s * p.kslot;
         mbar_arrive_expect_tx(&bars.full_k[s], p.kslot);
@@ -172,72 +186,147 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
           tma_load_3d(at + p.ka * kAtom, &p.a, &bars.full_k[s], 0, tile.slot * a.r, p.ka * k);
         }
       }
-      if (k == kst && mbar_wait(&bars.v_sums, 0, abort))  // every K stage has been read
-        while (n < nst) {
-          if (n > 1 && !mbar_wait(&bars.empty_n[n & 1], ((n >> 1) - 1) & 1, abort)) break;
-          load_n();
-        }
-      if (*abort) {  // copies in flight land before the block leaves
-        for (int i = k > p.nk ? k - p.nk : 0; i < k; ++i) drain(&bars.full_k[i % p.nk], (i / p.nk) & 1);
-        for (int i = n > 2 ? n - 2 : 0; i < n; ++i) drain(&bars.full_n[i & 1], (i >> 1) & 1);
-      }
+      ok = kdone == kst && mbar_wait(&bars.v_sums, 0, abort);  // every K stage has been read
+      while (ok && n < nst && n < 2) load_n();
     }
-  } else if (warp == kEpiWarps + 1) {  // ---- MMAs
+  } else if (warp == kEpiWarps + 1) {  // MMAs
     if (lane == 0) {
-      const uint32_t id1 = idesc_bf16_f32(128, 16 * steps), id2 = idesc_bf16_f32(128, 128);
-      bool ok = true;
+      const uint32_t id1 = idesc_bf16_f32(128, 16 * steps);
       for (int k = 0; ok && k < kst; ++k) {
         const int s = k % p.nk;
         ok = mbar_wait(&bars.full_k[s], (k / p.nk) & 1, abort);
         if (!ok) break;
         fence_after_sync();
         const uint32_t xs = smem_u32(ring + s * p.kslot), as = xs + p.ka * kAtom;
-        const int here = atoms - p.ka * k < p.ka ? atoms - p.ka * k : p.ka;
+        const int here = min(atoms - p.ka * (k0 + k), p.ka);
         for (int i = 0; i < 4 * here; ++i)
           mma_f16_ss(tmem, sdesc_k_sw128(xs + (i >> 2) * kAtom + (i & 3) * 32),
                      sdesc_k_sw128(as + (i >> 2) * p.r16 * 128 + (i & 3) * 32), id1, (k | i) != 0);
         mma_commit(&bars.empty_k[s]);
       }
-      if (ok) {
-        mma_commit(&bars.v_sums);
-        ok = mbar_wait(&bars.v_ready, 0, abort);
-        fence_after_sync();
+      if (ok) mma_commit(&bars.v_sums);
+    }
+  } else if (warp < kEpiWarps) {
+    ok = __all_sync(0xffffffffu, mbar_wait(&bars.v_sums, 0, abort));
+    fence_after_sync();
+  }
+  __syncwarp();
+
+  // ---- v: from tensor memory (in a cluster: every block's part of K, summed in block order) to shared
+  // memory, scaled, split, zero past the rank.  A thread has one row and every second rank step.
+  const int row = 32 * quarter + lane;
+  uint32_t hi[4][8], lo[4][8];
+  auto split = [&](int i, const float* f) {  // rank step half + 2 i
+    const int s = half + 2 * i;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float f0 = 16 * s + 2 * c < rk ? f[2 * c] * tile.scale : 0.f;
+      const float f1 = 16 * s + 2 * c + 1 < rk ? f[2 * c + 1] * tile.scale : 0.f;
+      hi[i][c] = pack_bf16(f0, f1);
+      lo[i][c] = pack_bf16(f0 - lo_f32(hi[i][c]), f1 - hi_f32(hi[i][c]));
+    }
+  };
+  float4* parts = (float4*)v_mem;  // [4 steps][128 rows]: this block's sums, where v's terms go afterwards
+  if (warp < kEpiWarps && ok) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (half + 2 * i < steps) {
+        uint32_t w[16];
+        tmem_ld_32x16(taddr(tmem, 32 * quarter, 16 * (half + 2 * i)), w);
+        tmem_ld_wait();
+        if (C == 1) {
+          split(i, (const float*)w);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            parts[(4 * (half + 2 * i) + c) * 128 + row] =
+                kst > 0 ? make_float4(__uint_as_float(w[4 * c]), __uint_as_float(w[4 * c + 1]),
+                                      __uint_as_float(w[4 * c + 2]), __uint_as_float(w[4 * c + 3]))
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
       }
-      const uint32_t hi = smem_u32(v_mem), lo = hi + p.katoms * kAtom;
-      for (int n = 0; ok && n < nblk; ++n) {
-        const int st = n / p.bps, sub = n % p.bps, s = st & 1, buf = n & 1;
-        if (n > 1) ok = mbar_wait(&bars.acc_empty[buf], ((n >> 1) - 1) & 1, abort);
+  }
+  if (C > 1) {
+    cluster.sync();
+    if (warp < kEpiWarps) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (half + 2 * i < steps) {
+          float f[16];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float4* at = &parts[(4 * (half + 2 * i) + c) * 128 + row];
+            float4 q = *cluster.map_shared_rank(at, 0);
+            for (int b = 1; b < C; ++b) {
+              const float4 o = *cluster.map_shared_rank(at, b);
+              q.x += o.x;
+              q.y += o.y;
+              q.z += o.z;
+              q.w += o.w;
+            }
+            f[4 * c] = q.x;
+            f[4 * c + 1] = q.y;
+            f[4 * c + 2] = q.z;
+            f[4 * c + 3] = q.w;
+          }
+          split(i, f);
+        }
+    }
+    cluster.sync();  // every block has read every part: their memory is v's now, and a block may leave
+  }
+
+  // ---- the second product
+  if (warp == kEpiWarps) {  // copies
+    if (lane == 0) {
+      while (ok && n < nst) {
+        ok = mbar_wait(&bars.empty_n[n & 1], ((n >> 1) - 1) & 1, abort);
+        if (ok) load_n();
+      }
+      if (*abort) {  // copies in flight land before the block leaves
+        for (int i = kdone > p.nk ? kdone - p.nk : 0; i < kdone; ++i) drain(&bars.full_k[i % p.nk], (i / p.nk) & 1);
+        for (int i = n > 2 ? n - 2 : 0; i < n; ++i) drain(&bars.full_n[i & 1], (i >> 1) & 1);
+      }
+    }
+  } else if (warp == kEpiWarps + 1) {  // MMAs
+    if (lane == 0) {
+      const uint32_t id2 = idesc_bf16_f32(128, 128);
+      if (ok) ok = mbar_wait(&bars.v_ready, 0, abort);
+      fence_after_sync();
+      const uint32_t vhi = smem_u32(v_mem), vlo = vhi + p.katoms * kAtom;
+      for (int b = 0; ok && b < nblk; ++b) {
+        const int st = b / p.bps, sub = b % p.bps, s = st & 1, buf = b & 1;
+        if (b > 1) ok = mbar_wait(&bars.acc_empty[buf], ((b >> 1) - 1) & 1, abort);
         if (ok && sub == 0) ok = mbar_wait(partial ? &bars.cut_n[s] : &bars.full_n[s], (st >> 1) & 1, abort);
         if (!ok) break;
         fence_after_sync();
         const uint32_t bs = smem_u32(ring + (1 - s) * p.nslot) + sub * kAtom, acc = tmem + 128 * buf;
         for (int i = 0; i < steps; ++i) {
           const uint32_t off = (i >> 2) * kAtom + (i & 3) * 32;
-          const uint64_t b = sdesc_k_sw128(bs + (i >> 2) * natom + (i & 3) * 32);
-          mma_f16_ss(acc, sdesc_k_sw128(lo + off), b, id2, i != 0);
-          mma_f16_ss(acc, sdesc_k_sw128(hi + off), b, id2, 1);
+          const uint64_t d = sdesc_k_sw128(bs + (i >> 2) * natom + (i & 3) * 32);
+          mma_f16_ss(acc, sdesc_k_sw128(vlo + off), d, id2, i != 0);
+          mma_f16_ss(acc, sdesc_k_sw128(vhi + off), d, id2, 1);
         }
-        if (sub == p.bps - 1 || n == nblk - 1) mma_commit(&bars.empty_n[s]);
+        if (sub == p.bps - 1 || b == nblk - 1) mma_commit(&bars.empty_n[s]);
         mma_commit(&bars.acc_full[buf]);
       }
       mma_commit(&bars.done);  // no arrival is on its way into this block's barriers when it leaves
       drain(&bars.done, 0);
     }
-  } else if (warp == kEpiWarps + 2) {  // ---- columns of B past the adapter's rank, where a step has some
+  } else if (warp == kEpiWarps + 2) {  // columns of B past the adapter's rank, where a step has some
     if (partial) {
       const int c0 = rk / 8, c1 = 2 * steps;  // 8-column chunks from the partial one on
-      for (int n = 0; n < nst; ++n) {
-        const int s = n & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars.full_n[s], (n >> 1) & 1, abort))) break;
+      for (int i = 0; i < nst; ++i) {
+        const int s = i & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars.full_n[s], (i >> 1) & 1, abort))) break;
         unsigned char* bs = ring + (1 - s) * p.nslot;
-        for (int row = lane; row < 128 * p.bps; row += 32)
+        for (int r = lane; r < 128 * p.bps; r += 32)
           for (int c = c0; c < c1; ++c) {
-            uint4* q = (uint4*)(bs + (c >> 3) * natom + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+            uint4* q = (uint4*)(bs + (c >> 3) * natom + r * 128 + (((c & 7) ^ (r & 7)) << 4));
             const int keep = rk - 8 * c;  // columns of the chunk that stay
             uint4 w = keep > 0 ? *q : make_uint4(0, 0, 0, 0);
             uint32_t* e = (uint32_t*)&w;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] = keep >= 2 * i + 2 ? e[i] : keep == 2 * i + 1 ? e[i] & 0xFFFFu : 0u;
+            for (int j = 0; j < 4; ++j) e[j] = keep >= 2 * j + 2 ? e[j] : keep == 2 * j + 1 ? e[j] & 0xFFFFu : 0u;
             *q = w;
           }
         fence_proxy_async_smem();
@@ -245,31 +334,17 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
         if (lane == 0) mbar_arrive(&bars.cut_n[s]);
       }
     }
-  } else {  // ---- v into shared memory, then out
-    const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
-    bool ok = __all_sync(0xffffffffu, mbar_wait(&bars.v_sums, 0, abort));
+  } else {  // epilogue
     if (ok) {
-      fence_after_sync();
-      for (int s = half; s < steps; s += 2) {
-        uint32_t w[16];
-        tmem_ld_32x16(taddr(tmem, 32 * quarter, 16 * s), w);
-        tmem_ld_wait();
-        uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float c0 = 16 * s + 2 * i < rk ? __uint_as_float(w[2 * i]) * tile.scale : 0.f;
-          const float c1 = 16 * s + 2 * i + 1 < rk ? __uint_as_float(w[2 * i + 1]) * tile.scale : 0.f;
-          hi[i] = pack_bf16(c0, c1);
-          lo[i] = pack_bf16(c0 - lo_f32(hi[i]), c1 - hi_f32(hi[i]));
-        }
-        unsigned char* to = v_mem;
+      for (int i = 0; i < 4; ++i)
+        if (half + 2 * i < steps)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          *(uint4*)(to + swz(row, 2 * s + h)) = make_uint4(hi[4 * h], hi[4 * h + 1], hi[4 * h + 2], hi[4 * h + 3]);
-          *(uint4*)(to + p.katoms * kAtom + swz(row, 2 * s + h)) =
-              make_uint4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]);
-        }
-      }
+          for (int h = 0; h < 2; ++h) {
+            unsigned char* to = v_mem + swz(row, 2 * (half + 2 * i) + h);
+            *(uint4*)to = make_uint4(hi[i][4 * h], hi[i][4 * h + 1], hi[i][4 * h + 2], hi[i][4 * h + 3]);
+            *(uint4*)(to + p.katoms * kAtom) = make_uint4(lo[i][4 * h], lo[i][4 * h + 1], lo[i][4 * h + 2], lo[i][4 * h + 3]);
+          }
       fence_before_sync();
       fence_proxy_async_smem();
       mbar_arrive(&bars.v_ready);
@@ -278,11 +353,11 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
     // the tile and four lanes a row's 128 bytes, which go out as they are.  Else it holds pairs of columns,
     // which are added in place to base in shared memory, from where the warp writes whole rows.
     const int g = lane >> 2, t = lane & 3, r0 = 32 * quarter;
-    for (int n = 0; ok && n < nblk; ++n) {
-      const int st = n / p.bps, sub = n % p.bps, s = st & 1, buf = n & 1, col = 128 * n + 64 * half;
-      const bool last = sub == p.bps - 1 || n == nblk - 1;
+    for (int b = 0; ok && b < nblk; ++b) {
+      const int st = b / p.bps, sub = b % p.bps, s = st & 1, buf = b & 1, col = 128 * (b0 + b) + 64 * half;
+      const bool last = sub == p.bps - 1 || b == nblk - 1;
       if (sub == 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars.full_n[s], (st >> 1) & 1, abort));
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars.acc_full[buf], (n >> 1) & 1, abort));
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars.acc_full[buf], (b >> 1) & 1, abort));
       if (!ok) break;
       fence_after_sync();
       uint32_t w[2][32];
@@ -306,12 +381,12 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
         for (int i = 0; i < 4; ++i) {
           const int r = r0 + g + 8 * i;
           if (r < tile.rows && col < a.N) {
-            const uint32_t* b = (const uint32_t*)y[i];
+            const uint32_t* yb = (const uint32_t*)y[i];
             uint32_t o[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              o[j] = pack_bf16(lo_f32(b[j]) + __uint_as_float(w[i >> 1][4 * j + 2 * (i & 1)]),
-                               hi_f32(b[j]) + __uint_as_float(w[i >> 1][4 * j + 2 * (i & 1) + 1]));
+              o[j] = pack_bf16(lo_f32(yb[j]) + __uint_as_float(w[i >> 1][4 * j + 2 * (i & 1)]),
+                               hi_f32(yb[j]) + __uint_as_float(w[i >> 1][4 * j + 2 * (i & 1) + 1]));
             st_global_v8(a.out + (int64_t)(tile.t0 + r) * a.ldo + col + 16 * t, o);
           }
         }
@@ -430,8 +505,26 @@ cudaError_t launch_adapter_tiles(const AdapterArgs& g, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     set.store(true, std::memory_order_relaxed);
   }
+  // Blocks of a cluster share a tile, each a part of K, then of N, while the device takes the clusters at once
+  // (half a tile over per request; a tenth of the SMs may not form clusters: 37 tiles by four 38 us, by two 25).
+  const int64_t likely = (int64_t)g.T / kBM + (g.R < g.T ? g.R : g.T) / 2, room = tc_num_sms() * 9 / 10;
+  const int cluster = 4 * likely <= room ? 4 : 2 * likely <= room ? 2 : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * cluster));
+  cfg.blockDim = dim3(32 * kTileWarps);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   note_launches(1);
-  return launch_pdl(adapter_tile_kernel, dim3((unsigned)tiles), dim3(32 * kTileWarps), kSmem, s, p);
+  return cudaLaunchKernelEx(&cfg, adapter_tile_kernel, p);
 }
 
 }  // namespace moe

@@ -379,16 +379,20 @@ def test_adapters(r, H, N):
 
 
 @pytest.mark.parametrize("r", [8, 16, 24, 40, 64, 72, 128])
-@pytest.mark.parametrize("H,N,pad", [(256, 128, 0), (2048, 1536, 16), (1000, 320, 0), (72, 64, 16), (512, 264, 8)])
+@pytest.mark.parametrize("H,N,pad", [(2048, 1536, 16), (1000, 320, 0), (512, 264, 8), (2048, 72, 0)])
 def test_adapters_long_requests(r, H, N, pad):
-    """Sizes whose requests fill whole tiles: every kernel for long requests, ranks and rows that end inside a
-    tile, requests without an adapter among them."""
+    """Sizes whose requests fill whole tiles: every kernel for long requests (T r (H + N) large enough for it, and
+    for a tile shared by four blocks, by two and by none), ranks and rows that end inside a tile, requests
+    without an adapter among them."""
     n = 3
     rank = [r, max(1, r - 5), max(1, r // 2)]
-    small = 200000 // r
-    run_adapters([small - 300, 1, 128, 0, 127, 4096, 600], [0, 1, 2, 0, 1, -1, 2], H, N, n, r, 11, rank=rank, pad=pad)
-    run_adapters([9000, 129], [1, 2], H, N, n, r, 12, rank=rank, pad=pad, in_place=True, scale=False)
-    run_adapters([200, 3000, 5200], [2, 7, 0], H, N, n, r, 13, pad=pad)
+    whole = next(v for v in (16, 32, 64, 128) if r <= v)
+    T = max(9200, int(9e8 / (whole * (H + N))) + 1)
+    run_adapters([T - 5000, 1, 128, 0, 127, 4096, 600], [0, 1, 2, 0, 1, -1, 2], H, N, n, r, 11, rank=rank, pad=pad)
+    run_adapters([T, 129], [1, 2], H, N, n, r, 12, rank=rank, pad=pad, in_place=True, scale=False)
+    run_adapters([200, T - 3000, 17000], [2, 7, 0], H, N, n, r, 13, pad=pad)
+    if whole == 128 and H + N > 2048:  # few enough tiles for four blocks each
+        run_adapters([2600, 500], [0, 1], H, N, n, r, 14, rank=rank, pad=pad)
 
 
 def test_adapters_many_requests_and_edges():
@@ -424,9 +428,9 @@ def test_adapters_nan_stays_in_its_row_and_runs_repeat():
         assert torch.equal(got[keep], want[keep])
         assert torch.isnan(got[77]).all() and not torch.isfinite(got[300]).any()
     # the same in tiles of 128 tokens, where neighbours share one product
-    x, base = rows(4096, 256, torch.bfloat16, g), rows(4096, 256, torch.bfloat16, g)
-    a = torch.randn((2, 64, 256), generator=g, device="cuda").bfloat16()
-    b = torch.randn((2, 256, 64), generator=g, device="cuda").bfloat16()
+    x, base = rows(4096, 1024, torch.bfloat16, g), rows(4096, 1024, torch.bfloat16, g)
+    a = torch.randn((2, 128, 1024), generator=g, device="cuda").bfloat16()
+    b = torch.randn((2, 1024, 128), generator=g, device="cuda").bfloat16()
     starts, slot = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, 1000, 4096], [1, 0]))
     want = M.moe_adapters_add(x, base, a, b, starts, slot)
     assert torch.equal(want, M.moe_adapters_add(x, base, a, b, starts, slot))
@@ -539,7 +543,7 @@ def test_example_runs():
 def test_operators_in_a_graph():
     """Captured once, replayed on new inputs: the same results as direct calls."""
     g = gen(21)
-    T, H, E, r = 4000, 256, 64, 64
+    T, H, E, r = 4000, 1024, 64, 128
     x, b = rows(T, H, torch.float32, g), rows(T, H, torch.bfloat16, g)
     (pre, _), (post, _) = make_norm("rms", H, torch.bfloat16, g), make_norm("layer", H, torch.bfloat16, g)
     lg = rows(T, E, torch.float32, g)
