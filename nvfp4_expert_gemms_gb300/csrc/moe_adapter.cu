@@ -13,8 +13,8 @@
 //
 // v enters the second product as two bf16 terms, hi = bf16(v) and lo = bf16(v - hi): 16 bits of
 // significand, so that an adapter as large as base costs the sum no precision that shows in out's own
-// bf16 rounding.  The extra MMAs are hidden: HBM bytes of x, base and out bound large batches, the
-// reads of A and B (L2) small ones.
+// bf16 rounding.  The extra MMAs are hidden: the register MMAs run at some 597 TFLOP/s here (1.04 ns per
+// m16n8k16 and SM), and what bounds these kernels is memory.
 #include <cooperative_groups.h>
 
 #include "moe_adapter.cuh"
@@ -64,6 +64,12 @@ __device__ __forceinline__ uint2 cut_rank(uint2 b, int k, int rk) {
 // and A are independent and all issued at once), v's parts are summed warp by warp in shared memory and
 // block by block through distributed shared memory, in a fixed order, and the blocks share N.  B and
 // base of a warp's first 32 columns are loaded before the sums meet.
+//
+// One token, 2048 -> 2048 at rank 16: 4.2 us on eight blocks, 6.2 on one (a launch alone takes 1.6): three
+// dependent trips to memory (requests, x and A, then only the sums' way round).  64 requests at rank 32: 6.2 us
+// on four blocks each, 9.2 on one.  4001 tokens of 37 requests at rank 16, 2048 -> 1536: 12.7 us against 6.0 by
+// HBM.  Latency bounds it: 287 blocks are one wave, 20% of the warps, and the L1 is 34% busy, the L2 18%, issue
+// slots 35% (sixteen warps per block in place of eight: 3% slower there, up to 1.7 times at rank 32).
 template <int RT>
 __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kernel(const AdapterArgs a) {
   extern __shared__ __align__(128) unsigned char few_smem[];
@@ -224,39 +230,35 @@ __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kern
   if (rk > 0 && C > 1) cluster.barrier_wait();  // no block leaves while another may still read its sums
 }
 
-// ---- many tokens per request -----------------------------------------------------------------
+// ---- many tokens per request, ranks up to 16 ---------------------------------------------------
 // One tile of 16 WM tokens per block, WM x WK warps: WM along the tokens, WK along K (first product)
 // and N (second).  x and A, then base and B, stream through a ring of NS shared-memory stages filled
 // by cp.async NS - 1 stages ahead, so the bytes in flight do not depend on registers or warps.
-//   K stage  kKC columns of x ([BM][kKC]) and of A ([16 RT][kKC]); row i's 16-byte piece p sits at
+//   K stage  kKC columns of x ([BM][kKC]) and of A ([16][kKC]); row i's 16-byte piece p sits at
 //            piece p ^ 4 (i & 1), so the 8 lanes that one 16-byte shared load serves at a time (two
 //            rows, four pieces) hit all banks once
 //   N stage  kNC columns of base ([BM][kNC], same placement) and kNC rows of B, row order (n-tile, lane
-//            group), pitch an odd multiple of 32 bytes (16 lanes of an 8-byte load: four rows)
+//            group), 32 bytes each (16 lanes of an 8-byte load: four rows, all banks once)
+// Tiles of 32 tokens, four to six blocks per SM: 16384 tokens, 2048 -> 2048 at rank 16 in 40.2 us (30.4 by
+// HBM; tiles of 64 39.6), 100 ragged requests of them 39.8 (tiles of 64 60.3: more empty rows).
 constexpr int kKC = 128, kNC = 128;
 
-template <int RT, int WM, int WK>
 struct Many {
-  static constexpr int BM = 16 * WM, threads = 32 * WM * WK;
-  static constexpr int pitch = 32 * (RT | 1);  // bytes of a row of B
-  static constexpr int xbytes = BM * kKC * 2, abytes = 16 * RT * kKC * 2;
-  static constexpr int ybytes = BM * kNC * 2, bbytes = kNC * pitch;
-  static constexpr int stage = xbytes + abytes > ybytes + bbytes ? xbytes + abytes : ybytes + bbytes;
-  static constexpr int vbytes = WK > 1 ? WM * 2 * RT * 32 * 16 : 0;  // one warp column's sums
-  static constexpr int budget = (BM > 64 ? 220 : 108) * 1024;         // one or two blocks per SM
-  static constexpr int NS = budget / stage > 4 ? 4 : budget / stage;
-  static constexpr int smem = NS * stage > vbytes ? NS * stage : vbytes;
-  static_assert(NS >= 2 && stage % 16 == 0 && vbytes <= stage, "");
+  static constexpr int RT = 1, WM = 2, WK = 2, NS = 4;
+  static constexpr int BM = 16 * WM, threads = 32 * WM * WK, pitch = 32;  // bytes of a row of B
+  static constexpr int xbytes = BM * kKC * 2, ybytes = BM * kNC * 2;
+  static constexpr int stage = xbytes + 16 * kKC * 2;  // of K; an N stage takes as much
+  static constexpr int smem = NS * stage;
+  static_assert(ybytes + kNC * pitch <= stage && WM * 2 * RT * 32 * 16 <= stage, "v's sums meet in one stage");
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
 
-template <int RT, int WM, int WK>
-__global__ void __launch_bounds__(32 * WM * WK) adapter_many_kernel(const AdapterArgs a) {
-  using G = Many<RT, WM, WK>;
-  constexpr int BM = G::BM, NT = G::threads, NS = G::NS;
+__global__ void __launch_bounds__(Many::threads) adapter_many_kernel(const AdapterArgs a) {
+  using G = Many;
+  constexpr int RT = G::RT, WM = G::WM, WK = G::WK, BM = G::BM, NT = G::threads, NS = G::NS;
   extern __shared__ __align__(128) unsigned char ring[];
   pdl_wait();
   pdl_trigger();
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(32 * WM * WK) adapter_many_kernel(const Adapte
     if (s < nst) fill_n(s, (s + 1) % NS);
     commit();
   }
-  if (WK == 2 && rk > 0) {
+  if (rk > 0) {
     float4* sum = (float4*)ring + wm * 2 * RT * 32 + lane;
     if (wk == 1)
 #pragma unroll
@@ -417,14 +419,11 @@ __global__ void __launch_bounds__(32 * WM * WK) adapter_many_kernel(const Adapte
   }
 }
 
-template <int RT, int WM, int WK>
 cudaError_t launch_many(const AdapterArgs& a, cudaStream_t s) {
-  using G = Many<RT, WM, WK>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(adapter_many_kernel<RT, WM, WK>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::smem);
+  const cudaError_t e = cudaFuncSetAttribute(adapter_many_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Many::smem);
   if (e != cudaSuccess) return e;
   note_launches(1);
-  return launch_pdl(adapter_many_kernel<RT, WM, WK>, dim3((unsigned)tile_bound(a, G::BM)), dim3(G::threads), G::smem, s, a);
+  return launch_pdl(adapter_many_kernel, dim3((unsigned)tile_bound(a, Many::BM)), dim3(Many::threads), Many::smem, s, a);
 }
 
 template <int RT>
@@ -454,19 +453,13 @@ cudaError_t launch_few(const AdapterArgs& a, int cluster, cudaStream_t s) {
 
 template <int RT>
 cudaError_t launch_rank(const AdapterArgs& a, cudaStream_t s) {
-#ifdef ADAPTER_PROBE
-  if (g_many == 1) return launch_many<RT, 4, 2>(a, s);
-  if (g_many == 4) return launch_many<RT, 2, 2>(a, s);
-  if (g_many == 5) return launch_adapter_tiles(a, s);
-  return launch_few<RT>(a, g_cluster, s);
-#endif
   const int64_t mean = a.T / (a.R > 0 ? a.R : 1), tiles = tile_bound(a, 16);
   // Long requests.  Ranks up to 16: register MMAs keep up with HBM (16384 tokens, 2048 -> 2048: 40.2 us, the
   // tcgen05 tiles 40.2 even and 59.4 ragged; 4096 tokens: tiles of 32 tokens 22.7 us, the kernel for few 15.4).
   // Higher ranks: the tcgen05 tiles from where the kernel for few, whose time goes by T r (H + N), takes longer
   // than their some 20 us (4096 tokens at rank 64: 22.0 against 28.9 us; at rank 32: 19.4 against 17.2).
   if constexpr (RT == 1)
-    if (a.T >= 8192 && mean >= 32) return launch_many<1, 2, 2>(a, s);
+    if (a.T >= 8192 && mean >= 32) return launch_many(a, s);
   if (RT > 1 && mean >= 128 && (double)a.T * (16 * RT) * (a.H + a.N) >= 8e8 && adapter_tiles_fit(a))
     return launch_adapter_tiles(a, s);
   // blocks of a cluster share a tile as long as the grid fits the device at once

@@ -15,55 +15,11 @@ __device__ __forceinline__ void from_f32(float v, float* p) { *p = v; }
 __device__ __forceinline__ void from_f32(float v, __half* p) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void from_f32(float v, __nv_bfloat16* p) { *p = __float2bfloat16_rn(v); }
 
-// V consecutive elements as they sit in memory: V = 8 in 16-byte pieces (p 16-byte aligned), V = 1
-// one element.
-template <typename E, int V>
-struct __align__(V == 8 ? 16 : sizeof(E)) Pack {
-  E e[V];
-};
-
-template <typename E, int V>
-__device__ __forceinline__ Pack<E, V> load_pack(const E* p) {
-  Pack<E, V> r;
-  if constexpr (V == 8) {
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(E) / 2; ++i) ((uint4*)&r)[i] = ((const uint4*)p)[i];
-  } else {
-    r.e[0] = *p;
-  }
-  return r;
-}
-
-template <typename E, int V>
-__device__ __forceinline__ void store_pack(E* p, const float* v) {
-  Pack<E, V> r;
-#pragma unroll
-  for (int i = 0; i < V; ++i) from_f32(v[i], &r.e[i]);
-  if constexpr (V == 8) {
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(E) / 2; ++i) ((uint4*)p)[i] = ((const uint4*)&r)[i];
-  } else {
-    *p = r.e[0];
-  }
-}
-
-// V elements of a tensor whose type is only known at run time (norm parameters, gates: small next
-// to the rows, so the branch, uniform over the grid, costs nothing that shows).
-template <int V>
-__device__ __forceinline__ void load_any(const void* base, int dt, int64_t at, float* v) {
-  if (dt == MOE_DT_F32) {
-    const Pack<float, V> r = load_pack<float, V>((const float*)base + at);
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = r.e[i];
-  } else if (dt == MOE_DT_F16) {
-    const Pack<__half, V> r = load_pack<__half, V>((const __half*)base + at);
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = to_f32(r.e[i]);
-  } else {
-    const Pack<__nv_bfloat16, V> r = load_pack<__nv_bfloat16, V>((const __nv_bfloat16*)base + at);
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = to_f32(r.e[i]);
-  }
+// One element of a tensor whose type is only known at run time.
+__device__ __forceinline__ float load_any(const void* base, int dt, int64_t at) {
+  if (dt == MOE_DT_F32) return ((const float*)base)[at];
+  if (dt == MOE_DT_F16) return to_f32(((const __half*)base)[at]);
+  return to_f32(((const __nv_bfloat16*)base)[at]);
 }
 
 // One call of the norm / residual kernel.  block == null: enter (y = next(x)); else leave.
