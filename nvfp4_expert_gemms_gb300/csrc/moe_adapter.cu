@@ -62,19 +62,19 @@ __device__ __forceinline__ uint2 cut_rank(uint2 b, int k, int rk) {
 // ---- few tokens per request ------------------------------------------------------------------
 // One tile of up to 16 tokens per cluster of blocks.  The blocks' warps share K (each lane's loads of x
 // and A are independent and all issued at once), v's parts are summed warp by warp in shared memory and
-// block by block through distributed shared memory, in a fixed order, and the blocks share N.  B and
-// base of a warp's first 32 columns are loaded before the sums meet.
+// block by block in a fixed order (each block writes its own into every block's shared memory: one barrier and
+// no remote read to wait for), and the blocks share N.  B and base of a warp's first 32 columns are loaded
+// before the sums meet.
 //
-// One token, 2048 -> 2048 at rank 16: 4.2 us on eight blocks, 6.2 on one (a launch alone takes 1.6): three
-// dependent trips to memory (requests, x and A, then only the sums' way round).  64 requests at rank 32: 6.2 us
-// on four blocks each, 9.2 on one.  4001 tokens of 37 requests at rank 16, 2048 -> 1536: 12.7 us against 6.0 by
-// HBM.  Latency bounds it: 287 blocks are one wave, 20% of the warps, and the L1 is 34% busy, the L2 18%, issue
-// slots 35% (sixteen warps per block in place of eight: 3% slower there, up to 1.7 times at rank 32).
+// One token, 2048 -> 2048 at rank 16: 3.6 us on eight blocks, 6.2 on one (a launch alone takes 1.6); of it 0.7 the
+// requests, 0.8 x and A, 0.9 the sums, 0.4 the second product.  64 requests at rank 32: 6.0 us on four blocks each,
+// 9.2 on one.  4001 tokens of 37 requests at rank 16, 2048 -> 1536: 12.6 us against 6.0 by HBM.  Latency bounds
+// it: 287 blocks are one wave, 20% of the warps, and the L1 is 34% busy, the L2 18%, issue slots 35% (sixteen warps per block in place of eight: 3% slower there, up to 1.7 times at rank 32).
 template <int RT>
 __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kernel(const AdapterArgs a) {
   extern __shared__ __align__(128) unsigned char few_smem[];
   float4(*part)[2 * RT][32] = (float4(*)[2 * RT][32])few_smem;  // [kWarps]
-  float4(*mine)[32] = part[kWarps];
+  float4(*got)[2 * RT][32] = part + kWarps;  // [C]: the blocks' sums
   cg::cluster_group cluster = cg::this_cluster();
   const int C = cluster.num_blocks(), crank = cluster.block_rank();
   pdl_wait();
@@ -118,6 +118,9 @@ __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kern
     }
   };
   if (rk > 0) {
+    // This block runs: its memory may be written.  Relaxed, nothing of its own is handed over yet (the default
+    // orders the accesses before it and holds up the loads below by 0.4 us).
+    if (C > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
     constexpr int U = RT == 1 ? 4 : RT == 2 ? 2 : 1;  // steps whose loads are in flight together
     for (int kb = 32 * part_w; kb < a.H; kb += 32 * parts * U) {
       uint4 p0[U], p1[U], q[U][2 * RT];
@@ -150,6 +153,7 @@ __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kern
     for (int j = 0; j < 2 * RT; ++j)
       if (ok0) part[warp][j][lane] = make_float4(v[j][0], v[j][1], v[j][2], v[j][3]);
     __syncthreads();
+    if (C > 1) asm volatile("barrier.cluster.wait;" ::: "memory");
     for (int e = threadIdx.x; e < 2 * RT * 32; e += 32 * kWarps) {
       const int j = e >> 5, l = e & 31;
       if ((l >> 2) >= tile.rows) continue;
@@ -162,11 +166,17 @@ __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kern
         s.z += o.z;
         s.w += o.w;
       }
-      mine[j][l] = s;
+      if (C == 1) {
+        got[0][j][l] = s;
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (c < C) *cluster.map_shared_rank(&got[crank][j][l], c) = s;
+      }
     }
-    const float4(*all)[32] = mine;
+    const float4(*all)[32] = got[0];
     if (C > 1) {
-      cluster.sync();
+      cluster.sync();  // the only accesses to another block's memory are behind it
       float4(*sum)[32] = part[0];
       for (int e = threadIdx.x; e < 2 * RT * 32; e += 32 * kWarps) {
         const int j = e >> 5, l = e & 31;
@@ -174,7 +184,7 @@ __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kern
         float4 o[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          if (c < C) o[c] = *cluster.map_shared_rank(&mine[j][l], c);
+          if (c < C) o[c] = got[c][j][l];
         float4 s = o[0];
 #pragma unroll
         for (int c = 1; c < 8; ++c)
@@ -187,7 +197,6 @@ __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kern
         sum[j][l] = s;
       }
       all = part[0];
-      cluster.barrier_arrive();  // this block reads no other block's memory from here on
     }
     __syncthreads();
 #pragma unroll
@@ -227,7 +236,6 @@ __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kern
     if (ok1 && col < a.N) *(uint4*)(o1 + col) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
     if (AHEAD) now = next;
   }
-  if (rk > 0 && C > 1) cluster.barrier_wait();  // no block leaves while another may still read its sums
 }
 
 // ---- many tokens per request, ranks up to 16 ---------------------------------------------------
@@ -428,7 +436,7 @@ cudaError_t launch_many(const AdapterArgs& a, cudaStream_t s) {
 
 template <int RT>
 cudaError_t launch_few(const AdapterArgs& a, int cluster, cudaStream_t s) {
-  constexpr int smem = (kWarps + 1) * 2 * RT * 32 * 16;
+  const int smem = (kWarps + cluster) * 2 * RT * 32 * 16;
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(adapter_few_kernel<RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
