@@ -437,7 +437,7 @@ cudaError_t launch_many(const AdapterArgs& a, cudaStream_t s) {
 template <int RT>
 cudaError_t launch_few(const AdapterArgs& a, int cluster, cudaStream_t s) {
   const int smem = (kWarps + cluster) * 2 * RT * 32 * 16;
-  if (smem > 48 * 1024) {
+  if (smem > 32 * 1024) {  // with the static part past the 48 KB that need no opt-in, or near it
     const cudaError_t e = cudaFuncSetAttribute(adapter_few_kernel<RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }

@@ -395,6 +395,22 @@ def test_adapters_long_requests(r, H, N, pad):
         run_adapters([2600, 500], [0, 1], H, N, n, r, 14, rank=rank, pad=pad)
 
 
+def test_adapters_first_call_of_a_process():
+    """Each kernel and cluster size as the first launch of its process: nothing an earlier call has set up (the
+    opt-in to more shared memory) may be needed.  A process per length; every rank class is new to it."""
+    import os
+    import subprocess
+    import sys
+
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = ("import sys; sys.path[:0] = [{!r}, {!r}]; import test_block_ops as t\n"
+            "for r in (8, 24, 40, 128): t.run_adapters([{}], [0], 64, 64, 1, r, 21)")
+    runs = [subprocess.Popen([sys.executable, "-c", code.format(here, os.path.dirname(here), T)], stdout=subprocess.PIPE,
+                             stderr=subprocess.STDOUT, text=True) for T in (16, 464, 944, 1904, 3184)]
+    outs = [p.communicate(timeout=300)[0] for p in runs]
+    assert all(p.returncode == 0 for p in runs), outs
+
+
 def test_adapters_many_requests_and_edges():
     # more requests than one pass of the tile search holds, empty ones among them; slots out of range
     lens = [(i * 7) % 4 for i in range(700)]
