@@ -24,7 +24,7 @@ namespace cg = cooperative_groups;
 namespace moe {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 8;  // of a block of the kernel for few
 
 __device__ __forceinline__ void mma_bf16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -60,7 +60,7 @@ __device__ __forceinline__ uint2 cut_rank(uint2 b, int k, int rk) {
 }
 
 // ---- few tokens per request ------------------------------------------------------------------
-// One tile of up to 16 tokens per cluster of blocks.  The blocks' warps share K (each lane's loads of x
+// One tile of up to 16 MT tokens per cluster of blocks.  The blocks' warps share K (each lane's loads of x
 // and A are independent and all issued at once), v's parts are summed warp by warp in shared memory and
 // block by block in a fixed order (each block writes its own into every block's shared memory: one barrier and
 // no remote read to wait for), and the blocks share N.  B and base of a warp's first 32 columns are loaded
@@ -68,45 +68,60 @@ __device__ __forceinline__ uint2 cut_rank(uint2 b, int k, int rk) {
 //
 // One token, 2048 -> 2048 at rank 16: 3.6 us on eight blocks, 6.2 on one (a launch alone takes 1.6); of it 0.7 the
 // requests, 0.8 x and A, 0.9 the sums, 0.4 the second product.  64 requests at rank 32: 6.0 us on four blocks each,
-// 9.2 on one.  4001 tokens of 37 requests at rank 16, 2048 -> 1536: 12.6 us against 6.0 by HBM.  Latency bounds
-// it: 287 blocks are one wave, 20% of the warps, and the L1 is 34% busy, the L2 18%, issue slots 35% (sixteen warps per block in place of eight: 3% slower there, up to 1.7 times at rank 32).
-template <int RT>
+// 9.2 on one.  4001 tokens of 37 requests at rank 16, 2048 -> 1536: 12.1 us in tiles of 32, two blocks each (12.6 in
+// tiles of 16), against 6.0 by HBM.  Latency bounds it: 324 blocks are one wave, 21% of the warps, and the L1 is
+// 32% busy, the L2 17%, issue slots 38% (sixteen warps per block in place of eight: 3% slower in tiles of 16, up to
+// 1.7 times at rank 32; 2% faster in tiles of 32, but 11% slower past one wave).
+//
+// Tiles of 32 (ranks up to 16) read A and B half as often: they are for batches whose tiles of 16 leave no four
+// blocks to a tile.  2048 -> 2048: 5000 ragged tokens 20.3 us against 24.3, 7000 22.0 against 28.2, 4096 even ones
+// 14.1 against 15.7, 1024 even ones 6.1 against 5.6.  At rank 32 they take 18.4 us against 17.5 at 4096 tokens.
+template <int RT, int MT>
 __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kernel(const AdapterArgs a) {
   extern __shared__ __align__(128) unsigned char few_smem[];
-  float4(*part)[2 * RT][32] = (float4(*)[2 * RT][32])few_smem;  // [kWarps]
-  float4(*got)[2 * RT][32] = part + kWarps;  // [C]: the blocks' sums
+  float4(*part)[2 * RT * MT][32] = (float4(*)[2 * RT * MT][32])few_smem;  // [kWarps]
+  float4(*got)[2 * RT * MT][32] = part + kWarps;  // [C]: the blocks' sums
   cg::cluster_group cluster = cg::this_cluster();
   const int C = cluster.num_blocks(), crank = cluster.block_rank();
   pdl_wait();
   pdl_trigger();
-  const Tile tile = find_tile<kWarps>(a, blockIdx.x / C, 16);
+  const Tile tile = find_tile<kWarps>(a, blockIdx.x / C, 16 * MT);
   if (tile.rows == 0) return;
   const int rk = tile.rk;
   if (rk == 0 && a.out == a.base) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const bool ok0 = g < tile.rows, ok1 = g + 8 < tile.rows;
-  const int64_t t0 = tile.t0 + (ok0 ? g : 0), t1 = tile.t0 + (ok1 ? g + 8 : 0);
+  bool ok[MT][2];
+  int64_t tok[MT][2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      ok[m][h] = 16 * m + 8 * h + g < tile.rows;
+      tok[m][h] = tile.t0 + (ok[m][h] ? 16 * m + 8 * h + g : 0);
+    }
   const uint4 zero = make_uint4(0, 0, 0, 0);
   const int part_w = crank * kWarps + warp, parts = C * kWarps;
-  float v[2 * RT][4];
+  float v[MT][2 * RT][4];
 #pragma unroll
-  for (int j = 0; j < 2 * RT; ++j)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[j][i] = 0.f;
+    for (int j = 0; j < 2 * RT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[m][j][i] = 0.f;
   const __nv_bfloat16* A = a.A + (int64_t)max(tile.slot, 0) * a.r * a.H;
-  const __nv_bfloat16 *x0 = a.x + t0 * a.ldx, *x1 = a.x + t1 * a.ldx;
   const __nv_bfloat16* B = a.B + (int64_t)max(tile.slot, 0) * a.N * a.r;
-  const __nv_bfloat16 *b0 = a.base + t0 * a.ldb, *b1 = a.base + t1 * a.ldb;
-  __nv_bfloat16 *o0 = a.out + t0 * a.ldo, *o1 = a.out + t1 * a.ldo;
   struct Cols {
     uint2 bq[4][RT];
-    uint4 y0, y1;
+    uint4 y[MT][2];
   };
   auto load_cols = [&](Cols& f, int c) {  // B and base of columns c .. c+31
     const int col = c + 8 * t;
-    f.y0 = ok0 && col < a.N ? *(const uint4*)(b0 + col) : zero;
-    f.y1 = ok1 && col < a.N ? *(const uint4*)(b1 + col) : zero;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        f.y[m][h] = ok[m][h] && col < a.N ? *(const uint4*)(a.base + tok[m][h] * a.ldb + col) : zero;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int n = c + 8 * (g >> 1) + 2 * j + (g & 1);
@@ -121,15 +136,18 @@ __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kern
     // This block runs: its memory may be written.  Relaxed, nothing of its own is handed over yet (the default
     // orders the accesses before it and holds up the loads below by 0.4 us).
     if (C > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
-    constexpr int U = RT == 1 ? 4 : RT == 2 ? 2 : 1;  // steps whose loads are in flight together
+    constexpr int U = RT == 1 ? 4 / MT : RT == 2 && MT == 1 ? 2 : 1;  // steps whose loads are in flight together
     for (int kb = 32 * part_w; kb < a.H; kb += 32 * parts * U) {
-      uint4 p0[U], p1[U], q[U][2 * RT];
+      uint4 p[U][MT][2], q[U][2 * RT];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int k = kb + 32 * parts * u + 8 * t;
         const bool in = k < a.H;
-        p0[u] = in && ok0 ? *(const uint4*)(x0 + k) : zero;
-        p1[u] = in && ok1 ? *(const uint4*)(x1 + k) : zero;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            p[u][m][h] = in && ok[m][h] ? *(const uint4*)(a.x + tok[m][h] * a.ldx + k) : zero;
 #pragma unroll
         for (int j = 0; j < 2 * RT; ++j) {
           const int row = 16 * (j >> 1) + 4 * (g >> 1) + 2 * (j & 1) + (g & 1);
@@ -140,23 +158,27 @@ __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kern
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int j = 0; j < 2 * RT; ++j)
-          if (16 * (j >> 1) < rk) {
-            mma_bf16(v[j], p0[u].x, p1[u].x, p0[u].y, p1[u].y, q[u][j].x, q[u][j].y);
-            mma_bf16(v[j], p0[u].z, p1[u].z, p0[u].w, p1[u].w, q[u][j].z, q[u][j].w);
-          }
+          if (16 * (j >> 1) < rk)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              mma_bf16(v[m][j], p[u][m][0].x, p[u][m][1].x, p[u][m][0].y, p[u][m][1].y, q[u][j].x, q[u][j].y);
+              mma_bf16(v[m][j], p[u][m][0].z, p[u][m][1].z, p[u][m][0].w, p[u][m][1].w, q[u][j].z, q[u][j].w);
+            }
     }
   }
   Cols now;
   load_cols(now, 32 * part_w);
   if (rk > 0) {
 #pragma unroll
-    for (int j = 0; j < 2 * RT; ++j)
-      if (ok0) part[warp][j][lane] = make_float4(v[j][0], v[j][1], v[j][2], v[j][3]);
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int j = 0; j < 2 * RT; ++j)
+        if (ok[m][0]) part[warp][2 * RT * m + j][lane] = make_float4(v[m][j][0], v[m][j][1], v[m][j][2], v[m][j][3]);
     __syncthreads();
     if (C > 1) asm volatile("barrier.cluster.wait;" ::: "memory");
-    for (int e = threadIdx.x; e < 2 * RT * 32; e += 32 * kWarps) {
+    for (int e = threadIdx.x; e < 2 * RT * MT * 32; e += 32 * kWarps) {
       const int j = e >> 5, l = e & 31;
-      if ((l >> 2) >= tile.rows) continue;
+      if (16 * (j / (2 * RT)) + (l >> 2) >= tile.rows) continue;
       float4 s = part[0][j][l];
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) {
@@ -178,9 +200,9 @@ __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kern
     if (C > 1) {
       cluster.sync();  // the only accesses to another block's memory are behind it
       float4(*sum)[32] = part[0];
-      for (int e = threadIdx.x; e < 2 * RT * 32; e += 32 * kWarps) {
+      for (int e = threadIdx.x; e < 2 * RT * MT * 32; e += 32 * kWarps) {
         const int j = e >> 5, l = e & 31;
-        if ((l >> 2) >= tile.rows) continue;
+        if (16 * (j / (2 * RT)) + (l >> 2) >= tile.rows) continue;
         float4 o[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c)
@@ -200,40 +222,48 @@ __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kern
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 2 * RT; ++j) {
-      const float4 s = ok0 ? all[j][lane] : make_float4(0.f, 0.f, 0.f, 0.f);
-      v[j][0] = s.x;
-      v[j][1] = s.y;
-      v[j][2] = s.z;
-      v[j][3] = s.w;
-    }
-  }
-  uint32_t hi[RT][4], lo[RT][4];
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-  for (int s = 0; s < RT; ++s) split_v(v[2 * s], v[2 * s + 1], tile.scale, hi[s], lo[s]);
+      for (int j = 0; j < 2 * RT; ++j) {
+        const float4 s = ok[m][0] ? all[2 * RT * m + j][lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[m][j][0] = s.x;
+        v[m][j][1] = s.y;
+        v[m][j][2] = s.z;
+        v[m][j][3] = s.w;
+      }
+  }
+  uint32_t hi[MT][RT][4], lo[MT][RT][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int s = 0; s < RT; ++s) split_v(v[m][2 * s], v[m][2 * s + 1], tile.scale, hi[m][s], lo[m][s]);
   for (int c = 32 * part_w; c < a.N; c += 32 * parts) {
-    constexpr bool AHEAD = RT <= 2;  // the next columns are loaded under these ones (registers allowing)
+    constexpr bool AHEAD = RT * MT <= 2;  // the next columns are loaded under these ones (registers allowing)
     Cols next;
     if (AHEAD && c + 32 * parts < a.N) load_cols(next, c + 32 * parts);
     if (!AHEAD && c != 32 * part_w) load_cols(now, c);
     const int col = c + 8 * t;
-    const uint32_t w0[4] = {now.y0.x, now.y0.y, now.y0.z, now.y0.w}, w1[4] = {now.y1.x, now.y1.y, now.y1.z, now.y1.w};
-    uint32_t q0[4], q1[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float d[4] = {lo_f32(w0[j]), hi_f32(w0[j]), lo_f32(w1[j]), hi_f32(w1[j])};
+    for (int m = 0; m < MT; ++m) {
+      const uint32_t w0[4] = {now.y[m][0].x, now.y[m][0].y, now.y[m][0].z, now.y[m][0].w};
+      const uint32_t w1[4] = {now.y[m][1].x, now.y[m][1].y, now.y[m][1].z, now.y[m][1].w};
+      uint32_t q0[4], q1[4];
 #pragma unroll
-      for (int s = 0; s < RT; ++s)
-        if (16 * s < rk) {
-          const uint2 b = cut_rank(now.bq[j][s], 16 * s + 4 * t, rk);
-          mma_bf16(d, lo[s][0], lo[s][1], lo[s][2], lo[s][3], b.x, b.y);
-          mma_bf16(d, hi[s][0], hi[s][1], hi[s][2], hi[s][3], b.x, b.y);
-        }
-      q0[j] = pack_bf16(d[0], d[1]);
-      q1[j] = pack_bf16(d[2], d[3]);
+      for (int j = 0; j < 4; ++j) {
+        float d[4] = {lo_f32(w0[j]), hi_f32(w0[j]), lo_f32(w1[j]), hi_f32(w1[j])};
+#pragma unroll
+        for (int s = 0; s < RT; ++s)
+          if (16 * s < rk) {
+            const uint2 b = cut_rank(now.bq[j][s], 16 * s + 4 * t, rk);
+            mma_bf16(d, lo[m][s][0], lo[m][s][1], lo[m][s][2], lo[m][s][3], b.x, b.y);
+            mma_bf16(d, hi[m][s][0], hi[m][s][1], hi[m][s][2], hi[m][s][3], b.x, b.y);
+          }
+        q0[j] = pack_bf16(d[0], d[1]);
+        q1[j] = pack_bf16(d[2], d[3]);
+      }
+      if (ok[m][0] && col < a.N) *(uint4*)(a.out + tok[m][0] * a.ldo + col) = make_uint4(q0[0], q0[1], q0[2], q0[3]);
+      if (ok[m][1] && col < a.N) *(uint4*)(a.out + tok[m][1] * a.ldo + col) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
     }
-    if (ok0 && col < a.N) *(uint4*)(o0 + col) = make_uint4(q0[0], q0[1], q0[2], q0[3]);
-    if (ok1 && col < a.N) *(uint4*)(o1 + col) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
     if (AHEAD) now = next;
   }
 }
@@ -434,15 +464,15 @@ cudaError_t launch_many(const AdapterArgs& a, cudaStream_t s) {
   return launch_pdl(adapter_many_kernel, dim3((unsigned)tile_bound(a, Many::BM)), dim3(Many::threads), Many::smem, s, a);
 }
 
-template <int RT>
+template <int RT, int MT>
 cudaError_t launch_few(const AdapterArgs& a, int cluster, cudaStream_t s) {
-  const int smem = (kWarps + cluster) * 2 * RT * 32 * 16;
+  const int smem = (kWarps + cluster) * 2 * RT * MT * 32 * 16;
   if (smem > 32 * 1024) {  // with the static part past the 48 KB that need no opt-in, or near it
-    const cudaError_t e = cudaFuncSetAttribute(adapter_few_kernel<RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(adapter_few_kernel<RT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tile_bound(a, 16) * cluster));
+  cfg.gridDim = dim3((unsigned)(tile_bound(a, 16 * MT) * cluster));
   cfg.blockDim = dim3(32 * kWarps);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -456,23 +486,30 @@ cudaError_t launch_few(const AdapterArgs& a, int cluster, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   note_launches(1);
-  return cudaLaunchKernelEx(&cfg, adapter_few_kernel<RT>, a);
+  return cudaLaunchKernelEx(&cfg, adapter_few_kernel<RT, MT>, a);
 }
 
 template <int RT>
 cudaError_t launch_rank(const AdapterArgs& a, cudaStream_t s) {
-  const int64_t mean = a.T / (a.R > 0 ? a.R : 1), tiles = tile_bound(a, 16);
-  // Long requests.  Ranks up to 16: register MMAs keep up with HBM (16384 tokens, 2048 -> 2048: 40.2 us, the
-  // tcgen05 tiles 40.2 even and 59.4 ragged; 4096 tokens: tiles of 32 tokens 22.7 us, the kernel for few 15.4).
-  // Higher ranks: the tcgen05 tiles from where the kernel for few, whose time goes by T r (H + N), takes longer
-  // than their some 20 us (4096 tokens at rank 64: 22.0 against 28.9 us; at rank 32: 19.4 against 17.2).
-  if constexpr (RT == 1)
-    if (a.T >= 8192 && mean >= 32) return launch_many(a, s);
-  if (RT > 1 && mean >= 128 && (double)a.T * (16 * RT) * (a.H + a.N) >= 8e8 && adapter_tiles_fit(a))
-    return launch_adapter_tiles(a, s);
+  const int64_t requests = a.R < a.T ? a.R : a.T, mean = a.T / requests;
+  const int64_t room = (int64_t)tc_num_sms() * (RT <= 4 ? 2 : 1);  // blocks that the device takes at once
+  // Tiles, with requests of mean > the tile's height half a tile over each.
+  const int64_t likely16 = a.T / 16 + requests / 2, likely32 = a.T / 32 + requests / 2;
   // blocks of a cluster share a tile as long as the grid fits the device at once
-  const int64_t room = (int64_t)tc_num_sms() * (RT <= 4 ? 2 : 1);
-  return launch_few<RT>(a, 8 * tiles <= room ? 8 : 4 * tiles <= room ? 4 : 2 * tiles <= room ? 2 : 1, s);
+  const auto blocks = [&](int64_t tiles) { return 8 * tiles <= room ? 8 : 4 * tiles <= room ? 4 : 2 * tiles <= room ? 2 : 1; };
+  if constexpr (RT == 1) {
+    // Long requests past one wave of tiles of 32: 16384 tokens, 2048 -> 2048, the ring 40.2 us, those tiles 44.1
+    // (tcgen05 tiles 40.2, 59.4 ragged); 10000 ragged 34.8 and 38.4; 7000, within a wave, 26.6 and 22.0.
+    if (mean >= 32 && likely32 > room) return launch_many(a, s);
+    if (mean > 16 && 4 * likely16 > room) return launch_few<1, 2>(a, blocks(likely32), s);
+  } else {
+    // The tcgen05 tiles from where the kernel for few, whose time goes by T r (H + N) and by waves of tiles, takes
+    // longer than their some 20 us: 4096 tokens, 2048 -> 2048 at rank 64 22.0 against 28.9 us, at rank 32 19.5 against
+    // 17.5, 6000 ragged at rank 32 25.2 against 30.1, 16384 of 512 -> 512 at rank 32 15.4 against 20.7.
+    const double work = (double)a.T * (16 * RT) * (a.H + a.N);
+    if (mean >= 128 && work >= (likely16 > room ? 5e8 : 8e8) && adapter_tiles_fit(a)) return launch_adapter_tiles(a, s);
+  }
+  return launch_few<RT, 1>(a, blocks(tile_bound(a, 16)), s);
 }
 
 }  // namespace

@@ -395,6 +395,19 @@ def test_adapters_long_requests(r, H, N, pad):
         run_adapters([2600, 500], [0, 1], H, N, n, r, 14, rank=rank, pad=pad)
 
 
+@pytest.mark.parametrize("r", [8, 16])
+@pytest.mark.parametrize("H,N,pad", [(2048, 1536, 16), (1000, 320, 0), (40, 264, 8)])
+def test_adapters_tiles_of_32(r, H, N, pad):
+    """Low ranks whose requests fill tiles of 32: shared by eight blocks, four, two and none, tiles of one to 32
+    rows, requests without tokens or without an adapter."""
+    rank = [r, max(1, r - 5), max(1, r // 2)]
+    run_adapters([1232], [1], H, N, 3, r, 31, rank=rank, pad=pad)
+    run_adapters([700, 33, 0, 1265], [0, 2, 1, -1], H, N, 3, r, 32, rank=rank, pad=pad, in_place=True)
+    run_adapters([1, 3000, 40, 8, 959, 24, 17], [0, 1, 2, 0, 1, -1, 2], H, N, 3, r, 33, rank=rank, pad=pad, scale=False)
+    run_adapters([31, 32, 33, 16, 15, 5000, 1007, 481], [2, 0, 1, 2, 0, 1, 7, 0], H, N, 3, r, 34, pad=pad)
+    run_adapters([17 + (7 * i) % 13 for i in range(120)], [i % 4 - 1 for i in range(120)], H, N, 3, r, 35, rank=rank, pad=pad)
+
+
 def test_adapters_first_call_of_a_process():
     """Each kernel and cluster size as the first launch of its process: nothing an earlier call has set up (the
     opt-in to more shared memory) may be needed.  A process per length; every rank class is new to it."""
