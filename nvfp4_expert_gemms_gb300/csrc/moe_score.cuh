@@ -11,8 +11,8 @@
 // bias, a score is expf and one correctly rounded reciprocal, and a softmax's common denominator is
 // left out of comparisons where it can be.
 //
-// Bound: instructions (some 660 per token at 256 experts, sigmoid, bias, 8 groups; 70% of issue slots): 16384
-// tokens 12.6 us, 2.7 by HBM.  By k rounds over all keys, every score exact, it took 22.5.
+// Bound: instructions (some 640 per token at 256 experts, sigmoid, bias, 8 groups; 70% of issue slots): 16384
+// tokens 12.4 us, 2.7 by HBM.  By k rounds over all keys, every score exact, it took 22.5.
 #pragma once
 #include "moe_block.cuh"
 
@@ -46,6 +46,13 @@ __device__ __forceinline__ float redux_max(float v) {
 
 // 1 / (1 + e^-l), each step rounded once.
 __device__ __forceinline__ float sigmoid_rn(float l) { return __frcp_rn(__fadd_rn(1.f, expf(-l))); }
+// The same to within 3e-7 (see score_token), in five instructions: what is subnormal on the way counts as zero.
+__device__ __forceinline__ float sigmoid_fast(float l) {
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.44269504f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  return s;
+}
 // e^(l - m); 0 for an empty row (m = -inf)
 __device__ __forceinline__ float exp_rn(float l, float m) { return m == -INFINITY ? 0.f : expf(__fsub_rn(l, m)); }
 
@@ -161,8 +168,8 @@ __device__ __forceinline__ bool pick_top(const float (&key)[VT], const float (&l
   }
   bound = fmaxf(bound, -INFINITY);  // NaN, fewer than k lanes with candidates: every candidate
   if (slack) {
-    if (isinf(bound)) return false;
-    bound -= 2.f * key_slack(bound);
+    if (bound == INFINITY) return false;
+    bound -= 2.f * key_slack(bound);  // -infinity stays
   }
   uint32_t mask = 0;
   if (!isnan(top)) {
@@ -270,10 +277,11 @@ __device__ __forceinline__ int score_token(const ScoreArgs& a, const ScoreGeom& 
   float sv = 0.f, b2 = -INFINITY;
   bool done = false;
   if constexpr (VT >= 4) {
-    // Sigmoid keys with a bias: the fast exponential and division place every key to within key_slack
-    // (__expf: 2 + 1.173 |l| units, less than 1e-7 of the score after its slope; the division 2 units;
-    // the sum's rounding), which leaves few experts that could be chosen, and only those get their exact
-    // key.  Where groups or keys stand closer than that, everything is done exactly below.
+    // Sigmoid keys with a bias: the fast exponential and reciprocal place every key to within key_slack
+    // (the power of two 2^-22 and 2^-23 |l|, the rounded product with its constant, relative, which the sigmoid's
+    // slope s (1 - s) <= 1/4, |l| s (1 - s) < 0.23, makes less than 1e-7 of the score; the sum and the reciprocal
+    // 2^-24 and 2^-23; the key's own rounding), which leaves few experts that could be chosen, and only those get
+    // their exact key.  Where groups or keys stand closer than that, everything is done exactly below.
     if (biased && !softmax) {
       float est[VT];
       if (g.full) {
@@ -286,13 +294,13 @@ __device__ __forceinline__ int score_token(const ScoreArgs& a, const ScoreGeom& 
           est[4 * i + 3] = q.w;
         }
 #pragma unroll
-        for (int i = 0; i < VT; ++i) est[i] = fmaxf(__fdividef(1.f, 1.f + __expf(-l[i])) + est[i], -INFINITY);
+        for (int i = 0; i < VT; ++i) est[i] = fmaxf(sigmoid_fast(l[i]) + est[i], -INFINITY);
       } else {
 #pragma unroll
         for (int i = 0; i < VT; ++i) est[i] = i < cnt ? a.bias[e0 + i] : 0.f;
 #pragma unroll
         for (int i = 0; i < VT; ++i)
-          est[i] = i < cnt ? fmaxf(__fdividef(1.f, 1.f + __expf(-l[i])) + est[i], -INFINITY) : kNoKey;
+          est[i] = i < cnt ? fmaxf(sigmoid_fast(l[i]) + est[i], -INFINITY) : kNoKey;
       }
       float top = g.full ? lane_top<true, VT>(est, cnt, two, b2) : lane_top<false, VT>(est, cnt, two, b2);
       bool clear = true;

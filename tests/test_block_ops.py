@@ -330,6 +330,28 @@ def test_route_ties_and_masked_experts():
 
 
 # ------------------------------------------------------------------------------------------ adapters
+@pytest.mark.parametrize("E,groups,tg", [(256, 8, 1), (256, 16, 2), (128, 8, 1), (240, 8, 1), (256, 8, 2)])
+def test_route_few_groups(E, groups, tg):
+    """Candidates in fewer lanes than are chosen, with a bias: keys apart by construction, experts that the bias or
+    the logits rule out (the bias's have equal keys: the lower index goes first)."""
+    S, k, inf = E // groups, 8, float("inf")
+    g = gen(E + groups)
+    bias = 0.0103 * torch.randperm(E, generator=g, device="cuda").float()
+    lg = torch.zeros((6, E), device="cuda")
+    lg[1] = -inf
+    lg[2, ::2] = -inf
+    lg[3] = inf
+    lg[4, ::3] = float("nan")
+    lg[5, : E // 2] = 40.0
+    for only in (None, 0, groups - 1):  # a group that wins with three experts left
+        b = bias.clone()
+        if only is not None:
+            b[only * S: only * S + 3] += 9.0
+            b[only * S + 3: (only + 1) * S] = -inf
+        for gt in (1, 2):
+            check_route(lg, k, "sigmoid", bias=b, groups=groups, top_groups=tg, group_top=gt, gaps=False)
+
+
 def ref_adapters(x, base, a, b, starts, slot, scale, rank):
     """base + scale B (A x) in fp64 and the bound of the error before the last rounding."""
     x, a, b, out = x.double(), a.double(), b.double(), base.double()
