@@ -611,18 +611,173 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) block_narrow_kernel(con
   }
 }
 
+// Rows that allow eight columns per access, too long for the kernels above: a row per block, its values kept as
+// fp32 in shared memory (columns 8 p .. 8 p + 3 at [p], the next four at [H / 8 + p]: neighbours on neighbouring
+// banks), so x and block are still read once.  A thread visits the same columns every time, so nothing but the
+// sums needs a barrier, and out may be x and y may be block.  Two blocks per SM up to 28000 columns, so that one's
+// loads run under the other's sums; one up to 57856.
+//
+// Both norms, a gate per channel, 4096 rows of bf16: 12288 columns 89.8 us (60.2 by HBM; the kernel below 448),
+// 16384 110 us (80.3; 588), 32768, with one block, 316 us (160.5).  One row of 16384 6.3 us (28.5).
+constexpr int kSharedThreads = 512, kSharedMost = 226 * 1024;
+
+template <typename X, typename A, typename P, bool LEAVE>
+__global__ void __launch_bounds__(kSharedThreads, 2) block_shared_kernel(const BlockArgs a) {
+  extern __shared__ __align__(16) float4 row[];
+  __shared__ __align__(16) float red[2][32];
+  constexpr int U = 2;  // pieces whose loads are in flight together, beside those of the block's other warps
+  const int H = a.H, pieces = H / 8;
+  const int64_t t = blockIdx.x;
+  const P *pb = (const P*)a.post.bias, *nb = (const P*)a.next.bias, *gate = (const P*)a.gate;
+  const bool full_gate = LEAVE && gate && a.gate_step && a.gate_ld, token_gate = LEAVE && gate && !a.gate_step;
+  const bool channel_gate = LEAVE && gate && a.gate_step && !a.gate_ld;
+  pdl_wait();
+  pdl_trigger();
+  const X* x = (const X*)a.x + t * a.ldx;
+  float gt = 1.f;
+  if (token_gate) gt = to_f32(gate[t * a.gate_ld]);
+  RowSum sum(red, kSharedThreads / 32);
+  const float inv = 1.f / (float)H;
+  auto get = [&](int p, F2 (&v)[4]) {
+    const float4 q = row[p], r = row[pieces + p];
+    v[0] = F2{q.x, q.y};
+    v[1] = F2{q.z, q.w};
+    v[2] = F2{r.x, r.y};
+    v[3] = F2{r.z, r.w};
+  };
+  auto put = [&](int p, const F2 (&v)[4]) {
+    row[p] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    row[pieces + p] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+  };
+  // A norm's sums over the row: `part` holds what the pass that wrote the row added up, of the values (LAYER) or
+  // of their squares.  Returns -mean (0 without one) and 1 / sqrt(mean square + eps).
+  F2 part[4];
+  auto clear = [&] {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) part[j] = dup(0.f);
+  };
+  auto add = [&](const moe_norm_t& n, const F2 (&v)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) part[j] = n.kind == MOE_NORM_LAYER ? add2(part[j], v[j]) : fma2(v[j], v[j], part[j]);
+  };
+  auto total = [&] {
+    const F2 all = add2(add2(part[0], part[1]), add2(part[2], part[3]));
+    return sum(all.x + all.y) * inv;
+  };
+  auto stats = [&](const moe_norm_t& n, float& minus_mean) {
+    minus_mean = 0.f;
+    float q = total();
+    if (n.kind == MOE_NORM_LAYER) {
+      minus_mean = -q;
+      clear();
+      for (int p = threadIdx.x; p < pieces; p += kSharedThreads) {
+        F2 v[4];
+        get(p, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const F2 d = add2(v[j], dup(minus_mean));
+          part[j] = fma2(d, d, part[j]);
+        }
+      }
+      q = total();
+    }
+    return rsqrtf(q + n.eps);
+  };
+  float minus_mean = 0.f, rstd = 1.f;
+  if constexpr (LEAVE) {
+    if (token_gate) gt = gate_value(gt, a.gate_act);
+    const A* b = (const A*)a.block + t * a.ldb;
+    clear();
+    for (int p0 = threadIdx.x; p0 < pieces; p0 += 2 * U * kSharedThreads) {
+      uint4 q[2 * U][kPieces<A>];
+#pragma unroll
+      for (int u = 0; u < 2 * U; ++u)
+        if (p0 + u * kSharedThreads < pieces) load_pieces(b + 8 * (p0 + u * kSharedThreads), q[u]);
+#pragma unroll
+      for (int u = 0; u < 2 * U; ++u) {
+        const int p = p0 + u * kSharedThreads;
+        if (p < pieces) {  // x is wanted after the sums
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(x + 8 * p));
+          F2 v[4];
+          widen8<A>(q[u], v);
+          put(p, v);
+          add(a.post, v);
+        }
+      }
+    }
+    if (a.post.kind) rstd = stats(a.post, minus_mean);
+  }
+  clear();
+  for (int p0 = threadIdx.x; p0 < pieces; p0 += U * kSharedThreads) {
+    uint4 q[U][kPieces<X>];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (p0 + u * kSharedThreads < pieces) load_pieces(x + 8 * (p0 + u * kSharedThreads), q[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int p = p0 + u * kSharedThreads;
+      if (p >= pieces) continue;
+      F2 v[4];
+      if constexpr (LEAVE) {
+        F2 xs[4], f[4];
+        widen8<X>(q[u], xs);
+        get(p, v);
+        post_factor<P>(a, channel_gate, 8 * p, f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = mul2(add2(v[j], dup(minus_mean)), f[j]);
+        if (!pb && !full_gate) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = fma2(v[j], dup(rstd * gt), mul2(dup(a.alpha), xs[j]));
+        } else {
+          F2 g[4];
+          if (full_gate) load8(gate + t * a.gate_ld + 8 * p, g);
+          leave_general<P>(a, channel_gate, pb, full_gate, g, 8 * p, rstd, gt, xs, v);
+        }
+        store8((X*)a.out + t * a.ldo + 8 * p, v);
+      } else {
+        widen8<X>(q[u], v);
+      }
+      put(p, v);
+      add(a.next, v);
+    }
+  }
+  if (a.next.kind) {
+    rstd = stats(a.next, minus_mean);
+    A* y = (A*)a.y + t * a.ldy;
+    for (int p = threadIdx.x; p < pieces; p += kSharedThreads) {
+      F2 v[4], f[4];
+      get(p, v);
+      next_factor<P>(a, 8 * p, f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = mul2(mul2(add2(v[j], dup(minus_mean)), dup(rstd)), f[j]);
+      if (nb) {
+        F2 u[4];
+        load8(nb + 8 * p, u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = add2(v[j], u[j]);
+      }
+      store8(y + 8 * p, v);
+    }
+  }
+}
+
 __device__ __forceinline__ void apply_norm(float* v, const moe_norm_t& n, int c, float mean, float rstd) {
   *v = (*v - mean) * rstd;
   if (n.weight) *v *= load_any(n.weight, n.dtype, c) + n.weight_offset;
   if (n.bias) *v += load_any(n.bias, n.dtype, c);
 }
 
-// Rows too long for one block's registers, and calls whose parameters differ in type: the row's values are computed again from x and block (by
-// now in L2) for each of its sums.  A thread visits the same columns every time and writes out and y
-// only in the last visit, so out may be x and y may be block.
+// Long rows that allow no eight columns per access, and calls whose parameters differ in type: one element at a
+// time.  `keep`: the row's values stay in shared memory as fp32 between its sums; longer rows are computed again
+// from x and block (by then in L2) each time.  A thread visits the same columns every time and writes out and y
+// only in the last visit, so out may be x and y may be block.  Bound: instructions (types looked up per element).
+// 4096 x 16385 bf16, both norms, a gate per channel: 433 us (80.3 by HBM; computed again 597; four elements in
+// flight but one block per SM 628).
 template <typename X, typename A, bool LEAVE>
-__global__ void __launch_bounds__(1024) block_long_kernel(const BlockArgs a) {
+__global__ void __launch_bounds__(1024, 2) block_long_kernel(const BlockArgs a, const bool keep) {
+  extern __shared__ __align__(16) float4 row[];
   __shared__ __align__(16) float red[2][32];
+  float* kept = (float*)row;
   const int64_t t = blockIdx.x;
   pdl_wait();
   pdl_trigger();
@@ -632,23 +787,36 @@ __global__ void __launch_bounds__(1024) block_long_kernel(const BlockArgs a) {
   const X* x = (const X*)a.x + t * a.ldx;
   const A* b = LEAVE ? (const A*)a.block + t * a.ldb : nullptr;
   float pm = 0.f, pr = 1.f, gt = 1.f;
+  // The mean of f(c) over the row's columns.
+  auto over = [&](auto f) {
+    float s = 0.f;
+#pragma unroll 2
+    for (int c = threadIdx.x; c < H; c += 1024) s += f(c);
+    return sum(s) * inv;
+  };
+  auto square = [](float v) { return v * v; };
+  auto first = [&](int c, float v) {  // the first of a value's visits
+    if (keep) kept[c] = v;
+    return v;
+  };
   if constexpr (LEAVE) {
     if (a.post.kind) {
-      float s = 0.f;
+      auto again = [&](int c) { return keep ? kept[c] : to_f32(b[c]); };
+      float q;
       if (a.post.kind == MOE_NORM_LAYER) {
-        for (int c = threadIdx.x; c < H; c += blockDim.x) s += to_f32(b[c]);
-        pm = sum(s) * inv;
+        pm = over([&](int c) { return first(c, to_f32(b[c])); });
+        q = over([&](int c) { return square(again(c) - pm); });
+      } else {
+        q = over([&](int c) { return square(first(c, to_f32(b[c]))); });
       }
-      s = 0.f;
-      for (int c = threadIdx.x; c < H; c += blockDim.x) s += (to_f32(b[c]) - pm) * (to_f32(b[c]) - pm);
-      pr = rsqrtf(sum(s) * inv + a.post.eps);
+      pr = rsqrtf(q + a.post.eps);
     }
     if (a.gate && a.gate_step == 0) gt = gate_value(load_any(a.gate, a.gate_dtype, t * a.gate_ld), a.gate_act);
     gt *= a.beta;
   }
   auto value = [&](int c) {
     if constexpr (LEAVE) {
-      float v = to_f32(b[c]);
+      float v = keep && a.post.kind ? kept[c] : to_f32(b[c]);
       if (a.post.kind) apply_norm(&v, a.post, c, pm, pr);
       if (a.gate && a.gate_step) v *= gate_value(load_any(a.gate, a.gate_dtype, t * a.gate_ld + c), a.gate_act);
       return a.alpha * to_f32(x[c]) + gt * v;
@@ -656,22 +824,21 @@ __global__ void __launch_bounds__(1024) block_long_kernel(const BlockArgs a) {
       return to_f32(x[c]);
     }
   };
+  auto again = [&](int c) { return keep && a.next.kind ? kept[c] : value(c); };
   float mean = 0.f, rstd = 1.f;
   if (a.next.kind) {
-    float s = 0.f;
+    float q;
     if (a.next.kind == MOE_NORM_LAYER) {
-      for (int c = threadIdx.x; c < H; c += blockDim.x) s += value(c);
-      mean = sum(s) * inv;
+      mean = over([&](int c) { return first(c, value(c)); });
+      q = over([&](int c) { return square(again(c) - mean); });
+    } else {
+      q = over([&](int c) { return square(first(c, value(c))); });
     }
-    s = 0.f;
-    for (int c = threadIdx.x; c < H; c += blockDim.x) {
-      const float d = value(c) - mean;
-      s += d * d;
-    }
-    rstd = rsqrtf(sum(s) * inv + a.next.eps);
+    rstd = rsqrtf(q + a.next.eps);
   }
-  for (int c = threadIdx.x; c < H; c += blockDim.x) {
-    float v = value(c);
+#pragma unroll 2
+  for (int c = threadIdx.x; c < H; c += 1024) {
+    float v = again(c);
     if constexpr (LEAVE) from_f32(v, (X*)a.out + t * a.ldo + c);
     if (a.next.kind) {
       apply_norm(&v, a.next, c, mean, rstd);
@@ -685,6 +852,33 @@ cudaError_t launch_row(const BlockArgs& a, cudaStream_t s) {
   return launch_pdl(block_row_kernel<X, A, P, LEAVE>, dim3(a.T), dim3((a.H / 8 + 31) / 32 * 32), 0, s, a);
 }
 
+template <typename X, typename A, bool LEAVE>
+cudaError_t launch_long(const BlockArgs& a, cudaStream_t s) {
+  static std::atomic<bool> set{false};
+  const auto kernel = block_long_kernel<X, A, LEAVE>;
+  if (!set.load(std::memory_order_relaxed)) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedMost);
+    if (e != cudaSuccess) return e;
+    set.store(true, std::memory_order_relaxed);
+  }
+  const bool keep = a.H <= kSharedMost / 4;
+  return launch_pdl(kernel, dim3(a.T), dim3(1024), keep ? a.H * 4 : 0, s, a, keep);
+}
+
+// Rows of whole pieces, of any length.
+template <typename X, typename A, typename P, bool LEAVE>
+cudaError_t launch_shared(const BlockArgs& a, cudaStream_t s) {
+  if (a.H > kSharedMost / 4) return launch_long<X, A, LEAVE>(a, s);
+  static std::atomic<bool> set{false};
+  const auto kernel = block_shared_kernel<X, A, P, LEAVE>;
+  if (!set.load(std::memory_order_relaxed)) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedMost);
+    if (e != cudaSuccess) return e;
+    set.store(true, std::memory_order_relaxed);
+  }
+  return launch_pdl(kernel, dim3(a.T), dim3(kSharedThreads), a.H * 4, s, a);
+}
+
 template <typename X, typename A, typename P, int W, int N, bool LEAVE>
 cudaError_t launch_stream(const BlockArgs& a, cudaStream_t s) {
   const bool full_gate = LEAVE && a.gate && a.gate_step && a.gate_ld;
@@ -692,7 +886,7 @@ cudaError_t launch_stream(const BlockArgs& a, cudaStream_t s) {
   const int factors = (LEAVE ? 4 : 2) * 512 * W * N;
   constexpr int most_groups = kStreamThreads<N> / (32 * W), most_smem = kStreamSmem<W, N>;
   const int fits = (most_smem - factors) / (2 * slot), groups = fits < most_groups ? fits : most_groups;
-  if (groups < 1) return launch_pdl(block_long_kernel<X, A, LEAVE>, dim3(a.T), dim3(1024), 0, s, a);
+  if (groups < 1) return launch_shared<X, A, P, LEAVE>(a, s);
   const int smem = factors + groups * 2 * slot;
   const auto kernel = block_stream_kernel<X, A, P, W, N, LEAVE>;
   static std::atomic<int> fit[2];  // resident blocks per SM of this kernel
@@ -725,6 +919,7 @@ cudaError_t launch_typed(const BlockArgs& a, bool wide, cudaStream_t s) {
       if (a.H <= 2048) return launch_stream<X, A, P, 2, 4, LEAVE>(a, s);
       if (a.H <= 4096) return launch_stream<X, A, P, 4, 4, LEAVE>(a, s);
       if (a.H <= 8192) return launch_stream<X, A, P, 8, 4, LEAVE>(a, s);
+      return launch_shared<X, A, P, LEAVE>(a, s);
     } else {
       return launch_row<X, A, P, LEAVE>(a, s);
     }
@@ -735,7 +930,7 @@ cudaError_t launch_typed(const BlockArgs& a, bool wide, cudaStream_t s) {
     if (a.H <= 4096) return launch_narrow<X, A, P, 512, 8, LEAVE>(a, s);
     if (a.H <= 8192) return launch_narrow<X, A, P, 1024, 8, LEAVE>(a, s);
   }
-  return launch_pdl(block_long_kernel<X, A, LEAVE>, dim3(a.T), dim3(1024), 0, s, a);
+  return launch_long<X, A, LEAVE>(a, s);
 }
 
 // The one type of the call's parameters and gate (0: they differ) picks the kernel.
@@ -744,7 +939,7 @@ cudaError_t launch_params(const BlockArgs& a, int act_dtype, int param_dtype, bo
   if (param_dtype == act_dtype) return launch_typed<X, A, A, LEAVE>(a, wide, s);
   if constexpr (sizeof(A) < 4)
     if (param_dtype == MOE_DT_F32) return launch_typed<X, A, float, LEAVE>(a, wide, s);
-  return launch_pdl(block_long_kernel<X, A, LEAVE>, dim3(a.T), dim3(1024), 0, s, a);
+  return launch_long<X, A, LEAVE>(a, s);
 }
 
 }  // namespace

@@ -124,6 +124,31 @@ def test_leave(types, gate, T, H):
             check(y, ry, ey, f"y {kind} {types} {gate} {act} {T}x{H}")
 
 
+@pytest.mark.parametrize("H", [8200, 16384, 20001, 28928, 57856, 57864])
+def test_long_rows(H):
+    """Rows kept in shared memory, to the last column that fits and past it; in place."""
+    for types, gate in (("bf16/bf16", "channel"), ("f16/f16", "full"), ("f32/f32", "token"), ("f32/bf16", "full"), ("f32/f16", "none")):
+        test_enter(types, 2, H)
+        test_leave(types, gate, 2, H)
+    g = gen(H)
+    for kind in ("rms", "layer"):
+        x, b = rows(3, H, torch.float32, g, 16), rows(3, H, torch.bfloat16, g, 16)
+        (p, _), (n, _) = make_norm(kind, H, torch.bfloat16, g), make_norm(kind, H, torch.bfloat16, g)
+        out, y = M.moe_block_leave(x, b, post=p, next=n, beta=0.5)
+        x2, b2 = x.clone(), b.clone()
+        M.moe_block_leave(x2, b2, post=p, next=n, beta=0.5, out=x2, y=b2)
+        assert torch.equal(x2, out) and torch.equal(b2, y)
+        # parameters of two types
+        (q, sq), (r, sr) = make_norm(kind, H, torch.float32, g), make_norm(kind, H, torch.bfloat16, g)
+        got, y = M.moe_block_leave(x, b, post=q, next=r)
+        v, e = ref_norm(b.double(), torch.zeros_like(b, dtype=torch.float64), *sq)
+        o = x.double() + v
+        e = e + 4 * U * (x.double().abs() + v.abs())
+        check(got, o, e, f"out {kind} {H}")
+        ry, ey = ref_norm(o, e, *sr)
+        check(y, ry, ey, f"y {kind} {H}")
+
+
 def test_leave_in_place_and_other_stream():
     g = gen(3)
     for T, H in ((6, 2048), (4, 1001), (1, 70000)):
