@@ -17,6 +17,8 @@
 // m16n8k16 and SM), and what bounds these kernels is memory.
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "moe_adapter.cuh"
 
 namespace cg = cooperative_groups;
@@ -60,7 +62,7 @@ __device__ __forceinline__ uint2 cut_rank(uint2 b, int k, int rk) {
 }
 
 // ---- few tokens per request ------------------------------------------------------------------
-// One tile of up to 16 MT tokens per cluster of blocks.  The blocks' warps share K (each lane's loads of x
+// One tile of up to 16 MT tokens of a request, or (GATHER) 16 of an adapter's, per cluster of blocks.  The blocks' warps share K (each lane's loads of x
 // and A are independent and all issued at once), v's parts are summed warp by warp in shared memory and
 // block by block in a fixed order (each block writes its own into every block's shared memory: one barrier and
 // no remote read to wait for), and the blocks share N.  B and base of a warp's first 32 columns are loaded
@@ -76,7 +78,7 @@ __device__ __forceinline__ uint2 cut_rank(uint2 b, int k, int rk) {
 // Tiles of 32 (ranks up to 16) read A and B half as often: they are for batches whose tiles of 16 leave no four
 // blocks to a tile.  2048 -> 2048: 5000 ragged tokens 20.3 us against 24.3, 7000 22.0 against 28.2, 4096 even ones
 // 14.1 against 15.7, 1024 even ones 6.1 against 5.6.  At rank 32 they take 18.4 us against 17.5 at 4096 tokens.
-template <int RT, int MT>
+template <int RT, int MT, bool GATHER>
 __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kernel(const AdapterArgs a) {
   extern __shared__ __align__(128) unsigned char few_smem[];
   float4(*part)[2 * RT * MT][32] = (float4(*)[2 * RT * MT][32])few_smem;  // [kWarps]
@@ -85,7 +87,11 @@ __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kern
   const int C = cluster.num_blocks(), crank = cluster.block_rank();
   pdl_wait();
   pdl_trigger();
-  const Tile tile = find_tile<kWarps>(a, blockIdx.x / C, 16 * MT);
+  static_assert(!GATHER || MT == 1);
+  __shared__ int from[16];  // GATHER: the tile's tokens
+  Tile tile;
+  if constexpr (GATHER) tile = gather_tile<kWarps>(a, blockIdx.x / C, from);
+  else tile = find_tile<kWarps>(a, blockIdx.x / C, 16 * MT);
   if (tile.rows == 0) return;
   const int rk = tile.rk;
   if (rk == 0 && a.out == a.base) return;
@@ -98,7 +104,8 @@ __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kern
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       ok[m][h] = 16 * m + 8 * h + g < tile.rows;
-      tok[m][h] = tile.t0 + (ok[m][h] ? 16 * m + 8 * h + g : 0);
+      const int i = ok[m][h] ? 16 * m + 8 * h + g : 0;
+      tok[m][h] = GATHER ? from[i] : tile.t0 + i;
     }
   const uint4 zero = make_uint4(0, 0, 0, 0);
   const int part_w = crank * kWarps + warp, parts = C * kWarps;
@@ -464,17 +471,19 @@ cudaError_t launch_many(const AdapterArgs& a, cudaStream_t s) {
   return launch_pdl(adapter_many_kernel, dim3((unsigned)tile_bound(a, Many::BM)), dim3(Many::threads), Many::smem, s, a);
 }
 
-template <int RT, int MT>
+template <int RT, int MT, bool GATHER>
 cudaError_t launch_few(const AdapterArgs& a, int cluster, cudaStream_t s) {
-  const int smem = (kWarps + cluster) * 2 * RT * MT * 32 * 16;
-  if (smem > 32 * 1024) {  // with the static part past the 48 KB that need no opt-in, or near it
-    const cudaError_t e = cudaFuncSetAttribute(adapter_few_kernel<RT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int per = 2 * RT * MT * 32 * 16, most = (kWarps + 8) * per;
+  static std::atomic<bool> set{false};
+  if (!set.load(std::memory_order_relaxed)) {
+    const cudaError_t e = cudaFuncSetAttribute(adapter_few_kernel<RT, MT, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
+    set.store(true, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tile_bound(a, 16 * MT) * cluster));
+  cfg.gridDim = dim3((unsigned)((GATHER ? gather_bound(a) : tile_bound(a, 16 * MT)) * cluster));
   cfg.blockDim = dim3(32 * kWarps);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = (kWarps + cluster) * per;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -486,7 +495,7 @@ cudaError_t launch_few(const AdapterArgs& a, int cluster, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   note_launches(1);
-  return cudaLaunchKernelEx(&cfg, adapter_few_kernel<RT, MT>, a);
+  return cudaLaunchKernelEx(&cfg, adapter_few_kernel<RT, MT, GATHER>, a);
 }
 
 template <int RT>
@@ -495,13 +504,17 @@ cudaError_t launch_rank(const AdapterArgs& a, cudaStream_t s) {
   const int64_t room = (int64_t)tc_num_sms() * (RT <= 4 ? 2 : 1);  // blocks that the device takes at once
   // Tiles, with requests of mean > the tile's height half a tile over each.
   const int64_t likely16 = a.T / 16 + requests / 2, likely32 = a.T / 32 + requests / 2;
-  // blocks of a cluster share a tile as long as the grid fits the device at once
-  const auto blocks = [&](int64_t tiles) { return 8 * tiles <= room ? 8 : 4 * tiles <= room ? 4 : 2 * tiles <= room ? 2 : 1; };
+  // Blocks of a cluster share a tile as long as the grid fits the device at once.  By eight only up to 80% of it
+  // (32 tiles at rank 16: 4.9 us by eight, 4.1 by four; at rank 128, a block per SM, 16.1 and 12.3), but for ranks
+  // 33 to 64, where the work outweighs it (32 tiles: 8.5 and 10.0).
+  const auto blocks = [&](int64_t tiles) {
+    return 80 * tiles <= room * (RT == 4 ? 10 : 8) ? 8 : 4 * tiles <= room ? 4 : 2 * tiles <= room ? 2 : 1;
+  };
   if constexpr (RT == 1) {
     // Long requests past one wave of tiles of 32: 16384 tokens, 2048 -> 2048, the ring 40.2 us, those tiles 44.1
     // (tcgen05 tiles 40.2, 59.4 ragged); 10000 ragged 34.8 and 38.4; 7000, within a wave, 26.6 and 22.0.
     if (mean >= 32 && likely32 > room) return launch_many(a, s);
-    if (mean > 16 && 4 * likely16 > room) return launch_few<1, 2>(a, blocks(likely32), s);
+    if (mean > 16 && 4 * likely16 > room) return launch_few<1, 2, false>(a, blocks(likely32), s);
   } else {
     // The tcgen05 tiles from where the kernel for few, whose time goes by T r (H + N) and by waves of tiles, takes
     // longer than their some 20 us: 4096 tokens, 2048 -> 2048 at rank 64 22.0 against 28.9 us, at rank 32 19.5 against
@@ -509,7 +522,13 @@ cudaError_t launch_rank(const AdapterArgs& a, cudaStream_t s) {
     const double work = (double)a.T * (16 * RT) * (a.H + a.N);
     if (mean >= 128 && work >= (likely16 > room ? 5e8 : 8e8) && adapter_tiles_fit(a)) return launch_adapter_tiles(a, s);
   }
-  return launch_few<RT, 1>(a, blocks(tile_bound(a, 16)), s);
+  // Short requests that share adapters, enough of them to pay for the longer search (0.4 to 1 us): one token each,
+  // 2048 -> 2048, 256 requests over 16 adapters: rank 16 6.9 us against 8.9, rank 64 10.2 against 22.2, rank 128 15.0
+  // against 58.0; over 64 adapters: rank 16 9.5 against 8.9, rank 32 11.2 against 12.4, rank 64 20.4 against 27.4.
+  if (a.R >= 32 && a.R <= kGatherRequests && a.n <= kGatherSlots && a.T <= 8 * (int64_t)a.R &&
+      (int64_t)a.R * (RT < 4 ? RT : 4) >= 8 * (int64_t)a.n)
+    return launch_few<RT, 1, true>(a, blocks(gather_bound(a)), s);
+  return launch_few<RT, 1, false>(a, blocks(tile_bound(a, 16)), s);
 }
 
 }  // namespace

@@ -455,6 +455,45 @@ def test_adapters_tiles_of_32(r, H, N, pad):
     run_adapters([17 + (7 * i) % 13 for i in range(120)], [i % 4 - 1 for i in range(120)], H, N, 3, r, 35, rank=rank, pad=pad)
 
 
+@pytest.mark.parametrize("r", [8, 16, 24, 32, 48, 64, 96, 128])
+@pytest.mark.parametrize("H,N,pad", [(256, 264, 8), (1000, 72, 0)])
+def test_adapters_shared_by_short_requests(r, H, N, pad):
+    """Tiles that gather an adapter's tokens from many requests: one token each and ragged ones, more of one adapter
+    than a tile holds, empty requests, slots out of range, none at all, the most requests the search takes and one more."""
+    rank = [r, max(1, r - 3), max(1, r // 2), 0]
+    run_adapters([1] * 64, [(i * i) % 5 - 1 for i in range(64)], H, N, 4, r, 41, rank=rank, pad=pad)
+    run_adapters([(i * 7) % 12 for i in range(90)], [(i * 3) % 7 - 2 for i in range(90)], H, N, 4, r, 42, rank=rank, in_place=True)
+    run_adapters([0, 31, 1, 16, 17] + [1] * 45, [2, 1, 1, 2, 1] + [0, 1, 2] * 15, H, N, 3, r, 43, pad=pad, scale=False)
+    run_adapters([1] * 40, [-1] * 40, H, N, 2, r, 44)
+    run_adapters([1] * 33, [0] * 33, H, N, 1, r, 45, rank=[r])
+    run_adapters([1] * 512, [(i * 11) % 60 for i in range(512)], H, N, 60, r, 46, pad=pad)
+    run_adapters([1] * 513, [(i * 11) % 60 for i in range(513)], H, N, 60, r, 47)
+
+
+def test_gathered_adapters_repeat_and_capture():
+    """NaN stays in its row among gathered ones, runs repeat, and a captured call follows its inputs."""
+    g = gen(51)
+    T, H, N, r = 96, 512, 264, 64
+    x, base = rows(T, H, torch.bfloat16, g), rows(T, N, torch.bfloat16, g)
+    a = torch.randn((3, r, H), generator=g, device="cuda").bfloat16()
+    b = torch.randn((3, N, r), generator=g, device="cuda").bfloat16()
+    starts = torch.arange(T + 1, dtype=torch.int32, device="cuda")
+    slot = torch.tensor([(i * 5) % 4 - 1 for i in range(T)], dtype=torch.int32, device="cuda")
+    want = M.moe_adapters_add(x, base, a, b, starts, slot)
+    assert torch.equal(want, M.moe_adapters_add(x, base, a, b, starts, slot))
+    x2 = x.clone()
+    x2[17, 3] = float("nan")
+    got = M.moe_adapters_add(x2, base, a, b, starts, slot)
+    keep = torch.arange(T, device="cuda") != 17
+    assert slot[17] >= 0 and torch.isnan(got[17]).all() and torch.equal(got[keep], want[keep])
+    graph, out = torch.cuda.CUDAGraph(), torch.empty_like(base)
+    with torch.cuda.graph(graph):
+        M.moe_adapters_add(x, base, a, b, starts, slot, out=out)
+    slot.copy_(slot.flip(0))
+    graph.replay()
+    assert torch.equal(out, M.moe_adapters_add(x, base, a, b, starts, slot))
+
+
 def test_adapters_first_call_of_a_process():
     """Each kernel and cluster size as the first launch of its process: nothing an earlier call has set up (the
     opt-in to more shared memory) may be needed.  A process per length; every rank class is new to it."""
@@ -464,7 +503,8 @@ def test_adapters_first_call_of_a_process():
 
     here = os.path.dirname(os.path.abspath(__file__))
     code = ("import sys; sys.path[:0] = [{!r}, {!r}]; import test_block_ops as t\n"
-            "for r in (8, 24, 40, 128): t.run_adapters([{}], [0], 64, 64, 1, r, 21)")
+            "for r in (8, 24, 40, 128): t.run_adapters([{}], [0], 64, 64, 1, r, 21)\n"
+            "for r in (8, 24, 40, 128): t.run_adapters([1] * 40, [0] * 40, 64, 64, 1, r, 22)")
     runs = [subprocess.Popen([sys.executable, "-c", code.format(here, os.path.dirname(here), T)], stdout=subprocess.PIPE,
                              stderr=subprocess.STDOUT, text=True) for T in (16, 464, 944, 1904, 3184)]
     outs = [p.communicate(timeout=300)[0] for p in runs]
