@@ -515,12 +515,21 @@ cudaError_t launch_rank(const AdapterArgs& a, cudaStream_t s) {
     // (tcgen05 tiles 40.2, 59.4 ragged); 10000 ragged 34.8 and 38.4; 7000, within a wave, 26.6 and 22.0.
     if (mean >= 32 && likely32 > room) return launch_many(a, s);
     if (mean > 16 && 4 * likely16 > room) return launch_few<1, 2, false>(a, blocks(likely32), s);
-  } else {
-    // The tcgen05 tiles from where the kernel for few, whose time goes by T r (H + N) and by waves of tiles, takes
-    // longer than their some 20 us: 4096 tokens, 2048 -> 2048 at rank 64 22.0 against 28.9 us, at rank 32 19.5 against
-    // 17.5, 6000 ragged at rank 32 25.2 against 30.1, 16384 of 512 -> 512 at rank 32 15.4 against 20.7.
-    const double work = (double)a.T * (16 * RT) * (a.H + a.N);
-    if (mean >= 128 && work >= (likely16 > room ? 5e8 : 8e8) && adapter_tiles_fit(a)) return launch_adapter_tiles(a, s);
+  } else if (mean >= 16) {
+    // The tcgen05 tiles or the kernel for few, by their waves over the SMs (a part of one where clusters share a
+    // tile), a wave of the tiles in units of the other's: 1.95, 0.85 and 1.1 at ranks up to 32, 64 and 128.  Times
+    // with the tiles and without, 2048 -> 2048: rank 32, 4096 tokens of 4 requests 19.5 and 17.5 us, 6000 of 40 25.2 and
+    // 30.1; rank 64, 2048 of 32 29.7 and 19.7, 4096 of 64 25.8 and 32.6, 16384 of 300 87 and 115, of 1000 197 and 161;
+    // rank 128, 2048 of 32 44.1 and 41.0, of 128 42 and 74, 8192 of 128 45 and 147, 16384 of 300 120 and 286.  The tiles'
+    // fixed cost wants some work against it: 2048 of 100, 256 -> 256, rank 64, 21.4 and 6.2, 3000 of 20, 1024 -> 1024
+    // 18.6 and 14.9; 16384 of 16, 512 -> 512, rank 32, 15.8 and 21.0, rank 64 16.2 and 35.7.
+    const int64_t sms = tc_num_sms(), likely128 = a.T / 128 + (mean >= 128 ? requests / 2 : requests);
+    const double full = likely128 > sms ? (double)likely128 / sms : 1.;
+    const double tiles = (RT == 2 ? 1.95 : RT == 4 ? 0.85 : 1.1) *
+                         (mean < 128 || 20 * likely128 > sms * 9 ? full : 40 * likely128 > sms * 9 ? 0.75 : 0.55);
+    const double few = blocks(likely16) == 1 ? (double)((likely16 + room - 1) / room) : blocks(likely16) == 2 ? 0.58 : 0.3;
+    const double work = few * (16 * RT) * (a.H + a.N);
+    if (tiles < few && work >= (RT == 2 ? 1.0e5 : 1.5e5) && adapter_tiles_fit(a)) return launch_adapter_tiles(a, s);
   }
   // Short requests that share adapters, enough of them to pay for the longer search (0.4 to 1 us): one token each,
   // 2048 -> 2048, 256 requests over 16 adapters: rank 16 6.9 us against 8.9, rank 64 10.2 against 22.2, rank 128 15.0
@@ -528,7 +537,7 @@ cudaError_t launch_rank(const AdapterArgs& a, cudaStream_t s) {
   if (a.R >= 32 && a.R <= kGatherRequests && a.n <= kGatherSlots && a.T <= 8 * (int64_t)a.R &&
       (int64_t)a.R * (RT < 4 ? RT : 4) >= 8 * (int64_t)a.n)
     return launch_few<RT, 1, true>(a, blocks(gather_bound(a)), s);
-  return launch_few<RT, 1, false>(a, blocks(tile_bound(a, 16)), s);
+  return launch_few<RT, 1, false>(a, blocks(mean > 16 ? likely16 : tile_bound(a, 16)), s);
 }
 
 }  // namespace
