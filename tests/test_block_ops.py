@@ -470,6 +470,27 @@ def test_adapters_shared_by_short_requests(r, H, N, pad):
     run_adapters([1] * 513, [(i * 11) % 60 for i in range(513)], H, N, 60, r, 47)
 
 
+@pytest.mark.parametrize("r", [16, 32, 64, 128])
+@pytest.mark.parametrize("R", [33, 40, 50, 90, 100, 257])
+def test_gathered_adapters_among_requests_without_one(r, R):
+    """Any number of requests, some without an adapter, out of place: every row its own, none outside the batch."""
+    H, N, n = 256, 264, 2
+    for ragged in (False, True):
+        lens = [(i * 7 + R) % 12 for i in range(R)] if ragged else [1] * R
+        slot = [-1 if i % 7 == 6 else i % n for i in range(R)]
+        g, T = gen(R + r), sum(lens)
+        starts = np.concatenate([[0], np.cumsum(lens)]).tolist()
+        x, base = rows(T, H, torch.bfloat16, g), rows(T, N, torch.bfloat16, g)
+        a = (torch.randn((n, r, H), generator=g, device="cuda") / math.sqrt(H)).bfloat16()
+        b = (torch.randn((n, N, r), generator=g, device="cuda") / math.sqrt(r)).bfloat16()
+        buf = torch.full((T + 128, N), 7.0, dtype=torch.bfloat16, device="cuda")
+        i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+        M.moe_adapters_add(x, base, a, b, i32(starts), i32(slot), out=buf[64:64 + T])
+        ref, err = ref_adapters(x, base, a, b, starts, slot, None, None)
+        check(buf[64:64 + T], ref, err, f"{R} requests, rank {r}")
+        assert (buf[:64] == 7.0).all() and (buf[64 + T:] == 7.0).all()
+
+
 def test_gathered_adapters_repeat_and_capture():
     """NaN stays in its row among gathered ones, runs repeat, and a captured call follows its inputs."""
     g = gen(51)
