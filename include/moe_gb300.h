@@ -394,7 +394,7 @@ moe_status_t moe_layer_forward_scored(const void* x, const moe_router_t* router,
 
 /* The low-rank adapters of many requests, added to the output of a projection that they share:
  *   out[t] = base[t] + scale[a] * B[a] (A[a] x[t]),   a = slot[q] of the request q that t is in,
- * and out[t] = base[t] where a is outside 0 .. n-1 (-1: a request without an adapter).
+ * and out[t] = base[t] where a is outside 0 .. n-1 (-1: a request without an adapter; n = 0: all of them).
  *   x (dev) bf16 [T, H] (pitch ldx); base, out (dev) bf16 [T, N] (pitches ldb, ldo); out may be
  *   base (same pitch: added in place), no other overlap.
  *   A (dev) bf16 [n, r, H], B (dev) bf16 [n, N, r]: n adapters' matrices, each as torch.nn.Linear

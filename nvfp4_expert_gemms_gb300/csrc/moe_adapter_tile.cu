@@ -474,8 +474,8 @@ static bool rows_map(CUtensorMap* m, const void* base, uint64_t rows, int r, int
   return bf16_map(m, base, 5, dims, strides, box);
 }
 
-bool adapter_tiles_fit(const AdapterArgs& a) {  // rows of A and B by 32-bit coordinates
-  return (int64_t)a.n * a.N < INT32_MAX && (int64_t)a.n * a.r < INT32_MAX;
+bool adapter_tiles_fit(const AdapterArgs& a) {  // rows of A and B by 32-bit coordinates; a map has some
+  return a.n > 0 && (int64_t)a.n * a.N < INT32_MAX && (int64_t)a.n * a.r < INT32_MAX;
 }
 
 cudaError_t launch_adapter_tiles(const AdapterArgs& g, cudaStream_t s) {

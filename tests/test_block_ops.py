@@ -577,6 +577,20 @@ def test_adapters_nan_stays_in_its_row_and_runs_repeat():
     assert M.moe_get_adapter_error() == 0
 
 
+@pytest.mark.parametrize("r", [16, 32, 64, 128])
+def test_no_adapters_at_all(r):
+    """n = 0: every request is one without an adapter, at any size."""
+    H, N = 2048, 2048
+    for lens in ([1], [1] * 40, [3, 0, 50], [4096, 4096], [500] * 33):
+        g, T, R = gen(r), sum(lens), len(lens)
+        x, base = rows(T, H, torch.bfloat16, g), rows(T, N, torch.bfloat16, g)
+        a = torch.empty((0, r, H), dtype=torch.bfloat16, device="cuda")
+        b = torch.empty((0, N, r), dtype=torch.bfloat16, device="cuda")
+        starts = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+        slot = torch.tensor([i % 3 - 1 for i in range(R)], dtype=torch.int32, device="cuda")
+        assert torch.equal(M.moe_adapters_add(x, base, a, b, starts, slot), base)
+
+
 # ------------------------------------------------------------------------------------------ together
 def bf16_experts(E, H, I, g):
     wgu = (0.05 * torch.randn((E, 2 * I, H), generator=g, device="cuda")).bfloat16()
