@@ -366,7 +366,8 @@ typedef enum { MOE_SCORE_SOFTMAX = 1, MOE_SCORE_SIGMOID = 2 } moe_score_t;
  *   choice    the top_k candidates of largest key, in descending order; ties between experts and
  *               between groups go to the lower index; NaN keys count as -infinity
  *   weight    scale * s_e, divided by the sum over the chosen if renormalize; 0 for all where that
- *               sum is 0 (every chosen logit -infinity) */
+ *               sum is 0 (every chosen logit -infinity)
+ * A +infinity logit makes softmax's scores of its row NaN: its weights are NaN. */
 typedef struct {
   int32_t score;       /* moe_score_t */
   int32_t groups;      /* divides E, 1 .. 32 */

@@ -265,12 +265,14 @@ __device__ __forceinline__ int score_token(const ScoreArgs& a, const ScoreGeom& 
       den = warp_sum(den);
     }
   }
+  // a logit's softmax: 0 in an empty row, NaN in one with a +inf logit
+  auto softmax_of = [&](float v) { return den == 0.f ? 0.f : __fdiv_rn(exp_rn(v, m), den); };
   // expert e's key (known: its logit, with few experts per lane); sv: its sigmoid score, or its logit where the score is a softmax's
   auto key_of = [&](int e, float known, float& sv) {
     const float lv = VT <= 4 ? known : load_logit(a, row + e);
     sv = softmax ? lv : sigmoid_rn(lv);
     if (!biased) return lv;
-    const float s = softmax ? (den > 0.f ? __fdiv_rn(exp_rn(lv, m), den) : 0.f) : sv;
+    const float s = softmax ? softmax_of(lv) : sv;
     return fmaxf(__fadd_rn(s, a.bias[e]), -INFINITY);
   };
   int mine = 0;
@@ -327,7 +329,7 @@ __device__ __forceinline__ int score_token(const ScoreArgs& a, const ScoreGeom& 
     if (biased) {
 #pragma unroll
       for (int i = 0; i < VT; ++i) {
-        const float s = softmax ? (den > 0.f ? __fdiv_rn(exp_rn(l[i], m), den) : 0.f) : sigmoid_rn(l[i]);
+        const float s = softmax ? softmax_of(l[i]) : sigmoid_rn(l[i]);
         key[i] = i < cnt ? fmaxf(__fadd_rn(s, a.bias[e0 + i]), -INFINITY) : kNoKey;
       }
     } else {
@@ -339,8 +341,9 @@ __device__ __forceinline__ int score_token(const ScoreArgs& a, const ScoreGeom& 
     if (grouped) {
       float g1 = top;
       if (two && !biased) {  // scores in place of logits, whose order they have
-        g1 = isnan(top) ? -INFINITY : softmax ? exp_rn(top, m) : sigmoid_rn(top);
-        b2 = cnt < 2 ? -INFINITY : softmax ? exp_rn(b2, m) : sigmoid_rn(b2);
+        const bool none = softmax && m == INFINITY;  // softmax's scores are all NaN
+        g1 = isnan(top) || none ? -INFINITY : softmax ? exp_rn(top, m) : sigmoid_rn(top);
+        b2 = cnt < 2 || none ? -INFINITY : softmax ? exp_rn(b2, m) : sigmoid_rn(b2);
       }
       const float gv = group_value(g1, b2, lanes, two);
       int front = 0;  // groups in front of this one
@@ -368,7 +371,8 @@ __device__ __forceinline__ int score_token(const ScoreArgs& a, const ScoreGeom& 
   if (softmax) {
     const float ms = a.r.renormalize ? redux_max(lane < k ? sv : -INFINITY) : m;
     s = lane < k ? exp_rn(sv, ms) : 0.f;
-    if (!a.r.renormalize) s = den > 0.f ? s / den : 0.f;
+    if (!a.r.renormalize) s = den == 0.f ? 0.f : s / den;
+    if (m == INFINITY) s = kNoKey;  // no score of the row is a number, whichever are chosen
   }
   if (a.r.renormalize) {
     float tot = s;

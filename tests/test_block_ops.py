@@ -354,6 +354,25 @@ def test_route_ties_and_masked_experts():
     assert idx.shape == (0, 8) and w.shape == (0, 8)
 
 
+@pytest.mark.parametrize("E,groups", [(7, 1), (64, 8), (128, 1), (256, 8)])
+def test_route_infinite_logit(E, groups):
+    """A +inf logit: softmax is NaN for the whole row, so are its weights; its neighbours and sigmoid scores are not."""
+    k = min(8, E)
+    lg = rows(3, E, torch.float32, gen(E))
+    lg[1, E // 2] = float("inf")
+    for renorm in (False, True):
+        idx, w = M.moe_route_scored(lg, M.Router("softmax", groups=groups, renormalize=renorm), k)
+        assert int(idx[1, 0]) == E // 2 and torch.isnan(w[1]).all() and torch.isfinite(w[[0, 2]]).all()
+        # with a bias every key of the row is NaN, hence -infinity: the lowest experts
+        idx, w = M.moe_route_scored(lg, M.Router("softmax", groups=groups, renormalize=renorm), k, bias=torch.randn(E, device="cuda"))
+        assert idx[1].tolist() == list(range(k)) and torch.isnan(w[1]).all() and torch.isfinite(w[[0, 2]]).all()
+        if groups > 1:  # groups by two scores: all of them -infinity, the lowest are kept
+            idx, w = M.moe_route_scored(lg, M.Router("softmax", groups=groups, top_groups=2, group_top=2, renormalize=renorm), k)
+            assert int(idx[1].max()) < 2 * E // groups and torch.isnan(w[1]).all() and torch.isfinite(w[[0, 2]]).all()
+    idx, w = M.moe_route_scored(lg, M.Router("sigmoid", groups=groups, renormalize=False), k)
+    assert int(idx[1, 0]) == E // 2 and w[1, 0] == 1.0 and torch.isfinite(w).all()
+
+
 # ------------------------------------------------------------------------------------------ adapters
 @pytest.mark.parametrize("E,groups,tg", [(256, 8, 1), (256, 16, 2), (128, 8, 1), (240, 8, 1), (256, 8, 2)])
 def test_route_few_groups(E, groups, tg):
