@@ -135,8 +135,9 @@ __device__ __forceinline__ float lane_top(const float (&key)[VT], int cnt, bool 
 }
 
 // The value of a lane's group, in every lane of the group, from its lanes' largest and second keys: their
-// sum, or the largest.
-__device__ __forceinline__ float group_value(float b1, float b2, int lanes, bool both) {
+// sum, or the largest.  reach: how far it may be off where the keys are estimates, which goes by the keys' sizes and
+// not by the sum's, where they cancel.
+__device__ __forceinline__ float group_value(float b1, float b2, int lanes, bool both, float& reach) {
   b1 = fmaxf(b1, -INFINITY);
   for (int off = lanes >> 1; off > 0; off >>= 1) {
     const float o1 = __shfl_xor_sync(0xffffffffu, b1, off);
@@ -146,6 +147,7 @@ __device__ __forceinline__ float group_value(float b1, float b2, int lanes, bool
     }
     b1 = fmaxf(b1, o1);
   }
+  reach = key_slack(b1) + (both ? key_slack(b2) : 0.f);
   return fmaxf(both ? __fadd_rn(b1, b2) : b1, -INFINITY);
 }
 
@@ -307,16 +309,17 @@ __device__ __forceinline__ int score_token(const ScoreArgs& a, const ScoreGeom& 
       float top = g.full ? lane_top<true, VT>(est, cnt, two, b2) : lane_top<false, VT>(est, cnt, two, b2);
       bool clear = true;
       if (grouped) {
-        const float gv = group_value(top, b2, lanes, two);
+        float reach;
+        const float gv = group_value(top, b2, lanes, two, reach);
         float bound = 0.f, rem = grp < a.r.groups ? gv : kNoKey;
 #pragma unroll 4
         for (int j = 0; j < a.r.top_groups; ++j) {
           bound = redux_max(rem);
           rem = rem == bound ? kNoKey : rem;
         }
-        // the last group kept, and no other within reach of it
-        const float gap = 4.f * key_slack(bound);
-        const uint32_t near = __ballot_sync(0xffffffffu, grp < a.r.groups && fabsf(gv - bound) <= gap);
+        // the last group kept, and no other within reach of it (-infinity is no estimate, and far from any other)
+        const float gap = reach + redux_max(gv == bound ? reach : kNoKey);
+        const uint32_t near = __ballot_sync(0xffffffffu, grp < a.r.groups && gv > -INFINITY && fabsf(gv - bound) <= gap);
         const uint32_t kept = __ballot_sync(0xffffffffu, grp < a.r.groups && gv >= bound);
         clear = __popc(near) == lanes && __popc(kept) == lanes * a.r.top_groups && !isinf(bound);
         if (!(gv >= bound)) top = kNoKey;
@@ -345,7 +348,8 @@ __device__ __forceinline__ int score_token(const ScoreArgs& a, const ScoreGeom& 
         g1 = isnan(top) || none ? -INFINITY : softmax ? exp_rn(top, m) : sigmoid_rn(top);
         b2 = cnt < 2 || none ? -INFINITY : softmax ? exp_rn(b2, m) : sigmoid_rn(b2);
       }
-      const float gv = group_value(g1, b2, lanes, two);
+      float reach;  // unused: the keys are exact
+      const float gv = group_value(g1, b2, lanes, two, reach);
       int front = 0;  // groups in front of this one
       for (int h = 0; h < a.r.groups; ++h) {
         const float o = __shfl_sync(0xffffffffu, gv, h << g.lanes_log2);

@@ -373,6 +373,26 @@ def test_route_infinite_logit(E, groups):
     assert int(idx[1, 0]) == E // 2 and w[1, 0] == 1.0 and torch.isfinite(w).all()
 
 
+@pytest.mark.parametrize("size", [64.0, 256.0, 4096.0])
+def test_route_groups_whose_keys_cancel(size):
+    """The choice does not depend on the kernel's path: the same experts among others that cannot win.  A group's best
+    two keys are near +size and -size, its value their sum, and the groups' values are a few of the keys' roundings apart."""
+    T, groups, S, wide = 200000, 8, 8, 32
+    g = gen(int(size))
+    # scores where a key's rounding turns, to within their own: half units of the keys, some 6 units apart
+    ulp = size * 2.0 ** -23
+    turn = 0.5 + (torch.randn((T, groups, S), generator=g, device="cuda").double() * 6).round() * ulp + ulp / 2
+    lg = (torch.logit(turn) + torch.randn((T, groups, S), generator=g, device="cuda") * 2.0 ** -22).float()
+    bias = torch.full((groups, S), -3.0 * size, device="cuda")
+    bias[:, 0], bias[:, 1] = size, -size - 1.0
+    r = M.Router("sigmoid", groups=groups, top_groups=4, group_top=2)
+    idx, w = M.moe_route_scored(lg.reshape(T, -1), r, 4, bias=bias.reshape(-1))
+    lg2, bias2 = torch.zeros((T, groups, wide), device="cuda"), torch.full((groups, wide), -9.0 * size, device="cuda")
+    lg2[..., :S], bias2[:, :S] = lg, bias
+    idx2, w2 = M.moe_route_scored(lg2.reshape(T, -1), r, 4, bias=bias2.reshape(-1))
+    assert torch.equal(idx2 // wide * S + idx2 % wide, idx) and torch.equal(w, w2)
+
+
 # ------------------------------------------------------------------------------------------ adapters
 @pytest.mark.parametrize("E,groups,tg", [(256, 8, 1), (256, 16, 2), (128, 8, 1), (240, 8, 1), (256, 8, 2)])
 def test_route_few_groups(E, groups, tg):
