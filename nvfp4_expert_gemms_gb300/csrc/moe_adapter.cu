@@ -37,18 +37,16 @@ __device__ __forceinline__ void mma_bf16(float* d, uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// v (the sums of one rank step's two MMA tiles) times the adapter's scale, as the second product's A
-// operand in two bf16 terms.
-__device__ __forceinline__ void split_v(const float (&v0)[4], const float (&v1)[4], float sc, uint32_t (&hi)[4],
+// v (the sums of one rank step's two MMA tiles; the lane's ranks are k .. k+3) times the adapter's scale, as the
+// second product's A operand in two bf16 terms.  Zero past the adapter's rank, where an infinite x leaves NaN.
+__device__ __forceinline__ void split_v(const float (&v0)[4], const float (&v1)[4], float sc, int k, int rk, uint32_t (&hi)[4],
                                         uint32_t (&lo)[4]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int row = 0; row < 2; ++row) {
       const float c0 = (h ? v1 : v0)[2 * row] * sc, c1 = (h ? v1 : v0)[2 * row + 1] * sc;
-      const uint32_t p = pack_bf16(c0, c1);
-      hi[2 * h + row] = p;
-      lo[2 * h + row] = pack_bf16(c0 - lo_f32(p), c1 - hi_f32(p));
+      split_pair(k + 2 * h < rk ? c0 : 0.f, k + 2 * h + 1 < rk ? c1 : 0.f, hi[2 * h + row], lo[2 * h + row]);
     }
 }
 
@@ -243,7 +241,7 @@ __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kern
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int s = 0; s < RT; ++s) split_v(v[m][2 * s], v[m][2 * s + 1], tile.scale, hi[m][s], lo[m][s]);
+    for (int s = 0; s < RT; ++s) split_v(v[m][2 * s], v[m][2 * s + 1], tile.scale, 16 * s + 4 * t, rk, hi[m][s], lo[m][s]);
   for (int c = 32 * part_w; c < a.N; c += 32 * parts) {
     constexpr bool AHEAD = RT * MT <= 2;  // the next columns are loaded under these ones (registers allowing)
     Cols next;
@@ -425,7 +423,7 @@ __global__ void __launch_bounds__(Many::threads) adapter_many_kernel(const Adapt
   }
   uint32_t hi[RT][4], lo[RT][4];
 #pragma unroll
-  for (int s = 0; s < RT; ++s) split_v(v[2 * s], v[2 * s + 1], tile.scale, hi[s], lo[s]);
+  for (int s = 0; s < RT; ++s) split_v(v[2 * s], v[2 * s + 1], tile.scale, 16 * s + 4 * t, rk, hi[s], lo[s]);
   const bool ok0 = r0 < tile.rows, ok1 = r1 < tile.rows;
   __nv_bfloat16 *o0 = a.out + (int64_t)(tile.t0 + r0) * a.ldo, *o1 = o0 + 8 * a.ldo;
   for (int st = 0; st < nst; ++st) {

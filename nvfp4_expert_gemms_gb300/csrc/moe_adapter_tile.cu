@@ -229,8 +229,7 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
     for (int c = 0; c < 8; ++c) {
       const float f0 = 16 * s + 2 * c < rk ? f[2 * c] * tile.scale : 0.f;
       const float f1 = 16 * s + 2 * c + 1 < rk ? f[2 * c + 1] * tile.scale : 0.f;
-      hi[i][c] = pack_bf16(f0, f1);
-      lo[i][c] = pack_bf16(f0 - lo_f32(hi[i][c]), f1 - hi_f32(hi[i][c]));
+      split_pair(f0, f1, hi[i][c], lo[i][c]);
     }
   };
   float4* parts = (float4*)v_mem;  // [4 steps][128 rows]: this block's sums, where v's terms go afterwards

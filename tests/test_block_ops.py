@@ -630,6 +630,46 @@ def test_no_adapters_at_all(r):
         assert torch.equal(M.moe_adapters_add(x, base, a, b, starts, slot), base)
 
 
+@pytest.mark.parametrize("lens,r", [([4], 8), ([4], 64), ([4], 128), ([1] * 40, 16), ([1] * 40, 64), ([400, 800], 16),
+                                    ([9000, 7000], 16), ([2000, 2000], 32), ([4096, 4096], 64), ([4096, 4096], 128), ([3000, 100], 128)])
+def test_adapters_keep_infinities(lens, r):
+    """A x infinite, or past bf16's largest value: what fp32 gives, not NaN; the other rows as they are."""
+    H, N, T = 1024, 1536, sum(lens)
+    g = gen(r)
+    x, base = rows(T, H, torch.bfloat16, g), rows(T, N, torch.bfloat16, g)
+    a, b = torch.ones((2, r, H), dtype=torch.bfloat16, device="cuda"), torch.randn((2, N, r), generator=g, device="cuda").bfloat16()
+    a[:, :, 1] = 0.0
+    a[:, 0, 1] = 2.0 ** -20
+    a[:, 1:, 0] = -1.0
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    starts, slot = i32(np.concatenate([[0], np.cumsum(lens)])), i32([i % 2 for i in range(len(lens))])
+    s = int(np.repeat(np.arange(len(lens)) % 2, lens)[T // 2])  # the changed row's adapter
+    for rank in (1, r):  # alone: its sign.  All: infinities of both signs, NaN
+        args = dict(scale=torch.full((2,), 1.0035, device="cuda"), rank=i32([rank, rank]))
+        want = M.moe_adapters_add(x, base, a, b, starts, slot, **args)
+        assert torch.isfinite(want).all()
+        y = x.clone()
+        y[T // 2, 0] = float("inf")
+        got = M.moe_adapters_add(y, base, a, b, starts, slot, **args)
+        keep = torch.arange(T, device="cuda") != T // 2
+        assert torch.equal(got[keep], want[keep])
+        ref = (float("inf") * b[s, :, 0].float()).bfloat16()
+        if rank == 1:
+            assert torch.equal(got[T // 2].isnan(), ref.isnan()) and torch.equal(got[T // 2].nan_to_num(7.0), ref.nan_to_num(7.0))
+        else:
+            assert not torch.isfinite(got[T // 2]).any()
+    # finite, but bf16's rounding alone would make it infinite
+    top = torch.finfo(torch.bfloat16).max
+    y = x.clone()
+    y[T // 2] = 0.0
+    y[T // 2, 2] = top
+    args = dict(scale=torch.full((2,), 1.0035, device="cuda"), rank=i32([1, 1]))
+    bt = b * 2.0 ** -120
+    got = M.moe_adapters_add(y, base, a, bt, starts, slot, **args)[T // 2].double()
+    exact = base[T // 2].double() + float(np.float32(1.0035)) * top * bt[s, :, 0].double()
+    assert ((got - exact).abs() <= exact.abs() * 2.0 ** -8 + base[T // 2].double().abs() * 2.0 ** -20 + (exact - base[T // 2].double()).abs() * 2.0 ** -16).all()
+
+
 # ------------------------------------------------------------------------------------------ together
 def bf16_experts(E, H, I, g):
     wgu = (0.05 * torch.randn((E, 2 * I, H), generator=g, device="cuda")).bfloat16()
