@@ -405,9 +405,9 @@ moe_status_t moe_layer_forward_scored(const void* x, const moe_router_t* router,
  *   starts (dev) i32 [R + 1]: request q has tokens starts[q] .. starts[q+1]-1 (none is allowed);
  *   starts[0] = 0, ascending, starts[R] = T.  slot (dev) i32 [R].  Values outside those ranges
  *   are cut to them: they leave rows unwritten, but touch no memory outside the tensors.
- * A[a] x is summed in fp32 and rounded to two bf16 terms (16 bits of significand) for the second
- * product, which is summed in fp32 with base and rounded once.  An infinite A[a] x gives what fp32
- * arithmetic gives; an infinite element of B may give NaN where that gives infinity (the terms' signs
+ * A[a] x is summed in fp32 and enters the second product with all of fp32's 24 bits (as three bf16 terms); that product
+ * is summed in fp32 with base and rounded once.  An infinite A[a] x gives what fp32 arithmetic gives; an infinite
+ * element of B may give NaN where that gives infinity (the terms' signs
  * differ, or one is 0).
  * H and N multiples of 8; r a multiple of 8, 8 .. 128; pointers to matrices 16-byte aligned and
  * pitches multiples of 8.

@@ -11,10 +11,10 @@
 // rows of B its B operand), and the 32 columns of an output group so that a lane holds 8 consecutive
 // ones (16 bytes of base and out).  No shared memory but for v's partial sums where warps share K.
 //
-// v enters the second product as two bf16 terms, hi = bf16(v) and lo = bf16(v - hi): 16 bits of
-// significand, so that an adapter as large as base costs the sum no precision that shows in out's own
-// bf16 rounding.  The extra MMAs are hidden: the register MMAs run at some 597 TFLOP/s here (1.04 ns per
-// m16n8k16 and SM), and what bounds these kernels is memory.
+// v enters the second product as three bf16 terms, each the rest of the one before: 24 bits of significand, as fp32
+// holds, so that the sum keeps its precision also where base and the adapter's part cancel.  The extra MMAs are
+// hidden: the register MMAs run at some 597 TFLOP/s here (1.04 ns per m16n8k16 and SM), and what bounds these kernels
+// is memory.
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -37,17 +37,29 @@ __device__ __forceinline__ void mma_bf16(float* d, uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// v (the sums of one rank step's two MMA tiles; the lane's ranks are k .. k+3) times the adapter's scale, as the
-// second product's A operand in two bf16 terms.  Zero past the adapter's rank, where an infinite x leaves NaN.
-__device__ __forceinline__ void split_v(const float (&v0)[4], const float (&v1)[4], float sc, int k, int rk, uint32_t (&hi)[4],
-                                        uint32_t (&lo)[4]) {
+// A rank step's two tiles of v (the lane's ranks are k .. k+3) times the adapter's scale.  Zero past the adapter's rank,
+// where an infinite x leaves NaN.
+__device__ __forceinline__ void scale_v(float (&v0)[4], float (&v1)[4], float sc, int k, int rk) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v0[i] = k + (i & 1) < rk ? v0[i] * sc : 0.f;
+    v1[i] = k + 2 + (i & 1) < rk ? v1[i] * sc : 0.f;
+  }
+}
+
+// The same as the second product's A operand: [2 h + row] of the three terms.
+__device__ __forceinline__ void split_v(const float (&v0)[4], const float (&v1)[4], Terms (&w)[4]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int row = 0; row < 2; ++row) {
-      const float c0 = (h ? v1 : v0)[2 * row] * sc, c1 = (h ? v1 : v0)[2 * row + 1] * sc;
-      split_pair(k + 2 * h < rk ? c0 : 0.f, k + 2 * h + 1 < rk ? c1 : 0.f, hi[2 * h + row], lo[2 * h + row]);
-    }
+    for (int row = 0; row < 2; ++row) w[2 * h + row] = split_pair((h ? v1 : v0)[2 * row], (h ? v1 : v0)[2 * row + 1]);
+}
+
+// d += v B^T of one rank step, the smallest terms first.
+__device__ __forceinline__ void mma_terms(float* d, const Terms (&w)[4], uint2 b) {
+  mma_bf16(d, w[0].lo, w[1].lo, w[2].lo, w[3].lo, b.x, b.y);
+  mma_bf16(d, w[0].mid, w[1].mid, w[2].mid, w[3].mid, b.x, b.y);
+  mma_bf16(d, w[0].hi, w[1].hi, w[2].hi, w[3].hi, b.x, b.y);
 }
 
 // Clears what stands past the adapter's rank in a lane's ranks k .. k+3 of a row of B.
@@ -237,11 +249,15 @@ __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kern
         v[m][j][3] = s.w;
       }
   }
-  uint32_t hi[MT][RT][4], lo[MT][RT][4];
+  constexpr bool HELD = RT * MT <= 2;  // v's terms are held; else made again for each group of columns (registers)
+  Terms held[HELD ? MT : 1][HELD ? RT : 1][4];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int s = 0; s < RT; ++s) split_v(v[m][2 * s], v[m][2 * s + 1], tile.scale, 16 * s + 4 * t, rk, hi[m][s], lo[m][s]);
+    for (int s = 0; s < RT; ++s) {
+      scale_v(v[m][2 * s], v[m][2 * s + 1], tile.scale, 16 * s + 4 * t, rk);
+      if constexpr (HELD) split_v(v[m][2 * s], v[m][2 * s + 1], held[m][s]);
+    }
   for (int c = 32 * part_w; c < a.N; c += 32 * parts) {
     constexpr bool AHEAD = RT * MT <= 2;  // the next columns are loaded under these ones (registers allowing)
     Cols next;
@@ -252,19 +268,28 @@ __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kern
     for (int m = 0; m < MT; ++m) {
       const uint32_t w0[4] = {now.y[m][0].x, now.y[m][0].y, now.y[m][0].z, now.y[m][0].w};
       const uint32_t w1[4] = {now.y[m][1].x, now.y[m][1].y, now.y[m][1].z, now.y[m][1].w};
+      float d[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        d[j][0] = lo_f32(w0[j]);
+        d[j][1] = hi_f32(w0[j]);
+        d[j][2] = lo_f32(w1[j]);
+        d[j][3] = hi_f32(w1[j]);
+      }
+#pragma unroll
+      for (int s = 0; s < RT; ++s)
+        if (16 * s < rk) {
+          Terms made[4];
+          if constexpr (!HELD) split_v(v[m][2 * s], v[m][2 * s + 1], made);
+          const Terms(&w)[4] = HELD ? held[HELD ? m : 0][HELD ? s : 0] : made;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mma_terms(d[j], w, cut_rank(now.bq[j][s], 16 * s + 4 * t, rk));
+        }
       uint32_t q0[4], q1[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        float d[4] = {lo_f32(w0[j]), hi_f32(w0[j]), lo_f32(w1[j]), hi_f32(w1[j])};
-#pragma unroll
-        for (int s = 0; s < RT; ++s)
-          if (16 * s < rk) {
-            const uint2 b = cut_rank(now.bq[j][s], 16 * s + 4 * t, rk);
-            mma_bf16(d, lo[m][s][0], lo[m][s][1], lo[m][s][2], lo[m][s][3], b.x, b.y);
-            mma_bf16(d, hi[m][s][0], hi[m][s][1], hi[m][s][2], hi[m][s][3], b.x, b.y);
-          }
-        q0[j] = pack_bf16(d[0], d[1]);
-        q1[j] = pack_bf16(d[2], d[3]);
+        q0[j] = pack_bf16(d[j][0], d[j][1]);
+        q1[j] = pack_bf16(d[j][2], d[j][3]);
       }
       if (ok[m][0] && col < a.N) *(uint4*)(a.out + tok[m][0] * a.ldo + col) = make_uint4(q0[0], q0[1], q0[2], q0[3]);
       if (ok[m][1] && col < a.N) *(uint4*)(a.out + tok[m][1] * a.ldo + col) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
@@ -421,9 +446,12 @@ __global__ void __launch_bounds__(Many::threads) adapter_many_kernel(const Adapt
         v[j][3] = o.w;
       }
   }
-  uint32_t hi[RT][4], lo[RT][4];
+  Terms w[RT][4];
 #pragma unroll
-  for (int s = 0; s < RT; ++s) split_v(v[2 * s], v[2 * s + 1], tile.scale, 16 * s + 4 * t, rk, hi[s], lo[s]);
+  for (int s = 0; s < RT; ++s) {
+    scale_v(v[2 * s], v[2 * s + 1], tile.scale, 16 * s + 4 * t, rk);
+    split_v(v[2 * s], v[2 * s + 1], w[s]);
+  }
   const bool ok0 = r0 < tile.rows, ok1 = r1 < tile.rows;
   __nv_bfloat16 *o0 = a.out + (int64_t)(tile.t0 + r0) * a.ldo, *o1 = o0 + 8 * a.ldo;
   for (int st = 0; st < nst; ++st) {
@@ -450,8 +478,7 @@ __global__ void __launch_bounds__(Many::threads) adapter_many_kernel(const Adapt
           if (s < steps) {
             uint2 b = *(const uint2*)(bs + (c + 8 * j + g) * G::pitch + 32 * s + 8 * t);
             if (16 * s + 16 > rk) b = cut_rank(b, 16 * s + 4 * t, rk);
-            mma_bf16(d, lo[s][0], lo[s][1], lo[s][2], lo[s][3], b.x, b.y);
-            mma_bf16(d, hi[s][0], hi[s][1], hi[s][2], hi[s][3], b.x, b.y);
+            mma_terms(d, w[s], b);
           }
         q0[j] = pack_bf16(d[0], d[1]);
         q1[j] = pack_bf16(d[2], d[3]);

@@ -12,11 +12,24 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ float lo_f32(uint32_t p) { return __uint_as_float(p << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); }
 
-// The pair f0, f1 as two bf16 terms each.  hi stops at bf16's largest value, so that an infinity, or what bf16 would
-// round to one, leaves a rest in lo and not a difference of infinities.
-__device__ __forceinline__ void split_pair(float f0, float f1, uint32_t& hi, uint32_t& lo) {
-  asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(f1), "f"(f0));
-  lo = pack_bf16(f0 - lo_f32(hi), f1 - hi_f32(hi));
+// The pair f0, f1 as three bf16 terms each, 24 bits of significand: all that fp32 has.  The first two stop at bf16's
+// largest value, so that an infinity, or what bf16 would round to one, leaves a rest and not a difference of infinities.
+struct Terms {
+  uint32_t hi, mid, lo;
+};
+__device__ __forceinline__ uint32_t pack_bf16_sat(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ Terms split_pair(float f0, float f1) {
+  Terms t;
+  t.hi = pack_bf16_sat(f0, f1);
+  f0 -= lo_f32(t.hi);
+  f1 -= hi_f32(t.hi);
+  t.mid = pack_bf16_sat(f0, f1);
+  t.lo = pack_bf16(f0 - lo_f32(t.mid), f1 - hi_f32(t.mid));
+  return t;
 }
 
 // Long requests on the 5th-generation tensor cores (moe_adapter_tile.cu): tiles of 128 tokens.

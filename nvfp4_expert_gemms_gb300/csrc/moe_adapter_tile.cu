@@ -2,13 +2,13 @@
 // 5th-generation tensor cores.
 //
 //   v = X A^T        M = 128 tokens, N = the adapter's rank (in steps of 16), K = H
-//   out = base + (scale v) B^T   M = 128, N = 128 columns at a time, K = rank, twice: v enters as two
-//                                bf16 terms, hi = bf16(v) and lo = bf16(v - hi) (16 bits of significand)
+//   out = base + (scale v) B^T   M = 128, N = 128 columns at a time, K = rank, three times: v enters as three
+//                                bf16 terms, each the rest of the one before (24 bits of significand)
 //
 // X and A, then B and base, arrive by TMA in the 128-byte swizzle that the MMA reads, through one ring of
 // shared memory that is cut into K stages for the first product and two stages of column blocks for the
 // second.  v goes from tensor memory through registers (scaled, split, zero past the adapter's rank) back
-// into shared memory as the second product's A operand.  The accumulator of the second product has two
+// into tensor memory as the second product's A operand.  The accumulator of the second product has two
 // 128-column buffers (the first one lies where v's sums were), so the epilogue of one column block runs
 // under the MMAs of the next.  A 5-D tensor map deals B's rows so that a lane's accumulator fragment is 16
 // consecutive output columns: out is then written in whole lines straight from registers (natural order,
@@ -45,8 +45,9 @@ __device__ int g_adapter_error;  // kDevOk or the first failure
 
 constexpr int kBM = 128, kEpiWarps = 8, kTileWarps = kEpiWarps + 3, kMaxSlots = 8;
 constexpr int kAtom = 128 * 128;  // bytes: 128 rows of 64 bf16 columns in the 128-byte swizzle
-constexpr int kTmemCols = 256;
-constexpr int kSmem = 225 * 1024;  // most that a block takes (one per SM): 1 KB alignment, v, two N stages
+// Columns of tensor memory: two accumulators of 128, then v's terms, 64 each (128 ranks, two to a column).
+constexpr int kTermCol = 256, kTermCols = 64, kTmemCols = 512;
+constexpr int kSmem = 225 * 1024;  // most that a block takes (one per SM): 1 KB alignment, v's parts, two N stages
 
 struct TileArgs {
   CUtensorMap x, a, b, y;
@@ -120,9 +121,10 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
     }
     return;
   }
-  unsigned char* v_mem = (unsigned char*)(((uintptr_t)dyn + 1023) & ~(uintptr_t)1023);
-  // v's hi and lo, then the K stages, whose memory is the two N stages' later
-  unsigned char* ring = v_mem + 2 * p.katoms * kAtom;
+  // in a cluster this block's part of v's sums, [4 steps][128 rows]; then the K stages, whose memory is the two N
+  // stages' later
+  float4* parts = (float4*)(((uintptr_t)dyn + 1023) & ~(uintptr_t)1023);
+  unsigned char* ring = (unsigned char*)parts + 2 * p.katoms * kAtom;
   const int natom = p.bps * kAtom, ybytes = p.katoms * natom;  // an atom of a stage's B; where its base begins
   // this block's part of the K stages and of the N stages (column blocks)
   const int atoms = (a.H + 63) / 64, kall = (atoms + p.ka - 1) / p.ka, kper = (kall + C - 1) / C;
@@ -219,20 +221,23 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
   }
   __syncwarp();
 
-  // ---- v: from tensor memory (in a cluster: every block's part of K, summed in block order) to shared
-  // memory, scaled, split, zero past the rank.  A thread has one row and every second rank step.
+  // ---- v: from tensor memory (in a cluster: every block's part of K, summed in block order) back to it, scaled, in
+  // three terms, zero past the rank.  A thread has one row and every second rank step.
   const int row = 32 * quarter + lane;
-  uint32_t hi[4][8], lo[4][8];
   auto split = [&](int i, const float* f) {  // rank step half + 2 i
     const int s = half + 2 * i;
+    uint32_t w[3][8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      const float f0 = 16 * s + 2 * c < rk ? f[2 * c] * tile.scale : 0.f;
-      const float f1 = 16 * s + 2 * c + 1 < rk ? f[2 * c + 1] * tile.scale : 0.f;
-      split_pair(f0, f1, hi[i][c], lo[i][c]);
+      const Terms t = split_pair(16 * s + 2 * c < rk ? f[2 * c] * tile.scale : 0.f,
+                                 16 * s + 2 * c + 1 < rk ? f[2 * c + 1] * tile.scale : 0.f);
+      w[0][c] = t.lo;
+      w[1][c] = t.mid;
+      w[2][c] = t.hi;
     }
+#pragma unroll
+    for (int j = 0; j < 3; ++j) tmem_st_32x8(taddr(tmem, 32 * quarter, kTermCol + j * kTermCols + 8 * s), w[j]);
   };
-  float4* parts = (float4*)v_mem;  // [4 steps][128 rows]: this block's sums, where v's terms go afterwards
   if (warp < kEpiWarps && ok) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -278,7 +283,7 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
           split(i, f);
         }
     }
-    cluster.sync();  // every block has read every part: their memory is v's now, and a block may leave
+    cluster.sync();  // every block has read every part: a block may leave
   }
 
   // ---- the second product
@@ -298,7 +303,6 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
       const uint32_t id2 = idesc_bf16_f32(128, 128);
       if (ok) ok = mbar_wait(&bars.v_ready, 0, abort);
       fence_after_sync();
-      const uint32_t vhi = smem_u32(v_mem), vlo = vhi + p.katoms * kAtom;
       for (int b = 0; ok && b < nblk; ++b) {
         const int st = b / p.bps, sub = b % p.bps, s = st & 1, buf = b & 1;
         if (b > 1) ok = mbar_wait(&bars.acc_empty[buf], ((b >> 1) - 1) & 1, abort);
@@ -307,10 +311,9 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
         fence_after_sync();
         const uint32_t bs = smem_u32(ring + (1 - s) * p.nslot) + sub * kAtom, acc = tmem + 128 * buf;
         for (int i = 0; i < steps; ++i) {
-          const uint32_t off = (i >> 2) * kAtom + (i & 3) * 32;
           const uint64_t d = sdesc_k_sw128(bs + (i >> 2) * natom + (i & 3) * 32);
-          mma_f16_ss(acc, sdesc_k_sw128(vlo + off), d, id2, i != 0);
-          mma_f16_ss(acc, sdesc_k_sw128(vhi + off), d, id2, 1);
+#pragma unroll
+          for (int j = 0; j < 3; ++j) mma_f16_ts(acc, tmem + kTermCol + j * kTermCols + 8 * i, d, id2, (i | j) != 0);
         }
         if (sub == p.bps - 1 || b == nblk - 1) mma_commit(&bars.empty_n[s]);
         mma_commit(&bars.acc_full[buf]);
@@ -341,18 +344,9 @@ __global__ void __launch_bounds__(32 * kTileWarps) adapter_tile_kernel(const __g
       }
     }
   } else {  // epilogue
+    tmem_st_wait();
     if (ok) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (half + 2 * i < steps)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            unsigned char* to = v_mem + swz(row, 2 * (half + 2 * i) + h);
-            *(uint4*)to = make_uint4(hi[i][4 * h], hi[i][4 * h + 1], hi[i][4 * h + 2], hi[i][4 * h + 3]);
-            *(uint4*)(to + p.katoms * kAtom) = make_uint4(lo[i][4 * h], lo[i][4 * h + 1], lo[i][4 * h + 2], lo[i][4 * h + 3]);
-          }
       fence_before_sync();
-      fence_proxy_async_smem();
       mbar_arrive(&bars.v_ready);
     }
     // The accumulator's fragments: with B's rows dealt, a lane holds 16 consecutive columns of four rows of

@@ -670,6 +670,27 @@ def test_adapters_keep_infinities(lens, r):
     assert ((got - exact).abs() <= exact.abs() * 2.0 ** -8 + base[T // 2].double().abs() * 2.0 ** -20 + (exact - base[T // 2].double()).abs() * 2.0 ** -16).all()
 
 
+@pytest.mark.parametrize("lens,r", [([4], 8), ([4], 64), ([4], 128), ([1] * 40, 16), ([1] * 40, 64), ([400, 800], 16),
+                                    ([9000, 7000], 16), ([2000, 2000], 32), ([4096, 4096], 64), ([4096, 4096], 128), ([3000, 100], 128)])
+def test_adapters_hold_all_bits_of_the_inner_product(lens, r):
+    """A x of 23 bits, and outputs that are differences of two of them: whole numbers, exact in fp32 from end to end."""
+    H, N, T = 1024, 1536, sum(lens)
+    g = gen(r + 1)
+    x = torch.zeros((T, H), device="cuda")
+    x[:, :64] = torch.randint(1, 256, (T, 64), generator=g, device="cuda").float()
+    a = torch.zeros((2, r, H), device="cuda")
+    a[:, 0::2, 0], a[:, 0::2, 1], a[:, 0::2, 2] = 2.0 ** 14, 2.0 ** 7, 1.0  # 22 bits
+    a[:, 1::2, 0], a[:, 1::2, 1] = 2.0 ** 14, 2.0 ** 7  # the same without the last
+    b = torch.zeros((2, N, r), device="cuda")
+    n = torch.arange(N, device="cuda")
+    b[:, n, n % (r // 2) * 2], b[:, n, n % (r // 2) * 2 + 1] = 1.0, -1.0
+    base = torch.zeros((T, N), dtype=torch.bfloat16, device="cuda")
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    starts, slot = i32(np.concatenate([[0], np.cumsum(lens)])), i32([i % 2 for i in range(len(lens))])
+    got = M.moe_adapters_add(x.bfloat16(), base, a.bfloat16(), b.bfloat16(), starts, slot)
+    assert torch.equal(got, x[:, 2:3].bfloat16().expand(T, N))
+
+
 # ------------------------------------------------------------------------------------------ together
 def bf16_experts(E, H, I, g):
     wgu = (0.05 * torch.randn((E, 2 * I, H), generator=g, device="cuda")).bfloat16()
