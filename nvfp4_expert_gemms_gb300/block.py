@@ -37,8 +37,8 @@ class _RouterDesc(C.Structure):
 
 
 class _NormKey(C.Structure):
-    """What the native side reads of a Norm: the C descriptor, the parameters' length (-1: none) and device."""
-    _fields_ = [("desc", _NormDesc), ("size", C.c_int64), ("device", C.c_int32)]
+    """What the native side reads of a Norm: the C descriptor's kind, eps and offset, and the tensors themselves."""
+    _fields_ = [("desc", _NormDesc), ("weight", C.c_void_p), ("bias", C.c_void_p)]
 
 
 def _refuse(where: str, why: str, status: int = INVALID_ARG):
@@ -90,7 +90,8 @@ def _handle(stream):
 
 class Norm:
     """A norm's kind and parameters: v / rms(v) ("rms") or (v - mean) / std ("layer"), times
-    weight + offset, plus bias (both optional, [H], one type)."""
+    weight + offset, plus bias (both optional, [H], one type).  weight and bias may be replaced, or given other
+    storage: a call uses what they are by then (a captured graph what they were)."""
 
     def __init__(self, kind="rms", weight=None, bias=None, eps=1e-6, offset=0.0):
         where = "Norm"
@@ -98,18 +99,28 @@ class Norm:
             _refuse(where, f"unknown kind {kind!r}")
         if not eps > 0.0:
             _refuse(where, "eps must be positive")
+        self._desc = _NormKey(_NormDesc(_KIND[kind], 1, eps, offset, None, None), None, None)
+        self._key = C.addressof(self._desc)
+        self._made = kind, eps, offset
+        self._set(weight, bias)
+        if weight is not None and bias is not None and (weight.dtype, weight.shape, weight.device) != (bias.dtype, bias.shape, bias.device):
+            _refuse(where, "weight and bias differ in type, size or device")
+
+    def _set(self, weight, bias):
         given = [t for t in (weight, bias) if t is not None]
         for t in given:
-            if t.dim() != 1 or not t.is_cuda or not t.is_contiguous() or t.dtype not in _DT:
-                _refuse(where, "weight and bias are contiguous [H] CUDA tensors of bf16, fp16 or fp32")
-            if t.dtype != given[0].dtype or t.shape != given[0].shape or t.device != given[0].device:
-                _refuse(where, "weight and bias differ in type, size or device")
-        self.weight, self.bias = weight, bias  # kept alive with the addresses below
-        self._desc = _NormKey(_NormDesc(_KIND[kind], _DT[given[0].dtype] if given else 1, eps, offset,
-                                        weight.data_ptr() if weight is not None else None,
-                                        bias.data_ptr() if bias is not None else None),
-                              given[0].shape[0] if given else -1, given[0].device.index if given else 0)
-        self._key = C.addressof(self._desc)
+            if not isinstance(t, torch.Tensor) or t.dim() != 1 or not t.is_cuda or not t.is_contiguous() or t.dtype not in _DT:
+                _refuse("Norm", "weight and bias are contiguous [H] CUDA tensors of bf16, fp16 or fp32")
+        # the native side reads the tensors at each call, so what they hold by then is what counts
+        self._weight, self._bias = weight, bias
+        self._desc.weight, self._desc.bias = (None if t is None else id(t) for t in (weight, bias))
+
+    weight = property(lambda self: self._weight, lambda self, t: self._set(t, self._bias))
+    bias = property(lambda self: self._bias, lambda self, t: self._set(self._weight, t))
+
+    def __reduce__(self):  # a copy has a descriptor of its own
+        kind, eps, offset = self._made
+        return Norm, (kind, self._weight, self._bias, eps, offset)
 
 
 class Router:
@@ -121,8 +132,14 @@ class Router:
         if score not in _SCORE:
             _refuse("Router", f"unknown score {score!r}")
         top_groups = groups if top_groups is None else top_groups
-        self.desc = _RouterDesc(_SCORE[score], groups, top_groups, group_top, int(bool(renormalize)), scale)
-        self._ref = C.addressof(self.desc)
+        self._desc = _RouterDesc(_SCORE[score], groups, top_groups, group_top, int(bool(renormalize)), scale)
+        self._ref = C.addressof(self._desc)
+        self._made = score, groups, top_groups, group_top, renormalize, scale
+
+    desc = property(lambda self: self._desc)  # never another one than _ref's
+
+    def __reduce__(self):  # a copy has a descriptor of its own
+        return Router, self._made
 
 
 def moe_block_enter(x, norm: Norm, dtype=None, out=None, stream=None):

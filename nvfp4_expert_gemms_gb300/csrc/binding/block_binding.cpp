@@ -29,9 +29,8 @@ PyObject* g_refuse;  // block._refuse(where, why, status): raises MoEError
 PyObject* g_key;     // "_key"
 
 struct NormKey {  // block._NormKey
-  moe_norm_t desc;
-  int64_t size;
-  int32_t device;
+  moe_norm_t desc;           // kind, eps, weight_offset
+  PyObject *weight, *bias;  // tensors that the Norm holds, or null
 };
 
 struct Refused {};  // a Python exception is set
@@ -80,16 +79,31 @@ void* vector(PyObject* o, const char* where, const char* name, int64_t n, at::Sc
   return t.data_ptr();
 }
 
-const moe_norm_t* norm(PyObject* o, const char* where, int64_t H, at::Device dev) {
+// The descriptor of a Norm (null for None), in d.  The parameters are read here and not when the Norm is made: they may
+// have been given other storage since.
+const moe_norm_t* norm(PyObject* o, const char* where, int64_t H, at::Device dev, moe_norm_t& d) {
   if (o == Py_None) return nullptr;
   PyObject* k = PyObject_GetAttr(o, g_key);
   if (!k) throw Refused();
   const NormKey* n = (const NormKey*)PyLong_AsVoidPtr(k);
   Py_DECREF(k);
   if (!n) throw Refused();
-  if (n->size >= 0 && (n->size != H || n->device != dev.index()))
-    refuse(where, "", "the norm's parameters have another length or device than the rows");
-  return &n->desc;
+  d = n->desc;
+  d.dtype = 0;
+  auto parameter = [&](PyObject* p) -> const void* {
+    if (!p) return nullptr;
+    const at::Tensor& t = THPVariable_Unpack(p);
+    if (t.dim() != 1 || t.size(0) != H || t.device() != dev)
+      refuse(where, "", "the norm's parameters have another length or device than the rows");
+    const int c = code(t.scalar_type());
+    if (!c || !t.is_contiguous() || (d.dtype && d.dtype != c))
+      refuse(where, "", "the norm's parameters are not contiguous and of one type, bf16, fp16 or fp32");
+    d.dtype = c;
+    return t.data_ptr();
+  };
+  d.weight = parameter(n->weight);
+  d.bias = parameter(n->bias);
+  return &d;
 }
 
 // The device, and where the caller names a stream that stream, for the length of a call: outputs are
@@ -155,7 +169,8 @@ PyObject* enter(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t ldx = matrix(x, w, "x", -1, -1, std::nullopt, std::nullopt), T = x.size(0), H = x.size(1);
     const at::Device dev = x.device();
     if (a[1] == Py_None) refuse(w, "", "a norm is needed");
-    const moe_norm_t* nm = norm(a[1], w, H, dev);
+    moe_norm_t desc;
+    const moe_norm_t* nm = norm(a[1], w, H, dev, desc);
     std::optional<at::ScalarType> type;
     if (a[2] != Py_None) {
       if (!THPDtype_Check(a[2])) refuse(w, "dtype", " is not a torch.dtype");
@@ -188,7 +203,8 @@ PyObject* leave(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Device dev = x.device();
     const at::Tensor& b = tensor(a[1], w, "block");
     const int64_t ldb = matrix(b, w, "block", T, H, std::nullopt, dev);
-    const moe_norm_t *post = norm(a[2], w, H, dev), *next = norm(a[7], w, H, dev);
+    moe_norm_t descs[2];
+    const moe_norm_t *post = norm(a[2], w, H, dev, descs[0]), *next = norm(a[7], w, H, dev, descs[1]);
     const void* gp = nullptr;
     int64_t gld = 0;
     int gstep = 0, gtype = MOE_DT_BF16;

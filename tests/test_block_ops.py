@@ -393,6 +393,56 @@ def test_route_groups_whose_keys_cancel(size):
     assert torch.equal(idx2 // wide * S + idx2 % wide, idx) and torch.equal(w, w2)
 
 
+def test_norm_follows_its_parameters():
+    """Parameters that are replaced, given other storage or written in place are the ones that the next call uses."""
+    g = gen(12)
+    x = rows(3, 64, torch.bfloat16, g)
+    w = torch.nn.Parameter(torch.ones(64, dtype=torch.bfloat16, device="cuda"))
+    old = w.data
+    n = M.Norm("rms", w)
+    one = M.moe_block_enter(x, n)
+    w.data = torch.full((64,), 2.0, dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(M.moe_block_enter(x, n), 2 * one)
+    n.weight = torch.full((64,), 4.0, dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(M.moe_block_enter(x, n), 4 * one)
+    n.weight.fill_(0.5)
+    assert torch.equal(M.moe_block_enter(x, n), one / 2)
+    n.weight, n.bias = None, torch.full((64,), 3.0, device="cuda")
+    assert (M.moe_block_enter(x.float(), n).mean() - 3.0).abs() < 1.0
+    n.bias = None
+    assert torch.equal(M.moe_block_enter(x, n), one)
+    n.weight = w
+    w.data = w.data[:32].clone()
+    refused(1, M.moe_block_enter, x, n)  # another length now
+    w.data = old.float()
+    assert torch.equal(M.moe_block_enter(x, n), one)
+    w.data = torch.ones(128, dtype=torch.bfloat16, device="cuda")[::2]
+    refused(1, M.moe_block_enter, x, n)
+    with pytest.raises(M.MoEError):
+        n.weight = torch.ones((2, 32), device="cuda")
+    del old
+
+
+def test_copies_of_norms_and_routers():
+    """A copy has its own descriptor and outlives what it was copied from."""
+    import copy
+    import gc
+
+    g = gen(13)
+    x, lg = rows(3, 64, torch.bfloat16, g), rows(3, 64, torch.float32, g)
+    n, _ = make_norm("layer", 64, torch.bfloat16, g, off=1.0)
+    r = M.Router("sigmoid", groups=4, top_groups=2, scale=2.5)
+    want, (idx, w) = M.moe_block_enter(x, n), M.moe_route_scored(lg, r, 4)
+    pairs = [(copy.copy(n), copy.copy(r)), (copy.deepcopy(n), copy.deepcopy(r))]
+    del n, r
+    gc.collect()
+    other = [M.Router("softmax", scale=9.0) for _ in range(100)]  # what the first one's memory may hold now
+    for m, q in pairs:
+        assert torch.equal(M.moe_block_enter(x, m), want)
+        assert torch.equal(M.moe_route_scored(lg, q, 4)[0], idx) and torch.equal(M.moe_route_scored(lg, q, 4)[1], w)
+    del other
+
+
 # ------------------------------------------------------------------------------------------ adapters
 @pytest.mark.parametrize("E,groups,tg", [(256, 8, 1), (256, 16, 2), (128, 8, 1), (240, 8, 1), (256, 8, 2)])
 def test_route_few_groups(E, groups, tg):
