@@ -411,8 +411,8 @@ moe_status_t moe_layer_forward_scored(const void* x, const moe_router_t* router,
  * differ, or one is 0).
  * H and N multiples of 8; r a multiple of 8, 8 .. 128; pointers to matrices 16-byte aligned and
  * pitches multiples of 8.
- * Errors: MOE_ERR_INVALID_ARG for sizes outside these, T < 0, R < 0, n < 0, a null or misaligned
- * pointer; MOE_ERR_UNSUPPORTED off sm_103; MOE_ERR_CUDA if the launch fails. */
+ * Errors: MOE_ERR_INVALID_ARG for sizes outside these, T < 0, R < 0, n < 0, tokens without a request
+ * (T > 0, R = 0), a null or misaligned pointer; MOE_ERR_UNSUPPORTED off sm_103; MOE_ERR_CUDA if the launch fails. */
 moe_status_t moe_adapters_add(const void* x, int64_t ldx, const void* base, int64_t ldb, const void* A, const void* B,
                               const float* scale, const int32_t* rank, const int32_t* starts, const int32_t* slot,
                               void* out, int64_t ldo, int T, int R, int n, int r, int H, int N, moe_stream_t stream);

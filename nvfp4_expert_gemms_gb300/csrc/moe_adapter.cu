@@ -568,7 +568,7 @@ cudaError_t launch_rank(const AdapterArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_adapters(const AdapterArgs& a, cudaStream_t s) {
-  if (a.T == 0 || a.R == 0 || a.N == 0) return cudaSuccess;
+  if (a.T == 0) return cudaSuccess;
   if (a.r <= 16) return launch_rank<1>(a, s);
   if (a.r <= 32) return launch_rank<2>(a, s);
   if (a.r <= 64) return launch_rank<4>(a, s);
@@ -587,7 +587,7 @@ extern "C" moe_status_t moe_adapters_add(const void* x, int64_t ldx, const void*
   const auto ok = [](const void* p, int64_t ld, int cols) {
     return p && (uintptr_t)p % 16 == 0 && ld >= cols && ld % 8 == 0;
   };
-  if (T > 0 && (!ok(x, ldx, H) || !ok(base, ldb, N) || !ok(out, ldo, N) || !starts || (R > 0 && !slot)))
+  if (T > 0 && (R < 1 || !ok(x, ldx, H) || !ok(base, ldb, N) || !ok(out, ldo, N) || !starts || !slot))
     return MOE_ERR_INVALID_ARG;
   if (n > 0 && (!ok(A, H, H) || !ok(B, N, N))) return MOE_ERR_INVALID_ARG;
   for (const void* p : {(const void*)scale, (const void*)rank, (const void*)starts, (const void*)slot})

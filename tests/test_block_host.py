@@ -73,3 +73,9 @@ def test_binding_refuses_host_tensors():
         with pytest.raises(M.MoEError) as e:
             call()
         assert e.value.status == 1 and "invalid argument" in str(e.value)
+
+
+def test_adapter_entry_point_refuses_tokens_of_no_request():
+    f = block._f()
+    call = lambda T, R: f.moe_adapters_add(P, 64, P, 64, P, P, None, None, P, P, P, 64, T, R, 1, 8, 64, 64, None)  # noqa: E731
+    assert call(4, 0) == call(1, 0) == 1  # nothing would write them

@@ -741,6 +741,14 @@ def test_adapters_hold_all_bits_of_the_inner_product(lens, r):
     assert torch.equal(got, x[:, 2:3].bfloat16().expand(T, N))
 
 
+def test_adapters_without_requests():
+    x = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")
+    a, b = torch.zeros((1, 8, 64), dtype=torch.bfloat16, device="cuda"), torch.zeros((1, 64, 8), dtype=torch.bfloat16, device="cuda")
+    z = torch.zeros(1, dtype=torch.int32, device="cuda")
+    refused(1, M.moe_adapters_add, x, x, a, b, z, z[:0])  # four tokens of no request: nothing would write them
+    assert M.moe_adapters_add(x[:0], x[:0], a, b, z, z[:0]).shape == (0, 64)
+
+
 # ------------------------------------------------------------------------------------------ together
 def bf16_experts(E, H, I, g):
     wgu = (0.05 * torch.randn((E, 2 * I, H), generator=g, device="cuda")).bfloat16()
