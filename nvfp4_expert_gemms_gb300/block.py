@@ -192,11 +192,12 @@ def moe_layer_forward_scored(x, logits, router: Router, desc, packed, top_k: int
         _refuse(where, f"logits are not a CUDA [{T}, {E}] of bf16, fp16 or fp32 with unit column stride")
     if bias is not None and (bias.shape != (E,) or bias.dtype != torch.float32 or not bias.is_contiguous() or bias.device != x.device):
         _refuse(where, f"bias is not a contiguous fp32 [{E}] on the logits' device")
-    _check(_f().moe_layer_forward_scored(x.data_ptr(), router._ref, logits.data_ptr(), max(logits.stride(0), E) if T <= 1 else
-                                         logits.stride(0), _DT[logits.dtype], None if bias is None else bias.data_ptr(), T,
-                                         C.byref(desc), packed.data_ptr(), top_k, out.data_ptr(), workspace.data_ptr(),
-                                         workspace.numel() * workspace.element_size(),
-                                         torch.cuda.current_stream(x.device).cuda_stream if stream is None else _handle(stream)), where)
+    ld = max(logits.stride(0), E) if T <= 1 else logits.stride(0)
+    with torch.cuda.device(x.device):
+        _check(_f().moe_layer_forward_scored(x.data_ptr(), router._ref, logits.data_ptr(), ld, _DT[logits.dtype],
+                                             None if bias is None else bias.data_ptr(), T, C.byref(desc), packed.data_ptr(), top_k,
+                                             out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                             torch.cuda.current_stream(x.device).cuda_stream if stream is None else _handle(stream)), where)
 
 
 def moe_get_adapter_error(stream=None) -> int:

@@ -17,8 +17,6 @@
 // is memory.
 #include <cooperative_groups.h>
 
-#include <atomic>
-
 #include "moe_adapter.cuh"
 
 namespace cg = cooperative_groups;
@@ -490,8 +488,8 @@ __global__ void __launch_bounds__(Many::threads) adapter_many_kernel(const Adapt
 }
 
 cudaError_t launch_many(const AdapterArgs& a, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(adapter_many_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Many::smem);
-  if (e != cudaSuccess) return e;
+  static SmemOptIn opt_in;
+  if (const cudaError_t e = opt_in(adapter_many_kernel, Many::smem); e != cudaSuccess) return e;
   note_launches(1);
   return launch_pdl(adapter_many_kernel, dim3((unsigned)tile_bound(a, Many::BM)), dim3(Many::threads), Many::smem, s, a);
 }
@@ -499,12 +497,8 @@ cudaError_t launch_many(const AdapterArgs& a, cudaStream_t s) {
 template <int RT, int MT, bool GATHER>
 cudaError_t launch_few(const AdapterArgs& a, int cluster, cudaStream_t s) {
   constexpr int per = 2 * RT * MT * 32 * 16, most = (kWarps + 8) * per;
-  static std::atomic<bool> set{false};
-  if (!set.load(std::memory_order_relaxed)) {
-    const cudaError_t e = cudaFuncSetAttribute(adapter_few_kernel<RT, MT, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (e != cudaSuccess) return e;
-    set.store(true, std::memory_order_relaxed);
-  }
+  static SmemOptIn opt_in;
+  if (const cudaError_t e = opt_in(adapter_few_kernel<RT, MT, GATHER>, most); e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((GATHER ? gather_bound(a) : tile_bound(a, 16 * MT)) * cluster));
   cfg.blockDim = dim3(32 * kWarps);

@@ -499,12 +499,8 @@ cudaError_t launch_adapter_tiles(const AdapterArgs& g, cudaStream_t s) {
                              : tc_make_map(&p.b, bf16, g.B, g.r, brows, (uint64_t)g.r * 2, 64, 128 * p.bps, sw) &&
                                    tc_make_map(&p.y, bf16, g.base, g.N, g.T, (uint64_t)g.ldb * 2, 64, kBM, sw);
   if (!maps || !nmaps) return cudaErrorInvalidValue;
-  static std::atomic<bool> set{false};
-  if (!set.load(std::memory_order_relaxed)) {
-    const cudaError_t e = cudaFuncSetAttribute(adapter_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    set.store(true, std::memory_order_relaxed);
-  }
+  static SmemOptIn opt_in;
+  if (const cudaError_t e = opt_in(adapter_tile_kernel, kSmem); e != cudaSuccess) return e;
   // Blocks of a cluster share a tile, each a part of K, then of N, while the device takes the clusters at once
   // (half a tile over per request; a tenth of the SMs may not form clusters: 37 tiles by four 38 us, by two 25).
   const int64_t likely = (int64_t)g.T / kBM + (g.R < g.T ? g.R : g.T) / 2, room = tc_num_sms() * 9 / 10;

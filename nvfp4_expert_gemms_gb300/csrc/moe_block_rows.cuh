@@ -15,7 +15,6 @@
 // (19.6); rows of 1999 fp16 with padded pitches, two layer norms and a tanh per element, 1237 of them: 11.6 us
 // (3.7; there 109 instructions per element bound it).
 #pragma once
-#include <atomic>
 #include <type_traits>
 
 #include "moe_block.cuh"
@@ -854,13 +853,9 @@ cudaError_t launch_row(const BlockArgs& a, cudaStream_t s) {
 
 template <typename X, typename A, bool LEAVE>
 cudaError_t launch_long(const BlockArgs& a, cudaStream_t s) {
-  static std::atomic<bool> set{false};
+  static SmemOptIn opt_in;
   const auto kernel = block_long_kernel<X, A, LEAVE>;
-  if (!set.load(std::memory_order_relaxed)) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedMost);
-    if (e != cudaSuccess) return e;
-    set.store(true, std::memory_order_relaxed);
-  }
+  if (const cudaError_t e = opt_in(kernel, kSharedMost); e != cudaSuccess) return e;
   const bool keep = a.H <= kSharedMost / 4;
   return launch_pdl(kernel, dim3(a.T), dim3(1024), keep ? a.H * 4 : 0, s, a, keep);
 }
@@ -869,13 +864,9 @@ cudaError_t launch_long(const BlockArgs& a, cudaStream_t s) {
 template <typename X, typename A, typename P, bool LEAVE>
 cudaError_t launch_shared(const BlockArgs& a, cudaStream_t s) {
   if (a.H > kSharedMost / 4) return launch_long<X, A, LEAVE>(a, s);
-  static std::atomic<bool> set{false};
+  static SmemOptIn opt_in;
   const auto kernel = block_shared_kernel<X, A, P, LEAVE>;
-  if (!set.load(std::memory_order_relaxed)) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedMost);
-    if (e != cudaSuccess) return e;
-    set.store(true, std::memory_order_relaxed);
-  }
+  if (const cudaError_t e = opt_in(kernel, kSharedMost); e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(a.T), dim3(kSharedThreads), a.H * 4, s, a);
 }
 
@@ -889,13 +880,16 @@ cudaError_t launch_stream(const BlockArgs& a, cudaStream_t s) {
   if (groups < 1) return launch_shared<X, A, P, LEAVE>(a, s);
   const int smem = factors + groups * 2 * slot;
   const auto kernel = block_stream_kernel<X, A, P, W, N, LEAVE>;
-  static std::atomic<int> fit[2];  // resident blocks per SM of this kernel
-  int per_sm = fit[full_gate].load(std::memory_order_relaxed);
+  static SmemOptIn opt_in;
+  if (const cudaError_t e = opt_in(kernel, most_smem); e != cudaSuccess) return e;
+  static PerDevice fit[2];  // resident blocks per SM of this kernel
+  std::atomic<int>* known;
+  if (const cudaError_t e = fit[full_gate].here(&known); e != cudaSuccess) return e;
+  int per_sm = known ? known->load(std::memory_order_relaxed) : 0;
   if (per_sm == 0) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, 32 * W * groups, smem);
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, 32 * W * groups, smem);
     if (e != cudaSuccess) return e;
-    fit[full_gate].store(per_sm, std::memory_order_relaxed);
+    if (known) known->store(per_sm, std::memory_order_relaxed);
   }
   const int all = (int)(((int64_t)a.T + groups - 1) / groups), most = tc_num_sms() * per_sm;
   return launch_pdl(kernel, dim3(all < most ? all : most), dim3(32 * W * groups), smem, s, a);

@@ -669,11 +669,8 @@ int fp4_row_block() { return kRows; }
 
 template <int MODE>
 static cudaError_t launch_fp4(const Fp4Args& a, int work, cudaStream_t s) {
-  static bool attr = false;
-  if (!attr) {
-    cudaFuncSetAttribute(fp4_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-    attr = true;
-  }
+  static SmemOptIn opt_in;
+  if (const cudaError_t e = opt_in(fp4_kernel<MODE>, (int)kSmem); e != cudaSuccess) return e;
   const int sms = tc_num_sms();
   return launch_pdl(fp4_kernel<MODE>, dim3(work < sms ? work : sms), dim3(Roles<MODE>::kThreads), kSmem, s, a);
 }

@@ -441,12 +441,10 @@ cudaError_t launch_experts_fp8dec(const moe_packed_desc_t& d, const char* packed
   const int E = d.E, H = d.H, I = d.I;
   const size_t R = (size_t)T * k;
   const MatView gu = mat_view(d, packed, 0), dn = mat_view(d, packed, 1);
-  static bool attr = false;
-  if (!attr) {
-    cudaFuncSetAttribute(fp8dec_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-    cudaFuncSetAttribute(fp8dec_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-    attr = true;
-  }
+  static SmemOptIn opt_in[2];
+  cudaError_t e = opt_in[0](fp8dec_kernel<0>, (int)kSmem);
+  if (e == cudaSuccess) e = opt_in[1](fp8dec_kernel<1>, (int)kSmem);
+  if (e != cudaSuccess) return e;
   Fp8Args a;
   memset(&a, 0, sizeof(a));
   a.perm = (const int32_t*)(ws + L.perm);

@@ -763,11 +763,8 @@ cudaError_t launch_one(const TcArgs& args, int grid_x, int grid_y, cudaStream_t 
   constexpr size_t need = TcCfg<FMT, BN>::kSmem;
   // at least 116 KB so that a single CTA (owning all 512 TMEM columns) runs per SM
   constexpr size_t smem = need > 116 * 1024 ? need : 116 * 1024;
-  static bool attr = false;
-  if (!attr) {
-    cudaFuncSetAttribute(tc_expert_gemm_kernel<FMT, MODE, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    attr = true;
-  }
+  static SmemOptIn opt_in;
+  if (const cudaError_t e = opt_in(tc_expert_gemm_kernel<FMT, MODE, BN>, (int)smem); e != cudaSuccess) return e;
   return launch_pdl(tc_expert_gemm_kernel<FMT, MODE, BN>,
                     dim3(grid_x * grid_y < num_sms() ? grid_x * grid_y : num_sms()), dim3(kThreads), smem, s, args);
 }

@@ -384,11 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1) tcw_expert_gemm_kernel(const __gr
 
 template <int MODE>
 cudaError_t launch_tcw(const TcwArgs& args, int items, cudaStream_t s) {
-  static bool attr = false;
-  if (!attr) {
-    cudaFuncSetAttribute(tcw_expert_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-    attr = true;
-  }
+  static SmemOptIn opt_in;
+  if (const cudaError_t e = opt_in(tcw_expert_gemm_kernel<MODE>, (int)kSmem); e != cudaSuccess) return e;
   const int sms = tc_num_sms();
   return launch_pdl(tcw_expert_gemm_kernel<MODE>, dim3(items < sms ? items : sms), dim3(kThreads), kSmem, s, args);
 }

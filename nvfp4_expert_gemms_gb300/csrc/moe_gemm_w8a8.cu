@@ -434,11 +434,8 @@ __global__ void __launch_bounds__(kThreads, 1) w8a8_kernel(const __grid_constant
 
 template <int MODE>
 cudaError_t launch_w8a8(const W8Args& a, int work, cudaStream_t s) {
-  static bool attr = false;
-  if (!attr) {
-    cudaFuncSetAttribute(w8a8_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-    attr = true;
-  }
+  static SmemOptIn opt_in;
+  if (const cudaError_t e = opt_in(w8a8_kernel<MODE>, (int)kSmem); e != cudaSuccess) return e;
   const int sms = tc_num_sms();
   return launch_pdl(w8a8_kernel<MODE>, dim3(work < sms ? work : sms), dim3(kThreads), kSmem, s, a);
 }

@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "../../include/moe_gb300.h"
+#include "moe_device.cuh"
 
 namespace moe {
 
