@@ -224,6 +224,53 @@ def test_offsets_past_32_bits():
     assert torch.equal(x, want)
 
 
+@pytest.mark.parametrize("types", ["bf16/bf16", "f16/f16", "f32/f32", "f32/bf16", "f32/f16"])
+@pytest.mark.parametrize("T,H", [(16384, 264), (12000, 512), (5200, 776), (6000, 1024), (2700, 1032), (3000, 2048), (1500, 2056), (1500, 4096),
+                                 (330, 4104), (400, 8192)])
+def test_many_rows(types, T, H):
+    """Rows that groups of warps walk with the grid's stride, several each: both slots of a group's ring and both of its
+    sums' buffers come round.  Every gate, norm and bias, padded rows, parameters in fp32, out of place and in place."""
+    xt, at = (DT[t] for t in types.split("/"))
+    combos = [("rms", "none", "none", True, True, False, 0, False), ("layer", "channel", "sigmoid", True, True, True, 8, False),
+              ("rms", "token", "sigmoid", True, True, True, 16, True), ("layer", "full", "tanh", True, True, True, 0, False),
+              ("layer", "full", "none", False, True, False, 8, True), ("rms", "full", "sigmoid", True, False, False, 0, False),
+              ("layer", "channel", "none", True, True, False, 0, True), ("layer", "token", "tanh", True, False, True, 24, False)]
+    for i, (kind, gate, act, post, nxt, bias, pad, wide) in enumerate(combos):
+        pt = torch.float32 if wide else at
+        g = gen(7 * T + H + i)
+        x, b = rows(T, H, xt, g, pad, 1.5, 0.2), rows(T, H, at, g, pad, 0.4, -0.1)
+        shape = {"none": None, "channel": (H,), "token": (T, 1), "full": (T, H)}[gate]
+        gt = None if shape is None else torch.randn(shape, generator=g, device="cuda").to(pt)
+        pn, ps = make_norm(kind, H, pt, g, bias=bias) if post else (None, None)
+        nn, ns = make_norm(kind, H, pt, g, bias=bias, off=1.0) if nxt else (None, None)
+        alpha, beta = 0.9, -1.3
+        got = M.moe_block_leave(x, b, post=pn, gate=gt, gate_act=act, alpha=alpha, beta=beta, next=nn)
+        v, e = b.double(), torch.zeros((1, 1), dtype=torch.float64, device="cuda").expand(T, H)
+        if post:
+            v, e = ref_norm(v, e, *ps)
+        if gt is not None:
+            gd = gt.double()
+            f = {"none": gd, "sigmoid": torch.sigmoid(gd), "tanh": torch.tanh(gd)}[act]
+            v, e = v * f, e * f.abs() + 8 * U * (v * f).abs()
+        a32, b32 = float(np.float32(alpha)), float(np.float32(beta))
+        e = abs(b32) * e + 4 * U * ((a32 * x.double()).abs() + (b32 * v).abs())
+        o = a32 * x.double() + b32 * v
+        out, y = got if nxt else (got, None)
+        what = f"{kind} {types} {gate} {act} {T}x{H} pad {pad}"
+        check(out, o, e, "out " + what)
+        if nxt:
+            ry, ey = ref_norm(o, e, *ns)
+            check(y, ry, ey, "y " + what)
+            got = M.moe_block_enter(x, nn, dtype=at)
+            ry, ey = ref_norm(x.double(), torch.zeros_like(o), *ns)
+            check(got, ry, ey, "enter " + what)
+            M.moe_block_leave(x, b, post=pn, gate=gt, gate_act=act, alpha=alpha, beta=beta, next=nn, out=x, y=b)
+            assert torch.equal(x, out) and torch.equal(b, y), "in place " + what
+            M.moe_block_enter(b, nn, out=b)
+            ry, ey = ref_norm(y.double(), torch.zeros_like(o), *ns)
+            check(b, ry, ey, "enter in place " + what)
+
+
 # ------------------------------------------------------------------------------------------ routing
 def ref_route(lg, bias, score, k, groups, top_groups, group_top, renorm, scale):
     """Indices, weights and each row's smallest gap between keys that decide, in fp64."""
