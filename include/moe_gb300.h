@@ -330,8 +330,10 @@ typedef enum { MOE_GATE_LINEAR = 0, MOE_GATE_SIGMOID = 1, MOE_GATE_TANH = 2 } mo
  *   x (dev) x_dtype [T, H] (pitch ldx); y (dev) y_dtype [T, H] (pitch ldy), may be x itself
  *   (same pitch and type) but overlap it in no other way.
  * Types: y_dtype equal to x_dtype, or x_dtype fp32 with any y_dtype.  Any H >= 1, any pitch and
- * any alignment of the element's size (rows that are multiples of 16 bytes and start on 16-byte
- * boundaries take wide loads).  Rows are independent: NaN and infinities stay in their row.
+ * any alignment of the element's size; wide loads where H and every pitch are multiples of 8 and every
+ * tensor of the call, parameters included, starts on a multiple of 8 elements (16 bytes, 32 of fp32);
+ * a gate per token has no such rule.
+ * Rows are independent: NaN and infinities stay in their row.
  * Errors: MOE_ERR_INVALID_ARG for T < 0, H < 1, a pitch below H, a null or misaligned pointer, an
  * unknown kind or type, eps <= 0; MOE_ERR_UNSUPPORTED for other type pairs or off sm_103;
  * MOE_ERR_CUDA if the launch fails.  T = 0 enqueues nothing. */

@@ -2,8 +2,8 @@
 // devices and strides, allocates the outputs that are not given and calls the C ABI.
 //
 // Native because a serving step calls these operators once per layer and token: at one token the
-// kernels take 2-3 us, a ctypes call with its Python checks took 12-18 us of host time (Grace core),
-// this one 4-6 us.  The C functions come as addresses from the library that the package has loaded, so
+// kernels take 1.5 to 3.4 us, a ctypes call with its Python checks took 12-18 us of host time (Grace core),
+// this one 3.1 to 4.3.  The C functions come as addresses from the library that the package has loaded, so
 // nothing is linked to it.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>

@@ -70,22 +70,23 @@ __device__ __forceinline__ uint2 cut_rank(uint2 b, int k, int rk) {
 }
 
 // ---- few tokens per request ------------------------------------------------------------------
-// One tile of up to 16 MT tokens of a request, or (GATHER) 16 of an adapter's, per cluster of blocks.  The blocks' warps share K (each lane's loads of x
-// and A are independent and all issued at once), v's parts are summed warp by warp in shared memory and
-// block by block in a fixed order (each block writes its own into every block's shared memory: one barrier and
-// no remote read to wait for), and the blocks share N.  B and base of a warp's first 32 columns are loaded
+// One tile of up to 16 MT tokens of a request, or (GATHER) 16 of an adapter's, per cluster of blocks.  The blocks' warps
+// share K (each lane's loads of x and A are independent and all issued at once), v's parts are summed warp by warp in
+// shared memory and block by block in a fixed order (each block writes its own into every block's shared memory: one
+// barrier and no remote read to wait for), and the blocks share N.  B and base of a warp's first 32 columns are loaded
 // before the sums meet.
 //
-// One token, 2048 -> 2048 at rank 16: 3.6 us on eight blocks, 6.2 on one (a launch alone takes 1.6); of it 0.7 the
-// requests, 0.8 x and A, 0.9 the sums, 0.4 the second product.  64 requests at rank 32: 6.0 us on four blocks each,
-// 9.2 on one.  4001 tokens of 37 requests at rank 16, 2048 -> 1536: 12.1 us in tiles of 32, two blocks each (12.6 in
-// tiles of 16), against 6.0 by HBM.  Latency bounds it: 324 blocks are one wave, 21% of the warps, and the L1 is
-// 32% busy, the L2 17%, issue slots 38% (sixteen warps per block in place of eight: 3% slower in tiles of 16, up to
-// 1.7 times at rank 32; 2% faster in tiles of 32, but 11% slower past one wave).
+// Times in a CUDA graph, as those of the other rules below.  One token, 2048 -> 2048 at rank 16: 3.2 us on eight blocks,
+// 6.3 on one (a launch alone takes 1.6); by a clock trace with two terms of v 0.7 of it are the requests, 0.8 x and A,
+// 0.9 the sums, 0.4 the second product.  64 requests at rank 32: 5.9 us on four blocks each, 8.4 on one.  4001 tokens of
+// 37 requests at rank 16, 2048 -> 1536: 12.1 us in tiles of 32, two blocks each (13.2 in tiles of 16), against 6.0 by HBM.
+// Latency bounds it: 324 blocks are one wave, 23% of the warps, issue slots 38% (with two terms of v the L1 was 32% busy,
+// the L2 17%, and sixteen warps per block in place of eight 3% slower in tiles of 16, up to 1.7 times at rank 32; 2%
+// faster in tiles of 32, but 11% slower past one wave).
 //
 // Tiles of 32 (ranks up to 16) read A and B half as often: they are for batches whose tiles of 16 leave no four
-// blocks to a tile.  2048 -> 2048: 5000 ragged tokens 20.3 us against 24.3, 7000 22.0 against 28.2, 4096 even ones
-// 14.1 against 15.7, 1024 even ones 6.1 against 5.6.  At rank 32 they take 18.4 us against 17.5 at 4096 tokens.
+// blocks to a tile.  2048 -> 2048: 5000 ragged tokens 20.2 us against 25.4, 7000 21.6 against 27.6, 4096 of 16 even
+// requests 13.9 against 15.5, 1024 of them 6.7 against 5.3.  At rank 32 they take 19.6 us against 17.6 at 4096 tokens.
 template <int RT, int MT, bool GATHER>
 __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kernel(const AdapterArgs a) {
   extern __shared__ __align__(128) unsigned char few_smem[];
@@ -305,8 +306,9 @@ __global__ void __launch_bounds__(32 * kWarps, RT <= 4 ? 2 : 1) adapter_few_kern
 //            rows, four pieces) hit all banks once
 //   N stage  kNC columns of base ([BM][kNC], same placement) and kNC rows of B, row order (n-tile, lane
 //            group), 32 bytes each (16 lanes of an 8-byte load: four rows, all banks once)
-// Tiles of 32 tokens, four to six blocks per SM: 16384 tokens, 2048 -> 2048 at rank 16 in 40.2 us (30.4 by
-// HBM; tiles of 64 39.6), 100 ragged requests of them 39.8 (tiles of 64 60.3: more empty rows).
+// Tiles of 32 tokens, four to six blocks per SM: 16384 tokens, 2048 -> 2048 at rank 16 in 42.0 us (30.4 by
+// HBM), 100 ragged requests of them 41.7 (with two terms of v 40.2 and 39.8, in tiles of 64 39.6 and 60.3: more empty
+// rows).
 constexpr int kKC = 128, kNC = 128;
 
 struct Many {
@@ -524,24 +526,27 @@ cudaError_t launch_rank(const AdapterArgs& a, cudaStream_t s) {
   // Tiles, with requests of mean > the tile's height half a tile over each.
   const int64_t likely16 = a.T / 16 + requests / 2, likely32 = a.T / 32 + requests / 2;
   // Blocks of a cluster share a tile as long as the grid fits the device at once.  By eight only up to 80% of it
-  // (32 tiles at rank 16: 4.9 us by eight, 4.1 by four; at rank 128, a block per SM, 16.1 and 12.3), but for ranks
-  // 33 to 64, where the work outweighs it (32 tiles: 8.5 and 10.0).
+  // (512 tokens of one request, 32 tiles, at rank 16: 4.6 us by eight, 4.2 by four; at rank 128, a block per SM, 25.8 and
+  // 12.3), but for ranks 33 to 64, where the work outweighs it (32 requests of 16 tokens at rank 64: 8.7 and 10.3, though
+  // one request 8.6 and 8.0).
   const auto blocks = [&](int64_t tiles) {
     return 80 * tiles <= room * (RT == 4 ? 10 : 8) ? 8 : 4 * tiles <= room ? 4 : 2 * tiles <= room ? 2 : 1;
   };
   if constexpr (RT == 1) {
-    // Long requests past one wave of tiles of 32: 16384 tokens, 2048 -> 2048, the ring 40.2 us, those tiles 44.1
-    // (tcgen05 tiles 40.2, 59.4 ragged); 10000 ragged 34.8 and 38.4; 7000, within a wave, 26.6 and 22.0.
+    // Long requests past one wave of tiles of 32: 16384 tokens, 2048 -> 2048, the ring 42.0 us, those tiles 43.5
+    // (tcgen05 tiles 40.0, 60.9 ragged); 10000 ragged 36.2 and 38.5; 7000, within a wave, 27.6 and 21.6.
     if (mean >= 32 && likely32 > room) return launch_many(a, s);
     if (mean > 16 && 4 * likely16 > room) return launch_few<1, 2, false>(a, blocks(likely32), s);
   } else if (mean >= 16) {
     // The tcgen05 tiles or the kernel for few, by their waves over the SMs (a part of one where clusters share a
     // tile), a wave of the tiles in units of the other's: 1.95, 0.85 and 1.1 at ranks up to 32, 64 and 128.  Times
-    // with the tiles and without, 2048 -> 2048: rank 32, 4096 tokens of 4 requests 19.5 and 17.5 us, 6000 of 40 25.2 and
-    // 30.1; rank 64, 2048 of 32 29.7 and 19.7, 4096 of 64 25.8 and 32.6, 16384 of 300 87 and 115, of 1000 197 and 161;
-    // rank 128, 2048 of 32 44.1 and 41.0, of 128 42 and 74, 8192 of 128 45 and 147, 16384 of 300 120 and 286.  The tiles'
-    // fixed cost wants some work against it: 2048 of 100, 256 -> 256, rank 64, 21.4 and 6.2, 3000 of 20, 1024 -> 1024
-    // 18.6 and 14.9; 16384 of 16, 512 -> 512, rank 32, 15.8 and 21.0, rank 64 16.2 and 35.7.
+    // with the tiles and without, 2048 -> 2048, ragged requests: rank 32, 4096 tokens of 4 requests 19.2 and 17.5 us, 6000
+    // of 40 24.6 and 30.3; rank 64, 2048 of 32 33.4 and 19.0, 4096 of 64 25.3 and 31.9, 16384 of 300 88 and 118, of 1000
+    // 200 and 165; rank 128, 2048 of 32 50.5 and 40.2, of 128 43.7 and 72.7, 8192 of 128 45.8 and 143, 16384 of 300 123 and
+    // 280.  Even requests may fill the tiles otherwise than guessed (6000 of 40, rank 32, 41.3 and 30.6; 2048 of 32, rank
+    // 128, 29.2 and 40.2).  The tiles' fixed cost wants some work against it: 2048 of 100, 256 -> 256, rank 64, 20.5 and
+    // 6.4; 16384 of 16, 512 -> 512, rank 32, 15.3 and 20.9, rank 64 15.9 and 35.6 (3000 of 20, 1024 -> 1024, near the
+    // bound, 14.4 and 16.3 ragged, 25.9 and 16.0 even).
     const int64_t sms = tc_num_sms(), likely128 = a.T / 128 + (mean >= 128 ? requests / 2 : requests);
     const double full = likely128 > sms ? (double)likely128 / sms : 1.;
     const double tiles = (RT == 2 ? 1.95 : RT == 4 ? 0.85 : 1.1) *
@@ -551,8 +556,8 @@ cudaError_t launch_rank(const AdapterArgs& a, cudaStream_t s) {
     if (tiles < few && work >= (RT == 2 ? 1.0e5 : 1.5e5) && adapter_tiles_fit(a)) return launch_adapter_tiles(a, s);
   }
   // Short requests that share adapters, enough of them to pay for the longer search (0.4 to 1 us): one token each,
-  // 2048 -> 2048, 256 requests over 16 adapters: rank 16 6.9 us against 8.9, rank 64 10.2 against 22.2, rank 128 15.0
-  // against 58.0; over 64 adapters: rank 16 9.5 against 8.9, rank 32 11.2 against 12.4, rank 64 20.4 against 27.4.
+  // 2048 -> 2048, 256 requests over 16 adapters: rank 16 6.7 us against 9.0, rank 64 10.8 against 26.0, rank 128 14.9
+  // against 61.1; over 64 adapters: rank 16 9.1 against 8.9, rank 32 10.4 against 13.4, rank 64 20.0 against 29.4.
   if (a.R >= 32 && a.R <= kGatherRequests && a.n <= kGatherSlots && a.T <= 8 * (int64_t)a.R &&
       (int64_t)a.R * (RT < 4 ? RT : 4) >= 8 * (int64_t)a.n)
     return launch_few<RT, 1, true>(a, blocks(gather_bound(a)), s);

@@ -12,15 +12,16 @@
 // 128-column buffers (the first one lies where v's sums were), so the epilogue of one column block runs
 // under the MMAs of the next.  A 5-D tensor map deals B's rows so that a lane's accumulator fragment is 16
 // consecutive output columns: out is then written in whole lines straight from registers (natural order,
-// with a way through shared memory, where N or out's rows do not allow it: 55.0 us for 41.3).
+// with a way through shared memory, where N or out's rows do not allow it: 55.0 us for 41.3, with two terms of v).
 // Where there are few tiles, the blocks of a cluster share one: each takes a part of K, the parts of v are
 // summed in block order through distributed shared memory, and each takes a part of N.
 //
-// 16384 tokens of 16 requests, 2048 -> 2048: 41.3 us at rank 64, 49.6 at 128, against 31.4 and 32.6 by HBM
-// (register MMAs in tiles of 64: 76 and 133).  By a clock trace at rank 64 the first product takes 16 us, the
-// second 17.  With two K stages the first took 20: 19 without A's copies, 12 without x's, 19 without the MMAs.  So
-// the copies pace it, at about 2.6 ns per 128-byte row and SM, and neither the MMAs nor HBM alone.
-// 4096 tokens at rank 64: 22.0 us with four blocks per tile, 31.4 with one.
+// 16384 tokens of 16 requests, 2048 -> 2048: 40.8 us at rank 64, 50.8 at 128, against 31.4 and 32.6 by HBM (in a CUDA
+// graph; with two terms of v, in shared memory, 40.2 and 49.3; register MMAs in tiles of 64: 76 and 133).  By a clock
+// trace at rank 64, of the form with two terms, the first product takes 16 us, the second 17.  With two K stages the
+// first took 20: 19 without A's copies, 12 without x's, 19 without the MMAs.  So the copies pace it, at about 2.6 ns per
+// 128-byte row and SM, and neither the MMAs nor HBM alone.
+// 4096 tokens at rank 64: 21.7 us with four blocks per tile (31.4 with one, and two terms).
 //
 // Every wait gives up after about a second (moe_tc.cuh); the block then waits, with the same limit, for
 // its own copies and MMAs, frees its tensor memory, leaves its rows unfinished and records a timeout that
