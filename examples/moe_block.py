@@ -4,7 +4,7 @@ Each block: norm -> router (sigmoid scores, balance bias, expert groups) -> quan
 low-rank adapter of each request added -> norm, sigmoid gate per token and residual scale back into an
 fp32 stream, with the following block's norm in the same pass.  Weights are random.
 
-    python examples/moe_block.py [--format nvfp4_w4a16] [--hidden 2048] [--experts 64]
+    python examples/moe_block.py [--format nvfp4_w4a16] [--hidden 2048] [--experts 64] [--few]
 """
 import argparse
 import os
@@ -16,12 +16,21 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import nvfp4_expert_gemms_gb300 as M  # noqa: E402
 
 
-def make_block(fmt, E, H, I, k, g):
+def fp8_weight(N, K, g):
+    """A random weight in the FP8 block format: E4M3 codes and a scale per 128 x 128 block."""
+    w = torch.randn((N, K), generator=g, device="cuda")
+    scale = torch.full(((N + 127) // 128, (K + 127) // 128), 1.0 / (100.0 * K ** 0.5), device="cuda")
+    return M.Fp8Weight((100.0 * w).clamp(-448.0, 448.0).to(torch.float8_e4m3fn), scale)
+
+
+def make_block(fmt, E, H, I, k, g, few=False):
     rnd = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
     layer = M.MoELayer(fmt, (rnd(E, 2 * I, H) / H ** 0.5).bfloat16(), (rnd(E, H, I) / I ** 0.5).bfloat16())
     router = M.Router("sigmoid", groups=8, top_groups=4, group_top=2, scale=2.5)
     norm = lambda: M.Norm("rms", (1.0 + 0.1 * rnd(H)).bfloat16())  # noqa: E731
-    return M.MoEBlock(layer, (rnd(E, H) / H ** 0.5).bfloat16(), router, k, norm(), norm(), 0.02 * rnd(E), beta=0.5)
+    # --few: decode steps through one call per layer, and an always-active FP8 expert beside the routed ones
+    extra = {"few_tokens": 32, "shared": (fp8_weight(2 * I, H, g), fp8_weight(H, I, g))} if few else {}
+    return M.MoEBlock(layer, (rnd(E, H) / H ** 0.5).bfloat16(), router, k, norm(), norm(), 0.02 * rnd(E), beta=0.5, **extra)
 
 
 def make_adapters(n, r, H, g):
@@ -54,9 +63,10 @@ def main(argv=None):
     p.add_argument("--experts", type=int, default=64)
     p.add_argument("--top-k", type=int, default=8)
     p.add_argument("--steps", type=int, default=3)
+    p.add_argument("--few", action="store_true", help="decode through moe_layer_few, with an always-active FP8 expert")
     a = p.parse_args(argv)
     g = torch.Generator(device="cuda").manual_seed(0)
-    blocks = [make_block(a.format, a.experts, a.hidden, a.inner, a.top_k, g) for _ in range(2)]
+    blocks = [make_block(a.format, a.experts, a.hidden, a.inner, a.top_k, g, a.few) for _ in range(2)]
     adapters = [make_adapters(4, 16, a.hidden, g) for _ in range(2)]
     slots = [0, -1, 3, 1, 1]  # the requests' adapters; the second has none
     lengths = [37, 5, 300, 1, 128]
@@ -68,8 +78,9 @@ def main(argv=None):
         x, h = step(blocks, adapters, [1] * len(slots), slots, x)
         print(f"decode {i}: rms {x.square().mean().sqrt().item():.3f}, next input {tuple(h.shape)} {h.dtype}")
     for b in blocks:
-        if M.moe_get_device_error(b.layer.workspace):
-            raise RuntimeError("device error flag set")
+        for w in (b.layer.workspace, b.layer.few_workspace):
+            if w is not None and M.moe_get_device_error(w):
+                raise RuntimeError("device error flag set")
     if M.moe_get_adapter_error():
         raise RuntimeError("adapter error flag set")
     if not torch.isfinite(x).all():

@@ -425,6 +425,65 @@ moe_status_t moe_adapters_add(const void* x, int64_t ldx, const void* base, int6
  * synchronisation fails. */
 moe_status_t moe_get_adapter_error(moe_stream_t stream, int32_t* code);
 
+/* ---- the layer for a few tokens, and products in the FP8 block format ------------------------- */
+
+/* The layer as a decode step runs it, router product included, for T <= MOE_FEW_MAX_TOKENS tokens in two kernels:
+ *   logits[t, e] = sum over h of x[t, h] w_router[e, h], the exact sum rounded once to fp32
+ *   experts and weights of each token: moe_router_t's rule on those logits (bias f32 [E] or NULL)
+ *   out[t] = sum_j w_tj Wd_e (silu(Wg_e x_t) * (Wu_e x_t)),   e = the j-th expert of t
+ * with the weights as stored (any format) and x, h and the sums in fp32: nothing is rounded to fewer bits
+ * but out, once; the formats that quantize activations at run time (W4A4, W8A8) do not here, where the weights' bytes
+ * set the pace.  Results do not depend on the order in which blocks run.
+ *   x (dev) bf16 [T, H] (pitch ldx); w_router (dev) w_dtype [E, H] (pitch ldw); packed (dev) as moe_pack_experts
+ *   writes it (of a buffer that holds images, only the canonical tensors are read); out (dev) bf16 [T, H] (pitch ldo), may be
+ *   x (same pitch), no other overlap; topk_idx (dev) i32 [T, top_k] and topk_w (dev) f32 [T, top_k], or NULL;
+ *   workspace (dev) >= moe_layer_few_workspace_size bytes, 256-byte aligned, any contents, one call at a time.
+ * Pitches are multiples of 8; x, w_router and out 16-byte, packed 256-byte aligned.  A row's NaN and infinities stay in
+ * the tokens that read them.  Bounded waits report through moe_get_device_error(workspace), as the layer's do.
+ * Errors: those of moe_route_scored for the router, E and top_k; MOE_ERR_INVALID_ARG for T outside
+ * 0 .. MOE_FEW_MAX_TOKENS, a bad desc, pitch or pointer; MOE_ERR_WORKSPACE; MOE_ERR_UNSUPPORTED off sm_103;
+ * MOE_ERR_CUDA if a launch fails.  T = 0 enqueues nothing. */
+#define MOE_FEW_MAX_TOKENS 32
+moe_status_t moe_layer_few_workspace_size(const moe_packed_desc_t* desc, int T, int top_k, size_t* bytes);
+moe_status_t moe_layer_few(const void* x, int64_t ldx, const void* w_router, int64_t ldw, int w_dtype,
+                           const moe_router_t* router, const float* bias, int T, const moe_packed_desc_t* desc,
+                           const void* packed, int top_k, void* out, int64_t ldo, int32_t* topk_idx, float* topk_w,
+                           void* workspace, size_t ws_bytes, moe_stream_t stream);
+
+/* Activations into the FP8 block format (clef-omni-fp8, "What was quantized" and "Recipe": the tile rule on a 1x128
+ * group): per group of 128 consecutive elements of a row (the last may be shorter)
+ *   s = 448 / max(amax, 1e-12),  code = E4M3(v * s),  scale_inv = 1 / s,   each one fp32 operation,
+ * codes to the nearest, ties to even, saturating at 448.  NaN does not count for amax and its code is NaN; a group
+ * with an infinity stands for NaN.
+ *   x (dev) x_dtype [T, K] (pitch ldx, any alignment of its element); codes (dev) u8 [T, K] (pitch ldq); scale_inv (dev)
+ *   f32 [T, ceil(K / 128)].  Wide accesses where K is a multiple of 128, x's rows start on multiples of 16 bytes and codes'
+ *   on multiples of 8.
+ * Errors: MOE_ERR_INVALID_ARG for T < 0, K < 1, a pitch below K, an unknown type, a null or misaligned pointer;
+ * MOE_ERR_UNSUPPORTED off sm_103; MOE_ERR_CUDA if the launch fails.  T = 0 enqueues nothing. */
+moe_status_t moe_fp8_quantize(const void* x, int64_t ldx, int x_dtype, uint8_t* codes, int64_t ldq, float* scale_inv,
+                              int T, int K, moe_stream_t stream);
+
+/* A product with weights in that format, for what stands beside the routed experts (an always-active expert,
+ * projections):
+ *   p[t, n] = sum over groups g of x_scale_inv[t, g] w_scale_inv[n / 128, g] sum over k in g of qx[t, k] qw[n, k]
+ *   out[t]  = act(p[t]) + base[t]     rounded once to out_dtype;  act: the identity, or (MOE_ACT_SILU_MUL)
+ *             silu(p[t, f]) * p[t, N/2 + f] for f < N/2 (rows 0 .. N/2-1 of w are gates, the rest ups)
+ * All sums in fp32.
+ *   x (dev): x_dtype bf16, fp16 or fp32 [T, K] (pitch ldx), which the call quantizes as moe_fp8_quantize does; or
+ *   MOE_DT_E4M3 codes (16-byte aligned, ldx a multiple of 16) with x_scale_inv (dev) f32 [T, ceil(K / 128)].
+ *   w (dev) E4M3 [N, K], contiguous, 16-byte aligned; w_scale_inv (dev) f32 [ceil(N / 128), ceil(K / 128)].
+ *   base (dev) out_dtype [T, n] or NULL; out (dev) out_dtype [T, n], n = N or N/2; out may be base (same pitch), no
+ *   other overlap.  K is a multiple of 16; T, N, pitches and out's alignment are free.
+ *   workspace (dev): moe_fp8_linear_workspace_size bytes (0 for codes), 256-byte aligned, any contents.
+ * Errors: MOE_ERR_INVALID_ARG for sizes, types, pitches or pointers outside these (N odd with MOE_ACT_SILU_MUL);
+ * MOE_ERR_WORKSPACE; MOE_ERR_UNSUPPORTED off sm_103; MOE_ERR_CUDA if a launch fails.  T = 0 enqueues nothing. */
+#define MOE_DT_E4M3 4
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SILU_MUL = 1 } moe_act_t;
+moe_status_t moe_fp8_linear_workspace_size(int x_dtype, int T, int K, int N, int act, size_t* bytes);
+moe_status_t moe_fp8_linear(const void* x, int64_t ldx, int x_dtype, const float* x_scale_inv, const uint8_t* w,
+                            const float* w_scale_inv, int act, const void* base, int64_t ldb, void* out, int64_t ldo,
+                            int out_dtype, int T, int K, int N, void* workspace, size_t ws_bytes, moe_stream_t stream);
+
 /* ---- measurement hooks ------------------------------------------------------------------ */
 
 /* Total number of CUDA kernels this library has enqueued in the calling process (all threads,

@@ -33,12 +33,15 @@ EXPORTS = ("moe_packed_size", "moe_pack_experts", "moe_workspace_size", "moe_lay
            "moe_debug_route", "moe_debug_dequant", "moe_debug_quant_act", "moe_kernel_launch_count",
            "moe_time_next_step", "moe_layer_forward_static_act", "moe_calibrate_act_scales",
            "moe_debug_quant_act_static", "moe_debug_quant_act_fp8", "moe_debug_wait_timeout", "moe_block_enter",
-           "moe_block_leave", "moe_route_scored", "moe_layer_forward_scored", "moe_adapters_add", "moe_get_adapter_error")
+           "moe_block_leave", "moe_route_scored", "moe_layer_forward_scored", "moe_adapters_add", "moe_get_adapter_error",
+           "moe_layer_few_workspace_size", "moe_layer_few", "moe_fp8_quantize", "moe_fp8_linear_workspace_size",
+           "moe_fp8_linear")
 
 # The operators around the experts live in block.py (which needs torch at import) and are names of
 # this package too.
 _BLOCK = ("Norm", "Router", "MoEBlock", "moe_block_enter", "moe_block_leave", "moe_route_scored",
-          "moe_layer_forward_scored", "moe_adapters_add", "moe_get_adapter_error")
+          "moe_layer_forward_scored", "moe_adapters_add", "moe_get_adapter_error", "moe_layer_few",
+          "moe_layer_few_workspace_size", "Fp8Weight", "moe_fp8_quantize", "moe_fp8_linear")
 
 
 def __getattr__(name):
@@ -311,7 +314,18 @@ class MoELayer:
         self.desc = moe_packed_size(fmt, E, H, N2 // 2)
         self.packed = torch.empty(self.desc.bytes, dtype=torch.uint8, device=w_gate_up.device)
         moe_pack_experts(self.desc, w_gate_up.contiguous(), w_down.contiguous(), self.packed, stream)
-        self.workspace = None
+        self.workspace = self.few_workspace = None
+
+    def ensure_few_workspace(self, T: int, top_k: int):
+        """The workspace of moe_layer_few, apart from the layer's own."""
+        import torch
+
+        from .block import moe_layer_few_workspace_size
+
+        n = moe_layer_few_workspace_size(self.desc, T, top_k)
+        if self.few_workspace is None or self.few_workspace.numel() < n:
+            self.few_workspace = torch.empty(n, dtype=torch.uint8, device=self.packed.device)
+        return self.few_workspace
 
     def ensure_workspace(self, T: int, top_k: int, host_io: bool = False):
         import torch

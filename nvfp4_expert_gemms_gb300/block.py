@@ -22,8 +22,10 @@ _DT = {torch.bfloat16: 1, torch.float16: 2, torch.float32: 3}
 _KIND = {"rms": 1, "layer": 2}
 _GATE = {"none": 0, "linear": 0, "sigmoid": 1, "tanh": 2}
 _SCORE = {"softmax": 1, "sigmoid": 2}
+_ACT = {"none": 0, "silu_mul": 1}
 
 INVALID_ARG, UNSUPPORTED = 1, 2
+FEW_MAX_TOKENS = 32
 
 
 class _NormDesc(C.Structure):
@@ -62,6 +64,11 @@ def _f():
         L.moe_layer_forward_scored.argtypes = [P, P, P, Q, I, P, I, C.POINTER(PackedDesc), P, I, P, P, C.c_size_t, P]
         L.moe_get_adapter_error.argtypes = [P, C.POINTER(C.c_int32)]
         L.moe_adapters_add.argtypes = [P, Q, P, Q, P, P, P, P, P, P, P, Q] + [I] * 6 + [P]
+        L.moe_layer_few_workspace_size.argtypes = [C.POINTER(PackedDesc), I, I, C.POINTER(C.c_size_t)]
+        L.moe_layer_few.argtypes = [P, Q, P, Q, I, P, P, I, P, P, I, P, Q, P, P, P, C.c_size_t, P]
+        L.moe_fp8_quantize.argtypes = [P, Q, I, P, Q, P, I, I, P]
+        L.moe_fp8_linear_workspace_size.argtypes = [I] * 5 + [C.POINTER(C.c_size_t)]
+        L.moe_fp8_linear.argtypes = [P, Q, I, P, P, P, I, P, Q, P, Q, I, I, I, I, P, C.c_size_t, P]
         _fns = L
     return _fns
 
@@ -79,7 +86,8 @@ def _native():
         spec.loader.exec_module(ext)
         addr = lambda f: C.cast(f, C.c_void_p).value  # noqa: E731
         ext.init(_refuse, addr(L.moe_block_enter), addr(L.moe_block_leave), addr(L.moe_route_scored),
-                 addr(L.moe_adapters_add))
+                 addr(L.moe_adapters_add), addr(L.moe_layer_few), addr(L.moe_fp8_quantize), addr(L.moe_fp8_linear),
+                 addr(L.moe_fp8_linear_workspace_size))
         _ext = ext
     return _ext
 
@@ -180,6 +188,57 @@ def moe_adapters_add(x, base, a, b, starts, slot, scale=None, rank=None, out=Non
                                         None if stream is None else _handle(stream))
 
 
+def moe_layer_few_workspace_size(desc, T: int, top_k: int) -> int:
+    """Bytes of workspace of moe_layer_few for up to T tokens."""
+    n = C.c_size_t()
+    _check(_f().moe_layer_few_workspace_size(C.byref(desc), T, top_k, C.byref(n)), "moe_layer_few_workspace_size")
+    return n.value
+
+
+def moe_layer_few(x, w_router, router: Router, desc, packed, top_k: int, workspace, bias=None, out=None, topk_idx=None,
+                  topk_w=None, stream=None):
+    """A whole layer for up to 32 tokens, router product included: x bf16 [T, H], w_router [E, H] (bf16, fp16 or fp32),
+    packed experts of any format, bias fp32 [E] or None.  Returns out bf16 [T, H] (which may be x); topk_idx (int32)
+    and topk_w (fp32) [T, top_k] are written where given.  workspace: moe_layer_few_workspace_size bytes."""
+    return (_ext or _native()).few(x, w_router, router._ref, C.addressof(desc), packed, top_k, workspace, bias, out, topk_idx, topk_w,
+                                   None if stream is None else _handle(stream))
+
+
+class Fp8Weight:
+    """A weight [N, K] in the FP8 block format: E4M3 codes (torch.float8_e4m3fn or their bytes) and one fp32 scale_inv per
+    128 x 128 block, [ceil(N / 128), ceil(K / 128)]; K a multiple of 16."""
+
+    def __init__(self, codes, scale_inv):
+        where = "Fp8Weight"
+        if not isinstance(codes, torch.Tensor) or codes.dim() != 2 or codes.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            _refuse(where, "codes are not a 2-D tensor of E4M3 codes")
+        N, K = codes.shape
+        if not codes.is_cuda or not codes.is_contiguous() or K % 16 or K < 16 or N < 1 or codes.data_ptr() % 16:
+            _refuse(where, "codes are not a contiguous, 16-byte aligned CUDA [N, K] with K a multiple of 16")
+        if (not isinstance(scale_inv, torch.Tensor) or scale_inv.shape != ((N + 127) // 128, (K + 127) // 128)
+                or scale_inv.dtype != torch.float32 or scale_inv.device != codes.device or not scale_inv.is_contiguous()):
+            _refuse(where, "scale_inv is not a contiguous fp32 [ceil(N / 128), ceil(K / 128)] on the codes' device")
+        self.codes, self.scale_inv = codes, scale_inv
+
+
+def moe_fp8_quantize(x, codes=None, scale_inv=None, stream=None):
+    """(codes [T, K] in torch.float8_e4m3fn, scale_inv fp32 [T, ceil(K / 128)]) of x [T, K] (bf16, fp16 or fp32): one
+    scale per 128 consecutive elements of a row."""
+    return (_ext or _native()).quantize(x, codes, scale_inv, None if stream is None else _handle(stream))
+
+
+def moe_fp8_linear(x, weight: Fp8Weight, x_scale=None, act="none", base=None, out=None, dtype=None, stream=None):
+    """out = act(x weight^T) + base, x quantized per 128 elements of a row in the call, or given as moe_fp8_quantize's
+    codes with x_scale.  act "silu_mul": the weight's first half of rows are gates, the rest ups, and out is
+    silu(gate) * up.  base, of out's type and shape, may be out.  dtype: out's type, by default base's, else x's (bf16 for
+    codes)."""
+    a = _ACT.get(act)
+    if a is None:
+        _refuse("moe_fp8_linear", f"unknown act {act!r}")
+    return (_ext or _native()).linear(x, x_scale, weight.codes, weight.scale_inv, a, base, out, dtype,
+                                      None if stream is None else _handle(stream))
+
+
 def moe_layer_forward_scored(x, logits, router: Router, desc, packed, top_k: int, out, workspace, bias=None, stream=None):
     """moe_layer_forward with the experts chosen and weighted by `router`: x and out bf16 [T, H] contiguous,
     logits [T, E] of any of the three types, bias fp32 [E] or None."""
@@ -213,12 +272,19 @@ class MoEBlock:
     adapters, and the way back into the residual stream.
 
         h   = pre(x);  logits = h @ w_router.T
-        m   = experts(h, router(logits))  [+ adapters(h)]
+        m   = experts(h, router(logits))  [+ shared(h)]  [+ adapters(h)]
         out = alpha x + beta g(gate) post(m);  y = next(out)   (the following block's h)
+
+    shared: None, or the (gate/up, down) Fp8Weight pair of an always-active expert, whose output is added to m.
+    few_tokens: up to so many tokens (32 at most) go through moe_layer_few, which computes the logits in fp32 (h @
+    w_router.T has w_router's type) and does not round or quantize the activations on the way.
     """
 
     def __init__(self, layer: MoELayer, w_router, router: Router, top_k: int, pre: Norm, post: Norm = None,
-                 router_bias=None, alpha=1.0, beta=1.0):
+                 router_bias=None, alpha=1.0, beta=1.0, shared=None, few_tokens=0):
+        if not 0 <= few_tokens <= FEW_MAX_TOKENS:
+            _refuse("MoEBlock", f"few_tokens is not in 0 .. {FEW_MAX_TOKENS}")
+        self.shared, self.few_tokens = shared, few_tokens
         self.layer, self.w_router, self.router, self.top_k = layer, w_router, router, top_k
         self.pre, self.post, self.router_bias, self.alpha, self.beta = pre, post, router_bias, alpha, beta
 
@@ -229,11 +295,19 @@ class MoEBlock:
         layer's workspace serves one stream at a time)."""
         if h is None:
             h = moe_block_enter(x, self.pre, dtype=torch.bfloat16)
-        logits = h @ self.w_router.t()
-        m = torch.empty_like(h)
-        ws = self.layer.ensure_workspace(int(h.shape[0]), self.top_k)
-        moe_layer_forward_scored(h, logits, self.router, self.layer.desc, self.layer.packed, self.top_k, m, ws,
-                                 bias=self.router_bias)
+        T = int(h.shape[0])
+        if T <= self.few_tokens:
+            m = moe_layer_few(h, self.w_router, self.router, self.layer.desc, self.layer.packed, self.top_k,
+                              self.layer.ensure_few_workspace(self.few_tokens, self.top_k), bias=self.router_bias)
+        else:
+            logits = h @ self.w_router.t()
+            m = torch.empty_like(h)
+            ws = self.layer.ensure_workspace(T, self.top_k)
+            moe_layer_forward_scored(h, logits, self.router, self.layer.desc, self.layer.packed, self.top_k, m, ws,
+                                     bias=self.router_bias)
+        if self.shared is not None:
+            gate_up, down = self.shared
+            m = moe_fp8_linear(moe_fp8_linear(h, gate_up, act="silu_mul"), down, base=m, out=m)
         if adapters is not None:
             moe_adapters_add(h, m, out=m, **adapters)
         return moe_block_leave(x, m, post=self.post, gate=gate, gate_act=gate_act, alpha=self.alpha, beta=self.beta,

@@ -25,6 +25,10 @@ decltype(&moe_block_enter) g_enter;
 decltype(&moe_block_leave) g_leave;
 decltype(&moe_route_scored) g_route;
 decltype(&moe_adapters_add) g_adapters;
+decltype(&moe_layer_few) g_few;
+decltype(&moe_fp8_quantize) g_quantize;
+decltype(&moe_fp8_linear) g_linear;
+decltype(&moe_fp8_linear_workspace_size) g_linear_size;
 PyObject* g_refuse;  // block._refuse(where, why, status): raises MoEError
 PyObject* g_key;     // "_key"
 
@@ -328,9 +332,163 @@ PyObject* adapters(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// init(refuse, enter, leave, route, adapters): the refusal and the C functions' addresses
+// few(x, w_router, router address, desc address, packed, top_k, workspace, bias, out, topk_idx, topk_w, stream)
+PyObject* few(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arity(n, 12)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const char* w = "moe_layer_few";
+    const moe_router_t* r = (const moe_router_t*)PyLong_AsVoidPtr(a[2]);
+    const moe_packed_desc_t* d = (const moe_packed_desc_t*)PyLong_AsVoidPtr(a[3]);
+    if (!r || !d) throw Refused();
+    const at::Tensor& x = tensor(a[0], w, "x");
+    const int64_t ldx = matrix(x, w, "x", -1, d->H, at::kBFloat16, std::nullopt), T = x.size(0);
+    const at::Device dev = x.device();
+    if (T > MOE_FEW_MAX_TOKENS) refuse(w, "x", " has more rows than the call takes (32)");
+    const at::Tensor& wr = tensor(a[1], w, "w_router");
+    const int64_t ldw = matrix(wr, w, "w_router", d->E, d->H, std::nullopt, dev);
+    const at::Tensor &packed = tensor(a[4], w, "packed"), &ws = tensor(a[6], w, "workspace");
+    if (packed.device() != dev || !packed.is_contiguous() || (uint64_t)packed.nbytes() < d->bytes)
+      refuse(w, "packed", " is smaller than the descriptor says, not contiguous, or on another device");
+    if (ws.device() != dev || !ws.is_contiguous()) refuse(w, "workspace", " is not contiguous or on another device");
+    const int k = whole(a[5]);
+    const float* bias = (const float*)vector(a[7], w, "bias", d->E, at::kFloat, dev);
+    void* top[2] = {nullptr, nullptr};
+    for (int i = 0; i < 2; ++i) {
+      if (a[9 + i] == Py_None) continue;
+      const char* name = i ? "topk_w" : "topk_idx";
+      const at::Tensor& o = tensor(a[9 + i], w, name);
+      if (o.dim() != 2 || o.size(0) != T || o.size(1) != k || o.scalar_type() != (i ? at::kFloat : at::kInt) || o.device() != dev ||
+          !o.is_contiguous())
+        refuse(w, name, " is not a contiguous [T, top_k] of its type on x's device");
+      top[i] = o.data_ptr();
+    }
+    const Place place(x, a[11]);
+    at::Tensor out;
+    int64_t ldo = d->H;
+    if (a[8] == Py_None) {
+      out = fresh(T, d->H, at::kBFloat16, dev);
+    } else {
+      out = tensor(a[8], w, "out");
+      ldo = matrix(out, w, "out", T, d->H, at::kBFloat16, dev);
+    }
+    check(g_few(x.data_ptr(), pitch(x, ldx), wr.data_ptr(), pitch(wr, ldw), code(wr.scalar_type()), r, bias, (int)T, d,
+                packed.data_ptr(), k, out.data_ptr(), pitch(out, ldo), (int32_t*)top[0], (float*)top[1], ws.data_ptr(),
+                ws.nbytes(), (moe_stream_t)place.stream),
+          w);
+    return THPVariable_Wrap(std::move(out));
+  });
+}
+
+bool is_codes(const at::Tensor& t) { return t.scalar_type() == at::kFloat8_e4m3fn || t.scalar_type() == at::kByte; }
+
+// A [rows, cols] CUDA tensor of E4M3 codes with unit column stride; its row pitch.
+int64_t codes(const at::Tensor& t, const char* where, const char* name, int64_t rows, int64_t cols, std::optional<at::Device> dev) {
+  if (t.dim() != 2 || !t.is_cuda() || !is_codes(t)) refuse(where, name, " is not a 2-D CUDA tensor of E4M3 codes");
+  if ((rows >= 0 && t.size(0) != rows) || (cols >= 0 && t.size(1) != cols)) refuse(where, name, " has another shape");
+  if (t.size(0) > INT32_MAX || t.size(1) > INT32_MAX) refuse(where, name, " has over 2^31 - 1 rows or columns");
+  if (dev && t.device() != *dev) refuse(where, name, " is on another device");
+  if ((t.stride(1) != 1 && t.size(1) > 1) || (t.size(0) > 1 && t.stride(0) < t.size(1)))
+    refuse(where, name, " needs unit column stride and rows that do not overlap");
+  return pitch(t, t.stride(0));
+}
+
+// Address of a contiguous fp32 [rows, cols].
+float* scales(PyObject* o, const char* where, const char* name, int64_t rows, int64_t cols, at::Device dev) {
+  const at::Tensor& t = tensor(o, where, name);
+  if (t.dim() != 2 || t.size(0) != rows || t.size(1) != cols || t.scalar_type() != at::kFloat || t.device() != dev || !t.is_contiguous())
+    refuse(where, name, " is not a contiguous fp32 tensor of a scale per block");
+  return (float*)t.data_ptr();
+}
+
+// quantize(x, codes, scale_inv, stream)
+PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arity(n, 4)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const char* w = "moe_fp8_quantize";
+    const at::Tensor& x = tensor(a[0], w, "x");
+    const int64_t ldx = matrix(x, w, "x", -1, -1, std::nullopt, std::nullopt), T = x.size(0), K = x.size(1), G = (K + 127) / 128;
+    const at::Device dev = x.device();
+    const Place place(x, a[3]);
+    at::Tensor q, s;
+    int64_t ldq = K;
+    if (a[1] == Py_None) {
+      q = fresh(T, K, at::kFloat8_e4m3fn, dev);
+    } else {
+      q = tensor(a[1], w, "codes");
+      ldq = codes(q, w, "codes", T, K, dev);
+    }
+    if (a[2] == Py_None) {
+      s = fresh(T, G, at::kFloat, dev);
+    } else {
+      s = tensor(a[2], w, "scale_inv");
+      scales(a[2], w, "scale_inv", T, G, dev);
+    }
+    check(g_quantize(x.data_ptr(), ldx, code(x.scalar_type()), (uint8_t*)q.data_ptr(), ldq, (float*)s.data_ptr(), (int)T, (int)K,
+                     (moe_stream_t)place.stream),
+          w);
+    PyObject *pq = THPVariable_Wrap(std::move(q)), *ps = THPVariable_Wrap(std::move(s));
+    PyObject* both = pq && ps ? PyTuple_Pack(2, pq, ps) : nullptr;
+    Py_XDECREF(pq);
+    Py_XDECREF(ps);
+    return both;
+  });
+}
+
+// linear(x, x_scale, weight codes, weight scales, act, base, out, dtype, stream)
+PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arity(n, 9)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const char* w = "moe_fp8_linear";
+    const at::Tensor &x = tensor(a[0], w, "x"), &wt = tensor(a[2], w, "weight");
+    const bool coded = a[1] != Py_None;
+    const int64_t ldx = coded ? codes(x, w, "x", -1, -1, std::nullopt) : matrix(x, w, "x", -1, -1, std::nullopt, std::nullopt);
+    const int64_t T = x.size(0), K = x.size(1), N = wt.dim() == 2 ? wt.size(0) : 0, G = (K + 127) / 128;
+    const at::Device dev = x.device();
+    if (codes(wt, w, "weight", -1, K, dev) != K) refuse(w, "weight", " is not contiguous");
+    const float* wsc = scales(a[3], w, "the weight's scale_inv", (N + 127) / 128, G, dev);
+    const float* xsc = coded ? scales(a[1], w, "x_scale", T, G, dev) : nullptr;
+    const int act = whole(a[4]);
+    if (act == MOE_ACT_SILU_MUL && N % 2) refuse(w, "weight", " has an odd number of rows: no gates and ups");
+    const int64_t cols = act == MOE_ACT_SILU_MUL ? N / 2 : N;
+    std::optional<at::ScalarType> type;
+    if (a[7] != Py_None) {
+      if (!THPDtype_Check(a[7])) refuse(w, "dtype", " is not a torch.dtype");
+      type = ((THPDtype*)a[7])->scalar_type;
+      if (!code(*type)) refuse(w, "dtype", " is not bf16, fp16 or fp32");
+    }
+    const Place place(x, a[8]);
+    at::Tensor out;
+    int64_t ldo = cols, ldb = cols;
+    if (a[6] != Py_None) {
+      out = tensor(a[6], w, "out");
+      ldo = matrix(out, w, "out", T, cols, type, dev);
+    }
+    const void* base = nullptr;
+    if (a[5] != Py_None) {
+      const at::Tensor& b = tensor(a[5], w, "base");
+      if (out.defined()) type = out.scalar_type();
+      ldb = matrix(b, w, "base", T, cols, type, dev);
+      type = b.scalar_type();
+      base = b.data_ptr();
+    }
+    if (!out.defined()) out = fresh(T, cols, type.value_or(coded ? at::kBFloat16 : x.scalar_type()), dev);
+    const int xt = coded ? MOE_DT_E4M3 : code(x.scalar_type());
+    size_t bytes = 0;
+    check(g_linear_size(xt, (int)T, (int)K, (int)N, act, &bytes), w);
+    at::Tensor ws;
+    if (bytes) ws = at::Tensor(at::detail::empty_cuda({(int64_t)bytes}, at::kByte, dev, std::nullopt));
+    check(g_linear(x.data_ptr(), ldx, xt, xsc, (const uint8_t*)wt.data_ptr(), wsc, act, base, ldb, out.data_ptr(), ldo,
+                   code(out.scalar_type()), (int)T, (int)K, (int)N, bytes ? ws.data_ptr() : nullptr, bytes,
+                   (moe_stream_t)place.stream),
+          w);
+    return THPVariable_Wrap(std::move(out));
+  });
+}
+
+// init(refuse, enter, leave, route, adapters, few, quantize, linear, linear's workspace size): the refusal and the C
+// functions' addresses
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!arity(n, 5)) return nullptr;
+  if (!arity(n, 9)) return nullptr;
   Py_INCREF(a[0]);
   g_refuse = a[0];
   g_key = PyUnicode_InternFromString("_key");
@@ -338,6 +496,10 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_leave = (decltype(g_leave))PyLong_AsVoidPtr(a[2]);
   g_route = (decltype(g_route))PyLong_AsVoidPtr(a[3]);
   g_adapters = (decltype(g_adapters))PyLong_AsVoidPtr(a[4]);
+  g_few = (decltype(g_few))PyLong_AsVoidPtr(a[5]);
+  g_quantize = (decltype(g_quantize))PyLong_AsVoidPtr(a[6]);
+  g_linear = (decltype(g_linear))PyLong_AsVoidPtr(a[7]);
+  g_linear_size = (decltype(g_linear_size))PyLong_AsVoidPtr(a[8]);
   if (PyErr_Occurred()) return nullptr;
   Py_RETURN_NONE;
 }
@@ -347,6 +509,9 @@ PyMethodDef g_methods[] = {{"init", (PyCFunction)(void*)init, METH_FASTCALL, nul
                            {"leave", (PyCFunction)(void*)leave, METH_FASTCALL, nullptr},
                            {"route", (PyCFunction)(void*)route, METH_FASTCALL, nullptr},
                            {"adapters", (PyCFunction)(void*)adapters, METH_FASTCALL, nullptr},
+                           {"few", (PyCFunction)(void*)few, METH_FASTCALL, nullptr},
+                           {"quantize", (PyCFunction)(void*)quantize, METH_FASTCALL, nullptr},
+                           {"linear", (PyCFunction)(void*)linear, METH_FASTCALL, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_block_ext", nullptr, -1, g_methods};
 

@@ -87,6 +87,8 @@ static bool desc_ok(const moe_packed_desc_t* d) {
          d->I % 128 == 0;
 }
 
+bool packed_desc_ok(const moe_packed_desc_t* d) { return desc_ok(d); }
+
 static bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 // The kernels are built for sm_103a only; refuse other devices before launching anything.

@@ -92,6 +92,8 @@ WsLayout route_layout(int E, int T, int k);
 // MOE_OK on an sm_103 device (the only target the kernels are built for), else
 // MOE_ERR_UNSUPPORTED (or MOE_ERR_CUDA if the device cannot be queried).
 moe_status_t device_ok();
+// The descriptor's own sizes are in range.
+bool packed_desc_ok(const moe_packed_desc_t* d);
 
 // ---- launches (each returns cudaGetLastError() after enqueueing) -------------------------
 // Work folded into the first routing launch: zero the h row maxima and (optionally) record the
