@@ -31,26 +31,76 @@ struct Pair {
 constexpr int kRouterThreads = 256;
 constexpr int kRouterTokens = 4;  // tokens per pass over an expert's row
 
-// logits[t, e] = sum over h of x[t, h] w[e, h], one block per expert.  The sum is carried in pairs, so that it is the
-// exact sum rounded once (but for one case in some 2^20): which experts a token gets must not hang on the order of a
-// sum.
-__global__ void __launch_bounds__(kRouterThreads) few_router_kernel(const FewArgs a) {
+// Eight elements of the router's row, as fp32.
+__device__ __forceinline__ void load_router8(const void* base, int dt, int64_t at, float (&w)[8]) {
+  if (dt == MOE_DT_F32) {
+    const float4 a = ((const float4*)((const float*)base + at))[0], b = ((const float4*)((const float*)base + at))[1];
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    return;
+  }
+  const uint4 u = *(const uint4*)((const uint16_t*)base + at);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = dt == MOE_DT_F16 ? to_f32(((const __half*)&u)[i]) : to_f32(((const __nv_bfloat16*)&u)[i]);
+}
+
+// Blocks below E: logits[t, e] = sum over h of x[t, h] w[e, h], one block per expert.  The sum is carried in pairs, so
+// that it is the exact sum rounded once (but for one case in some 2^20): which experts a token gets must not hang on the
+// order of a sum.  Blocks from E on: a token's row scaled into fp16 for the experts.  Block 0 zeroes the counters.
+__global__ void __launch_bounds__(kRouterThreads) few_router_kernel(const FewArgs a, int zero_words) {
   __shared__ Pair part[kRouterThreads / 32][kRouterTokens];
+  __shared__ uint32_t s_max[kRouterThreads / 32];
   const int e = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H = a.d.H;
   pdl_wait();
   pdl_trigger();
-  if (e == 0 && threadIdx.x == 0) a.status[0] = 0;
+  if (e == 0)
+    for (int i = threadIdx.x; i < zero_words; i += kRouterThreads) a.status[i] = 0;
+  if (e >= a.d.E) {
+    const int t = e - a.d.E;
+    uint32_t m = 0;
+    for (int i = threadIdx.x; i < H / 8; i += kRouterThreads) {
+      const uint4 u = *(const uint4*)(a.x + t * a.ldx + 8 * i);
+      m = __vmaxu2(m, __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu), __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu)));
+    }
+    m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+    if (lane == 0) s_max[warp] = m;
+    __syncthreads();
+    m = 0;
+#pragma unroll
+    for (int w = 0; w < kRouterThreads / 32; ++w) m = max(m, s_max[w]);
+    const float scale = row_scale(m << 16);
+    if (threadIdx.x == 0) a.xinv[t] = row_scale_inv(m << 16);
+    for (int i = threadIdx.x; i < H / 8; i += kRouterThreads) {
+      const uint4 u = *(const uint4*)(a.x + t * a.ldx + 8 * i);
+      const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+      __half2 o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        o[j] = __floats2half2_rn(__uint_as_float(v[j] << 16) * scale, __uint_as_float(v[j] & 0xFFFF0000u) * scale);
+      *(uint4*)(a.xs + (size_t)t * H + 8 * i) = *(const uint4*)o;
+    }
+    return;
+  }
   for (int t0 = 0; t0 < a.T; t0 += kRouterTokens) {
     const int nt = min(kRouterTokens, a.T - t0);
     Pair acc[kRouterTokens];
-    for (int i = threadIdx.x; i < H; i += kRouterThreads) {
-      const float w = load_any(a.wr, a.w_dtype, e * a.ldw + i);
+    for (int i = 8 * threadIdx.x; i < H; i += 8 * kRouterThreads) {
+      float w[8];
+      load_router8(a.wr, a.w_dtype, e * a.ldw + i, w);
 #pragma unroll
       for (int t = 0; t < kRouterTokens; ++t)
-        if (t < nt) acc[t].add_product(__bfloat162float(a.x[(t0 + t) * a.ldx + i]), w);
+        if (t < nt) {
+          const uint4 u = *(const uint4*)(a.x + (t0 + t) * a.ldx + i);
+          const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc[t].add_product(__uint_as_float(v[j] << 16), w[2 * j]);
+            acc[t].add_product(__uint_as_float(v[j] & 0xFFFF0000u), w[2 * j + 1]);
+          }
+        }
     }
 #pragma unroll
     for (int t = 0; t < kRouterTokens; ++t) {
+      if (t >= nt) break;
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) {
         Pair o;
@@ -70,69 +120,6 @@ __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(const FewArg
   }
 }
 
-// One weight, dequantized: element (n, k) of expert e's gate/up (which = 0) or down matrix.
-__device__ float weight_at(const FewArgs& a, int which, int e, int n, int k) {
-  const int N = which ? a.d.H : 2 * a.d.I, K = which ? a.d.I : a.d.H;
-  const char* A = a.packed + a.d.offset[which ? MOE_T_D_A : MOE_T_GU_A];
-  const char* B = a.packed + a.d.offset[which ? MOE_T_D_B : MOE_T_GU_B];
-  const size_t at = ((size_t)e * N + n) * K + k;
-  switch (a.d.fmt) {
-    case MOE_FMT_BF16:
-      return bf16_to_f32(((const uint16_t*)A)[at]);
-    case MOE_FMT_FP8_B128_W8A16:
-    case MOE_FMT_FP8_B128_W8A8:
-      return e4m3_to_f32(((const uint8_t*)A)[at]) * ((const float*)B)[((size_t)e * (N / 128) + n / 128) * (K / 128) + k / 128];
-    case MOE_FMT_INT4_G128_W4A16: {
-      const uint32_t w = ((const uint32_t*)A)[((size_t)e * (K / 8) + k / 8) * N + n];
-      return ((int)((w >> (4 * (k % 8))) & 15u) - 8) * __half2float(((const __half*)B)[((size_t)e * (K / 128) + k / 128) * N + n]);
-    }
-    default: {
-      const uint8_t c = ((const uint8_t*)A)[at / 2];
-      const float gs = ((const float*)(a.packed + a.d.offset[which ? MOE_T_D_GS : MOE_T_GU_GS]))[e];
-      return e2m1_to_f32(k & 1 ? c >> 4 : c & 15) * e4m3_to_f32(((const uint8_t*)B)[at / 16]) / gs;
-    }
-  }
-}
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  return v;
-}
-
-// One warp per (slot, feature).
-__global__ void few_gate_up_kernel(const FewArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  const int f = blockIdx.x * 8 + (threadIdx.x >> 5), r = blockIdx.y, lane = threadIdx.x & 31;
-  if (f >= a.d.I) return;
-  const int e = a.idx[r];
-  float g = 0.f, u = 0.f;
-  for (int k = lane; k < a.d.H; k += 32) {
-    const float xv = __bfloat162float(a.x[(r / a.k) * a.ldx + k]);
-    g = fmaf(weight_at(a, 0, e, f, k), xv, g);
-    u = fmaf(weight_at(a, 0, e, a.d.I + f, k), xv, u);
-  }
-  g = warp_sum(g);
-  u = warp_sum(u);
-  if (lane == 0) a.h[(size_t)r * a.d.I + f] = g / (1.f + expf(-g)) * u;
-}
-
-// One warp per (token, feature).
-__global__ void few_down_kernel(const FewArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  const int n = blockIdx.x * 8 + (threadIdx.x >> 5), t = blockIdx.y, lane = threadIdx.x & 31;
-  float y = 0.f;
-  for (int j = 0; j < a.k; ++j) {
-    const int r = t * a.k + j, e = a.idx[r];
-    float s = 0.f;
-    for (int k = lane; k < a.d.I; k += 32) s = fmaf(weight_at(a, 1, e, n, k), a.h[(size_t)r * a.d.I + k], s);
-    y = fmaf(a.wt[r], warp_sum(s), y);
-  }
-  if (lane == 0) a.out[t * a.ldo + n] = __float2bfloat16_rn(y);
-}
-
 }  // namespace
 
 FewLayout few_layout(const moe_packed_desc_t& d, int T, int k) {
@@ -143,23 +130,25 @@ FewLayout few_layout(const moe_packed_desc_t& d, int T, int k) {
     cur += (bytes + 255) / 256 * 256;
     return o;
   };
-  const size_t R = (size_t)T * k;
+  const size_t R = (size_t)T * k, active = R < (size_t)d.E ? R : (size_t)d.E;
   L.status = take(256);
-  L.idx = take(4 * R);
-  L.wt = take(4 * R);
+  L.done = take(4 * active);
+  L.tile = take(4 * (size_t)(d.H / 16));
+  L.hmax = take(4 * R);
+  L.zero_end = cur;
+  L.xinv = take(4 * (size_t)T);
   L.logits = take(4 * (size_t)T * d.E);
+  L.xs = take(few_scales_x(d.fmt) ? 2 * (size_t)T * d.H : 0);
   L.h = take(4 * R * d.I);
+  L.y = take(4 * R * (size_t)d.H);
   L.total = cur;
   return L;
 }
 
-cudaError_t launch_few(const FewArgs& a, const ScoreArgs& r, int32_t* idx, float* wt, cudaStream_t s) {
-  note_launches(3);
-  cudaError_t e = launch_pdl(few_router_kernel, dim3(a.d.E), dim3(kRouterThreads), 0, s, a);
-  if (e == cudaSuccess) e = launch_route_scored(r, a.T, a.d.E, a.k, idx, wt, s);
-  if (e == cudaSuccess) e = launch_pdl(few_gate_up_kernel, dim3((a.d.I + 7) / 8, a.T * a.k), dim3(256), 0, s, a);
-  if (e == cudaSuccess) e = launch_pdl(few_down_kernel, dim3(a.d.H / 8, a.T), dim3(256), 0, s, a);
-  return e;
+cudaError_t launch_few_router(const FewArgs& a, size_t zero_bytes, cudaStream_t s) {
+  note_launches(1);
+  const int grid = a.d.E + (few_scales_x(a.d.fmt) ? a.T : 0);
+  return launch_pdl(few_router_kernel, dim3(grid), dim3(kRouterThreads), 0, s, a, (int)(zero_bytes / 4));
 }
 
 }  // namespace moe
@@ -185,6 +174,7 @@ extern "C" moe_status_t moe_layer_few(const void* x, int64_t ldx, const void* w_
   if ((uintptr_t)x % 16 || (uintptr_t)w_router % 16 || (uintptr_t)out % 16 || (uintptr_t)packed % 256 ||
       (uintptr_t)workspace % 256 || (uintptr_t)bias % 4 || (uintptr_t)topk_idx % 4 || (uintptr_t)topk_w % 4)
     return MOE_ERR_INVALID_ARG;
+  if (H > kFewWidth || desc->I > kFewWidth) return MOE_ERR_UNSUPPORTED;
   const FewLayout L = few_layout(*desc, T, top_k);
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
   const moe_status_t dv = device_ok();
@@ -203,13 +193,19 @@ extern "C" moe_status_t moe_layer_few(const void* x, int64_t ldx, const void* w_
   a.ldo = ldo;
   a.T = T;
   a.k = top_k;
-  a.logits = (float*)(ws + L.logits);
-  int32_t* idx = topk_idx ? topk_idx : (int32_t*)(ws + L.idx);
-  float* wt = topk_w ? topk_w : (float*)(ws + L.wt);
-  a.idx = idx;
-  a.wt = wt;
-  a.h = (float*)(ws + L.h);
+  a.topk_idx = topk_idx;
+  a.topk_w = topk_w;
   a.status = (int*)(ws + L.status);
-  const ScoreArgs r = {*router, a.logits, E, MOE_DT_F32, bias};
-  return launch_few(a, r, idx, wt, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  a.done = (int*)(ws + L.done);
+  a.tile = (int*)(ws + L.tile);
+  a.hmax = (unsigned*)(ws + L.hmax);
+  a.xinv = (float*)(ws + L.xinv);
+  a.logits = (float*)(ws + L.logits);
+  a.xs = (__half*)(ws + L.xs);
+  a.h = (float*)(ws + L.h);
+  a.y = (float*)(ws + L.y);
+  a.router = {*router, a.logits, E, MOE_DT_F32, bias};
+  cudaError_t e = launch_few_router(a, L.zero_end, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = launch_few_experts(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

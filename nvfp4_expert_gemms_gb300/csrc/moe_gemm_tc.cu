@@ -793,6 +793,15 @@ bool tc_make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint6
                  uint32_t b0, uint32_t b1, CUtensorMapSwizzle sw) {
   return make_map(m, dt, base, d0, d1, pitch, b0, b1, sw);
 }
+bool tc_make_map_nd(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank, const uint64_t* dims,
+                    const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle sw) {
+  auto fn = encode_fn();
+  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  return fn && rank <= 5 &&
+         fn(m, dt, rank, const_cast<void*>(base), (const cuuint64_t*)dims, (const cuuint64_t*)strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 int tc_num_sms() { return num_sms(); }
 bool tc_act_map(CUtensorMap* m, const void* base, uint64_t R, int K, int bn) { return act_map(m, base, R, K, bn); }
 

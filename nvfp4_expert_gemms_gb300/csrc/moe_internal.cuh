@@ -219,6 +219,9 @@ void note_launches(int n);
 int tc_row_block(int fmt, int T, int k, int E);
 bool tc_make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t d0, uint64_t d1, uint64_t pitch,
                  uint32_t b0, uint32_t b1, CUtensorMapSwizzle sw);
+// The same of any rank up to 5: extents in elements, strides (of dimensions 1 and up) in bytes; zeros outside.
+bool tc_make_map_nd(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank, const uint64_t* dims,
+                    const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle sw);
 int tc_num_sms();
 // Activation rows [R, K] bf16 as a 3-D map ([K/64 atoms][R rows][64]) whose box brings bn rows x
 // 128 K, both 128-byte swizzle atoms, in one copy.
