@@ -441,8 +441,8 @@ moe_status_t moe_get_adapter_error(moe_stream_t stream, int32_t* code);
  * Pitches are multiples of 8; x, w_router and out 16-byte, packed 256-byte aligned.  A row's NaN and infinities stay in
  * the tokens that read them.  Bounded waits report through moe_get_device_error(workspace), as the layer's do.
  * Errors: those of moe_route_scored for the router, E and top_k; MOE_ERR_INVALID_ARG for T outside
- * 0 .. MOE_FEW_MAX_TOKENS, a bad desc, pitch or pointer; MOE_ERR_WORKSPACE; MOE_ERR_UNSUPPORTED for H or I over
- * 16384 or off sm_103; MOE_ERR_CUDA if a launch fails.  T = 0 enqueues nothing. */
+ * 0 .. MOE_FEW_MAX_TOKENS, a bad desc, pitch or pointer; MOE_ERR_WORKSPACE; MOE_ERR_UNSUPPORTED off sm_103;
+ * MOE_ERR_CUDA if a launch fails.  T = 0 enqueues nothing. */
 #define MOE_FEW_MAX_TOKENS 32
 moe_status_t moe_layer_few_workspace_size(const moe_packed_desc_t* desc, int T, int top_k, size_t* bytes);
 moe_status_t moe_layer_few(const void* x, int64_t ldx, const void* w_router, int64_t ldw, int w_dtype,

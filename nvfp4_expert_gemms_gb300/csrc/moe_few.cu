@@ -1,4 +1,4 @@
-// A whole mixture-of-experts layer for a few tokens (moe_layer_few): argument checks and the router's product.
+// A whole mixture-of-experts layer for a few tokens (moe_layer_few): argument checks, the router's product and its choice.
 #include "moe_few.cuh"
 #include "moe_formats.cuh"
 
@@ -6,59 +6,118 @@ namespace moe {
 
 namespace {
 
-// A sum kept as an unevaluated pair of fp32 numbers, hi + lo: adding v loses nothing of hi + v (the rounding error of
-// a sum is itself a number that fp32 holds, found by subtracting what was added), and lo collects what hi lost.
-struct Pair {
-  float hi = 0.f, lo = 0.f;
-  __device__ __forceinline__ void add(float v) {
-    const float s = __fadd_rn(hi, v), b = __fsub_rn(s, hi);
-    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(v, b)));
+constexpr int kCluster = 8;          // blocks per token
+constexpr int kAhead = 4;            // pieces a lane loads before it multiplies them
+constexpr int kRouterWarps = 16, kRouterThreads = 32 * kRouterWarps;
+
+// Two sums at once, each kept as an unevaluated pair of fp32 numbers, hi + lo.  Adding p loses nothing: with s the rounded
+// hi + p and b = s - hi, what rounding left out is itself a number that fp32 holds, (hi - (s - b)) + (p - b), and lo collects
+// it.  A product of bf16 and a 16-bit number is such a p, which fma computes on the way; of an fp32 number it is the
+// rounded product, whose own error lo takes as well.
+struct Pairs {
+  float2 hi = {0.f, 0.f}, lo = {0.f, 0.f};
+  static __device__ __forceinline__ uint64_t bits(float2 v) { return *(const uint64_t*)&v; }
+  static __device__ __forceinline__ float2 add(float2 a, float2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+    return *(const float2*)&r;
+  }
+  static __device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+    return *(const float2*)&r;
+  }
+  static __device__ __forceinline__ float2 sub(float2 a, float2 b) { return fma(b, make_float2(-1.f, -1.f), a); }
+  static __device__ __forceinline__ float2 neg(float2 a) { return make_float2(-a.x, -a.y); }
+  __device__ __forceinline__ void add_product(float2 x, float2 w) {
+    const float2 s = fma(x, w, hi), b = sub(s, hi);
+    lo = add(lo, add(sub(hi, sub(s, b)), fma(x, w, neg(b))));
     hi = s;
   }
-  __device__ __forceinline__ void add_product(float a, float b) {
-    const float p = __fmul_rn(a, b);
-    lo = __fadd_rn(lo, __fmaf_rn(a, b, -p));  // 0 where both are bf16
-    add(p);
+  __device__ __forceinline__ void add_wide_product(float2 x, float2 w) {
+    const float2 p = fma(x, w, make_float2(0.f, 0.f)), s = add(hi, p), b = sub(s, hi);
+    lo = add(add(lo, fma(x, w, neg(p))), add(sub(hi, sub(s, b)), sub(p, b)));
+    hi = s;
   }
-  __device__ __forceinline__ void add(const Pair& o) {
-    lo = __fadd_rn(lo, o.lo);
-    add(o.hi);
-  }
-  // the sum rounded once; past fp32's range lo is not a number and hi alone counts
-  __device__ __forceinline__ float rounded() const { return isfinite(hi) ? __fadd_rn(hi, lo) : hi; }
 };
-
-constexpr int kRouterThreads = 256;
-constexpr int kRouterTokens = 4;  // tokens per pass over an expert's row
-
-// Eight elements of the router's row, as fp32.
-__device__ __forceinline__ void load_router8(const void* base, int dt, int64_t at, float (&w)[8]) {
-  if (dt == MOE_DT_F32) {
-    const float4 a = ((const float4*)((const float*)base + at))[0], b = ((const float4*)((const float*)base + at))[1];
-    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-    return;
-  }
-  const uint4 u = *(const uint4*)((const uint16_t*)base + at);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = dt == MOE_DT_F16 ? to_f32(((const __half*)&u)[i]) : to_f32(((const __nv_bfloat16*)&u)[i]);
+__device__ __forceinline__ void add_pair(float& hi, float& lo, float ohi, float olo) {
+  const float s = __fadd_rn(hi, ohi), b = __fsub_rn(s, hi);
+  lo = __fadd_rn(__fadd_rn(lo, olo), __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(ohi, b)));
+  hi = s;
 }
 
-// Blocks below E: logits[t, e] = sum over h of x[t, h] w[e, h], one block per expert.  The sum is carried in pairs, so
-// that it is the exact sum rounded once (but for one case in some 2^20): which experts a token gets must not hang on the
-// order of a sum.  Blocks from E on: a token's row scaled into fp16 for the experts.  Block 0 zeroes the counters.
-__global__ void __launch_bounds__(kRouterThreads) few_router_kernel(const FewArgs a, int zero_words) {
-  __shared__ Pair part[kRouterThreads / 32][kRouterTokens];
-  __shared__ uint32_t s_max[kRouterThreads / 32];
-  const int e = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H = a.d.H;
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Eight bf16 or fp16 elements as fp32.
+__device__ __forceinline__ void unpack8(const uint4& u, bool f16, float2 (&w)[4]) {
+  const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = f16 ? __half22float2(*(const __half2*)&v[i]) : make_float2(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xFFFF0000u));
+}
+
+// A cluster of eight blocks per token: its logits, its experts and its row scaled into fp16.
+//   logits[t, e] = sum over h of x[t, h] w[e, h], a warp per expert.  The sum is carried in pairs, so that it is the exact sum
+//   rounded once (but for one case in some 2^20): which experts a token gets must not hang on the order of a sum.
+// Eight blocks of sixteen warps per token because one token's products (E H of them, seven operations each for two) would
+// take one SM several microseconds.  Past fp32's range lo is not a number and hi alone counts.  Block 0 zeroes the counters.
+template <int VT>
+__global__ void __launch_bounds__(kRouterThreads, 1) few_router_kernel(const __grid_constant__ FewArgs a, const ScoreGeom geom, int zero_words) {
+  __shared__ ScoreScratch scratch;
+  __shared__ uint32_t s_max[kRouterWarps];
+  const int t = blockIdx.x / kCluster, rank = blockIdx.x % kCluster, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H = a.d.H, E = a.d.E;
+  const __nv_bfloat16* x = a.x + t * a.ldx;
   pdl_wait();
   pdl_trigger();
-  if (e == 0)
+  if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < zero_words; i += kRouterThreads) a.status[i] = 0;
-  if (e >= a.d.E) {
-    const int t = e - a.d.E;
+  for (int e = rank * kRouterWarps + warp; e < E; e += kCluster * kRouterWarps) {
+    Pairs sum;
+    for (int i0 = 8 * lane; i0 < H; i0 += 256 * kAhead) {  // a lane's pieces of eight, the loads of kAhead of them first
+      uint4 u[kAhead], w[2 * kAhead];
+#pragma unroll
+      for (int n = 0; n < kAhead; ++n) {
+        const int i = i0 + 256 * n;
+        if (i >= H) break;
+        u[n] = *(const uint4*)(x + i);
+        if (a.w_dtype == MOE_DT_F32) {
+          const uint4* p = (const uint4*)((const float*)a.wr + e * a.ldw + i);
+          w[2 * n] = p[0], w[2 * n + 1] = p[1];
+        } else {
+          w[2 * n] = *(const uint4*)((const uint16_t*)a.wr + e * a.ldw + i);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < kAhead; ++n) {
+        if (i0 + 256 * n >= H) break;
+        float2 xv[4], wv[4];
+        unpack8(u[n], false, xv);
+        if (a.w_dtype == MOE_DT_F32) {
+          const float2* p = (const float2*)(w + 2 * n);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum.add_wide_product(xv[j], p[j]);
+        } else {
+          unpack8(w[2 * n], a.w_dtype == MOE_DT_F16, wv);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum.add_product(xv[j], wv[j]);
+        }
+      }
+    }
+    float hi = sum.hi.x, lo = sum.lo.x;
+    add_pair(hi, lo, sum.hi.y, sum.lo.y);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      const float ohi = __shfl_xor_sync(0xffffffffu, hi, off), olo = __shfl_xor_sync(0xffffffffu, lo, off);
+      add_pair(hi, lo, ohi, olo);
+    }
+    if (lane == 0) a.logits[(size_t)t * E + e] = isfinite(hi) ? __fadd_rn(hi, lo) : hi;
+  }
+  if (rank == 1 && few_scales_x(a.d.fmt)) {  // the row for the experts
     uint32_t m = 0;
     for (int i = threadIdx.x; i < H / 8; i += kRouterThreads) {
-      const uint4 u = *(const uint4*)(a.x + t * a.ldx + 8 * i);
+      const uint4 u = *(const uint4*)(x + 8 * i);
       m = __vmaxu2(m, __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu), __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu)));
     }
     m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
@@ -66,11 +125,11 @@ __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(const FewArg
     __syncthreads();
     m = 0;
 #pragma unroll
-    for (int w = 0; w < kRouterThreads / 32; ++w) m = max(m, s_max[w]);
+    for (int w = 0; w < kRouterWarps; ++w) m = max(m, s_max[w]);
     const float scale = row_scale(m << 16);
     if (threadIdx.x == 0) a.xinv[t] = row_scale_inv(m << 16);
     for (int i = threadIdx.x; i < H / 8; i += kRouterThreads) {
-      const uint4 u = *(const uint4*)(a.x + t * a.ldx + 8 * i);
+      const uint4 u = *(const uint4*)(x + 8 * i);
       const uint32_t v[4] = {u.x, u.y, u.z, u.w};
       __half2 o[4];
 #pragma unroll
@@ -78,46 +137,9 @@ __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(const FewArg
         o[j] = __floats2half2_rn(__uint_as_float(v[j] << 16) * scale, __uint_as_float(v[j] & 0xFFFF0000u) * scale);
       *(uint4*)(a.xs + (size_t)t * H + 8 * i) = *(const uint4*)o;
     }
-    return;
   }
-  for (int t0 = 0; t0 < a.T; t0 += kRouterTokens) {
-    const int nt = min(kRouterTokens, a.T - t0);
-    Pair acc[kRouterTokens];
-    for (int i = 8 * threadIdx.x; i < H; i += 8 * kRouterThreads) {
-      float w[8];
-      load_router8(a.wr, a.w_dtype, e * a.ldw + i, w);
-#pragma unroll
-      for (int t = 0; t < kRouterTokens; ++t)
-        if (t < nt) {
-          const uint4 u = *(const uint4*)(a.x + (t0 + t) * a.ldx + i);
-          const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            acc[t].add_product(__uint_as_float(v[j] << 16), w[2 * j]);
-            acc[t].add_product(__uint_as_float(v[j] & 0xFFFF0000u), w[2 * j + 1]);
-          }
-        }
-    }
-#pragma unroll
-    for (int t = 0; t < kRouterTokens; ++t) {
-      if (t >= nt) break;
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        Pair o;
-        o.hi = __shfl_xor_sync(0xffffffffu, acc[t].hi, off);
-        o.lo = __shfl_xor_sync(0xffffffffu, acc[t].lo, off);
-        acc[t].add(o);
-      }
-      if (lane == 0) part[warp][t] = acc[t];
-    }
-    __syncthreads();
-    if (threadIdx.x < nt) {
-      Pair s = part[0][threadIdx.x];
-      for (int w = 1; w < kRouterThreads / 32; ++w) s.add(part[w][threadIdx.x]);
-      a.logits[(t0 + threadIdx.x) * a.d.E + e] = s.rounded();
-    }
-    __syncthreads();
-  }
+  cluster_sync();
+  if (rank == 0 && warp == 0) score_token<VT, true>(a.router, geom, t, a.k, lane, a.idx, a.wt, scratch);
 }
 
 }  // namespace
@@ -130,12 +152,14 @@ FewLayout few_layout(const moe_packed_desc_t& d, int T, int k) {
     cur += (bytes + 255) / 256 * 256;
     return o;
   };
-  const size_t R = (size_t)T * k, active = R < (size_t)d.E ? R : (size_t)d.E;
+  const size_t R = (size_t)T * k;
   L.status = take(256);
-  L.done = take(4 * active);
-  L.tile = take(4 * (size_t)(d.H / 16));
+  L.done = take(4 * R);
+  L.tile = take(4 * (size_t)(d.H / 32));
   L.hmax = take(4 * R);
   L.zero_end = cur;
+  L.idx = take(4 * R);
+  L.wt = take(4 * R);
   L.xinv = take(4 * (size_t)T);
   L.logits = take(4 * (size_t)T * d.E);
   L.xs = take(few_scales_x(d.fmt) ? 2 * (size_t)T * d.H : 0);
@@ -146,9 +170,26 @@ FewLayout few_layout(const moe_packed_desc_t& d, int T, int k) {
 }
 
 cudaError_t launch_few_router(const FewArgs& a, size_t zero_bytes, cudaStream_t s) {
+  const ScoreGeom g = score_geom(a.router, a.d.E);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.T * kCluster);
+  cfg.blockDim = dim3(kRouterThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const int words = (int)(zero_bytes / 4);
   note_launches(1);
-  const int grid = a.d.E + (few_scales_x(a.d.fmt) ? a.T : 0);
-  return launch_pdl(few_router_kernel, dim3(grid), dim3(kRouterThreads), 0, s, a, (int)(zero_bytes / 4));
+  if (g.per <= 1) return cudaLaunchKernelEx(&cfg, few_router_kernel<1>, a, g, words);
+  if (g.per <= 2) return cudaLaunchKernelEx(&cfg, few_router_kernel<2>, a, g, words);
+  if (g.per <= 4) return cudaLaunchKernelEx(&cfg, few_router_kernel<4>, a, g, words);
+  if (g.per <= 8) return cudaLaunchKernelEx(&cfg, few_router_kernel<8>, a, g, words);
+  return cudaLaunchKernelEx(&cfg, few_router_kernel<16>, a, g, words);
 }
 
 }  // namespace moe
@@ -174,7 +215,6 @@ extern "C" moe_status_t moe_layer_few(const void* x, int64_t ldx, const void* w_
   if ((uintptr_t)x % 16 || (uintptr_t)w_router % 16 || (uintptr_t)out % 16 || (uintptr_t)packed % 256 ||
       (uintptr_t)workspace % 256 || (uintptr_t)bias % 4 || (uintptr_t)topk_idx % 4 || (uintptr_t)topk_w % 4)
     return MOE_ERR_INVALID_ARG;
-  if (H > kFewWidth || desc->I > kFewWidth) return MOE_ERR_UNSUPPORTED;
   const FewLayout L = few_layout(*desc, T, top_k);
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
   const moe_status_t dv = device_ok();
@@ -193,8 +233,8 @@ extern "C" moe_status_t moe_layer_few(const void* x, int64_t ldx, const void* w_
   a.ldo = ldo;
   a.T = T;
   a.k = top_k;
-  a.topk_idx = topk_idx;
-  a.topk_w = topk_w;
+  a.idx = topk_idx ? topk_idx : (int32_t*)(ws + L.idx);
+  a.wt = topk_w ? topk_w : (float*)(ws + L.wt);
   a.status = (int*)(ws + L.status);
   a.done = (int*)(ws + L.done);
   a.tile = (int*)(ws + L.tile);

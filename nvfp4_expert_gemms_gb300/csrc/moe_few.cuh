@@ -1,7 +1,7 @@
 // Declarations of the whole layer for a few tokens (moe_layer_few): its workspace and what its two kernels share.
 //
 // Operands.  The products run on mma.sync m16n8k16 with the weights as the 16-row operand and up to eight tokens as
-// the 8-column one: a step reads each weight once from HBM, so bytes set the pace and not the MMA rate, and the
+// the 8-column one (up to four where h comes in two terms): a step reads each weight once from HBM, so bytes set the pace and not the MMA rate, and the
 // operands may come from registers, straight from the decoded codes, with no second trip through shared memory.
 // E4M3, E2M1 x E4M3 and INT4 weights are all exact in fp16, whose products with fp16 activations are exact in the
 // fp32 accumulator; a row of activations is scaled by a power of two so that fp16 holds its bf16 values exactly (but for
@@ -13,13 +13,12 @@
 namespace moe {
 
 constexpr int kFewTokens = MOE_FEW_MAX_TOKENS;
-constexpr int kFewWidth = 16384;  // H and I at most: a unit's NVFP4 scales stand in shared memory whole
 constexpr int kFewSlots = kFewTokens * kMaxTopK;  // (token, choice) pairs
 
 // Byte offsets in the workspace.  status: the device error word (as in ws_layout), the ticket counter; zero .. zero_end:
 // what the first kernel zeroes with them.
 struct FewLayout {
-  size_t status, done, tile, hmax, zero_end, xinv, logits, xs, h, y, total;
+  size_t status, done, tile, hmax, zero_end, idx, wt, xinv, logits, xs, h, y, total;
 };
 FewLayout few_layout(const moe_packed_desc_t& d, int T, int k);
 
@@ -35,11 +34,11 @@ struct FewArgs {
   int64_t ldo;
   int T, k;
   ScoreArgs router;  // its logits are the first kernel's [T, E]
-  int32_t* topk_idx; // or null
-  float* topk_w;
+  int32_t* idx;      // [T, k]: the choice
+  float* wt;
   int* status;       // [0] error word, [1] tickets handed out
-  int* done;         // [active expert]: units of its gate/up rows that are finished
-  int* tile;         // [down tile]: units that are finished
+  int* done;         // [entry]: 16-feature tiles of its h that are finished
+  int* tile;         // [32-column tile of y]: entries that are finished
   unsigned* hmax;    // [T k]: largest |h| of a slot, as bits
   float* logits;     // [T, E]
   __half* xs;        // [T, H]: x scaled by a power of two per row (bf16 weights: unused)
@@ -50,7 +49,7 @@ struct FewArgs {
 cudaError_t launch_few_router(const FewArgs& a, size_t zero_bytes, cudaStream_t s);
 cudaError_t launch_few_experts(const FewArgs& a, cudaStream_t s);
 
-inline bool few_scales_x(int fmt) { return fmt != MOE_FMT_BF16; }
+__host__ __device__ inline bool few_scales_x(int fmt) { return fmt != MOE_FMT_BF16; }
 
 // The power of two that takes a row whose largest magnitude has these bits to below 2^15 (at 2^14 or more, but for rows
 // below 2^-112), and its inverse.  A row with infinities or NaN counts as fp32's largest.

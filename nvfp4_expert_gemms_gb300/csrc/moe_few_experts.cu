@@ -1,16 +1,23 @@
-// The experts of moe_layer_few in one kernel: routing, gate/up, down and the combine.
+// The experts of moe_layer_few in one kernel: gate/up, down and the combine.
 //
-// Work is cut into units of some weight rows of one expert, whole along K: first every unit of the gate/up matrices, in
-// the order of the active experts, then those of the down matrices.  Blocks take them by ticket in that order, so whoever
-// waits (a down unit for its expert's h) waits for units that running blocks hold and that wait for nothing: no two blocks
-// have to be resident together, and calls on other streams cannot stand in the way.
+// Tokens of one expert go four at a time (an entry: an expert and up to four of its (token, choice) slots).  Work is cut into
+// units of an entry's weight rows, whole along K: 16 gates and the same features' ups, or 32 outputs (a multiple of these
+// where K is short); first every unit of the gate/up matrices, entry by entry, then those of the down matrices.  Blocks
+// take runs of units by ticket in that order, so whoever waits (a down unit for its entry's h) waits for units that running
+// blocks hold and that wait for nothing: no two blocks have to be resident together, and calls on other streams cannot
+// stand in the way.  An atomic's answer takes over a microsecond here, so a block takes few tickets (one per matrix where there
+// are few units) and asks for the next one as it starts a run.
 //
-// In a block, one warp keeps a ring of shared memory full by TMA (in flight per SM: 144 to 160 KB; weights need about
-// 45 KB at HBM's rate and latency) and runs ahead of everyone, into the down matrices while h is not there yet.  Sixteen
-// warps each take a piece of 128 columns (64 of bf16) of 16 rows, decode it into MMA operands and multiply it with up to
-// eight tokens; four more add the pieces up, four units in flight, and finish them: h = silu(gate) up, or the weighted row
-// of y.  The block that finishes the last expert's rows of some output columns sums them over each token's experts,
-// in their order.
+// One warp of a block copies by TMA, eight pieces of 128 columns (64 of bf16) by 32 rows to a stage of shared memory,
+// 108 to 192 KB ahead (HBM's rate and latency ask for some 45), into the down matrices while h is not there yet.  Sixteen warps
+// take a piece of a unit each, decode it straight into MMA operands, multiply it with the entry's tokens, whose operands stay in
+// registers from unit to unit, and leave their sums in shared memory.  Three more take the units in turn, add
+// the sums up and finish the rows: h = silu(gate) up, or weighted rows of y; they tell other blocks once per run.  The
+// block that finishes the last entry of 32 output columns sums them over each token's experts, in their order.
+//
+// What it takes: every warp's work on a unit is a chain of latencies, about 1000 cycles, where HBM brings a unit of FP8 in 2800
+// and one of four bits in 1500.  So nothing in that chain may wait for L2: no spilled register (with 222 KB of
+// shared memory there is next to no L1), no scale or address that was not asked for early, and the copies are another warp's.
 #include "moe_few.cuh"
 #include "moe_formats.cuh"
 #include "moe_tc.cuh"
@@ -21,54 +28,57 @@ using namespace tc;
 
 namespace {
 
-constexpr int kMulWarps = 16, kEndWarps = 4, kProdWarp = kMulWarps + kEndWarps;
-constexpr int kWarps = kProdWarp + 1, kThreads = 32 * kWarps;
+constexpr int kMulWarps = 16, kEndWarps = 3, kCopyWarp = kMulWarps + kEndWarps, kWarps = kCopyWarp + 1, kThreads = 32 * kWarps;
+constexpr int kEntryRows = 4;
+constexpr int kStagePieces = 8;
 constexpr int kMaxStages = 8;
-constexpr int kColumns = 16;  // pieces of K per slab at most: one per multiplying warp
-constexpr size_t kSmemMax = 227 * 1024 - 14 * 1024;  // beside the tables below
+constexpr int kBatch = 32;  // tiles of 32 columns of y a finishing warp tells about at once
 
 template <int FMT>
 struct Format {
-  static constexpr int kPiece = FMT == MOE_FMT_BF16 ? 64 : 128;  // columns of a piece
-  static constexpr int kRowBytes = FMT == MOE_FMT_NVFP4_W4A16 || FMT == MOE_FMT_INT4_G128_W4A16 ? 64 : 128;  // of a piece
-  static constexpr int kTiles = kRowBytes == 64 ? 2 : 1;         // 16-row tiles a warp multiplies per piece
-  static constexpr int kRegs = kPiece / 8;                       // registers of a piece's activations
+  static constexpr bool kNvfp4 = FMT == MOE_FMT_NVFP4_W4A16, kInt4 = FMT == MOE_FMT_INT4_G128_W4A16, kBf16 = FMT == MOE_FMT_BF16;
+  static constexpr int kPiece = kBf16 ? 64 : 128;                   // columns of a piece
+  static constexpr int kRegs = kPiece / 8;                          // registers of a piece's activations
+  static constexpr int kRowBytes = kNvfp4 || kInt4 ? 64 : 128;      // of a piece
+  static constexpr int kCodes = 32 * kRowBytes;                     // bytes of a piece's codes, 32 rows
+  static constexpr int kScales = kNvfp4 ? 256 : kInt4 ? 64 : 0;     // and of the scales that come along
+  static constexpr int kStage = kStagePieces * (kCodes + kScales);  // a multiple of 512
+  static constexpr int kStages = kNvfp4 || kInt4 ? kMaxStages : 6;
+  static constexpr int kParts = kEndWarps * kMulWarps * 512;
+  static constexpr int kSmem = 1024 + kStages * ((kStage + 1023) / 1024 * 1024) + kParts;
 };
 
-// One of the two matrices: how its rows and columns are cut.
+// One of the two matrices.
 struct Cut {
-  int K, rows;       // columns; features (gate/up) or outputs (down)
-  int pieces;        // pieces of K
-  int columns;       // pieces per slab
-  int slabs;         // slabs of a unit
-  int groups;        // warps along the rows per piece of K
-  int mt;            // 16-row tiles per unit
-  int step;          // features or outputs per unit: 8 mt or 16 mt
-  int units;         // per expert
-  int run;           // consecutive units per ticket
-  uint32_t bytes;    // codes of a slab
-  const char* scales;
+  const char *codes, *scales;
   const float* gs;
+  int N, K;          // stored rows and columns per expert
+  int rows, pieces;  // features or outputs; pieces of K
+  int columns;       // warps along K
+  int halves;        // stages along K: columns / 8, rounded up
+  int groups;        // warps along the rows
+  int step;          // features or outputs per unit
+  int units;         // per entry
+  int steps;         // times the warps go along K
 };
 
 struct Args {
-  CUtensorMap map[2], smap[2];
+  CUtensorMap map[2], smap[2];  // codes, and INT4's scales
   FewArgs f;
-  ScoreGeom geom;
   Cut cut[2];
-  int stages, stage_bytes;
 };
+__device__ __forceinline__ Cut cut_of(const Args& a, int kind) { return kind ? a.cut[1] : a.cut[0]; }
 
-struct Tables {  // what routing leaves in shared memory
+struct Tables {
   int idx[kFewSlots];
   float wt[kFewSlots];
-  uint8_t rows[kMaxE][kFewTokens];  // slots of an active expert
-  uint8_t expert[kMaxE], count[kMaxE], active_of[kMaxE];
-  int leaders[kFewSlots / 32 + 1];
-  int nactive, down_passes;         // passes over all active experts
+  uint8_t rows[kFewSlots][kEntryRows];  // an entry's slots
+  uint8_t expert[kFewSlots], count[kFewSlots];
+  uint16_t first[kMaxE];                // an expert's first entry
+  int sums[kWarps];
+  float xinv[kFewTokens];
+  int entries;
 };
-
-__device__ __forceinline__ int passes(int kind, int count) { return kind ? (count + 3) / 4 : (count + 7) / 8; }
 
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1, bool bf) {
   if (bf)
@@ -97,18 +107,17 @@ __device__ __forceinline__ void e2m1x8_f16(uint32_t c, uint32_t (&o)[4]) {
       : "r"(c));
 }
 
-// Where the q-th eight elements of a lane's share of a piece stand in the piece (t: lane % 4).  The MMA's K order is free as
-// long as both operands use the same one, so a lane takes what it can read in wide, conflict-free accesses.
+// Where the j-th eight elements of a lane's share of a piece stand in the piece (t: lane % 4).  The MMA's K order is free as
+// long as both operands use the same one, so a lane takes what it can read in whole 16-byte parts without bank conflicts.
 template <int FMT>
-__device__ __forceinline__ int element(int t, int q) {
-  if (FMT == MOE_FMT_INT4_G128_W4A16) return 8 * (t + 4 * q);
-  return Format<FMT>::kPiece / 4 * t + 8 * q;
+__device__ __forceinline__ int element(int t, int j) {
+  return Format<FMT>::kInt4 ? 8 * (t + 4 * j) : Format<FMT>::kPiece / 4 * t + 8 * j;
 }
 
 // INT4 words decode into pairs of elements (j, j + 4): the same order for the activations.
 template <int FMT>
 __device__ __forceinline__ void order_pairs(uint32_t* b) {
-  if (FMT != MOE_FMT_INT4_G128_W4A16) return;
+  if (!Format<FMT>::kInt4) return;
   const uint32_t r0 = b[0], r1 = b[1], r2 = b[2], r3 = b[3];
   b[0] = __byte_perm(r0, r2, 0x5410);
   b[1] = __byte_perm(r0, r2, 0x7632);
@@ -116,132 +125,116 @@ __device__ __forceinline__ void order_pairs(uint32_t* b) {
   b[3] = __byte_perm(r1, r3, 0x7632);
 }
 
-// A piece of the activations as the MMA's column operand: x of up to eight tokens, ...
+// A piece of an entry's activations as the MMA's column operand: x in the columns 0 .. 3, ...
 template <int FMT>
-__device__ __forceinline__ void load_x(const FewArgs& f, const Tables& s, int ai, int pass, int col, int lane, uint32_t (&b)[Format<FMT>::kRegs]) {
-  const int g = lane >> 2, t = lane & 3, r = 8 * pass + g;
-  const bool live = r < s.count[ai];
-  const int token = s.rows[ai][live ? r : 0] / f.k;
-  const uint16_t* row = FMT == MOE_FMT_BF16 ? (const uint16_t*)(f.x + token * f.ldx) : (const uint16_t*)(f.xs + (size_t)token * f.d.H);
+__device__ __forceinline__ void load_x(const FewArgs& f, const Tables& s, int entry, int col, int lane, uint32_t (&b)[Format<FMT>::kRegs]) {
+  const int g = lane >> 2, t = lane & 3;
+  const bool live = g < s.count[entry];
+  const int token = s.rows[entry][live ? g : 0] / f.k;
+  const uint16_t* row = (Format<FMT>::kBf16 ? (const uint16_t*)f.x + token * f.ldx : (const uint16_t*)f.xs + (size_t)token * f.d.H) + col;
 #pragma unroll
-  for (int q = 0; q < Format<FMT>::kRegs / 4; ++q) {
-    const uint4 u = live ? *(const uint4*)(row + col + element<FMT>(t, q)) : make_uint4(0, 0, 0, 0);
-    b[4 * q] = u.x, b[4 * q + 1] = u.y, b[4 * q + 2] = u.z, b[4 * q + 3] = u.w;
-    order_pairs<FMT>(b + 4 * q);
+  for (int j = 0; j < Format<FMT>::kRegs / 4; ++j) {
+    const uint4 u = live ? *(const uint4*)(row + element<FMT>(t, j)) : make_uint4(0, 0, 0, 0);
+    b[4 * j] = u.x, b[4 * j + 1] = u.y, b[4 * j + 2] = u.z, b[4 * j + 3] = u.w;
+    order_pairs<FMT>(b + 4 * j);
   }
 }
 
-// ... or h of up to four: the columns 0 .. 3 hold the nearest fp16 (bf16) of each, 4 .. 7 what is left.
+// ... or h: the nearest fp16 (bf16) of each in the columns 0 .. 3, what is left in 4 .. 7.
 template <int FMT>
-__device__ __forceinline__ void load_h(const FewArgs& f, const Tables& s, int ai, int pass, int col, int lane, uint32_t (&b)[Format<FMT>::kRegs]) {
-  const int g = lane >> 2, t = lane & 3, r = 4 * pass + (g & 3);
-  const bool live = r < s.count[ai], low = g >= 4;
-  const int slot = s.rows[ai][live ? r : 0];
+__device__ __forceinline__ void load_h(const FewArgs& f, const Tables& s, int entry, int col, int lane, uint32_t (&b)[Format<FMT>::kRegs]) {
+  const int g = lane >> 2, t = lane & 3, r = g & 3;
+  const bool live = r < s.count[entry], low = g >= 4;
+  const int slot = s.rows[entry][live ? r : 0];
   const float* row = f.h + (size_t)slot * f.d.I + col;
-  const float scale = FMT == MOE_FMT_BF16 ? 1.f : row_scale(__ldcg(f.hmax + slot));
+  const float scale = Format<FMT>::kBf16 ? 1.f : row_scale(__ldcg(f.hmax + slot));
 #pragma unroll
-  for (int q = 0; q < Format<FMT>::kRegs / 4; ++q) {
-    const float4* p = (const float4*)(row + element<FMT>(t, q));
+  for (int j = 0; j < Format<FMT>::kRegs / 4; ++j) {
+    const float4* p = (const float4*)(row + element<FMT>(t, j));
     const float4 u0 = live ? __ldcg(p) : make_float4(0, 0, 0, 0), u1 = live ? __ldcg(p + 1) : make_float4(0, 0, 0, 0);
     const float v[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (FMT == MOE_FMT_BF16) {
-        __nv_bfloat162 hi = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-        if (low) hi = __floats2bfloat162_rn(v[2 * j] - __low2float(hi), v[2 * j + 1] - __high2float(hi));
-        b[4 * q + j] = *(const uint32_t*)&hi;
+    for (int i = 0; i < 4; ++i) {
+      if (Format<FMT>::kBf16) {
+        __nv_bfloat162 hi = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        if (low) hi = __floats2bfloat162_rn(v[2 * i] - __low2float(hi), v[2 * i + 1] - __high2float(hi));
+        b[4 * j + i] = *(const uint32_t*)&hi;
       } else {
-        const float x = v[2 * j] * scale, y = v[2 * j + 1] * scale;
+        const float x = v[2 * i] * scale, y = v[2 * i + 1] * scale;
         __half2 hi = __floats2half2_rn(x, y);
         if (low) hi = __floats2half2_rn(x - __low2float(hi), y - __high2float(hi));
-        b[4 * q + j] = *(const uint32_t*)&hi;
+        b[4 * j + i] = *(const uint32_t*)&hi;
       }
     }
-    order_pairs<FMT>(b + 4 * q);
+    order_pairs<FMT>(b + 4 * j);
   }
 }
 
-// c += one piece of a 16-row tile times the activations.  sm: the slab's codes; tile m of mt; piece: in the slab.  Rows: gate/up
-// holds the 8 mt gate rows and then the ups, a tile's rows 0 .. 7 its gates and 8 .. 15 the same features' ups.
+// acc += a piece of 32 rows at `sm` (its scales at `sc`) times the activations.  Tile m's MMA rows g and g + 8 are gate and up
+// n0 + 8 m + g of the features, or outputs n0 + 16 m + g and 8 further on.
 template <int FMT>
-__device__ __forceinline__ void multiply(const Cut& cut, int kind, const char* sm, const char* sc, int e, int n0, int m, int slab, int piece,
-                                         int lane, const uint32_t (&b)[Format<FMT>::kRegs], float (&c)[4]) {
-  const int g = lane >> 2, t = lane & 3, mt = cut.mt;
-  // the tile's rows g and g + 8 within the slab
-  const int r0 = kind ? 16 * m + g : 8 * m + g, r1 = kind ? r0 + 8 : 8 * mt + r0;
-  const char* at = sm + (size_t)piece * (16 * mt * Format<FMT>::kRowBytes);
-  float p[4] = {0.f, 0.f, 0.f, 0.f};
-  if constexpr (FMT == MOE_FMT_FP8_B128_W8A16) {
-    // rows of 128 bytes, 16-byte parts XORed with the row: a lane's two parts of eight lanes lie in different banks
-    const int col = cut.columns * slab + piece, f0 = n0 + (kind ? r0 : 8 * m + g), f1 = kind ? n0 + r1 : cut.rows + f0;
-    const int per = (kind ? cut.rows : 2 * cut.rows) / 128;  // blocks of rows
-    const float* s = (const float*)cut.scales + (size_t)e * per * cut.pieces + col;
-    // (a tile past the matrix's end is not stored: any scale will do)
-    const float s0 = __ldg(s + (size_t)min(f0 / 128, per - 1) * cut.pieces), s1 = __ldg(s + (size_t)min(f1 / 128, per - 1) * cut.pieces);
+__device__ __forceinline__ void multiply(const char* sm, const char* sc, int kind, float s0, float s1, int lane, const uint32_t (&b)[Format<FMT>::kRegs],
+                                         float (&acc)[2][4]) {
+  const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int part = (2 * t + q) ^ g;
-      const uint4 u = *(const uint4*)(at + 128 * r0 + 16 * part), v = *(const uint4*)(at + 128 * r1 + 16 * part);
+  for (int m = 0; m < 2; ++m) {
+    float p[4] = {0.f, 0.f, 0.f, 0.f};
+    auto step = [&](uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, int i) { mma(p, a0, a1, a2, a3, b[i], b[i + 1], Format<FMT>::kBf16); };
+    const int r0 = kind ? 16 * m + g : 8 * m + g, r1 = kind ? r0 + 8 : r0 + 16;
+    if constexpr (Format<FMT>::kInt4) {
+      // words hold eight columns of a row and lie side by side along the rows, 128 bytes per column group: 16-byte parts
+      // XORed with the group (gate/up: each half's four parts by the group mod 4)
+      s0 = __half2float(((const __half*)sc)[r0]), s1 = __half2float(((const __half*)sc)[r1]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int kr = t + 4 * j, swap = (kr & (kind ? 7 : 3)) << 4;
+        const char* line = sm + 128 * kr;
+        const uint32_t w[2] = {*(const uint32_t*)(line + ((4 * r0) ^ swap)), *(const uint32_t*)(line + ((4 * r1) ^ swap))};
+        uint32_t x[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {  // 1024 + code in fp16, less 1032 the weight
+            const uint32_t v = ((w[i] >> (4 * n)) & 0x000F000Fu) | 0x64006400u;
+            const __half2 d = __hsub2(*(const __half2*)&v, __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408)));
+            x[i][n] = *(const uint32_t*)&d;
+          }
+        step(x[0][0], x[1][0], x[0][1], x[1][1], 4 * j);
+        step(x[0][2], x[1][2], x[0][3], x[1][3], 4 * j + 2);
+      }
+    } else if constexpr (Format<FMT>::kNvfp4) {
+      // a code times its block's scale has six significant bits: exact in fp16 (2^-10 at the least, 2688 at most)
+      const uint32_t q0 = e4m3x2_f16(*(const uint16_t*)(sc + 8 * r0 + 2 * t)), q1 = e4m3x2_f16(*(const uint16_t*)(sc + 8 * r1 + 2 * t));
+      const uint4 u = *(const uint4*)(sm + 64 * r0 + 16 * t), v = *(const uint4*)(sm + 64 * r1 + 16 * t);
       const uint32_t w0[4] = {u.x, u.y, u.z, u.w}, w1[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        mma(p, e4m3x2_f16(w0[j]), e4m3x2_f16(w1[j]), e4m3x2_f16(w0[j] >> 16), e4m3x2_f16(w1[j] >> 16), b[8 * q + 2 * j], b[8 * q + 2 * j + 1], false);
-    }
-    c[0] = fmaf(p[0], s0, c[0]), c[1] = fmaf(p[1], s0, c[1]), c[2] = fmaf(p[2], s1, c[2]), c[3] = fmaf(p[3], s1, c[3]);
-  } else if constexpr (FMT == MOE_FMT_BF16) {
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t z0 = __byte_perm(q0, q0, j < 2 ? 0x1010 : 0x3232), z1 = __byte_perm(q1, q1, j < 2 ? 0x1010 : 0x3232);
+        uint32_t x[4], y[4];
+        e2m1x8_f16(w0[j], x);
+        e2m1x8_f16(w1[j], y);
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int part = (2 * t + q) ^ g;
-      const uint4 u = *(const uint4*)(at + 128 * r0 + 16 * part), v = *(const uint4*)(at + 128 * r1 + 16 * part);
-      mma(p, u.x, v.x, u.y, v.y, b[4 * q], b[4 * q + 1], true);
-      mma(p, u.z, v.z, u.w, v.w, b[4 * q + 2], b[4 * q + 3], true);
-    }
+        for (int i = 0; i < 2; ++i) step(hmul2(x[2 * i], z0), hmul2(y[2 * i], z1), hmul2(x[2 * i + 1], z0), hmul2(y[2 * i + 1], z1), 4 * j + 2 * i);
+      }
+    } else {
+      // rows of 128 bytes, 16-byte parts XORed with the row
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] += p[i];
-  } else if constexpr (FMT == MOE_FMT_NVFP4_W4A16) {
-    // rows of 64 bytes: eight lanes read 128 consecutive ones.  A code times its block's scale has six significant bits: exact in
-    // fp16 (2^-10 at the least, 2688 at most).
-    const int col = cut.columns * slab + piece, per = cut.K / 16;
-    const uint32_t q0 = e4m3x2_f16(*(const uint16_t*)(sc + r0 * per + 8 * col + 2 * t)), q1 = e4m3x2_f16(*(const uint16_t*)(sc + r1 * per + 8 * col + 2 * t));
-    const uint4 u = *(const uint4*)(at + 64 * r0 + 16 * t), v = *(const uint4*)(at + 64 * r1 + 16 * t);
-    const uint32_t w0[4] = {u.x, u.y, u.z, u.w}, w1[4] = {v.x, v.y, v.z, v.w};
+      for (int q = 0; q < 2; ++q) {
+        const int part = ((2 * t + q) ^ g) << 4;
+        const uint4 u = *(const uint4*)(sm + 128 * r0 + part), v = *(const uint4*)(sm + 128 * r1 + part);
+        if constexpr (Format<FMT>::kBf16) {
+          step(u.x, v.x, u.y, v.y, 4 * q);
+          step(u.z, v.z, u.w, v.w, 4 * q + 2);
+        } else {
+          const uint32_t w0[4] = {u.x, u.y, u.z, u.w}, w1[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t s0 = __byte_perm(q0, q0, j < 2 ? 0x1010 : 0x3232), s1 = __byte_perm(q1, q1, j < 2 ? 0x1010 : 0x3232);
-      uint32_t x[4], y[4];
-      e2m1x8_f16(w0[j], x);
-      e2m1x8_f16(w1[j], y);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        mma(p, hmul2(x[2 * i], s0), hmul2(y[2 * i], s1), hmul2(x[2 * i + 1], s0), hmul2(y[2 * i + 1], s1), b[4 * j + 2 * i], b[4 * j + 2 * i + 1], false);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] += p[i];
-  } else {
-    // a word holds eight columns of one row, and words of a column group lie side by side along the rows: a group of warps has
-    // its 32 rows' words (128 bytes, or 64 of gates and 64 of ups; 16-byte parts of these XORed with the column group) to itself.  Half-words of nibbles become
-    // 1024 + code in fp16, less 1032 the weight.
-    const __half* s = (const __half*)sc + (size_t)piece * 16 * mt;
-    const float s0 = __half2float(s[r0]), s1 = __half2float(s[r1]);
-    const char* words = sm + (size_t)(m >> 1) * (cut.columns * 2048) + 2048 * piece;
-    const int at0 = 4 * (kind ? 16 * (m & 1) + g : 8 * (m & 1) + g), at1 = at0 + (kind ? 32 : 64);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int kr = t + 4 * q, swap = (kr & (kind ? 7 : 3)) << 4;
-      const uint32_t w[2] = {*(const uint32_t*)(words + 128 * kr + (at0 ^ swap)), *(const uint32_t*)(words + 128 * kr + (at1 ^ swap))};
-      uint32_t x[2][4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t v = ((w[i] >> (4 * j)) & 0x000F000Fu) | 0x64006400u;
-          const __half2 d = __hsub2(*(const __half2*)&v, __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408)));
-          x[i][j] = *(const uint32_t*)&d;
+          for (int j = 0; j < 4; ++j)
+            step(e4m3x2_f16(w0[j]), e4m3x2_f16(w1[j]), e4m3x2_f16(w0[j] >> 16), e4m3x2_f16(w1[j] >> 16), 8 * q + 2 * j);
         }
-      mma(p, x[0][0], x[1][0], x[0][1], x[1][1], b[4 * q], b[4 * q + 1], false);
-      mma(p, x[0][2], x[1][2], x[0][3], x[1][3], b[4 * q + 2], b[4 * q + 3], false);
+      }
     }
-    c[0] = fmaf(p[0], s0, c[0]), c[1] = fmaf(p[1], s0, c[1]), c[2] = fmaf(p[2], s1, c[2]), c[3] = fmaf(p[3], s1, c[3]);
+    acc[m][0] = fmaf(p[0], s0, acc[m][0]), acc[m][1] = fmaf(p[1], s0, acc[m][1]);
+    acc[m][2] = fmaf(p[2], s1, acc[m][2]), acc[m][3] = fmaf(p[3], s1, acc[m][3]);
   }
 }
 
@@ -264,315 +257,389 @@ __device__ __forceinline__ bool wait_count(const int* p, int want, int lane, vol
   return __shfl_sync(0xffffffffu, ok, 0);
 }
 
-// The experts and weights of every token, and the active experts' rows, in shared memory.
-__device__ __noinline__ void route_tokens(const Args& a, Tables& s, ScoreScratch* scratch) {
-  const FewArgs& f = a.f;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, R = f.T * f.k;
-  for (int t = warp; t < f.T; t += kWarps) {
-    if (a.geom.per <= 1) score_token<1>(f.router, a.geom, t, f.k, lane, s.idx, s.wt, scratch[warp]);
-    else if (a.geom.per <= 2) score_token<2>(f.router, a.geom, t, f.k, lane, s.idx, s.wt, scratch[warp]);
-    else if (a.geom.per <= 4) score_token<4>(f.router, a.geom, t, f.k, lane, s.idx, s.wt, scratch[warp]);
-    else if (a.geom.per <= 8) score_token<8>(f.router, a.geom, t, f.k, lane, s.idx, s.wt, scratch[warp]);
-    else score_token<16>(f.router, a.geom, t, f.k, lane, s.idx, s.wt, scratch[warp]);
-  }
+// The entries, from every token's experts, in shared memory.
+__device__ __forceinline__ void make_entries(const FewArgs& f, Tables& s) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, R = f.T * f.k, i = threadIdx.x;
+  const int e = i < R ? f.idx[i] : -1;
+  if (i < kFewSlots) s.idx[i] = e;
+  if (i < R) s.wt[i] = f.wt[i];
+  if (i < f.T) s.xinv[i] = f.xinv[i];
   __syncthreads();
-  // an expert is active as of its first slot, in the order of those
-  const int i = threadIdx.x, e = i < R ? s.idx[i] : -1;
+  // Slot i's rank among its expert's; the first slot of an expert lays down its entries, in the order of those slots.
   int rank = 0, total = 0;
-  if (i < R)
-    for (int j = 0; j < R; ++j) {
-      const bool same = s.idx[j] == e;
-      rank += same && j < i;
-      total += same;
+  if (32 * warp < R) {
+    for (int j = 0; j < R; j += 4) {  // (past R: no expert)
+      const int4 o = *(const int4*)(s.idx + j);
+      const int v[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const bool same = v[n] == e;
+        rank += same && j + n < i;
+        total += same;
+      }
     }
-  const bool leader = i < R && rank == 0;
-  const uint32_t ballot = __ballot_sync(0xffffffffu, leader);
-  if (lane == 0 && warp < kFewSlots / 32) s.leaders[warp] = __popc(ballot);
-  __syncthreads();
-  if (leader) {
-    int ai = __popc(ballot & ((1u << lane) - 1));
-    for (int w = 0; w < warp; ++w) ai += s.leaders[w];
-    s.expert[ai] = (uint8_t)e;
-    s.count[ai] = (uint8_t)total;
-    s.active_of[e] = (uint8_t)ai;
   }
-  if (i == 0) {
-    int n = 0;
-    for (int w = 0; w < kFewSlots / 32; ++w) n += s.leaders[w];
-    s.nactive = n;
-    s.down_passes = 0;
+  const int own = i < R && rank == 0 ? (total + kEntryRows - 1) / kEntryRows : 0;
+  int upto = own;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, upto, off);
+    if (lane >= off) upto += o;
+  }
+  if (lane == 31) s.sums[warp] = upto;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kFewSlots / 32; ++w) {
+    before += w < warp ? s.sums[w] : 0;
+    all += s.sums[w];
+  }
+  if (i == 0) s.entries = all;
+  if (own) {
+    const int at = before + upto - own;
+    s.first[e] = (uint16_t)at;
+    for (int j = 0; j < own; ++j) {
+      s.expert[at + j] = (uint8_t)e;
+      s.count[at + j] = (uint8_t)min(kEntryRows, total - kEntryRows * j);
+    }
   }
   __syncthreads();
-  if (i < R) s.rows[s.active_of[e]][rank] = (uint8_t)i;
-  if (leader) atomicAdd(&s.down_passes, passes(1, total));
-  if (blockIdx.x == 0 && i < R) {
-    if (f.topk_idx) f.topk_idx[i] = e;
-    if (f.topk_w) f.topk_w[i] = s.wt[i];
-  }
+  if (i < R) s.rows[s.first[e] + rank / kEntryRows][rank % kEntryRows] = (uint8_t)i;
   __syncthreads();
+}
+
+// Finishes 32 rows of an entry (one warp): lane 16 m + 2 g + t (t < 2) holds tile m's sums of its rows g and g + 8 for the
+// entry's rows 2 t and 2 t + 1.  n0: the first feature or output; factor: what the two rows' sums are multiplied with.
+template <int FMT>
+__device__ __forceinline__ void finish_rows(const FewArgs& f, int kind, int rows, int n0, int lane, const float (&c)[4], const bool (&live)[2],
+                                            const int (&slot)[2], const float (&factor)[2]) {
+  const int m = lane >> 4, g = lane >> 1 & 7;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (kind == 0) {
+      const float gate = c[i] * factor[i], up = c[2 + i] * factor[i], h = gate / (1.f + expf(-gate)) * up;
+      if (live[i]) f.h[(size_t)slot[i] * rows + n0 + 8 * m + g] = h;
+      if (!Format<FMT>::kBf16) {
+        uint32_t hm = __float_as_uint(fabsf(h));
+#pragma unroll
+        for (int off = 2; off < 32; off <<= 1) hm = max(hm, __shfl_xor_sync(0xffffffffu, hm, off));  // all features of the row
+        if (lane < 2 && live[i]) atomicMax(f.hmax + slot[i], hm);
+      }
+    } else if (live[i]) {
+      float* y = f.y + (size_t)slot[i] * rows + n0 + 16 * m + g;
+      y[0] = c[i] * factor[i];
+      y[8] = c[2 + i] * factor[i];
+    }
+  }
+}
+
+// out for 32 columns, y and out pointing at the first, of every token (one warp).
+__device__ __noinline__ void combine(const float* y, __nv_bfloat16* out, int64_t ldo, int T, int k, int H, int lane) {
+  for (int i = lane; i < T * 8; i += 32) {  // four outputs of a token
+    const int token = i >> 3, n = 4 * (i & 7);
+    const float* at = y + (size_t)token * k * H + n;
+    float4 v[kMaxTopK];
+#pragma unroll
+    for (int j = 0; j < kMaxTopK; ++j)
+      if (j < k) v[j] = __ldcg((const float4*)(at + (size_t)j * H));
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < kMaxTopK; ++j)
+      if (j < k) o[0] += v[j].x, o[1] += v[j].y, o[2] += v[j].z, o[3] += v[j].w;
+    __nv_bfloat162 w[2] = {__floats2bfloat162_rn(o[0], o[1]), __floats2bfloat162_rn(o[2], o[3])};
+    *(uint2*)(out + token * ldo + n) = *(const uint2*)w;
+  }
 }
 
 template <int FMT>
 __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_constant__ Args a) {
-  constexpr int kRegs = Format<FMT>::kRegs, kTiles = Format<FMT>::kTiles;
+  using F = Format<FMT>;
+  constexpr int kStageBytes = (F::kStage + 1023) / 1024 * 1024;
   extern __shared__ __align__(1024) char smem_raw[];
   __shared__ Tables s;
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], ufull[kEndWarps], uempty[kEndWarps];
-  __shared__ int s_unit[kMaxStages], s_end[kEndWarps][2], s_abort;
+  __shared__ int4 s_stage[kMaxStages], s_unit[kEndWarps];  // matrix (-1: no more), entry, first row, among the last of its run
+  __shared__ int s_abort;
+  __shared__ uint16_t s_told[kEndWarps][kBatch];
   char* ring = (char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  float4* parts = (float4*)(ring + (size_t)a.stages * a.stage_bytes);  // [unit % 4][tile][piece][lane]
-  constexpr int kPartsPerUnit = kTiles * kColumns * 32;
+  float4* parts = (float4*)(ring + F::kStages * kStageBytes);  // [unit % 3][warp][tile][16]
   const FewArgs& f = a.f;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < a.stages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], kMulWarps);
+    for (int j = 0; j < F::kStages; ++j) {
+      mbar_init(&full[j], F::kNvfp4 ? 33 : 1);
+      mbar_init(&empty[j], kMulWarps);
     }
-    for (int i = 0; i < kEndWarps; ++i) {
-      mbar_init(&ufull[i], kMulWarps);
-      mbar_init(&uempty[i], 1);
+    for (int j = 0; j < kEndWarps; ++j) {
+      mbar_init(&ufull[j], kMulWarps);
+      mbar_init(&uempty[j], 1);
     }
     s_abort = 0;
     fence_barrier_init();
   }
-  if (warp == kProdWarp && lane < 2) prefetch_tmap(&a.map[lane]);
-  pdl_wait();  // the router's logits and the scaled rows
+  if (warp == kCopyWarp && lane < 2) prefetch_tmap(&a.map[lane]);
+  pdl_wait();  // the choice of experts and the scaled rows
   pdl_trigger();
-  route_tokens(a, s, (ScoreScratch*)parts);
-  const int ngu = s.nactive * a.cut[0].units, nunits = ngu + s.nactive * a.cut[1].units;
-  // a unit: its matrix, active expert and place there
-  auto place = [&](int unit, int& kind, int& ai, int& tile) {
-    kind = unit >= ngu;
-    const int j = kind ? unit - ngu : unit, per = a.cut[kind].units;
-    ai = j / per;
-    tile = j % per;
-  };
+  int ticket = 0;
+  if (threadIdx.x == 32 * kCopyWarp) ticket = atomicAdd(f.status + 1, 1);
+  make_entries(f, s);
+  const int ngu = s.entries * a.cut[0].units, nunits = ngu + s.entries * a.cut[1].units;
 
-  if (warp == kProdWarp) {
-    // ---------------- weights into the ring (lane 0) ----------------
-    if (lane == 0) {
-      const int run0 = a.cut[0].run, run1 = a.cut[1].run, t0 = (ngu + run0 - 1) / run0;
-      int it = 0, armed[kMaxStages];
-      for (int i = 0; i < kMaxStages; ++i) armed[i] = 0;
-      bool ok = true;
-      int ticket = atomicAdd(f.status + 1, 1);
-      while (ok) {
-        const int lo = ticket < t0 ? ticket * run0 : ngu + (ticket - t0) * run1;
-        const int hi = min(lo + (ticket < t0 ? run0 : run1), ticket < t0 ? ngu : nunits);
-        const int next = lo < nunits ? atomicAdd(f.status + 1, 1) : 0;
-        for (int unit = lo < nunits ? lo : -1; ok && unit < hi; ++unit) {
-          int kind = 0, ai = 0, tile = 0;
-          if (unit >= 0) place(unit, kind, ai, tile);
-          const Cut& cut = a.cut[kind];
-          // a unit of several slabs is streamed again for each pass over its tokens
-          const int copies = unit < 0 ? 1 : cut.slabs == 1 ? 1 : cut.slabs * passes(kind, s.count[ai]);
-          for (int c = 0; ok && c < copies; ++c, ++it) {
-            const int st = it % a.stages;
-            ok = mbar_wait(&empty[st], ((it / a.stages) & 1) ^ 1, &s_abort);
-            if (!ok) break;
-            s_unit[st] = unit;
-            if (unit < 0) {
-              mbar_arrive(&full[st]);
-              continue;
-            }
-            const int slab = c % cut.slabs, e = s.expert[ai], n0 = tile * cut.step, live = min(cut.step, cut.rows - n0);
-            char* dst = ring + (size_t)st * a.stage_bytes;
-            uint32_t bytes = cut.bytes, sbytes = 0;
-            if (FMT == MOE_FMT_NVFP4_W4A16) bytes += 2 * (sbytes = live * (cut.K / 16) / (kind ? 2 : 1));
-            if (FMT == MOE_FMT_INT4_G128_W4A16) bytes += cut.columns * 32 * cut.mt;
-            mbar_arrive_expect_tx(&full[st], bytes);
-            ++armed[st];
-            if (FMT == MOE_FMT_INT4_G128_W4A16) {
-              for (int i = 0; i < cut.groups; ++i) {
-                char* to = dst + (size_t)i * (cut.columns * 2048);
-                if (kind == 0) tma_load_4d(to, &a.map[0], &full[st], n0 + 16 * i, 0, 16 * cut.columns * slab, e);
-                else tma_load_3d(to, &a.map[1], &full[st], n0 + 32 * i, 16 * cut.columns * slab, e);
+  if (warp == kCopyWarp) {
+    // ---------------- copies ----------------
+    // A matrix's units are divided evenly into as many tickets as there are blocks, or up to eight times as many.
+    const int blocks = gridDim.x;
+    const int n0 = blocks * min(8, max(1, ngu / (4 * blocks))), n1 = blocks * min(8, max(1, (nunits - ngu) / (4 * blocks)));
+    int slot = 0, phase = 1, armed = 0;
+    bool ok = true;
+    // the next stage, free; the descriptor is its first stage's
+    auto take_stage = [&](int kind, int entry, int row, int flush) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], phase, &s_abort));
+      if (ok && lane == 0) s_stage[slot] = make_int4(kind, entry, row, flush);
+      __syncwarp();
+      return ok;
+    };
+    auto next_stage = [&]() {
+      armed |= 1 << slot;
+      if (++slot == F::kStages) {
+        slot = 0;
+        phase ^= 1;
+      }
+    };
+    for (;;) {
+      const int t = __shfl_sync(0xffffffffu, ticket, 0);
+      if (t >= n0 + n1) break;
+      const int kind = t >= n0;
+      const int64_t u = kind ? nunits - ngu : ngu, n = kind ? n1 : n0, at = kind ? t - n0 : t;
+      int unit = (int)(at * u / n);
+      const int end = (int)((at + 1) * u / n);
+      if (lane == 0) ticket = atomicAdd(f.status + 1, 1);
+      const Cut cut = cut_of(a, kind);
+      int entry = unit / cut.units, tile = unit - entry * cut.units;
+      for (; ok && unit < end; ++unit) {
+        const int e = s.expert[entry], row = tile * cut.step;
+        for (int step = 0; ok && step < cut.steps; ++step)
+          for (int group = 0; ok && group < cut.groups; ++group)
+            for (int half = 0; ok && half < cut.halves; ++half) {
+              if (!take_stage(kind, entry, row, end - unit <= kEndWarps)) break;
+              char* to = ring + slot * kStageBytes;
+              const int r = row + group * (kind ? 32 : 16), piece = step * kMulWarps + half * kStagePieces;
+              const int count = min(kStagePieces, cut.columns - half * kStagePieces);  // pieces the maps bring (their box)
+              if constexpr (F::kNvfp4) {  // scales: a lane per row, eight bytes per piece
+                const int i = kind ? 0 : lane >> 4, n = kind ? r + lane : r + (lane & 15);
+                const char* sc = cut.scales + ((size_t)e * cut.N + i * cut.rows + n) * (cut.K / 16) + 8 * piece;
+                if (n < cut.rows)
+                  for (int j = 0; j < count && piece + j < cut.pieces; ++j) cp_async_8(smem_u32(to + kStagePieces * F::kCodes + j * F::kScales + 8 * lane), sc + 8 * j);
+                cp_async_mbar_arrive_noinc(&full[slot]);
               }
-              if (kind == 0) tma_load_4d(dst + cut.bytes, &a.smap[0], &full[st], n0, 0, cut.columns * slab, e);
-              else tma_load_3d(dst + cut.bytes, &a.smap[1], &full[st], n0, cut.columns * slab, e);
-            } else {
-              if (kind == 0) tma_load_5d(dst, &a.map[0], &full[st], 0, n0, 0, cut.columns * slab, e);
-              else tma_load_4d(dst, &a.map[1], &full[st], 0, n0, cut.columns * slab, e);
-              if (FMT == MOE_FMT_NVFP4_W4A16) {
-                const size_t row = (size_t)cut.K / 16;
-                char* sc = dst + cut.bytes;
-                if (kind == 0) {
-                  const char* src = cut.scales + ((size_t)e * 2 * cut.rows + n0) * row;
-                  bulk_load(sc, src, sbytes, &full[st]);
-                  bulk_load(sc + cut.step * row, src + cut.rows * row, sbytes, &full[st]);
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&full[slot], cut.columns < kStagePieces ? cut.columns * (F::kCodes + (F::kInt4 ? F::kScales : 0))
+                                                                               : kStagePieces * (F::kCodes + (F::kInt4 ? F::kScales : 0)));
+                if constexpr (F::kInt4) {
+                  char* sc = to + kStagePieces * F::kCodes;
+                  if (kind == 0) {
+                    tma_load_4d(to, &a.map[0], &full[slot], r, 0, 16 * piece, e);
+                    tma_load_4d(sc, &a.smap[0], &full[slot], r, 0, piece, e);
+                  } else {
+                    tma_load_3d(to, &a.map[1], &full[slot], r, 16 * piece, e);
+                    tma_load_3d(sc, &a.smap[1], &full[slot], r, piece, e);
+                  }
                 } else {
-                  bulk_load(sc, cut.scales + ((size_t)e * cut.rows + n0) * row, 2 * sbytes, &full[st]);
+                  if (kind == 0) tma_load_5d(to, &a.map[0], &full[slot], 0, r, 0, piece, e);
+                  else tma_load_4d(to, &a.map[1], &full[slot], 0, r, piece, e);
                 }
               }
+              __syncwarp();
+              next_stage();
             }
-          }
-          if (unit < 0) break;
+        if (++tile == cut.units) {
+          tile = 0;
+          ++entry;
         }
-        if (lo >= nunits) break;
-        ticket = next;
       }
-      if (s_abort) {  // let every issued copy land before shared memory goes away
-        volatile int no_abort = 0;
-        for (int i = 0; i < a.stages; ++i)
-          if (armed[i]) mbar_wait(&full[i], (armed[i] - 1) & 1, &no_abort);
-      }
+      if (!ok) break;
+    }
+    if (ok && take_stage(-1, 0, 0, 0)) {
+      if (F::kNvfp4) mbar_arrive(&full[slot]);
+      if (lane == 0) mbar_arrive(&full[slot]);
+    }
+    __syncwarp();
+    if (F::kNvfp4) cp_async_wait<0>();
+    if (lane == 0 && s_abort) {  // let every issued copy land before shared memory goes away
+      volatile int no_abort = 0;
+      for (int i = 0; i < F::kStages; ++i)
+        if (armed >> i & 1) mbar_wait(&full[i], (i < slot ? phase : phase ^ 1) ^ 1, &no_abort);
     }
     __syncwarp();
   } else if (warp < kMulWarps) {
     // ---------------- pieces: decode and multiply ----------------
-    uint32_t b[kRegs];
-    int key = -1, it = 0, u = 0;
+    int slot = 0, phase = 0, end_slot = 0, end_phase = 1, ready = -1, key = -1;
+    uint32_t b[F::kRegs];
     bool ok = true;
-    auto acquire = [&](int n) { return __all_sync(0xffffffffu, mbar_wait(&full[n % a.stages], (n / a.stages) & 1, &s_abort)); };
-    auto release = [&](int n) {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[n % a.stages]);
-    };
-    // hand over a pass of a unit: this warp's sums, tile by tile
-    auto post = [&](int unit, int pass, const float (&c)[kTiles][4], const Cut* cut, int group, int piece) {
-      const int q = u % kEndWarps;
-      if (!__all_sync(0xffffffffu, mbar_wait(&uempty[q], ((u / kEndWarps) & 1) ^ 1, &s_abort))) return false;
-      if (cut) {
-#pragma unroll
-        for (int m = 0; m < kTiles; ++m)
-          parts[q * kPartsPerUnit + ((group * kTiles + m) * cut->columns + piece) * 32 + lane] = make_float4(c[m][0], c[m][1], c[m][2], c[m][3]);
-      }
-      if (warp == 0 && lane == 0) {
-        s_end[q][0] = unit;
-        s_end[q][1] = pass;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ufull[q]);
-      ++u;
-      return true;
-    };
-    while (ok) {
-      ok = acquire(it);
+    auto acquire = [&]() { ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], phase, &s_abort)); };
+    // this matrix's share of the warp: its stage of each step, its place in it; what it takes to find its scales
+    int kind = -1, mine = 0, local = 0, col = 0, stages = 0, steps = 0, pieces = 0, rows = 0, above = 0;
+    const float* scales = nullptr;
+    for (;;) {
+      acquire();
       if (!ok) break;
-      const int unit = *(volatile int*)&s_unit[it % a.stages];
-      float c[kTiles][4];
-      if (unit < 0) {
-        for (int i = 0; i < kEndWarps && ok; ++i) ok = post(-1, 0, c, nullptr, 0, 0);
-        break;
+      const int4 d = s_stage[slot];
+      if (d.x < 0) break;
+      if (d.x != kind) {
+        kind = d.x;
+        const Cut cut = cut_of(a, kind);
+        const int group = warp / cut.columns;
+        col = warp - group * cut.columns;
+        mine = group < cut.groups ? group * cut.halves + col / kStagePieces : -1;
+        local = col % kStagePieces;
+        stages = cut.groups * cut.halves;
+        steps = cut.steps;
+        pieces = cut.pieces;
+        rows = cut.rows;
+        above = group * (kind ? 32 : 16);
+        scales = (const float*)cut.scales;
       }
-      int kind, ai, tile;
-      place(unit, kind, ai, tile);
-      const Cut& cut = a.cut[kind];
-      const int e = s.expert[ai], n0 = tile * cut.step, np = passes(kind, s.count[ai]);
-      const int piece = warp % cut.columns, group = warp / cut.columns;
-      const bool active = group < cut.groups;
-      for (int p = 0; ok && p < np; ++p) {
-#pragma unroll
-        for (int m = 0; m < kTiles; ++m) c[m][0] = c[m][1] = c[m][2] = c[m][3] = 0.f;
-        for (int slab = 0; ok && slab < cut.slabs; ++slab) {
-          const int col = slab * cut.columns + piece;
-          const bool mine = active && col < cut.pieces;
-          const int want = cut.slabs == 1 ? (kind * kMaxE + ai) * kFewTokens + p : -2;
-          if (want != key || want == -2) {  // the activations are kept from one unit of an expert to the next
-            if (kind) ok = wait_count(f.done + ai, a.cut[0].units * passes(0, s.count[ai]), lane, &s_abort);
-            if (mine && ok) {
-              if (kind) load_h<FMT>(f, s, ai, p, col * Format<FMT>::kPiece, lane, b);
-              else load_x<FMT>(f, s, ai, p, col * Format<FMT>::kPiece, lane, b);
-            }
+      const int entry = d.y, n0 = d.z + above;
+      float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll 1
+      for (int step = 0; ok && step < steps; ++step) {
+        const int piece = step * kMulWarps + col;
+        const bool live = mine >= 0 && piece < pieces && n0 < rows;
+        float s0 = 1.f, s1 = 1.f;
+        if (live) {
+          if (FMT == MOE_FMT_FP8_B128_W8A16) {
+            const int e = s.expert[entry];
+            s0 = __ldg(scales + (size_t)((kind ? e * rows : 2 * e * rows) / 128 + n0 / 128) * pieces + piece);
+            s1 = kind ? s0 : __ldg(scales + (size_t)((2 * e + 1) * rows / 128 + n0 / 128) * pieces + piece);
+          }
+          const int want = (kind * kFewSlots + entry) << 16 | piece;
+          if (want != key) {  // the activations are kept from one unit to the next
             key = want;
+            if (kind == 0) {
+              load_x<FMT>(f, s, entry, piece * F::kPiece, lane, b);
+            } else {
+              if (ready != entry) ok = wait_count(f.done + entry, a.cut[0].rows / 16, lane, &s_abort);
+              ready = entry;
+              load_h<FMT>(f, s, entry, piece * F::kPiece, lane, b);
+            }
           }
-          if (ok && (slab > 0 || (cut.slabs > 1 && p > 0))) ok = acquire(it);
-          if (mine && ok) {
-            const char* sm = ring + (size_t)(it % a.stages) * a.stage_bytes;
-#pragma unroll
-            for (int m = 0; m < kTiles; ++m)
-              multiply<FMT>(cut, kind, sm, sm + cut.bytes, e, n0, group * kTiles + m, slab, piece, lane, b, c[m]);
-          }
-          if (ok && (cut.slabs > 1 || p == np - 1)) release(it++);
         }
-        if (ok) ok = post(unit, p, c, active ? &cut : nullptr, group, piece);
+        for (int i = 0; ok && i < stages; ++i) {
+          if (step + i > 0) acquire();
+          if (!ok) break;
+          if (live && i == mine) {
+            const char* sm = ring + slot * kStageBytes + local * F::kCodes;
+            const char* sc = ring + slot * kStageBytes + kStagePieces * F::kCodes + local * F::kScales;
+            multiply<FMT>(sm, sc, kind, s0, s1, lane, b, acc);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty[slot]);
+          if (++slot == F::kStages) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (kind) {  // both terms of h
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[m][i] += __shfl_down_sync(0xffffffffu, acc[m][i], 2);
+      }
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(&uempty[end_slot], end_phase, &s_abort));
+      if (!ok) break;
+      float4* to = parts + (end_slot * kMulWarps + warp) * 32 + (lane >> 2) * 2 + (lane & 3);
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        if ((lane & 3) < 2) to[16 * m] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
+      if (threadIdx.x == 0) s_unit[end_slot] = d;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ufull[end_slot]);
+      if (++end_slot == kEndWarps) {
+        end_slot = 0;
+        end_phase ^= 1;
+      }
+    }
+    for (int i = 0; ok && i < kEndWarps; ++i) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&uempty[end_slot], end_phase, &s_abort));
+      if (!ok) break;
+      if (threadIdx.x == 0) s_unit[end_slot] = make_int4(-1, 0, 0, 0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ufull[end_slot]);
+      if (++end_slot == kEndWarps) {
+        end_slot = 0;
+        end_phase ^= 1;
       }
     }
   } else {
     // ---------------- sums over the pieces, h and y, the combine ----------------
-    const int q = warp - kMulWarps, g = lane >> 2, t = lane & 3;
-    for (int u = 0;; ++u) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&ufull[q], u & 1, &s_abort))) break;
-      const int unit = *(volatile int*)&s_end[q][0], p = *(volatile int*)&s_end[q][1];
-      if (unit < 0) break;
-      int kind, ai, tile;
-      place(unit, kind, ai, tile);
-      const Cut& cut = a.cut[kind];
-      const int e = s.expert[ai], n0 = tile * cut.step, count = s.count[ai];
-      const int r = (kind ? 4 : 8) * p + 2 * t;  // the lane's columns are the expert's rows r and r + 1
-      const bool live[2] = {r < count && (!kind || t < 2), r + 1 < count && (!kind || t < 2)};
-      const int slot[2] = {s.rows[ai][live[0] ? r : 0], s.rows[ai][live[1] ? r + 1 : 0]};
-      float factor[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        factor[i] = FMT == MOE_FMT_BF16 ? 1.f : kind ? row_scale_inv(__ldcg(f.hmax + slot[i])) : f.xinv[slot[i] / f.k];
-        if (kind) factor[i] *= s.wt[slot[i]];
+    const int q = warp - kMulWarps, t = lane & 1;
+    int told = 0, told_kind = 0, told_entry = -1;  // 32-row tiles that are finished but not told of: a count, and with y which
+    auto tell = [&]() {
+      if (told == 0) return;
+      __syncwarp();
+      if (lane == 0) __threadfence();
+      __syncwarp();
+      if (told_kind == 0) {
+        if (lane == 0) atomicAdd(f.done + told_entry, told);
+      } else {
+        const bool last = lane < told && atomicAdd(f.tile + s_told[q][lane], 1) == s.entries - 1;
+        uint32_t mask = __ballot_sync(0xffffffffu, last);
+        if (mask) __threadfence();
+        for (; mask; mask &= mask - 1) {
+          const int n = 32 * s_told[q][__ffs(mask) - 1];
+          combine(f.y + n, f.out + n, f.ldo, f.T, f.k, f.d.H, lane);
+        }
       }
-      const float gs = FMT == MOE_FMT_NVFP4_W4A16 ? __ldg(cut.gs + e) : 1.f;
-      uint32_t hm[2] = {0, 0};
-      for (int m = 0; m < cut.mt; ++m) {
-        const float4* v = parts + q * kPartsPerUnit + m * cut.columns * 32 + lane;
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int i = 0; i < cut.columns; ++i) {
-          const float4 x = v[32 * i];
-          c[0] += x.x, c[1] += x.y, c[2] += x.z, c[3] += x.w;
-        }
-        if (kind) {  // both terms of h
+      told = 0;
+      __syncwarp();
+    };
+    bool live[2] = {false, false};
+    int slot[2] = {0, 0};
+    float factor[2] = {0.f, 0.f}, gs = 1.f;
+    for (int phase = 0;; phase ^= 1) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&ufull[q], phase, &s_abort))) break;
+      const int4 u = s_unit[q];
+      const int kind = u.x, entry = u.y, n1 = u.z, flush = u.w;
+      if (kind < 0) break;
+      const Cut cut = cut_of(a, kind);
+      if (kind != told_kind || entry != told_entry) {
+        if (kind == 0 || told_kind == 0) tell();
+        told_kind = kind;
+        told_entry = entry;
+        const int count = s.count[entry];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) c[i] += __shfl_down_sync(0xffffffffu, c[i], 2);
+        for (int i = 0; i < 2; ++i) {
+          live[i] = 2 * t + i < count;
+          slot[i] = s.rows[entry][live[i] ? 2 * t + i : 0];
+          factor[i] = kind == 0 ? (F::kBf16 ? 1.f : s.xinv[slot[i] / f.k]) : (F::kBf16 ? 1.f : row_scale_inv(__ldcg(f.hmax + slot[i]))) * s.wt[slot[i]];
         }
-        if (FMT == MOE_FMT_NVFP4_W4A16) {
+        if (F::kNvfp4) gs = __ldg(cut.gs + s.expert[entry]);
+      }
+      const int live_groups = min(cut.groups, (cut.rows - n1) / (kind ? 32 : 16));
+      for (int group = 0; group < live_groups; ++group) {
+        const float4* v = parts + (q * kMulWarps + group * cut.columns) * 32 + lane;
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+        for (int i = 0; i < cut.columns; ++i) {
+          const float4 w = v[32 * i];
+          c[0] += w.x, c[1] += w.y, c[2] += w.z, c[3] += w.w;
+        }
+        if (group + 1 == live_groups) {  // the warps may overwrite
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&uempty[q]);
+        }
+        if (F::kNvfp4) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) c[i] = c[i] / gs;
         }
-        if (kind == 0) {
-          const int n = n0 + 8 * m + g;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float gate = c[i] * factor[i], up = c[2 + i] * factor[i], h = gate / (1.f + expf(-gate)) * up;
-            if (live[i] && n < cut.rows) {
-              f.h[(size_t)slot[i] * cut.rows + n] = h;
-              hm[i] = max(hm[i], __float_as_uint(fabsf(h)));
-            }
-          }
-        } else {
-          const int n = n0 + 16 * m + g;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (live[i & 1] && n + 8 * (i >> 1) < cut.rows) f.y[(size_t)slot[i & 1] * cut.rows + n + 8 * (i >> 1)] = c[i] * factor[i & 1];
-        }
+        const int n0 = n1 + group * (kind ? 32 : 16);
+        finish_rows<FMT>(f, kind, cut.rows, n0, lane, c, live, slot, factor);
+        if (kind && lane == 0) s_told[q][told] = (uint16_t)(n0 / 32);
+        if (++told == kBatch) tell();
       }
-      if (kind == 0 && FMT != MOE_FMT_BF16) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int off = 4; off < 32; off <<= 1) hm[i] = max(hm[i], __shfl_xor_sync(0xffffffffu, hm[i], off));
-          if (g == 0 && live[i]) atomicMax(f.hmax + slot[i], hm[i]);
-        }
-      }
-      __syncwarp();
-      bool last = false;
-      if (lane == 0) {
-        mbar_arrive(&uempty[q]);
-        __threadfence();
-        if (kind == 0) atomicAdd(f.done + ai, 1);
-        else last = atomicAdd(f.tile + tile, 1) == s.down_passes - 1;
-      }
-      if (!__shfl_sync(0xffffffffu, last, 0)) continue;
-      __threadfence();
-      const int quads = min(cut.step, cut.rows - n0) / 4;
-      for (int i = lane; i < f.T * quads; i += 32) {
-        const int token = i / quads, n = n0 + 4 * (i % quads);
-        float o[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int j = 0; j < f.k; ++j) {
-          const float4 v = __ldcg((const float4*)(f.y + (size_t)(token * f.k + j) * cut.rows + n));
-          o[0] += v.x, o[1] += v.y, o[2] += v.z, o[3] += v.w;
-        }
-        __nv_bfloat162 w[2] = {__floats2bfloat162_rn(o[0], o[1]), __floats2bfloat162_rn(o[2], o[3])};
-        *(uint2*)(f.out + token * f.ldo + n) = *(const uint2*)w;
-      }
+      if (flush) tell();
     }
   }
   __syncthreads();
@@ -581,88 +648,70 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
 
 template <int FMT>
 bool make_cut(Args& a, int kind) {
-  const FewArgs& f = a.f;
-  const moe_packed_desc_t& d = f.d;
+  using F = Format<FMT>;
+  const moe_packed_desc_t& d = a.f.d;
   Cut& c = a.cut[kind];
-  const MatView v = mat_view(d, f.packed, kind);
-  c.K = kind ? d.I : d.H;
-  c.rows = kind ? d.H : d.I;
+  const MatView v = mat_view(d, a.f.packed, kind);
+  c.codes = (const char*)v.a;
   c.scales = (const char*)v.b;
   c.gs = v.gs;
-  c.pieces = c.K / Format<FMT>::kPiece;
-  c.columns = c.pieces < kColumns ? c.pieces : kColumns;
-  c.slabs = (c.pieces + c.columns - 1) / c.columns;
-  const int R = f.T * f.k, active = R < d.E ? R : d.E, sms = tc_num_sms();
-  // As many rows per unit as keep all the warps busy (128 at most), unless there are then fewer than four units for every SM.
+  c.N = v.N;
+  c.K = v.K;
+  c.rows = kind ? d.H : d.I;
+  c.pieces = c.K / F::kPiece;
+  c.columns = c.pieces < kMulWarps ? c.pieces : kMulWarps;
+  c.halves = (c.columns + kStagePieces - 1) / kStagePieces;
+  c.steps = (c.pieces + c.columns - 1) / c.columns;
+  // as many rows per unit as keep all the warps busy, unless there are then fewer than four units for every SM
+  const int R = a.f.T * a.f.k, active = R < d.E ? R : d.E;
   auto size = [&](int groups) {
     c.groups = groups;
-    c.mt = groups * Format<FMT>::kTiles;
-    c.step = (kind ? 16 : 8) * c.mt;
+    c.step = groups * (kind ? 32 : 16);
     c.units = (c.rows + c.step - 1) / c.step;
   };
-  size(kColumns / c.columns < 8 / Format<FMT>::kTiles ? kColumns / c.columns : 8 / Format<FMT>::kTiles);
-  while (c.groups > 1 && active * c.units < 4 * sms) size(c.groups / 2);
-  c.bytes = (uint32_t)c.mt * c.columns * 16 * Format<FMT>::kRowBytes;
-  const int per = active * c.units / (8 * sms);
-  c.run = per < 1 ? 1 : per > 8 ? 8 : per;
+  size(kMulWarps / c.columns);
+  while (c.groups > 1 && (long)active * c.units < 4l * tc_num_sms()) size(c.groups / 2);
 
-  const uint64_t E = d.E, N = v.N, K = c.K;
-  if (FMT == MOE_FMT_INT4_G128_W4A16) {
-    const uint32_t w = c.step, cols = c.columns;
+  const uint64_t E = d.E, N = v.N, K = c.K, rows = c.rows;
+  const uint32_t cols = c.columns < kStagePieces ? c.columns : kStagePieces;
+  const auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, U16 = CU_TENSOR_MAP_DATA_TYPE_UINT16, U32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
+  if (F::kInt4) {
     if (kind == 0) {
-      const uint64_t dims[4] = {(uint64_t)c.rows, 2, K / 8, E}, strides[3] = {4 * (uint64_t)c.rows, 4 * N, N * K / 2};
-      const uint32_t box[4] = {16, 2, 16 * cols, 1};
-      const uint64_t sdims[4] = {(uint64_t)c.rows, 2, K / 128, E}, sstrides[3] = {2 * (uint64_t)c.rows, 2 * N, N * K / 64};
-      const uint32_t sbox[4] = {w, 2, cols, 1};
-      return tc_make_map_nd(&a.map[0], CU_TENSOR_MAP_DATA_TYPE_UINT32, v.a, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B) &&
-             tc_make_map_nd(&a.smap[0], CU_TENSOR_MAP_DATA_TYPE_UINT16, v.b, 4, sdims, sstrides, sbox, CU_TENSOR_MAP_SWIZZLE_NONE);
+      const uint64_t dims[4] = {rows, 2, K / 8, E}, strides[3] = {4 * rows, 4 * N, N * K / 2};
+      const uint64_t sdims[4] = {rows, 2, K / 128, E}, sstrides[3] = {2 * rows, 2 * N, N * K / 64};
+      const uint32_t box[4] = {16, 2, 16 * cols, 1}, sbox[4] = {16, 2, cols, 1};
+      return tc_make_map_nd(&a.map[0], U32, v.a, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B) &&
+             tc_make_map_nd(&a.smap[0], U16, v.b, 4, sdims, sstrides, sbox, CU_TENSOR_MAP_SWIZZLE_NONE);
     }
     const uint64_t dims[3] = {N, K / 8, E}, strides[2] = {4 * N, N * K / 2};
-    const uint32_t box[3] = {32, 16 * cols, 1};
     const uint64_t sdims[3] = {N, K / 128, E}, sstrides[2] = {2 * N, N * K / 64};
-    const uint32_t sbox[3] = {w, cols, 1};
-    return tc_make_map_nd(&a.map[1], CU_TENSOR_MAP_DATA_TYPE_UINT32, v.a, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) &&
-           tc_make_map_nd(&a.smap[1], CU_TENSOR_MAP_DATA_TYPE_UINT16, v.b, 3, sdims, sstrides, sbox, CU_TENSOR_MAP_SWIZZLE_NONE);
+    const uint32_t box[3] = {32, 16 * cols, 1}, sbox[3] = {32, cols, 1};
+    return tc_make_map_nd(&a.map[1], U32, v.a, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) &&
+           tc_make_map_nd(&a.smap[1], U16, v.b, 3, sdims, sstrides, sbox, CU_TENSOR_MAP_SWIZZLE_NONE);
   }
-  const uint32_t rb = Format<FMT>::kRowBytes;
-  const uint64_t row = (uint64_t)c.pieces * rb;  // bytes of a matrix row
+  const uint64_t rb = F::kRowBytes, row = c.pieces * rb;  // bytes of a piece's row and of a whole one
   const CUtensorMapSwizzle sw = rb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
   if (kind == 0) {
-    const uint64_t dims[5] = {rb, (uint64_t)c.rows, 2, (uint64_t)c.pieces, E}, strides[4] = {row, row * c.rows, rb, row * N};
-    const uint32_t box[5] = {rb, (uint32_t)c.step, 2, (uint32_t)c.columns, 1};
-    return tc_make_map_nd(&a.map[0], CU_TENSOR_MAP_DATA_TYPE_UINT8, v.a, 5, dims, strides, box, sw);
+    const uint64_t dims[5] = {rb, rows, 2, (uint64_t)c.pieces, E}, strides[4] = {row, row * rows, rb, row * N};
+    const uint32_t box[5] = {(uint32_t)rb, 16, 2, cols, 1};
+    return tc_make_map_nd(&a.map[0], U8, v.a, 5, dims, strides, box, sw);
   }
   const uint64_t dims[4] = {rb, N, (uint64_t)c.pieces, E}, strides[3] = {row, rb, row * N};
-  const uint32_t box[4] = {rb, (uint32_t)c.step, (uint32_t)c.columns, 1};
-  return tc_make_map_nd(&a.map[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, v.a, 4, dims, strides, box, sw);
+  const uint32_t box[4] = {(uint32_t)rb, 32, cols, 1};
+  return tc_make_map_nd(&a.map[1], U8, v.a, 4, dims, strides, box, sw);
 }
 
 template <int FMT>
 cudaError_t launch(const FewArgs& f, cudaStream_t s) {
   static SmemOptIn opt_in;
-  if (const cudaError_t e = opt_in(few_experts_kernel<FMT>, (int)kSmemMax); e != cudaSuccess) return e;
+  if (const cudaError_t e = opt_in(few_experts_kernel<FMT>, Format<FMT>::kSmem); e != cudaSuccess) return e;
   Args a;
   a.f = f;
-  a.geom = score_geom(f.router, f.d.E);
-  a.stage_bytes = 0;
-  for (int kind = 0; kind < 2; ++kind) {
-    if (!make_cut<FMT>(a, kind)) return cudaErrorInvalidValue;
-    const Cut& c = a.cut[kind];
-    int bytes = (int)c.bytes;
-    if (FMT == MOE_FMT_NVFP4_W4A16) bytes += 16 * c.mt * (c.K / 16);
-    if (FMT == MOE_FMT_INT4_G128_W4A16) bytes += c.columns * 32 * c.mt;
-    bytes = (bytes + 1023) / 1024 * 1024;
-    if (bytes > a.stage_bytes) a.stage_bytes = bytes;
-  }
-  const size_t parts = (size_t)kEndWarps * Format<FMT>::kTiles * kColumns * 512;
-  a.stages = (int)((kSmemMax - 1024 - parts) / a.stage_bytes);
-  if (a.stages > kMaxStages) a.stages = kMaxStages;
-  if (a.stages < 2) return cudaErrorInvalidValue;
-  const int R = f.T * f.k, active = R < f.d.E ? R : f.d.E, sms = tc_num_sms();
-  const long units = (long)active * (a.cut[0].units + a.cut[1].units);
+  if (!make_cut<FMT>(a, 0) || !make_cut<FMT>(a, 1)) return cudaErrorInvalidValue;
+  const long R = (long)f.T * f.k, active = R < f.d.E ? R : f.d.E, sms = tc_num_sms();
+  const long most = active * (a.cut[0].units > a.cut[1].units ? a.cut[0].units : a.cut[1].units);
   note_launches(1);
-  return launch_pdl(few_experts_kernel<FMT>, dim3((unsigned)(units < sms ? units : sms)), dim3(kThreads),
-                    1024 + parts + (size_t)a.stages * a.stage_bytes, s, a);
+  return launch_pdl(few_experts_kernel<FMT>, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads), Format<FMT>::kSmem, s, a);
 }
 
 }  // namespace
