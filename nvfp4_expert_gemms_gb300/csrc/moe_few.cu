@@ -7,7 +7,6 @@ namespace moe {
 namespace {
 
 constexpr int kCluster = 8;          // blocks per token
-constexpr int kAhead = 4;            // pieces a lane loads before it multiplies them
 constexpr int kRouterWarps = 16, kRouterThreads = 32 * kRouterWarps;
 
 // Two sums at once, each kept as an unevaluated pair of fp32 numbers, hi + lo.  Adding p loses nothing: with s the rounded
@@ -46,8 +45,14 @@ __device__ __forceinline__ void add_pair(float& hi, float& lo, float ohi, float 
   hi = s;
 }
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// *p of the cluster's first block
+__device__ __forceinline__ void store_in_first(float* p, float v) {
+  asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, 0;\n st.shared::cluster.f32 [a], %1;\n}" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(p)),
+               "f"(v)
+               : "memory");
 }
 
 // Eight bf16 or fp16 elements as fp32.
@@ -62,31 +67,37 @@ __device__ __forceinline__ void unpack8(const uint4& u, bool f16, float2 (&w)[4]
 //   logits[t, e] = sum over h of x[t, h] w[e, h], a warp per expert.  The sum is carried in pairs, so that it is the exact sum
 //   rounded once (but for one case in some 2^20): which experts a token gets must not hang on the order of a sum.
 // Eight blocks of sixteen warps per token because one token's products (E H of them, seven operations each for two) would
-// take one SM several microseconds.  Past fp32's range lo is not a number and hi alone counts.  Block 0 zeroes the counters.
-template <int VT>
-__global__ void __launch_bounds__(kRouterThreads, 1) few_router_kernel(const __grid_constant__ FewArgs a, const ScoreGeom geom, int zero_words) {
+// take one SM several microseconds; the logits go straight to the first block's shared memory, where one warp chooses.  Past fp32's range lo is not a number and hi alone counts.  h and y are filled with
+// the mark of what is not there yet.
+template <int VT, bool F32>
+__global__ void __launch_bounds__(kRouterThreads, 1) few_router_kernel(const __grid_constant__ FewArgs a, const ScoreGeom geom, size_t pieces) {
   __shared__ ScoreScratch scratch;
+  __shared__ __align__(16) float s_logits[kMaxE];  // the first block's
+  constexpr int kAhead = F32 ? 4 : 8;  // pieces of eight a lane loads before it multiplies them
   __shared__ uint32_t s_max[kRouterWarps];
   const int t = blockIdx.x / kCluster, rank = blockIdx.x % kCluster, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H = a.d.H, E = a.d.E;
   const __nv_bfloat16* x = a.x + t * a.ldx;
+  cluster_arrive();  // the first block's shared memory is there once all have started
   pdl_wait();
   pdl_trigger();
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < zero_words; i += kRouterThreads) a.status[i] = 0;
+  if (blockIdx.x == 0 && threadIdx.x < 2) a.status[threadIdx.x] = 0;
+  for (size_t i = blockIdx.x * kRouterThreads + threadIdx.x; i < pieces; i += gridDim.x * kRouterThreads)
+    ((uint4*)a.h)[i] = make_uint4(kFewUnset, kFewUnset, kFewUnset, kFewUnset);
+  cluster_wait();
   for (int e = rank * kRouterWarps + warp; e < E; e += kCluster * kRouterWarps) {
     Pairs sum;
     for (int i0 = 8 * lane; i0 < H; i0 += 256 * kAhead) {  // a lane's pieces of eight, the loads of kAhead of them first
-      uint4 u[kAhead], w[2 * kAhead];
+      uint4 u[kAhead], w[F32 ? 2 * kAhead : kAhead];
 #pragma unroll
       for (int n = 0; n < kAhead; ++n) {
         const int i = i0 + 256 * n;
         if (i >= H) break;
         u[n] = *(const uint4*)(x + i);
-        if (a.w_dtype == MOE_DT_F32) {
+        if constexpr (F32) {
           const uint4* p = (const uint4*)((const float*)a.wr + e * a.ldw + i);
           w[2 * n] = p[0], w[2 * n + 1] = p[1];
         } else {
-          w[2 * n] = *(const uint4*)((const uint16_t*)a.wr + e * a.ldw + i);
+          w[n] = *(const uint4*)((const uint16_t*)a.wr + e * a.ldw + i);
         }
       }
 #pragma unroll
@@ -94,12 +105,15 @@ __global__ void __launch_bounds__(kRouterThreads, 1) few_router_kernel(const __g
         if (i0 + 256 * n >= H) break;
         float2 xv[4], wv[4];
         unpack8(u[n], false, xv);
-        if (a.w_dtype == MOE_DT_F32) {
-          const float2* p = (const float2*)(w + 2 * n);
+        if constexpr (F32) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sum.add_wide_product(xv[j], p[j]);
+          for (int j = 0; j < 4; ++j) {
+            const uint4& q = w[2 * n + j / 2];
+            wv[j] = j % 2 ? make_float2(__uint_as_float(q.z), __uint_as_float(q.w)) : make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+            sum.add_wide_product(xv[j], wv[j]);
+          }
         } else {
-          unpack8(w[2 * n], a.w_dtype == MOE_DT_F16, wv);
+          unpack8(w[n], a.w_dtype == MOE_DT_F16, wv);
 #pragma unroll
           for (int j = 0; j < 4; ++j) sum.add_product(xv[j], wv[j]);
         }
@@ -112,8 +126,10 @@ __global__ void __launch_bounds__(kRouterThreads, 1) few_router_kernel(const __g
       const float ohi = __shfl_xor_sync(0xffffffffu, hi, off), olo = __shfl_xor_sync(0xffffffffu, lo, off);
       add_pair(hi, lo, ohi, olo);
     }
-    if (lane == 0) a.logits[(size_t)t * E + e] = isfinite(hi) ? __fadd_rn(hi, lo) : hi;
+    if (lane == 0) store_in_first(s_logits + e, isfinite(hi) ? __fadd_rn(hi, lo) : hi);
   }
+  __syncwarp();
+  cluster_arrive();
   if (rank == 1 && few_scales_x(a.d.fmt)) {  // the row for the experts
     uint32_t m = 0;
     for (int i = threadIdx.x; i < H / 8; i += kRouterThreads) {
@@ -138,8 +154,12 @@ __global__ void __launch_bounds__(kRouterThreads, 1) few_router_kernel(const __g
       *(uint4*)(a.xs + (size_t)t * H + 8 * i) = *(const uint4*)o;
     }
   }
-  cluster_sync();
-  if (rank == 0 && warp == 0) score_token<VT, true>(a.router, geom, t, a.k, lane, a.idx, a.wt, scratch);
+  cluster_wait();
+  if (rank == 0 && warp == 0) {
+    ScoreArgs r = a.router;
+    r.logits = s_logits;
+    score_token<VT>(r, geom, 0, a.k, lane, a.idx + t * a.k, a.wt + t * a.k, scratch);
+  }
 }
 
 }  // namespace
@@ -154,14 +174,9 @@ FewLayout few_layout(const moe_packed_desc_t& d, int T, int k) {
   };
   const size_t R = (size_t)T * k;
   L.status = take(256);
-  L.done = take(4 * R);
-  L.tile = take(4 * (size_t)(d.H / 32));
-  L.hmax = take(4 * R);
-  L.zero_end = cur;
   L.idx = take(4 * R);
   L.wt = take(4 * R);
   L.xinv = take(4 * (size_t)T);
-  L.logits = take(4 * (size_t)T * d.E);
   L.xs = take(few_scales_x(d.fmt) ? 2 * (size_t)T * d.H : 0);
   L.h = take(4 * R * d.I);
   L.y = take(4 * R * (size_t)d.H);
@@ -169,7 +184,7 @@ FewLayout few_layout(const moe_packed_desc_t& d, int T, int k) {
   return L;
 }
 
-cudaError_t launch_few_router(const FewArgs& a, size_t zero_bytes, cudaStream_t s) {
+cudaError_t launch_few_router(const FewArgs& a, size_t fill_bytes, cudaStream_t s) {
   const ScoreGeom g = score_geom(a.router, a.d.E);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.T * kCluster);
@@ -183,13 +198,14 @@ cudaError_t launch_few_router(const FewArgs& a, size_t zero_bytes, cudaStream_t 
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const int words = (int)(zero_bytes / 4);
+  const size_t pieces = fill_bytes / 16;
   note_launches(1);
-  if (g.per <= 1) return cudaLaunchKernelEx(&cfg, few_router_kernel<1>, a, g, words);
-  if (g.per <= 2) return cudaLaunchKernelEx(&cfg, few_router_kernel<2>, a, g, words);
-  if (g.per <= 4) return cudaLaunchKernelEx(&cfg, few_router_kernel<4>, a, g, words);
-  if (g.per <= 8) return cudaLaunchKernelEx(&cfg, few_router_kernel<8>, a, g, words);
-  return cudaLaunchKernelEx(&cfg, few_router_kernel<16>, a, g, words);
+  const bool f32 = a.w_dtype == MOE_DT_F32;
+  if (g.per <= 1) return cudaLaunchKernelEx(&cfg, f32 ? few_router_kernel<1, true> : few_router_kernel<1, false>, a, g, pieces);
+  if (g.per <= 2) return cudaLaunchKernelEx(&cfg, f32 ? few_router_kernel<2, true> : few_router_kernel<2, false>, a, g, pieces);
+  if (g.per <= 4) return cudaLaunchKernelEx(&cfg, f32 ? few_router_kernel<4, true> : few_router_kernel<4, false>, a, g, pieces);
+  if (g.per <= 8) return cudaLaunchKernelEx(&cfg, f32 ? few_router_kernel<8, true> : few_router_kernel<8, false>, a, g, pieces);
+  return cudaLaunchKernelEx(&cfg, f32 ? few_router_kernel<16, true> : few_router_kernel<16, false>, a, g, pieces);
 }
 
 }  // namespace moe
@@ -236,16 +252,12 @@ extern "C" moe_status_t moe_layer_few(const void* x, int64_t ldx, const void* w_
   a.idx = topk_idx ? topk_idx : (int32_t*)(ws + L.idx);
   a.wt = topk_w ? topk_w : (float*)(ws + L.wt);
   a.status = (int*)(ws + L.status);
-  a.done = (int*)(ws + L.done);
-  a.tile = (int*)(ws + L.tile);
-  a.hmax = (unsigned*)(ws + L.hmax);
   a.xinv = (float*)(ws + L.xinv);
-  a.logits = (float*)(ws + L.logits);
   a.xs = (__half*)(ws + L.xs);
   a.h = (float*)(ws + L.h);
   a.y = (float*)(ws + L.y);
-  a.router = {*router, a.logits, E, MOE_DT_F32, bias};
-  cudaError_t e = launch_few_router(a, L.zero_end, (cudaStream_t)stream);
+  a.router = {*router, workspace, E, MOE_DT_F32, bias};  // (the logits stay in shared memory)
+  cudaError_t e = launch_few_router(a, L.total - L.h, (cudaStream_t)stream);
   if (e == cudaSuccess) e = launch_few_experts(a, (cudaStream_t)stream);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

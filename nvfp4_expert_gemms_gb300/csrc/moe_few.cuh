@@ -15,10 +15,18 @@ namespace moe {
 constexpr int kFewTokens = MOE_FEW_MAX_TOKENS;
 constexpr int kFewSlots = kFewTokens * kMaxTopK;  // (token, choice) pairs
 
-// Byte offsets in the workspace.  status: the device error word (as in ws_layout), the ticket counter; zero .. zero_end:
-// what the first kernel zeroes with them.
+// What h and y hold before they are there: a NaN that is never written (few_value), so that whoever needs them can see from
+// the values alone whether they are, with no flag to fence.
+constexpr uint32_t kFewUnset = 0xFFFFFFFFu;
+__device__ __forceinline__ uint32_t few_value(float v) {
+  const uint32_t bits = __float_as_uint(v);
+  return bits == kFewUnset ? 0x7FFFFFFFu : bits;
+}
+
+// Byte offsets in the workspace.  status: the device error word (as in ws_layout), the ticket counter; h and what follows is
+// filled with kFewUnset.
 struct FewLayout {
-  size_t status, done, tile, hmax, zero_end, idx, wt, xinv, logits, xs, h, y, total;
+  size_t status, idx, wt, xinv, xs, h, y, total;
 };
 FewLayout few_layout(const moe_packed_desc_t& d, int T, int k);
 
@@ -33,20 +41,16 @@ struct FewArgs {
   __nv_bfloat16* out;
   int64_t ldo;
   int T, k;
-  ScoreArgs router;  // its logits are the first kernel's [T, E]
+  ScoreArgs router;  // its logits are the first kernel's own
   int32_t* idx;      // [T, k]: the choice
   float* wt;
   int* status;       // [0] error word, [1] tickets handed out
-  int* done;         // [entry]: 16-feature tiles of its h that are finished
-  int* tile;         // [32-column tile of y]: entries that are finished
-  unsigned* hmax;    // [T k]: largest |h| of a slot, as bits
-  float* logits;     // [T, E]
   __half* xs;        // [T, H]: x scaled by a power of two per row (bf16 weights: unused)
   float* xinv;       // [T]: the scale's inverse
   float* h;          // [T k, I]
   float* y;          // [T k, H]: weighted rows
 };
-cudaError_t launch_few_router(const FewArgs& a, size_t zero_bytes, cudaStream_t s);
+cudaError_t launch_few_router(const FewArgs& a, size_t fill_bytes, cudaStream_t s);
 cudaError_t launch_few_experts(const FewArgs& a, cudaStream_t s);
 
 __host__ __device__ inline bool few_scales_x(int fmt) { return fmt != MOE_FMT_BF16; }

@@ -9,11 +9,15 @@
 // are few units) and asks for the next one as it starts a run.
 //
 // One warp of a block copies by TMA, eight pieces of 128 columns (64 of bf16) by 32 rows to a stage of shared memory,
-// 108 to 192 KB ahead (HBM's rate and latency ask for some 45), into the down matrices while h is not there yet.  Sixteen warps
+// 144 to 192 KB ahead (HBM's rate and latency ask for some 45), into the down matrices while h is not there yet.  Sixteen warps
 // take a piece of a unit each, decode it straight into MMA operands, multiply it with the entry's tokens, whose operands stay in
-// registers from unit to unit, and leave their sums in shared memory.  Three more take the units in turn, add
-// the sums up and finish the rows: h = silu(gate) up, or weighted rows of y; they tell other blocks once per run.  The
-// block that finishes the last entry of 32 output columns sums them over each token's experts, in their order.
+// registers from unit to unit, and leave their sums in shared memory.  Three more take the units in turn, add the sums up
+// and finish the rows: h = silu(gate) up, or weighted rows of y.  What copied sums y over each token's experts at the end,
+// in their order.
+//
+// h and y carry no flags: a value that is not there yet is a NaN that is never written, and who needs it loads until it has
+// changed.  With counters behind fences in their place a block's units took up to half as long again (134 us for 90 at 16
+// tokens of FP8, 128 experts of 2048 x 768, whichever warp fenced); a fence waits for the SM's traffic.
 //
 // What it takes: every warp's work on a unit is a chain of latencies, about 1000 cycles, where HBM brings a unit of FP8 in 2800
 // and one of four bits in 1500.  So nothing in that chain may wait for L2: no spilled register (with 222 KB of
@@ -28,11 +32,12 @@ using namespace tc;
 
 namespace {
 
-constexpr int kMulWarps = 16, kEndWarps = 3, kCopyWarp = kMulWarps + kEndWarps, kWarps = kCopyWarp + 1, kThreads = 32 * kWarps;
+constexpr int kMulWarps = 16, kEndWarps = 3, kCopyWarp = kMulWarps + kEndWarps;
+constexpr int kWarps = kCopyWarp + 1, kThreads = 32 * kWarps;
 constexpr int kEntryRows = 4;
 constexpr int kStagePieces = 8;
 constexpr int kMaxStages = 8;
-constexpr int kBatch = 32;  // tiles of 32 columns of y a finishing warp tells about at once
+constexpr int kTokens = 4;  // per combined piece of 32 columns
 
 template <int FMT>
 struct Format {
@@ -140,27 +145,73 @@ __device__ __forceinline__ void load_x(const FewArgs& f, const Tables& s, int en
   }
 }
 
-// ... or h: the nearest fp16 (bf16) of each in the columns 0 .. 3, what is left in 4 .. 7.
+// Four values that other blocks write, as they are now.
+__device__ __forceinline__ uint4 load_now(const float* p) {
+  uint4 v;
+  asm volatile("ld.relaxed.gpu.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ bool all_set(const uint4& v) { return v.x != kFewUnset && v.y != kFewUnset && v.z != kFewUnset && v.w != kFewUnset; }
+__device__ __forceinline__ void store_now(float* p, float v) {
+  asm volatile("st.relaxed.gpu.global.b32 [%0], %1;" ::"l"(p), "r"(few_value(v)) : "memory");
+}
+// A wait's clock: true once it has run out, or another thread of the block has given up.
+struct Patience {
+  long long since = 0;
+  __device__ __forceinline__ bool over(volatile int* abort) {
+    const long long now = clock64();
+    if (since == 0) since = now;
+    if (now - since > kWaitLimitCycles) *abort = 1;
+    __nanosleep(100);
+    return *abort;
+  }
+};
+
+// ... or h, once it is there: the nearest fp16 (bf16) of each in the columns 0 .. 3, what is left in 4 .. 7, after scaling by a power of
+// two per row of the piece; inv: its inverse for the rows of the lane's MMA columns 2 t and 2 t + 1.  False if it never came.
 template <int FMT>
-__device__ __forceinline__ void load_h(const FewArgs& f, const Tables& s, int entry, int col, int lane, uint32_t (&b)[Format<FMT>::kRegs]) {
+__device__ __forceinline__ bool load_h(const FewArgs& f, const Tables& s, int entry, int col, int lane, uint32_t (&b)[Format<FMT>::kRegs],
+                                       float (&inv)[2], volatile int* abort) {
   const int g = lane >> 2, t = lane & 3, r = g & 3;
   const bool live = r < s.count[entry], low = g >= 4;
-  const int slot = s.rows[entry][live ? r : 0];
-  const float* row = f.h + (size_t)slot * f.d.I + col;
-  const float scale = Format<FMT>::kBf16 ? 1.f : row_scale(__ldcg(f.hmax + slot));
+  const float* row = f.h + (size_t)s.rows[entry][live ? r : 0] * f.d.I + col;
+  uint4 v[Format<FMT>::kRegs / 2];
+  for (Patience p;;) {
+    bool set = true;
+#pragma unroll
+    for (int j = 0; j < Format<FMT>::kRegs / 4; ++j) {
+      v[2 * j] = load_now(row + element<FMT>(t, j));
+      v[2 * j + 1] = load_now(row + element<FMT>(t, j) + 4);
+    }
+#pragma unroll
+    for (int j = 0; j < Format<FMT>::kRegs / 2; ++j) set = set && all_set(v[j]);
+    if (__all_sync(0xffffffffu, set)) break;
+    if (__any_sync(0xffffffffu, p.over(abort))) return false;
+  }
+  float scale = 1.f;
+  if (!Format<FMT>::kBf16) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < Format<FMT>::kRegs / 2; ++j)
+      m = max(m, max(max(v[j].x & 0x7FFFFFFFu, v[j].y & 0x7FFFFFFFu), max(v[j].z & 0x7FFFFFFFu, v[j].w & 0x7FFFFFFFu)));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    scale = row_scale(m);
+    const float back = row_scale_inv(m);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) inv[i] = __shfl_sync(0xffffffffu, back, 4 * ((2 * t + i) & 3));
+  }
 #pragma unroll
   for (int j = 0; j < Format<FMT>::kRegs / 4; ++j) {
-    const float4* p = (const float4*)(row + element<FMT>(t, j));
-    const float4 u0 = live ? __ldcg(p) : make_float4(0, 0, 0, 0), u1 = live ? __ldcg(p + 1) : make_float4(0, 0, 0, 0);
-    const float v[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+    const uint32_t w[8] = {v[2 * j].x, v[2 * j].y, v[2 * j].z, v[2 * j].w, v[2 * j + 1].x, v[2 * j + 1].y, v[2 * j + 1].z, v[2 * j + 1].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      const float x = live ? __uint_as_float(w[2 * i]) * scale : 0.f, y = live ? __uint_as_float(w[2 * i + 1]) * scale : 0.f;
       if (Format<FMT>::kBf16) {
-        __nv_bfloat162 hi = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        if (low) hi = __floats2bfloat162_rn(v[2 * i] - __low2float(hi), v[2 * i + 1] - __high2float(hi));
+        __nv_bfloat162 hi = __floats2bfloat162_rn(x, y);
+        if (low) hi = __floats2bfloat162_rn(x - __low2float(hi), y - __high2float(hi));
         b[4 * j + i] = *(const uint32_t*)&hi;
       } else {
-        const float x = v[2 * i] * scale, y = v[2 * i + 1] * scale;
         __half2 hi = __floats2half2_rn(x, y);
         if (low) hi = __floats2half2_rn(x - __low2float(hi), y - __high2float(hi));
         b[4 * j + i] = *(const uint32_t*)&hi;
@@ -168,13 +219,14 @@ __device__ __forceinline__ void load_h(const FewArgs& f, const Tables& s, int en
     }
     order_pairs<FMT>(b + 4 * j);
   }
+  return true;
 }
 
 // acc += a piece of 32 rows at `sm` (its scales at `sc`) times the activations.  Tile m's MMA rows g and g + 8 are gate and up
-// n0 + 8 m + g of the features, or outputs n0 + 16 m + g and 8 further on.
+// n0 + 8 m + g of the features, or outputs n0 + 16 m + g and 8 further on.  inv: what the two columns' activations were scaled by.
 template <int FMT>
-__device__ __forceinline__ void multiply(const char* sm, const char* sc, int kind, float s0, float s1, int lane, const uint32_t (&b)[Format<FMT>::kRegs],
-                                         float (&acc)[2][4]) {
+__device__ __forceinline__ void multiply(const char* sm, const char* sc, int kind, float s0, float s1, const float (&inv)[2], int lane,
+                                         const uint32_t (&b)[Format<FMT>::kRegs], float (&acc)[2][4]) {
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
@@ -233,28 +285,10 @@ __device__ __forceinline__ void multiply(const char* sm, const char* sc, int kin
         }
       }
     }
-    acc[m][0] = fmaf(p[0], s0, acc[m][0]), acc[m][1] = fmaf(p[1], s0, acc[m][1]);
-    acc[m][2] = fmaf(p[2], s1, acc[m][2]), acc[m][3] = fmaf(p[3], s1, acc[m][3]);
+    // (the scales one after the other: their product may be below fp32's range where the sums are not)
+    acc[m][0] = fmaf(p[0] * s0, inv[0], acc[m][0]), acc[m][1] = fmaf(p[1] * s0, inv[1], acc[m][1]);
+    acc[m][2] = fmaf(p[2] * s1, inv[0], acc[m][2]), acc[m][3] = fmaf(p[3] * s1, inv[1], acc[m][3]);
   }
-}
-
-// Whole warp: wait until *p >= want (bounded).
-__device__ __forceinline__ bool wait_count(const int* p, int want, int lane, volatile int* abort) {
-  bool ok = true;
-  if (lane == 0) {
-    const long long t0 = clock64();
-    int v;
-    for (int i = 0;; ++i) {
-      asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-      if (v >= want) break;
-      if ((i & 63) == 63 && (*abort || clock64() - t0 > kWaitLimitCycles)) {
-        *abort = 1;
-        ok = false;
-        break;
-      }
-    }
-  }
-  return __shfl_sync(0xffffffffu, ok, 0);
 }
 
 // The entries, from every token's experts, in shared memory.
@@ -310,45 +344,48 @@ __device__ __forceinline__ void make_entries(const FewArgs& f, Tables& s) {
 
 // Finishes 32 rows of an entry (one warp): lane 16 m + 2 g + t (t < 2) holds tile m's sums of its rows g and g + 8 for the
 // entry's rows 2 t and 2 t + 1.  n0: the first feature or output; factor: what the two rows' sums are multiplied with.
-template <int FMT>
 __device__ __forceinline__ void finish_rows(const FewArgs& f, int kind, int rows, int n0, int lane, const float (&c)[4], const bool (&live)[2],
                                             const int (&slot)[2], const float (&factor)[2]) {
   const int m = lane >> 4, g = lane >> 1 & 7;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     if (kind == 0) {
-      const float gate = c[i] * factor[i], up = c[2 + i] * factor[i], h = gate / (1.f + expf(-gate)) * up;
-      if (live[i]) f.h[(size_t)slot[i] * rows + n0 + 8 * m + g] = h;
-      if (!Format<FMT>::kBf16) {
-        uint32_t hm = __float_as_uint(fabsf(h));
-#pragma unroll
-        for (int off = 2; off < 32; off <<= 1) hm = max(hm, __shfl_xor_sync(0xffffffffu, hm, off));  // all features of the row
-        if (lane < 2 && live[i]) atomicMax(f.hmax + slot[i], hm);
-      }
+      const float gate = c[i] * factor[i], up = c[2 + i] * factor[i];
+      if (live[i]) store_now(f.h + (size_t)slot[i] * rows + n0 + 8 * m + g, gate / (1.f + expf(-gate)) * up);
     } else if (live[i]) {
       float* y = f.y + (size_t)slot[i] * rows + n0 + 16 * m + g;
-      y[0] = c[i] * factor[i];
-      y[8] = c[2 + i] * factor[i];
+      store_now(y, c[i] * factor[i]);
+      store_now(y + 8, c[2 + i] * factor[i]);
     }
   }
 }
 
-// out for 32 columns, y and out pointing at the first, of every token (one warp).
-__device__ __noinline__ void combine(const float* y, __nv_bfloat16* out, int64_t ldo, int T, int k, int H, int lane) {
-  for (int i = lane; i < T * 8; i += 32) {  // four outputs of a token
-    const int token = i >> 3, n = 4 * (i & 7);
-    const float* at = y + (size_t)token * k * H + n;
-    float4 v[kMaxTopK];
+// out for 32 columns of four tokens, a lane for four columns of one (one warp): the token's rows of y, once they are there,
+// in their order.  False if they never came.
+__device__ __noinline__ bool combine(const float* y, __nv_bfloat16* out, int64_t ldo, int T, int k, int H, int lane, volatile int* abort) {
+  const int token = lane >> 3, n = 4 * (lane & 7);
+  const bool live = token < T;
+  const float* at = y + (size_t)(live ? token : 0) * k * H + n;
+  uint4 v[kMaxTopK];
+  for (Patience p;;) {
+    bool set = true;
 #pragma unroll
     for (int j = 0; j < kMaxTopK; ++j)
-      if (j < k) v[j] = __ldcg((const float4*)(at + (size_t)j * H));
-    float o[4] = {0.f, 0.f, 0.f, 0.f};
+      if (j < k) v[j] = load_now(at + (size_t)j * H);
 #pragma unroll
     for (int j = 0; j < kMaxTopK; ++j)
-      if (j < k) o[0] += v[j].x, o[1] += v[j].y, o[2] += v[j].z, o[3] += v[j].w;
-    __nv_bfloat162 w[2] = {__floats2bfloat162_rn(o[0], o[1]), __floats2bfloat162_rn(o[2], o[3])};
-    *(uint2*)(out + token * ldo + n) = *(const uint2*)w;
+      if (j < k) set = set && all_set(v[j]);
+    if (__all_sync(0xffffffffu, set)) break;
+    if (__any_sync(0xffffffffu, p.over(abort))) return false;
   }
+  float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < kMaxTopK; ++j)
+    if (j < k)
+      o[0] += __uint_as_float(v[j].x), o[1] += __uint_as_float(v[j].y), o[2] += __uint_as_float(v[j].z), o[3] += __uint_as_float(v[j].w);
+  const __nv_bfloat162 w[2] = {__floats2bfloat162_rn(o[0], o[1]), __floats2bfloat162_rn(o[2], o[3])};
+  if (live) *(uint2*)(out + token * ldo + n) = *(const uint2*)w;
+  return true;
 }
 
 template <int FMT>
@@ -357,10 +394,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
   constexpr int kStageBytes = (F::kStage + 1023) / 1024 * 1024;
   extern __shared__ __align__(1024) char smem_raw[];
   __shared__ Tables s;
-  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], ufull[kEndWarps], uempty[kEndWarps];
-  __shared__ int4 s_stage[kMaxStages], s_unit[kEndWarps];  // matrix (-1: no more), entry, first row, among the last of its run
+  __shared__ uint64_t said[kMaxStages], full[kMaxStages], empty[kMaxStages], ufull[kEndWarps], uempty[kEndWarps];
+  __shared__ int4 s_stage[kMaxStages], s_unit[kEndWarps];  // matrix (-1: no more), entry, first row
   __shared__ int s_abort;
-  __shared__ uint16_t s_told[kEndWarps][kBatch];
   char* ring = (char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   float4* parts = (float4*)(ring + F::kStages * kStageBytes);  // [unit % 3][warp][tile][16]
   const FewArgs& f = a.f;
@@ -368,6 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
 
   if (threadIdx.x == 0) {
     for (int j = 0; j < F::kStages; ++j) {
+      mbar_init(&said[j], 1);
       mbar_init(&full[j], F::kNvfp4 ? 33 : 1);
       mbar_init(&empty[j], kMulWarps);
     }
@@ -394,9 +431,12 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
     int slot = 0, phase = 1, armed = 0;
     bool ok = true;
     // the next stage, free; the descriptor is its first stage's
-    auto take_stage = [&](int kind, int entry, int row, int flush) {
+    auto take_stage = [&](int kind, int entry, int row) {
       ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], phase, &s_abort));
-      if (ok && lane == 0) s_stage[slot] = make_int4(kind, entry, row, flush);
+      if (ok && lane == 0) {
+        s_stage[slot] = make_int4(kind, entry, row, 0);
+        mbar_arrive(&said[slot]);
+      }
       __syncwarp();
       return ok;
     };
@@ -422,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
         for (int step = 0; ok && step < cut.steps; ++step)
           for (int group = 0; ok && group < cut.groups; ++group)
             for (int half = 0; ok && half < cut.halves; ++half) {
-              if (!take_stage(kind, entry, row, end - unit <= kEndWarps)) break;
+              if (!take_stage(kind, entry, row)) break;
               char* to = ring + slot * kStageBytes;
               const int r = row + group * (kind ? 32 : 16), piece = step * kMulWarps + half * kStagePieces;
               const int count = min(kStagePieces, cut.columns - half * kStagePieces);  // pieces the maps bring (their box)
@@ -460,11 +500,15 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
       }
       if (!ok) break;
     }
-    if (ok && take_stage(-1, 0, 0, 0)) {
-      if (F::kNvfp4) mbar_arrive(&full[slot]);
-      if (lane == 0) mbar_arrive(&full[slot]);
+    if (ok) take_stage(-1, 0, 0);
+    // the combine, in tickets of its own behind all others
+    const int sets = (f.T + kTokens - 1) / kTokens, pieces = f.d.H / 32 * sets;
+    for (int t = __shfl_sync(0xffffffffu, ticket, 0) - n0 - n1; ok && t < pieces;) {
+      if (lane == 0) ticket = atomicAdd(f.status + 1, 1);
+      const int n = 32 * (t / sets), token = kTokens * (t % sets);
+      ok = combine(f.y + (size_t)token * f.k * f.d.H + n, f.out + token * f.ldo + n, f.ldo, f.T - token, f.k, f.d.H, lane, &s_abort);
+      t = __shfl_sync(0xffffffffu, ticket, 0) - n0 - n1;
     }
-    __syncwarp();
     if (F::kNvfp4) cp_async_wait<0>();
     if (lane == 0 && s_abort) {  // let every issued copy land before shared memory goes away
       volatile int no_abort = 0;
@@ -474,15 +518,16 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
     __syncwarp();
   } else if (warp < kMulWarps) {
     // ---------------- pieces: decode and multiply ----------------
-    int slot = 0, phase = 0, end_slot = 0, end_phase = 1, ready = -1, key = -1;
+    int slot = 0, phase = 0, end_slot = 0, end_phase = 1, key = -1;
     uint32_t b[F::kRegs];
+    float inv[2] = {1.f, 1.f};
     bool ok = true;
-    auto acquire = [&]() { ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], phase, &s_abort)); };
+    auto acquire = [&](uint64_t* bar) { ok = ok && __all_sync(0xffffffffu, mbar_wait(&bar[slot], phase, &s_abort)); };
     // this matrix's share of the warp: its stage of each step, its place in it; what it takes to find its scales
     int kind = -1, mine = 0, local = 0, col = 0, stages = 0, steps = 0, pieces = 0, rows = 0, above = 0;
     const float* scales = nullptr;
     for (;;) {
-      acquire();
+      acquire(said);  // the unit is known, its weights may still be on their way
       if (!ok) break;
       const int4 d = s_stage[slot];
       if (d.x < 0) break;
@@ -516,22 +561,17 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
           const int want = (kind * kFewSlots + entry) << 16 | piece;
           if (want != key) {  // the activations are kept from one unit to the next
             key = want;
-            if (kind == 0) {
-              load_x<FMT>(f, s, entry, piece * F::kPiece, lane, b);
-            } else {
-              if (ready != entry) ok = wait_count(f.done + entry, a.cut[0].rows / 16, lane, &s_abort);
-              ready = entry;
-              load_h<FMT>(f, s, entry, piece * F::kPiece, lane, b);
-            }
+            if (kind == 0) load_x<FMT>(f, s, entry, piece * F::kPiece, lane, b);
+            else ok = load_h<FMT>(f, s, entry, piece * F::kPiece, lane, b, inv, &s_abort);
           }
         }
         for (int i = 0; ok && i < stages; ++i) {
-          if (step + i > 0) acquire();
+          acquire(full);
           if (!ok) break;
           if (live && i == mine) {
             const char* sm = ring + slot * kStageBytes + local * F::kCodes;
             const char* sc = ring + slot * kStageBytes + kStagePieces * F::kCodes + local * F::kScales;
-            multiply<FMT>(sm, sc, kind, s0, s1, lane, b, acc);
+            multiply<FMT>(sm, sc, kind, s0, s1, inv, lane, b, acc);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&empty[slot]);
@@ -573,51 +613,31 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
       }
     }
   } else {
-    // ---------------- sums over the pieces, h and y, the combine ----------------
+    // ---------------- sums over the pieces, h and y ----------------
     const int q = warp - kMulWarps, t = lane & 1;
-    int told = 0, told_kind = 0, told_entry = -1;  // 32-row tiles that are finished but not told of: a count, and with y which
-    auto tell = [&]() {
-      if (told == 0) return;
-      __syncwarp();
-      if (lane == 0) __threadfence();
-      __syncwarp();
-      if (told_kind == 0) {
-        if (lane == 0) atomicAdd(f.done + told_entry, told);
-      } else {
-        const bool last = lane < told && atomicAdd(f.tile + s_told[q][lane], 1) == s.entries - 1;
-        uint32_t mask = __ballot_sync(0xffffffffu, last);
-        if (mask) __threadfence();
-        for (; mask; mask &= mask - 1) {
-          const int n = 32 * s_told[q][__ffs(mask) - 1];
-          combine(f.y + n, f.out + n, f.ldo, f.T, f.k, f.d.H, lane);
-        }
-      }
-      told = 0;
-      __syncwarp();
-    };
+    int last_kind = 0, last_entry = -1;
     bool live[2] = {false, false};
     int slot[2] = {0, 0};
     float factor[2] = {0.f, 0.f}, gs = 1.f;
     for (int phase = 0;; phase ^= 1) {
       if (!__all_sync(0xffffffffu, mbar_wait(&ufull[q], phase, &s_abort))) break;
       const int4 u = s_unit[q];
-      const int kind = u.x, entry = u.y, n1 = u.z, flush = u.w;
+      const int kind = u.x, entry = u.y;
       if (kind < 0) break;
       const Cut cut = cut_of(a, kind);
-      if (kind != told_kind || entry != told_entry) {
-        if (kind == 0 || told_kind == 0) tell();
-        told_kind = kind;
-        told_entry = entry;
+      if (kind != last_kind || entry != last_entry) {
+        last_kind = kind;
+        last_entry = entry;
         const int count = s.count[entry];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           live[i] = 2 * t + i < count;
           slot[i] = s.rows[entry][live[i] ? 2 * t + i : 0];
-          factor[i] = kind == 0 ? (F::kBf16 ? 1.f : s.xinv[slot[i] / f.k]) : (F::kBf16 ? 1.f : row_scale_inv(__ldcg(f.hmax + slot[i]))) * s.wt[slot[i]];
+          factor[i] = kind ? s.wt[slot[i]] : F::kBf16 ? 1.f : s.xinv[slot[i] / f.k];
         }
         if (F::kNvfp4) gs = __ldg(cut.gs + s.expert[entry]);
       }
-      const int live_groups = min(cut.groups, (cut.rows - n1) / (kind ? 32 : 16));
+      const int live_groups = min(cut.groups, (cut.rows - u.z) / (kind ? 32 : 16));
       for (int group = 0; group < live_groups; ++group) {
         const float4* v = parts + (q * kMulWarps + group * cut.columns) * 32 + lane;
         float c[4] = {0.f, 0.f, 0.f, 0.f};
@@ -634,12 +654,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
 #pragma unroll
           for (int i = 0; i < 4; ++i) c[i] = c[i] / gs;
         }
-        const int n0 = n1 + group * (kind ? 32 : 16);
-        finish_rows<FMT>(f, kind, cut.rows, n0, lane, c, live, slot, factor);
-        if (kind && lane == 0) s_told[q][told] = (uint16_t)(n0 / 32);
-        if (++told == kBatch) tell();
+        finish_rows(f, kind, cut.rows, u.z + group * (kind ? 32 : 16), lane, c, live, slot, factor);
       }
-      if (flush) tell();
     }
   }
   __syncthreads();

@@ -244,9 +244,8 @@ __device__ __forceinline__ int pick_by_rounds(float (&key)[VT], int e0, int k, i
 }
 
 // Writes the token's top_k experts and weights; returns the lane's expert (lane < k).  VT >= g.per; sc:
-// this warp's.  FEW: a warp on its own, whose time is the instructions' latency: no estimates and no candidates, k rounds
-// over every exact key (the same choice).
-template <int VT, bool FEW = false>
+// this warp's.
+template <int VT>
 __device__ __forceinline__ int score_token(const ScoreArgs& a, const ScoreGeom& g, int t, int k, int lane,
                                            int32_t* __restrict__ topk_idx, float* __restrict__ topk_w, ScoreScratch& sc) {
   const int lanes = 1 << g.lanes_log2, grp = lane >> g.lanes_log2, sub = lane & (lanes - 1);
@@ -281,7 +280,7 @@ __device__ __forceinline__ int score_token(const ScoreArgs& a, const ScoreGeom& 
   int mine = 0;
   float sv = 0.f, b2 = -INFINITY;
   bool done = false;
-  if constexpr (VT >= 4 && !FEW) {
+  if constexpr (VT >= 4) {
     // Sigmoid keys with a bias: the fast exponential and reciprocal place every key to within key_slack
     // (the power of two 2^-22 and 2^-23 |l|, the rounded product with its constant, relative, which the sigmoid's
     // slope s (1 - s) <= 1/4, |l| s (1 - s) < 0.23, makes less than 1e-7 of the score; the sum and the reciprocal
@@ -362,7 +361,7 @@ __device__ __forceinline__ int score_token(const ScoreArgs& a, const ScoreGeom& 
         for (int i = 0; i < VT; ++i) key[i] = kNoKey;
       }
     }
-    if constexpr (VT >= 4 && !FEW)
+    if constexpr (VT >= 4)
       done = pick_top<VT>(key, l, top, false, e0, k, lane, sc, key_of, mine, sv);
     if (!done) {
       mine = pick_by_rounds<VT>(key, e0, k, lane);
