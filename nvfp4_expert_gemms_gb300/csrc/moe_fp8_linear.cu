@@ -4,44 +4,6 @@
 namespace moe {
 namespace {
 
-__device__ __forceinline__ void store_any(void* base, int dt, int64_t at, float v) {
-  if (dt == MOE_DT_F32) ((float*)base)[at] = v;
-  else if (dt == MOE_DT_F16) ((__half*)base)[at] = __float2half_rn(v);
-  else ((__nv_bfloat16*)base)[at] = __float2bfloat16_rn(v);
-}
-
-constexpr int kTile = 32;
-
-// One thread per output, 32 x 32 of them per block.
-__global__ void __launch_bounds__(kTile* kTile) fp8_linear_kernel(const Fp8LinearArgs a) {
-  __shared__ float sx[kTile][kTile + 1], sw[2][kTile][kTile + 1];
-  pdl_wait();
-  pdl_trigger();
-  const int n0 = blockIdx.x * kTile, t0 = blockIdx.y * kTile, i = threadIdx.x % kTile, j = threadIdx.x / kTile;
-  const bool pair = a.out_n != a.N;
-  float acc[2] = {0.f, 0.f};
-  for (int g = 0; g < a.groups; ++g) {
-    float p[2] = {0.f, 0.f};
-    for (int k0 = 128 * g; k0 < min(128 * g + 128, a.K); k0 += kTile) {
-      const int k = k0 + i;
-      sx[j][i] = t0 + j < a.T && k < a.K ? e4m3_to_f32(a.q[(t0 + j) * a.ldq + k]) : 0.f;
-      for (int h = 0; h < 1 + pair; ++h)
-        sw[h][j][i] = n0 + j < a.out_n && k < a.K ? e4m3_to_f32(a.w[(int64_t)(h * a.out_n + n0 + j) * a.K + k]) : 0.f;
-      __syncthreads();
-      for (int c = 0; c < kTile; ++c)
-        for (int h = 0; h < 1 + pair; ++h) p[h] = fmaf(sx[j][c], sw[h][i][c], p[h]);
-      __syncthreads();
-    }
-    if (t0 + j < a.T && n0 + i < a.out_n)
-      for (int h = 0; h < 1 + pair; ++h)
-        acc[h] = fmaf(p[h], a.qs[(int64_t)(t0 + j) * a.groups + g] * a.ws[(int64_t)((h * a.out_n + n0 + i) / 128) * a.groups + g], acc[h]);
-  }
-  if (t0 + j >= a.T || n0 + i >= a.out_n) return;
-  float y = pair ? silu_mul(acc[0], acc[1]) : acc[0];
-  if (a.base) y += load_any(a.base, a.out_dtype, (t0 + j) * a.ldb + n0 + i);
-  store_any(a.out, a.out_dtype, (t0 + j) * a.ldo + n0 + i, y);
-}
-
 // What a call needs beside its tensors: the codes and scales of activations that come unquantized.
 size_t codes_bytes(int T, int K) { return ((size_t)T * K + 255) / 256 * 256; }
 size_t workspace_bytes(int x_dtype, int T, int K) {
@@ -83,17 +45,17 @@ extern "C" moe_status_t moe_fp8_linear(const void* x, int64_t ldx, int x_dtype, 
   if (T == 0) return MOE_OK;
   const int groups = (K + 127) / 128;
   const cudaStream_t s = (cudaStream_t)stream;
-  Fp8LinearArgs a = {(const uint8_t*)x, ldx, x_scale_inv, w, w_scale_inv, base, ldb, out, ldo, out_dtype, T, K, N, groups, out_n};
+  Fp8LinearArgs a = {x, ldx, x_dtype, x_scale_inv, w, w_scale_inv, base, ldb, out, ldo, out_dtype, T, K, N, groups, out_n};
+  if (T <= kFp8Rows) return launch_fp8_rows(a, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   if (!coded) {
     uint8_t* q = (uint8_t*)workspace;
     float* qs = (float*)(q + codes_bytes(T, K));
     const Fp8QuantArgs qa = {x, ldx, x_dtype, q, K, qs, T, K, groups};
     if (launch_fp8_quantize(qa, s) != cudaSuccess) return MOE_ERR_CUDA;
-    a.q = q;
-    a.ldq = K;
+    a.x = q;
+    a.ldx = K;
+    a.x_dtype = MOE_DT_E4M3;
     a.qs = qs;
   }
-  note_launches(1);
-  const dim3 grid((out_n + kTile - 1) / kTile, (T + kTile - 1) / kTile);
-  return launch_pdl(fp8_linear_kernel, grid, dim3(kTile * kTile), 0, s, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launch_fp8_tiles(a, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

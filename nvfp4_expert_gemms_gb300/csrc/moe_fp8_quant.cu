@@ -7,25 +7,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kLanes = 16;  // lanes of a group, eight elements each
 
-// Eight elements as fp32; 0 past n.
-template <class T, bool WIDE>
-__device__ __forceinline__ void load8(const T* p, int n, float (&v)[8]) {
-  if (WIDE) {
-    if (sizeof(T) == 4) {
-      const float4 a = ((const float4*)p)[0], b = ((const float4*)p)[1];
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-      const uint4 u = *(const uint4*)p;
-      const T* e = (const T*)&u;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = to_f32(e[i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f32(p[i]) : 0.f;
-  }
-}
-
 // Sixteen lanes per group.  NaN does not count for the group's maximum (fmaxf) and stays NaN as a code.
 // WIDE: every group is whole and every row starts on a multiple of 16 bytes (8 of codes).
 template <class T, bool WIDE>
@@ -51,15 +32,11 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(const Fp8QuantAr
     for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
 #pragma unroll
     for (int off = kLanes / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    const float s = __fdiv_rn(448.f, fmaxf(m, 1e-12f));
+    const float s = fp8_scale(m);
     if (left <= 0) continue;
     uint32_t c[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(v[4 * j], s), __fmul_rn(v[4 * j + 1], s)), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(v[4 * j + 2], s), __fmul_rn(v[4 * j + 3], s)), __NV_SATFINITE, __NV_E4M3);
-      c[j] = lo | hi << 16;
-    }
+    for (int j = 0; j < 2; ++j) c[j] = fp8_codes2(v[4 * j], v[4 * j + 1], s) | fp8_codes2(v[4 * j + 2], v[4 * j + 3], s) << 16;
     uint8_t* q = a.q + t * a.ldq + k;
     if (WIDE) {
       *(uint2*)q = make_uint2(c[0], c[1]);
