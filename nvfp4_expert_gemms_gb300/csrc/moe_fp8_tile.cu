@@ -23,15 +23,17 @@ struct Shape {
   static constexpr int kPromote = BN / 16;  // warps: a row per thread, 64 columns per warp
   static constexpr int kThreads = 32 * (kPromote + 2);
   static constexpr int kStage = kTileA + BN * 128;
-  static constexpr int kStages = BN == 256 ? 4 : 4;
+  static constexpr int kStages = 3;
   static constexpr int kBuffers = BN == 256 ? 2 : 4;
-  static constexpr int kSmem = 1024 + kStages * kStage;
+  static constexpr int kBox = 4096;  // per promoting warp: outputs on their way
+  static constexpr int kSmem = 1024 + kStages * kStage + kPromote * kBox;
 };
 
 struct Args {
-  CUtensorMap x, w;
+  CUtensorMap x, w, out, base;
   Fp8LinearArgs l;
   int tiles_m, tiles_n;
+  bool boxed;  // outputs leave (and base comes) by TMA, 32 rows of a warp's columns at a time
 };
 
 // 32 lanes x 8 columns of 32-bit words.
@@ -44,6 +46,20 @@ __device__ __forceinline__ void tmem_ld_32x8(uint32_t taddr, uint32_t* v) {
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// A 2-D tiled load into the same place of every block of the cluster that `mask` names, completing on bar in each.
+__device__ __forceinline__ void tma_load_2d_multicast(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1, uint16_t mask) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%3, %4}], [%2], "
+      "%5;" ::"r"(smem_u32(dst)),
+      "l"(m), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "h"(mask)
+      : "memory");
+}
+// mma_commit, arriving on *bar of every block that `mask` names.
+__device__ __forceinline__ void mma_commit_multicast(uint64_t* bar, uint16_t mask) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+               "h"(mask)
+               : "memory");
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -55,50 +71,91 @@ __device__ __forceinline__ void store_remote4(uint32_t addr, uint32_t rank, cons
                : "memory");
 }
 
-// The first n of y as consecutive outputs of a row from column c0 on, with base added.
-template <class T, int n>
-__device__ __forceinline__ void store_row(const Fp8LinearArgs& l, int64_t row, int c0, const float* y) {
-  T* out = (T*)l.out + row * l.ldo + c0;
-  const T* base = l.base ? (const T*)l.base + row * l.ldb + c0 : nullptr;
-  constexpr int kVec = 16 / sizeof(T);
-  if (n % kVec == 0 && c0 + n <= l.out_n && (uintptr_t)out % 16 == 0 && (uintptr_t)base % 16 == 0) {
+// A warp's W outputs of each of its 32 rows (lane r holds row r's, from column c0 on) with base added, through 4 KB of shared
+// memory, so that lanes write side by side: columns of any alignment (a lane's own row at a time, 1237 x 1111 fp32 outputs took
+// 20 us).  Element (r, c) stands at column c ^ r: neither a row nor a column meets a bank twice.
+template <class T, int W>
+__device__ __forceinline__ void store_columns(const Fp8LinearArgs& l, float* box, int64_t row0, int c0, const float* y, int lane) {
+  constexpr int kRows = 32 / W;  // rows written at a time
+  __syncwarp();
 #pragma unroll
-    for (int i = 0; i < n; i += kVec) {
-      uint4 u;
-      T* e = (T*)&u;
-      float b[kVec];
-      if (base) {
-        u = *(const uint4*)(base + i);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) b[j] = to_f32(e[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) from_f32(base ? y[i + j] + b[j] : y[i + j], e + j);
-      *(uint4*)(out + i) = u;
+  for (int j = 0; j < W; ++j) box[lane * W + (j ^ (lane % W))] = y[j];
+  __syncwarp();
+  const int c = c0 + lane % W;
+  T* out = (T*)l.out + c;
+  const T* base = (const T*)l.base + c;
+  const bool in = c < l.out_n;
+#pragma unroll 8
+  for (int i = 0; i < 32; i += kRows) {
+    const int r = i + lane / W;
+    if (in && row0 + r < l.T) {
+      float v = box[r * W + (lane % W ^ (r % W))];
+      if (l.base) v += to_f32(base[(row0 + r) * l.ldb]);
+      from_f32(v, out + (row0 + r) * l.ldo);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < n; ++i)
-      if (c0 + i < l.out_n) from_f32(base ? y[i] + to_f32(base[i]) : y[i], out + i);
   }
 }
 template <int n>
-__device__ __forceinline__ void store_typed(const Fp8LinearArgs& l, int64_t row, int c0, const float* y) {
-  if (l.out_dtype == MOE_DT_F32) store_row<float, n>(l, row, c0, y);
-  else if (l.out_dtype == MOE_DT_F16) store_row<__half, n>(l, row, c0, y);
-  else store_row<__nv_bfloat16, n>(l, row, c0, y);
+__device__ __forceinline__ void store_any_columns(const Fp8LinearArgs& l, float* box, int64_t row0, int c0, const float* y, int lane) {
+  constexpr int W = n < 32 ? n : 32;
+#pragma unroll
+  for (int j = 0; j < n; j += W) {
+    if (l.out_dtype == MOE_DT_F32) store_columns<float, W>(l, box, row0, c0 + j, y + j, lane);
+    else if (l.out_dtype == MOE_DT_F16) store_columns<__half, W>(l, box, row0, c0 + j, y + j, lane);
+    else store_columns<__nv_bfloat16, W>(l, box, row0, c0 + j, y + j, lane);
+  }
 }
 
-// A tile per cluster of SPLIT blocks, which share its groups of columns and join their sums through each other's shared memory; SPLIT = 1:
-// blocks walk the tiles.  PAIR: the tile's weight rows are BN / 2 gates and the same features' ups; a thread's sums
+// The same for 16-bit outputs whose rows TMA can store: n of them per lane into the box, 16-byte parts swizzled (128-byte rows by the row,
+// 64-byte ones by half of it), where base already stands if there is one.
+template <int n>
+__device__ __forceinline__ void fill_box(char* box, int out_dtype, bool base, const float* y, int lane) {
+  constexpr int kParts = n / 8;
+  const int swap = kParts == 8 ? lane & 7 : lane >> 1 & 3;
+#pragma unroll
+  for (int j = 0; j < kParts; ++j) {
+    uint4* at = (uint4*)(box + lane * (16 * kParts) + ((j ^ swap) << 4));
+    uint32_t w[4];
+    if (base) {
+      const uint4 u = *at;
+      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = y[8 * j + 2 * i], b = y[8 * j + 2 * i + 1];
+      if (out_dtype == MOE_DT_F16) {
+        const float2 v = base ? __half22float2(*(const __half2*)&w[i]) : make_float2(0.f, 0.f);
+        const __half2 h = __floats2half2_rn(a + v.x, b + v.y);
+        w[i] = *(const uint32_t*)&h;
+      } else {
+        const float2 v = base ? make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)) : make_float2(0.f, 0.f);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a + v.x, b + v.y);
+        w[i] = *(const uint32_t*)&h;
+      }
+    }
+    *at = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(m), "r"(smem_u32(src)), "r"(c0), "r"(c1)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// SHARE: clusters of 2 x 2 blocks walk squares of 2 x 2 tiles.  Each block loads half of its rows of x for itself and its neighbour
+// along the outputs, and half of its weight rows for itself and its neighbour along the rows (TMA multicast): 24 KB of a
+// group's 48 come from L2.  A single block's tile takes 48 KB per 8.4 MFLOP, at which L2 holds every SM to some 50 GB/s
+// and the device to 1.33 PFLOP/s (16384 x 2048 x 4096: 206 us).
+// Else a tile per cluster of SPLIT blocks, which share its groups of columns and join their sums through each other's shared memory;
+// SPLIT = 1: blocks walk the tiles.  PAIR: the tile's weight rows are BN / 2 gates and the same features' ups; a thread's sums
 // then alternate gate, up.
-template <int BN, bool PAIR, int SPLIT>
-__global__ void __launch_bounds__(Shape<BN>::kThreads, 1) fp8_tile_kernel(const __grid_constant__ Args a) {
+template <int BN, bool PAIR, int SPLIT, bool SHARE>
+__global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_tile_kernel(const __grid_constant__ Args a) {
   using S = Shape<BN>;
   constexpr int kBufs = S::kBuffers, kStages = S::kStages;
   extern __shared__ __align__(1024) char smem_raw[];
   char* ring = (char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  __shared__ uint64_t full[kStages], empty[kStages], pfull[kBufs], pempty[kBufs], drain;
+  __shared__ uint64_t full[kStages], empty[kStages], pfull[kBufs], pempty[kBufs], bfull[S::kPromote], drain;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const Fp8LinearArgs& l = a.l;
@@ -107,12 +164,13 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 1) fp8_tile_kernel(const 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], SHARE ? 3 : 1);
     }
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(&pfull[i], 1);
       mbar_init(&pempty[i], S::kPromote);
     }
+    for (int i = 0; i < S::kPromote; ++i) mbar_init(&bfull[i], 1);
     mbar_init(&drain, 1);
     s_abort = 0;
     fence_barrier_init();
@@ -129,14 +187,21 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 1) fp8_tile_kernel(const 
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = s_tmem;
-  const int rank = SPLIT > 1 ? (int)cluster_rank() : 0;
-  const int tiles = a.tiles_m * a.tiles_n, first = blockIdx.x / SPLIT, stride = gridDim.x / SPLIT;
+  const int rank = SPLIT > 1 || SHARE ? (int)cluster_rank() : 0;
+  if (SHARE) {  // every block's barriers are there before another one arrives on them
+    cluster_arrive();
+    cluster_wait();
+  }
+  const int cm = SHARE ? rank >> 1 : 0, cn = SHARE ? rank & 1 : 0;  // place in the square
+  constexpr int kBlocks = SHARE ? 4 : SPLIT;
+  const int across = SHARE ? (a.tiles_m + 1) / 2 : a.tiles_m;  // tiles or squares along the rows
+  const int tiles = across * (SHARE ? (a.tiles_n + 1) / 2 : a.tiles_n), first = blockIdx.x / kBlocks, stride = gridDim.x / kBlocks;
+  auto tile_row = [&](int i) { return kM * (SHARE ? 2 * (i % across) + cm : i % across); };
+  auto tile_col = [&](int i) { return (PAIR ? BN / 2 : BN) * (SHARE ? 2 * (i / across) + cn : i / across); };
   // this block's groups of columns
-  const int g0 = l.groups * rank / SPLIT, g1 = l.groups * (rank + 1) / SPLIT;
+  const int g0 = SPLIT > 1 ? l.groups * rank / SPLIT : 0, g1 = SPLIT > 1 ? l.groups * (rank + 1) / SPLIT : l.groups;
   pdl_wait();
   pdl_trigger();
-  // tile i: rows 128 (i % tiles_m), outputs from (BN or BN / 2) (i / tiles_m) on
-  constexpr int kOut = PAIR ? BN / 2 : BN;
 
   if (warp == kProd) {
     int armed = 0;
@@ -144,7 +209,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 1) fp8_tile_kernel(const 
       int it = 0;
       bool ok = true;
       for (int i = first; ok && i < tiles; i += stride) {
-        const int row = kM * (i % a.tiles_m), n0 = kOut * (i / a.tiles_m), n1 = PAIR ? l.out_n + n0 : n0 + BN / 2;
+        const int row = tile_row(i), n0 = tile_col(i), n1 = PAIR ? l.out_n + n0 : n0 + BN / 2;
         for (int g = g0; g < g1; ++g, ++it) {
           const int st = it % kStages;
           ok = mbar_wait(&empty[st], ((it / kStages) & 1) ^ 1, &s_abort);
@@ -152,9 +217,14 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 1) fp8_tile_kernel(const 
           char* to = ring + st * S::kStage;
           mbar_arrive_expect_tx(&full[st], S::kStage);
           armed = it + 1;
-          tma_load_2d(to, &a.x, &full[st], 128 * g, row);
-          tma_load_2d(to + kTileA, &a.w, &full[st], 128 * g, n0);
-          tma_load_2d(to + kTileA + BN * 64, &a.w, &full[st], 128 * g, n1);
+          if constexpr (SHARE) {
+            tma_load_2d_multicast(to + kTileA / 2 * cn, &a.x, &full[st], 128 * g, row + kM / 2 * cn, (uint16_t)(3 << (2 * cm)));
+            tma_load_2d_multicast(to + kTileA + BN * 64 * cm, &a.w, &full[st], 128 * g, cm ? n1 : n0, (uint16_t)(5 << cn));
+          } else {
+            tma_load_2d(to, &a.x, &full[st], 128 * g, row);
+            tma_load_2d(to + kTileA, &a.w, &full[st], 128 * g, n0);
+            tma_load_2d(to + kTileA + BN * 64, &a.w, &full[st], 128 * g, n1);
+          }
         }
       }
       if (s_abort) {  // let every issued copy land before shared memory goes away
@@ -178,7 +248,8 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 1) fp8_tile_kernel(const 
           const uint32_t xa = smem_u32(ring + st * S::kStage), wa = xa + kTileA;
 #pragma unroll
           for (int k = 0; k < 4; ++k) dec::mma_f8_ss(tmem + b * BN, sdesc_k_sw128(xa + 32 * k), sdesc_k_sw128(wa + 32 * k), idesc, k != 0);
-          mma_commit(&empty[st]);
+          if (SHARE) mma_commit_multicast(&empty[st], (uint16_t)(3 << (2 * cm) | 5 << cn));  // whoever writes this stage
+          else mma_commit(&empty[st]);
           mma_commit(&pfull[b]);
         }
         __syncwarp();
@@ -188,10 +259,12 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 1) fp8_tile_kernel(const 
   } else {
     const int q = warp & 3, grp = warp >> 2, r = 32 * q + lane;  // tensor-memory lanes of this warp; its columns
     int it = 0;
+    uint32_t box_phase = 0;
     bool ok = true;
+    char* box = ring + kStages * S::kStage + warp * S::kBox;
     for (int i = first; ok && i < tiles; i += stride) {
-      const int64_t row = (int64_t)kM * (i % a.tiles_m) + r;
-      const int n0 = kOut * (i / a.tiles_m);
+      const int64_t row = tile_row(i) + r;
+      const int n0 = tile_col(i);
       const float* sx = l.qs + min(row, (int64_t)l.T - 1) * l.groups;
       // the weight rows of the thread's columns: 64 from c on, or (PAIR) 32 gates from c on and 32 ups.  Ups may cross into another
       // block of rows, `cross` columns from their first.
@@ -200,6 +273,15 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 1) fp8_tile_kernel(const 
       const float* sa = l.ws + (int64_t)min(c / 128, last) * l.groups;
       const float* sb = PAIR ? l.ws + (int64_t)min(up / 128, last) * l.groups : sa;
       const float* sc = PAIR ? l.ws + (int64_t)min(up / 128 + 1, last) * l.groups : sa;
+      const bool some = tile_row(i) + 32 * q < l.T && c < l.out_n;  // the warp has outputs
+      if (SPLIT == 1 && a.boxed && lane == 0) {
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last tile's have been read
+        if (l.base && some) {
+          mbar_arrive_expect_tx(&bfull[warp], 32 * (PAIR ? 64 : 128));
+          tma_load_2d(box, &a.base, &bfull[warp], c, tile_row(i) + 32 * q);
+        }
+      }
+      __syncwarp();
       float acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = 0.f;
@@ -241,17 +323,31 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 1) fp8_tile_kernel(const 
         }
       }
       if constexpr (SPLIT == 1) {
-        if (ok && row < l.T) {
-          if constexpr (PAIR) {
+        constexpr int kMine = PAIR ? 32 : 64;
+        if constexpr (PAIR) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) acc[j] = silu_mul(acc[2 * j], acc[2 * j + 1]);
+          for (int j = 0; j < 32; ++j) acc[j] = silu_mul(acc[2 * j], acc[2 * j + 1]);
+        }
+        if (a.boxed) {
+          if (l.base && some) {  // (whoever has given up: nothing is in flight into the box when the block ends)
+            volatile int alone = 0;
+            const bool came = mbar_wait(&bfull[warp], box_phase, &alone);
+            box_phase ^= 1;
+            ok = __all_sync(0xffffffffu, ok && came);
           }
-          store_typed<PAIR ? 32 : 64>(l, row, c, acc);
+          if (ok && some) {
+            fill_box<kMine>(box, l.out_dtype, l.base != nullptr, acc, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tma_store_2d(&a.out, box, c, tile_row(i) + 32 * q);
+          }
+        } else if (ok && some) {
+          store_any_columns<kMine>(l, (float*)box, tile_row(i) + 32 * q, c, acc, lane);
         }
       } else {
         // Every block takes 64 / SPLIT of a thread's sums from all of them.  Its ring is free: the MMAs that read it are done.
         constexpr int kMine = 64 / SPLIT;
-        float* box = (float*)ring;  // [from][sum / 4][thread][4]
+        float* meet = (float*)ring;  // [from][sum / 4][thread][4]
         constexpr int kThr = 32 * S::kPromote;
         __syncwarp();
         cluster_arrive();
@@ -260,7 +356,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 1) fp8_tile_kernel(const 
         for (int to = 0; to < SPLIT; ++to)
 #pragma unroll
           for (int j = 0; j < kMine; j += 4)
-            store_remote4(smem_u32(box + ((rank * (kMine / 4) + j / 4) * kThr + threadIdx.x) * 4), to, acc + kMine * to + j);
+            store_remote4(smem_u32(meet + ((rank * (kMine / 4) + j / 4) * kThr + threadIdx.x) * 4), to, acc + kMine * to + j);
         cluster_arrive();
         cluster_wait();
         float y[kMine];
@@ -269,17 +365,15 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 1) fp8_tile_kernel(const 
         for (int from = 0; from < SPLIT; ++from)
 #pragma unroll
           for (int j = 0; j < kMine; j += 4) {
-            const float4 v = *(const float4*)(box + ((from * (kMine / 4) + j / 4) * kThr + threadIdx.x) * 4);
+            const float4 v = *(const float4*)(meet + ((from * (kMine / 4) + j / 4) * kThr + threadIdx.x) * 4);
             y[j] += v.x, y[j + 1] += v.y, y[j + 2] += v.z, y[j + 3] += v.w;
           }
-        if (ok && row < l.T) {
-          constexpr int n = PAIR ? kMine / 2 : kMine;
-          if constexpr (PAIR) {
+        constexpr int kOut = PAIR ? kMine / 2 : kMine;
+        if constexpr (PAIR) {
 #pragma unroll
-            for (int j = 0; j < n; ++j) y[j] = silu_mul(y[2 * j], y[2 * j + 1]);
-          }
-          store_typed<n>(l, row, c + n * rank, y);
+          for (int j = 0; j < kOut; ++j) y[j] = silu_mul(y[2 * j], y[2 * j + 1]);
         }
+        if (ok && some) store_any_columns<kOut>(l, (float*)(ring + kStages * S::kStage + warp * S::kBox), tile_row(i) + 32 * q, c + kOut * rank, y, lane);
       }
     }
   }
@@ -290,6 +384,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 1) fp8_tile_kernel(const 
       cluster_wait();
     }
   }
+  if (warp < kProd && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // outputs have left
   {
     volatile int no_abort = 0;
     mbar_wait(&drain, 0, &no_abort);  // bounded; every MMA of this block has completed
@@ -297,26 +392,39 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 1) fp8_tile_kernel(const 
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
+  if (SHARE) {  // no block leaves while another one may still write or arrive in it
+    cluster_arrive();
+    cluster_wait();
+  }
   if (warp == kMma) tmem_dealloc(tmem, kBufs * BN);
 }
 
-template <int BN, bool PAIR, int SPLIT>
+template <int BN, bool PAIR, int SPLIT, bool SHARE>
 cudaError_t launch(const Fp8LinearArgs& l, cudaStream_t s) {
   using S = Shape<BN>;
   static SmemOptIn opt_in;
-  if (const cudaError_t e = opt_in(fp8_tile_kernel<BN, PAIR, SPLIT>, S::kSmem); e != cudaSuccess) return e;
+  if (const cudaError_t e = opt_in(fp8_tile_kernel<BN, PAIR, SPLIT, SHARE>, S::kSmem); e != cudaSuccess) return e;
   Args a;
   a.l = l;
   a.tiles_m = (l.T + kM - 1) / kM;
   a.tiles_n = (l.out_n + (PAIR ? BN / 2 : BN) - 1) / (PAIR ? BN / 2 : BN);
   const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  if (!tc_make_map(&a.x, u8, l.x, l.K, l.T, l.ldx, 128, kM, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  if (!tc_make_map(&a.x, u8, l.x, l.K, l.T, l.ldx, 128, SHARE ? kM / 2 : kM, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !tc_make_map(&a.w, u8, l.w, l.K, l.N, l.K, 128, BN / 2, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
-  const int64_t most = SPLIT > 1 ? tiles : (int64_t)tc_num_sms() * (BN == 256 ? 1 : 2);
+  a.boxed = false;
+  if (SPLIT == 1 && l.out_dtype != MOE_DT_F32 && (uintptr_t)l.out % 16 == 0 && (uintptr_t)l.base % 16 == 0 && l.ldo % 8 == 0 &&
+      (!l.base || l.ldb % 8 == 0)) {
+    const auto type = CU_TENSOR_MAP_DATA_TYPE_UINT16;
+    const auto sw = PAIR ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    if (!tc_make_map(&a.out, type, l.out, l.out_n, l.T, 2 * l.ldo, PAIR ? 32 : 64, 32, sw) ||
+        (l.base && !tc_make_map(&a.base, type, l.base, l.out_n, l.T, 2 * l.ldb, PAIR ? 32 : 64, 32, sw)))
+      return cudaErrorInvalidValue;
+    a.boxed = true;
+  }
+  constexpr int kBlocks = SHARE ? 4 : SPLIT;
+  const int64_t tiles = SHARE ? (int64_t)((a.tiles_m + 1) / 2) * ((a.tiles_n + 1) / 2) : (int64_t)a.tiles_m * a.tiles_n;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * SPLIT));
   cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = s;
@@ -324,23 +432,43 @@ cudaError_t launch(const Fp8LinearArgs& l, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = SPLIT;
+  attr[1].val.clusterDim.x = kBlocks;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = SPLIT > 1 ? 2 : 1;
+  cfg.numAttrs = kBlocks > 1 ? 2 : 1;
+  int64_t most = tiles;
+  if (SHARE) {  // as many clusters as the device holds at once
+    static PerDevice held;
+    std::atomic<int>* at;
+    if (const cudaError_t e = held.here(&at); e != cudaSuccess) return e;
+    int n = at ? at->load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+      cfg.gridDim = dim3(kBlocks);
+      cudaLaunchConfig_t ask = cfg;
+      ask.attrs = attr + 1;
+      ask.numAttrs = 1;
+      if (const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, fp8_tile_kernel<BN, PAIR, SPLIT, SHARE>, &ask); e != cudaSuccess) return e;
+      if (n < 1) n = 1;
+      if (at) at->store(n, std::memory_order_relaxed);
+    }
+    most = n;
+  } else if (SPLIT == 1) {
+    most = (int64_t)tc_num_sms() * (BN == 256 ? 1 : 2);
+  }
+  cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * kBlocks));
   note_launches(1);
-  return cudaLaunchKernelEx(&cfg, fp8_tile_kernel<BN, PAIR, SPLIT>, a);
+  return cudaLaunchKernelEx(&cfg, fp8_tile_kernel<BN, PAIR, SPLIT, SHARE>, a);
 }
 
 template <bool PAIR>
 cudaError_t choose(const Fp8LinearArgs& l, cudaStream_t s) {
   const int64_t rows = (l.T + kM - 1) / kM, sms = tc_num_sms();
   auto tiles = [&](int bn) { return rows * ((l.out_n + (PAIR ? bn / 2 : bn) - 1) / (PAIR ? bn / 2 : bn)); };
-  if (tiles(256) >= sms) return launch<256, PAIR, 1>(l, s);
+  if (tiles(256) >= sms) return rows > 1 ? launch<256, PAIR, 1, true>(l, s) : launch<256, PAIR, 1, false>(l, s);
   const int64_t n = tiles(64);
-  if (n >= sms || l.groups < 2) return launch<64, PAIR, 1>(l, s);
-  if (n * 2 >= sms || l.groups < 4) return launch<64, PAIR, 2>(l, s);
-  return launch<64, PAIR, 4>(l, s);
+  if (n >= sms || l.groups < 2) return launch<64, PAIR, 1, false>(l, s);
+  if (n * 2 >= sms || l.groups < 4) return launch<64, PAIR, 2, false>(l, s);
+  return launch<64, PAIR, 4, false>(l, s);
 }
 
 }  // namespace
