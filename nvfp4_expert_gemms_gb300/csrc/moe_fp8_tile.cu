@@ -23,9 +23,11 @@ struct Shape {
   static constexpr int kPromote = BN / 16;  // warps: a row per thread, 64 columns per warp
   static constexpr int kThreads = 32 * (kPromote + 2);
   static constexpr int kStage = kTileA + BN * 128;
-  static constexpr int kStages = 3;
+  // A stage comes back some 3100 cycles after it was freed (clusters: the slowest of three blocks frees it), a group's MMAs take 640: the
+  // more stages the better, and the outputs make do with 2 KB per warp (16384 x 2048 x 4096: three stages 169 us).
+  static constexpr int kStages = BN == 256 ? 4 : 3;
   static constexpr int kBuffers = BN == 256 ? 2 : 4;
-  static constexpr int kBox = 4096;  // per promoting warp: outputs on their way
+  static constexpr int kBox = BN == 256 ? 2048 : 4096;  // per promoting warp: outputs on their way
   static constexpr int kSmem = 1024 + kStages * kStage + kPromote * kBox;
 };
 
@@ -35,6 +37,14 @@ struct Args {
   int tiles_m, tiles_n;
   bool boxed;  // outputs leave (and base comes) by TMA, 32 rows of a warp's columns at a time
 };
+
+// Two sums at once: a += p f, b += q g.
+__device__ __forceinline__ void fma2(float& a, float& b, uint32_t p, uint32_t q, float f, float g) {
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n mov.b64 z, {%4, %5};\n fma.rn.f32x2 x, y, z, x;\n"
+      " mov.b64 {%0, %1}, x;\n}"
+      : "+f"(a), "+f"(b)
+      : "r"(p), "r"(q), "f"(f), "f"(g));
+}
 
 // 32 lanes x 8 columns of 32-bit words.
 __device__ __forceinline__ void tmem_ld_32x8(uint32_t taddr, uint32_t* v) {
@@ -71,8 +81,8 @@ __device__ __forceinline__ void store_remote4(uint32_t addr, uint32_t rank, cons
                : "memory");
 }
 
-// A warp's W outputs of each of its 32 rows (lane r holds row r's, from column c0 on) with base added, through 4 KB of shared
-// memory, so that lanes write side by side: columns of any alignment (a lane's own row at a time, 1237 x 1111 fp32 outputs took
+// A warp's W outputs of each of its 32 rows (lane r holds row r's, from column c0 on) with base added, through the warp's box of
+// shared memory, so that lanes write side by side: columns of any alignment (a lane's own row at a time, 1237 x 1111 fp32 outputs took
 // 20 us).  Element (r, c) stands at column c ^ r: neither a row nor a column meets a bank twice.
 template <class T, int W>
 __device__ __forceinline__ void store_columns(const Fp8LinearArgs& l, float* box, int64_t row0, int c0, const float* y, int lane) {
@@ -95,9 +105,9 @@ __device__ __forceinline__ void store_columns(const Fp8LinearArgs& l, float* box
     }
   }
 }
-template <int n>
+template <int n, int most>
 __device__ __forceinline__ void store_any_columns(const Fp8LinearArgs& l, float* box, int64_t row0, int c0, const float* y, int lane) {
-  constexpr int W = n < 32 ? n : 32;
+  constexpr int W = n < most ? n : most;
 #pragma unroll
   for (int j = 0; j < n; j += W) {
     if (l.out_dtype == MOE_DT_F32) store_columns<float, W>(l, box, row0, c0 + j, y + j, lane);
@@ -106,15 +116,12 @@ __device__ __forceinline__ void store_any_columns(const Fp8LinearArgs& l, float*
   }
 }
 
-// The same for 16-bit outputs whose rows TMA can store: n of them per lane into the box, 16-byte parts swizzled (128-byte rows by the row,
-// 64-byte ones by half of it), where base already stands if there is one.
-template <int n>
+// The same for 16-bit outputs whose rows TMA can store: 32 of them per lane into the box, 64-byte rows whose 16-byte parts are
+// XORed with half the row, where base already stands if there is one.
 __device__ __forceinline__ void fill_box(char* box, int out_dtype, bool base, const float* y, int lane) {
-  constexpr int kParts = n / 8;
-  const int swap = kParts == 8 ? lane & 7 : lane >> 1 & 3;
 #pragma unroll
-  for (int j = 0; j < kParts; ++j) {
-    uint4* at = (uint4*)(box + lane * (16 * kParts) + ((j ^ swap) << 4));
+  for (int j = 0; j < 4; ++j) {
+    uint4* at = (uint4*)(box + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4));
     uint32_t w[4];
     if (base) {
       const uint4 u = *at;
@@ -274,13 +281,15 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
       const float* sb = PAIR ? l.ws + (int64_t)min(up / 128, last) * l.groups : sa;
       const float* sc = PAIR ? l.ws + (int64_t)min(up / 128 + 1, last) * l.groups : sa;
       const bool some = tile_row(i) + 32 * q < l.T && c < l.out_n;  // the warp has outputs
-      if (SPLIT == 1 && a.boxed && lane == 0) {
-        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last tile's have been read
-        if (l.base && some) {
-          mbar_arrive_expect_tx(&bfull[warp], 32 * (PAIR ? 64 : 128));
-          tma_load_2d(box, &a.base, &bfull[warp], c, tile_row(i) + 32 * q);
+      // the box, free again, and base's 32 columns from c0 on into it (lane 0)
+      auto open_box = [&](int c0) {
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        if (l.base && c0 < l.out_n) {
+          mbar_arrive_expect_tx(&bfull[warp], 32 * 64);
+          tma_load_2d(box, &a.base, &bfull[warp], c0, tile_row(i) + 32 * q);
         }
-      }
+      };
+      if (SPLIT == 1 && a.boxed && some && lane == 0) open_box(c);
       __syncwarp();
       float acc[64];
 #pragma unroll
@@ -318,8 +327,8 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
             if (lane == 0) mbar_arrive(&pempty[b]);
           }
 #pragma unroll
-          for (int j = 0; j < kAtOnce; ++j)
-            acc[h + j] = fmaf(__uint_as_float(p[j]), !PAIR || j % 2 == 0 ? fa : (h + j) / 2 < cross ? fb : fc, acc[h + j]);
+          for (int j = 0; j < kAtOnce; j += 2)
+            fma2(acc[h + j], acc[h + j + 1], p[j], p[j + 1], fa, !PAIR ? fa : (h + j) / 2 < cross ? fb : fc);
         }
       }
       if constexpr (SPLIT == 1) {
@@ -328,21 +337,29 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
 #pragma unroll
           for (int j = 0; j < 32; ++j) acc[j] = silu_mul(acc[2 * j], acc[2 * j + 1]);
         }
-        if (a.boxed) {
-          if (l.base && some) {  // (whoever has given up: nothing is in flight into the box when the block ends)
-            volatile int alone = 0;
-            const bool came = mbar_wait(&bfull[warp], box_phase, &alone);
-            box_phase ^= 1;
-            ok = __all_sync(0xffffffffu, ok && came);
-          }
-          if (ok && some) {
-            fill_box<kMine>(box, l.out_dtype, l.base != nullptr, acc, lane);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) tma_store_2d(&a.out, box, c, tile_row(i) + 32 * q);
+        if (a.boxed && some) {
+#pragma unroll
+          for (int h = 0; h < kMine; h += 32) {
+            if (c + h >= l.out_n) break;
+            if (h > 0) {
+              if (lane == 0) open_box(c + h);
+              __syncwarp();
+            }
+            if (l.base) {  // (whoever has given up: nothing is in flight into the box when the block ends)
+              volatile int alone = 0;
+              const bool came = mbar_wait(&bfull[warp], box_phase, &alone);
+              box_phase ^= 1;
+              ok = __all_sync(0xffffffffu, ok && came);
+            }
+            if (ok) {
+              fill_box(box, l.out_dtype, l.base != nullptr, acc + h, lane);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) tma_store_2d(&a.out, box, c + h, tile_row(i) + 32 * q);
+            }
           }
         } else if (ok && some) {
-          store_any_columns<kMine>(l, (float*)box, tile_row(i) + 32 * q, c, acc, lane);
+          store_any_columns<kMine, S::kBox / 128>(l, (float*)box, tile_row(i) + 32 * q, c, acc, lane);
         }
       } else {
         // Every block takes 64 / SPLIT of a thread's sums from all of them.  Its ring is free: the MMAs that read it are done.
@@ -373,7 +390,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
 #pragma unroll
           for (int j = 0; j < kOut; ++j) y[j] = silu_mul(y[2 * j], y[2 * j + 1]);
         }
-        if (ok && some) store_any_columns<kOut>(l, (float*)(ring + kStages * S::kStage + warp * S::kBox), tile_row(i) + 32 * q, c + kOut * rank, y, lane);
+        if (ok && some) store_any_columns<kOut, S::kBox / 128>(l, (float*)(ring + kStages * S::kStage + warp * S::kBox), tile_row(i) + 32 * q, c + kOut * rank, y, lane);
       }
     }
   }
@@ -416,9 +433,9 @@ cudaError_t launch(const Fp8LinearArgs& l, cudaStream_t s) {
   if (SPLIT == 1 && l.out_dtype != MOE_DT_F32 && (uintptr_t)l.out % 16 == 0 && (uintptr_t)l.base % 16 == 0 && l.ldo % 8 == 0 &&
       (!l.base || l.ldb % 8 == 0)) {
     const auto type = CU_TENSOR_MAP_DATA_TYPE_UINT16;
-    const auto sw = PAIR ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
-    if (!tc_make_map(&a.out, type, l.out, l.out_n, l.T, 2 * l.ldo, PAIR ? 32 : 64, 32, sw) ||
-        (l.base && !tc_make_map(&a.base, type, l.base, l.out_n, l.T, 2 * l.ldb, PAIR ? 32 : 64, 32, sw)))
+    const auto sw = CU_TENSOR_MAP_SWIZZLE_64B;
+    if (!tc_make_map(&a.out, type, l.out, l.out_n, l.T, 2 * l.ldo, 32, 32, sw) ||
+        (l.base && !tc_make_map(&a.base, type, l.base, l.out_n, l.T, 2 * l.ldb, 32, 32, sw)))
       return cudaErrorInvalidValue;
     a.boxed = true;
   }
