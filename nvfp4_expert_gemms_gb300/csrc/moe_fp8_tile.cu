@@ -95,13 +95,19 @@ __device__ __forceinline__ void store_columns(const Fp8LinearArgs& l, float* box
   T* out = (T*)l.out + c;
   const T* base = (const T*)l.base + c;
   const bool in = c < l.out_n;
-#pragma unroll 8
-  for (int i = 0; i < 32; i += kRows) {
-    const int r = i + lane / W;
-    if (in && row0 + r < l.T) {
-      float v = box[r * W + (lane % W ^ (r % W))];
-      if (l.base) v += to_f32(base[(row0 + r) * l.ldb]);
-      from_f32(v, out + (row0 + r) * l.ldo);
+  constexpr int kAtOnce = W == 32 ? 32 : 8;  // rows (or sets of them) whose base is loaded first
+#pragma unroll 1
+  for (int i0 = 0; i0 < 32; i0 += kAtOnce * kRows) {
+    float v[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int r = i0 + i * kRows + lane / W;
+      v[i] = l.base && in && r < 32 && row0 + r < l.T ? to_f32(base[(row0 + r) * l.ldb]) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int r = i0 + i * kRows + lane / W;
+      if (in && r < 32 && row0 + r < l.T) from_f32(box[r * W + (lane % W ^ (r % W))] + v[i], out + (row0 + r) * l.ldo);
     }
   }
 }
