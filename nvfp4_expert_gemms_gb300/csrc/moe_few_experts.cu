@@ -5,8 +5,8 @@
 // where K is short); first every unit of the gate/up matrices, entry by entry, then those of the down matrices.  Blocks
 // take runs of units by ticket in that order, so whoever waits (a down unit for its entry's h) waits for units that running
 // blocks hold and that wait for nothing: no two blocks have to be resident together, and calls on other streams cannot
-// stand in the way.  An atomic's answer takes over a microsecond here, so a block takes few tickets (one per matrix where there
-// are few units) and asks for the next one as it starts a run.
+// stand in the way.  An atomic's answer takes over a microsecond, so a block gets along with one ticket per matrix and asks for
+// the next one as it starts a run.
 //
 // One warp of a block copies by TMA, eight pieces of 128 columns (64 of bf16) by 32 rows to a stage of shared memory,
 // 144 to 192 KB ahead (HBM's rate and latency ask for some 45), into the down matrices while h is not there yet.  Sixteen warps
@@ -65,10 +65,11 @@ struct Cut {
   int step;          // features or outputs per unit
   int units;         // per entry
   int steps;         // times the warps go along K
+  int pairs;         // NVFP4: pieces are copied two by two, 128 bytes of a row, and the scales of eight of them (K % 256 = 0)
 };
 
 struct Args {
-  CUtensorMap map[2], smap[2];  // codes, and INT4's scales
+  CUtensorMap map[2], smap[2];  // codes, and 4-bit formats' scales
   FewArgs f;
   Cut cut[2];
 };
@@ -116,24 +117,40 @@ __device__ __forceinline__ void e2m1x8_f16(uint32_t c, uint32_t (&o)[4]) {
 // long as both operands use the same one, so a lane takes what it can read in whole 16-byte parts without bank conflicts.
 template <int FMT>
 __device__ __forceinline__ int element(int t, int j) {
-  return Format<FMT>::kInt4 ? 8 * (t + 4 * j) : Format<FMT>::kPiece / 4 * t + 8 * j;
+  return Format<FMT>::kInt4 ? 16 * t + 8 * (j & 1) + 64 * (j >> 1) : Format<FMT>::kPiece / 4 * t + 8 * j;
 }
 
-// INT4 words decode into pairs of elements (j, j + 4): the same order for the activations.
+// INT4 words decode into pairs of elements (j, j + 4), every other pair 16 times too large: the same order, and that taken back, for the
+// activations.  Their sum goes to `sum`.
 template <int FMT>
-__device__ __forceinline__ void order_pairs(uint32_t* b) {
-  if (!Format<FMT>::kInt4) return;
-  const uint32_t r0 = b[0], r1 = b[1], r2 = b[2], r3 = b[3];
-  b[0] = __byte_perm(r0, r2, 0x5410);
-  b[1] = __byte_perm(r0, r2, 0x7632);
-  b[2] = __byte_perm(r1, r3, 0x5410);
-  b[3] = __byte_perm(r1, r3, 0x7632);
+__device__ __forceinline__ void order_pairs(uint32_t* b, float& sum) {
+  if constexpr (Format<FMT>::kInt4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = __half22float2(*(const __half2*)&b[i]);
+      sum += v.x + v.y;
+    }
+    const uint32_t r0 = b[0], r1 = b[1], r2 = b[2], r3 = b[3];
+    b[0] = __byte_perm(r0, r2, 0x5410);
+    b[1] = hmul2(__byte_perm(r0, r2, 0x7632), 0x2C002C00u);
+    b[2] = __byte_perm(r1, r3, 0x5410);
+    b[3] = hmul2(__byte_perm(r1, r3, 0x7632), 0x2C002C00u);
+  }
+}
+// -8 times the sums of the lane's MMA columns 2 t and 2 t + 1, from each lane's share of column g.
+__device__ __forceinline__ void share_sums(float sum, int lane, float (&eights)[2]) {
+  sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+  sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) eights[i] = -8.f * __shfl_sync(0xffffffffu, sum, 4 * (2 * (lane & 3) + i));
 }
 
 // A piece of an entry's activations as the MMA's column operand: x in the columns 0 .. 3, ...
 template <int FMT>
-__device__ __forceinline__ void load_x(const FewArgs& f, const Tables& s, int entry, int col, int lane, uint32_t (&b)[Format<FMT>::kRegs]) {
+__device__ __forceinline__ void load_x(const FewArgs& f, const Tables& s, int entry, int col, int lane, uint32_t (&b)[Format<FMT>::kRegs],
+                                       float (&eights)[2]) {
   const int g = lane >> 2, t = lane & 3;
+  float sum = 0.f;
   const bool live = g < s.count[entry];
   const int token = s.rows[entry][live ? g : 0] / f.k;
   const uint16_t* row = (Format<FMT>::kBf16 ? (const uint16_t*)f.x + token * f.ldx : (const uint16_t*)f.xs + (size_t)token * f.d.H) + col;
@@ -141,8 +158,9 @@ __device__ __forceinline__ void load_x(const FewArgs& f, const Tables& s, int en
   for (int j = 0; j < Format<FMT>::kRegs / 4; ++j) {
     const uint4 u = live ? *(const uint4*)(row + element<FMT>(t, j)) : make_uint4(0, 0, 0, 0);
     b[4 * j] = u.x, b[4 * j + 1] = u.y, b[4 * j + 2] = u.z, b[4 * j + 3] = u.w;
-    order_pairs<FMT>(b + 4 * j);
+    order_pairs<FMT>(b + 4 * j, sum);
   }
+  if (Format<FMT>::kInt4) share_sums(sum, lane, eights);
 }
 
 // Four values that other blocks write, as they are now.
@@ -171,7 +189,7 @@ struct Patience {
 // two per row of the piece; inv: its inverse for the rows of the lane's MMA columns 2 t and 2 t + 1.  False if it never came.
 template <int FMT>
 __device__ __forceinline__ bool load_h(const FewArgs& f, const Tables& s, int entry, int col, int lane, uint32_t (&b)[Format<FMT>::kRegs],
-                                       float (&inv)[2], volatile int* abort) {
+                                       float (&inv)[2], float (&eights)[2], volatile int* abort) {
   const int g = lane >> 2, t = lane & 3, r = g & 3;
   const bool live = r < s.count[entry], low = g >= 4;
   const float* row = f.h + (size_t)s.rows[entry][live ? r : 0] * f.d.I + col;
@@ -188,7 +206,7 @@ __device__ __forceinline__ bool load_h(const FewArgs& f, const Tables& s, int en
     if (__all_sync(0xffffffffu, set)) break;
     if (__any_sync(0xffffffffu, p.over(abort))) return false;
   }
-  float scale = 1.f;
+  float scale = 1.f, sum = 0.f;
   if (!Format<FMT>::kBf16) {
     uint32_t m = 0;
 #pragma unroll
@@ -217,15 +235,17 @@ __device__ __forceinline__ bool load_h(const FewArgs& f, const Tables& s, int en
         b[4 * j + i] = *(const uint32_t*)&hi;
       }
     }
-    order_pairs<FMT>(b + 4 * j);
+    order_pairs<FMT>(b + 4 * j, sum);
   }
+  if (Format<FMT>::kInt4) share_sums(sum, lane, eights);
   return true;
 }
 
 // acc += a piece of 32 rows at `sm` (its scales at `sc`) times the activations.  Tile m's MMA rows g and g + 8 are gate and up
-// n0 + 8 m + g of the features, or outputs n0 + 16 m + g and 8 further on.  inv: what the two columns' activations were scaled by.
+// n0 + 8 m + g of the features, or outputs n0 + 16 m + g and 8 further on.  inv: what the two columns' activations were scaled by;
+// eights: -8 times their sums (INT4).
 template <int FMT>
-__device__ __forceinline__ void multiply(const char* sm, const char* sc, int kind, float s0, float s1, const float (&inv)[2], int lane,
+__device__ __forceinline__ void multiply(const char* sm, const char* sc, int pair, int kind, float s0, float s1, const float (&inv)[2], const float (&eights)[2], int lane,
                                          const uint32_t (&b)[Format<FMT>::kRegs], float (&acc)[2][4]) {
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -235,29 +255,39 @@ __device__ __forceinline__ void multiply(const char* sm, const char* sc, int kin
     const int r0 = kind ? 16 * m + g : 8 * m + g, r1 = kind ? r0 + 8 : r0 + 16;
     if constexpr (Format<FMT>::kInt4) {
       // words hold eight columns of a row and lie side by side along the rows, 128 bytes per column group: 16-byte parts
-      // XORed with the group (gate/up: each half's four parts by the group mod 4)
+      // XORed with the group (gate/up: each half's four parts by the group mod 4).  With groups two apart the four lanes of a row
+      // read different banks, in gate/up if two of them read the ups first.
       s0 = __half2float(((const __half*)sc)[r0]), s1 = __half2float(((const __half*)sc)[r1]);
+      const bool turn = kind == 0 && t >= 2;
+      const int at0 = 4 * (turn ? r1 : r0), at1 = 4 * (turn ? r0 : r1);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int kr = t + 4 * j, swap = (kr & (kind ? 7 : 3)) << 4;
+        const int kr = 2 * t + (j & 1) + 8 * (j >> 1), swap = (kr & (kind ? 7 : 3)) << 4;
         const char* line = sm + 128 * kr;
-        const uint32_t w[2] = {*(const uint32_t*)(line + ((4 * r0) ^ swap)), *(const uint32_t*)(line + ((4 * r1) ^ swap))};
+        const uint32_t y0 = *(const uint32_t*)(line + (at0 ^ swap)), y1 = *(const uint32_t*)(line + (at1 ^ swap));
+        const uint32_t w[2] = {turn ? y1 : y0, turn ? y0 : y1};
+        // A nibble of a half-word is, as it stands, a subnormal fp16 number: code 2^-24, the next one 16 times that, which
+        // the activations take back (order_pairs).  Where each weight became 1024 + code - 1032 the decoding took a third of the
+        // time at 16 tokens.
         uint32_t x[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {  // 1024 + code in fp16, less 1032 the weight
-            const uint32_t v = ((w[i] >> (4 * n)) & 0x000F000Fu) | 0x64006400u;
-            const __half2 d = __hsub2(*(const __half2*)&v, __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408)));
-            x[i][n] = *(const uint32_t*)&d;
+          for (int n = 0; n < 4; n += 2) {
+            const uint32_t v = w[i] >> (4 * n);
+            x[i][n] = v & 0x000F000Fu;
+            x[i][n + 1] = v & 0x00F000F0u;
           }
         step(x[0][0], x[1][0], x[0][1], x[1][1], 4 * j);
         step(x[0][2], x[1][2], x[0][3], x[1][3], 4 * j + 2);
       }
     } else if constexpr (Format<FMT>::kNvfp4) {
       // a code times its block's scale has six significant bits: exact in fp16 (2^-10 at the least, 2688 at most)
-      const uint32_t q0 = e4m3x2_f16(*(const uint16_t*)(sc + 8 * r0 + 2 * t)), q1 = e4m3x2_f16(*(const uint16_t*)(sc + 8 * r1 + 2 * t));
-      const uint4 u = *(const uint4*)(sm + 64 * r0 + 16 * t), v = *(const uint4*)(sm + 64 * r1 + 16 * t);
+      // pair < 0: rows of 64 bytes and of 8 scales; else the pair-th half of rows of 128 bytes, 16-byte parts XORed with the row, and
+      // rows of 64 scales
+      const int srow = pair < 0 ? 8 : 64, row = pair < 0 ? 64 : 128, part = (pair < 0 ? t : (4 * pair + t) ^ g) << 4;
+      const uint32_t q0 = e4m3x2_f16(*(const uint16_t*)(sc + srow * r0 + 2 * t)), q1 = e4m3x2_f16(*(const uint16_t*)(sc + srow * r1 + 2 * t));
+      const uint4 u = *(const uint4*)(sm + row * r0 + part), v = *(const uint4*)(sm + row * r1 + part);
       const uint32_t w0[4] = {u.x, u.y, u.z, u.w}, w1[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -284,6 +314,10 @@ __device__ __forceinline__ void multiply(const char* sm, const char* sc, int kin
             step(e4m3x2_f16(w0[j]), e4m3x2_f16(w1[j]), e4m3x2_f16(w0[j] >> 16), e4m3x2_f16(w1[j] >> 16), 8 * q + 2 * j);
         }
       }
+    }
+    if constexpr (Format<FMT>::kInt4) {  // code 2^-24 -> code - 8
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] = fmaf(p[i], 16777216.f, eights[i & 1]);
     }
     // (the scales one after the other: their product may be below fp32's range where the sums are not)
     acc[m][0] = fmaf(p[0] * s0, inv[0], acc[m][0]), acc[m][1] = fmaf(p[1] * s0, inv[1], acc[m][1]);
@@ -425,9 +459,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
 
   if (warp == kCopyWarp) {
     // ---------------- copies ----------------
-    // A matrix's units are divided evenly into as many tickets as there are blocks, or up to eight times as many.
-    const int blocks = gridDim.x;
-    const int n0 = blocks * min(8, max(1, ngu / (4 * blocks))), n1 = blocks * min(8, max(1, (nunits - ngu) / (4 * blocks)));
+    // A matrix's units are divided evenly into as many tickets as there are blocks: a run stays with an entry, whose operands
+    // the warps then keep (with eight times as many tickets 16 tokens of FP8 took 103 us for 94).
+    const int n0 = gridDim.x, n1 = gridDim.x;
     int slot = 0, phase = 1, armed = 0;
     bool ok = true;
     // the next stage, free; the descriptor is its first stage's
@@ -465,17 +499,21 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
               if (!take_stage(kind, entry, row)) break;
               char* to = ring + slot * kStageBytes;
               const int r = row + group * (kind ? 32 : 16), piece = step * kMulWarps + half * kStagePieces;
-              const int count = min(kStagePieces, cut.columns - half * kStagePieces);  // pieces the maps bring (their box)
-              if constexpr (F::kNvfp4) {  // scales: a lane per row, eight bytes per piece
+              const int count = min(kStagePieces, cut.columns - half * kStagePieces);  // pieces of this stage
+              const bool lone = F::kNvfp4 && !cut.pairs;
+              if (lone) {  // scales: a lane per row, eight bytes per piece
                 const int i = kind ? 0 : lane >> 4, n = kind ? r + lane : r + (lane & 15);
                 const char* sc = cut.scales + ((size_t)e * cut.N + i * cut.rows + n) * (cut.K / 16) + 8 * piece;
                 if (n < cut.rows)
                   for (int j = 0; j < count && piece + j < cut.pieces; ++j) cp_async_8(smem_u32(to + kStagePieces * F::kCodes + j * F::kScales + 8 * lane), sc + 8 * j);
                 cp_async_mbar_arrive_noinc(&full[slot]);
+              } else if (F::kNvfp4) {
+                mbar_arrive(&full[slot]);  // (the barrier counts every lane's scales)
+                __syncwarp();
               }
               if (lane == 0) {
-                mbar_arrive_expect_tx(&full[slot], cut.columns < kStagePieces ? cut.columns * (F::kCodes + (F::kInt4 ? F::kScales : 0))
-                                                                               : kStagePieces * (F::kCodes + (F::kInt4 ? F::kScales : 0)));
+                const int box = min(cut.columns, kStagePieces);  // pieces that the maps bring (of pairs, even)
+                mbar_arrive_expect_tx(&full[slot], box * (F::kCodes + (F::kInt4 ? F::kScales : 0)) + (F::kNvfp4 && cut.pairs ? 32 * 64 : 0));
                 if constexpr (F::kInt4) {
                   char* sc = to + kStagePieces * F::kCodes;
                   if (kind == 0) {
@@ -486,8 +524,14 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
                     tma_load_3d(sc, &a.smap[1], &full[slot], r, piece, e);
                   }
                 } else {
-                  if (kind == 0) tma_load_5d(to, &a.map[0], &full[slot], 0, r, 0, piece, e);
-                  else tma_load_4d(to, &a.map[1], &full[slot], 0, r, piece, e);
+                  const int at = F::kNvfp4 && cut.pairs ? piece / 2 : piece;
+                  if (kind == 0) tma_load_5d(to, &a.map[0], &full[slot], 0, r, 0, at, e);
+                  else tma_load_4d(to, &a.map[1], &full[slot], 0, r, at, e);
+                  if (F::kNvfp4 && cut.pairs) {
+                    char* sc = to + kStagePieces * F::kCodes;
+                    if (kind == 0) tma_load_4d(sc, &a.smap[0], &full[slot], 8 * piece, r, 0, e);
+                    else tma_load_3d(sc, &a.smap[1], &full[slot], 8 * piece, r, e);
+                  }
                 }
               }
               __syncwarp();
@@ -520,11 +564,11 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
     // ---------------- pieces: decode and multiply ----------------
     int slot = 0, phase = 0, end_slot = 0, end_phase = 1, key = -1;
     uint32_t b[F::kRegs];
-    float inv[2] = {1.f, 1.f};
+    float inv[2] = {1.f, 1.f}, eights[2] = {0.f, 0.f};
     bool ok = true;
     auto acquire = [&](uint64_t* bar) { ok = ok && __all_sync(0xffffffffu, mbar_wait(&bar[slot], phase, &s_abort)); };
     // this matrix's share of the warp: its stage of each step, its place in it; what it takes to find its scales
-    int kind = -1, mine = 0, local = 0, col = 0, stages = 0, steps = 0, pieces = 0, rows = 0, above = 0;
+    int kind = -1, mine = 0, local = 0, col = 0, stages = 0, steps = 0, pieces = 0, rows = 0, above = 0, pairs = 0;
     const float* scales = nullptr;
     for (;;) {
       acquire(said);  // the unit is known, its weights may still be on their way
@@ -541,6 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
         stages = cut.groups * cut.halves;
         steps = cut.steps;
         pieces = cut.pieces;
+        pairs = cut.pairs;
         rows = cut.rows;
         above = group * (kind ? 32 : 16);
         scales = (const float*)cut.scales;
@@ -561,17 +606,18 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
           const int want = (kind * kFewSlots + entry) << 16 | piece;
           if (want != key) {  // the activations are kept from one unit to the next
             key = want;
-            if (kind == 0) load_x<FMT>(f, s, entry, piece * F::kPiece, lane, b);
-            else ok = load_h<FMT>(f, s, entry, piece * F::kPiece, lane, b, inv, &s_abort);
+            if (kind == 0) load_x<FMT>(f, s, entry, piece * F::kPiece, lane, b, eights);
+            else ok = load_h<FMT>(f, s, entry, piece * F::kPiece, lane, b, inv, eights, &s_abort);
           }
         }
         for (int i = 0; ok && i < stages; ++i) {
           acquire(full);
           if (!ok) break;
           if (live && i == mine) {
-            const char* sm = ring + slot * kStageBytes + local * F::kCodes;
-            const char* sc = ring + slot * kStageBytes + kStagePieces * F::kCodes + local * F::kScales;
-            multiply<FMT>(sm, sc, kind, s0, s1, inv, lane, b, acc);
+            const int pair = F::kNvfp4 && pairs ? local & 1 : -1;
+            const char* sm = ring + slot * kStageBytes + (pair < 0 ? local : local & ~1) * F::kCodes;
+            const char* sc = ring + slot * kStageBytes + kStagePieces * F::kCodes + local * (pair < 0 ? F::kScales : 8);
+            multiply<FMT>(sm, sc, pair, kind, s0, s1, inv, eights, lane, b, acc);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&empty[slot]);
@@ -678,6 +724,7 @@ bool make_cut(Args& a, int kind) {
   c.columns = c.pieces < kMulWarps ? c.pieces : kMulWarps;
   c.halves = (c.columns + kStagePieces - 1) / kStagePieces;
   c.steps = (c.pieces + c.columns - 1) / c.columns;
+  c.pairs = F::kNvfp4 && c.K % 256 == 0;
   // as many rows per unit as keep all the warps busy, unless there are then fewer than four units for every SM
   const int R = a.f.T * a.f.k, active = R < d.E ? R : d.E;
   auto size = [&](int groups) {
@@ -705,15 +752,22 @@ bool make_cut(Args& a, int kind) {
     return tc_make_map_nd(&a.map[1], U32, v.a, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) &&
            tc_make_map_nd(&a.smap[1], U16, v.b, 3, sdims, sstrides, sbox, CU_TENSOR_MAP_SWIZZLE_NONE);
   }
-  const uint64_t rb = F::kRowBytes, row = c.pieces * rb;  // bytes of a piece's row and of a whole one
+  const uint64_t row = (uint64_t)c.pieces * F::kRowBytes;  // bytes of a matrix row
+  const uint64_t rb = c.pairs ? 128 : F::kRowBytes, parts = row / rb;  // bytes of it that a piece, or two, take
+  const uint32_t box_parts = c.pairs ? cols / 2 : cols;
+  if (c.pairs) {
+    const uint64_t sdims[4] = {K / 16, rows, kind ? E : 2, E}, sstrides[3] = {K / 16, kind ? N * (K / 16) : rows * (K / 16), N * (K / 16)};
+    const uint32_t sbox[4] = {64, kind ? 32u : 16u, kind ? 1u : 2u, 1};
+    if (!tc_make_map_nd(&a.smap[kind], U8, v.b, kind ? 3 : 4, sdims, sstrides, sbox, CU_TENSOR_MAP_SWIZZLE_NONE)) return false;
+  }
   const CUtensorMapSwizzle sw = rb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
   if (kind == 0) {
-    const uint64_t dims[5] = {rb, rows, 2, (uint64_t)c.pieces, E}, strides[4] = {row, row * rows, rb, row * N};
-    const uint32_t box[5] = {(uint32_t)rb, 16, 2, cols, 1};
+    const uint64_t dims[5] = {rb, rows, 2, parts, E}, strides[4] = {row, row * rows, rb, row * N};
+    const uint32_t box[5] = {(uint32_t)rb, 16, 2, box_parts, 1};
     return tc_make_map_nd(&a.map[0], U8, v.a, 5, dims, strides, box, sw);
   }
-  const uint64_t dims[4] = {rb, N, (uint64_t)c.pieces, E}, strides[3] = {row, rb, row * N};
-  const uint32_t box[4] = {(uint32_t)rb, 32, cols, 1};
+  const uint64_t dims[4] = {rb, N, parts, E}, strides[3] = {row, rb, row * N};
+  const uint32_t box[4] = {(uint32_t)rb, 32, box_parts, 1};
   return tc_make_map_nd(&a.map[1], U8, v.a, 4, dims, strides, box, sw);
 }
 

@@ -77,8 +77,9 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(const Fp8QuantAr
   }
 }
 
-// Any others: sixteen lanes per group, eight elements each, one at a time.
-template <class T>
+// Any others: sixteen lanes per group, eight elements each; WIDE: these are whole and on multiples of 16 bytes (8 of codes), else one
+// at a time.
+template <class T, bool WIDE>
 __global__ void __launch_bounds__(kThreads) fp8_quantize_any_kernel(const Fp8QuantArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_any_kernel(const Fp8Qua
     const int g = live ? (int)(i - t * a.groups) : 0, k = 128 * g + 8 * sub, left = live ? a.K - k : 0;
     float v[8];
     if (left > 0) {
-      load8<T, false>((const T*)a.x + t * a.ldx + k, left, v);
+      load8<T, WIDE>((const T*)a.x + t * a.ldx + k, left, v);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = 0.f;
@@ -104,11 +105,18 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_any_kernel(const Fp8Qua
     const float s = fp8_scale(m);
     if (left <= 0) continue;
     uint8_t* q = a.q + t * a.ldq + k;
+    if (WIDE) {
+      uint32_t c[2];
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      const uint32_t c = fp8_codes2(v[j], v[j + 1], s);
-      if (j < left) q[j] = (uint8_t)c;
-      if (j + 1 < left) q[j + 1] = (uint8_t)(c >> 8);
+      for (int j = 0; j < 2; ++j) c[j] = fp8_codes2(v[4 * j], v[4 * j + 1], s) | fp8_codes2(v[4 * j + 2], v[4 * j + 3], s) << 16;
+      *(uint2*)q = make_uint2(c[0], c[1]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const uint32_t c = fp8_codes2(v[j], v[j + 1], s);
+        if (j < left) q[j] = (uint8_t)c;
+        if (j + 1 < left) q[j + 1] = (uint8_t)(c >> 8);
+      }
     }
     if (sub == 0) a.sinv[i] = __fdiv_rn(1.f, s);
   }
@@ -116,13 +124,14 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_any_kernel(const Fp8Qua
 
 template <class T>
 cudaError_t launch(const Fp8QuantArgs& a, cudaStream_t s) {
-  const bool wide = a.K % 128 == 0 && (uintptr_t)a.x % 16 == 0 && a.ldx * sizeof(T) % 16 == 0 && (uintptr_t)a.q % 8 == 0 && a.ldq % 8 == 0;
+  const bool parts = a.K % 8 == 0 && (uintptr_t)a.x % 16 == 0 && a.ldx * sizeof(T) % 16 == 0 && (uintptr_t)a.q % 8 == 0 && a.ldq % 8 == 0, wide = parts && a.K % 128 == 0;
   const int per = wide ? kThreads / 8 : kThreads / 16;  // groups of a block
   const int64_t blocks = ((int64_t)a.T * a.groups + per - 1) / per, cap = (int64_t)tc_num_sms() * (wide ? 8 : 64);
   const dim3 grid((unsigned)(blocks < cap ? blocks : cap));
   note_launches(1);
   return wide ? launch_pdl(fp8_quantize_kernel<T>, grid, dim3(kThreads), 0, s, a)
-              : launch_pdl(fp8_quantize_any_kernel<T>, grid, dim3(kThreads), 0, s, a);
+         : parts ? launch_pdl(fp8_quantize_any_kernel<T, true>, grid, dim3(kThreads), 0, s, a)
+                 : launch_pdl(fp8_quantize_any_kernel<T, false>, grid, dim3(kThreads), 0, s, a);
 }
 
 }  // namespace
