@@ -1,27 +1,28 @@
 // The experts of moe_layer_few in one kernel: gate/up, down and the combine.
 //
 // Tokens of one expert go four at a time (an entry: an expert and up to four of its (token, choice) slots).  Work is cut into
-// units of an entry's weight rows, whole along K: 16 gates and the same features' ups, or 32 outputs (a multiple of these
-// where K is short); first every unit of the gate/up matrices, entry by entry, then those of the down matrices.  Blocks
+// units of an entry's weight rows, whole along K: 16 gates and the same features' ups, or 32 outputs (twice these where K
+// is short); first every unit of the gate/up matrices, entry by entry, then those of the down matrices.  Blocks
 // take runs of units by ticket in that order, so whoever waits (a down unit for its entry's h) waits for units that running
 // blocks hold and that wait for nothing: no two blocks have to be resident together, and calls on other streams cannot
 // stand in the way.  An atomic's answer takes over a microsecond, so a block gets along with one ticket per matrix and asks for
 // the next one as it starts a run.
 //
 // One warp of a block copies by TMA, eight pieces of 128 columns (64 of bf16) by 32 rows to a stage of shared memory,
-// 144 to 192 KB ahead (HBM's rate and latency ask for some 45), into the down matrices while h is not there yet.  Sixteen warps
-// take a piece of a unit each, decode it straight into MMA operands, multiply it with the entry's tokens, whose operands stay in
-// registers from unit to unit, and leave their sums in shared memory.  Three more take the units in turn, add the sums up
-// and finish the rows: h = silu(gate) up, or weighted rows of y.  What copied sums y over each token's experts at the end,
-// in their order.
+// 108 to 128 KB ahead (HBM's rate and latency ask for some 45), into the down matrices while h is not there yet.  Two teams of eight
+// warps, with stages of their own, take the units in turn: a warp takes a piece of a stage, decodes it straight into MMA operands, multiplies it with
+// the entry's tokens, whose operands it keeps in shared memory from unit to unit, and leaves its sums of 32 rows there too.  A
+// ninth warp per team adds them up and finishes the rows: h = silu(gate) up, or weighted rows of y.  What copied sums y over each
+// token's experts at the end, in their order.
 //
 // h and y carry no flags: a value that is not there yet is a NaN that is never written, and who needs it loads until it has
 // changed.  With counters behind fences in their place a block's units took up to half as long again (134 us for 90 at 16
 // tokens of FP8, 128 experts of 2048 x 768, whichever warp fenced); a fence waits for the SM's traffic.
 //
-// What it takes: every warp's work on a unit is a chain of latencies, about 1000 cycles, where HBM brings a unit of FP8 in 2800
-// and one of four bits in 1500.  So nothing in that chain may wait for L2: no spilled register (with 222 KB of
-// shared memory there is next to no L1), no scale or address that was not asked for early, and the copies are another warp's.
+// What it takes: a warp's work on a unit is a chain of latencies, some 2000 cycles without its bytes, where HBM brings a unit of FP8 in 2800
+// and one of four bits in 1500: hence teams, each on a unit of its own (one team of sixteen: 94 us at 16 tokens of FP8, 89 of INT4).
+// And nothing in that chain may wait for L2: no spilled register (with 222 KB of shared memory there is next to no L1), no scale or
+// address that was not asked for early; the copies are another warp's.
 #include "moe_few.cuh"
 #include "moe_formats.cuh"
 #include "moe_tc.cuh"
@@ -32,11 +33,13 @@ using namespace tc;
 
 namespace {
 
-constexpr int kMulWarps = 16, kEndWarps = 3, kCopyWarp = kMulWarps + kEndWarps;
+constexpr int kTeams = 2, kTeam = 8, kMulWarps = kTeams * kTeam, kCopyWarp = kMulWarps + kTeams;
 constexpr int kWarps = kCopyWarp + 1, kThreads = 32 * kWarps;
 constexpr int kEntryRows = 4;
-constexpr int kStagePieces = 8;
-constexpr int kMaxStages = 8;
+constexpr int kStagePieces = kTeam;
+constexpr int kQueue = 8;   // units that the copies may be ahead of the warps
+constexpr int kParts = 3;   // blocks of 32 rows that a team may be ahead of its ninth warp
+constexpr int kMaxStages = 3;
 constexpr int kTokens = 4;  // per combined piece of 32 columns
 
 template <int FMT>
@@ -48,9 +51,10 @@ struct Format {
   static constexpr int kCodes = 32 * kRowBytes;                     // bytes of a piece's codes, 32 rows
   static constexpr int kScales = kNvfp4 ? 256 : kInt4 ? 64 : 0;     // and of the scales that come along
   static constexpr int kStage = kStagePieces * (kCodes + kScales);  // a multiple of 512
-  static constexpr int kStages = kNvfp4 || kInt4 ? kMaxStages : 6;
-  static constexpr int kParts = kEndWarps * kMulWarps * 512;
-  static constexpr int kSmem = 1024 + kStages * ((kStage + 1023) / 1024 * 1024) + kParts;
+  static constexpr int kStages = kNvfp4 || kInt4 ? 3 : 2;           // of each team: whoever waits for a stage has seen all that were in its place
+  static constexpr int kOperands = kRegs * 128;                     // bytes of a piece's activations
+  static constexpr int kKept = 4096 / kOperands;                    // pieces per unit whose activations a warp keeps
+  static constexpr int kSmem = 1024 + kTeams * kStages * ((kStage + 1023) / 1024 * 1024) + kMulWarps * 4096 + kTeams * kParts * kTeam * 512;
 };
 
 // One of the two matrices.
@@ -59,12 +63,10 @@ struct Cut {
   const float* gs;
   int N, K;          // stored rows and columns per expert
   int rows, pieces;  // features or outputs; pieces of K
-  int columns;       // warps along K
-  int halves;        // stages along K: columns / 8, rounded up
-  int groups;        // warps along the rows
+  int steps;         // stages along K
+  int blocks;        // of 32 weight rows per unit
   int step;          // features or outputs per unit
   int units;         // per entry
-  int steps;         // times the warps go along K
   int pairs;         // NVFP4: pieces are copied two by two, 128 bytes of a row, and the scales of eight of them (K % 256 = 0)
 };
 
@@ -428,23 +430,26 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
   constexpr int kStageBytes = (F::kStage + 1023) / 1024 * 1024;
   extern __shared__ __align__(1024) char smem_raw[];
   __shared__ Tables s;
-  __shared__ uint64_t said[kMaxStages], full[kMaxStages], empty[kMaxStages], ufull[kEndWarps], uempty[kEndWarps];
-  __shared__ int4 s_stage[kMaxStages], s_unit[kEndWarps];  // matrix (-1: no more), entry, first row
+  __shared__ uint64_t said[kQueue], heard[kQueue], full[kTeams][kMaxStages], empty[kTeams][kMaxStages], bfull[kTeams][kParts], bempty[kTeams][kParts];
+  __shared__ int4 s_unit[kQueue], s_block[kTeams][kParts];  // matrix (-1: no more), entry, first feature or output
   __shared__ int s_abort;
   char* ring = (char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  float4* parts = (float4*)(ring + F::kStages * kStageBytes);  // [unit % 3][warp][tile][16]
+  float4* parts = (float4*)(ring + kTeams * F::kStages * kStageBytes + kMulWarps * 4096);  // [team][block % 3][warp][tile][16]
   const FewArgs& f = a.f;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int j = 0; j < F::kStages; ++j) {
-      mbar_init(&said[j], 1);
-      mbar_init(&full[j], F::kNvfp4 ? 33 : 1);
-      mbar_init(&empty[j], kMulWarps);
+    for (int j = 0; j < kTeams * kMaxStages; ++j) {
+      mbar_init(&full[0][j], F::kNvfp4 ? 33 : 1);
+      mbar_init(&empty[0][j], kTeam);
     }
-    for (int j = 0; j < kEndWarps; ++j) {
-      mbar_init(&ufull[j], kMulWarps);
-      mbar_init(&uempty[j], 1);
+    for (int j = 0; j < kQueue; ++j) {
+      mbar_init(&said[j], 1);
+      mbar_init(&heard[j], kMulWarps);
+    }
+    for (int j = 0; j < kTeams * kParts; ++j) {
+      mbar_init(&bfull[0][j], kTeam);
+      mbar_init(&bempty[0][j], 1);
     }
     s_abort = 0;
     fence_barrier_init();
@@ -462,24 +467,16 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
     // A matrix's units are divided evenly into as many tickets as there are blocks: a run stays with an entry, whose operands
     // the warps then keep (with eight times as many tickets 16 tokens of FP8 took 103 us for 94).
     const int n0 = gridDim.x, n1 = gridDim.x;
-    int slot = 0, phase = 1, armed = 0;
+    int slots[kTeams] = {0, 0}, phases[kTeams] = {1, 1}, armed = 0, count = 0;  // stage next, parity of its being free
     bool ok = true;
-    // the next stage, free; the descriptor is its first stage's
-    auto take_stage = [&](int kind, int entry, int row) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], phase, &s_abort));
+    auto say = [&](int4 unit) {  // what comes next
+      ok = __all_sync(0xffffffffu, mbar_wait(&heard[count % kQueue], ((count / kQueue) & 1) ^ 1, &s_abort));
       if (ok && lane == 0) {
-        s_stage[slot] = make_int4(kind, entry, row, 0);
-        mbar_arrive(&said[slot]);
+        s_unit[count % kQueue] = unit;
+        mbar_arrive(&said[count % kQueue]);
       }
       __syncwarp();
-      return ok;
-    };
-    auto next_stage = [&]() {
-      armed |= 1 << slot;
-      if (++slot == F::kStages) {
-        slot = 0;
-        phase ^= 1;
-      }
+      ++count;
     };
     for (;;) {
       const int t = __shfl_sync(0xffffffffu, ticket, 0);
@@ -493,50 +490,59 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
       int entry = unit / cut.units, tile = unit - entry * cut.units;
       for (; ok && unit < end; ++unit) {
         const int e = s.expert[entry], row = tile * cut.step;
-        for (int step = 0; ok && step < cut.steps; ++step)
-          for (int group = 0; ok && group < cut.groups; ++group)
-            for (int half = 0; ok && half < cut.halves; ++half) {
-              if (!take_stage(kind, entry, row)) break;
-              char* to = ring + slot * kStageBytes;
-              const int r = row + group * (kind ? 32 : 16), piece = step * kMulWarps + half * kStagePieces;
-              const int count = min(kStagePieces, cut.columns - half * kStagePieces);  // pieces of this stage
+        const int team = count % kTeams;
+        say(make_int4(kind, entry, row, 0));
+        int slot = team ? slots[1] : slots[0], phase = team ? phases[1] : phases[0];
+        for (int block = 0; ok && block < cut.blocks; ++block)
+          for (int step = 0; ok && step < cut.steps; ++step) {
+              ok = __all_sync(0xffffffffu, mbar_wait(&empty[team][slot], phase, &s_abort));
+              if (!ok) break;
+              char* to = ring + (team * F::kStages + slot) * kStageBytes;
+              uint64_t* bar = &full[team][slot];
+              const int r = row + block * (kind ? 32 : 16), piece = step * kStagePieces;
               const bool lone = F::kNvfp4 && !cut.pairs;
               if (lone) {  // scales: a lane per row, eight bytes per piece
                 const int i = kind ? 0 : lane >> 4, n = kind ? r + lane : r + (lane & 15);
                 const char* sc = cut.scales + ((size_t)e * cut.N + i * cut.rows + n) * (cut.K / 16) + 8 * piece;
                 if (n < cut.rows)
-                  for (int j = 0; j < count && piece + j < cut.pieces; ++j) cp_async_8(smem_u32(to + kStagePieces * F::kCodes + j * F::kScales + 8 * lane), sc + 8 * j);
-                cp_async_mbar_arrive_noinc(&full[slot]);
+                  for (int j = 0; j < kStagePieces && piece + j < cut.pieces; ++j) cp_async_8(smem_u32(to + kStagePieces * F::kCodes + j * F::kScales + 8 * lane), sc + 8 * j);
+                cp_async_mbar_arrive_noinc(bar);
               } else if (F::kNvfp4) {
-                mbar_arrive(&full[slot]);  // (the barrier counts every lane's scales)
+                mbar_arrive(bar);  // (the barrier counts every lane's scales)
                 __syncwarp();
               }
               if (lane == 0) {
-                const int box = min(cut.columns, kStagePieces);  // pieces that the maps bring (of pairs, even)
-                mbar_arrive_expect_tx(&full[slot], box * (F::kCodes + (F::kInt4 ? F::kScales : 0)) + (F::kNvfp4 && cut.pairs ? 32 * 64 : 0));
+                const int box = min(cut.pieces, kStagePieces);  // pieces that the maps bring (of pairs, even)
+                mbar_arrive_expect_tx(bar, box * (F::kCodes + (F::kInt4 ? F::kScales : 0)) + (F::kNvfp4 && cut.pairs ? 32 * 64 : 0));
                 if constexpr (F::kInt4) {
                   char* sc = to + kStagePieces * F::kCodes;
                   if (kind == 0) {
-                    tma_load_4d(to, &a.map[0], &full[slot], r, 0, 16 * piece, e);
-                    tma_load_4d(sc, &a.smap[0], &full[slot], r, 0, piece, e);
+                    tma_load_4d(to, &a.map[0], bar, r, 0, 16 * piece, e);
+                    tma_load_4d(sc, &a.smap[0], bar, r, 0, piece, e);
                   } else {
-                    tma_load_3d(to, &a.map[1], &full[slot], r, 16 * piece, e);
-                    tma_load_3d(sc, &a.smap[1], &full[slot], r, piece, e);
+                    tma_load_3d(to, &a.map[1], bar, r, 16 * piece, e);
+                    tma_load_3d(sc, &a.smap[1], bar, r, piece, e);
                   }
                 } else {
                   const int at = F::kNvfp4 && cut.pairs ? piece / 2 : piece;
-                  if (kind == 0) tma_load_5d(to, &a.map[0], &full[slot], 0, r, 0, at, e);
-                  else tma_load_4d(to, &a.map[1], &full[slot], 0, r, at, e);
+                  if (kind == 0) tma_load_5d(to, &a.map[0], bar, 0, r, 0, at, e);
+                  else tma_load_4d(to, &a.map[1], bar, 0, r, at, e);
                   if (F::kNvfp4 && cut.pairs) {
                     char* sc = to + kStagePieces * F::kCodes;
-                    if (kind == 0) tma_load_4d(sc, &a.smap[0], &full[slot], 8 * piece, r, 0, e);
-                    else tma_load_3d(sc, &a.smap[1], &full[slot], 8 * piece, r, e);
+                    if (kind == 0) tma_load_4d(sc, &a.smap[0], bar, 8 * piece, r, 0, e);
+                    else tma_load_3d(sc, &a.smap[1], bar, 8 * piece, r, e);
                   }
                 }
               }
               __syncwarp();
-              next_stage();
+              armed |= 1 << (team * kMaxStages + slot);
+              if (++slot == F::kStages) {
+                slot = 0;
+                phase ^= 1;
+              }
             }
+        if (team) slots[1] = slot, phases[1] = phase;
+        else slots[0] = slot, phases[0] = phase;
         if (++tile == cut.units) {
           tile = 0;
           ++entry;
@@ -544,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
       }
       if (!ok) break;
     }
-    if (ok) take_stage(-1, 0, 0);
+    if (ok) say(make_int4(-1, 0, 0, 0));
     // the combine, in tickets of its own behind all others
     const int sets = (f.T + kTokens - 1) / kTokens, pieces = f.d.H / 32 * sets;
     for (int t = __shfl_sync(0xffffffffu, ticket, 0) - n0 - n1; ok && t < pieces;) {
@@ -556,121 +562,145 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
     if (F::kNvfp4) cp_async_wait<0>();
     if (lane == 0 && s_abort) {  // let every issued copy land before shared memory goes away
       volatile int no_abort = 0;
-      for (int i = 0; i < F::kStages; ++i)
-        if (armed >> i & 1) mbar_wait(&full[i], (i < slot ? phase : phase ^ 1) ^ 1, &no_abort);
+      for (int t = 0; t < kTeams; ++t)
+        for (int i = 0; i < F::kStages; ++i)
+          if (armed >> (t * kMaxStages + i) & 1) mbar_wait(&full[t][i], (i < slots[t] ? phases[t] : phases[t] ^ 1) ^ 1, &no_abort);
     }
     __syncwarp();
   } else if (warp < kMulWarps) {
     // ---------------- pieces: decode and multiply ----------------
-    int slot = 0, phase = 0, end_slot = 0, end_phase = 1, key = -1;
-    uint32_t b[F::kRegs];
-    float inv[2] = {1.f, 1.f}, eights[2] = {0.f, 0.f};
+    const int team = warp / kTeam, w = warp % kTeam;
+    uint4* kept = (uint4*)(ring + kTeams * F::kStages * kStageBytes + warp * 4096) + lane;  // [piece][4 registers][lane]
+    float4* my_parts = parts + (team * kParts * kTeam + w) * 32 + (lane >> 2) * 2 + (lane & 3);
+    int slot = 0, phase = 0, part = 0, part_phase = 1;
+    int key[F::kKept];  // whose activations are kept
+#pragma unroll
+    for (int i = 0; i < F::kKept; ++i) key[i] = -1;
+    float inv[F::kKept][2], eights[F::kKept][2];
+#pragma unroll
+    for (int i = 0; i < F::kKept; ++i) inv[i][0] = inv[i][1] = 1.f, eights[i][0] = eights[i][1] = 0.f;
     bool ok = true;
-    auto acquire = [&](uint64_t* bar) { ok = ok && __all_sync(0xffffffffu, mbar_wait(&bar[slot], phase, &s_abort)); };
-    // this matrix's share of the warp: its stage of each step, its place in it; what it takes to find its scales
-    int kind = -1, mine = 0, local = 0, col = 0, stages = 0, steps = 0, pieces = 0, rows = 0, above = 0, pairs = 0;
+    // hand a block over to the ninth warp
+    auto hand_over = [&](int4 block, const float (*acc)[4]) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(&bempty[team][part], part_phase, &s_abort));
+      if (!ok) return;
+      if (acc) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+          if ((lane & 3) < 2) my_parts[part * (kTeam * 32) + 16 * m] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
+      }
+      if (w == 0 && lane == 0) s_block[team][part] = block;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bfull[team][part]);
+      if (++part == kParts) {
+        part = 0;
+        part_phase ^= 1;
+      }
+    };
+    int kind = -1, steps = 0, blocks = 0, pieces = 0, rows = 0, pairs = 0;  // of this matrix
     const float* scales = nullptr;
-    for (;;) {
-      acquire(said);  // the unit is known, its weights may still be on their way
+    for (int n = 0;; ++n) {
+      const int at = n % kQueue;
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(&said[at], (n / kQueue) & 1, &s_abort));
       if (!ok) break;
-      const int4 d = s_stage[slot];
+      const int4 d = s_unit[at];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&heard[at]);
       if (d.x < 0) break;
       if (d.x != kind) {
         kind = d.x;
         const Cut cut = cut_of(a, kind);
-        const int group = warp / cut.columns;
-        col = warp - group * cut.columns;
-        mine = group < cut.groups ? group * cut.halves + col / kStagePieces : -1;
-        local = col % kStagePieces;
-        stages = cut.groups * cut.halves;
         steps = cut.steps;
+        blocks = cut.blocks;
         pieces = cut.pieces;
         pairs = cut.pairs;
         rows = cut.rows;
-        above = group * (kind ? 32 : 16);
         scales = (const float*)cut.scales;
       }
-      const int entry = d.y, n0 = d.z + above;
-      float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      if (n % kTeams != team) continue;  // the other team's
+      const int entry = d.y;
+      for (int block = 0; ok && block < blocks; ++block) {
+        const int n0 = d.z + block * (kind ? 32 : 16);
+        float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll 1
-      for (int step = 0; ok && step < steps; ++step) {
-        const int piece = step * kMulWarps + col;
-        const bool live = mine >= 0 && piece < pieces && n0 < rows;
-        float s0 = 1.f, s1 = 1.f;
-        if (live) {
-          if (FMT == MOE_FMT_FP8_B128_W8A16) {
-            const int e = s.expert[entry];
-            s0 = __ldg(scales + (size_t)((kind ? e * rows : 2 * e * rows) / 128 + n0 / 128) * pieces + piece);
-            s1 = kind ? s0 : __ldg(scales + (size_t)((2 * e + 1) * rows / 128 + n0 / 128) * pieces + piece);
+        for (int step = 0; ok && step < steps; ++step) {
+          const int piece = step * kStagePieces + w;
+          const bool live = piece < pieces;
+          uint32_t b[F::kRegs];
+          float f2[2] = {1.f, 1.f}, e2[2] = {0.f, 0.f}, s0 = 1.f, s1 = 1.f;
+          if (live) {
+            if (FMT == MOE_FMT_FP8_B128_W8A16) {
+              const int e = s.expert[entry];
+              s0 = __ldg(scales + (size_t)((kind ? e * rows : 2 * e * rows) / 128 + n0 / 128) * pieces + piece);
+              s1 = kind ? s0 : __ldg(scales + (size_t)((2 * e + 1) * rows / 128 + n0 / 128) * pieces + piece);
+            }
+            const int want = (kind * kFewSlots + entry) << 16 | piece;
+            const int k = step < F::kKept ? step : F::kKept - 1;  // (past what is kept: loaded each time)
+            int had = key[0];
+#pragma unroll
+            for (int i = 1; i < F::kKept; ++i) had = k == i ? key[i] : had;
+            if (want != had) {
+              if (kind == 0) load_x<FMT>(f, s, entry, piece * F::kPiece, lane, b, e2);
+              else ok = load_h<FMT>(f, s, entry, piece * F::kPiece, lane, b, f2, e2, &s_abort);
+#pragma unroll
+              for (int i = 0; i < F::kRegs / 4; ++i)
+                kept[(k * (F::kRegs / 4) + i) * 32] = make_uint4(b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]);
+#pragma unroll
+              for (int i = 0; i < F::kKept; ++i)
+                if (k == i) {
+                  key[i] = want;
+                  inv[i][0] = f2[0], inv[i][1] = f2[1], eights[i][0] = e2[0], eights[i][1] = e2[1];
+                }
+            } else {
+#pragma unroll
+              for (int i = 0; i < F::kRegs / 4; ++i) {
+                const uint4 u = kept[(k * (F::kRegs / 4) + i) * 32];
+                b[4 * i] = u.x, b[4 * i + 1] = u.y, b[4 * i + 2] = u.z, b[4 * i + 3] = u.w;
+              }
+#pragma unroll
+              for (int i = 0; i < F::kKept; ++i)
+                if (k == i) f2[0] = inv[i][0], f2[1] = inv[i][1], e2[0] = eights[i][0], e2[1] = eights[i][1];
+            }
           }
-          const int want = (kind * kFewSlots + entry) << 16 | piece;
-          if (want != key) {  // the activations are kept from one unit to the next
-            key = want;
-            if (kind == 0) load_x<FMT>(f, s, entry, piece * F::kPiece, lane, b, eights);
-            else ok = load_h<FMT>(f, s, entry, piece * F::kPiece, lane, b, inv, eights, &s_abort);
-          }
-        }
-        for (int i = 0; ok && i < stages; ++i) {
-          acquire(full);
+          ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[team][slot], phase, &s_abort));
           if (!ok) break;
-          if (live && i == mine) {
-            const int pair = F::kNvfp4 && pairs ? local & 1 : -1;
-            const char* sm = ring + slot * kStageBytes + (pair < 0 ? local : local & ~1) * F::kCodes;
-            const char* sc = ring + slot * kStageBytes + kStagePieces * F::kCodes + local * (pair < 0 ? F::kScales : 8);
-            multiply<FMT>(sm, sc, pair, kind, s0, s1, inv, eights, lane, b, acc);
+          if (live) {
+            const int pair = F::kNvfp4 && pairs ? w & 1 : -1;
+            const char* stage = ring + (team * F::kStages + slot) * kStageBytes;
+            const char* sm = stage + (pair < 0 ? w : w & ~1) * F::kCodes;
+            const char* sc = stage + kStagePieces * F::kCodes + w * (pair < 0 ? F::kScales : 8);
+            multiply<FMT>(sm, sc, pair, kind, s0, s1, f2, e2, lane, b, acc);
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&empty[slot]);
+          if (lane == 0) mbar_arrive(&empty[team][slot]);
           if (++slot == F::kStages) {
             slot = 0;
             phase ^= 1;
           }
         }
-      }
-      if (kind) {  // both terms of h
+        if (kind) {  // both terms of h
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+          for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[m][i] += __shfl_down_sync(0xffffffffu, acc[m][i], 2);
-      }
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(&uempty[end_slot], end_phase, &s_abort));
-      if (!ok) break;
-      float4* to = parts + (end_slot * kMulWarps + warp) * 32 + (lane >> 2) * 2 + (lane & 3);
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-        if ((lane & 3) < 2) to[16 * m] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
-      if (threadIdx.x == 0) s_unit[end_slot] = d;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ufull[end_slot]);
-      if (++end_slot == kEndWarps) {
-        end_slot = 0;
-        end_phase ^= 1;
+            for (int i = 0; i < 4; ++i) acc[m][i] += __shfl_down_sync(0xffffffffu, acc[m][i], 2);
+        }
+        hand_over(make_int4(kind, entry, n0, 0), acc);
       }
     }
-    for (int i = 0; ok && i < kEndWarps; ++i) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&uempty[end_slot], end_phase, &s_abort));
-      if (!ok) break;
-      if (threadIdx.x == 0) s_unit[end_slot] = make_int4(-1, 0, 0, 0);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ufull[end_slot]);
-      if (++end_slot == kEndWarps) {
-        end_slot = 0;
-        end_phase ^= 1;
-      }
-    }
+    hand_over(make_int4(-1, 0, 0, 0), nullptr);
   } else {
     // ---------------- sums over the pieces, h and y ----------------
-    const int q = warp - kMulWarps, t = lane & 1;
-    int last_kind = 0, last_entry = -1;
+    const int team = warp - kMulWarps, t = lane & 1;
+    int last_kind = 0, last_entry = -1, part = 0, phase = 0;
     bool live[2] = {false, false};
     int slot[2] = {0, 0};
     float factor[2] = {0.f, 0.f}, gs = 1.f;
-    for (int phase = 0;; phase ^= 1) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&ufull[q], phase, &s_abort))) break;
-      const int4 u = s_unit[q];
+    for (;;) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&bfull[team][part], phase, &s_abort))) break;
+      const int4 u = s_block[team][part];
       const int kind = u.x, entry = u.y;
       if (kind < 0) break;
-      const Cut cut = cut_of(a, kind);
+      const int columns = min(kTeam, kind ? a.cut[1].pieces : a.cut[0].pieces);
       if (kind != last_kind || entry != last_entry) {
         last_kind = kind;
         last_entry = entry;
@@ -681,27 +711,27 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
           slot[i] = s.rows[entry][live[i] ? 2 * t + i : 0];
           factor[i] = kind ? s.wt[slot[i]] : F::kBf16 ? 1.f : s.xinv[slot[i] / f.k];
         }
-        if (F::kNvfp4) gs = __ldg(cut.gs + s.expert[entry]);
+        if (F::kNvfp4) gs = __ldg((kind ? a.cut[1].gs : a.cut[0].gs) + s.expert[entry]);
       }
-      const int live_groups = min(cut.groups, (cut.rows - u.z) / (kind ? 32 : 16));
-      for (int group = 0; group < live_groups; ++group) {
-        const float4* v = parts + (q * kMulWarps + group * cut.columns) * 32 + lane;
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-        for (int i = 0; i < cut.columns; ++i) {
-          const float4 w = v[32 * i];
-          c[0] += w.x, c[1] += w.y, c[2] += w.z, c[3] += w.w;
-        }
-        if (group + 1 == live_groups) {  // the warps may overwrite
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&uempty[q]);
-        }
-        if (F::kNvfp4) {
+      const float4* v = parts + (team * kParts + part) * (kTeam * 32) + lane;
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) c[i] = c[i] / gs;
+      for (int i = 0; i < kTeam; ++i)
+        if (i < columns) {
+          const float4 x = v[32 * i];
+          c[0] += x.x, c[1] += x.y, c[2] += x.z, c[3] += x.w;
         }
-        finish_rows(f, kind, cut.rows, u.z + group * (kind ? 32 : 16), lane, c, live, slot, factor);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bempty[team][part]);  // the team may overwrite
+      if (++part == kParts) {
+        part = 0;
+        phase ^= 1;
       }
+      if (F::kNvfp4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = c[i] / gs;
+      }
+      finish_rows(f, kind, kind ? a.cut[1].rows : a.cut[0].rows, u.z, lane, c, live, slot, factor);
     }
   }
   __syncthreads();
@@ -721,22 +751,20 @@ bool make_cut(Args& a, int kind) {
   c.K = v.K;
   c.rows = kind ? d.H : d.I;
   c.pieces = c.K / F::kPiece;
-  c.columns = c.pieces < kMulWarps ? c.pieces : kMulWarps;
-  c.halves = (c.columns + kStagePieces - 1) / kStagePieces;
-  c.steps = (c.pieces + c.columns - 1) / c.columns;
+  c.steps = (c.pieces + kStagePieces - 1) / kStagePieces;
   c.pairs = F::kNvfp4 && c.K % 256 == 0;
-  // as many rows per unit as keep all the warps busy, unless there are then fewer than four units for every SM
+  // two blocks of rows per unit where K is a single stage, unless there are then fewer than four units for every SM
   const int R = a.f.T * a.f.k, active = R < d.E ? R : d.E;
-  auto size = [&](int groups) {
-    c.groups = groups;
-    c.step = groups * (kind ? 32 : 16);
-    c.units = (c.rows + c.step - 1) / c.step;
+  auto size = [&](int blocks) {
+    c.blocks = blocks;
+    c.step = blocks * (kind ? 32 : 16);
+    c.units = c.rows / c.step;
   };
-  size(kMulWarps / c.columns);
-  while (c.groups > 1 && (long)active * c.units < 4l * tc_num_sms()) size(c.groups / 2);
+  size(c.steps == 1 ? 2 : 1);
+  if ((long)active * c.units < 4l * tc_num_sms()) size(1);
 
   const uint64_t E = d.E, N = v.N, K = c.K, rows = c.rows;
-  const uint32_t cols = c.columns < kStagePieces ? c.columns : kStagePieces;
+  const uint32_t cols = c.pieces < kStagePieces ? c.pieces : kStagePieces;
   const auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, U16 = CU_TENSOR_MAP_DATA_TYPE_UINT16, U32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
   if (F::kInt4) {
     if (kind == 0) {
