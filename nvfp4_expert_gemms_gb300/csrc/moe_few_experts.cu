@@ -2,27 +2,29 @@
 //
 // Tokens of one expert go four at a time (an entry: an expert and up to four of its (token, choice) slots).  Work is cut into
 // units of an entry's weight rows, whole along K: 16 gates and the same features' ups, or 32 outputs (twice these where K
-// is short); first every unit of the gate/up matrices, entry by entry, then those of the down matrices.  Blocks
+// is short); first every unit of the gate/up matrices, entry by entry, then those of the down matrices.  Teams of warps
 // take runs of units by ticket in that order, so whoever waits (a down unit for its entry's h) waits for units that running
-// blocks hold and that wait for nothing: no two blocks have to be resident together, and calls on other streams cannot
-// stand in the way.  An atomic's answer takes over a microsecond, so a block gets along with one ticket per matrix and asks for
+// teams hold and that wait for nothing: no two blocks have to be resident together, and calls on other streams cannot
+// stand in the way.  An atomic's answer takes over a microsecond, so a team gets along with one ticket per matrix and asks for
 // the next one as it starts a run.
 //
-// One warp of a block copies by TMA, eight pieces of 128 columns (64 of bf16) by 32 rows to a stage of shared memory,
-// 108 to 128 KB ahead (HBM's rate and latency ask for some 45), into the down matrices while h is not there yet.  Two teams of eight
-// warps, with stages of their own, take the units in turn: a warp takes a piece of a stage, decodes it straight into MMA operands, multiplies it with
-// the entry's tokens, whose operands it keeps in shared memory from unit to unit, and leaves its sums of 32 rows there too.  A
-// ninth warp per team adds them up and finishes the rows: h = silu(gate) up, or weighted rows of y.  What copied sums y over each
-// token's experts at the end, in their order.
+// A block holds two teams.  One thread of a team copies by TMA, eight pieces of 128 columns (64 of bf16) by 32 rows to a stage of shared
+// memory, 54 to 64 KB ahead (HBM's rate and latency ask for some 45 per block), into the down matrices while h is not there
+// yet.  Eight warps take a piece of a stage each, decode it straight into MMA operands, multiply it with the entry's tokens, whose
+// operands they keep in shared memory from unit to unit, and leave their sums of 32 rows there too.  A ninth adds them up and
+// finishes the rows: h = silu(gate) up, or weighted rows of y.  Who copied sums y over each token's experts at the end,
+// in their order.
 //
 // h and y carry no flags: a value that is not there yet is a NaN that is never written, and who needs it loads until it has
 // changed.  With counters behind fences in their place a block's units took up to half as long again (134 us for 90 at 16
 // tokens of FP8, 128 experts of 2048 x 768, whichever warp fenced); a fence waits for the SM's traffic.
 //
-// What it takes: a warp's work on a unit is a chain of latencies, some 2000 cycles without its bytes, where HBM brings a unit of FP8 in 2800
-// and one of four bits in 1500: hence teams, each on a unit of its own (one team of sixteen: 94 us at 16 tokens of FP8, 89 of INT4).
-// And nothing in that chain may wait for L2: no spilled register (with 222 KB of shared memory there is next to no L1), no scale or
-// address that was not asked for early; the copies are another warp's.
+// What it takes: a unit's way is a chain of single warps' instructions, at some six cycles each: of the copying thread, the
+// multiplying warps and the finishing one, each of which must keep up with HBM, which brings a unit of FP8 in 2800 cycles per SM and one
+// of four bits in 1500.  Hence teams, each on a unit of its own, and as little as possible per stage for the copying thread (one
+// warp that copied for both, with votes and constants looked up per stage: 91 us at 16 tokens of FP8, 90 of INT4).  And nothing
+// in that chain may wait for L2: no spilled register (with 222 KB of shared memory there is next to no L1), no scale or address
+// that was not asked for early.
 #include "moe_few.cuh"
 #include "moe_formats.cuh"
 #include "moe_tc.cuh"
@@ -34,7 +36,7 @@ using namespace tc;
 namespace {
 
 constexpr int kTeams = 2, kTeam = 8, kMulWarps = kTeams * kTeam, kCopyWarp = kMulWarps + kTeams;
-constexpr int kWarps = kCopyWarp + 1, kThreads = 32 * kWarps;
+constexpr int kWarps = kCopyWarp + kTeams, kThreads = 32 * kWarps;
 constexpr int kEntryRows = 4;
 constexpr int kStagePieces = kTeam;
 constexpr int kQueue = 8;   // units that the copies may be ahead of the warps
@@ -430,8 +432,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
   constexpr int kStageBytes = (F::kStage + 1023) / 1024 * 1024;
   extern __shared__ __align__(1024) char smem_raw[];
   __shared__ Tables s;
-  __shared__ uint64_t said[kQueue], heard[kQueue], full[kTeams][kMaxStages], empty[kTeams][kMaxStages], bfull[kTeams][kParts], bempty[kTeams][kParts];
-  __shared__ int4 s_unit[kQueue], s_block[kTeams][kParts];  // matrix (-1: no more), entry, first feature or output
+  __shared__ uint64_t said[kTeams][kQueue], heard[kTeams][kQueue], full[kTeams][kMaxStages], empty[kTeams][kMaxStages], bfull[kTeams][kParts], bempty[kTeams][kParts];
+  __shared__ int4 s_unit[kTeams][kQueue], s_block[kTeams][kParts];  // matrix (-1: no more), entry, first feature or output
   __shared__ int s_abort;
   char* ring = (char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   float4* parts = (float4*)(ring + kTeams * F::kStages * kStageBytes + kMulWarps * 4096);  // [team][block % 3][warp][tile][16]
@@ -443,9 +445,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
       mbar_init(&full[0][j], F::kNvfp4 ? 33 : 1);
       mbar_init(&empty[0][j], kTeam);
     }
-    for (int j = 0; j < kQueue; ++j) {
-      mbar_init(&said[j], 1);
-      mbar_init(&heard[j], kMulWarps);
+    for (int j = 0; j < kTeams * kQueue; ++j) {
+      mbar_init(&said[0][j], 1);
+      mbar_init(&heard[0][j], kTeam);
     }
     for (int j = 0; j < kTeams * kParts; ++j) {
       mbar_init(&bfull[0][j], kTeam);
@@ -454,103 +456,108 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
     s_abort = 0;
     fence_barrier_init();
   }
-  if (warp == kCopyWarp && lane < 2) prefetch_tmap(&a.map[lane]);
+  if (warp >= kCopyWarp && lane < 2) prefetch_tmap(&a.map[lane]);
   pdl_wait();  // the choice of experts and the scaled rows
   pdl_trigger();
-  int ticket = 0;
-  if (threadIdx.x == 32 * kCopyWarp) ticket = atomicAdd(f.status + 1, 1);
+  int ticket = 0;  // the team's next one
+  if (warp >= kCopyWarp && lane == 0) ticket = atomicAdd(f.status + 1, 1);
   make_entries(f, s);
   const int ngu = s.entries * a.cut[0].units, nunits = ngu + s.entries * a.cut[1].units;
 
-  if (warp == kCopyWarp) {
+  if (warp >= kCopyWarp) {
     // ---------------- copies ----------------
-    // A matrix's units are divided evenly into as many tickets as there are blocks: a run stays with an entry, whose operands
+    // A matrix's units are divided evenly into as many tickets as there are teams: a run stays with an entry, whose operands
     // the warps then keep (with eight times as many tickets 16 tokens of FP8 took 103 us for 94).
-    const int n0 = gridDim.x, n1 = gridDim.x;
-    int slots[kTeams] = {0, 0}, phases[kTeams] = {1, 1}, armed = 0, count = 0;  // stage next, parity of its being free
+    const int team = warp - kCopyWarp, n0 = kTeams * gridDim.x, n1 = n0;
+    int slot = 0, phase = 1, armed = 0, at = 0, at_phase = 1;  // stage next, parity of its being free; place in the queue
     bool ok = true;
-    auto say = [&](int4 unit) {  // what comes next
-      ok = __all_sync(0xffffffffu, mbar_wait(&heard[count % kQueue], ((count / kQueue) & 1) ^ 1, &s_abort));
-      if (ok && lane == 0) {
-        s_unit[count % kQueue] = unit;
-        mbar_arrive(&said[count % kQueue]);
+    auto say = [&](int4 unit) {  // what comes next (one thread)
+      ok = mbar_wait(&heard[team][at], at_phase, &s_abort);
+      if (!ok) return;
+      s_unit[team][at] = unit;
+      mbar_arrive(&said[team][at]);
+      if (++at == kQueue) {
+        at = 0;
+        at_phase ^= 1;
       }
-      __syncwarp();
-      ++count;
     };
     for (;;) {
       const int t = __shfl_sync(0xffffffffu, ticket, 0);
       if (t >= n0 + n1) break;
       const int kind = t >= n0;
-      const int64_t u = kind ? nunits - ngu : ngu, n = kind ? n1 : n0, at = kind ? t - n0 : t;
-      int unit = (int)(at * u / n);
-      const int end = (int)((at + 1) * u / n);
+      const int64_t u = kind ? nunits - ngu : ngu, n = kind ? n1 : n0, nth = kind ? t - n0 : t;
+      int unit = (int)(nth * u / n);
+      const int end = (int)((nth + 1) * u / n);
       if (lane == 0) ticket = atomicAdd(f.status + 1, 1);
       const Cut cut = cut_of(a, kind);
-      int entry = unit / cut.units, tile = unit - entry * cut.units;
+      const int units = cut.units, blocks = cut.blocks, steps = cut.steps, add = cut.step, rows = kind ? 32 : 16;
+      const bool lone = F::kNvfp4 && !cut.pairs;  // NVFP4's scales by every lane, eight bytes at a time
+      const uint32_t bytes = min(cut.pieces, kStagePieces) * (F::kCodes + (F::kInt4 ? F::kScales : 0)) + (F::kNvfp4 && !lone ? 32 * 64 : 0);
+      const CUtensorMap *map = kind ? &a.map[1] : &a.map[0], *smap = kind ? &a.smap[1] : &a.smap[0];
+      int entry = unit / units, tile = unit - entry * units;
+      // a stage's TMA copies (one thread)
+      auto copy = [&](char* to, uint64_t* bar, int r, int piece, int e) {
+        mbar_arrive_expect_tx(bar, bytes);
+        char* sc = to + kStagePieces * F::kCodes;
+        if constexpr (F::kInt4) {
+          if (kind == 0) {
+            tma_load_4d(to, map, bar, r, 0, 16 * piece, e);
+            tma_load_4d(sc, smap, bar, r, 0, piece, e);
+          } else {
+            tma_load_3d(to, map, bar, r, 16 * piece, e);
+            tma_load_3d(sc, smap, bar, r, piece, e);
+          }
+        } else {
+          const int nth = F::kNvfp4 && !lone ? piece / 2 : piece;
+          if (kind == 0) tma_load_5d(to, map, bar, 0, r, 0, nth, e);
+          else tma_load_4d(to, map, bar, 0, r, nth, e);
+          if (F::kNvfp4 && !lone) {
+            if (kind == 0) tma_load_4d(sc, smap, bar, 8 * piece, r, 0, e);
+            else tma_load_3d(sc, smap, bar, 8 * piece, r, e);
+          }
+        }
+      };
       for (; ok && unit < end; ++unit) {
-        const int e = s.expert[entry], row = tile * cut.step;
-        const int team = count % kTeams;
-        say(make_int4(kind, entry, row, 0));
-        int slot = team ? slots[1] : slots[0], phase = team ? phases[1] : phases[0];
-        for (int block = 0; ok && block < cut.blocks; ++block)
-          for (int step = 0; ok && step < cut.steps; ++step) {
-              ok = __all_sync(0xffffffffu, mbar_wait(&empty[team][slot], phase, &s_abort));
+        const int e = s.expert[entry], row = tile * add;
+        if (lane == 0) say(make_int4(kind, entry, row, 0));
+        if (lone) ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (lane == 0 || lone)
+          for (int block = 0; ok && block < blocks; ++block)
+            for (int step = 0; ok && step < steps; ++step) {
+              ok = mbar_wait(&empty[team][slot], phase, &s_abort);
+              if (lone) ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
               char* to = ring + (team * F::kStages + slot) * kStageBytes;
               uint64_t* bar = &full[team][slot];
-              const int r = row + block * (kind ? 32 : 16), piece = step * kStagePieces;
-              const bool lone = F::kNvfp4 && !cut.pairs;
-              if (lone) {  // scales: a lane per row, eight bytes per piece
+              const int r = row + block * rows, piece = step * kStagePieces;
+              if (lone) {
                 const int i = kind ? 0 : lane >> 4, n = kind ? r + lane : r + (lane & 15);
                 const char* sc = cut.scales + ((size_t)e * cut.N + i * cut.rows + n) * (cut.K / 16) + 8 * piece;
-                if (n < cut.rows)
-                  for (int j = 0; j < kStagePieces && piece + j < cut.pieces; ++j) cp_async_8(smem_u32(to + kStagePieces * F::kCodes + j * F::kScales + 8 * lane), sc + 8 * j);
+                for (int j = 0; j < kStagePieces && piece + j < cut.pieces; ++j) cp_async_8(smem_u32(to + kStagePieces * F::kCodes + j * F::kScales + 8 * lane), sc + 8 * j);
                 cp_async_mbar_arrive_noinc(bar);
-              } else if (F::kNvfp4) {
-                mbar_arrive(bar);  // (the barrier counts every lane's scales)
-                __syncwarp();
+              } else if (F::kNvfp4) {  // (the barrier counts every lane's)
+                mbar_arrive_many(bar, 32);
               }
-              if (lane == 0) {
-                const int box = min(cut.pieces, kStagePieces);  // pieces that the maps bring (of pairs, even)
-                mbar_arrive_expect_tx(bar, box * (F::kCodes + (F::kInt4 ? F::kScales : 0)) + (F::kNvfp4 && cut.pairs ? 32 * 64 : 0));
-                if constexpr (F::kInt4) {
-                  char* sc = to + kStagePieces * F::kCodes;
-                  if (kind == 0) {
-                    tma_load_4d(to, &a.map[0], bar, r, 0, 16 * piece, e);
-                    tma_load_4d(sc, &a.smap[0], bar, r, 0, piece, e);
-                  } else {
-                    tma_load_3d(to, &a.map[1], bar, r, 16 * piece, e);
-                    tma_load_3d(sc, &a.smap[1], bar, r, piece, e);
-                  }
-                } else {
-                  const int at = F::kNvfp4 && cut.pairs ? piece / 2 : piece;
-                  if (kind == 0) tma_load_5d(to, &a.map[0], bar, 0, r, 0, at, e);
-                  else tma_load_4d(to, &a.map[1], bar, 0, r, at, e);
-                  if (F::kNvfp4 && cut.pairs) {
-                    char* sc = to + kStagePieces * F::kCodes;
-                    if (kind == 0) tma_load_4d(sc, &a.smap[0], bar, 8 * piece, r, 0, e);
-                    else tma_load_3d(sc, &a.smap[1], bar, 8 * piece, r, e);
-                  }
-                }
-              }
-              __syncwarp();
-              armed |= 1 << (team * kMaxStages + slot);
+              if (lane == 0) copy(to, bar, r, piece, e);
+              armed |= 1 << slot;
               if (++slot == F::kStages) {
                 slot = 0;
                 phase ^= 1;
               }
             }
-        if (team) slots[1] = slot, phases[1] = phase;
-        else slots[0] = slot, phases[0] = phase;
-        if (++tile == cut.units) {
+        if (++tile == units) {
           tile = 0;
           ++entry;
         }
       }
+      __syncwarp();
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      slot = __shfl_sync(0xffffffffu, slot, 0);  // (lane 0's, where it worked alone)
+      phase = __shfl_sync(0xffffffffu, phase, 0);
       if (!ok) break;
     }
-    if (ok) say(make_int4(-1, 0, 0, 0));
+    if (ok && lane == 0) say(make_int4(-1, 0, 0, 0));
+    ok = __shfl_sync(0xffffffffu, ok, 0);
     // the combine, in tickets of its own behind all others
     const int sets = (f.T + kTokens - 1) / kTokens, pieces = f.d.H / 32 * sets;
     for (int t = __shfl_sync(0xffffffffu, ticket, 0) - n0 - n1; ok && t < pieces;) {
@@ -562,9 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
     if (F::kNvfp4) cp_async_wait<0>();
     if (lane == 0 && s_abort) {  // let every issued copy land before shared memory goes away
       volatile int no_abort = 0;
-      for (int t = 0; t < kTeams; ++t)
-        for (int i = 0; i < F::kStages; ++i)
-          if (armed >> (t * kMaxStages + i) & 1) mbar_wait(&full[t][i], (i < slots[t] ? phases[t] : phases[t] ^ 1) ^ 1, &no_abort);
+      for (int i = 0; i < F::kStages; ++i)
+        if (armed >> i & 1) mbar_wait(&full[team][i], (i < slot ? phase : phase ^ 1) ^ 1, &no_abort);
     }
     __syncwarp();
   } else if (warp < kMulWarps) {
@@ -601,11 +607,11 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
     const float* scales = nullptr;
     for (int n = 0;; ++n) {
       const int at = n % kQueue;
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(&said[at], (n / kQueue) & 1, &s_abort));
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(&said[team][at], (n / kQueue) & 1, &s_abort));
       if (!ok) break;
-      const int4 d = s_unit[at];
+      const int4 d = s_unit[team][at];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&heard[at]);
+      if (lane == 0) mbar_arrive(&heard[team][at]);
       if (d.x < 0) break;
       if (d.x != kind) {
         kind = d.x;
@@ -617,7 +623,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
         rows = cut.rows;
         scales = (const float*)cut.scales;
       }
-      if (n % kTeams != team) continue;  // the other team's
       const int entry = d.y;
       for (int block = 0; ok && block < blocks; ++block) {
         const int n0 = d.z + block * (kind ? 32 : 16);
@@ -807,7 +812,7 @@ cudaError_t launch(const FewArgs& f, cudaStream_t s) {
   a.f = f;
   if (!make_cut<FMT>(a, 0) || !make_cut<FMT>(a, 1)) return cudaErrorInvalidValue;
   const long R = (long)f.T * f.k, active = R < f.d.E ? R : f.d.E, sms = tc_num_sms();
-  const long most = active * (a.cut[0].units > a.cut[1].units ? a.cut[0].units : a.cut[1].units);
+  const long most = active * (a.cut[0].units > a.cut[1].units ? a.cut[0].units : a.cut[1].units);  // (a team may go without)
   note_launches(1);
   return launch_pdl(few_experts_kernel<FMT>, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads), Format<FMT>::kSmem, s, a);
 }
