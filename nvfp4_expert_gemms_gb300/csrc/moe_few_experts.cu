@@ -121,7 +121,7 @@ __device__ __forceinline__ void e2m1x8_f16(uint32_t c, uint32_t (&o)[4]) {
 // long as both operands use the same one, so a lane takes what it can read in whole 16-byte parts without bank conflicts.
 template <int FMT>
 __device__ __forceinline__ int element(int t, int j) {
-  return Format<FMT>::kInt4 ? 16 * t + 8 * (j & 1) + 64 * (j >> 1) : Format<FMT>::kPiece / 4 * t + 8 * j;
+  return Format<FMT>::kInt4 ? 8 * t + 32 * j : Format<FMT>::kPiece / 4 * t + 8 * j;
 }
 
 // INT4 words decode into pairs of elements (j, j + 4), every other pair 16 times too large: the same order, and that taken back, for the
@@ -245,47 +245,56 @@ __device__ __forceinline__ bool load_h(const FewArgs& f, const Tables& s, int en
   return true;
 }
 
+// INT4: which four of a unit's 32 stored rows are a lane's.
+__device__ __forceinline__ int four_rows(int lane) { return lane >> 3 | (lane >> 2 & 1) << 2; }
+
 // acc += a piece of 32 rows at `sm` (its scales at `sc`) times the activations.  Tile m's MMA rows g and g + 8 are gate and up
-// n0 + 8 m + g of the features, or outputs n0 + 16 m + g and 8 further on.  inv: what the two columns' activations were scaled by;
+// n0 + 8 m + g of the features, or outputs n0 + 16 m + g and 8 further on; INT4: stored rows 2 m and 2 m + 1 of the lane's four.  inv: what the two columns' activations were scaled by;
 // eights: -8 times their sums (INT4).
 template <int FMT>
 __device__ __forceinline__ void multiply(const char* sm, const char* sc, int pair, int kind, float s0, float s1, const float (&inv)[2], const float (&eights)[2], int lane,
                                          const uint32_t (&b)[Format<FMT>::kRegs], float (&acc)[2][4]) {
   const int g = lane >> 2, t = lane & 3;
+  if constexpr (Format<FMT>::kInt4) {
+    // Words hold eight columns of a row and lie side by side along the rows, 128 bytes per column group: 16-byte parts XORed with
+    // the group (gate/up: each half's four parts by the group mod 4).  A lane reads parts, four rows, which are its rows of both
+    // tiles; even g take the first half's and odd ones the second's, gates and ups or outputs 16 apart, and eight lanes that
+    // read together find different banks.  (With a word of each row at a time, two lanes of four turned about for the
+    // banks' sake, 16 tokens took 88 us.)
+    const int q = four_rows(lane);
+    const uint2 sv = *(const uint2*)(sc + 8 * q);
+    const float2 s01 = __half22float2(*(const __half2*)&sv.x), s23 = __half22float2(*(const __half2*)&sv.y);
+    const char* part[2] = {sm + 128 * t + ((q ^ t) << 4), sm + 128 * t + ((q ^ t ^ (kind ? 4 : 0)) << 4)};
+    float p[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint4 u = *(const uint4*)(part[j & 1] + 512 * j);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      // A nibble of a half-word is, as it stands, a subnormal fp16 number: code 2^-24, the next one 16 times that, which
+      // the activations take back (order_pairs).  Where each weight became 1024 + code - 1032 the decoding took a third of the
+      // time at 16 tokens.
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const uint32_t v0 = w[2 * m] >> (8 * n), v1 = w[2 * m + 1] >> (8 * n);
+          mma(p[m], v0 & 0x000F000Fu, v1 & 0x000F000Fu, v0 & 0x00F000F0u, v1 & 0x00F000F0u, b[4 * j + 2 * n], b[4 * j + 2 * n + 1], false);
+        }
+    }
+    const float scale[4] = {s01.x, s01.y, s23.x, s23.y};
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // code 2^-24 -> code - 8
+        acc[m][i] = fmaf(fmaf(p[m][i], 16777216.f, eights[i & 1]) * scale[2 * m + i / 2], inv[i & 1], acc[m][i]);
+    return;
+  }
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
     float p[4] = {0.f, 0.f, 0.f, 0.f};
     auto step = [&](uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, int i) { mma(p, a0, a1, a2, a3, b[i], b[i + 1], Format<FMT>::kBf16); };
     const int r0 = kind ? 16 * m + g : 8 * m + g, r1 = kind ? r0 + 8 : r0 + 16;
-    if constexpr (Format<FMT>::kInt4) {
-      // words hold eight columns of a row and lie side by side along the rows, 128 bytes per column group: 16-byte parts
-      // XORed with the group (gate/up: each half's four parts by the group mod 4).  With groups two apart the four lanes of a row
-      // read different banks, in gate/up if two of them read the ups first.
-      s0 = __half2float(((const __half*)sc)[r0]), s1 = __half2float(((const __half*)sc)[r1]);
-      const bool turn = kind == 0 && t >= 2;
-      const int at0 = 4 * (turn ? r1 : r0), at1 = 4 * (turn ? r0 : r1);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int kr = 2 * t + (j & 1) + 8 * (j >> 1), swap = (kr & (kind ? 7 : 3)) << 4;
-        const char* line = sm + 128 * kr;
-        const uint32_t y0 = *(const uint32_t*)(line + (at0 ^ swap)), y1 = *(const uint32_t*)(line + (at1 ^ swap));
-        const uint32_t w[2] = {turn ? y1 : y0, turn ? y0 : y1};
-        // A nibble of a half-word is, as it stands, a subnormal fp16 number: code 2^-24, the next one 16 times that, which
-        // the activations take back (order_pairs).  Where each weight became 1024 + code - 1032 the decoding took a third of the
-        // time at 16 tokens.
-        uint32_t x[2][4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int n = 0; n < 4; n += 2) {
-            const uint32_t v = w[i] >> (4 * n);
-            x[i][n] = v & 0x000F000Fu;
-            x[i][n + 1] = v & 0x00F000F0u;
-          }
-        step(x[0][0], x[1][0], x[0][1], x[1][1], 4 * j);
-        step(x[0][2], x[1][2], x[0][3], x[1][3], 4 * j + 2);
-      }
-    } else if constexpr (Format<FMT>::kNvfp4) {
+    if constexpr (Format<FMT>::kNvfp4) {
       // a code times its block's scale has six significant bits: exact in fp16 (2^-10 at the least, 2688 at most)
       // pair < 0: rows of 64 bytes and of 8 scales; else the pair-th half of rows of 128 bytes, 16-byte parts XORed with the row, and
       // rows of 64 scales
@@ -318,10 +327,6 @@ __device__ __forceinline__ void multiply(const char* sm, const char* sc, int pai
             step(e4m3x2_f16(w0[j]), e4m3x2_f16(w1[j]), e4m3x2_f16(w0[j] >> 16), e4m3x2_f16(w1[j] >> 16), 8 * q + 2 * j);
         }
       }
-    }
-    if constexpr (Format<FMT>::kInt4) {  // code 2^-24 -> code - 8
-#pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = fmaf(p[i], 16777216.f, eights[i & 1]);
     }
     // (the scales one after the other: their product may be below fp32's range where the sums are not)
     acc[m][0] = fmaf(p[0] * s0, inv[0], acc[m][0]), acc[m][1] = fmaf(p[1] * s0, inv[1], acc[m][1]);
@@ -382,18 +387,32 @@ __device__ __forceinline__ void make_entries(const FewArgs& f, Tables& s) {
 
 // Finishes 32 rows of an entry (one warp): lane 16 m + 2 g + t (t < 2) holds tile m's sums of its rows g and g + 8 for the
 // entry's rows 2 t and 2 t + 1.  n0: the first feature or output; factor: what the two rows' sums are multiplied with.
-__device__ __forceinline__ void finish_rows(const FewArgs& f, int kind, int rows, int n0, int lane, const float (&c)[4], const bool (&live)[2],
+template <int FMT>
+__device__ __forceinline__ void finish_rows(const FewArgs& f, int kind, int rows, int n0, int lane, float (&c)[4], const bool (&live)[2],
                                             const int (&slot)[2], const float (&factor)[2]) {
   const int m = lane >> 4, g = lane >> 1 & 7;
+  int feature = n0 + 8 * m + g, output = n0 + 16 * m + g, next = 8;
+  if (Format<FMT>::kInt4) {
+    const int q = four_rows(2 * (lane & 15));
+    feature = n0 + 4 * (q & 3) + 2 * m + (g & 1), output = n0 + 4 * q + 2 * m, next = 1;
+    if (kind == 0) {  // even g hold two features' gates, odd ones their ups: the first feature to the even ones
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float theirs = __shfl_xor_sync(0xffffffffu, g & 1 ? c[i] : c[2 + i], 2);
+        if (g & 1) c[i] = theirs;
+        else c[2 + i] = theirs;
+      }
+    }
+  }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     if (kind == 0) {
       const float gate = c[i] * factor[i], up = c[2 + i] * factor[i];
-      if (live[i]) store_now(f.h + (size_t)slot[i] * rows + n0 + 8 * m + g, gate / (1.f + expf(-gate)) * up);
+      if (live[i]) store_now(f.h + (size_t)slot[i] * rows + feature, gate / (1.f + expf(-gate)) * up);
     } else if (live[i]) {
-      float* y = f.y + (size_t)slot[i] * rows + n0 + 16 * m + g;
+      float* y = f.y + (size_t)slot[i] * rows + output;
       store_now(y, c[i] * factor[i]);
-      store_now(y + 8, c[2 + i] * factor[i]);
+      store_now(y + next, c[2 + i] * factor[i]);
     }
   }
 }
@@ -736,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[i] = c[i] / gs;
       }
-      finish_rows(f, kind, kind ? a.cut[1].rows : a.cut[0].rows, u.z, lane, c, live, slot, factor);
+      finish_rows<FMT>(f, kind, kind ? a.cut[1].rows : a.cut[0].rows, u.z, lane, c, live, slot, factor);
     }
   }
   __syncthreads();
