@@ -39,9 +39,9 @@ constexpr int kTeams = 2, kTeam = 8, kMulWarps = kTeams * kTeam, kCopyWarp = kMu
 constexpr int kWarps = kCopyWarp + kTeams, kThreads = 32 * kWarps;
 constexpr int kEntryRows = 4;
 constexpr int kStagePieces = kTeam;
-constexpr int kQueue = 8;   // units that the copies may be ahead of the warps
 constexpr int kParts = 3;   // blocks of 32 rows that a team may be ahead of its ninth warp
 constexpr int kMaxStages = 3;
+constexpr int kLast = 1 << 16;
 constexpr int kTokens = 4;  // per combined piece of 32 columns
 
 template <int FMT>
@@ -177,6 +177,18 @@ __device__ __forceinline__ bool all_set(const uint4& v) { return v.x != kFewUnse
 __device__ __forceinline__ void store_now(float* p, float v) {
   asm volatile("st.relaxed.gpu.global.b32 [%0], %1;" ::"l"(p), "r"(few_value(v)) : "memory");
 }
+// mbar_wait in few instructions: a block's roles have to fit the instruction caches together.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  long long since = 0;
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    const long long now = clock64();
+    if (since == 0) since = now;
+    if (now - since > kWaitLimitCycles) *abort = 1;
+    if (*abort) return false;
+  }
+  return true;
+}
 // A wait's clock: true once it has run out, or another thread of the block has given up.
 struct Patience {
   long long since = 0;
@@ -253,8 +265,14 @@ __device__ __forceinline__ int four_rows(int lane) { return lane >> 3 | (lane >>
 // eights: -8 times their sums (INT4).
 template <int FMT>
 __device__ __forceinline__ void multiply(const char* sm, const char* sc, int pair, int kind, float s0, float s1, const float (&inv)[2], const float (&eights)[2], int lane,
-                                         const uint32_t (&b)[Format<FMT>::kRegs], float (&acc)[2][4]) {
+                                         const uint4* kept, float (&acc)[2][4]) {
   const int g = lane >> 2, t = lane & 3;
+  uint32_t b[Format<FMT>::kRegs];
+#pragma unroll
+  for (int i = 0; i < Format<FMT>::kRegs / 4; ++i) {
+    const uint4 u = kept[32 * i];
+    b[4 * i] = u.x, b[4 * i + 1] = u.y, b[4 * i + 2] = u.z, b[4 * i + 3] = u.w;
+  }
   if constexpr (Format<FMT>::kInt4) {
     // Words hold eight columns of a row and lie side by side along the rows, 128 bytes per column group: 16-byte parts XORed with
     // the group (gate/up: each half's four parts by the group mod 4).  A lane reads parts, four rows, which are its rows of both
@@ -287,50 +305,50 @@ __device__ __forceinline__ void multiply(const char* sm, const char* sc, int pai
 #pragma unroll
       for (int i = 0; i < 4; ++i)  // code 2^-24 -> code - 8
         acc[m][i] = fmaf(fmaf(p[m][i], 16777216.f, eights[i & 1]) * scale[2 * m + i / 2], inv[i & 1], acc[m][i]);
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    float p[4] = {0.f, 0.f, 0.f, 0.f};
-    auto step = [&](uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, int i) { mma(p, a0, a1, a2, a3, b[i], b[i + 1], Format<FMT>::kBf16); };
-    const int r0 = kind ? 16 * m + g : 8 * m + g, r1 = kind ? r0 + 8 : r0 + 16;
-    if constexpr (Format<FMT>::kNvfp4) {
-      // a code times its block's scale has six significant bits: exact in fp16 (2^-10 at the least, 2688 at most)
-      // pair < 0: rows of 64 bytes and of 8 scales; else the pair-th half of rows of 128 bytes, 16-byte parts XORed with the row, and
-      // rows of 64 scales
-      const int srow = pair < 0 ? 8 : 64, row = pair < 0 ? 64 : 128, part = (pair < 0 ? t : (4 * pair + t) ^ g) << 4;
-      const uint32_t q0 = e4m3x2_f16(*(const uint16_t*)(sc + srow * r0 + 2 * t)), q1 = e4m3x2_f16(*(const uint16_t*)(sc + srow * r1 + 2 * t));
-      const uint4 u = *(const uint4*)(sm + row * r0 + part), v = *(const uint4*)(sm + row * r1 + part);
-      const uint32_t w0[4] = {u.x, u.y, u.z, u.w}, w1[4] = {v.x, v.y, v.z, v.w};
+    for (int m = 0; m < 2; ++m) {
+      float p[4] = {0.f, 0.f, 0.f, 0.f};
+      auto step = [&](uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, int i) { mma(p, a0, a1, a2, a3, b[i], b[i + 1], Format<FMT>::kBf16); };
+      const int r0 = kind ? 16 * m + g : 8 * m + g, r1 = kind ? r0 + 8 : r0 + 16;
+      if constexpr (Format<FMT>::kNvfp4) {
+        // a code times its block's scale has six significant bits: exact in fp16 (2^-10 at the least, 2688 at most)
+        // pair < 0: rows of 64 bytes and of 8 scales; else the pair-th half of rows of 128 bytes, 16-byte parts XORed with the row, and
+        // rows of 64 scales
+        const int srow = pair < 0 ? 8 : 64, row = pair < 0 ? 64 : 128, part = (pair < 0 ? t : (4 * pair + t) ^ g) << 4;
+        const uint32_t q0 = e4m3x2_f16(*(const uint16_t*)(sc + srow * r0 + 2 * t)), q1 = e4m3x2_f16(*(const uint16_t*)(sc + srow * r1 + 2 * t));
+        const uint4 u = *(const uint4*)(sm + row * r0 + part), v = *(const uint4*)(sm + row * r1 + part);
+        const uint32_t w0[4] = {u.x, u.y, u.z, u.w}, w1[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t z0 = __byte_perm(q0, q0, j < 2 ? 0x1010 : 0x3232), z1 = __byte_perm(q1, q1, j < 2 ? 0x1010 : 0x3232);
-        uint32_t x[4], y[4];
-        e2m1x8_f16(w0[j], x);
-        e2m1x8_f16(w1[j], y);
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t z0 = __byte_perm(q0, q0, j < 2 ? 0x1010 : 0x3232), z1 = __byte_perm(q1, q1, j < 2 ? 0x1010 : 0x3232);
+          uint32_t x[4], y[4];
+          e2m1x8_f16(w0[j], x);
+          e2m1x8_f16(w1[j], y);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) step(hmul2(x[2 * i], z0), hmul2(y[2 * i], z1), hmul2(x[2 * i + 1], z0), hmul2(y[2 * i + 1], z1), 4 * j + 2 * i);
-      }
-    } else {
-      // rows of 128 bytes, 16-byte parts XORed with the row
+          for (int i = 0; i < 2; ++i) step(hmul2(x[2 * i], z0), hmul2(y[2 * i], z1), hmul2(x[2 * i + 1], z0), hmul2(y[2 * i + 1], z1), 4 * j + 2 * i);
+        }
+      } else {
+        // rows of 128 bytes, 16-byte parts XORed with the row
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int part = ((2 * t + q) ^ g) << 4;
-        const uint4 u = *(const uint4*)(sm + 128 * r0 + part), v = *(const uint4*)(sm + 128 * r1 + part);
-        if constexpr (Format<FMT>::kBf16) {
-          step(u.x, v.x, u.y, v.y, 4 * q);
-          step(u.z, v.z, u.w, v.w, 4 * q + 2);
-        } else {
-          const uint32_t w0[4] = {u.x, u.y, u.z, u.w}, w1[4] = {v.x, v.y, v.z, v.w};
+        for (int q = 0; q < 2; ++q) {
+          const int part = ((2 * t + q) ^ g) << 4;
+          const uint4 u = *(const uint4*)(sm + 128 * r0 + part), v = *(const uint4*)(sm + 128 * r1 + part);
+          if constexpr (Format<FMT>::kBf16) {
+            step(u.x, v.x, u.y, v.y, 4 * q);
+            step(u.z, v.z, u.w, v.w, 4 * q + 2);
+          } else {
+            const uint32_t w0[4] = {u.x, u.y, u.z, u.w}, w1[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            step(e4m3x2_f16(w0[j]), e4m3x2_f16(w1[j]), e4m3x2_f16(w0[j] >> 16), e4m3x2_f16(w1[j] >> 16), 8 * q + 2 * j);
+            for (int j = 0; j < 4; ++j)
+              step(e4m3x2_f16(w0[j]), e4m3x2_f16(w1[j]), e4m3x2_f16(w0[j] >> 16), e4m3x2_f16(w1[j] >> 16), 8 * q + 2 * j);
+          }
         }
       }
+      // (the scales one after the other: their product may be below fp32's range where the sums are not)
+      acc[m][0] = fmaf(p[0] * s0, inv[0], acc[m][0]), acc[m][1] = fmaf(p[1] * s0, inv[1], acc[m][1]);
+      acc[m][2] = fmaf(p[2] * s1, inv[0], acc[m][2]), acc[m][3] = fmaf(p[3] * s1, inv[1], acc[m][3]);
     }
-    // (the scales one after the other: their product may be below fp32's range where the sums are not)
-    acc[m][0] = fmaf(p[0] * s0, inv[0], acc[m][0]), acc[m][1] = fmaf(p[1] * s0, inv[1], acc[m][1]);
-    acc[m][2] = fmaf(p[2] * s1, inv[0], acc[m][2]), acc[m][3] = fmaf(p[3] * s1, inv[1], acc[m][3]);
   }
 }
 
@@ -451,8 +469,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
   constexpr int kStageBytes = (F::kStage + 1023) / 1024 * 1024;
   extern __shared__ __align__(1024) char smem_raw[];
   __shared__ Tables s;
-  __shared__ uint64_t said[kTeams][kQueue], heard[kTeams][kQueue], full[kTeams][kMaxStages], empty[kTeams][kMaxStages], bfull[kTeams][kParts], bempty[kTeams][kParts];
-  __shared__ int4 s_unit[kTeams][kQueue], s_block[kTeams][kParts];  // matrix (-1: no more), entry, first feature or output
+  __shared__ uint64_t full[kTeams][kMaxStages], empty[kTeams][kMaxStages], bfull[kTeams][kParts], bempty[kTeams][kParts];
+  __shared__ int4 s_stage[kTeams][kMaxStages], s_block[kTeams][kParts];  // matrix (-1: no more), entry, first feature or output, step (kLast: the last)
   __shared__ int s_abort;
   char* ring = (char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   float4* parts = (float4*)(ring + kTeams * F::kStages * kStageBytes + kMulWarps * 4096);  // [team][block % 3][warp][tile][16]
@@ -463,10 +481,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
     for (int j = 0; j < kTeams * kMaxStages; ++j) {
       mbar_init(&full[0][j], F::kNvfp4 ? 33 : 1);
       mbar_init(&empty[0][j], kTeam);
-    }
-    for (int j = 0; j < kTeams * kQueue; ++j) {
-      mbar_init(&said[0][j], 1);
-      mbar_init(&heard[0][j], kTeam);
     }
     for (int j = 0; j < kTeams * kParts; ++j) {
       mbar_init(&bfull[0][j], kTeam);
@@ -488,18 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
     // A matrix's units are divided evenly into as many tickets as there are teams: a run stays with an entry, whose operands
     // the warps then keep (with eight times as many tickets 16 tokens of FP8 took 103 us for 94).
     const int team = warp - kCopyWarp, n0 = kTeams * gridDim.x, n1 = n0;
-    int slot = 0, phase = 1, armed = 0, at = 0, at_phase = 1;  // stage next, parity of its being free; place in the queue
+    int slot = 0, phase = 1, armed = 0;  // stage next, parity of its being free
     bool ok = true;
-    auto say = [&](int4 unit) {  // what comes next (one thread)
-      ok = mbar_wait(&heard[team][at], at_phase, &s_abort);
-      if (!ok) return;
-      s_unit[team][at] = unit;
-      mbar_arrive(&said[team][at]);
-      if (++at == kQueue) {
-        at = 0;
-        at_phase ^= 1;
-      }
-    };
     for (;;) {
       const int t = __shfl_sync(0xffffffffu, ticket, 0);
       if (t >= n0 + n1) break;
@@ -538,12 +542,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
       };
       for (; ok && unit < end; ++unit) {
         const int e = s.expert[entry], row = tile * add;
-        if (lane == 0) say(make_int4(kind, entry, row, 0));
-        if (lone) ok = __shfl_sync(0xffffffffu, ok, 0);
         if (lane == 0 || lone)
           for (int block = 0; ok && block < blocks; ++block)
             for (int step = 0; ok && step < steps; ++step) {
-              ok = mbar_wait(&empty[team][slot], phase, &s_abort);
+              ok = wait(&empty[team][slot], phase, &s_abort);
               if (lone) ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
               char* to = ring + (team * F::kStages + slot) * kStageBytes;
@@ -557,7 +559,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
               } else if (F::kNvfp4) {  // (the barrier counts every lane's)
                 mbar_arrive_many(bar, 32);
               }
-              if (lane == 0) copy(to, bar, r, piece, e);
+              if (lane == 0) {
+                s_stage[team][slot] = make_int4(kind, entry, r, step + 1 == steps ? step | kLast : step);
+                copy(to, bar, r, piece, e);
+              }
               armed |= 1 << slot;
               if (++slot == F::kStages) {
                 slot = 0;
@@ -575,7 +580,18 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
       phase = __shfl_sync(0xffffffffu, phase, 0);
       if (!ok) break;
     }
-    if (ok && lane == 0) say(make_int4(-1, 0, 0, 0));
+    if (ok && lane == 0) {
+      ok = wait(&empty[team][slot], phase, &s_abort);
+      if (ok) {
+        s_stage[team][slot] = make_int4(-1, 0, 0, 0);
+        mbar_arrive_many(&full[team][slot], F::kNvfp4 ? 33 : 1);
+        armed |= 1 << slot;
+        if (++slot == F::kStages) {
+          slot = 0;
+          phase ^= 1;
+        }
+      }
+    }
     ok = __shfl_sync(0xffffffffu, ok, 0);
     // the combine, in tickets of its own behind all others
     const int sets = (f.T + kTokens - 1) / kTokens, pieces = f.d.H / 32 * sets;
@@ -596,122 +612,108 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
     // ---------------- pieces: decode and multiply ----------------
     const int team = warp / kTeam, w = warp % kTeam;
     uint4* kept = (uint4*)(ring + kTeams * F::kStages * kStageBytes + warp * 4096) + lane;  // [piece][4 registers][lane]
-    float4* my_parts = parts + (team * kParts * kTeam + w) * 32 + (lane >> 2) * 2 + (lane & 3);
+    float4* my_parts = parts + (team * kParts * kTeam + w) * 32 + (lane & 2) * 8 + (lane >> 2) * 2 + (lane & 1);
     int slot = 0, phase = 0, part = 0, part_phase = 1;
-    int key[F::kKept];  // whose activations are kept
+    int kind = -1, pieces = 0, rows = 0, steps = 0, pairs = 0;  // of the matrix
+    const float* scales = nullptr;
+    int entry = -1, have = 0;            // the steps of which entry's activations are kept,
+    int line = -1, have_scales = 0;      // and of which 128 rows' scales (FP8)
+    float inv[F::kKept][2], eights[F::kKept][2], s0[F::kKept], s1[F::kKept];
 #pragma unroll
-    for (int i = 0; i < F::kKept; ++i) key[i] = -1;
-    float inv[F::kKept][2], eights[F::kKept][2];
-#pragma unroll
-    for (int i = 0; i < F::kKept; ++i) inv[i][0] = inv[i][1] = 1.f, eights[i][0] = eights[i][1] = 0.f;
+    for (int i = 0; i < F::kKept; ++i) inv[i][0] = inv[i][1] = 1.f, eights[i][0] = eights[i][1] = 0.f, s0[i] = s1[i] = 1.f;
+    float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     bool ok = true;
-    // hand a block over to the ninth warp
-    auto hand_over = [&](int4 block, const float (*acc)[4]) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(&bempty[team][part], part_phase, &s_abort));
-      if (!ok) return;
-      if (acc) {
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-          if ((lane & 3) < 2) my_parts[part * (kTeam * 32) + 16 * m] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
+#pragma unroll 1
+    while (__all_sync(0xffffffffu, wait(&full[team][slot], phase, &s_abort))) {
+      const int4 d = s_stage[team][slot];
+      if (d.x < 0) break;
+      if (d.x != kind) {
+        kind = d.x;
+        const Cut cut = cut_of(a, kind);
+        pieces = cut.pieces;
+        rows = cut.rows;
+        steps = cut.steps;
+        pairs = cut.pairs;
+        scales = (const float*)cut.scales;
+        entry = -1;
       }
-      if (w == 0 && lane == 0) s_block[team][part] = block;
+      if (d.y != entry) {
+        entry = d.y;
+        have = have_scales = 0;
+      }
+      const int step = d.w & (kLast - 1), piece = step * kStagePieces + w;
+      if (piece < pieces) {
+        const int k = min(step, F::kKept - 1), keep = steps <= F::kKept || step < F::kKept - 1 ? 1 << k : 0;  // (past what is kept: loaded each time)
+        uint4* mine = kept + k * (F::kRegs / 4 * 32);
+        float f2[2] = {1.f, 1.f}, e2[2] = {0.f, 0.f}, s2[2] = {1.f, 1.f};
+        if (FMT == MOE_FMT_FP8_B128_W8A16) {
+          if (d.z / 128 != line) {
+            line = d.z / 128;
+            have_scales = 0;
+          }
+          if (!(have_scales >> k & 1)) {
+            const int e = s.expert[entry];
+            s2[0] = __ldg(scales + (size_t)((kind ? e * rows : 2 * e * rows) / 128 + line) * pieces + piece);
+            s2[1] = kind ? s2[0] : __ldg(scales + (size_t)((2 * e + 1) * rows / 128 + line) * pieces + piece);
+#pragma unroll
+            for (int i = 0; i < F::kKept; ++i)
+              if (k == i) s0[i] = s2[0], s1[i] = s2[1];
+            have_scales |= keep;
+          }
+        }
+        if (!(have >> k & 1)) {
+          uint32_t b[F::kRegs];
+          if (kind == 0) load_x<FMT>(f, s, entry, piece * F::kPiece, lane, b, e2);
+          else ok = load_h<FMT>(f, s, entry, piece * F::kPiece, lane, b, f2, e2, &s_abort);
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < F::kRegs / 4; ++i) mine[32 * i] = make_uint4(b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]);
+#pragma unroll
+          for (int i = 0; i < F::kKept; ++i)
+            if (k == i) inv[i][0] = f2[0], inv[i][1] = f2[1], eights[i][0] = e2[0], eights[i][1] = e2[1];
+          have |= keep;
+        }
+#pragma unroll
+        for (int i = 0; i < F::kKept; ++i)
+          if (k == i) f2[0] = inv[i][0], f2[1] = inv[i][1], e2[0] = eights[i][0], e2[1] = eights[i][1], s2[0] = s0[i], s2[1] = s1[i];
+        const int pair = F::kNvfp4 && pairs ? w & 1 : -1;
+        const char* stage = ring + (team * F::kStages + slot) * kStageBytes;
+        const char* sm = stage + (pair < 0 ? w : w & ~1) * F::kCodes;
+        const char* sc = stage + kStagePieces * F::kCodes + w * (pair < 0 ? F::kScales : 8);
+        multiply<FMT>(sm, sc, pair, kind, s2[0], s2[1], f2, e2, lane, mine, acc);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[team][slot]);
+      if (++slot == F::kStages) {
+        slot = 0;
+        phase ^= 1;
+      }
+      if (!(d.w & kLast)) continue;
+      // hand the block over to the ninth warp: lanes t < 2 tile 0, the others tile 1, both terms of h added up
+      float4 sum;
+      float* c = &sum.x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float own = lane & 2 ? acc[1][i] : acc[0][i], other = __shfl_xor_sync(0xffffffffu, lane & 2 ? acc[0][i] : acc[1][i], 2);
+        c[i] = kind ? own + other : lane & 2 ? other : own;
+        acc[0][i] = acc[1][i] = 0.f;
+      }
+      ok = __all_sync(0xffffffffu, wait(&bempty[team][part], part_phase, &s_abort));
+      if (!ok) break;
+      my_parts[part * (kTeam * 32)] = sum;
+      if (w == 0 && lane == 0) s_block[team][part] = d;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bfull[team][part]);
       if (++part == kParts) {
         part = 0;
         part_phase ^= 1;
       }
-    };
-    int kind = -1, steps = 0, blocks = 0, pieces = 0, rows = 0, pairs = 0;  // of this matrix
-    const float* scales = nullptr;
-    for (int n = 0;; ++n) {
-      const int at = n % kQueue;
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(&said[team][at], (n / kQueue) & 1, &s_abort));
-      if (!ok) break;
-      const int4 d = s_unit[team][at];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&heard[team][at]);
-      if (d.x < 0) break;
-      if (d.x != kind) {
-        kind = d.x;
-        const Cut cut = cut_of(a, kind);
-        steps = cut.steps;
-        blocks = cut.blocks;
-        pieces = cut.pieces;
-        pairs = cut.pairs;
-        rows = cut.rows;
-        scales = (const float*)cut.scales;
-      }
-      const int entry = d.y;
-      for (int block = 0; ok && block < blocks; ++block) {
-        const int n0 = d.z + block * (kind ? 32 : 16);
-        float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll 1
-        for (int step = 0; ok && step < steps; ++step) {
-          const int piece = step * kStagePieces + w;
-          const bool live = piece < pieces;
-          uint32_t b[F::kRegs];
-          float f2[2] = {1.f, 1.f}, e2[2] = {0.f, 0.f}, s0 = 1.f, s1 = 1.f;
-          if (live) {
-            if (FMT == MOE_FMT_FP8_B128_W8A16) {
-              const int e = s.expert[entry];
-              s0 = __ldg(scales + (size_t)((kind ? e * rows : 2 * e * rows) / 128 + n0 / 128) * pieces + piece);
-              s1 = kind ? s0 : __ldg(scales + (size_t)((2 * e + 1) * rows / 128 + n0 / 128) * pieces + piece);
-            }
-            const int want = (kind * kFewSlots + entry) << 16 | piece;
-            const int k = step < F::kKept ? step : F::kKept - 1;  // (past what is kept: loaded each time)
-            int had = key[0];
-#pragma unroll
-            for (int i = 1; i < F::kKept; ++i) had = k == i ? key[i] : had;
-            if (want != had) {
-              if (kind == 0) load_x<FMT>(f, s, entry, piece * F::kPiece, lane, b, e2);
-              else ok = load_h<FMT>(f, s, entry, piece * F::kPiece, lane, b, f2, e2, &s_abort);
-#pragma unroll
-              for (int i = 0; i < F::kRegs / 4; ++i)
-                kept[(k * (F::kRegs / 4) + i) * 32] = make_uint4(b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]);
-#pragma unroll
-              for (int i = 0; i < F::kKept; ++i)
-                if (k == i) {
-                  key[i] = want;
-                  inv[i][0] = f2[0], inv[i][1] = f2[1], eights[i][0] = e2[0], eights[i][1] = e2[1];
-                }
-            } else {
-#pragma unroll
-              for (int i = 0; i < F::kRegs / 4; ++i) {
-                const uint4 u = kept[(k * (F::kRegs / 4) + i) * 32];
-                b[4 * i] = u.x, b[4 * i + 1] = u.y, b[4 * i + 2] = u.z, b[4 * i + 3] = u.w;
-              }
-#pragma unroll
-              for (int i = 0; i < F::kKept; ++i)
-                if (k == i) f2[0] = inv[i][0], f2[1] = inv[i][1], e2[0] = eights[i][0], e2[1] = eights[i][1];
-            }
-          }
-          ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[team][slot], phase, &s_abort));
-          if (!ok) break;
-          if (live) {
-            const int pair = F::kNvfp4 && pairs ? w & 1 : -1;
-            const char* stage = ring + (team * F::kStages + slot) * kStageBytes;
-            const char* sm = stage + (pair < 0 ? w : w & ~1) * F::kCodes;
-            const char* sc = stage + kStagePieces * F::kCodes + w * (pair < 0 ? F::kScales : 8);
-            multiply<FMT>(sm, sc, pair, kind, s0, s1, f2, e2, lane, b, acc);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&empty[team][slot]);
-          if (++slot == F::kStages) {
-            slot = 0;
-            phase ^= 1;
-          }
-        }
-        if (kind) {  // both terms of h
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[m][i] += __shfl_down_sync(0xffffffffu, acc[m][i], 2);
-        }
-        hand_over(make_int4(kind, entry, n0, 0), acc);
-      }
     }
-    hand_over(make_int4(-1, 0, 0, 0), nullptr);
+    if (__all_sync(0xffffffffu, wait(&bempty[team][part], part_phase, &s_abort))) {  // no more
+      if (w == 0 && lane == 0) s_block[team][part] = make_int4(-1, 0, 0, 0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bfull[team][part]);
+    }
   } else {
     // ---------------- sums over the pieces, h and y ----------------
     const int team = warp - kMulWarps, t = lane & 1;
@@ -720,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
     int slot[2] = {0, 0};
     float factor[2] = {0.f, 0.f}, gs = 1.f;
     for (;;) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&bfull[team][part], phase, &s_abort))) break;
+      if (!__all_sync(0xffffffffu, wait(&bfull[team][part], phase, &s_abort))) break;
       const int4 u = s_block[team][part];
       const int kind = u.x, entry = u.y;
       if (kind < 0) break;
