@@ -80,7 +80,7 @@ struct Args {
 __device__ __forceinline__ Cut cut_of(const Args& a, int kind) { return kind ? a.cut[1] : a.cut[0]; }
 
 struct Tables {
-  int idx[kFewSlots];
+  alignas(8) uint8_t slots[kMaxE][kFewSlots / 32];  // an expert's, of each 32
   float wt[kFewSlots];
   uint8_t rows[kFewSlots][kEntryRows];  // an entry's slots
   uint8_t expert[kFewSlots], count[kFewSlots];
@@ -352,26 +352,27 @@ __device__ __forceinline__ void multiply(const char* sm, const char* sc, int pai
   }
 }
 
-// The entries, from every token's experts, in shared memory.
+static_assert(kFewSlots == 256, "eight bytes of Tables::slots");
+
+// The entries, from every token's experts, in shared memory (slots: zeros).
 __device__ __forceinline__ void make_entries(const FewArgs& f, Tables& s) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, R = f.T * f.k, i = threadIdx.x;
   const int e = i < R ? f.idx[i] : -1;
-  if (i < kFewSlots) s.idx[i] = e;
   if (i < R) s.wt[i] = f.wt[i];
   if (i < f.T) s.xinv[i] = f.xinv[i];
+  // Slot i's rank among its expert's: those before it in its own 32 and in the earlier ones.  The first slot of an expert
+  // lays down its entries, in the order of those slots.
+  const uint32_t same = __match_any_sync(0xffffffffu, e);
+  int rank = __popc(same & ((1u << lane) - 1)), total = 0;
+  if (e >= 0 && rank == 0) s.slots[e][warp] = (uint8_t)__popc(same);
   __syncthreads();
-  // Slot i's rank among its expert's; the first slot of an expert lays down its entries, in the order of those slots.
-  int rank = 0, total = 0;
-  if (32 * warp < R) {
-    for (int j = 0; j < R; j += 4) {  // (past R: no expert)
-      const int4 o = *(const int4*)(s.idx + j);
-      const int v[4] = {o.x, o.y, o.z, o.w};
+  if (e >= 0) {
+    const uint2 n = *(const uint2*)s.slots[e];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const bool same = v[n] == e;
-        rank += same && j + n < i;
-        total += same;
-      }
+    for (int w = 0; w < kFewSlots / 32; ++w) {
+      const int c = (w < 4 ? n.x >> (8 * w) : n.y >> (8 * w - 32)) & 0xFF;
+      rank += w < warp ? c : 0;
+      total += c;
     }
   }
   const int own = i < R && rank == 0 ? (total + kEntryRows - 1) / kEntryRows : 0;
@@ -490,6 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
     fence_barrier_init();
   }
   if (warp >= kCopyWarp && lane < 2) prefetch_tmap(&a.map[lane]);
+  for (int i = threadIdx.x; i < kMaxE; i += kThreads) *(uint2*)s.slots[i] = make_uint2(0, 0);
+  __syncthreads();
   pdl_wait();  // the choice of experts and the scaled rows
   pdl_trigger();
   int ticket = 0;  // the team's next one
