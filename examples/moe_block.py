@@ -83,6 +83,8 @@ def main(argv=None):
                 raise RuntimeError("device error flag set")
     if M.moe_get_adapter_error():
         raise RuntimeError("adapter error flag set")
+    if M.moe_get_fp8_linear_error():
+        raise RuntimeError("product error flag set")
     if not torch.isfinite(x).all():
         raise RuntimeError("the stream is not finite")
     return x

@@ -484,6 +484,9 @@ moe_status_t moe_fp8_linear(const void* x, int64_t ldx, int x_dtype, const float
                             const float* w_scale_inv, int act, const void* base, int64_t ldb, void* out, int64_t ldo,
                             int out_dtype, int T, int K, int N, void* workspace, size_t ws_bytes, moe_stream_t stream);
 
+/* As moe_get_adapter_error, of moe_fp8_linear: synchronise `stream`, then read and clear the current device's error word. */
+moe_status_t moe_get_fp8_linear_error(moe_stream_t stream, int32_t* code);
+
 /* ---- measurement hooks ------------------------------------------------------------------ */
 
 /* Total number of CUDA kernels this library has enqueued in the calling process (all threads,

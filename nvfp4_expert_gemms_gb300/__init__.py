@@ -35,13 +35,13 @@ EXPORTS = ("moe_packed_size", "moe_pack_experts", "moe_workspace_size", "moe_lay
            "moe_debug_quant_act_static", "moe_debug_quant_act_fp8", "moe_debug_wait_timeout", "moe_block_enter",
            "moe_block_leave", "moe_route_scored", "moe_layer_forward_scored", "moe_adapters_add", "moe_get_adapter_error",
            "moe_layer_few_workspace_size", "moe_layer_few", "moe_fp8_quantize", "moe_fp8_linear_workspace_size",
-           "moe_fp8_linear")
+           "moe_fp8_linear", "moe_get_fp8_linear_error")
 
 # The operators around the experts live in block.py (which needs torch at import) and are names of
 # this package too.
 _BLOCK = ("Norm", "Router", "MoEBlock", "moe_block_enter", "moe_block_leave", "moe_route_scored",
           "moe_layer_forward_scored", "moe_adapters_add", "moe_get_adapter_error", "moe_layer_few",
-          "moe_layer_few_workspace_size", "Fp8Weight", "moe_fp8_quantize", "moe_fp8_linear")
+          "moe_layer_few_workspace_size", "Fp8Weight", "moe_fp8_quantize", "moe_fp8_linear", "moe_get_fp8_linear_error")
 
 
 def __getattr__(name):

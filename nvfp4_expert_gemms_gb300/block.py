@@ -63,6 +63,7 @@ def _f():
         L.moe_route_scored.argtypes = [P, P, Q, I, P, I, I, I, P, P, P]
         L.moe_layer_forward_scored.argtypes = [P, P, P, Q, I, P, I, C.POINTER(PackedDesc), P, I, P, P, C.c_size_t, P]
         L.moe_get_adapter_error.argtypes = [P, C.POINTER(C.c_int32)]
+        L.moe_get_fp8_linear_error.argtypes = [P, C.POINTER(C.c_int32)]
         L.moe_adapters_add.argtypes = [P, Q, P, Q, P, P, P, P, P, P, P, Q] + [I] * 6 + [P]
         L.moe_layer_few_workspace_size.argtypes = [C.POINTER(PackedDesc), I, I, C.POINTER(C.c_size_t)]
         L.moe_layer_few.argtypes = [P, Q, P, Q, I, P, P, I, P, P, I, P, Q, P, P, P, C.c_size_t, P]
@@ -264,6 +265,14 @@ def moe_get_adapter_error(stream=None) -> int:
     code = C.c_int32()
     _check(_f().moe_get_adapter_error(torch.cuda.current_stream().cuda_stream if stream is None else _handle(stream),
                                       C.byref(code)), "moe_get_adapter_error")
+    return code.value
+
+
+def moe_get_fp8_linear_error(stream=None) -> int:
+    """Synchronise the stream, then read and clear the current device's error word of moe_fp8_linear (0: none)."""
+    code = C.c_int32()
+    _check(_f().moe_get_fp8_linear_error(torch.cuda.current_stream().cuda_stream if stream is None else _handle(stream),
+                                         C.byref(code)), "moe_get_fp8_linear_error")
     return code.value
 
 

@@ -16,6 +16,8 @@ using namespace tc;
 
 namespace {
 
+__device__ int g_fp8_error;  // kDevOk or the first failure: the call has no workspace of its own to keep one in
+
 constexpr int kM = 128, kTileA = kM * 128;  // rows of x per tile; bytes of its group of 128 columns
 
 template <int BN>
@@ -355,6 +357,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
               volatile int alone = 0;
               const bool came = mbar_wait(&bfull[warp], box_phase, &alone);
               box_phase ^= 1;
+              if (!came) s_abort = 1;
               ok = __all_sync(0xffffffffu, ok && came);
             }
             if (ok) {
@@ -410,11 +413,12 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
   if (warp < kProd && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // outputs have left
   {
     volatile int no_abort = 0;
-    mbar_wait(&drain, 0, &no_abort);  // bounded; every MMA of this block has completed
+    if (!mbar_wait(&drain, 0, &no_abort)) s_abort = 1;  // bounded; every MMA of this block has completed
   }
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
+  if (threadIdx.x == 0 && s_abort) set_dev_error(&g_fp8_error, kDevTimeout);
   if (SHARE) {  // no block leaves while another one may still write or arrive in it
     cluster_arrive();
     cluster_wait();
@@ -436,7 +440,8 @@ cudaError_t launch(const Fp8LinearArgs& l, cudaStream_t s) {
       !tc_make_map(&a.w, u8, l.w, l.K, l.N, l.K, 128, BN / 2, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   a.boxed = false;
-  if (SPLIT == 1 && l.out_dtype != MOE_DT_F32 && (uintptr_t)l.out % 16 == 0 && (uintptr_t)l.base % 16 == 0 && l.ldo % 8 == 0 &&
+  // (a TMA store clips a row of odd length at 16 bytes, not at the element: such rows are stored by the lanes)
+  if (SPLIT == 1 && l.out_dtype != MOE_DT_F32 && l.out_n % 8 == 0 && (uintptr_t)l.out % 16 == 0 && (uintptr_t)l.base % 16 == 0 && l.ldo % 8 == 0 &&
       (!l.base || l.ldb % 8 == 0)) {
     const auto type = CU_TENSOR_MAP_DATA_TYPE_UINT16;
     const auto sw = CU_TENSOR_MAP_SWIZZLE_64B;
@@ -501,3 +506,18 @@ cudaError_t launch_fp8_tiles(const Fp8LinearArgs& l, cudaStream_t s) {
 }
 
 }  // namespace moe
+
+extern "C" moe_status_t moe_get_fp8_linear_error(moe_stream_t stream, int32_t* code) {
+  using namespace moe;
+  if (!code) return MOE_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  int32_t v = 0;
+  const int zero = 0;
+  if (cudaMemcpyFromSymbolAsync(&v, g_fp8_error, sizeof(v), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess ||
+      cudaMemcpyToSymbolAsync(g_fp8_error, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  *code = v;
+  return MOE_OK;
+}

@@ -73,6 +73,7 @@ def test_linear_refuses():
                 dict(xd=4, xs=P, lx=72), dict(xd=4, xs=P + 1)):
         assert call(**bad) == 1, bad
     assert call(n=16) == 3
+    assert f.moe_get_fp8_linear_error(None, None) == 1
 
 
 def test_binding_refuses_host_tensors():

@@ -112,6 +112,7 @@ class Layer:
         assert M.moe_get_device_error(self.ws) == 0
 
 
+MANY = [(32, 256, 8, 384, 128), (31, 100, 7, 640, 896), (8, 6, 6, 9216, 256), (2, 4, 2, 256, 5120)]
 SIZES = [(1, 8, 2, 256, 128), (3, 16, 4, 384, 256), (32, 8, 8, 128, 128), (5, 60, 4, 1408, 640), (2, 256, 8, 512, 384), (1, 1, 1, 128, 128),
          (9, 12, 3, 2304, 1152), (4, 5, 5, 4352, 128), (17, 9, 1, 128, 2176)]
 
@@ -121,6 +122,16 @@ SIZES = [(1, 8, 2, 256, 128), (3, 16, 4, 384, 256), (32, 8, 8, 128, 128), (5, 60
 def test_few(fmt, T, E, k, H, I):
     layer = Layer(fmt, T, E, k, H, I, seed=T + H)
     layer.check(layer.run())
+
+
+@pytest.mark.parametrize("fmt", sorted(M.FORMATS))
+@pytest.mark.parametrize("T,E,k,H,I", MANY)
+def test_few_of_many_slots_and_long_rows(fmt, T, E, k, H, I):
+    # every slot there can be; matrices of more stages than the warps keep activations of
+    layer = Layer(fmt, T, E, k, H, I, seed=T + I, router=M.Router("sigmoid"), bias=True)
+    want = layer.run()
+    layer.check(want)
+    assert torch.equal(layer.run(), want)
 
 
 @pytest.mark.parametrize("fmt,T", [("fp8", 1), ("fp8", 16), ("int4", 4), ("nvfp4_w4a16", 1), ("nvfp4_w4a16", 32), ("bf16", 2)])
@@ -458,6 +469,76 @@ def test_linear_at_full_size(T, K, N, act):
     out = M.moe_fp8_linear(x, w, act=act)
     check_linear(out, x, w, act)
     assert torch.equal(M.moe_fp8_linear(x, w, act=act), out)
+
+
+@pytest.mark.parametrize("T,K,N,act", [(2000, 400, 2742, "silu_mul"), (2305, 272, 2808, "none"), (100, 512, 39000, "none"), (70, 144, 39002, "silu_mul")])
+@pytest.mark.parametrize("out_type", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("pad", [0, 1])
+def test_linear_in_large_tiles(T, K, N, act, out_type, pad):
+    # enough outputs for the tiles of 256: an odd number of them along either axis, ups that cross a block of 128 rows (1371 and
+    # 19501 gates), the last tiles ragged; rows of out on multiples of 16 bytes and not; base elsewhere and in place
+    g = gen(T + N)
+    n = N // 2 if act == "silu_mul" else N
+    x = torch.randn((T, K), generator=g, device="cuda").bfloat16()
+    w = make_weight(N, K, g)
+    wide = n + -n % 8 + 8 + pad
+    out = torch.full((T + 1, wide), 7.0, dtype=DT[out_type], device="cuda")
+    M.moe_fp8_linear(x, w, act=act, out=out[:T, :n])
+    assert (out[:T, n:] == 7.0).all() and (out[T:] == 7.0).all()
+    check_linear(out[:T, :n], x, w, act)
+    base = torch.randn((T + 1, wide), generator=g, device="cuda").to(DT[out_type])
+    keep = base.clone()
+    M.moe_fp8_linear(x, w, act=act, base=base[:T, :n], out=out[:T, :n])
+    check_linear(out[:T, :n], x, w, act, keep[:T, :n])
+    M.moe_fp8_linear(x, w, act=act, base=base[:T, :n], out=base[:T, :n])
+    assert torch.equal(base[:T, :n], out[:T, :n]) and torch.equal(base[:T, n:], keep[:T, n:]) and torch.equal(base[T:], keep[T:])
+    assert M.moe_get_fp8_linear_error() == 0
+
+
+def test_linear_of_the_smallest_largest_and_empty_groups():
+    # weights and activations of zero, of the largest code, of scales that are zero, tiny and large
+    for T in (5, 150):
+        x = torch.full((T, 256), 1.0, device="cuda")
+        x[1], x[2], x[3] = 0.0, 3e38, 1e-30
+        codes = torch.full((130, 256), 448.0, device="cuda").to(torch.float8_e4m3fn)
+        codes[7] = 0.0
+        scale = torch.tensor([[1.0, 0.0], [1e-36, 1e-3]], device="cuda")
+        w = M.Fp8Weight(codes, scale)
+        out = M.moe_fp8_linear(x, w, dtype=torch.float32)
+        rows = [t for t in range(T) if t != 2]
+        q, qs = plain_quantize(x)
+        ref, tol = linear_reference(q.cuda(), qs.cuda(), w, "none", None, torch.float32)
+        # a product of two scales below 2^-126 may be lost: 2^-126 for each of 256 products of codes up to 448^2
+        assert ((out.double() - ref).abs() <= tol + 2.0 ** -126 * 256 * 448.0 ** 2)[rows].all()
+        assert (out[:, 7] == 0).all() and (out[1] == 0).all() and out[2, 0].isinf()  # 3e38 448 128 is past fp32
+
+
+def test_operators_beside_each_other():
+    # the layer for few tokens, products and the layer for many, each on a stream of its own, again and again
+    a = Layer("int4", 32, 256, 8, 512, 256, seed=43)
+    b = Layer("nvfp4_w4a16", 5, 16, 4, 640, 384, seed=47)
+    g = gen(53)
+    x = torch.randn((1500, 512), generator=g, device="cuda").bfloat16()
+    w, w2 = make_weight(3000, 512, g), make_weight(200, 512, g)
+    y = torch.empty_like(x[:64])
+    logits = torch.randn((64, 256), generator=g, device="cuda")
+    ws = torch.empty(M.moe_workspace_size(a.desc, 64, 8), dtype=torch.uint8, device="cuda")
+    calls = [lambda s: a.run(stream=s), lambda s: b.run(stream=s), lambda s: M.moe_fp8_linear(x, w, stream=s),
+             lambda s: M.moe_fp8_linear(x[:100], w2, act="silu_mul", stream=s),
+             lambda s: (M.moe_layer_forward_scored(x[:64], logits, M.Router(), a.desc, a.packed, 8, y, ws, stream=s), y)[1].clone()]
+    want = [c(None) for c in calls]
+    torch.cuda.synchronize()
+    a.check(want[0])
+    b.check(want[1])
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = []
+    for _ in range(10):
+        for c, s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                got.append(c(s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i % len(calls)]) for i, o in enumerate(got))
+    assert M.moe_get_device_error(a.ws) == M.moe_get_device_error(b.ws) == M.moe_get_device_error(ws) == M.moe_get_fp8_linear_error() == 0
 
 
 @pytest.mark.parametrize("T", [4, 64, 300])
