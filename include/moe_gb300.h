@@ -431,15 +431,15 @@ moe_status_t moe_get_adapter_error(moe_stream_t stream, int32_t* code);
  *   logits[t, e] = sum over h of x[t, h] w_router[e, h], the exact sum rounded once to fp32
  *   experts and weights of each token: moe_router_t's rule on those logits (bias f32 [E] or NULL)
  *   out[t] = sum_j w_tj Wd_e (silu(Wg_e x_t) * (Wu_e x_t)),   e = the j-th expert of t
- * with the weights as stored (any format) and x, h and the sums in fp32: nothing is rounded to fewer bits
- * but out, once; the formats that quantize activations at run time (W4A4, W8A8) do not here, where the weights' bytes
+ * with the weights as stored (any format), x as it is and the sums in fp32; h enters the down product with 22 bits of the
+ * largest of its 128 neighbours (with bf16 weights: 16 bits of each element), and out is rounded once.  The formats that quantize activations at run time (W4A4, W8A8) do not here, where the weights' bytes
  * set the pace.  Results do not depend on the order in which blocks run.
  *   x (dev) bf16 [T, H] (pitch ldx); w_router (dev) w_dtype [E, H] (pitch ldw); packed (dev) as moe_pack_experts
  *   writes it (of a buffer that holds images, only the canonical tensors are read); out (dev) bf16 [T, H] (pitch ldo), may be
  *   x (same pitch), no other overlap; topk_idx (dev) i32 [T, top_k] and topk_w (dev) f32 [T, top_k], or NULL;
  *   workspace (dev) >= moe_layer_few_workspace_size bytes, 256-byte aligned, any contents, one call at a time.
  * Pitches are multiples of 8; x, w_router and out 16-byte, packed 256-byte aligned.  A row's NaN and infinities stay in
- * the tokens that read them.  Bounded waits report through moe_get_device_error(workspace), as the layer's do.
+ * the tokens that read them; an infinite weight (bf16, or a scale) may give NaN where fp32 arithmetic gives infinity.  Bounded waits report through moe_get_device_error(workspace), as the layer's do.
  * Errors: those of moe_route_scored for the router, E and top_k; MOE_ERR_INVALID_ARG for T outside
  * 0 .. MOE_FEW_MAX_TOKENS, a bad desc, pitch or pointer; MOE_ERR_WORKSPACE; MOE_ERR_UNSUPPORTED off sm_103;
  * MOE_ERR_CUDA if a launch fails.  T = 0 enqueues nothing. */
@@ -458,7 +458,7 @@ moe_status_t moe_layer_few(const void* x, int64_t ldx, const void* w_router, int
  *   x (dev) x_dtype [T, K] (pitch ldx, any alignment of its element); codes (dev) u8 [T, K] (pitch ldq); scale_inv (dev)
  *   f32 [T, ceil(K / 128)].  Wide accesses where K is a multiple of 128, x's rows start on multiples of 16 bytes and codes'
  *   on multiples of 8.
- * Errors: MOE_ERR_INVALID_ARG for T < 0, K < 1, a pitch below K, an unknown type, a null or misaligned pointer;
+ * Errors: MOE_ERR_INVALID_ARG for T < 0, K < 1, K over 2^31 - 513, a pitch below K, an unknown type, a null or misaligned pointer;
  * MOE_ERR_UNSUPPORTED off sm_103; MOE_ERR_CUDA if the launch fails.  T = 0 enqueues nothing. */
 moe_status_t moe_fp8_quantize(const void* x, int64_t ldx, int x_dtype, uint8_t* codes, int64_t ldq, float* scale_inv,
                               int T, int K, moe_stream_t stream);
@@ -473,7 +473,7 @@ moe_status_t moe_fp8_quantize(const void* x, int64_t ldx, int x_dtype, uint8_t* 
  *   MOE_DT_E4M3 codes (16-byte aligned, ldx a multiple of 16) with x_scale_inv (dev) f32 [T, ceil(K / 128)].
  *   w (dev) E4M3 [N, K], contiguous, 16-byte aligned; w_scale_inv (dev) f32 [ceil(N / 128), ceil(K / 128)].
  *   base (dev) out_dtype [T, n] or NULL; out (dev) out_dtype [T, n], n = N or N/2; out may be base (same pitch), no
- *   other overlap.  K is a multiple of 16; T, N, pitches and out's alignment are free.
+ *   other overlap.  K is a multiple of 16; T, N (these three up to 2^31 - 513), pitches and out's alignment are free.
  *   workspace (dev): moe_fp8_linear_workspace_size bytes (0 for codes), 256-byte aligned, any contents.
  * Errors: MOE_ERR_INVALID_ARG for sizes, types, pitches or pointers outside these (N odd with MOE_ACT_SILU_MUL);
  * MOE_ERR_WORKSPACE; MOE_ERR_UNSUPPORTED off sm_103; MOE_ERR_CUDA if a launch fails.  T = 0 enqueues nothing. */

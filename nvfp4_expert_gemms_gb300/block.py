@@ -294,6 +294,8 @@ class MoEBlock:
         if not 0 <= few_tokens <= FEW_MAX_TOKENS:
             _refuse("MoEBlock", f"few_tokens is not in 0 .. {FEW_MAX_TOKENS}")
         self.shared, self.few_tokens = shared, few_tokens
+        if few_tokens:  # now, and not while a graph is captured
+            layer.ensure_few_workspace(few_tokens, top_k)
         self.layer, self.w_router, self.router, self.top_k = layer, w_router, router, top_k
         self.pre, self.post, self.router_bias, self.alpha, self.beta = pre, post, router_bias, alpha, beta
 

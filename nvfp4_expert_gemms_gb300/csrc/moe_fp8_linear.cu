@@ -9,8 +9,9 @@ size_t codes_bytes(int T, int K) { return ((size_t)T * K + 255) / 256 * 256; }
 size_t workspace_bytes(int x_dtype, int T, int K) {
   return x_dtype == MOE_DT_E4M3 ? 0 : codes_bytes(T, K) + 4 * (size_t)T * ((K + 127) / 128);
 }
+constexpr int kMost = INT32_MAX - 512;  // what rounds up to tiles stays an int
 bool sizes_ok(int x_dtype, int T, int K, int N, int act) {
-  return (dtype_ok(x_dtype) || x_dtype == MOE_DT_E4M3) && T >= 0 && K >= 16 && K % 16 == 0 && N >= 1 &&
+  return (dtype_ok(x_dtype) || x_dtype == MOE_DT_E4M3) && T >= 0 && T <= kMost && K >= 16 && K <= kMost && K % 16 == 0 && N >= 1 && N <= kMost &&
          (act == MOE_ACT_NONE || (act == MOE_ACT_SILU_MUL && N % 2 == 0));
 }
 

@@ -149,7 +149,7 @@ using namespace moe;
 
 extern "C" moe_status_t moe_fp8_quantize(const void* x, int64_t ldx, int x_dtype, uint8_t* codes, int64_t ldq,
                                          float* scale_inv, int T, int K, moe_stream_t stream) {
-  if (T < 0 || K < 1 || !dtype_ok(x_dtype) || ldx < K || ldq < K) return MOE_ERR_INVALID_ARG;
+  if (T < 0 || K < 1 || K > INT32_MAX - 512 || !dtype_ok(x_dtype) || ldx < K || ldq < K) return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!x || !codes || !scale_inv)) return MOE_ERR_INVALID_ARG;
   if ((uintptr_t)x % dtype_size(x_dtype) || (uintptr_t)scale_inv % 4) return MOE_ERR_INVALID_ARG;
   const moe_status_t dv = device_ok();

@@ -48,7 +48,7 @@ def test_few_refuses():
 def test_quantize_refuses():
     f = block._f()
     call = lambda **k: f.moe_fp8_quantize(*{**dict(x=P, lx=64, dt=1, q=P, lq=64, s=P, T=4, K=64, st=None), **k}.values())  # noqa: E731
-    for bad in (dict(T=-1), dict(K=0), dict(dt=0), dict(dt=4), dict(lx=63), dict(lq=63), dict(x=None), dict(q=None), dict(s=None), dict(x=P + 1),
+    for bad in (dict(T=-1), dict(K=0), dict(K=2 ** 31 - 512, lx=1 << 31, lq=1 << 31), dict(dt=0), dict(dt=4), dict(lx=63), dict(lq=63), dict(x=None), dict(q=None), dict(s=None), dict(x=P + 1),
                 dict(s=P + 2)):
         assert call(**bad) == 1, bad
 
@@ -59,6 +59,7 @@ def test_linear_refuses():
     size = lambda *a: f.moe_fp8_linear_workspace_size(*a, C.byref(n))  # noqa: E731
     assert size(1, 4, 64, 32, 0) == size(4, 4, 64, 32, 1) == 0
     for bad in ((0, 4, 64, 32, 0), (5, 4, 64, 32, 0), (1, -1, 64, 32, 0), (1, 4, 0, 32, 0), (1, 4, 24, 32, 0), (1, 4, 64, 0, 0), (1, 4, 64, 33, 1),
+                (1, 2 ** 31 - 512, 64, 32, 0), (1, 4, 2 ** 31 - 16, 32, 0), (1, 4, 64, 2 ** 31 - 512, 0),
                 (1, 4, 64, 32, 2)):
         assert size(*bad) == 1, bad
     assert f.moe_fp8_linear_workspace_size(1, 4, 64, 32, 0, None) == 1

@@ -132,6 +132,9 @@ def test_few_of_many_slots_and_long_rows(fmt, T, E, k, H, I):
     want = layer.run()
     layer.check(want)
     assert torch.equal(layer.run(), want)
+    x = layer.x.clone()
+    layer.run(x, out=x)  # in place
+    assert torch.equal(x, want)
 
 
 @pytest.mark.parametrize("fmt,T", [("fp8", 1), ("fp8", 16), ("int4", 4), ("nvfp4_w4a16", 1), ("nvfp4_w4a16", 32), ("bf16", 2)])
