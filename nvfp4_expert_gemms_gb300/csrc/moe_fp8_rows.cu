@@ -12,6 +12,7 @@ namespace {
 
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kPass = 8;  // rows of x at a time
+static_assert(kFp8Rows == 2 * kPass, "one or two passes");
 
 __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t c) {  // the two codes in c's low half
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xFFFFu), __NV_E4M3);
@@ -56,9 +57,9 @@ __device__ __forceinline__ float quantize_group(const T* p, int left, int t, uin
   return __fdiv_rn(1.f, s);
 }
 
-template <bool PAIR>
-__global__ void __launch_bounds__(kThreads, 2) fp8_rows_kernel(const Fp8LinearArgs a, const bool wide) {
-  __shared__ float4 part[kWarps][32];
+template <bool PAIR, int PASSES>
+__global__ void __launch_bounds__(kThreads, PASSES == 1 ? 2 : 1) fp8_rows_kernel(const Fp8LinearArgs a, const bool wide) {
+  __shared__ float4 part[kWarps][PASSES][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   pdl_wait();
   pdl_trigger();
@@ -67,19 +68,20 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_rows_kernel(const Fp8LinearAr
   const int r0 = min(n0 + g, a.out_n - 1), r1 = PAIR ? a.out_n + r0 : min(n0 + 8 + g, a.N - 1);
   const uint8_t *w0 = a.w + (int64_t)r0 * a.K + 16 * t, *w1 = a.w + (int64_t)r1 * a.K + 16 * t;
   const float *s0 = a.ws + (int64_t)(r0 / 128) * a.groups, *s1 = a.ws + (int64_t)(r1 / 128) * a.groups;
-  for (int t0 = 0; t0 < a.T; t0 += kPass) {
-    const int row = min(t0 + g, a.T - 1);  // the lane's row of x (past the end: the last one, not stored)
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int grp = warp; grp < a.groups; grp += kWarps) {
-      const int k = 128 * grp, left = a.K - k;
-      uint4 u[2], v[2];
+  float acc[PASSES][4] = {};
+  for (int grp = warp; grp < a.groups; grp += kWarps) {
+    const int k = 128 * grp, left = a.K - k;
+    uint4 u[2], v[2];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const bool in = left > 64 * q + 16 * t;
-        u[q] = in ? __ldg((const uint4*)(w0 + k + 64 * q)) : make_uint4(0, 0, 0, 0);
-        v[q] = in ? __ldg((const uint4*)(w1 + k + 64 * q)) : make_uint4(0, 0, 0, 0);
-      }
-      const float f0 = __ldg(s0 + grp), f1 = __ldg(s1 + grp);
+    for (int q = 0; q < 2; ++q) {
+      const bool in = left > 64 * q + 16 * t;
+      u[q] = in ? __ldg((const uint4*)(w0 + k + 64 * q)) : make_uint4(0, 0, 0, 0);
+      v[q] = in ? __ldg((const uint4*)(w1 + k + 64 * q)) : make_uint4(0, 0, 0, 0);
+    }
+    const float f0 = __ldg(s0 + grp), f1 = __ldg(s1 + grp);
+#pragma unroll
+    for (int pass = 0; pass < PASSES; ++pass) {
+      const int row = min(kPass * pass + g, a.T - 1);  // the lane's row of x (past the end: the last one, not stored)
       uint32_t b[16];
       float sx;
       if (a.x_dtype == MOE_DT_E4M3) {
@@ -112,33 +114,33 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_rows_kernel(const Fp8LinearAr
       }
       // columns 2 t and 2 t + 1 of the MMA are rows of x that lanes 4 (2 t) and 4 (2 t + 1) quantized
       const float x0 = __shfl_sync(0xffffffffu, sx, 8 * t), x1 = __shfl_sync(0xffffffffu, sx, 8 * t + 4);
-      acc[0] = fmaf(p[0], f0 * x0, acc[0]), acc[1] = fmaf(p[1], f0 * x1, acc[1]);
-      acc[2] = fmaf(p[2], f1 * x0, acc[2]), acc[3] = fmaf(p[3], f1 * x1, acc[3]);
+      acc[pass][0] = fmaf(p[0], f0 * x0, acc[pass][0]), acc[pass][1] = fmaf(p[1], f0 * x1, acc[pass][1]);
+      acc[pass][2] = fmaf(p[2], f1 * x0, acc[pass][2]), acc[pass][3] = fmaf(p[3], f1 * x1, acc[pass][3]);
     }
-    part[warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    __syncthreads();
-    if (threadIdx.x < 128) {  // thread i: value i % 4 of lane i / 4
-      const int used = min(kWarps, a.groups), l = threadIdx.x >> 2, i = threadIdx.x & 3;
-      float y = 0.f;
-      for (int w = 0; w < used; ++w) y += ((const float*)&part[w][l])[i];
-      const int token = t0 + 2 * (l & 3) + (i & 1);
-      if (PAIR) {  // values 0 and 1 are gates, 2 and 3 the same features' ups
-        const float up = __shfl_down_sync(0xffffffffu, y, 2);
-        const int n = n0 + (l >> 2);
-        if (i < 2 && token < a.T && n < a.out_n) {
-          y = silu_mul(y, up);
-          if (a.base) y += load_any(a.base, a.out_dtype, token * a.ldb + n);
-          store_any(a.out, a.out_dtype, token * a.ldo + n, y);
-        }
-      } else {
-        const int n = n0 + (l >> 2) + 8 * (i >> 1);
-        if (token < a.T && n < a.out_n) {
-          if (a.base) y += load_any(a.base, a.out_dtype, token * a.ldb + n);
-          store_any(a.out, a.out_dtype, token * a.ldo + n, y);
-        }
-      }
+  }
+#pragma unroll
+  for (int pass = 0; pass < PASSES; ++pass) part[warp][pass][lane] = make_float4(acc[pass][0], acc[pass][1], acc[pass][2], acc[pass][3]);
+  __syncthreads();
+  if (threadIdx.x >= 128 * PASSES) return;
+  // thread i: value i % 4 of lane i / 4, 128 for each pass
+  const int used = min(kWarps, a.groups), pass = threadIdx.x / 128, l = threadIdx.x >> 2 & 31, i = threadIdx.x & 3;
+  float y = 0.f;
+  for (int w = 0; w < used; ++w) y += ((const float*)&part[w][pass][l])[i];
+  const int token = kPass * pass + 2 * (l & 3) + (i & 1);
+  if (PAIR) {  // values 0 and 1 are gates, 2 and 3 the same features' ups
+    const float up = __shfl_down_sync(0xffffffffu, y, 2);
+    const int n = n0 + (l >> 2);
+    if (i < 2 && token < a.T && n < a.out_n) {
+      y = silu_mul(y, up);
+      if (a.base) y += load_any(a.base, a.out_dtype, token * a.ldb + n);
+      store_any(a.out, a.out_dtype, token * a.ldo + n, y);
     }
-    __syncthreads();
+  } else {
+    const int n = n0 + (l >> 2) + 8 * (i >> 1);
+    if (token < a.T && n < a.out_n) {
+      if (a.base) y += load_any(a.base, a.out_dtype, token * a.ldb + n);
+      store_any(a.out, a.out_dtype, token * a.ldo + n, y);
+    }
   }
 }
 
@@ -149,8 +151,11 @@ cudaError_t launch_fp8_rows(const Fp8LinearArgs& a, cudaStream_t s) {
   const bool pair = a.out_n != a.N, wide = (uintptr_t)a.x % 16 == 0 && a.ldx * es % 16 == 0;
   note_launches(1);
   const dim3 grid((a.out_n + (pair ? 7 : 15)) / (pair ? 8 : 16));
-  return pair ? launch_pdl(fp8_rows_kernel<true>, grid, dim3(kThreads), 0, s, a, wide)
-              : launch_pdl(fp8_rows_kernel<false>, grid, dim3(kThreads), 0, s, a, wide);
+  if (a.T <= kPass)
+    return pair ? launch_pdl(fp8_rows_kernel<true, 1>, grid, dim3(kThreads), 0, s, a, wide)
+                : launch_pdl(fp8_rows_kernel<false, 1>, grid, dim3(kThreads), 0, s, a, wide);
+  return pair ? launch_pdl(fp8_rows_kernel<true, 2>, grid, dim3(kThreads), 0, s, a, wide)
+              : launch_pdl(fp8_rows_kernel<false, 2>, grid, dim3(kThreads), 0, s, a, wide);
 }
 
 }  // namespace moe

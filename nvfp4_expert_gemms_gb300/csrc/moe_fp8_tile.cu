@@ -25,7 +25,7 @@ struct Shape {
   static constexpr int kPromote = BN / 16;  // warps: a row per thread, 64 columns per warp
   static constexpr int kThreads = 32 * (kPromote + 2);
   static constexpr int kStage = kTileA + BN * 128;
-  // A stage comes back some 3100 cycles after it was freed (clusters: the slowest of three blocks frees it), a group's MMAs take 640: the
+  // A stage comes back some 3100 cycles after it was freed (), a group's MMAs take 640: the
   // more stages the better, and the outputs make do with 2 KB per warp (16384 x 2048 x 4096: three stages 169 us).
   static constexpr int kStages = BN == 256 ? 4 : 3;
   static constexpr int kBuffers = BN == 256 ? 2 : 4;
@@ -48,30 +48,8 @@ __device__ __forceinline__ void fma2(float& a, float& b, uint32_t p, uint32_t q,
       : "r"(p), "r"(q), "f"(f), "f"(g));
 }
 
-// 32 lanes x 8 columns of 32-bit words.
-__device__ __forceinline__ void tmem_ld_32x8(uint32_t taddr, uint32_t* v) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-               : "r"(taddr)
-               : "memory");
-}
-
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// A 2-D tiled load into the same place of every block of the cluster that `mask` names, completing on bar in each.
-__device__ __forceinline__ void tma_load_2d_multicast(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1, uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%3, %4}], [%2], "
-      "%5;" ::"r"(smem_u32(dst)),
-      "l"(m), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "h"(mask)
-      : "memory");
-}
-// mma_commit, arriving on *bar of every block that `mask` names.
-__device__ __forceinline__ void mma_commit_multicast(uint64_t* bar, uint16_t mask) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
-               "h"(mask)
-               : "memory");
-}
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -157,14 +135,10 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* s
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-// SHARE: clusters of 2 x 2 blocks walk squares of 2 x 2 tiles.  Each block loads half of its rows of x for itself and its neighbour
-// along the outputs, and half of its weight rows for itself and its neighbour along the rows (TMA multicast): 24 KB of a
-// group's 48 come from L2.  A single block's tile takes 48 KB per 8.4 MFLOP, at which L2 holds every SM to some 50 GB/s
-// and the device to 1.33 PFLOP/s (16384 x 2048 x 4096: 206 us).
-// Else a tile per cluster of SPLIT blocks, which share its groups of columns and join their sums through each other's shared memory;
+// A tile per cluster of SPLIT blocks, which share its groups of columns and join their sums through each other's shared memory;
 // SPLIT = 1: blocks walk the tiles.  PAIR: the tile's weight rows are BN / 2 gates and the same features' ups; a thread's sums
-// then alternate gate, up.
-template <int BN, bool PAIR, int SPLIT, bool SHARE>
+// are then 32 of each (alternating, so that a factor had to be chosen for each, 1024 x 2048 x 6000 took twice as long).
+template <int BN, bool PAIR, int SPLIT>
 __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_tile_kernel(const __grid_constant__ Args a) {
   using S = Shape<BN>;
   constexpr int kBufs = S::kBuffers, kStages = S::kStages;
@@ -179,7 +153,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], SHARE ? 3 : 1);
+      mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(&pfull[i], 1);
@@ -202,17 +176,16 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = s_tmem;
-  const int rank = SPLIT > 1 || SHARE ? (int)cluster_rank() : 0;
-  if (SHARE) {  // every block's barriers are there before another one arrives on them
-    cluster_arrive();
-    cluster_wait();
-  }
-  const int cm = SHARE ? rank >> 1 : 0, cn = SHARE ? rank & 1 : 0;  // place in the square
-  constexpr int kBlocks = SHARE ? 4 : SPLIT;
-  const int across = SHARE ? (a.tiles_m + 1) / 2 : a.tiles_m;  // tiles or squares along the rows
-  const int tiles = across * (SHARE ? (a.tiles_n + 1) / 2 : a.tiles_n), first = blockIdx.x / kBlocks, stride = gridDim.x / kBlocks;
-  auto tile_row = [&](int i) { return kM * (SHARE ? 2 * (i % across) + cm : i % across); };
-  auto tile_col = [&](int i) { return (PAIR ? BN / 2 : BN) * (SHARE ? 2 * (i / across) + cn : i / across); };
+  const int rank = SPLIT > 1 ? (int)cluster_rank() : 0;
+  const int tiles = a.tiles_m * a.tiles_n, first = blockIdx.x / SPLIT, stride = gridDim.x / SPLIT;
+  // kHigh tiles along the rows, then the next along the outputs: those that are worked on at a time, 152 or 304, share x and w in L2
+  // (all rows first: 16384 x 4096 x 4096 took 406 us for 341)
+  constexpr int kHigh = BN == 256 ? 12 : 24;
+  auto place = [&](int i, int& row, int& col) {
+    const int band = i / (kHigh * a.tiles_n), j = i - band * kHigh * a.tiles_n, h = min(kHigh, a.tiles_m - kHigh * band);
+    row = kM * (kHigh * band + j % h);
+    col = (PAIR ? BN / 2 : BN) * (j / h);
+  };
   // this block's groups of columns
   const int g0 = SPLIT > 1 ? l.groups * rank / SPLIT : 0, g1 = SPLIT > 1 ? l.groups * (rank + 1) / SPLIT : l.groups;
   pdl_wait();
@@ -224,7 +197,9 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
       int it = 0;
       bool ok = true;
       for (int i = first; ok && i < tiles; i += stride) {
-        const int row = tile_row(i), n0 = tile_col(i), n1 = PAIR ? l.out_n + n0 : n0 + BN / 2;
+        int row, n0;
+        place(i, row, n0);
+        const int n1 = PAIR ? l.out_n + n0 : n0 + BN / 2;
         for (int g = g0; g < g1; ++g, ++it) {
           const int st = it % kStages;
           ok = mbar_wait(&empty[st], ((it / kStages) & 1) ^ 1, &s_abort);
@@ -232,14 +207,9 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
           char* to = ring + st * S::kStage;
           mbar_arrive_expect_tx(&full[st], S::kStage);
           armed = it + 1;
-          if constexpr (SHARE) {
-            tma_load_2d_multicast(to + kTileA / 2 * cn, &a.x, &full[st], 128 * g, row + kM / 2 * cn, (uint16_t)(3 << (2 * cm)));
-            tma_load_2d_multicast(to + kTileA + BN * 64 * cm, &a.w, &full[st], 128 * g, cm ? n1 : n0, (uint16_t)(5 << cn));
-          } else {
-            tma_load_2d(to, &a.x, &full[st], 128 * g, row);
-            tma_load_2d(to + kTileA, &a.w, &full[st], 128 * g, n0);
-            tma_load_2d(to + kTileA + BN * 64, &a.w, &full[st], 128 * g, n1);
-          }
+          tma_load_2d(to, &a.x, &full[st], 128 * g, row);
+          tma_load_2d(to + kTileA, &a.w, &full[st], 128 * g, n0);
+          tma_load_2d(to + kTileA + BN * 64, &a.w, &full[st], 128 * g, n1);
         }
       }
       if (s_abort) {  // let every issued copy land before shared memory goes away
@@ -263,8 +233,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
           const uint32_t xa = smem_u32(ring + st * S::kStage), wa = xa + kTileA;
 #pragma unroll
           for (int k = 0; k < 4; ++k) dec::mma_f8_ss(tmem + b * BN, sdesc_k_sw128(xa + 32 * k), sdesc_k_sw128(wa + 32 * k), idesc, k != 0);
-          if (SHARE) mma_commit_multicast(&empty[st], (uint16_t)(3 << (2 * cm) | 5 << cn));  // whoever writes this stage
-          else mma_commit(&empty[st]);
+          mma_commit(&empty[st]);
           mma_commit(&pfull[b]);
         }
         __syncwarp();
@@ -272,14 +241,16 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
     if (lane == 0) mma_commit(&drain);
     __syncwarp();
   } else {
-    const int q = warp & 3, grp = warp >> 2, r = 32 * q + lane;  // tensor-memory lanes of this warp; its columns
+    const int q = warp & 3, grp = warp >> 2;  // tensor-memory lanes of this warp; its columns
     int it = 0;
     uint32_t box_phase = 0;
     bool ok = true;
     char* box = ring + kStages * S::kStage + warp * S::kBox;
     for (int i = first; ok && i < tiles; i += stride) {
-      const int64_t row = tile_row(i) + r;
-      const int n0 = tile_col(i);
+      int row0, n0;
+      place(i, row0, n0);
+      row0 += 32 * q;
+      const int64_t row = row0 + lane;
       const float* sx = l.qs + min(row, (int64_t)l.T - 1) * l.groups;
       // the weight rows of the thread's columns: 64 from c on, or (PAIR) 32 gates from c on and 32 ups.  Ups may cross into another
       // block of rows, `cross` columns from their first.
@@ -288,13 +259,13 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
       const float* sa = l.ws + (int64_t)min(c / 128, last) * l.groups;
       const float* sb = PAIR ? l.ws + (int64_t)min(up / 128, last) * l.groups : sa;
       const float* sc = PAIR ? l.ws + (int64_t)min(up / 128 + 1, last) * l.groups : sa;
-      const bool some = tile_row(i) + 32 * q < l.T && c < l.out_n;  // the warp has outputs
+      const bool some = row0 < l.T && c < l.out_n;  // the warp has outputs
       // the box, free again, and base's 32 columns from c0 on into it (lane 0)
       auto open_box = [&](int c0) {
         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         if (l.base && c0 < l.out_n) {
           mbar_arrive_expect_tx(&bfull[warp], 32 * 64);
-          tma_load_2d(box, &a.base, &bfull[warp], c0, tile_row(i) + 32 * q);
+          tma_load_2d(box, &a.base, &bfull[warp], c0, row0);
         }
       };
       if (SPLIT == 1 && a.boxed && some && lane == 0) open_box(c);
@@ -313,37 +284,31 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
 #pragma unroll
         for (int h = 0; h < 64; h += kAtOnce) {
           uint32_t p[kAtOnce];
-          if (PAIR) {
-            uint32_t e[kAtOnce];
-            static_assert(kAtOnce % 16 == 0, "");
+          const int from = PAIR ? (h < 32 ? h : BN / 2 + h - 32) + 32 * grp : h + 64 * grp;
 #pragma unroll
-            for (int j = 0; j < kAtOnce / 2; j += 8) {
-              tmem_ld_32x8(at + 32 * grp + h / 2 + j, e + j);
-              tmem_ld_32x8(at + BN / 2 + 32 * grp + h / 2 + j, e + kAtOnce / 2 + j);
-            }
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < kAtOnce; ++j) p[j] = e[j / 2 + j % 2 * (kAtOnce / 2)];
-          } else {
-#pragma unroll
-            for (int j = 0; j < kAtOnce; j += 16) tmem_ld_32x16(at + 64 * grp + h + j, p + j);
-            tmem_ld_wait();
-          }
+          for (int j = 0; j < kAtOnce; j += 16) tmem_ld_32x16(at + from + j, p + j);
+          tmem_ld_wait();
           if (h + kAtOnce == 64) {
             fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&pempty[b]);
           }
+          const float f = PAIR && h >= 32 ? fb : fa;
+          if (PAIR && h >= 32 && cross < 32) {
 #pragma unroll
-          for (int j = 0; j < kAtOnce; j += 2)
-            fma2(acc[h + j], acc[h + j + 1], p[j], p[j + 1], fa, !PAIR ? fa : (h + j) / 2 < cross ? fb : fc);
+            for (int j = 0; j < kAtOnce; j += 2)
+              fma2(acc[h + j], acc[h + j + 1], p[j], p[j + 1], h - 32 + j < cross ? fb : fc, h - 31 + j < cross ? fb : fc);
+          } else {
+#pragma unroll
+            for (int j = 0; j < kAtOnce; j += 2) fma2(acc[h + j], acc[h + j + 1], p[j], p[j + 1], f, f);
+          }
         }
       }
       if constexpr (SPLIT == 1) {
         constexpr int kMine = PAIR ? 32 : 64;
         if constexpr (PAIR) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) acc[j] = silu_mul(acc[2 * j], acc[2 * j + 1]);
+          for (int j = 0; j < 32; ++j) acc[j] = silu_mul(acc[j], acc[32 + j]);
         }
         if (a.boxed && some) {
 #pragma unroll
@@ -364,11 +329,11 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
               fill_box(box, l.out_dtype, l.base != nullptr, acc + h, lane);
               fence_proxy_async_smem();
               __syncwarp();
-              if (lane == 0) tma_store_2d(&a.out, box, c + h, tile_row(i) + 32 * q);
+              if (lane == 0) tma_store_2d(&a.out, box, c + h, row0);
             }
           }
         } else if (ok && some) {
-          store_any_columns<kMine, S::kBox / 128>(l, (float*)box, tile_row(i) + 32 * q, c, acc, lane);
+          store_any_columns<kMine, S::kBox / 128>(l, (float*)box, row0, c, acc, lane);
         }
       } else {
         // Every block takes 64 / SPLIT of a thread's sums from all of them.  Its ring is free: the MMAs that read it are done.
@@ -381,8 +346,10 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
 #pragma unroll
         for (int to = 0; to < SPLIT; ++to)
 #pragma unroll
-          for (int j = 0; j < kMine; j += 4)
-            store_remote4(smem_u32(meet + ((rank * (kMine / 4) + j / 4) * kThr + threadIdx.x) * 4), to, acc + kMine * to + j);
+          for (int j = 0; j < kMine; j += 4) {
+            const int from = !PAIR ? kMine * to + j : j < kMine / 2 ? kMine / 2 * to + j : 32 + kMine / 2 * (to - 1) + j;
+            store_remote4(smem_u32(meet + ((rank * (kMine / 4) + j / 4) * kThr + threadIdx.x) * 4), to, acc + from);
+          }
         cluster_arrive();
         cluster_wait();
         float y[kMine];
@@ -397,9 +364,9 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
         constexpr int kOut = PAIR ? kMine / 2 : kMine;
         if constexpr (PAIR) {
 #pragma unroll
-          for (int j = 0; j < kOut; ++j) y[j] = silu_mul(y[2 * j], y[2 * j + 1]);
+          for (int j = 0; j < kOut; ++j) y[j] = silu_mul(y[j], y[kOut + j]);
         }
-        if (ok && some) store_any_columns<kOut, S::kBox / 128>(l, (float*)(ring + kStages * S::kStage + warp * S::kBox), tile_row(i) + 32 * q, c + kOut * rank, y, lane);
+        if (ok && some) store_any_columns<kOut, S::kBox / 128>(l, (float*)(ring + kStages * S::kStage + warp * S::kBox), row0, c + kOut * rank, y, lane);
       }
     }
   }
@@ -419,24 +386,20 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
   __syncthreads();
   fence_after_sync();
   if (threadIdx.x == 0 && s_abort) set_dev_error(&g_fp8_error, kDevTimeout);
-  if (SHARE) {  // no block leaves while another one may still write or arrive in it
-    cluster_arrive();
-    cluster_wait();
-  }
   if (warp == kMma) tmem_dealloc(tmem, kBufs * BN);
 }
 
-template <int BN, bool PAIR, int SPLIT, bool SHARE>
+template <int BN, bool PAIR, int SPLIT>
 cudaError_t launch(const Fp8LinearArgs& l, cudaStream_t s) {
   using S = Shape<BN>;
   static SmemOptIn opt_in;
-  if (const cudaError_t e = opt_in(fp8_tile_kernel<BN, PAIR, SPLIT, SHARE>, S::kSmem); e != cudaSuccess) return e;
+  if (const cudaError_t e = opt_in(fp8_tile_kernel<BN, PAIR, SPLIT>, S::kSmem); e != cudaSuccess) return e;
   Args a;
   a.l = l;
   a.tiles_m = (l.T + kM - 1) / kM;
   a.tiles_n = (l.out_n + (PAIR ? BN / 2 : BN) - 1) / (PAIR ? BN / 2 : BN);
   const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  if (!tc_make_map(&a.x, u8, l.x, l.K, l.T, l.ldx, 128, SHARE ? kM / 2 : kM, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  if (!tc_make_map(&a.x, u8, l.x, l.K, l.T, l.ldx, 128, kM, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !tc_make_map(&a.w, u8, l.w, l.K, l.N, l.K, 128, BN / 2, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   a.boxed = false;
@@ -450,8 +413,7 @@ cudaError_t launch(const Fp8LinearArgs& l, cudaStream_t s) {
       return cudaErrorInvalidValue;
     a.boxed = true;
   }
-  constexpr int kBlocks = SHARE ? 4 : SPLIT;
-  const int64_t tiles = SHARE ? (int64_t)((a.tiles_m + 1) / 2) * ((a.tiles_n + 1) / 2) : (int64_t)a.tiles_m * a.tiles_n;
+  const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = S::kSmem;
@@ -460,43 +422,24 @@ cudaError_t launch(const Fp8LinearArgs& l, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kBlocks;
+  attr[1].val.clusterDim.x = SPLIT;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = kBlocks > 1 ? 2 : 1;
-  int64_t most = tiles;
-  if (SHARE) {  // as many clusters as the device holds at once
-    static PerDevice held;
-    std::atomic<int>* at;
-    if (const cudaError_t e = held.here(&at); e != cudaSuccess) return e;
-    int n = at ? at->load(std::memory_order_relaxed) : 0;
-    if (n == 0) {
-      cfg.gridDim = dim3(kBlocks);
-      cudaLaunchConfig_t ask = cfg;
-      ask.attrs = attr + 1;
-      ask.numAttrs = 1;
-      if (const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, fp8_tile_kernel<BN, PAIR, SPLIT, SHARE>, &ask); e != cudaSuccess) return e;
-      if (n < 1) n = 1;
-      if (at) at->store(n, std::memory_order_relaxed);
-    }
-    most = n;
-  } else if (SPLIT == 1) {
-    most = (int64_t)tc_num_sms() * (BN == 256 ? 1 : 2);
-  }
-  cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * kBlocks));
+  cfg.numAttrs = SPLIT > 1 ? 2 : 1;
+  const int64_t most = SPLIT > 1 ? tiles : (int64_t)tc_num_sms() * (BN == 256 ? 1 : 2);
+  cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * SPLIT));
   note_launches(1);
-  return cudaLaunchKernelEx(&cfg, fp8_tile_kernel<BN, PAIR, SPLIT, SHARE>, a);
+  return cudaLaunchKernelEx(&cfg, fp8_tile_kernel<BN, PAIR, SPLIT>, a);
 }
 
 template <bool PAIR>
 cudaError_t choose(const Fp8LinearArgs& l, cudaStream_t s) {
   const int64_t rows = (l.T + kM - 1) / kM, sms = tc_num_sms();
   auto tiles = [&](int bn) { return rows * ((l.out_n + (PAIR ? bn / 2 : bn) - 1) / (PAIR ? bn / 2 : bn)); };
-  if (tiles(256) >= sms) return rows > 1 ? launch<256, PAIR, 1, true>(l, s) : launch<256, PAIR, 1, false>(l, s);
+  if (rows > 1 && tiles(256) * 2 >= sms) return launch<256, PAIR, 1>(l, s);
   const int64_t n = tiles(64);
-  if (n >= sms || l.groups < 2) return launch<64, PAIR, 1, false>(l, s);
-  if (n * 2 >= sms || l.groups < 4) return launch<64, PAIR, 2, false>(l, s);
-  return launch<64, PAIR, 4, false>(l, s);
+  if (n * 2 > sms || l.groups < 8) return launch<64, PAIR, 1>(l, s);
+  return n * 4 > sms ? launch<64, PAIR, 2>(l, s) : launch<64, PAIR, 4>(l, s);
 }
 
 }  // namespace
