@@ -23,7 +23,10 @@ constexpr int kM = 128, kTileA = kM * 128;  // rows of x per tile; bytes of its 
 template <int BN>
 struct Shape {
   static constexpr int kPromote = BN / 16;  // warps: a row per thread, 64 columns per warp
-  static constexpr int kThreads = 32 * (kPromote + 2);
+  // A warp of its own brings the groups' scales where 96 registers a thread leave nothing for it (each promoting thread loading its
+  // row's, each from a line of its own: 16384 x 4096 x 4096 359 us).  For BN = 64 a seventh warp would cost the others 40 registers.
+  static constexpr bool kScaleWarp = BN == 256;
+  static constexpr int kThreads = 32 * (kPromote + 2 + kScaleWarp);
   static constexpr int kStage = kTileA + BN * 128;
   // A stage comes back some 3100 cycles after it was freed (), a group's MMAs take 640: the
   // more stages the better, and the outputs make do with 2 KB per warp (16384 x 2048 x 4096: three stages 169 us).
@@ -136,15 +139,17 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* s
 }
 
 // A tile per cluster of SPLIT blocks, which share its groups of columns and join their sums through each other's shared memory;
-// SPLIT = 1: blocks walk the tiles.  PAIR: the tile's weight rows are BN / 2 gates and the same features' ups; a thread's sums
+// SPLIT = 1: blocks walk the tiles.  MODE 1, 2 (PAIR): the tile's weight rows are BN / 2 gates and the same features' ups; a thread's sums
 // are then 32 of each (alternating, so that a factor had to be chosen for each, 1024 x 2048 x 6000 took twice as long).
-template <int BN, bool PAIR, int SPLIT>
+template <int BN, int MODE, int SPLIT>
 __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_tile_kernel(const __grid_constant__ Args a) {
   using S = Shape<BN>;
+  constexpr bool PAIR = MODE != 0, CROSS = MODE == 2;
   constexpr int kBufs = S::kBuffers, kStages = S::kStages;
   extern __shared__ __align__(1024) char smem_raw[];
   char* ring = (char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   __shared__ uint64_t full[kStages], empty[kStages], pfull[kBufs], pempty[kBufs], bfull[S::kPromote], drain;
+  __shared__ float s_x[kBufs][kM], s_w[kBufs][4];  // a group's scales: of the rows; of the blocks of weight rows
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const Fp8LinearArgs& l = a.l;
@@ -156,7 +161,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < kBufs; ++i) {
-      mbar_init(&pfull[i], 1);
+      mbar_init(&pfull[i], S::kScaleWarp ? 2 : 1);
       mbar_init(&pempty[i], S::kPromote);
     }
     for (int i = 0; i < S::kPromote; ++i) mbar_init(&bfull[i], 1);
@@ -240,6 +245,36 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
       }
     if (lane == 0) mma_commit(&drain);
     __syncwarp();
+  } else if (S::kScaleWarp && warp == kMma + 1) {
+    // The scales of a group's 128 rows and of its blocks of weight rows, loaded a group ahead.
+    int it = 0;
+    bool ok = true;
+    for (int i = first; ok && i < tiles; i += stride) {
+      int row0, n0;
+      place(i, row0, n0);
+      const int block = lane == 0 ? n0 / 128 : PAIR ? (l.out_n + n0) / 128 + lane - 1 : n0 / 128 + 1;
+      const float *w = l.ws + (int64_t)min(block, (l.N - 1) / 128) * l.groups, *x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = l.qs + min((int64_t)row0 + 32 * j + lane, (int64_t)l.T - 1) * l.groups;
+      float sx[4], sw = 0.f;
+      auto load = [&](int g) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sx[j] = x[j][g];
+        if (lane < 3) sw = w[g];
+      };
+      load(g0);
+      for (int g = g0; g < g1; ++g, ++it) {
+        const int b = it % kBufs;
+        ok = __all_sync(0xffffffffu, mbar_wait(&pempty[b], ((it / kBufs) & 1) ^ 1, &s_abort));
+        if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s_x[b][32 * j + lane] = sx[j];
+        if (lane < 3) s_w[b][lane] = sw;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[b]);
+        if (g + 1 < g1) load(g + 1);
+      }
+    }
   } else {
     const int q = warp & 3, grp = warp >> 2;  // tensor-memory lanes of this warp; its columns
     int it = 0;
@@ -250,15 +285,13 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
       int row0, n0;
       place(i, row0, n0);
       row0 += 32 * q;
-      const int64_t row = row0 + lane;
-      const float* sx = l.qs + min(row, (int64_t)l.T - 1) * l.groups;
-      // the weight rows of the thread's columns: 64 from c on, or (PAIR) 32 gates from c on and 32 ups.  Ups may cross into another
+      // the weight rows of the thread's columns: 64 from c on, or (PAIR) 32 gates from c on and 32 ups.  CROSS: ups may get into another
       // block of rows, `cross` columns from their first.
-      const int c = n0 + (PAIR ? 32 : 64) * grp, last = (l.N - 1) / 128;
-      const int up = l.out_n + c, cross = PAIR ? 128 - up % 128 : 128;
-      const float* sa = l.ws + (int64_t)min(c / 128, last) * l.groups;
-      const float* sb = PAIR ? l.ws + (int64_t)min(up / 128, last) * l.groups : sa;
-      const float* sc = PAIR ? l.ws + (int64_t)min(up / 128 + 1, last) * l.groups : sa;
+      const int c = n0 + (PAIR ? 32 : 64) * grp, up = l.out_n + c, cross = CROSS ? 128 - up % 128 : 128;
+      const int block = PAIR ? 1 + up / 128 - (l.out_n + n0) / 128 : c / 128 - n0 / 128;  // whose scale, of s_w
+      const int last = (l.N - 1) / 128;
+      const float *sx = l.qs + min((int64_t)row0 + lane, (int64_t)l.T - 1) * l.groups, *sa = l.ws + (int64_t)min(c / 128, last) * l.groups;
+      const float *sb = PAIR ? l.ws + (int64_t)min(up / 128, last) * l.groups : sa, *sc = CROSS ? l.ws + (int64_t)min(up / 128 + 1, last) * l.groups : sa;
       const bool some = row0 < l.T && c < l.out_n;  // the warp has outputs
       // the box, free again, and base's 32 columns from c0 on into it (lane 0)
       auto open_box = [&](int c0) {
@@ -275,12 +308,23 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
       for (int j = 0; j < 64; ++j) acc[j] = 0.f;
       for (int g = g0; g < g1; ++g, ++it) {
         const int b = it % kBufs;
-        const float s = sx[g], fa = s * __ldg(sa + g), fb = PAIR ? s * __ldg(sb + g) : fa, fc = PAIR && cross < 32 ? s * __ldg(sc + g) : fb;
+        float s, wa, wb = 0.f, wc = 0.f;
+        if (!S::kScaleWarp) {
+          s = sx[g], wa = __ldg(sa + g);
+          if (PAIR) wb = __ldg(sb + g);
+          if (CROSS && cross < 32) wc = __ldg(sc + g);
+        }
         ok = __all_sync(0xffffffffu, ok && mbar_wait(&pfull[b], (it / kBufs) & 1, &s_abort));
         if (!ok) break;
         fence_after_sync();
+        if (S::kScaleWarp) {
+          s = s_x[b][32 * q + lane], wa = s_w[b][PAIR ? 0 : block];
+          if (PAIR) wb = s_w[b][block];
+          if (CROSS) wc = s_w[b][min(block + 1, 2)];
+        }
+        const float fa = s * wa, fb = PAIR ? s * wb : fa, fc = CROSS ? s * wc : fb;
         const uint32_t at = taddr(tmem, 32 * q, b * BN);
-        constexpr int kAtOnce = BN == 256 ? 16 : 32;  // sums per wait: as registers allow
+        constexpr int kAtOnce = CROSS ? 16 : 32;  // sums per wait, as registers allow (16384 x 2048 x 4096: 32 143 us, 16 148; CROSS: 16 45, 32 59)
 #pragma unroll
         for (int h = 0; h < 64; h += kAtOnce) {
           uint32_t p[kAtOnce];
@@ -294,7 +338,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
             if (lane == 0) mbar_arrive(&pempty[b]);
           }
           const float f = PAIR && h >= 32 ? fb : fa;
-          if (PAIR && h >= 32 && cross < 32) {
+          if (CROSS && h >= 32 && cross < 32) {
 #pragma unroll
             for (int j = 0; j < kAtOnce; j += 2)
               fma2(acc[h + j], acc[h + j + 1], p[j], p[j + 1], h - 32 + j < cross ? fb : fc, h - 31 + j < cross ? fb : fc);
@@ -389,11 +433,12 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
   if (warp == kMma) tmem_dealloc(tmem, kBufs * BN);
 }
 
-template <int BN, bool PAIR, int SPLIT>
+template <int BN, int MODE, int SPLIT>
 cudaError_t launch(const Fp8LinearArgs& l, cudaStream_t s) {
   using S = Shape<BN>;
+  constexpr bool PAIR = MODE != 0;
   static SmemOptIn opt_in;
-  if (const cudaError_t e = opt_in(fp8_tile_kernel<BN, PAIR, SPLIT>, S::kSmem); e != cudaSuccess) return e;
+  if (const cudaError_t e = opt_in(fp8_tile_kernel<BN, MODE, SPLIT>, S::kSmem); e != cudaSuccess) return e;
   Args a;
   a.l = l;
   a.tiles_m = (l.T + kM - 1) / kM;
@@ -429,23 +474,25 @@ cudaError_t launch(const Fp8LinearArgs& l, cudaStream_t s) {
   const int64_t most = SPLIT > 1 ? tiles : (int64_t)tc_num_sms() * (BN == 256 ? 1 : 2);
   cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * SPLIT));
   note_launches(1);
-  return cudaLaunchKernelEx(&cfg, fp8_tile_kernel<BN, PAIR, SPLIT>, a);
+  return cudaLaunchKernelEx(&cfg, fp8_tile_kernel<BN, MODE, SPLIT>, a);
 }
 
-template <bool PAIR>
+template <int MODE>
 cudaError_t choose(const Fp8LinearArgs& l, cudaStream_t s) {
+  constexpr bool PAIR = MODE != 0;
   const int64_t rows = (l.T + kM - 1) / kM, sms = tc_num_sms();
   auto tiles = [&](int bn) { return rows * ((l.out_n + (PAIR ? bn / 2 : bn) - 1) / (PAIR ? bn / 2 : bn)); };
-  if (rows > 1 && tiles(256) * 2 >= sms) return launch<256, PAIR, 1>(l, s);
+  if (rows > 1 && tiles(256) * 2 >= sms) return launch<256, MODE, 1>(l, s);
   const int64_t n = tiles(64);
-  if (n * 2 > sms || l.groups < 8) return launch<64, PAIR, 1>(l, s);
-  return n * 4 > sms ? launch<64, PAIR, 2>(l, s) : launch<64, PAIR, 4>(l, s);
+  if (n * 2 > sms || l.groups < 8) return launch<64, MODE, 1>(l, s);
+  return n * 4 > sms ? launch<64, MODE, 2>(l, s) : launch<64, MODE, 4>(l, s);
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_tiles(const Fp8LinearArgs& l, cudaStream_t s) {
-  return l.out_n != l.N ? choose<true>(l, s) : choose<false>(l, s);
+  if (l.out_n == l.N) return choose<0>(l, s);
+  return l.out_n % 32 == 0 ? choose<1>(l, s) : choose<2>(l, s);
 }
 
 }  // namespace moe
