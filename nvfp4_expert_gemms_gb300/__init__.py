@@ -8,7 +8,8 @@ Names mirror the C ABI: moe_packed_size, moe_pack_experts, moe_workspace_size,
 moe_layer_forward, moe_workspace_size_host_io, moe_layer_forward_host,
 moe_get_device_error, moe_status_string, moe_debug_route, moe_debug_dequant,
 moe_debug_quant_act.  The operators around the experts (norms in and out of the block, scored
-routing, request adapters) and MoEBlock, which runs them together, are in block.py.
+routing, request adapters, the layer for a few tokens, FP8 products beside the experts) and MoEBlock, which runs
+them together, are in block.py.
 """
 from __future__ import annotations
 

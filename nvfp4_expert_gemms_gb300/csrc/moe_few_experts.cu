@@ -8,8 +8,9 @@
 // stand in the way.  An atomic's answer takes over a microsecond, so a team gets along with one ticket per matrix and asks for
 // the next one as it starts a run.
 //
-// A block holds two teams.  One thread of a team copies by TMA, eight pieces of 128 columns (64 of bf16) by 32 rows to a stage of shared
-// memory, 54 to 64 KB ahead (HBM's rate and latency ask for some 45 per block), into the down matrices while h is not there
+// A block holds two teams, each with stages of its own (with stages for both, of which a team skips the other's, a barrier could run
+// a lap ahead of who waits on it).  One thread of a team copies by TMA, eight pieces of 128 columns (64 of bf16) by 32 rows to a stage of
+// shared memory, 50 to 64 KB ahead (HBM's rate and latency ask for some 45 per block), into the down matrices while h is not there
 // yet.  Eight warps take a piece of a stage each, decode it straight into MMA operands, multiply it with the entry's tokens, whose
 // operands they keep in shared memory from unit to unit, and leave their sums of 32 rows there too.  A ninth adds them up and
 // finishes the rows: h = silu(gate) up, or weighted rows of y.  Who copied sums y over each token's experts at the end,
@@ -19,12 +20,14 @@
 // changed.  With counters behind fences in their place a block's units took up to half as long again (134 us for 90 at 16
 // tokens of FP8, 128 experts of 2048 x 768, whichever warp fenced); a fence waits for the SM's traffic.
 //
-// What it takes: a unit's way is a chain of single warps' instructions, at some six cycles each: of the copying thread, the
-// multiplying warps and the finishing one, each of which must keep up with HBM, which brings a unit of FP8 in 2800 cycles per SM and one
-// of four bits in 1500.  Hence teams, each on a unit of its own, and as little as possible per stage for the copying thread (one
-// warp that copied for both, with votes and constants looked up per stage: 91 us at 16 tokens of FP8, 90 of INT4).  And nothing
-// in that chain may wait for L2: no spilled register (with 222 KB of shared memory there is next to no L1), no scale or address
-// that was not asked for early.
+// What it takes (128 experts of 2048 x 768, 8 per token, with the router's kernel): FP8 20.9 us at 1 token and 82 at 16, where HBM alone would
+// take 5.6 and 57; NVFP4 42 at 4 tokens (11.5), INT4 69 at 16 (29.6).  Some 7 to 10 us are the router and the entries, 3 to 5 the waits
+// for the last h and the last y; the rest is instructions: of a piece's multiplication (130 to 210 per warp) and of what surrounds
+// it (some 190, shared by eight warps in part), at six to nine cycles each.  HBM brings a unit of FP8 in 2800 cycles per SM and one of
+// four bits in 1500.  Hence teams, each on a unit of its own; one wait per stage, whose description comes with it (a queue of units
+// beside the stages, and scales loaded for each: 89 us for 83 at 16 tokens of FP8, 73 for 69.5 of INT4); as little as possible per stage for the
+// copying thread (one warp that copied for both: 91).  And nothing in that chain may wait for L2: no spilled register (with 222 KB of
+// shared memory there is next to no L1), no scale or address that was not asked for early.
 #include "moe_few.cuh"
 #include "moe_formats.cuh"
 #include "moe_tc.cuh"

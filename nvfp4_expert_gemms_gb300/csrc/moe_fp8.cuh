@@ -30,7 +30,7 @@ struct Fp8LinearArgs {
   int T, K, N, groups;
   int out_n;  // N, or N / 2 with SiLU(gate) * up
 };
-// Up to kFp8Rows rows, of any x_dtype (moe_fp8_rows.cu); any number, of codes (moe_fp8_tile.cu).
+// Up to kFp8Rows rows, of any x_dtype (moe_fp8_rows.cu); any number, of codes (moe_fp8_tile.cu).  moe_fp8_linear.cu chooses.
 constexpr int kFp8Rows = 16;
 cudaError_t launch_fp8_rows(const Fp8LinearArgs& a, cudaStream_t s);
 cudaError_t launch_fp8_tiles(const Fp8LinearArgs& a, cudaStream_t s);

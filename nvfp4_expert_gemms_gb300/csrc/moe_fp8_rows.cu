@@ -1,10 +1,10 @@
 // moe_fp8_linear for a few rows: one kernel that quantizes the rows on the way.
 //
-// A block takes 16 weight rows (8 gates and the same features' ups), sixteen warps a group of 128 columns each.  A lane loads its
-// shares of the weights and of up to eight rows of x straight into registers, all at once; four lanes hold a row's group, so
+// A block takes 16 weight rows (8 gates and the same features' ups), sixteen warps a group of 128 columns each, and up to eight or
+// 16 rows of x.  A lane loads its shares of the weights and of eight rows of x straight into registers, all at once; four lanes hold a row's group, so
 // its maximum is two shuffles away, and every warp quantizes what it multiplies.  E4M3 times E4M3 is exact in fp16 operands
 // with an fp32 accumulator (mma.sync m16n8k16: the weights' bytes set the pace).  The sums meet in shared memory.
-// Bound: latency, and from some 16 MB on HBM.
+// Bound: latency (1 x 2048 x 4096: 3.8 us in a graph, 1.2 by HBM), for large matrices L2, from which every block reads all of x.
 #include "moe_fp8.cuh"
 
 namespace moe {
@@ -57,6 +57,7 @@ __device__ __forceinline__ float quantize_group(const T* p, int left, int t, uin
   return __fdiv_rn(1.f, s);
 }
 
+// (Two passes with two blocks per SM, 64 registers a thread, spill: 9 x 2048 x 1536 pairs 5.5 us for 4.6.)
 template <bool PAIR, int PASSES>
 __global__ void __launch_bounds__(kThreads, PASSES == 1 ? 2 : 1) fp8_rows_kernel(const Fp8LinearArgs a, const bool wide) {
   __shared__ float4 part[kWarps][PASSES][32];

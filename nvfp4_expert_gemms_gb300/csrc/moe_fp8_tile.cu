@@ -3,7 +3,8 @@
 // Both operands go to the tensor cores as stored codes (kind::f8f6f4, M = 128 rows of x, N = BN weight rows, K = 32; TMA tiles in
 // the 128-byte swizzle).  Their scales change every 128 columns, so each group's partial sum goes to a tensor-memory
 // buffer of its own, and promoting warps read it back, scale it and add it to sums that they keep in registers, while the MMAs
-// of the next groups fill the other buffers.
+// of the next groups fill the other buffers.  16384 x 2048 x 4096 takes 143 us (1.92 PFLOP/s), x 4096 258 us (2.13 PFLOP/s): half of
+// what the MMAs alone would take is the promotion, 64 sums a thread and group, and the L2's rate (48 KB per 8.4 MFLOP).
 #include <cudaTypedefs.h>
 
 #include "moe_dec.cuh"
@@ -28,8 +29,8 @@ struct Shape {
   static constexpr bool kScaleWarp = BN == 256;
   static constexpr int kThreads = 32 * (kPromote + 2 + kScaleWarp);
   static constexpr int kStage = kTileA + BN * 128;
-  // A stage comes back some 3100 cycles after it was freed (), a group's MMAs take 640: the
-  // more stages the better, and the outputs make do with 2 KB per warp (16384 x 2048 x 4096: three stages 169 us).
+  // A stage comes back thousands of cycles after it was freed, a group's MMAs take 640: the more stages the better, and the outputs make
+  // do with 2 KB per warp.
   static constexpr int kStages = BN == 256 ? 4 : 3;
   static constexpr int kBuffers = BN == 256 ? 2 : 4;
   static constexpr int kBox = BN == 256 ? 2048 : 4096;  // per promoting warp: outputs on their way
@@ -40,6 +41,7 @@ struct Args {
   CUtensorMap x, w, out, base;
   Fp8LinearArgs l;
   int tiles_m, tiles_n;
+  int box_m;   // rows of x that a tile's copies ask for
   bool boxed;  // outputs leave (and base comes) by TMA, 32 rows of a warp's columns at a time
 };
 
@@ -210,7 +212,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
           ok = mbar_wait(&empty[st], ((it / kStages) & 1) ^ 1, &s_abort);
           if (!ok) break;
           char* to = ring + st * S::kStage;
-          mbar_arrive_expect_tx(&full[st], S::kStage);
+          mbar_arrive_expect_tx(&full[st], 128 * (a.box_m + BN));
           armed = it + 1;
           tma_load_2d(to, &a.x, &full[st], 128 * g, row);
           tma_load_2d(to + kTileA, &a.w, &full[st], 128 * g, n0);
@@ -444,7 +446,10 @@ cudaError_t launch(const Fp8LinearArgs& l, cudaStream_t s) {
   a.tiles_m = (l.T + kM - 1) / kM;
   a.tiles_n = (l.out_n + (PAIR ? BN / 2 : BN) - 1) / (PAIR ? BN / 2 : BN);
   const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  if (!tc_make_map(&a.x, u8, l.x, l.K, l.T, l.ldx, 128, kM, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  // No more rows than there are, in 32s: what is left of a single tile multiplies whatever stands in shared memory, into rows that
+  // are not stored.  (Copies of 128 rows of a matrix of fewer than 32 took almost twice as long: 20 x 4096 x 14336 34.8 us, 32 rows 20.6.)
+  a.box_m = l.T < kM ? (l.T + 31) / 32 * 32 : kM;
+  if (!tc_make_map(&a.x, u8, l.x, l.K, l.T, l.ldx, 128, a.box_m, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !tc_make_map(&a.w, u8, l.w, l.K, l.N, l.K, 128, BN / 2, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   a.boxed = false;
@@ -482,8 +487,14 @@ cudaError_t choose(const Fp8LinearArgs& l, cudaStream_t s) {
   constexpr bool PAIR = MODE != 0;
   const int64_t rows = (l.T + kM - 1) / kM, sms = tc_num_sms();
   auto tiles = [&](int bn) { return rows * ((l.out_n + (PAIR ? bn / 2 : bn) - 1) / (PAIR ? bn / 2 : bn)); };
+  // Tiles of 256 columns from half of one wave on (us, 64 and 256: 512 x 2048 x 4096, 64 tiles, 10.9 and 13; 600 x 4096 x 4096, 80 tiles,
+  // 31.4 and 29.6; 1024 x 2048 x 4096 18.5 and 13.3); a single row of tiles streams weights, and more and smaller tiles do that better
+  // (128 x 2048 x 40960 27.7 and 30.4).
   if (rows > 1 && tiles(256) * 2 >= sms) return launch<256, MODE, 1>(l, s);
   const int64_t n = tiles(64);
+  // K split where that leaves every block an SM of its own and each share two groups or more: the blocks' meetings cost over a
+  // microsecond (us, SPLIT 1, 2 and 4: 64 x 2048 x 1024, 16 tiles, 9.8, 8.9 and 7.1; 32 x 2048 x 4096, 64 tiles, 11.3, 11.0 and 12.1;
+  // 256 x 2048 x 4096, 128 tiles, 10.1, 10.4 and 17.3; 128 x 512 x 2048, 32 tiles of 4 groups, 4.4, 6.1 and 5.6).
   if (n * 2 > sms || l.groups < 8) return launch<64, MODE, 1>(l, s);
   return n * 4 > sms ? launch<64, MODE, 2>(l, s) : launch<64, MODE, 4>(l, s);
 }
