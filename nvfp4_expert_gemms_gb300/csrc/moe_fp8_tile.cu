@@ -3,7 +3,7 @@
 // Both operands go to the tensor cores as stored codes (kind::f8f6f4, M = 128 rows of x, N = BN weight rows, K = 32; TMA tiles in
 // the 128-byte swizzle).  Their scales change every 128 columns, so each group's partial sum goes to a tensor-memory
 // buffer of its own, and promoting warps read it back, scale it and add it to sums that they keep in registers, while the MMAs
-// of the next groups fill the other buffers.  16384 x 2048 x 4096 takes 143 us (1.92 PFLOP/s), x 4096 258 us (2.13 PFLOP/s): half of
+// of the next groups fill the other buffers.  16384 x 2048 x 4096 takes 143 us (1.91 PFLOP/s), x 4096 258 us (2.13 PFLOP/s): half of
 // what the MMAs alone would take is the promotion, 64 sums a thread and group, and the L2's rate (48 KB per 8.4 MFLOP).
 #include <cudaTypedefs.h>
 
