@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(kRouterThreads, 1) few_router_kernel(const __g
   if (blockIdx.x == 0 && threadIdx.x < 2) a.status[threadIdx.x] = 0;
   for (size_t i = blockIdx.x * kRouterThreads + threadIdx.x; i < pieces; i += gridDim.x * kRouterThreads)
     ((uint4*)a.h)[i] = make_uint4(kFewUnset, kFewUnset, kFewUnset, kFewUnset);
+  __syncwarp();  // (the loop may end inside a warp, and the barrier takes whole ones)
   cluster_wait();
   for (int e = rank * kRouterWarps + warp; e < E; e += kCluster * kRouterWarps) {
     Pairs sum;
@@ -154,6 +155,7 @@ __global__ void __launch_bounds__(kRouterThreads, 1) few_router_kernel(const __g
       *(uint4*)(a.xs + (size_t)t * H + 8 * i) = *(const uint4*)o;
     }
   }
+  __syncwarp();
   cluster_wait();
   if (rank == 0 && warp == 0) {
     ScoreArgs r = a.router;

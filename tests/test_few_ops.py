@@ -124,6 +124,16 @@ def test_few(fmt, T, E, k, H, I):
     layer.check(layer.run())
 
 
+@pytest.mark.parametrize("T,E,k,H,I", [(1, 1, 1, 128, 128), (1, 3, 3, 640, 128), (3, 7, 5, 1152, 128), (5, 256, 1, 4224, 128)])
+def test_few_rows_and_marks_that_end_inside_a_warp(T, E, k, H, I):
+    # H / 8 pieces of a row, and a sixteenth of h's and y's bytes, that are no multiples of 32: lanes of one warp take
+    # different numbers of turns before the router's blocks meet
+    layer = Layer("fp8", T, E, k, H, I, seed=H)
+    want = layer.run()
+    layer.check(want)
+    assert all(torch.equal(layer.run(), want) for _ in range(20))
+
+
 @pytest.mark.parametrize("fmt", sorted(M.FORMATS))
 @pytest.mark.parametrize("T,E,k,H,I", MANY)
 def test_few_of_many_slots_and_long_rows(fmt, T, E, k, H, I):
