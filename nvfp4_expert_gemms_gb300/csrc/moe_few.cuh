@@ -5,7 +5,7 @@
 // operands may come from registers, straight from the decoded codes, with no second trip through shared memory.
 // E4M3, E2M1 x E4M3 and INT4 weights are all exact in fp16, whose products with fp16 activations are exact in the
 // fp32 accumulator; a row of activations is scaled by a power of two so that fp16 holds its bf16 values exactly (but for
-// elements below 2^-29 of the row's largest, 2^-25 with INT4 weights, which lose low bits), and an fp32 row of h is held in two fp16 terms.
+// elements below 2^-29 of the row's largest, which lose low bits), and an fp32 row of h is held in two fp16 terms.
 // bf16 weights meet bf16 activations, h in two bf16 terms.
 #pragma once
 #include "moe_score.cuh"

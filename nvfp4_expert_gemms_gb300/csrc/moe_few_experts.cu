@@ -21,8 +21,8 @@
 // tokens of FP8, 128 experts of 2048 x 768, whichever warp fenced); a fence waits for the SM's traffic.
 //
 // What it takes (128 experts of 2048 x 768, 8 per token, with the router's kernel): FP8 20.9 us at 1 token and 82 at 16, where HBM alone would
-// take 5.6 and 57; NVFP4 42 at 4 tokens (11.5), INT4 69 at 16 (29.6).  Some 7 to 10 us are the router and the entries, 3 to 5 the waits
-// for the last h and the last y; the rest is instructions: of a piece's multiplication (130 to 210 per warp) and of what surrounds
+// take 5.6 and 57; NVFP4 42 at 4 tokens (11.5), INT4 80 at 16 (29.6).  Some 7 to 10 us are the router and the entries, 3 to 5 the waits
+// for the last h and the last y; the rest is instructions: of a piece's multiplication (some 130 to 230 per warp) and of what surrounds
 // it (some 190, shared by eight warps in part), at six to nine cycles each.  HBM brings a unit of FP8 in 2800 cycles per SM and one of
 // four bits in 1500.  Hence teams, each on a unit of its own; one wait per stage, whose description comes with it (a queue of units
 // beside the stages, and scales loaded for each: 89 us for 83 at 16 tokens of FP8, 73 for 69.5 of INT4); as little as possible per stage for the
@@ -127,37 +127,31 @@ __device__ __forceinline__ int element(int t, int j) {
   return Format<FMT>::kInt4 ? 8 * t + 32 * j : Format<FMT>::kPiece / 4 * t + 8 * j;
 }
 
-// INT4 words decode into pairs of elements (j, j + 4), every other pair 16 times too large: the same order, and that taken back, for the
-// activations.  Their sum goes to `sum`.
+// INT4 words decode into pairs of elements (j, j + 4): the same order for the activations.
 template <int FMT>
-__device__ __forceinline__ void order_pairs(uint32_t* b, float& sum) {
+__device__ __forceinline__ void order_pairs(uint32_t* b) {
   if constexpr (Format<FMT>::kInt4) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 v = __half22float2(*(const __half2*)&b[i]);
-      sum += v.x + v.y;
-    }
     const uint32_t r0 = b[0], r1 = b[1], r2 = b[2], r3 = b[3];
     b[0] = __byte_perm(r0, r2, 0x5410);
-    b[1] = hmul2(__byte_perm(r0, r2, 0x7632), 0x2C002C00u);
+    b[1] = __byte_perm(r0, r2, 0x7632);
     b[2] = __byte_perm(r1, r3, 0x5410);
-    b[3] = hmul2(__byte_perm(r1, r3, 0x7632), 0x2C002C00u);
+    b[3] = __byte_perm(r1, r3, 0x7632);
   }
 }
-// -8 times the sums of the lane's MMA columns 2 t and 2 t + 1, from each lane's share of column g.
-__device__ __forceinline__ void share_sums(float sum, int lane, float (&eights)[2]) {
-  sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-  sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) eights[i] = -8.f * __shfl_sync(0xffffffffu, sum, 4 * (2 * (lane & 3) + i));
+// The weights code - 8 of two nibbles, one per half-word, at bits 0 .. 3 or (HIGH) 4 .. 7.  Set into the mantissa of 1024 a nibble makes
+// 1024 + code, or 1024 + 16 code; both steps from there are exact.
+template <bool HIGH>
+__device__ __forceinline__ uint32_t int4x2_f16(uint32_t w) {
+  const uint32_t v = (w & (HIGH ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u, c = HIGH ? 0xD480D480u : 0xE408E408u, sixteenth = 0x2C002C00u;
+  const __half2 h = *(const __half2*)&v, bias = *(const __half2*)&c;  // -72, -1032
+  const __half2 r = HIGH ? __hfma2(h, *(const __half2*)&sixteenth, bias) : __hadd2(h, bias);
+  return *(const uint32_t*)&r;
 }
 
 // A piece of an entry's activations as the MMA's column operand: x in the columns 0 .. 3, ...
 template <int FMT>
-__device__ __forceinline__ void load_x(const FewArgs& f, const Tables& s, int entry, int col, int lane, uint32_t (&b)[Format<FMT>::kRegs],
-                                       float (&eights)[2]) {
+__device__ __forceinline__ void load_x(const FewArgs& f, const Tables& s, int entry, int col, int lane, uint32_t (&b)[Format<FMT>::kRegs]) {
   const int g = lane >> 2, t = lane & 3;
-  float sum = 0.f;
   const bool live = g < s.count[entry];
   const int token = s.rows[entry][live ? g : 0] / f.k;
   const uint16_t* row = (Format<FMT>::kBf16 ? (const uint16_t*)f.x + token * f.ldx : (const uint16_t*)f.xs + (size_t)token * f.d.H) + col;
@@ -165,9 +159,8 @@ __device__ __forceinline__ void load_x(const FewArgs& f, const Tables& s, int en
   for (int j = 0; j < Format<FMT>::kRegs / 4; ++j) {
     const uint4 u = live ? *(const uint4*)(row + element<FMT>(t, j)) : make_uint4(0, 0, 0, 0);
     b[4 * j] = u.x, b[4 * j + 1] = u.y, b[4 * j + 2] = u.z, b[4 * j + 3] = u.w;
-    order_pairs<FMT>(b + 4 * j, sum);
+    order_pairs<FMT>(b + 4 * j);
   }
-  if (Format<FMT>::kInt4) share_sums(sum, lane, eights);
 }
 
 // Four values that other blocks write, as they are now.
@@ -208,7 +201,7 @@ struct Patience {
 // two per row of the piece; inv: its inverse for the rows of the lane's MMA columns 2 t and 2 t + 1.  False if it never came.
 template <int FMT>
 __device__ __forceinline__ bool load_h(const FewArgs& f, const Tables& s, int entry, int col, int lane, uint32_t (&b)[Format<FMT>::kRegs],
-                                       float (&inv)[2], float (&eights)[2], volatile int* abort) {
+                                       float (&inv)[2], volatile int* abort) {
   const int g = lane >> 2, t = lane & 3, r = g & 3;
   const bool live = r < s.count[entry], low = g >= 4;
   const float* row = f.h + (size_t)s.rows[entry][live ? r : 0] * f.d.I + col;
@@ -225,7 +218,7 @@ __device__ __forceinline__ bool load_h(const FewArgs& f, const Tables& s, int en
     if (__all_sync(0xffffffffu, set)) break;
     if (__any_sync(0xffffffffu, p.over(abort))) return false;
   }
-  float scale = 1.f, sum = 0.f;
+  float scale = 1.f;
   if (!Format<FMT>::kBf16) {
     uint32_t m = 0;
 #pragma unroll
@@ -254,9 +247,8 @@ __device__ __forceinline__ bool load_h(const FewArgs& f, const Tables& s, int en
         b[4 * j + i] = *(const uint32_t*)&hi;
       }
     }
-    order_pairs<FMT>(b + 4 * j, sum);
+    order_pairs<FMT>(b + 4 * j);
   }
-  if (Format<FMT>::kInt4) share_sums(sum, lane, eights);
   return true;
 }
 
@@ -264,10 +256,9 @@ __device__ __forceinline__ bool load_h(const FewArgs& f, const Tables& s, int en
 __device__ __forceinline__ int four_rows(int lane) { return lane >> 3 | (lane >> 2 & 1) << 2; }
 
 // acc += a piece of 32 rows at `sm` (its scales at `sc`) times the activations.  Tile m's MMA rows g and g + 8 are gate and up
-// n0 + 8 m + g of the features, or outputs n0 + 16 m + g and 8 further on; INT4: stored rows 2 m and 2 m + 1 of the lane's four.  inv: what the two columns' activations were scaled by;
-// eights: -8 times their sums (INT4).
+// n0 + 8 m + g of the features, or outputs n0 + 16 m + g and 8 further on; INT4: stored rows 2 m and 2 m + 1 of the lane's four.  inv: what the two columns' activations were scaled by.
 template <int FMT>
-__device__ __forceinline__ void multiply(const char* sm, const char* sc, int pair, int kind, float s0, float s1, const float (&inv)[2], const float (&eights)[2], int lane,
+__device__ __forceinline__ void multiply(const char* sm, const char* sc, int pair, int kind, float s0, float s1, const float (&inv)[2], int lane,
                                          const uint4* kept, float (&acc)[2][4]) {
   const int g = lane >> 2, t = lane & 3;
   uint32_t b[Format<FMT>::kRegs];
@@ -291,23 +282,21 @@ __device__ __forceinline__ void multiply(const char* sm, const char* sc, int pai
     for (int j = 0; j < 4; ++j) {
       const uint4 u = *(const uint4*)(part[j & 1] + 512 * j);
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-      // A nibble of a half-word is, as it stands, a subnormal fp16 number: code 2^-24, the next one 16 times that, which
-      // the activations take back (order_pairs).  Where each weight became 1024 + code - 1032 the decoding took a third of the
-      // time at 16 tokens.
+      // (Codes multiplied as they are, as subnormals, and 8 times the activations' sum subtracted afterwards take 69 us for 80 at 16
+      // tokens, but leave errors that go by 8 |x| and not by |code - 8| |x|: a weight of zero did not take its activation out.)
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           const uint32_t v0 = w[2 * m] >> (8 * n), v1 = w[2 * m + 1] >> (8 * n);
-          mma(p[m], v0 & 0x000F000Fu, v1 & 0x000F000Fu, v0 & 0x00F000F0u, v1 & 0x00F000F0u, b[4 * j + 2 * n], b[4 * j + 2 * n + 1], false);
+          mma(p[m], int4x2_f16<false>(v0), int4x2_f16<false>(v1), int4x2_f16<true>(v0), int4x2_f16<true>(v1), b[4 * j + 2 * n], b[4 * j + 2 * n + 1], false);
         }
     }
     const float scale[4] = {s01.x, s01.y, s23.x, s23.y};
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)  // code 2^-24 -> code - 8
-        acc[m][i] = fmaf(fmaf(p[m][i], 16777216.f, eights[i & 1]) * scale[2 * m + i / 2], inv[i & 1], acc[m][i]);
+      for (int i = 0; i < 4; ++i) acc[m][i] = fmaf(p[m][i] * scale[2 * m + i / 2], inv[i & 1], acc[m][i]);
   } else {
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
@@ -624,9 +613,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
     const float* scales = nullptr;
     int entry = -1, have = 0;            // the steps of which entry's activations are kept,
     int line = -1, have_scales = 0;      // and of which 128 rows' scales (FP8)
-    float inv[F::kKept][2], eights[F::kKept][2], s0[F::kKept], s1[F::kKept];
+    float inv[F::kKept][2], s0[F::kKept], s1[F::kKept];
 #pragma unroll
-    for (int i = 0; i < F::kKept; ++i) inv[i][0] = inv[i][1] = 1.f, eights[i][0] = eights[i][1] = 0.f, s0[i] = s1[i] = 1.f;
+    for (int i = 0; i < F::kKept; ++i) inv[i][0] = inv[i][1] = 1.f, s0[i] = s1[i] = 1.f;
     float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     bool ok = true;
 #pragma unroll 1
@@ -651,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
       if (piece < pieces) {
         const int k = min(step, F::kKept - 1), keep = steps <= F::kKept || step < F::kKept - 1 ? 1 << k : 0;  // (past what is kept: loaded each time)
         uint4* mine = kept + k * (F::kRegs / 4 * 32);
-        float f2[2] = {1.f, 1.f}, e2[2] = {0.f, 0.f}, s2[2] = {1.f, 1.f};
+        float f2[2] = {1.f, 1.f}, s2[2] = {1.f, 1.f};
         if (FMT == MOE_FMT_FP8_B128_W8A16) {
           if (d.z / 128 != line) {
             line = d.z / 128;
@@ -669,24 +658,24 @@ __global__ void __launch_bounds__(kThreads, 1) few_experts_kernel(const __grid_c
         }
         if (!(have >> k & 1)) {
           uint32_t b[F::kRegs];
-          if (kind == 0) load_x<FMT>(f, s, entry, piece * F::kPiece, lane, b, e2);
-          else ok = load_h<FMT>(f, s, entry, piece * F::kPiece, lane, b, f2, e2, &s_abort);
+          if (kind == 0) load_x<FMT>(f, s, entry, piece * F::kPiece, lane, b);
+          else ok = load_h<FMT>(f, s, entry, piece * F::kPiece, lane, b, f2, &s_abort);
           if (!ok) break;
 #pragma unroll
           for (int i = 0; i < F::kRegs / 4; ++i) mine[32 * i] = make_uint4(b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]);
 #pragma unroll
           for (int i = 0; i < F::kKept; ++i)
-            if (k == i) inv[i][0] = f2[0], inv[i][1] = f2[1], eights[i][0] = e2[0], eights[i][1] = e2[1];
+            if (k == i) inv[i][0] = f2[0], inv[i][1] = f2[1];
           have |= keep;
         }
 #pragma unroll
         for (int i = 0; i < F::kKept; ++i)
-          if (k == i) f2[0] = inv[i][0], f2[1] = inv[i][1], e2[0] = eights[i][0], e2[1] = eights[i][1], s2[0] = s0[i], s2[1] = s1[i];
+          if (k == i) f2[0] = inv[i][0], f2[1] = inv[i][1], s2[0] = s0[i], s2[1] = s1[i];
         const int pair = F::kNvfp4 && pairs ? w & 1 : -1;
         const char* stage = ring + (team * F::kStages + slot) * kStageBytes;
         const char* sm = stage + (pair < 0 ? w : w & ~1) * F::kCodes;
         const char* sc = stage + kStagePieces * F::kCodes + w * (pair < 0 ? F::kScales : 8);
-        multiply<FMT>(sm, sc, pair, kind, s2[0], s2[1], f2, e2, lane, mine, acc);
+        multiply<FMT>(sm, sc, pair, kind, s2[0], s2[1], f2, lane, mine, acc);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[team][slot]);

@@ -208,6 +208,22 @@ def test_few_of_any_magnitude(fmt, scale):
         layer.check(layer.run(x), x, [0, 1, 3] if scale == 1e12 else slice(None))
 
 
+@pytest.mark.parametrize("T,E,k,H,I", [(1, 8, 2, 512, 256), (16, 16, 4, 2304, 1152)])
+@pytest.mark.parametrize("above", [2.0 ** 10, 2.0 ** 14, 2.0 ** 18])
+def test_few_int4_weights_of_zero_take_large_activations_out(T, E, k, H, I, above):
+    # channels far above the others that every gate and up gives a weight of zero (code 8): what they leave is an error by
+    # the weights' sizes, sum |w| |x|, to which they add nothing
+    layer = Layer("int4", T, E, k, H, I, seed=T)
+    gu = M.packed_view(layer.desc, layer.packed, M.MOE_T_GU_A)  # words [E, H / 8, 2 I] of eight channels, lowest nibble first
+    layer.x = torch.randn((T, H), generator=gen(H), device="cuda").bfloat16()
+    for c in (5, 130, H - 2):
+        gu[:, c // 8] = gu[:, c // 8] & ~(15 << 4 * (c % 8)) | 8 << 4 * (c % 8)
+        layer.x[:, c] *= above
+    layer.check(layer.run())
+    gu.fill_(-0x77777778)  # 0x88888888: weights of zero alone
+    assert (layer.run() == 0).all()
+
+
 def test_few_keeps_nan_and_infinity_in_their_rows():
     for fmt in ("fp8", "int4", "nvfp4_w4a16", "bf16"):
         layer = Layer(fmt, 5, 8, 4, 256, 256, seed=13)
