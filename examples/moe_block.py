@@ -78,7 +78,7 @@ def main(argv=None):
         x, h = step(blocks, adapters, [1] * len(slots), slots, x)
         print(f"decode {i}: rms {x.square().mean().sqrt().item():.3f}, next input {tuple(h.shape)} {h.dtype}")
     for b in blocks:
-        for w in (b.layer.workspace, b.layer.few_workspace):
+        for w in (b.layer.workspace, b.few_workspace):
             if w is not None and M.moe_get_device_error(w):
                 raise RuntimeError("device error flag set")
     if M.moe_get_adapter_error():

@@ -316,16 +316,19 @@ class MoELayer:
         self.packed = torch.empty(self.desc.bytes, dtype=torch.uint8, device=w_gate_up.device)
         moe_pack_experts(self.desc, w_gate_up.contiguous(), w_down.contiguous(), self.packed, stream)
         self.workspace = self.few_workspace = None
+        self._few_workspaces = []  # all there have been: captured graphs write to them
 
     def ensure_few_workspace(self, T: int, top_k: int):
-        """The workspace of moe_layer_few, apart from the layer's own."""
+        """The workspace of moe_layer_few, apart from the layer's own; its error word is 0 at first.  One that is replaced by a
+        larger one stays as long as the layer, for the graphs that hold its address."""
         import torch
 
         from .block import moe_layer_few_workspace_size
 
         n = moe_layer_few_workspace_size(self.desc, T, top_k)
         if self.few_workspace is None or self.few_workspace.numel() < n:
-            self.few_workspace = torch.empty(n, dtype=torch.uint8, device=self.packed.device)
+            self.few_workspace = torch.zeros(n, dtype=torch.uint8, device=self.packed.device)
+            self._few_workspaces.append(self.few_workspace)
         return self.few_workspace
 
     def ensure_workspace(self, T: int, top_k: int, host_io: bool = False):

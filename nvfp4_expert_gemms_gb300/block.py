@@ -286,7 +286,8 @@ class MoEBlock:
 
     shared: None, or the (gate/up, down) Fp8Weight pair of an always-active expert, whose output is added to m.
     few_tokens: up to so many tokens (32 at most) go through moe_layer_few, which computes the logits in fp32 (h @
-    w_router.T has w_router's type) and does not round or quantize the activations on the way.
+    w_router.T has w_router's type) and does not round or quantize the activations on the way; few_workspace is what they
+    use (None without), taken when the block is made: shared with the layer's other blocks, or larger than theirs.
     """
 
     def __init__(self, layer: MoELayer, w_router, router: Router, top_k: int, pre: Norm, post: Norm = None,
@@ -294,8 +295,8 @@ class MoEBlock:
         if not 0 <= few_tokens <= FEW_MAX_TOKENS:
             _refuse("MoEBlock", f"few_tokens is not in 0 .. {FEW_MAX_TOKENS}")
         self.shared, self.few_tokens = shared, few_tokens
-        if few_tokens:  # now, and not while a graph is captured
-            layer.ensure_few_workspace(few_tokens, top_k)
+        # now, and not while a graph is captured; and kept, whatever the layer's later blocks ask for
+        self.few_workspace = layer.ensure_few_workspace(few_tokens, top_k) if few_tokens else None
         self.layer, self.w_router, self.router, self.top_k = layer, w_router, router, top_k
         self.pre, self.post, self.router_bias, self.alpha, self.beta = pre, post, router_bias, alpha, beta
 
@@ -309,7 +310,7 @@ class MoEBlock:
         T = int(h.shape[0])
         if T <= self.few_tokens:
             m = moe_layer_few(h, self.w_router, self.router, self.layer.desc, self.layer.packed, self.top_k,
-                              self.layer.ensure_few_workspace(self.few_tokens, self.top_k), bias=self.router_bias)
+                              self.few_workspace, bias=self.router_bias)
         else:
             logits = h @ self.w_router.t()
             m = torch.empty_like(h)

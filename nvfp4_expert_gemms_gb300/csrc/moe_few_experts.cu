@@ -22,7 +22,7 @@
 //
 // What it takes (128 experts of 2048 x 768, 8 per token, with the router's kernel): FP8 20.9 us at 1 token and 82 at 16, where HBM alone would
 // take 5.6 and 57; NVFP4 42 at 4 tokens (11.5), INT4 80 at 16 (29.6).  Some 7 to 10 us are the router and the entries, 3 to 5 the waits
-// for the last h and the last y; the rest is instructions: of a piece's multiplication (some 130 to 230 per warp) and of what surrounds
+// for the last h and the last y; the rest is instructions: of a piece's multiplication (130 to 210 per warp) and of what surrounds
 // it (some 190, shared by eight warps in part), at six to nine cycles each.  HBM brings a unit of FP8 in 2800 cycles per SM and one of
 // four bits in 1500.  Hence teams, each on a unit of its own; one wait per stage, whose description comes with it (a queue of units
 // beside the stages, and scales loaded for each: 89 us for 83 at 16 tokens of FP8, 73 for 69.5 of INT4); as little as possible per stage for the

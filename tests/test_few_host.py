@@ -1,6 +1,8 @@
 """Argument checks of the layer for a few tokens and of the FP8 block products that need no GPU: the C entry points
 refuse before any CUDA call, and the binding refuses tensors that are not on a CUDA device."""
 import ctypes as C
+import gc
+import weakref
 
 import pytest
 import torch
@@ -87,3 +89,36 @@ def test_binding_refuses_host_tensors():
         with pytest.raises(M.MoEError) as e:
             call()
         assert e.value.status == 1 and "invalid argument" in str(e.value)
+
+
+@pytest.fixture
+def host_layer(monkeypatch):
+    """A layer whose buffers stand on the host and hold nothing: for what MoELayer and MoEBlock keep and choose."""
+    monkeypatch.setattr(M, "moe_pack_experts", lambda *a: None)
+    return M.MoELayer("fp8", torch.zeros((4, 256, 256), dtype=torch.bfloat16), torch.zeros((4, 256, 128), dtype=torch.bfloat16))
+
+
+def block_of(layer, **kw):
+    return M.MoEBlock(layer, torch.zeros((4, 256), dtype=torch.bfloat16), M.Router(), 2, M.Norm("rms"), **kw)
+
+
+def test_few_workspaces_outlive_their_replacement(host_layer):
+    a = block_of(host_layer, few_tokens=2)
+    first = a.few_workspace.data_ptr()
+    held = weakref.ref(host_layer.ensure_few_workspace(2, 2))
+    assert held().data_ptr() == first  # no other for no more tokens
+    b = block_of(host_layer, few_tokens=32)
+    assert b.few_workspace.numel() > a.few_workspace.numel() and a.few_workspace.data_ptr() == first
+    del a
+    gc.collect()
+    assert held() is not None  # a graph that block a captured may still write there
+    assert block_of(host_layer).few_workspace is None
+
+
+def test_few_workspace_reports_no_error_before_its_first_call(host_layer):
+    torch.use_deterministic_algorithms(True)  # fills what torch.empty gives
+    try:
+        ws = host_layer.ensure_few_workspace(4, 2)
+    finally:
+        torch.use_deterministic_algorithms(False)
+    assert ws[:256].view(torch.int32).eq(0).all()

@@ -671,6 +671,30 @@ def test_block_with_a_shared_expert_and_few_tokens():
         M.MoEBlock(layer, wr, router, k, pre, few_tokens=33)
 
 
+def test_few_graph_outlives_a_larger_block_on_the_same_layer():
+    g = gen(59)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    E, H, I, k = 16, 512, 256, 4
+    layer = M.MoELayer("fp8", (rnd(E, 2 * I, H) / H ** 0.5).bfloat16(), (rnd(E, H, I) / I ** 0.5).bfloat16())
+    wr = (rnd(E, H) / H ** 0.5).bfloat16()
+    make = lambda n: M.MoEBlock(layer, wr, M.Router(), k, M.Norm("rms"), few_tokens=n)  # noqa: E731
+    a = make(2)
+    assert M.moe_get_device_error(a.few_workspace) == 0  # polled before its first call
+    x = rnd(2, H)
+    want = a.forward(x)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = a.forward(x)
+    b = make(32)
+    n = a.few_workspace.numel()
+    assert b.few_workspace.numel() > n
+    over = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for _ in range(8)]  # whatever was given back
+    graph.replay()
+    assert torch.equal(y, want) and all((o == 7).all() for o in over)
+    assert torch.equal(b.forward(x), want) and torch.equal(a.forward(x), want)
+    assert M.moe_get_device_error(a.few_workspace) == M.moe_get_device_error(b.few_workspace) == 0
+
+
 def test_example_runs_with_few_tokens():
     sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
     import moe_block
