@@ -308,7 +308,7 @@ class MoEBlock:
         if h is None:
             h = moe_block_enter(x, self.pre, dtype=torch.bfloat16)
         T = int(h.shape[0])
-        if T <= self.few_tokens:
+        if 0 < T <= self.few_tokens:
             m = moe_layer_few(h, self.w_router, self.router, self.layer.desc, self.layer.packed, self.top_k,
                               self.few_workspace, bias=self.router_bias)
         else:

@@ -122,3 +122,16 @@ def test_few_workspace_reports_no_error_before_its_first_call(host_layer):
     finally:
         torch.use_deterministic_algorithms(False)
     assert ws[:256].view(torch.int32).eq(0).all()
+
+
+@pytest.mark.parametrize("few_tokens", [0, 8])
+def test_block_sends_no_tokens_the_way_of_many(host_layer, monkeypatch, few_tokens):
+    # w_router may be any view there, of which the operator for few tokens takes whole aligned rows alone
+    blk = block_of(host_layer, few_tokens=few_tokens)
+    blk.w_router = torch.zeros((256, 4), dtype=torch.bfloat16).t()
+    went = []
+    monkeypatch.setattr(block, "moe_layer_few", lambda *a, **k: went.append("few"))
+    monkeypatch.setattr(block, "moe_layer_forward_scored", lambda *a, **k: went.append("many"))
+    monkeypatch.setattr(block, "moe_block_leave", lambda x, m, **k: m)
+    assert blk.forward(torch.zeros((0, 256)), h=torch.zeros((0, 256), dtype=torch.bfloat16)).shape == (0, 256)
+    assert went == ["many"]

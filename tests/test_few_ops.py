@@ -671,6 +671,13 @@ def test_block_with_a_shared_expert_and_few_tokens():
         M.MoEBlock(layer, wr, router, k, pre, few_tokens=33)
 
 
+@pytest.mark.parametrize("few_tokens", [0, 8])
+def test_block_of_no_tokens(few_tokens):
+    layer = M.MoELayer("fp8", torch.zeros((4, 256, 256), dtype=torch.bfloat16, device="cuda"), torch.zeros((4, 256, 128), dtype=torch.bfloat16, device="cuda"))
+    blk = M.MoEBlock(layer, torch.zeros((256, 4), dtype=torch.bfloat16, device="cuda").t(), M.Router(), 2, M.Norm("rms"), few_tokens=few_tokens)
+    assert blk.forward(torch.zeros((0, 256), device="cuda")).shape == (0, 256)
+
+
 def test_few_graph_outlives_a_larger_block_on_the_same_layer():
     g = gen(59)
     rnd = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
