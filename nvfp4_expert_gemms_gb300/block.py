@@ -285,9 +285,10 @@ class MoEBlock:
         out = alpha x + beta g(gate) post(m);  y = next(out)   (the following block's h)
 
     shared: None, or the (gate/up, down) Fp8Weight pair of an always-active expert, whose output is added to m.
-    few_tokens: up to so many tokens (32 at most) go through moe_layer_few, which computes the logits in fp32 (h @
-    w_router.T has w_router's type) and does not round or quantize the activations on the way; few_workspace is what they
-    use (None without), taken when the block is made: shared with the layer's other blocks, or larger than theirs.
+    w_router: bf16, fp16 or fp32; the logits have its type, or fp32 where h's and its are different 16-bit ones.
+    few_tokens: up to so many tokens (32 at most) go through moe_layer_few, whose logits are fp32 and which does not round or
+    quantize the activations on the way; few_workspace is what they use (None without), taken when the block is made: shared
+    with the layer's other blocks, or larger than theirs.
     """
 
     def __init__(self, layer: MoELayer, w_router, router: Router, top_k: int, pre: Norm, post: Norm = None,
@@ -312,7 +313,8 @@ class MoEBlock:
             m = moe_layer_few(h, self.w_router, self.router, self.layer.desc, self.layer.packed, self.top_k,
                               self.few_workspace, bias=self.router_bias)
         else:
-            logits = h @ self.w_router.t()
+            t = torch.promote_types(h.dtype, self.w_router.dtype)
+            logits = h.to(t) @ self.w_router.to(t).t()
             m = torch.empty_like(h)
             ws = self.layer.ensure_workspace(T, self.top_k)
             moe_layer_forward_scored(h, logits, self.router, self.layer.desc, self.layer.packed, self.top_k, m, ws,

@@ -135,3 +135,17 @@ def test_block_sends_no_tokens_the_way_of_many(host_layer, monkeypatch, few_toke
     monkeypatch.setattr(block, "moe_block_leave", lambda x, m, **k: m)
     assert blk.forward(torch.zeros((0, 256)), h=torch.zeros((0, 256), dtype=torch.bfloat16)).shape == (0, 256)
     assert went == ["many"]
+
+
+@pytest.mark.parametrize("w_dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_block_multiplies_routers_of_any_type(host_layer, monkeypatch, w_dtype):
+    g = torch.Generator().manual_seed(3)
+    h = torch.randn((3, 256), generator=g).bfloat16()
+    blk = block_of(host_layer)
+    blk.w_router = torch.randn((4, 256), generator=g).to(w_dtype)
+    seen = []
+    monkeypatch.setattr(block, "moe_layer_forward_scored", lambda x, logits, *a, **k: seen.append(logits))
+    monkeypatch.setattr(block, "moe_block_leave", lambda x, m, **k: m)
+    blk.forward(torch.zeros((3, 256)), h=h)
+    want = h @ blk.w_router.t() if w_dtype == torch.bfloat16 else h.float() @ blk.w_router.float().t()
+    assert seen[0].dtype == want.dtype and torch.equal(seen[0], want)

@@ -671,6 +671,26 @@ def test_block_with_a_shared_expert_and_few_tokens():
         M.MoEBlock(layer, wr, router, k, pre, few_tokens=33)
 
 
+@pytest.mark.parametrize("w_dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_block_takes_its_router_at_any_length(w_dtype):
+    g = gen(61)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    E, H, I, k = 16, 512, 256, 4
+    layer = M.MoELayer("fp8", (rnd(E, 2 * I, H) / H ** 0.5).bfloat16(), (rnd(E, H, I) / I ** 0.5).bfloat16())
+    wr, router, pre = (rnd(E, H) / H ** 0.5).to(w_dtype), M.Router(), M.Norm("rms")
+    blk = M.MoEBlock(layer, wr, router, k, pre, few_tokens=8)
+    for T in (0, 1, 8, 9, 300):
+        x = rnd(T, H)
+        h = M.moe_block_enter(x, pre, dtype=torch.bfloat16)
+        m = torch.empty_like(h)
+        if 0 < T <= 8:
+            m = M.moe_layer_few(h, wr, router, layer.desc, layer.packed, k, blk.few_workspace)
+        else:
+            logits = h @ wr.t() if w_dtype == torch.bfloat16 else h.float() @ wr.float().t()
+            M.moe_layer_forward_scored(h, logits, router, layer.desc, layer.packed, k, m, layer.ensure_workspace(T, k))
+        assert torch.equal(blk.forward(x), M.moe_block_leave(x, m))
+
+
 @pytest.mark.parametrize("few_tokens", [0, 8])
 def test_block_of_no_tokens(few_tokens):
     layer = M.MoELayer("fp8", torch.zeros((4, 256, 256), dtype=torch.bfloat16, device="cuda"), torch.zeros((4, 256, 128), dtype=torch.bfloat16, device="cuda"))
