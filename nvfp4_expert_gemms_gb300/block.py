@@ -284,7 +284,7 @@ class MoEBlock:
         m   = experts(h, router(logits))  [+ shared(h)]  [+ adapters(h)]
         out = alpha x + beta g(gate) post(m);  y = next(out)   (the following block's h)
 
-    shared: None, or the (gate/up, down) Fp8Weight pair of an always-active expert, whose output is added to m.
+    shared: None, or the (gate/up [2 I, H], down [H, I]) Fp8Weight pair of an always-active expert, whose output is added to m.
     w_router: bf16, fp16 or fp32; the logits have its type, or fp32 where h's and its are different 16-bit ones.
     few_tokens: up to so many tokens (32 at most) go through moe_layer_few, whose logits are fp32 and which does not round or
     quantize the activations on the way; few_workspace is what they use (None without), taken when the block is made: shared
@@ -295,6 +295,12 @@ class MoEBlock:
                  router_bias=None, alpha=1.0, beta=1.0, shared=None, few_tokens=0):
         if not 0 <= few_tokens <= FEW_MAX_TOKENS:
             _refuse("MoEBlock", f"few_tokens is not in 0 .. {FEW_MAX_TOKENS}")
+        if shared is not None:
+            if not isinstance(shared, (tuple, list)) or len(shared) != 2 or not all(isinstance(w, Fp8Weight) for w in shared):
+                _refuse("MoEBlock", "shared is not a pair of Fp8Weight")
+            (N, K), (H, I) = (w.codes.shape for w in shared)
+            if N != 2 * I or K != layer.desc.H or H != layer.desc.H or any(w.codes.device != layer.packed.device for w in shared):
+                _refuse("MoEBlock", f"shared is not a [2 I, {layer.desc.H}] and a [{layer.desc.H}, I] on the layer's device")
         self.shared, self.few_tokens = shared, few_tokens
         # now, and not while a graph is captured; and kept, whatever the layer's later blocks ask for
         self.few_workspace = layer.ensure_few_workspace(few_tokens, top_k) if few_tokens else None

@@ -149,3 +149,20 @@ def test_block_multiplies_routers_of_any_type(host_layer, monkeypatch, w_dtype):
     blk.forward(torch.zeros((3, 256)), h=h)
     want = h @ blk.w_router.t() if w_dtype == torch.bfloat16 else h.float() @ blk.w_router.float().t()
     assert seen[0].dtype == want.dtype and torch.equal(seen[0], want)
+
+
+def host_weight(N, K, device="cpu"):
+    w = object.__new__(M.Fp8Weight)  # (the class takes CUDA tensors alone)
+    w.codes, w.scale_inv = torch.zeros((N, K), dtype=torch.uint8, device=device), torch.ones(((N + 127) // 128, (K + 127) // 128), device=device)
+    return w
+
+
+def test_block_refuses_a_shared_pair_when_it_is_made(host_layer):  # H = 256
+    for pair in ((host_weight(192, 256), host_weight(256, 96)), [host_weight(32, 256), host_weight(256, 16)]):
+        assert block_of(host_layer, shared=pair).shared is pair
+    up, down = host_weight(192, 256), host_weight(256, 96)
+    for bad in (up, (up,), (up, down, down), (up, None), (up.codes, down.codes), (down, up), (up, host_weight(256, 192)), (up, host_weight(128, 96)),
+                (host_weight(192, 128), down), (host_weight(190, 256), down), (up, host_weight(256, 96, "meta"))):
+        with pytest.raises(M.MoEError) as e:
+            block_of(host_layer, shared=bad)
+        assert e.value.status == 1
