@@ -468,7 +468,8 @@ moe_status_t moe_fp8_quantize(const void* x, int64_t ldx, int x_dtype, uint8_t* 
  *   p[t, n] = sum over groups g of x_scale_inv[t, g] w_scale_inv[n / 128, g] sum over k in g of qx[t, k] qw[n, k]
  *   out[t]  = act(p[t]) + base[t]     rounded once to out_dtype;  act: the identity, or (MOE_ACT_SILU_MUL)
  *             silu(p[t, f]) * p[t, N/2 + f] for f < N/2 (rows 0 .. N/2-1 of w are gates, the rest ups)
- * All sums in fp32.
+ * All sums in fp32.  A group's two scales are applied so that no product of the two alone leaves fp32's range (normal
+ * scales, or 0): only a sum that does itself gives an infinity or loses bits.
  *   x (dev): x_dtype bf16, fp16 or fp32 [T, K] (pitch ldx), which the call quantizes as moe_fp8_quantize does; or
  *   MOE_DT_E4M3 codes (16-byte aligned, ldx a multiple of 16) with x_scale_inv (dev) f32 [T, ceil(K / 128)].
  *   w (dev) E4M3 [N, K], contiguous, 16-byte aligned; w_scale_inv (dev) f32 [ceil(N / 128), ceil(K / 128)].

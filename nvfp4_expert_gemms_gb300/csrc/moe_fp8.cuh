@@ -44,6 +44,16 @@ __device__ __forceinline__ uint32_t fp8_codes2(float a, float b, float s) {
   return __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(a, s), __fmul_rn(b, s)), __NV_SATFINITE, __NV_E4M3);
 }
 
+// A group's partial sum p is multiplied with two scales, w of the weights and x of the row.  Their product alone may leave fp32's
+// normal range where p w x does not (a row near 3e38 and a weight scale of 1000: 0 times infinity where codes are zero).  w and x are
+// then on the same side of 1, and p times one and then the other stays in range as long as the result does: p is multiplied with
+// scale_before first, and with scale_after then.
+__device__ __forceinline__ bool scales_meet(float t) { return fabsf(t) >= 1.17549435e-38f && fabsf(t) <= 3.40282347e38f; }
+__device__ __forceinline__ float scale_before(float w, float x) { return scales_meet(w * x) ? 1.f : w; }
+__device__ __forceinline__ float scale_after(float w, float x) { return scales_meet(w * x) ? w * x : x; }
+// Two scales of which each is at least 2^-63 and below 2^64 meet.
+__device__ __forceinline__ bool scale_moderate(float v) { return (__float_as_uint(v) & 0x7FFFFFFFu) - 0x20000000u < 0x3F800000u; }
+
 // Eight elements as fp32; 0 past n.  WIDE: all eight, 16-byte aligned.
 template <class T, bool WIDE>
 __device__ __forceinline__ void load8(const T* p, int n, float (&v)[8]) {

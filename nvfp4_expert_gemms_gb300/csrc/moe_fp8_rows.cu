@@ -57,6 +57,10 @@ __device__ __forceinline__ float quantize_group(const T* p, int left, int t, uin
   return __fdiv_rn(1.f, s);
 }
 
+__device__ __forceinline__ float add_scaled(float p, float w, float x, float acc) {
+  return fmaf(p * scale_before(w, x), scale_after(w, x), acc);
+}
+
 // (Two passes with two blocks per SM, 64 registers a thread, spill: 9 x 2048 x 1536 pairs 5.5 us for 4.6.)
 template <bool PAIR, int PASSES>
 __global__ void __launch_bounds__(kThreads, PASSES == 1 ? 2 : 1) fp8_rows_kernel(const Fp8LinearArgs a, const bool wide) {
@@ -115,8 +119,8 @@ __global__ void __launch_bounds__(kThreads, PASSES == 1 ? 2 : 1) fp8_rows_kernel
       }
       // columns 2 t and 2 t + 1 of the MMA are rows of x that lanes 4 (2 t) and 4 (2 t + 1) quantized
       const float x0 = __shfl_sync(0xffffffffu, sx, 8 * t), x1 = __shfl_sync(0xffffffffu, sx, 8 * t + 4);
-      acc[pass][0] = fmaf(p[0], f0 * x0, acc[pass][0]), acc[pass][1] = fmaf(p[1], f0 * x1, acc[pass][1]);
-      acc[pass][2] = fmaf(p[2], f1 * x0, acc[pass][2]), acc[pass][3] = fmaf(p[3], f1 * x1, acc[pass][3]);
+      acc[pass][0] = add_scaled(p[0], f0, x0, acc[pass][0]), acc[pass][1] = add_scaled(p[1], f0, x1, acc[pass][1]);
+      acc[pass][2] = add_scaled(p[2], f1, x0, acc[pass][2]), acc[pass][3] = add_scaled(p[3], f1, x1, acc[pass][3]);
     }
   }
 #pragma unroll

@@ -3,8 +3,8 @@
 // Both operands go to the tensor cores as stored codes (kind::f8f6f4, M = 128 rows of x, N = BN weight rows, K = 32; TMA tiles in
 // the 128-byte swizzle).  Their scales change every 128 columns, so each group's partial sum goes to a tensor-memory
 // buffer of its own, and promoting warps read it back, scale it and add it to sums that they keep in registers, while the MMAs
-// of the next groups fill the other buffers.  16384 x 2048 x 4096 takes 143 us (1.91 PFLOP/s), x 4096 258 us (2.13 PFLOP/s): half of
-// what the MMAs alone would take is the promotion, 64 sums a thread and group, and the L2's rate (48 KB per 8.4 MFLOP).
+// of the next groups fill the other buffers.  16384 x 2048 x 4096 takes 147 us (1.87 PFLOP/s), x 4096 267 us (2.06 PFLOP/s), the tensor
+// pipe busy for 41% of it: what paces the tiles is the promotion, 64 sums a thread and group, and the L2's rate (48 KB per 8.4 MFLOP).
 #include <cudaTypedefs.h>
 
 #include "moe_dec.cuh"
@@ -45,6 +45,13 @@ struct Args {
   bool boxed;  // outputs leave (and base comes) by TMA, 32 rows of a warp's columns at a time
 };
 
+// 32 lanes x 8 columns
+__device__ __forceinline__ void tmem_ld_32x8(uint32_t taddr, uint32_t* v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(taddr)
+               : "memory");
+}
 // Two sums at once: a += p f, b += q g.
 __device__ __forceinline__ void fma2(float& a, float& b, uint32_t p, uint32_t q, float f, float g) {
   asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n mov.b64 z, {%4, %5};\n fma.rn.f32x2 x, y, z, x;\n"
@@ -151,7 +158,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
   extern __shared__ __align__(1024) char smem_raw[];
   char* ring = (char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   __shared__ uint64_t full[kStages], empty[kStages], pfull[kBufs], pempty[kBufs], bfull[S::kPromote], drain;
-  __shared__ float s_x[kBufs][kM], s_w[kBufs][4];  // a group's scales: of the rows; of the blocks of weight rows
+  __shared__ float s_x[kBufs][kM], s_w[kBufs][4];  // a group's scales: of the rows; of the blocks of weight rows, and 1 where some may not meet
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const Fp8LinearArgs& l = a.l;
@@ -271,7 +278,9 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
         if (!ok) break;
 #pragma unroll
         for (int j = 0; j < 4; ++j) s_x[b][32 * j + lane] = sx[j];
-        if (lane < 3) s_w[b][lane] = sw;
+        const bool moderate = scale_moderate(sx[0]) && scale_moderate(sx[1]) && scale_moderate(sx[2]) && scale_moderate(sx[3]) && (lane >= 3 || scale_moderate(sw));
+        const bool apart = !__all_sync(0xffffffffu, moderate);
+        if (lane < 4) s_w[b][lane] = lane < 3 ? sw : apart ? 1.f : 0.f;
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[b]);
         if (g + 1 < g1) load(g + 1);
@@ -324,21 +333,55 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 256 ? 1 : 2) fp8_ti
           if (PAIR) wb = s_w[b][block];
           if (CROSS) wc = s_w[b][min(block + 1, 2)];
         }
-        const float fa = s * wa, fb = PAIR ? s * wb : fa, fc = CROSS ? s * wc : fb;
         const uint32_t at = taddr(tmem, 32 * q, b * BN);
+        auto columns = [&](int h) { return at + (PAIR ? (h < 32 ? h : BN / 2 + h - 32) + 32 * grp : h + 64 * grp); };
+        auto release = [&]() {
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&pempty[b]);
+        };
         constexpr int kAtOnce = CROSS ? 16 : 32;  // sums per wait, as registers allow (16384 x 2048 x 4096: 32 143 us, 16 148; CROSS: 16 45, 32 59)
+        uint32_t p[kAtOnce];
+        if (!S::kScaleWarp) {  // (the scales come meanwhile)
+#pragma unroll
+          for (int j = 0; j < kAtOnce; j += 16) tmem_ld_32x16(columns(0) + j, p + j);
+        }
+        const bool apart = S::kScaleWarp ? s_w[b][3] != 0.f
+                                         : !__all_sync(0xffffffffu, scale_moderate(s) && scale_moderate(wa) && (!PAIR || scale_moderate(wb)) &&
+                                                                        (!CROSS || cross >= 32 || scale_moderate(wc)));
+        // Rare, and eight sums at a time, so that it asks for no more registers than the other way.  (To have it at all takes 147 us for 143 at
+        // 16384 x 2048 x 4096.)
+        if (apart) {
+          if (!S::kScaleWarp) tmem_ld_wait();
+#pragma unroll
+          for (int h = 0; h < 64; h += 8) {
+            const bool ups = PAIR && h >= 32;
+            tmem_ld_32x8(columns(h), p);
+            if (S::kScaleWarp) {  // (read again, for the same reason)
+              s = ((volatile float*)s_x[b])[32 * q + lane], wa = ((volatile float*)s_w[b])[PAIR && !ups ? 0 : block];
+              if (CROSS && ups) wc = ((volatile float*)s_w[b])[min(block + 1, 2)];
+            } else if (ups) {
+              wa = wb;
+            }
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float w = CROSS && ups && h - 32 + j >= cross ? wc : wa;
+              acc[h + j] = fmaf(__uint_as_float(p[j]) * scale_before(w, s), scale_after(w, s), acc[h + j]);
+            }
+          }
+          release();
+          continue;
+        }
+        const float fa = s * wa, fb = PAIR ? s * wb : fa, fc = CROSS ? s * wc : fb;
 #pragma unroll
         for (int h = 0; h < 64; h += kAtOnce) {
-          uint32_t p[kAtOnce];
-          const int from = PAIR ? (h < 32 ? h : BN / 2 + h - 32) + 32 * grp : h + 64 * grp;
+          if (h > 0 || S::kScaleWarp) {
 #pragma unroll
-          for (int j = 0; j < kAtOnce; j += 16) tmem_ld_32x16(at + from + j, p + j);
-          tmem_ld_wait();
-          if (h + kAtOnce == 64) {
-            fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&pempty[b]);
+            for (int j = 0; j < kAtOnce; j += 16) tmem_ld_32x16(columns(h) + j, p + j);
           }
+          tmem_ld_wait();
+          if (h + kAtOnce == 64) release();
           const float f = PAIR && h >= 32 ? fb : fa;
           if (CROSS && h >= 32 && cross < 32) {
 #pragma unroll

@@ -542,6 +542,43 @@ def test_linear_of_the_smallest_largest_and_empty_groups():
         assert (out[:, 7] == 0).all() and (out[1] == 0).all() and out[2, 0].isinf()  # 3e38 448 128 is past fp32
 
 
+@pytest.mark.parametrize("T,K,N,act", [(1, 256, 200, "none"), (5, 272, 256, "silu_mul"), (12, 256, 200, "silu_mul"), (16, 2048, 130, "none"), (24, 256, 200, "none"),
+                                       (24, 2048, 200, "silu_mul"), (40, 2048, 3200, "none"), (150, 256, 256, "silu_mul"), (150, 256, 200, "silu_mul"),
+                                       (600, 256, 4096, "none"), (600, 256, 4096, "silu_mul"), (700, 256, 3998, "silu_mul")])
+@pytest.mark.parametrize("turn", range(4))
+def test_linear_scales_whose_product_alone_leaves_the_range(T, K, N, act, turn):
+    # rows and blocks of weight rows with scales from 2^-120 to 2^120, in every combination; codes of zero among them.  Sums that
+    # fp32 holds come out within their bound, zeros as zeros
+    g = gen(T + N + turn)
+    G = (K + 127) // 128
+    codes = lambda *s: (torch.randn(s, generator=g, device="cuda") * 100).clamp(-448, 448).to(torch.float8_e4m3fn)  # noqa: E731
+    near = lambda *s: 0.75 + 0.25 * torch.rand(s, generator=g, device="cuda")  # noqa: E731
+    x, w = codes(T, K), codes(N, K)
+    x[T // 2] = 0.0
+    w[3], w[N // 2 + 5] = 0.0, 0.0
+    of_row = torch.tensor([1.0, 2.0 ** 100, 2.0 ** -100, 2.0 ** 120, 2.0 ** -120, 1e30, 2.0 ** -45, 0.0], device="cuda")
+    of_block = torch.tensor([2.0 ** 100, 2.0 ** -100, 1e3, 2.0 ** -70, 1.0, 2.0 ** 70, 2.0 ** -120, 0.0], device="cuda")
+    xs = near(T, G) * of_row[(torch.arange(T, device="cuda") * 5 + turn) % 8][:, None]
+    ws = near((N + 127) // 128, G) * of_block[(torch.arange((N + 127) // 128, device="cuda") * 3 + 2 * turn) % 8][:, None]
+    weight = M.Fp8Weight(w, ws)
+    out = M.moe_fp8_linear(x, weight, x_scale=xs, act=act, dtype=torch.float32).double()
+    a = x.double() * xs.double().repeat_interleave(128, 1)[:, :K]
+    b = w.double() * ws.double().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+    y, size = a @ b.t(), a.abs() @ b.abs().t()
+    e = size * (K + 16) * 2.0 ** -23 + 2.0 ** -149 * (G + 1)  # a subnormal sum is rounded to 2^-150 at each step
+    held = size < 2.0 ** 126
+    if act == "silu_mul":
+        n = N // 2
+        v, u, ev, eu = y[:, :n], y[:, n:], e[:, :n], e[:, n:]
+        sv = v * torch.sigmoid(v)
+        held = held[:, :n] & held[:, n:]
+        # past e^88.7 the exponential is an infinity and silu 0, 88.8 e^-88.7 < 3e-37 at most
+        y, e = sv * u, 1.1 * ev * (u.abs() + eu) + sv.abs() * eu + 16 * U * (sv * u).abs() + 3e-37 * u.abs() + 2.0 ** -148 * (1.0 + u.abs())
+        held &= y.abs() + e < 2.0 ** 126
+    assert held.any() and (out[held] - y[held]).abs().le((e + U * (y.abs() + e))[held]).all()
+    assert (out[(size[:, :out.shape[1]] == 0) & held] == 0).all()
+
+
 def test_operators_beside_each_other():
     # the layer for few tokens, products and the layer for many, each on a stream of its own, again and again
     a = Layer("int4", 32, 256, 8, 512, 256, seed=43)
