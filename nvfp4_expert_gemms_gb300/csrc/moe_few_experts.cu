@@ -237,12 +237,16 @@ __device__ __forceinline__ bool load_h(const FewArgs& f, const Tables& s, int en
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float x = live ? __uint_as_float(w[2 * i]) * scale : 0.f, y = live ? __uint_as_float(w[2 * i + 1]) * scale : 0.f;
+      // (an infinity is the largest number and, left over, an infinity: infinity less infinity would be NaN.  So are the fp32 numbers that
+      // bf16 rounds to infinity the largest and a rest.)
+      constexpr float kMost = Format<FMT>::kBf16 ? 3.38953139e38f : 65504.f;
+      const float xm = fminf(fmaxf(x, -kMost), kMost), ym = fminf(fmaxf(y, -kMost), kMost);
       if (Format<FMT>::kBf16) {
-        __nv_bfloat162 hi = __floats2bfloat162_rn(x, y);
+        __nv_bfloat162 hi = __floats2bfloat162_rn(xm, ym);
         if (low) hi = __floats2bfloat162_rn(x - __low2float(hi), y - __high2float(hi));
         b[4 * j + i] = *(const uint32_t*)&hi;
       } else {
-        __half2 hi = __floats2half2_rn(x, y);
+        __half2 hi = __floats2half2_rn(xm, ym);
         if (low) hi = __floats2half2_rn(x - __low2float(hi), y - __high2float(hi));
         b[4 * j + i] = *(const uint32_t*)&hi;
       }

@@ -237,6 +237,42 @@ def test_few_keeps_nan_and_infinity_in_their_rows():
         assert M.moe_get_device_error(layer.ws) == 0
 
 
+def large_h(fmt, gate, up, down, x):
+    """A layer of one expert, 128 x 128, of which the seventh feature alone has ups, and its output."""
+    layer = Layer(fmt, x.shape[0], 1, 1, 128, 128)
+    wgu, g = torch.zeros((1, 256, 128), device="cuda"), gen(67)
+    wgu[0, :128] = torch.randn((128, 128), generator=g, device="cuda")
+    wgu[0, 7], wgu[0, 128 + 7] = gate, up
+    M.moe_pack_experts(layer.desc, wgu.bfloat16(), down[None].bfloat16(), layer.packed)
+    layer.x = x
+    return layer, layer.run()
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "int4", "nvfp4_w4a16", "bf16"])
+def test_few_h_past_fp32_gives_infinities(fmt):
+    # silu(gate) up of row 0 is of the order of 1e50: an infinity times the down weight, with its sign, NaN where that is zero
+    x = torch.randn((2, 128), generator=gen(71), device="cuda").bfloat16()
+    ones, down = torch.ones(128, device="cuda"), torch.randn((128, 128), generator=gen(73), device="cuda")
+    down[5, 7] = 0.0
+    _, clean = large_h(fmt, ones, ones, down, x)
+    x[0] = 1e25
+    layer, out = large_h(fmt, ones, ones, down, x)
+    w = weights(layer.desc, layer.packed, 1, 0)[:, 7]
+    assert w[5] == 0.0 and torch.equal(out[0].isnan(), w == 0.0)
+    assert torch.equal(out[0].float()[w != 0.0], torch.full_like(w, float("inf"), dtype=torch.float32)[w != 0.0] * w.float().sign()[w != 0.0])
+    assert torch.equal(out[1], clean[1])
+
+
+def test_few_h_that_bf16_would_round_to_infinity():
+    # gate = x_0, up = x_1, and (1 + 2^-7) (1 - 2^-7) 2^128 is a number of fp32 above the largest of bf16
+    e0, e1 = torch.eye(128, device="cuda")[:2]
+    down = torch.full((128, 128), 2.0 ** -20, device="cuda")
+    x = torch.zeros((1, 128), dtype=torch.bfloat16, device="cuda")
+    x[0, 0], x[0, 1] = (1 + 2.0 ** -7) * 2.0 ** 63, (1 - 2.0 ** -7) * 2.0 ** 65
+    _, out = large_h("bf16", e0, e1, down, x)
+    assert (out == 2.0 ** 108).all()  # (1 - 2^-14) 2^108, rounded
+
+
 def test_few_pitches_aliases_streams_and_repeats():
     layer = Layer("fp8", 7, 16, 4, 512, 256, seed=17)
     want = layer.run()
