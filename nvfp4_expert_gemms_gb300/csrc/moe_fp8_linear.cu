@@ -48,8 +48,9 @@ extern "C" moe_status_t moe_fp8_linear(const void* x, int64_t ldx, int x_dtype, 
   const cudaStream_t s = (cudaStream_t)stream;
   Fp8LinearArgs a = {x, ldx, x_dtype, x_scale_inv, w, w_scale_inv, base, ldb, out, ldo, out_dtype, T, K, N, groups, out_n};
   // Few rows in one launch that quantizes on the way.  Its blocks read all of x for 16 weight rows each, which past eight rows and some
-  // 2^24 weights costs more than the tiles' second launch (us, one launch and tiles: 8 x 4096 x 14336 18.5 and 20.3, 9 x 2048 x 4096 8.2
-  // and 11.2, 9 x 2048 x 8192 13.9 and 11.5, 16 x 4096 x 4096 13.8 and 14.7, 16 x 4096 x 14336 37.0 and 20.5).
+  // 2^24 weights costs more than the tiles' second launch (us, one launch and tiles: 8 x 4096 x 14336 18.2 and 20.3, 16 x 2048 x 4096 7.4
+  // and 11.2, 16 x 4096 x 3584 13.9 and 14.7, 16 x 4096 x 14336 37.0 and 20.6; at 2^24 itself it goes by the shape, 16 x 4096 x 4096 14.0 and
+  // 14.8, 16 x 2048 x 8192 14.4 and 11.9).
   if (T <= kFp8Rows / 2 || (T <= kFp8Rows && (int64_t)N * K < 1 << 24)) return launch_fp8_rows(a, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   if (!coded) {
     uint8_t* q = (uint8_t*)workspace;

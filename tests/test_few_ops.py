@@ -525,6 +525,43 @@ def test_linear_types(T, x_type, out_type, act, with_base):
         assert torch.equal(M.moe_fp8_linear(x, w, x_scale=xs, act=act, base=b, out=b), got)
 
 
+@pytest.mark.parametrize("T", [8, 9, 16, 17])
+@pytest.mark.parametrize("K,N,act", [(4096, 4096, "none"), (4096, 4097, "none"), (4096, 14336, "none"), (4096, 14336, "silu_mul")])
+def test_linear_rows_of_large_matrices(T, K, N, act):
+    # both sides of 8 and 16 rows and of 2^24 weights, where one kernel takes over from another
+    g = gen(T + N)
+    x = torch.randn((T, K), generator=g, device="cuda").bfloat16()
+    w = make_weight(N, K, g)
+    out = M.moe_fp8_linear(x, w, act=act)
+    check_linear(out, x, w, act)
+    for t in (0, T - 1):  # and a row comes out of them alike, but for the order of its sums
+        check_linear(M.moe_fp8_linear(x[t:t + 1], w, act=act), x[t:t + 1], w, act)
+
+
+@pytest.mark.parametrize("T", [24, 100])
+@pytest.mark.parametrize("K,N,act", [(2048, 200, "silu_mul"), (2048, 2742, "silu_mul"), (1040, 256, "silu_mul"), (2048, 2752, "silu_mul"), (2048, 1111, "none"),
+                                     (4112, 64, "none")])
+@pytest.mark.parametrize("out_type", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("with_base", [False, True])
+def test_linear_of_long_rows_in_clusters(T, K, N, act, out_type, with_base):
+    # eight groups of columns and more, in few tiles: a cluster's blocks share the groups, two or four to a tile; ups that cross a
+    # block of 128 rows among them (100 and 1371 gates)
+    g = gen(T + K + N)
+    n = N // 2 if act == "silu_mul" else N
+    x = torch.randn((T, K), generator=g, device="cuda").bfloat16()
+    w = make_weight(N, K, g)
+    base = torch.randn((T, n + 3), generator=g, device="cuda").to(DT[out_type])[:, 2:2 + n] if with_base else None
+    out = torch.full((T + 1, n + 5), 7.0, dtype=DT[out_type], device="cuda")
+    M.moe_fp8_linear(x, w, act=act, base=base, out=out[:T, 1:1 + n])
+    assert (out[:, :1] == 7.0).all() and (out[:, 1 + n:] == 7.0).all() and (out[T:] == 7.0).all()
+    check_linear(out[:T, 1:1 + n], x, w, act, base)
+    assert torch.equal(M.moe_fp8_linear(x, w, act=act, base=base, dtype=DT[out_type]), out[:T, 1:1 + n])
+    if with_base:
+        b = base.clone()
+        assert torch.equal(M.moe_fp8_linear(x, w, act=act, base=b, out=b), out[:T, 1:1 + n])
+    assert M.moe_get_fp8_linear_error() == 0
+
+
 @pytest.mark.parametrize("T,K,N,act", [(1, 2048, 4096, "none"), (96, 2048, 3200, "silu_mul"), (1237, 1504, 1111, "none"), (2500, 1536, 2048, "none"),
                                        (4000, 1024, 2304, "silu_mul")])
 def test_linear_at_full_size(T, K, N, act):
