@@ -305,6 +305,12 @@ def packed_view(desc: PackedDesc, packed, which: int):
     return raw.view(E, N, K // 2) if which in (MOE_T_GU_A, MOE_T_D_A) else raw.view(E, N, K // 16)
 
 
+def _capturing() -> bool:
+    import torch
+
+    return torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing()
+
+
 class MoELayer:
     """Convenience holder: packed experts of one layer plus a reusable workspace."""
 
@@ -317,6 +323,7 @@ class MoELayer:
         moe_pack_experts(self.desc, w_gate_up.contiguous(), w_down.contiguous(), self.packed, stream)
         self.workspace = self.few_workspace = None
         self._few_workspaces = []  # all there have been: captured graphs write to them
+        self._captured_workspaces = []  # the layer's own (which may be large) that were handed out during a capture
 
     def ensure_few_workspace(self, T: int, top_k: int):
         """The workspace of moe_layer_few, apart from the layer's own; its error word is 0 at first.  One that is replaced by a
@@ -332,11 +339,15 @@ class MoELayer:
         return self.few_workspace
 
     def ensure_workspace(self, T: int, top_k: int, host_io: bool = False):
+        """The layer's workspace, replaced by a larger one where T asks for it.  One that was handed out while a graph was captured
+        stays as long as the layer, for the graph that holds its address."""
         import torch
 
         n = (moe_workspace_size_host_io if host_io else moe_workspace_size)(self.desc, T, top_k)
         if self.workspace is None or self.workspace.numel() < n:
             self.workspace = torch.empty(n, dtype=torch.uint8, device=self.packed.device)
+        if _capturing() and not any(w is self.workspace for w in self._captured_workspaces):
+            self._captured_workspaces.append(self.workspace)
         return self.workspace
 
     def forward(self, x, router_logits, top_k: int, out=None, stream=None):

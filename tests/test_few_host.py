@@ -115,6 +115,17 @@ def test_few_workspaces_outlive_their_replacement(host_layer):
     assert block_of(host_layer).few_workspace is None
 
 
+def test_captured_workspaces_outlive_their_replacement(host_layer, monkeypatch):
+    eager = weakref.ref(host_layer.ensure_workspace(4, 2))
+    monkeypatch.setattr(M, "_capturing", lambda: True, raising=False)
+    captured = weakref.ref(host_layer.ensure_workspace(64, 2))
+    assert host_layer.ensure_workspace(64, 2) is captured() and len(host_layer._captured_workspaces) == 1
+    monkeypatch.setattr(M, "_capturing", lambda: False, raising=False)
+    host_layer.ensure_workspace(512, 2)
+    gc.collect()
+    assert eager() is None and captured() is not None and captured() is not host_layer.workspace
+
+
 def test_few_workspace_reports_no_error_before_its_first_call(host_layer):
     torch.use_deterministic_algorithms(True)  # fills what torch.empty gives
     try:

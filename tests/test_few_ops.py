@@ -832,6 +832,26 @@ def test_few_graph_outlives_a_larger_block_on_the_same_layer():
     assert M.moe_get_device_error(a.few_workspace) == M.moe_get_device_error(b.few_workspace) == 0
 
 
+def test_graph_outlives_a_larger_batch_on_the_same_layer():
+    g = gen(79)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    E, H, I, k = 16, 512, 256, 4
+    layer = M.MoELayer("fp8", (rnd(E, 2 * I, H) / H ** 0.5).bfloat16(), (rnd(E, H, I) / I ** 0.5).bfloat16())
+    blk = M.MoEBlock(layer, (rnd(E, H) / H ** 0.5).bfloat16(), M.Router(), k, M.Norm("rms"))
+    x, many = rnd(40, H), rnd(900, H)
+    want = blk.forward(x)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = blk.forward(x)
+    n = layer.workspace.numel()
+    blk.forward(many)
+    assert layer.workspace.numel() > n
+    over = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for _ in range(4)]  # whatever was given back
+    graph.replay()
+    assert torch.equal(y, want) and all((o == 7).all() for o in over)
+    assert torch.equal(blk.forward(x), want)
+
+
 def test_example_runs_with_few_tokens():
     sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
     import moe_block
