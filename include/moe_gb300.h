@@ -274,6 +274,11 @@ moe_status_t moe_debug_quant_act_fp8(const void* x, int T, int H, uint8_t* codes
  * MOE_ERR_INVALID_ARG for a null or misaligned workspace. */
 moe_status_t moe_debug_wait_timeout(void* workspace, moe_stream_t stream);
 
+/* The same for the waits of moe_layer_few: makes this thread's next call of it that enqueues kernels leave the gate/up products out, so
+ * that the waits for their results run out.  out is then not written in full, and the workspace's error word reports
+ * MOE_ERR_DEVICE_TIMEOUT.  The call copies from pageable host memory: not during a capture. */
+void moe_debug_few_timeout(void);
+
 /* ---- routing without any caller workspace ----------------------------------------------- */
 
 /* The pages have no counterpart to this entry point; it exists for callers that cannot obtain

@@ -33,7 +33,7 @@ EXPORTS = ("moe_packed_size", "moe_pack_experts", "moe_workspace_size", "moe_lay
            "moe_workspace_size_host_io", "moe_layer_forward_host", "moe_get_device_error", "moe_status_string",
            "moe_debug_route", "moe_debug_dequant", "moe_debug_quant_act", "moe_kernel_launch_count",
            "moe_time_next_step", "moe_layer_forward_static_act", "moe_calibrate_act_scales",
-           "moe_debug_quant_act_static", "moe_debug_quant_act_fp8", "moe_debug_wait_timeout", "moe_block_enter",
+           "moe_debug_quant_act_static", "moe_debug_quant_act_fp8", "moe_debug_wait_timeout", "moe_debug_few_timeout", "moe_block_enter",
            "moe_block_leave", "moe_route_scored", "moe_layer_forward_scored", "moe_adapters_add", "moe_get_adapter_error",
            "moe_layer_few_workspace_size", "moe_layer_few", "moe_fp8_quantize", "moe_fp8_linear_workspace_size",
            "moe_fp8_linear", "moe_get_fp8_linear_error")
@@ -98,6 +98,7 @@ def lib() -> C.CDLL:
         L.moe_debug_quant_act_static.argtypes = [P, I32, I32, P, P, P, P]
         L.moe_debug_quant_act_fp8.argtypes = [P, I32, I32, P, P, P]
         L.moe_debug_wait_timeout.argtypes = [P, P]
+        L.moe_debug_few_timeout.argtypes, L.moe_debug_few_timeout.restype = [], None
         L.moe_layer_forward_static_act.argtypes = [P, P, I32, PD, P, I32, P, P, P, SZ, P]
         L.moe_calibrate_act_scales.argtypes = [P, P, I32, PD, P, I32, P, P, SZ, P]
         L.moe_kernel_launch_count.restype = C.c_uint64
@@ -264,6 +265,12 @@ def moe_debug_wait_timeout(workspace, stream=None):
     """Enqueue a device wait that runs out (about a second) and records MOE_ERR_DEVICE_TIMEOUT in
     the workspace's error word; read it with moe_get_device_error."""
     _check(lib().moe_debug_wait_timeout(_ptr(workspace), _stream(stream)), "moe_debug_wait_timeout")
+
+
+def moe_debug_few_timeout():
+    """This thread's next moe_layer_few (of one token or more) leaves its gate/up products out: its waits run out after about a
+    second and its workspace reports MOE_ERR_DEVICE_TIMEOUT."""
+    lib().moe_debug_few_timeout()
 
 
 def moe_debug_quant_act(x, stream=None):

@@ -214,6 +214,10 @@ cudaError_t launch_few_router(const FewArgs& a, size_t fill_bytes, cudaStream_t 
 
 using namespace moe;
 
+static thread_local bool t_lose_h = false;
+
+extern "C" void moe_debug_few_timeout(void) { t_lose_h = true; }
+
 extern "C" moe_status_t moe_layer_few_workspace_size(const moe_packed_desc_t* desc, int T, int top_k, size_t* bytes) {
   if (!bytes || !packed_desc_ok(desc) || T < 0 || T > kFewTokens || top_k < 1 || top_k > kMaxTopK || top_k > desc->E)
     return MOE_ERR_INVALID_ARG;
@@ -259,7 +263,9 @@ extern "C" moe_status_t moe_layer_few(const void* x, int64_t ldx, const void* w_
   a.h = (float*)(ws + L.h);
   a.y = (float*)(ws + L.y);
   a.router = {*router, workspace, E, MOE_DT_F32, bias};  // (the logits stay in shared memory)
+  const bool lose_h = t_lose_h;
+  t_lose_h = false;
   cudaError_t e = launch_few_router(a, L.total - L.h, (cudaStream_t)stream);
-  if (e == cudaSuccess) e = launch_few_experts(a, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = launch_few_experts(a, lose_h, (cudaStream_t)stream);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

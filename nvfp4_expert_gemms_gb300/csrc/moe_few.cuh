@@ -51,7 +51,8 @@ struct FewArgs {
   float* y;          // [T k, H]: weighted rows
 };
 cudaError_t launch_few_router(const FewArgs& a, size_t fill_bytes, cudaStream_t s);
-cudaError_t launch_few_experts(const FewArgs& a, cudaStream_t s);
+// lose_h: gate/up products are left out and the waits for them run out (moe_debug_few_timeout).
+cudaError_t launch_few_experts(const FewArgs& a, bool lose_h, cudaStream_t s);
 
 __host__ __device__ inline bool few_scales_x(int fmt) { return fmt != MOE_FMT_BF16; }
 

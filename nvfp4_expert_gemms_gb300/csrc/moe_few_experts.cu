@@ -825,7 +825,7 @@ bool make_cut(Args& a, int kind) {
 }
 
 template <int FMT>
-cudaError_t launch(const FewArgs& f, cudaStream_t s) {
+cudaError_t launch(const FewArgs& f, bool lose_h, cudaStream_t s) {
   static SmemOptIn opt_in;
   if (const cudaError_t e = opt_in(few_experts_kernel<FMT>, Format<FMT>::kSmem); e != cudaSuccess) return e;
   Args a;
@@ -833,23 +833,28 @@ cudaError_t launch(const FewArgs& f, cudaStream_t s) {
   if (!make_cut<FMT>(a, 0) || !make_cut<FMT>(a, 1)) return cudaErrorInvalidValue;
   const long R = (long)f.T * f.k, active = R < f.d.E ? R : f.d.E, sms = tc_num_sms();
   const long most = active * (a.cut[0].units > a.cut[1].units ? a.cut[0].units : a.cut[1].units);  // (a team may go without)
+  const unsigned blocks = (unsigned)(most < sms ? most : sms);
+  if (lose_h) {  // the gate/up tickets as given out already
+    const int tickets = kTeams * (int)blocks;
+    if (const cudaError_t e = cudaMemcpyAsync(f.status + 1, &tickets, sizeof(tickets), cudaMemcpyHostToDevice, s); e != cudaSuccess) return e;
+  }
   note_launches(1);
-  return launch_pdl(few_experts_kernel<FMT>, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads), Format<FMT>::kSmem, s, a);
+  return launch_pdl(few_experts_kernel<FMT>, dim3(blocks), dim3(kThreads), Format<FMT>::kSmem, s, a);
 }
 
 }  // namespace
 
-cudaError_t launch_few_experts(const FewArgs& a, cudaStream_t s) {
+cudaError_t launch_few_experts(const FewArgs& a, bool lose_h, cudaStream_t s) {
   switch (a.d.fmt) {
     case MOE_FMT_FP8_B128_W8A16:
     case MOE_FMT_FP8_B128_W8A8:
-      return launch<MOE_FMT_FP8_B128_W8A16>(a, s);
+      return launch<MOE_FMT_FP8_B128_W8A16>(a, lose_h, s);
     case MOE_FMT_INT4_G128_W4A16:
-      return launch<MOE_FMT_INT4_G128_W4A16>(a, s);
+      return launch<MOE_FMT_INT4_G128_W4A16>(a, lose_h, s);
     case MOE_FMT_BF16:
-      return launch<MOE_FMT_BF16>(a, s);
+      return launch<MOE_FMT_BF16>(a, lose_h, s);
     default:
-      return launch<MOE_FMT_NVFP4_W4A16>(a, s);
+      return launch<MOE_FMT_NVFP4_W4A16>(a, lose_h, s);
   }
 }
 
