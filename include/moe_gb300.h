@@ -433,12 +433,18 @@ moe_status_t moe_get_adapter_error(moe_stream_t stream, int32_t* code);
 /* ---- the layer for a few tokens, and products in the FP8 block format ------------------------- */
 
 /* The layer as a decode step runs it, router product included, for T <= MOE_FEW_MAX_TOKENS tokens in two kernels:
- *   logits[t, e] = sum over h of x[t, h] w_router[e, h], the exact sum rounded once to fp32
+ *   logits[t, e] = sum over h of x[t, h] w_router[e, h], carried in pairs of fp32 numbers and rounded once to fp32.  The pair is
+ *             off by at most (H / 64 + 12)^2 2^-48 of sum |x w| (four times that with an fp32 w_router), so the logit is the exact
+ *             sum's nearest number unless the sum cancels by about as much or ends as close to a midpoint
  *   experts and weights of each token: moe_router_t's rule on those logits (bias f32 [E] or NULL)
  *   out[t] = sum_j w_tj Wd_e (silu(Wg_e x_t) * (Wu_e x_t)),   e = the j-th expert of t
- * with the weights as stored (any format), x as it is and the sums in fp32; h enters the down product with 22 bits of the
- * largest of its 128 neighbours (with bf16 weights: 16 bits of each element), and out is rounded once.  The formats that quantize activations at run time (W4A4, W8A8) do not here, where the weights' bytes
- * set the pace.  Results do not depend on the order in which blocks run.
+ * with the weights as stored (any format; INT4's as code - 8 before they are multiplied), x as it is but for what is below 2^-39 of
+ * its row's largest (with bf16 weights: as it is) and the sums in fp32; h enters the down product with 22 bits of the
+ * largest of its 128 neighbours (with bf16 weights: 16 bits of each element), and out is rounded once.  The formats that quantize
+ * activations at run time (W4A4, W8A8) do not here, where the weights' bytes set the pace.  Results do not depend on the order in which blocks run.
+ * An expert's weights are read once for every four of its tokens: with few large experts moe_layer_forward_scored is the faster from
+ * a few tokens on (this one is the faster with 8 experts of 4096 x 14336, top 2, up to 1 token of W4A4, 2 of FP8, 4 of BF16 and 8 of INT4 and
+ * NVFP4 W4A16; with 128 of 2048 x 768, top 8, and 16 of 2048 x 2048, top 2, up to 24 to 32).
  *   x (dev) bf16 [T, H] (pitch ldx); w_router (dev) w_dtype [E, H] (pitch ldw); packed (dev) as moe_pack_experts
  *   writes it (of a buffer that holds images, only the canonical tensors are read); out (dev) bf16 [T, H] (pitch ldo), may be
  *   x (same pitch), no other overlap; topk_idx (dev) i32 [T, top_k] and topk_w (dev) f32 [T, top_k], or NULL;

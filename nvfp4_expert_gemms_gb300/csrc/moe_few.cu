@@ -64,8 +64,10 @@ __device__ __forceinline__ void unpack8(const uint4& u, bool f16, float2 (&w)[4]
 }
 
 // A cluster of eight blocks per token: its logits, its experts and its row scaled into fp16.
-//   logits[t, e] = sum over h of x[t, h] w[e, h], a warp per expert.  The sum is carried in pairs, so that it is the exact sum
-//   rounded once (but for one case in some 2^20): which experts a token gets must not hang on the order of a sum.
+//   logits[t, e] = sum over h of x[t, h] w[e, h], a warp per expert.  The sum is carried in pairs: which experts a token gets must not
+//   hang on the order of a sum.  Of a pair lo alone is rounded, n = H / 64 times in a lane and twice in each of six meetings, while it grows to
+//   n 2^-24 of the largest partial sum: together less than (n + 12)^2 2^-48 of sum |x w| (four times that for fp32 w, whose products add a
+//   rounding of their own).  Without cancellation that leaves one logit in some 2^20 that is not the exact sum's nearest.
 // Eight blocks of sixteen warps per token because one token's products (E H of them, seven operations each for two) would
 // take one SM several microseconds; the logits go straight to the first block's shared memory, where one warp chooses.  Past fp32's range lo is not a number and hi alone counts.  h and y are filled with
 // the mark of what is not there yet.

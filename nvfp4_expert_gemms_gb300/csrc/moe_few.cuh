@@ -1,11 +1,12 @@
 // Declarations of the whole layer for a few tokens (moe_layer_few): its workspace and what its two kernels share.
 //
-// Operands.  The products run on mma.sync m16n8k16 with the weights as the 16-row operand and up to eight tokens as
-// the 8-column one (up to four where h comes in two terms): a step reads each weight once from HBM, so bytes set the pace and not the MMA rate, and the
-// operands may come from registers, straight from the decoded codes, with no second trip through shared memory.
+// Operands.  The products run on mma.sync m16n8k16 with the weights as the 16-row operand and up to four tokens of an expert in
+// the 8-column one (x in four columns; h, in two terms, in eight): bytes set the pace there and not the MMA rate, and the
+// operands may come from registers, straight from the decoded codes, with no second trip through shared memory.  More than four tokens
+// of one expert read its weights again.
 // E4M3, E2M1 x E4M3 and INT4 weights are all exact in fp16, whose products with fp16 activations are exact in the
 // fp32 accumulator; a row of activations is scaled by a power of two so that fp16 holds its bf16 values exactly (but for
-// elements below 2^-29 of the row's largest, which lose low bits), and an fp32 row of h is held in two fp16 terms.
+// what is below 2^-39 of the row's largest, the last place of a subnormal), and an fp32 row of h is held in two fp16 terms.
 // bf16 weights meet bf16 activations, h in two bf16 terms.
 #pragma once
 #include "moe_score.cuh"

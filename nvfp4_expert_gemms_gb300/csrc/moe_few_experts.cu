@@ -20,14 +20,14 @@
 // changed.  With counters behind fences in their place a block's units took up to half as long again (134 us for 90 at 16
 // tokens of FP8, 128 experts of 2048 x 768, whichever warp fenced); a fence waits for the SM's traffic.
 //
-// What it takes (128 experts of 2048 x 768, 8 per token, with the router's kernel): FP8 20.9 us at 1 token and 82 at 16, where HBM alone would
+// What it takes (128 experts of 2048 x 768, 8 per token, with the router's kernel): FP8 21.2 us at 1 token and 83 at 16, where HBM alone would
 // take 5.6 and 57; NVFP4 42 at 4 tokens (11.5), INT4 80 at 16 (29.6).  Some 7 to 10 us are the router and the entries, 3 to 5 the waits
 // for the last h and the last y; the rest is instructions: of a piece's multiplication (130 to 210 per warp) and of what surrounds
 // it (some 190, shared by eight warps in part), at six to nine cycles each.  HBM brings a unit of FP8 in 2800 cycles per SM and one of
 // four bits in 1500.  Hence teams, each on a unit of its own; one wait per stage, whose description comes with it (a queue of units
-// beside the stages, and scales loaded for each: 89 us for 83 at 16 tokens of FP8, 73 for 69.5 of INT4); as little as possible per stage for the
+// beside the stages, and scales loaded for each: 89 us for 83 at 16 tokens of FP8); as little as possible per stage for the
 // copying thread (one warp that copied for both: 91).  And nothing in that chain may wait for L2: no spilled register (with 222 KB of
-// shared memory there is next to no L1), no scale or address that was not asked for early.
+// shared memory there is next to no L1; the NVFP4 kernel spills 16 bytes), no scale or address that was not asked for early.
 #include "moe_few.cuh"
 #include "moe_formats.cuh"
 #include "moe_tc.cuh"

@@ -4,7 +4,7 @@
 // the 128-byte swizzle).  Their scales change every 128 columns, so each group's partial sum goes to a tensor-memory
 // buffer of its own, and promoting warps read it back, scale it and add it to sums that they keep in registers, while the MMAs
 // of the next groups fill the other buffers.  16384 x 2048 x 4096 takes 147 us (1.87 PFLOP/s), x 4096 267 us (2.06 PFLOP/s), the tensor
-// pipe busy for 41% of it: what paces the tiles is the promotion, 64 sums a thread and group, and the L2's rate (48 KB per 8.4 MFLOP).
+// pipe busy for 40% of it: what paces the tiles is the promotion, 64 sums a thread and group, and the L2's rate (48 KB per 8.4 MFLOP).
 #include <cudaTypedefs.h>
 
 #include "moe_dec.cuh"
@@ -24,7 +24,8 @@ constexpr int kM = 128, kTileA = kM * 128;  // rows of x per tile; bytes of its 
 template <int BN>
 struct Shape {
   static constexpr int kPromote = BN / 16;  // warps: a row per thread, 64 columns per warp
-  // A warp of its own brings the groups' scales where 96 registers a thread leave nothing for it (each promoting thread loading its
+  // A warp of its own brings the groups' scales where 96 registers a thread leave nothing for it (as it is they spill 20 bytes, 28 with pairs, 56
+  // with pairs that cross blocks; each promoting thread loading its
   // row's, each from a line of its own: 16384 x 4096 x 4096 359 us).  For BN = 64 a seventh warp would cost the others 40 registers.
   static constexpr bool kScaleWarp = BN == 256;
   static constexpr int kThreads = 32 * (kPromote + 2 + kScaleWarp);
