@@ -289,8 +289,8 @@ class MoEBlock:
     few_tokens: up to so many tokens (32 at most) go through moe_layer_few, whose logits are fp32 and which does not round or
     quantize the activations on the way.  It reads an expert's weights once for every four of its tokens, so the number up to
     which it is the faster hangs on the layer (8 experts of 4096 x 14336, top 2: 1 token of W4A4, 2 of FP8, 4 of BF16, 8 of
-    INT4 and NVFP4 W4A16; 16 of 2048 x 2048, top 2, or 128 of 2048 x 768, top 8: 24 to 32).  few_workspace is what it uses (None without), taken when the block is made: shared with the
-    layer's other blocks, or larger than theirs.
+    INT4 and NVFP4 W4A16; 16 of 2048 x 2048, top 2, or 128 of 2048 x 768, top 8: 24 to 32).  few_workspace is what it uses
+    (None without), taken when the block is made: shared with the layer's other blocks, or larger than theirs.
     """
 
     def __init__(self, layer: MoELayer, w_router, router: Router, top_k: int, pre: Norm, post: Norm = None,
